@@ -234,12 +234,9 @@ def _run_own(s):
             s["cu"], interleaved=c["interleaved"], err_flag=s["err"])
         return _rope_outputs(s, s["out"])
     if c["op"] == "decode":
-        if "workspace" not in s:
-            s["workspace"] = pk.decode_window_workspace(c["seqs"], c["q_heads"], c["kv_heads"], c["head_dim"],
-                                                        s["tables"].shape[1], c["window"], c["sinks"])
         getattr(pk, "decode_attention_window" + quant)(
             s["out"], s["q"], s["k_pool"], s["v_pool"], s["tables"], s["starts"], s["scale"], c["window"], c["sinks"],
-            workspace=s["workspace"], err_flag=s["err"])
+            err_flag=s["err"])
         return s["out"]
     pk.prefill_attention_window(s["out"], s["q"], s["k_pool"], s["v_pool"], s["tables"], s["starts"], s["cu"], s["scale"],
                                 s["max_chunk"], c["window"], c["sinks"], err_flag=s["err"])
