@@ -426,6 +426,83 @@ pa_status pa_decode_attention_noalloc(void* out, const void* q, const void* k_po
                                       float scale, pa_dtype dtype, int32_t* dev_err_flag,
                                       void* stream);
 
+/*
+ * pa_rope_append_kv -- write new K/V tokens at explicit positions with the position
+ * rotation applied on the way, and rotate the tokens' queries in the same launch
+ * (the pages' engines rotate nothing; this is this library's addition for models with
+ * rotary positions, beside pa_append_kv).
+ *
+ *   k_pool, v_pool   pools of type `dtype`: PA_F32, PA_BF16, PA_FP8_E4M3 or PA_FP4_E2M1
+ *   k_new, v_new     new rows [num_kv_heads][head_dim], f32 for f32 pools, bf16 otherwise;
+ *                    row r starts k_stride / v_stride * r elements on (a column range of
+ *                    a fused projection's output needs no copy)
+ *   q, q_out         the rows' queries [num_q_heads][head_dim] of the same type and
+ *                    where they go, with strides of their own; q_out may be q (with the
+ *                    same stride), else the two do not overlap; both NULL: no queries
+ *   inv_freq         double [rotary_dim / 2] (device): radians per position
+ *   rotary_dim       a multiple of 16, at most head_dim (64 or 128)
+ *   interleaved      0: dims (f, f + rotary_dim / 2) form plane f; else (2 f, 2 f + 1)
+ *   block_tables, start_pos, cu_new_tokens   as pa_append_kv: row cu_new_tokens[s] + i is
+ *                    the token at position p = start_pos[s] + i of sequence s
+ * Plane f of every query and key head of the row is turned by p * inv_freq[f]:
+ *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin;  dims rotary_dim and up pass through.
+ * Angles are exact to about 1e-7 radian at any position; the turn is computed in fp32 and
+ * rounded once to the destination's type (for FP8 / FP4 pools the fp32 row is quantised
+ * by the rules of pa_append_kv_fp8 / _fp4; values are never rotated).
+ * Rows must start on 16-byte boundaries and not overlap.  A row without a valid place
+ * (flagged as in pa_append_kv) is skipped: neither the pools nor its q_out row change.
+ */
+pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void* q,
+                            const void* k_new, const void* v_new, int64_t q_out_stride,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* start_pos, const int32_t* cu_new_tokens,
+                            int32_t num_seqs, int32_t total_new_tokens, int32_t num_blocks,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            pa_dtype dtype, int32_t* dev_err_flag, void* stream);
+
+/*
+ * pa_decode_attention_window -- pa_decode_attention where the query at position L - 1
+ * (L = context_lens[s]) sees only the last `window` positions, j >= L - window, and the
+ * first `num_sinks` positions of the sequence.
+ *
+ *   dtype            of the pools: PA_F32 (q and out f32), PA_BF16, PA_FP8_E4M3 or
+ *                    PA_FP4_E2M1 (q and out bf16)
+ *   window           at least 1 (the query's own position); num_sinks at least 0
+ * Other arguments and the arithmetic as pa_decode_attention, without a workspace.  Only
+ * blocks that hold a visible position are read: the table entries between the sinks and
+ * the window may be anything (blocks freed and given to others, -1).  A zero-length
+ * context gives zeros.  A sequence's result does not depend on the rest of the batch (for
+ * the same table width).
+ */
+pa_status pa_decode_attention_window(void* out, const void* q, const void* k_pool,
+                                     const void* v_pool, const int32_t* block_tables,
+                                     const int32_t* context_lens, int32_t num_seqs,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t max_blocks_per_seq, int32_t num_blocks,
+                                     int32_t window, int32_t num_sinks, float scale,
+                                     pa_dtype dtype, int32_t* dev_err_flag, void* stream);
+
+/*
+ * pa_prefill_attention_window -- pa_prefill_attention under the same mask: row (s, i) at
+ * position p = start_pos[s] + i sees positions j <= p with j > p - window or
+ * j < num_sinks, i.e. it equals pa_decode_attention_window of that query with context
+ * length p + 1.  Only the blocks of the sinks and of the chunk's windows are read.
+ * A chunk outside rows 0 .. total_q sets PA_DEV_ERR_BAD_CU and is skipped; rows of a
+ * chunk past max_chunk set PA_DEV_ERR_HINT and are not computed.  A value that is not
+ * finite reaches, besides the rows that see it, at most rows of the same chunk near them
+ * (within 256 tokens), never rows when it is hidden from the whole chunk.
+ */
+pa_status pa_prefill_attention_window(void* out, const void* q, const void* k_pool,
+                                      const void* v_pool, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* start_pos,
+                                      const int32_t* cu_q, int32_t num_seqs, int32_t total_q,
+                                      int32_t max_chunk, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                      int32_t window, int32_t num_sinks, float scale,
+                                      pa_dtype dtype, int32_t* dev_err_flag, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Host block manager (no GPU; spindle, "Paging").
  *

@@ -13,6 +13,9 @@ from ._native import (  # noqa: F401
     copy_block_fp8,
     fp4_pool_shape, append_kv_fp4, decode_attention_fp4, copy_block_fp4,
     prefill_attention,
+    rope_append_kv, rope_append_kv_fp8, rope_append_kv_fp4,
+    decode_attention_window, decode_attention_window_fp8, decode_attention_window_fp4,
+    prefill_attention_window,
     DEV_ERR_BAD_BLOCK, DEV_ERR_BAD_POS, DEV_ERR_HINT, DEV_ERR_BAD_CU, DEV_ERR_TIMEOUT,
     DEV_ERR_BAD_PAIR, DEV_ERR_BAD_PREFIX,
 )

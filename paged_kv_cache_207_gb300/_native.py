@@ -41,7 +41,8 @@ EXPORTED = [
     "pa_decode_attention_noalloc", "pa_append_kv_fp8", "pa_decode_attention_fp8",
     "pa_append_decode_attention_fp8",
     "pa_append_kv_fp4", "pa_decode_attention_fp4",
-    "pa_prefill_attention", "pa_bm_create", "pa_bm_destroy",
+    "pa_prefill_attention", "pa_rope_append_kv", "pa_decode_attention_window",
+    "pa_prefill_attention_window", "pa_bm_create", "pa_bm_destroy",
     "pa_bm_add_seq", "pa_bm_fork", "pa_bm_free_seq", "pa_bm_blocks_needed",
     "pa_bm_prepare_append", "pa_bm_block_table", "pa_bm_block_tables", "pa_bm_seq_len",
     "pa_bm_refcount", "pa_bm_stats",
@@ -111,6 +112,16 @@ def lib() -> ctypes.CDLL:
     L.pa_prefill_attention.argtypes = [p, p, p, p, p, i32, p, p, i32, i32, i32, i32, i32, i32, i32,
                                        ctypes.c_float, ctypes.c_int, p, p]
     L.pa_prefill_attention.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    L.pa_rope_append_kv.argtypes = [p, p, p, p, p, p, i64, i64, i64, i64, p, i32, i32, p, i32, p, p,
+                                    i32, i32, i32, i32, i32, i32, ctypes.c_int, p, p]
+    L.pa_rope_append_kv.restype = ctypes.c_int
+    L.pa_decode_attention_window.argtypes = [p, p, p, p, p, p, i32, i32, i32, i32, i32, i32, i32, i32,
+                                             ctypes.c_float, ctypes.c_int, p, p]
+    L.pa_decode_attention_window.restype = ctypes.c_int
+    L.pa_prefill_attention_window.argtypes = [p, p, p, p, p, i32, p, p, i32, i32, i32, i32, i32, i32,
+                                              i32, i32, i32, ctypes.c_float, ctypes.c_int, p, p]
+    L.pa_prefill_attention_window.restype = ctypes.c_int
     L.pa_decode_attention_noalloc.argtypes = [p, p, p, p, p, p, i32, i32, i32, i32, i32, i32, i32,
                                               ctypes.c_float, ctypes.c_int, p, p]
     L.pa_decode_attention_noalloc.restype = ctypes.c_int
@@ -409,6 +420,159 @@ def prefill_attention(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, sca
         block_tables.shape[1], _i32(start_pos, "start_pos"), _i32(cu_q, "cu_q"),
         start_pos.shape[0], q.shape[0], int(max_chunk), q.shape[1], hkv, d, nb, float(scale),
         _dtype_code(q), None if err_flag is None else _i32(err_flag, "err_flag"), _stream(stream)))
+
+
+_POOL_F32, _POOL_BF16, _POOL_FP8, _POOL_FP4 = 0, 1, 2, 3
+
+
+def _bound(x) -> int:
+    """A window, sink count or chunk bound: anything past int32 is as good as the largest."""
+    return min(int(x), 2**31 - 1)
+
+
+def _call_on(device, stream, fn, args) -> None:
+    """Calls a library function on the tensors' device, its current stream by default."""
+    with torch.cuda.device(device):
+        check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+
+
+def _checked(dev, t, name, dtype, shape):
+    """Address of a contiguous tensor of this device, type and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(dev, t, name, dtype, shape):
+    """Address and row stride of rows [n][heads][head_dim] whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    n, heads, d = shape
+    if n and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d)
+
+
+def _pools(k_pool, v_pool, dims):
+    nb, hkv, d = dims(k_pool)
+    dev = k_pool.device
+    kp = _checked(dev, k_pool, "k_pool", k_pool.dtype, k_pool.shape)
+    vp = _checked(dev, v_pool, "v_pool", k_pool.dtype, k_pool.shape)
+    return dev, nb, hkv, d, kp, vp
+
+
+def _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                 cu_new_tokens, interleaved, err_flag, stream, dims, code, rows) -> None:
+    dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, dims)
+    n, s = k_new.shape[0], start_pos.shape[0]
+    hq = 0 if q is None else q.shape[1]
+    kn, ks = _rows(dev, k_new, "k_new", rows, (n, hkv, d))
+    vn, vs = _rows(dev, v_new, "v_new", rows, (n, hkv, d))
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    qi, qs = (None, 0) if q is None else _rows(dev, q, "q", rows, (n, hq, d))
+    qo, qos = (None, 0) if q is None else _rows(dev, q_out, "q_out", rows, (n, hq, d))
+    freq = _checked(dev, inv_freq, "inv_freq", torch.float64, (inv_freq.shape[0],))
+    width = block_tables.shape[1]
+    _call_on(dev, stream, "pa_rope_append_kv", (
+        kp, vp, qo, qi, kn, vn, qos, qs, ks, vs, freq, 2 * inv_freq.shape[0], int(bool(interleaved)),
+        _checked(dev, block_tables, "block_tables", torch.int32, (s, width)), width,
+        _checked(dev, start_pos, "start_pos", torch.int32, (s,)),
+        _checked(dev, cu_new_tokens, "cu_new_tokens", torch.int32, (s + 1,)), s, n, nb, hq, hkv, d, code,
+        None if err_flag is None else _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)))
+
+
+def rope_append_kv(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                   cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
+    """append_kv with the position rotation on the way: queries and keys of row i of sequence s
+    are turned by (start_pos[s] + i) * inv_freq (float64 [rotary_dim / 2] on the device), keys
+    and values go to the pools, the turned queries to q_out (which may be q; both None: no
+    queries).  Rows [tokens][heads][D] may be column ranges of a wider tensor."""
+    code = _dtype_code(k_pool)
+    _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                 cu_new_tokens, interleaved, err_flag, stream, _pool_dims, code, k_pool.dtype)
+
+
+def rope_append_kv_fp8(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                       cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
+    """rope_append_kv of bf16 rows into FP8 pools."""
+    _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                 cu_new_tokens, interleaved, err_flag, stream, _fp8_dims, _POOL_FP8, torch.bfloat16)
+
+
+def rope_append_kv_fp4(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                       cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
+    """rope_append_kv of bf16 rows into MXFP4 pools."""
+    _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                 cu_new_tokens, interleaved, err_flag, stream, _fp4_dims, _POOL_FP4, torch.bfloat16)
+
+
+def _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
+                   err_flag, stream, dims, code, rows) -> None:
+    dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, dims)
+    s, hq = q.shape[0], q.shape[1]
+    width = block_tables.shape[1]
+    _call_on(dev, stream, "pa_decode_attention_window", (
+        _checked(dev, out, "out", rows, (s, hq, d)), _checked(dev, q, "q", rows, (s, hq, d)), kp, vp,
+        _checked(dev, block_tables, "block_tables", torch.int32, (s, width)),
+        _checked(dev, context_lens, "context_lens", torch.int32, (s,)), s, hq, hkv, d, width, nb,
+        _bound(window), _bound(num_sinks), float(scale), code,
+        None if err_flag is None else _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)))
+
+
+def decode_attention_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window: int,
+                            num_sinks: int = 0, err_flag=None, stream=None) -> None:
+    """decode_attention over the last ``window`` positions and the first ``num_sinks``; table
+    entries of blocks that hold none of them are not read."""
+    code = _dtype_code(k_pool)
+    _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
+                   err_flag, stream, _pool_dims, code, k_pool.dtype)
+
+
+def decode_attention_window_fp8(out, q, k_pool, v_pool, block_tables, context_lens, scale,
+                                window: int, num_sinks: int = 0, err_flag=None, stream=None) -> None:
+    """decode_attention_window over FP8 pools (bf16 q and out)."""
+    _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
+                   err_flag, stream, _fp8_dims, _POOL_FP8, torch.bfloat16)
+
+
+def decode_attention_window_fp4(out, q, k_pool, v_pool, block_tables, context_lens, scale,
+                                window: int, num_sinks: int = 0, err_flag=None, stream=None) -> None:
+    """decode_attention_window over MXFP4 pools (bf16 q and out)."""
+    _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
+                   err_flag, stream, _fp4_dims, _POOL_FP4, torch.bfloat16)
+
+
+def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, scale,
+                             max_chunk: int, window: int, num_sinks: int = 0, err_flag=None,
+                             stream=None) -> None:
+    """prefill_attention with every row limited to the last ``window`` positions up to its own
+    and the first ``num_sinks`` (bf16)."""
+    dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, _pool_dims)
+    code = _dtype_code(k_pool)
+    n, hq, s = q.shape[0], q.shape[1], start_pos.shape[0]
+    width = block_tables.shape[1]
+    _call_on(dev, stream, "pa_prefill_attention_window", (
+        _checked(dev, out, "out", k_pool.dtype, (n, hq, d)), _checked(dev, q, "q", k_pool.dtype, (n, hq, d)),
+        kp, vp, _checked(dev, block_tables, "block_tables", torch.int32, (s, width)), width,
+        _checked(dev, start_pos, "start_pos", torch.int32, (s,)),
+        _checked(dev, cu_q, "cu_q", torch.int32, (s + 1,)), s, n, _bound(max_chunk), hq, hkv, d, nb,
+        _bound(window), _bound(num_sinks), float(scale), code,
+        None if err_flag is None else _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024

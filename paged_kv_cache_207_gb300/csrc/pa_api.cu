@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "pa_internal.h"
+#include "pa_window.h"
 
 namespace {
 
@@ -528,6 +529,157 @@ pa_status pa_prefill_attention(void* out, const void* q, const void* k_pool, con
     a.num_blocks = num_blocks;
     a.scale = scale;
     return cuda_status(pa::launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void* q,
+                            const void* k_new, const void* v_new, int64_t q_out_stride,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* start_pos, const int32_t* cu_new_tokens,
+                            int32_t num_seqs, int32_t total_new_tokens, int32_t num_blocks,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
+    if (!dtype_ok(dtype) && dtype != PA_FP8_E4M3 && dtype != PA_FP4_E2M1) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_new_tokens < 0 || num_blocks <= 0 || num_kv_heads <= 0 ||
+        max_blocks_per_seq <= 0 || rotary_dim <= 0 || rotary_dim > head_dim)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if ((q == nullptr) != (q_out == nullptr)) return PA_ERR_INVALID_ARG;
+    if (q && num_q_heads <= 0) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 && total_new_tokens != 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!k_pool || !v_pool || !inv_freq || !block_tables || !start_pos || !cu_new_tokens)
+        return PA_ERR_INVALID_ARG;
+    if (total_new_tokens > 0 && (!k_new || !v_new)) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned16(q) || !aligned16(q_out) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
+        return PA_ERR_INVALID_ARG;
+    if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX) return PA_ERR_INVALID_ARG;
+    // rows start on 16-byte boundaries and do not overlap
+    const int64_t piece = dtype == PA_F32 ? 4 : 8;
+    const int64_t kv_row = (int64_t)num_kv_heads * head_dim, q_row = (int64_t)num_q_heads * head_dim;
+    if (total_new_tokens > 1) {
+        if (k_stride < kv_row || v_stride < kv_row || k_stride % piece != 0 || v_stride % piece != 0)
+            return PA_ERR_INVALID_ARG;
+        if (q && (q_stride < q_row || q_out_stride < q_row || q_stride % piece != 0 ||
+                  q_out_stride % piece != 0 || (q == q_out && q_stride != q_out_stride)))
+            return PA_ERR_INVALID_ARG;
+    }
+    pa::RopeArgs a;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.q_out = q_out;
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.q_out_stride = q_out_stride;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.inv_freq = inv_freq;
+    a.block_tables = block_tables;
+    a.start_pos = start_pos;
+    a.cu_new = cu_new_tokens;
+    a.err = dev_err_flag;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved != 0;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_seqs = num_seqs;
+    a.total_new = total_new_tokens;
+    a.num_blocks = num_blocks;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.dtype = dtype;
+    return cuda_status(pa::launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_decode_attention_window(void* out, const void* q, const void* k_pool,
+                                     const void* v_pool, const int32_t* block_tables,
+                                     const int32_t* context_lens, int32_t num_seqs,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t max_blocks_per_seq, int32_t num_blocks,
+                                     int32_t window, int32_t num_sinks, float scale,
+                                     pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
+    if (!dtype_ok(dtype) && dtype != PA_FP8_E4M3 && dtype != PA_FP4_E2M1) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0 || window <= 0 || num_sinks < 0 || !std::isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > 8) return PA_ERR_UNSUPPORTED;
+    if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
+        return PA_ERR_INVALID_ARG;
+    pa::WindowArgs a;
+    a.out = out;
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.err = dev_err_flag;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.window = window;
+    a.sinks = num_sinks;
+    a.scale = scale;
+    a.dtype = dtype;
+    return cuda_status(pa::launch_window_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_prefill_attention_window(void* out, const void* q, const void* k_pool,
+                                      const void* v_pool, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* start_pos,
+                                      const int32_t* cu_q, int32_t num_seqs, int32_t total_q,
+                                      int32_t max_chunk, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                      int32_t window, int32_t num_sinks, float scale,
+                                      pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
+    if (num_seqs < 0 || total_q < 0 || max_chunk < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_blocks <= 0 || max_blocks_per_seq <= 0 || window <= 0 || num_sinks < 0 ||
+        !std::isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if (dtype != PA_BF16) return dtype_ok(dtype) ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > 8) return PA_ERR_UNSUPPORTED;
+    if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q == 0 || max_chunk == 0) return PA_OK;
+    if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !start_pos || !cu_q)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
+        return PA_ERR_INVALID_ARG;
+    pa::PrefillArgs a;
+    a.out = out;
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.block_tables = block_tables;
+    a.start_pos = start_pos;
+    a.cu_q = cu_q;
+    a.err = dev_err_flag;
+    a.num_seqs = num_seqs;
+    // (no chunk is longer than all rows, so a generous bound costs no empty items)
+    a.max_chunk = max_chunk < total_q ? max_chunk : total_q;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.scale = scale;
+    return cuda_status(pa::launch_prefill_window(a, total_q, window, num_sinks, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

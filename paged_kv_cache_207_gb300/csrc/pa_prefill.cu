@@ -29,6 +29,7 @@
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "pa_tc.cuh"
+#include "pa_window.h"
 
 namespace pa {
 
@@ -62,6 +63,9 @@ struct PParams {
     int slot_mult;
     // prefill: query tiles per chunk (of TQ tokens) and work items (nqt x Hkv x num_seqs)
     int nqt, num_items;
+    // windowed prefill: a row at position p sees positions p - window + 1 .. p and the first `sinks`
+    int window, sinks;
+    int total_q, max_chunk;
 };
 
 __device__ __forceinline__ void raise_flag(int32_t* err, int bits) {
@@ -223,9 +227,10 @@ __device__ __forceinline__ uint64_t fadd_f32x2(uint64_t a, uint64_t b) {
 // lane (-1 past the CTA's last block), a window ahead of its use: read one tile ahead,
 // every tile would wait for a dependent load (over a microsecond when HBM is busy).
 constexpr int kWinTiles = 32 / kKeyBlocks;
-__device__ __forceinline__ int32_t fetch_window(const int32_t* trow, int w, int lim, int lane) {
+template <bool WIN>
+__device__ __forceinline__ int32_t fetch_window(const int32_t* trow, const VisibleBlocks& v, int w, int lim, int lane) {
     const int b = 32 * w + lane;
-    return b < lim ? __ldg(trow + b) : -1;
+    return b < lim ? __ldg(trow + (WIN ? v.block(b) : b)) : -1;
 }
 // Table entry of block `lane` of key tile j from the window holding it (-1 for lanes past
 // the tile's blocks or the CTA's last block).
@@ -254,13 +259,19 @@ struct Item {
     int qrow0, p0, rows;        // prefill: the tile's first chunk row (a row of q), its position, its rows
     int p_last, nblk;           // last position attended to, blocks read
     const int32_t* trow;
+    // windowed prefill: the item's keys are the blocks of this list (nblk of them), those that
+    // hold a sink or a position from `first`, its first row's oldest one, to p_last
+    VisibleBlocks v;
+    int first;
     bool live;                  // rows and keys to process
     bool bad_pos;               // a position outside the table (flagged, skipped)
+    int bad;                    // windowed prefill: further PA_DEV_ERR_ bits of the chunk
 };
 // The prefill's items as the CTA's list keeps them: the natural index and the geometry that
 // would otherwise take three dependent loads per item.
 struct ListEntry { int it, qrow0, p0, rows; };
 
+template <bool WIN>
 __device__ __forceinline__ Item finish_item(const PParams& p, int it, int qrow0, int p0, int rows) {
     Item g{};
     const int s = it / (p.nqt * p.Hkv);
@@ -275,11 +286,17 @@ __device__ __forceinline__ Item finish_item(const PParams& p, int it, int qrow0,
         g.bad_pos = true;
         return g;
     }
-    g.nblk = g.p_last / kBlockTokens + 1;
+    if constexpr (WIN) {
+        g.first = max(0, p0 - p.window + 1);
+        g.v = visible_blocks(g.first, g.p_last, p.sinks);
+        g.nblk = g.v.count;
+    } else {
+        g.nblk = g.p_last / kBlockTokens + 1;
+    }
     g.live = true;
     return g;
 }
-template <bool PREFIX>
+template <bool PREFIX, bool WIN>
 __device__ __forceinline__ Item item_at(const PParams& p, int it) {
     if constexpr (PREFIX) {
         Item g{};
@@ -295,14 +312,26 @@ __device__ __forceinline__ Item item_at(const PParams& p, int it) {
         const int i0 = (p.nqt - 1 - x) * p.TQ;
         // the chunk's place: three loads in flight together
         const int q0 = __ldg(p.cu_q + s), q1 = __ldg(p.cu_q + s + 1), start = __ldg(p.start_pos + s);
+        if constexpr (WIN) {
+            // (nothing of a chunk outside q is touched, and positions do not overflow)
+            const int cap = p.max_blocks * kBlockTokens;
+            const bool chunk_ok = q0 >= 0 && q0 <= q1 && q1 <= p.total_q;
+            const int n = chunk_ok ? min(q1 - q0, p.max_chunk) : 0, rows = min(n - i0, p.TQ);
+            Item g = finish_item<true>(p, it, q0 + i0, start < 0 || start > cap - i0 - rows ? -1 : start + i0, rows);
+            if (i0 == 0) g.bad = !chunk_ok ? PA_DEV_ERR_BAD_CU : q1 - q0 > p.max_chunk ? PA_DEV_ERR_HINT : 0;
+            return g;
+        }
         // (a chunk's start is checked with its first tile's positions)
-        return finish_item(p, it, q0 + i0, start < 0 ? -1 : start + i0, min(q1 - q0 - i0, p.TQ));
+        return finish_item<WIN>(p, it, q0 + i0, start < 0 ? -1 : start + i0, min(q1 - q0 - i0, p.TQ));
     }
 }
 // Cost of the items of query tile nqt - 1 - x of sequence s (every kv head alike): their
-// key tiles, 0 without work, -1 for positions outside the table.
+// key tiles, 0 without work, -1 for positions outside the table (a windowed chunk's other
+// faults are flagged here).
+template <bool WIN>
 __device__ __forceinline__ int group_cost(const PParams& p, int grp) {
-    const Item g = item_at<false>(p, grp / p.nqt * p.Hkv * p.nqt + grp % p.nqt);
+    const Item g = item_at<false, WIN>(p, grp / p.nqt * p.Hkv * p.nqt + grp % p.nqt);
+    if (WIN && g.bad) raise_flag(p.err, g.bad);
     if (g.bad_pos) return -1;
     return g.live ? (g.nblk + kKeyBlocks - 1) / kKeyBlocks : 0;
 }
@@ -320,7 +349,7 @@ __device__ __forceinline__ int group_cost(const PParams& p, int grp) {
 // keeps the list of its own items with their geometry.  Where the costs or the list would
 // not fit, the CTA takes items blockIdx.x, + gridDim.x, ... instead (list length -1).
 constexpr int kTileCost = 179, kItemCost = 370;      // (units of 10 ns)
-template <int D>
+template <int D, bool WIN>
 __device__ void build_schedule(const PParams& p, uint8_t* smem) {
     using L = Smem<D, 2>;
     int* cnt = reinterpret_cast<int*>(smem + L::Q);      // [ncost] counts, then offsets
@@ -342,7 +371,7 @@ __device__ void build_schedule(const PParams& p, uint8_t* smem) {
     if (!sorted) {
         // positions outside the table, flagged once: each CTA checks its share of the groups
         for (int g = cta * nthr + tid; g < ngroups; g += grid * nthr)
-            if (group_cost(p, g) < 0) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+            if (group_cost<WIN>(p, g) < 0) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
         if (tid == 0) *nlist = -1;
         __syncthreads();
         return;
@@ -350,7 +379,7 @@ __device__ void build_schedule(const PParams& p, uint8_t* smem) {
     for (int c = tid; c < ncost; c += nthr) cnt[c] = 0;
     __syncthreads();
     for (int g = tid; g < ngroups; g += nthr) {
-        const Item it = item_at<false>(p, g / p.nqt * p.Hkv * p.nqt + g % p.nqt);
+        const Item it = item_at<false, WIN>(p, g / p.nqt * p.Hkv * p.nqt + g % p.nqt);
         const int c = it.bad_pos ? -1 : it.live ? (it.nblk + kKeyBlocks - 1) / kKeyBlocks : 0;
         gcost[g] = c;
         gq[g] = it.qrow0;
@@ -358,6 +387,7 @@ __device__ void build_schedule(const PParams& p, uint8_t* smem) {
         gr[g] = it.rows;
         if (c > 0) atomicAdd(&cnt[c], 1);
         else if (c < 0 && cta == 0) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+        if (WIN && it.bad && cta == 0) raise_flag(p.err, it.bad);
     }
     __syncthreads();
     if (tid < 32) {
@@ -437,7 +467,11 @@ __device__ void build_schedule(const PParams& p, uint8_t* smem) {
 // partial (o, max, sum) into the decode workspace for the split-KV merge.
 // SW = 1 launches 256 threads under the same per-thread register budget (168), so a
 // CTA takes 256 x 168 registers and leaves room for a decode CTA on its SM.
-template <int D, bool PREFIX, int SW>
+// WIN = true: the prefill with every row limited to its window and the sinks.  An item's keys
+// are the listed blocks (VisibleBlocks), packed into the same 128-key tiles: the sinks' blocks
+// come first and share a tile with the window's first ones, so a tile costs the same whatever
+// it holds, and masks are needed only in the tiles that a row's window or the causal limit cuts.
+template <int D, bool PREFIX, int SW, bool WIN>
 __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams p) {
     using L = Smem<D, SW>;
     constexpr int kSoftWarps = Roles<SW>::kSoftWarps;
@@ -447,6 +481,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
     constexpr int TILE = L::TILE, KTILE = L::KTILE, KST = L::KST, VST = L::VST;
     constexpr int KSTEPS = D / 16;
     static_assert(PREFIX || SW == 2, "the prefill runs two Q tiles per CTA");
+    static_assert(!(PREFIX && WIN), "a shared prefix is visible to every row");
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (PREFIX && p.wait_first) grid_dependency_wait();
@@ -492,7 +527,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
         fence_proxy_async_smem();
     }
     // The CTA's items: the i-th is item_of(i, the (i-1)-th), -1 past the last.
-    if constexpr (!PREFIX) build_schedule<D>(p, smem);
+    if constexpr (!PREFIX) build_schedule<D, WIN>(p, smem);
     const int nlist = PREFIX ? 1 : *reinterpret_cast<volatile int*>(smem + L::SLOT + 8);
     const ListEntry* list = reinterpret_cast<const ListEntry*>(smem + L::LIST);
     auto item_of = [&](int i, int prev) -> int {       // a list position, or a natural index
@@ -501,17 +536,17 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
         } else {
             if (nlist >= 0) return i < nlist ? i : -1;
             for (int it = i == 0 ? (int)blockIdx.x : prev + (int)gridDim.x; it < p.num_items; it += gridDim.x)
-                if (item_at<false>(p, it).live) return it;
+                if (item_at<false, WIN>(p, it).live) return it;
             return -1;
         }
     };
     auto item_get = [&](int idx) -> Item {             // the item item_of gave
         if constexpr (PREFIX) {
-            return item_at<true>(p, 0);
+            return item_at<true, false>(p, 0);
         } else {
-            if (nlist < 0) return item_at<false>(p, idx);
+            if (nlist < 0) return item_at<false, WIN>(p, idx);
             const ListEntry e = list[idx];
-            return finish_item(p, e.it, e.qrow0, e.p0, e.rows);
+            return finish_item<WIN>(p, e.it, e.qrow0, e.p0, e.rows);
         }
     };
     // The copy warps start at once, without the setup barrier of the others: warp 0
@@ -554,13 +589,14 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             for (int i = 0, it = item_of(0, -1); ok && it >= 0; it = item_of(++i, it)) {
                 const Item g = item_get(it);
                 const int ntiles = (g.nblk + kKeyBlocks - 1) / kKeyBlocks;
-                int32_t win = fetch_window(g.trow, 0, g.nblk, lane), win_next = fetch_window(g.trow, 1, g.nblk, lane);
+                int32_t win = fetch_window<WIN>(g.trow, g.v, 0, g.nblk, lane);
+                int32_t win_next = fetch_window<WIN>(g.trow, g.v, 1, g.nblk, lane);
                 int wcur = 0;
                 auto block_of = [&](int j) {
                     while (j / kWinTiles > wcur) {
                         win = win_next;
                         ++wcur;
-                        win_next = fetch_window(g.trow, wcur + 1, g.nblk, lane);
+                        win_next = fetch_window<WIN>(g.trow, g.v, wcur + 1, g.nblk, lane);
                     }
                     return window_block(win, j, lane, g.nblk);
                 };
@@ -700,7 +736,27 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
                 if (hh == 0) {
                     ok = warp_wait(bar(kVFull + st), (t / VST) & 1);
                     if (!ok) return;
-                    if (j == ntiles - 1) {
+                    if constexpr (WIN) {
+                        // V rows hidden from every row of the item may hold anything (even NaN):
+                        // those past its last position, after the last sink and before its first
+                        // row's window
+                        const int ends[3] = {nblk - 1, g.v.sink_blocks - 1, g.first / kBlockTokens - g.v.jump};
+                        bool wrote = false;
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) {
+                            const int b = ends[e] - j * kKeyBlocks;            // block of the tile
+                            if (b < 0 || b >= nb) continue;
+                            const uint32_t vis = visible_slots(g.v.block(ends[e]) * kBlockTokens, g.p_last + 1, g.first, p.sinks);
+                            if (vis == 0xffffu) continue;
+                            uint8_t* vt = smem + L::V + st * KTILE + b * TILE;
+                            for (int idx = lane; idx < (D / 8) * kBlockTokens; idx += 32)
+                                if (!((vis >> (idx % kBlockTokens)) & 1u))
+                                    *reinterpret_cast<uint4*>(vt + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            wrote = true;
+                        }
+                        if (wrote) fence_proxy_async_smem();
+                        __syncwarp();
+                    } else if (j == ntiles - 1) {
                         // V rows past the last attended position may hold anything (even NaN)
                         const int first_stale = g.p_last - (nblk - 1) * kBlockTokens + 1;
                         if (first_stale < kBlockTokens) {
@@ -850,12 +906,15 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
     // derived again for the epilogue: the registers go to the row of S).
     int it = item_of(0, -1);
     int ntiles = 0, pos = 0;
+    int near_from = 0, near_off = 0;      // WIN: listed blocks from near_from on are near_off positions further on
     if (!PREFIX) grid_dependency_wait();                 // the queries may come from a kernel before
     if (it >= 0) {
         const Item g = item_get(it);
         ntiles = (g.nblk + kKeyBlocks - 1) / kKeyBlocks;
         const RowOf r = row_of(g);
         pos = r.pos;
+        near_from = g.v.sink_blocks;
+        near_off = g.v.jump * kBlockTokens;
         load_q(r);
     }
     tc_fence_before();
@@ -898,7 +957,14 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             const int tok0 = j * kKeyTok;
             // every key of the tile is visible to every row of the warp: warp-uniform, so
             // that the warp-collective TMEM stores below run with all 32 lanes
-            const bool full = __all_sync(0xffffffffu, tok0 + kKeyTok - 1 <= pos);
+            bool row_full = tok0 + kKeyTok - 1 <= pos;
+            if constexpr (WIN) {
+                // (a tile with sinks and window blocks both: take the masks)
+                const int b0 = j * kKeyBlocks, t0w = tok0 + (b0 >= near_from ? near_off : 0);
+                row_full = (near_off == 0 || b0 >= near_from || b0 + kKeyBlocks <= near_from) &&
+                           t0w + kKeyTok - 1 <= pos && (pos - t0w < p.window || t0w + kKeyTok <= p.sinks);
+            }
+            const bool full = __all_sync(0xffffffffu, row_full);
             float mx;
             if (full) {
                 // the row maximum of the unscaled scores (c >= 0), four independent chains
@@ -912,6 +978,20 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             } else {
                 // scale and causal mask (select: unread or stale columns may hold NaN)
                 mx = -INFINITY;
+                if constexpr (WIN) {
+                    const int far = min(p.sinks, pos + 1);       // sinks up to the row itself
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int b = j * kKeyBlocks + 2 * c + i / kBlockTokens;
+                            const int tok = tok0 + 32 * c + i + (b >= near_from ? near_off : 0);
+                            const bool see = (uint32_t)(pos - tok) < (uint32_t)p.window || tok < far;
+                            const float x = see ? __uint_as_float(sr[c][i]) * cs : -INFINITY;
+                            sr[c][i] = __float_as_uint(x);
+                            mx = fmaxf(mx, x);
+                        }
+                } else
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -949,9 +1029,12 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             // probabilities, bf16 pairs, over the first 64 columns of S_h (already read), 16
             // columns per store (32 scores: the fewest registers held beside the row); a full
             // tile takes s c - m for two keys in one packed FFMA and sums in pairs
+            // (a row whose window starts in a later tile has no maximum yet: its scores are all
+            // -inf, and their probabilities must be 0, not exp2(-inf + inf))
+            const float m_sub = WIN && m_used == -INFINITY ? 0.f : m_used;
             float sum;
             if (full) {
-                const uint64_t c2 = pack_f32x2(cs, cs), nm2 = pack_f32x2(-m_used, -m_used);
+                const uint64_t c2 = pack_f32x2(cs, cs), nm2 = pack_f32x2(-m_sub, -m_sub);
                 uint64_t sum2[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -974,8 +1057,8 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float e0 = fast_exp2(__uint_as_float(sr[c][i]) - m_used);
-                        const float e1 = fast_exp2(__uint_as_float(sr[c][i + 1]) - m_used);
+                        const float e0 = fast_exp2(__uint_as_float(sr[c][i]) - m_sub);
+                        const float e1 = fast_exp2(__uint_as_float(sr[c][i + 1]) - m_sub);
                         sum += e0 + e1;
                         pk[i >> 1] = pack_bf16x2(e0, e1);
                     }
@@ -991,12 +1074,14 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
         if (!ok) break;
         // the next item's query rows (published once this item's output is read)
         const int it_next = item_of(ic + 1, it);
-        int ntiles_next = 0, pos_next = 0;
+        int ntiles_next = 0, pos_next = 0, near_from_next = 0, near_off_next = 0;
         if (it_next >= 0) {
             const Item gn = item_get(it_next);
             ntiles_next = (gn.nblk + kKeyBlocks - 1) / kKeyBlocks;
             const RowOf rn = row_of(gn);
             pos_next = rn.pos;
+            near_from_next = gn.v.sink_blocks;
+            near_off_next = gn.v.jump * kBlockTokens;
             if (PREFIX || nlist < 0) load_q(rn);          // (else under way since the last tile)
         }
         const RowOf rw = row_of(item_get(it));
@@ -1084,6 +1169,8 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
         it = it_next;
         ntiles = ntiles_next;
         pos = pos_next;
+        near_from = near_from_next;
+        near_off = near_off_next;
     }
     if (!ok) {
         // a wait gave up: the rows of this item and of the CTA's later items are incomplete,
@@ -1130,9 +1217,9 @@ cudaError_t set_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int D, bool PREFIX, int SW>
+template <int D, bool PREFIX, int SW, bool WIN = false>
 cudaError_t launch_tc(const PParams& pp, dim3 grid, cudaStream_t stream) {
-    auto k = tc::prefill_tc_kernel<D, PREFIX, SW>;
+    auto k = tc::prefill_tc_kernel<D, PREFIX, SW, WIN>;
     constexpr int smem = tc::Smem<D, SW>::BYTES;
     cudaError_t e = set_smem(k, smem);
     if (e != cudaSuccess) return e;
@@ -1176,23 +1263,44 @@ int sm_count() {
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
-    PParams pp = common_params(a.q, a.k_pool, a.v_pool, a.block_tables, a.err, a.num_q_heads,
-                               a.num_kv_heads, a.max_blocks, a.num_blocks, a.scale);
+// Fills in the persistent launch of a prefill; no items: nothing to launch.
+static cudaError_t prefill_params(const PrefillArgs& a, PParams& pp, dim3& grid) {
+    pp = common_params(a.q, a.k_pool, a.v_pool, a.block_tables, a.err, a.num_q_heads,
+                       a.num_kv_heads, a.max_blocks, a.num_blocks, a.scale);
     pp.out = a.out;
     pp.start_pos = a.start_pos;
     pp.cu_q = a.cu_q;
     pp.TQ = tc::kRowsTC / pp.G;
     pp.num_seqs = a.num_seqs;
-    pp.nqt = (a.max_chunk + pp.TQ - 1) / pp.TQ;
+    pp.nqt = (int)(((long long)a.max_chunk + pp.TQ - 1) / pp.TQ);
     const long long items = (long long)pp.nqt * pp.Hkv * a.num_seqs;
-    if (items <= 0) return cudaSuccess;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
-    pp.num_items = (int)items;
+    pp.num_items = items > 0 ? (int)items : 0;
     // persistent: one CTA per SM at most (a CTA fills an SM's shared memory and TMEM)
-    const dim3 grid((unsigned)std::min<long long>(items, sm_count()));
+    grid = dim3((unsigned)std::min<long long>(pp.num_items, sm_count()));
+    return cudaSuccess;
+}
+
+cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
+    PParams pp;
+    dim3 grid;
+    const cudaError_t e = prefill_params(a, pp, grid);
+    if (e != cudaSuccess || pp.num_items == 0) return e;
     if (a.head_dim == 64) return launch_tc<64, false, 2>(pp, grid, stream);
     return launch_tc<128, false, 2>(pp, grid, stream);
+}
+
+cudaError_t launch_prefill_window(const PrefillArgs& a, int total_q, int window, int sinks, cudaStream_t stream) {
+    PParams pp;
+    dim3 grid;
+    const cudaError_t e = prefill_params(a, pp, grid);
+    if (e != cudaSuccess || pp.num_items == 0) return e;
+    pp.window = window;
+    pp.sinks = sinks;
+    pp.total_q = total_q;
+    pp.max_chunk = a.max_chunk;
+    if (a.head_dim == 64) return launch_tc<64, false, 2, true>(pp, grid, stream);
+    return launch_tc<128, false, 2, true>(pp, grid, stream);
 }
 
 cudaError_t launch_prefix_tc(const DecodeArgs& a, bool after_suffix, cudaStream_t stream) {
