@@ -474,7 +474,8 @@ pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void*
  * blocks that hold a visible position are read: the table entries between the sinks and
  * the window may be anything (blocks freed and given to others, -1).  A zero-length
  * context gives zeros.  A sequence's result does not depend on the rest of the batch (for
- * the same table width).
+ * the same table width).  For f32 pools the products run on the tensor cores with every
+ * factor as a sum of two tf32 numbers (2^-21 of a product); visible rows must be finite.
  */
 pa_status pa_decode_attention_window(void* out, const void* q, const void* k_pool,
                                      const void* v_pool, const int32_t* block_tables,

@@ -430,49 +430,61 @@ def _bound(x) -> int:
     return min(int(x), 2**31 - 1)
 
 
-def _call_on(device, stream, fn, args) -> None:
-    """Calls a library function on the tensors' device, its current stream by default."""
-    with torch.cuda.device(device):
-        check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+def _call_on(dev: int, stream, fn, args) -> None:
+    """Calls a library function on device `dev`, on its current stream by default."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, args)
+    # (the raw handle: building a Stream object costs as much as the launch)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    status = fn(*args, raw)
+    if status != PA_OK:
+        check(fn.__name__, status)
 
 
-def _checked(dev, t, name, dtype, shape):
-    """Address of a contiguous tensor of this device, type and shape."""
+def _refuse(dev, t, name, dtype, shape):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the pools' device")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _checked(dev, t, name, dtype, shape):
+    """Address of a contiguous tensor of this device (an index), type and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev >= 0 and t.is_contiguous()):
+        _refuse(dev, t, name, dtype, shape)
     return t.data_ptr()
 
 
 def _rows(dev, t, name, dtype, shape):
     """Address and row stride of rows [n][heads][head_dim] whose rows may lie apart."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev >= 0):
+        _refuse(dev, t, name, dtype, shape)
     n, heads, d = shape
-    if n and ((d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d)):
+    stride = t.stride()
+    if n and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d)
+    return t.data_ptr(), (stride[0] if n > 1 else heads * d)
+
+
+def _flag(dev, err_flag):
+    if err_flag is None:
+        return None
+    return _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)
 
 
 def _pools(k_pool, v_pool, dims):
     nb, hkv, d = dims(k_pool)
-    dev = k_pool.device
-    kp = _checked(dev, k_pool, "k_pool", k_pool.dtype, k_pool.shape)
-    vp = _checked(dev, v_pool, "v_pool", k_pool.dtype, k_pool.shape)
-    return dev, nb, hkv, d, kp, vp
+    dev, shape = k_pool.get_device(), k_pool.shape
+    return (dev, nb, hkv, d, _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
+            _checked(dev, v_pool, "v_pool", k_pool.dtype, shape))
 
 
 def _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
@@ -488,12 +500,12 @@ def _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
     qo, qos = (None, 0) if q is None else _rows(dev, q_out, "q_out", rows, (n, hq, d))
     freq = _checked(dev, inv_freq, "inv_freq", torch.float64, (inv_freq.shape[0],))
     width = block_tables.shape[1]
-    _call_on(dev, stream, "pa_rope_append_kv", (
+    _call_on(dev, stream, lib().pa_rope_append_kv, (
         kp, vp, qo, qi, kn, vn, qos, qs, ks, vs, freq, 2 * inv_freq.shape[0], int(bool(interleaved)),
         _checked(dev, block_tables, "block_tables", torch.int32, (s, width)), width,
         _checked(dev, start_pos, "start_pos", torch.int32, (s,)),
         _checked(dev, cu_new_tokens, "cu_new_tokens", torch.int32, (s + 1,)), s, n, nb, hq, hkv, d, code,
-        None if err_flag is None else _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)))
+        _flag(dev, err_flag)))
 
 
 def rope_append_kv(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
@@ -526,12 +538,12 @@ def _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, wi
     dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, dims)
     s, hq = q.shape[0], q.shape[1]
     width = block_tables.shape[1]
-    _call_on(dev, stream, "pa_decode_attention_window", (
+    _call_on(dev, stream, lib().pa_decode_attention_window, (
         _checked(dev, out, "out", rows, (s, hq, d)), _checked(dev, q, "q", rows, (s, hq, d)), kp, vp,
         _checked(dev, block_tables, "block_tables", torch.int32, (s, width)),
         _checked(dev, context_lens, "context_lens", torch.int32, (s,)), s, hq, hkv, d, width, nb,
         _bound(window), _bound(num_sinks), float(scale), code,
-        None if err_flag is None else _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)))
+        _flag(dev, err_flag)))
 
 
 def decode_attention_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window: int,
@@ -566,13 +578,13 @@ def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu
     code = _dtype_code(k_pool)
     n, hq, s = q.shape[0], q.shape[1], start_pos.shape[0]
     width = block_tables.shape[1]
-    _call_on(dev, stream, "pa_prefill_attention_window", (
+    _call_on(dev, stream, lib().pa_prefill_attention_window, (
         _checked(dev, out, "out", k_pool.dtype, (n, hq, d)), _checked(dev, q, "q", k_pool.dtype, (n, hq, d)),
         kp, vp, _checked(dev, block_tables, "block_tables", torch.int32, (s, width)), width,
         _checked(dev, start_pos, "start_pos", torch.int32, (s,)),
         _checked(dev, cu_q, "cu_q", torch.int32, (s + 1,)), s, n, _bound(max_chunk), hq, hkv, d, nb,
         _bound(window), _bound(num_sinks), float(scale), code,
-        None if err_flag is None else _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)))
+        _flag(dev, err_flag)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024

@@ -8,14 +8,18 @@
 // blocks, then the window's), so the work does not grow with the context, and a cache may
 // free the blocks between; hidden slots of a listed block are masked, whatever they hold.
 //
-// One warp-level pass over the keys with a running maximum and sum (fp32): each warp takes
-// every NW-th listed block through a private ring of shared-memory stages, two bulk copies
-// (K and V tile of the (block, kv head)) per stage on its mbarrier.  Scores of 16 tokens x 8
-// heads (the kv head's G <= 8 query heads) come from the tensor cores (mma.sync, tokens on M),
-// probabilities are transposed in registers and multiplied with V on the tensor cores again;
-// the f32 cache uses FMAs, for fp32 accuracy.  The bound is HBM: about G operations per byte.
+// One warp-level pass over the keys with a running maximum and sum (fp32): the listed blocks
+// go to the warps in pairs, through private shared-memory stages filled by bulk copies.  A
+// stage's K half and V half have an mbarrier each: K is refilled as soon as the scores are
+// taken, V after the products.  Scores of 32 tokens x 8 heads (the kv head's G <= 8 query
+// heads) come from the tensor cores (mma.sync, tokens on M), the probabilities are transposed
+// in registers and multiplied with V on the tensor cores again.  Two blocks at a time because
+// the chain scores -> maximum -> probabilities -> products is what a warp waits for when few
+// CTAs run, and its shuffles and rescaling are shared by the pair.  The bound is HBM: about G
+// operations per byte.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "pa_ptx.cuh"
@@ -28,6 +32,18 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 200000000ull;   // 200 ms: a real tile copy takes microseconds
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kWarps = 4;
+// Blocks of a part, at least.  A part's end costs a warp about as much as two blocks (FP4:
+// four, with its scale references to set again), so longer parts are cheaper where one CTA
+// goes through all of them and shorter ones faster where each has its own CTA.  On GB300, 32
+// against 64 blocks at 32 / 8 heads of 128: bf16, one sequence, window 4096: 9.9 / 12.4 us;
+// FP4, 128 sequences, window 2047: 97.5 / 91.0 us.
+constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 64 : 32; }
+// (sequence, kv head) pairs below which each part gets a CTA of its own.  At 32 / 8 heads of
+// 128, bf16, window 4096, a CTA per part against one for all: 9.9 / 40.1 us for one sequence,
+// 16.9 / 41.0 for 4, but 55.5 / 46.7 for 16 and 692 / 581 for 256 (a cluster's CTAs start
+// together and wait for one another); with window 2048 and 8 sequences 16.0 / 22.9.
+constexpr int kSplitBelow = 65;
 
 struct WParams {
     void* out;
@@ -39,25 +55,40 @@ struct WParams {
     int32_t* err;
     int Hq, Hkv, G, max_blocks, num_blocks;
     int window, sinks;
+    int part_len;            // listed blocks of a part
+    int split;               // a CTA per part, in clusters; else a CTA goes through all parts
     float scale_log2;
 };
 
-// Running maxima (log2 units) and this lane's share of the sums of heads 2c, 2c + 1.
+// Running maxima (log2 units) and this lane's share of the sums of heads 2c, 2c + 1, and the
+// factors that the last pair's maxima put on what was summed before.
 struct Running {
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float al0 = 1.f, al1 = 1.f;
+    bool rescale = false;        // any lane's factor is not 1
 };
 
-// The cache types.  A lane is r = lane / 4, c = lane % 4; it holds the scores of two tokens,
-// lo() and hi() of the block, for heads 2c and 2c + 1.  o[mi] accumulates dims 16 mi + r, + 8
-// of the same heads.
+template <int KS>
+__device__ __forceinline__ void rescale_rows(const Running& run, float (&o)[KS][4]) {
+#pragma unroll
+    for (int mi = 0; mi < KS; ++mi) {
+        o[mi][0] *= run.al0; o[mi][1] *= run.al1; o[mi][2] *= run.al0; o[mi][3] *= run.al1;
+    }
+}
+
+// The cache types.  A lane is r = lane / 4, c = lane % 4; of each block it holds the scores of
+// two tokens, lo() and hi(), for heads 2c and 2c + 1: s[0..1] and s[2..3].  o[mi] accumulates
+// dims 16 mi + r, + 8 of the same heads.
 
 template <int D>
 struct Bf16Cache {
+    using Out = __nv_bfloat16;
     static constexpr int TILE = kBlockTokens * D * 2;         // bytes of a (block, kv head) tile
     static constexpr int KS = D / 16;
+    static constexpr int SCRATCH = 0;
     uint32_t qb[KS][2];                                       // query fragments (B operand)
     int lane, r, c;
-    __device__ __forceinline__ Bf16Cache(int lane_) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {}
+    __device__ __forceinline__ Bf16Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {}
     __device__ __forceinline__ int lo() const { return r; }
     __device__ __forceinline__ int hi() const { return r + 8; }
     __device__ __forceinline__ void load_q(const void* q, size_t row0, int G) {
@@ -68,45 +99,56 @@ struct Bf16Cache {
             qb[kk][1] = r < G ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8 + 2 * c) : 0u;
         }
     }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
         const uint32_t addr = smem_u32(kt) + lane * 16;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[2][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-            uint32_t a0, a1, a2, a3;
-            ldmatrix_x4(addr + kk * 512, a0, a1, a2, a3);
-            mma_bf16_16816(acc, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
-        }
+        for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = acc[i] * scale;
+            for (int b = 0; b < 2; ++b) {
+                uint32_t a0, a1, a2, a3;
+                ldmatrix_x4(addr + b * TILE + kk * 512, a0, a1, a2, a3);
+                mma_bf16_16816(acc[b], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+            }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[b][i] = acc[b][i] * scale;
+    }
+    // Hidden slots of a V tile may hold anything (even NaN): zero them, 16-byte pieces of 16 slots.
+    __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
+        for (int i = lane; i < TILE / 16; i += 32)
+            if (!((vis >> (i % kBlockTokens)) & 1u)) *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
     // Probabilities are rounded to bf16 for the tensor cores, and the sums take the rounded
     // ones, so that a weighted mean of equal values stays exact.
-    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[4], uint32_t vis, bool, bool,
-                                       Running& run, float al0, float al1, bool rescale, float (&o)[KS][4]) {
-        const uint32_t x0 = pack_bf16x2(pr[0], pr[1]), x1 = pack_bf16x2(pr[2], pr[3]);
-        run.l0 = run.l0 * al0 + (bf16_lo_to_f32(x0) + bf16_lo_to_f32(x1));
-        run.l1 = run.l1 * al1 + (bf16_hi_to_f32(x0) + bf16_hi_to_f32(x1));
-        const uint32_t pb0 = movmatrix_trans(x0), pb1 = movmatrix_trans(x1);
-        // V^T fragments hold tokens 2c, 2c+1 (regs 0, 1) and 2c+8, 2c+9 (regs 2, 3); hidden
-        // slots may hold anything (even NaN), so zero them
-        uint32_t ma = 0xffffffffu, mb = 0xffffffffu;
-        if (vis != 0xffffu) {
-            const uint32_t w = vis >> (2 * c);
-            ma = ((w & 1u) ? 0x0000ffffu : 0u) | ((w & 2u) ? 0xffff0000u : 0u);
-            mb = ((w & 0x100u) ? 0x0000ffffu : 0u) | ((w & 0x200u) ? 0xffff0000u : 0u);
+    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[2][4], Running& run,
+                                       float (&o)[KS][4]) {
+        uint32_t pb[2][2];
+        run.l0 *= run.al0;
+        run.l1 *= run.al1;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t x0 = pack_bf16x2(pr[b][0], pr[b][1]), x1 = pack_bf16x2(pr[b][2], pr[b][3]);
+            run.l0 += bf16_lo_to_f32(x0) + bf16_lo_to_f32(x1);
+            run.l1 += bf16_hi_to_f32(x0) + bf16_hi_to_f32(x1);
+            pb[b][0] = movmatrix_trans(x0);
+            pb[b][1] = movmatrix_trans(x1);
         }
+        if (run.rescale) rescale_rows(run, o);
         const int vm = lane >> 3;
         const uint32_t addr = smem_u32(vt) + (uint32_t)(((vm & 1) * 16 + (vm >> 1) * 8 + (lane & 7)) * 16);
 #pragma unroll
-        for (int mi = 0; mi < KS; ++mi) {
-            uint32_t v0, v1, v2, v3;
-            ldmatrix_x4_trans(addr + mi * 512, v0, v1, v2, v3);
-            v0 &= ma; v1 &= ma; v2 &= mb; v3 &= mb;
-            if (rescale) { o[mi][0] *= al0; o[mi][1] *= al1; o[mi][2] *= al0; o[mi][3] *= al1; }
-            mma_bf16_16816(o[mi], v0, v1, v2, v3, pb0, pb1);
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int mi = 0; mi < KS; ++mi) {
+                uint32_t v0, v1, v2, v3;
+                ldmatrix_x4_trans(addr + b * TILE + mi * 512, v0, v1, v2, v3);
+                mma_bf16_16816(o[mi], v0, v1, v2, v3, pb[b][0], pb[b][1]);
+            }
         }
     }
+    __device__ __forceinline__ void reset() {}
     __device__ __forceinline__ void finish(Running&, float (&)[KS][4]) {}
 };
 
@@ -118,12 +160,14 @@ struct Bf16Cache {
 //   to keep the product in f16's normal range (taken out of the sums at the end).
 template <int D>
 struct Fp8Cache {
+    using Out = __nv_bfloat16;
     static constexpr int TILE = 16 * D + 64;
     static constexpr int KS = D / 16;
+    static constexpr int SCRATCH = 0;
     static constexpr float kPScale = 256.f;
     uint32_t qb[KS][2];
     int lane, r, c;
-    __device__ __forceinline__ Fp8Cache(int lane_) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {}
+    __device__ __forceinline__ Fp8Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {}
     __device__ __forceinline__ int lo() const { return 4 * (r >> 1) + (r & 1); }
     __device__ __forceinline__ int hi() const { return lo() + 2; }
     __device__ __forceinline__ void load_q(const void* q, size_t row0, int G) {
@@ -138,84 +182,115 @@ struct Fp8Cache {
     static __device__ __forceinline__ uint32_t half(uint32_t x, int i) {
         return e4m3x2_to_f16x2((uint16_t)(i ? x >> 16 : x & 0xffffu));
     }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
         const int km = lane >> 3, kr = lane & 7;
         const int tok = 4 * (kr >> 1) + (kr & 1) + ((km & 1) ? 2 : 0);
         const uint32_t addr = smem_u32(kt) + (uint32_t)(((km >> 1) * kBlockTokens + tok) * 16);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[2][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < KS; kk += 2) {
-            uint32_t x0, x1, x2, x3;
-            ldmatrix_x4(addr + kk * 256, x0, x1, x2, x3);
-            mma_f16_16816(acc, half(x0, 0), half(x1, 0), half(x0, 1), half(x1, 1), qb[kk][0], qb[kk][1]);
-            mma_f16_16816(acc, half(x2, 0), half(x3, 0), half(x2, 1), half(x3, 1), qb[kk + 1][0], qb[kk + 1][1]);
+        for (int kk = 0; kk < KS; kk += 2)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t x0, x1, x2, x3;
+                ldmatrix_x4(addr + b * TILE + kk * 256, x0, x1, x2, x3);
+                mma_f16_16816(acc[b], half(x0, 0), half(x1, 0), half(x0, 1), half(x1, 1), qb[kk][0], qb[kk][1]);
+                mma_f16_16816(acc[b], half(x2, 0), half(x3, 0), half(x2, 1), half(x3, 1), qb[kk + 1][0], qb[kk + 1][1]);
+            }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float* ks = reinterpret_cast<const float*>(kt + b * TILE + 16 * D);
+            const float s0 = ks[lo()] * scale, s1 = ks[hi()] * scale;
+            s[b][0] = acc[b][0] * s0;
+            s[b][1] = acc[b][1] * s0;
+            s[b][2] = acc[b][2] * s1;
+            s[b][3] = acc[b][3] * s1;
         }
-        const float* ks = reinterpret_cast<const float*>(kt + 16 * D);
-        const float s0 = ks[lo()] * scale, s1 = ks[hi()] * scale;
-        s[0] = acc[0] * s0;
-        s[1] = acc[1] * s0;
-        s[2] = acc[2] * s1;
-        s[3] = acc[3] * s1;
     }
-    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[4], uint32_t vis, bool ok0, bool ok1,
-                                       Running& run, float al0, float al1, bool rescale, float (&o)[KS][4]) {
-        run.l0 = run.l0 * al0 + (pr[0] + pr[2]);
-        run.l1 = run.l1 * al1 + (pr[1] + pr[3]);
-        // hidden slots carry arbitrary scales (even inf): select rather than multiply
-        const float* vs = reinterpret_cast<const float*>(vt + 16 * D);
-        const float v0 = vs[lo()] * kPScale, v1 = vs[hi()] * kPScale;
-        const uint32_t pb0 = movmatrix_trans(pack_f16x2(ok0 ? pr[0] * v0 : 0.f, ok0 ? pr[1] * v0 : 0.f));
-        const uint32_t pb1 = movmatrix_trans(pack_f16x2(ok1 ? pr[2] * v1 : 0.f, ok1 ? pr[3] * v1 : 0.f));
-        // a V register holds tokens 4c .. 4c+3 of one dim: hidden ones' codes may be NaN
-        uint32_t vm = 0xffffffffu;
-        if (vis != 0xffffu) {
-            const uint32_t w = vis >> (4 * c);
-            vm = ((w & 1u) ? 0xffu : 0u) | ((w & 2u) ? 0xff00u : 0u) | ((w & 4u) ? 0xff0000u : 0u) |
-                 ((w & 8u) ? 0xff000000u : 0u);
+    // Hidden slots may hold anything (NaN codes, scales of inf): a dim's 16 slots are 16 bytes.
+    __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
+        uint32_t m[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t v = vis >> (4 * w);
+            m[w] = ((v & 1u) ? 0xffu : 0u) | ((v & 2u) ? 0xff00u : 0u) | ((v & 4u) ? 0xff0000u : 0u) | ((v & 8u) ? 0xff000000u : 0u);
         }
+        for (int d = lane; d < D; d += 32) {
+            uint4* row = reinterpret_cast<uint4*>(vt + d * 16);
+            const uint4 x = *row;
+            *row = make_uint4(x.x & m[0], x.y & m[1], x.z & m[2], x.w & m[3]);
+        }
+        if (lane < kBlockTokens && !((vis >> lane) & 1u)) *reinterpret_cast<float*>(vt + 16 * D + 4 * lane) = 0.f;
+    }
+    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[2][4], Running& run,
+                                       float (&o)[KS][4]) {
+        uint32_t pb[2][2];
+        run.l0 = run.l0 * run.al0 + ((pr[0][0] + pr[0][2]) + (pr[1][0] + pr[1][2]));
+        run.l1 = run.l1 * run.al1 + ((pr[0][1] + pr[0][3]) + (pr[1][1] + pr[1][3]));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float* vs = reinterpret_cast<const float*>(vt + b * TILE + 16 * D);
+            const float v0 = vs[lo()] * kPScale, v1 = vs[hi()] * kPScale;
+            pb[b][0] = movmatrix_trans(pack_f16x2(pr[b][0] * v0, pr[b][1] * v0));
+            pb[b][1] = movmatrix_trans(pack_f16x2(pr[b][2] * v1, pr[b][3] * v1));
+        }
+        if (run.rescale) rescale_rows(run, o);
         const uint32_t addr = smem_u32(vt) + lane * 16;
 #pragma unroll
-        for (int mi = 0; mi < KS; mi += 2) {
-            uint32_t y[4];                       // dims 16 mi .. + 7, + 8 .., 16 (mi + 1) .., + 8 ..
-            ldmatrix_x4(addr + mi * 256, y[0], y[1], y[2], y[3]);
+        for (int b = 0; b < 2; ++b) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float(&om)[4] = o[mi + x];
-                const uint32_t ya = y[2 * x] & vm, yb = y[2 * x + 1] & vm;
-                if (rescale) { om[0] *= al0; om[1] *= al1; om[2] *= al0; om[3] *= al1; }
-                mma_f16_16816(om, half(ya, 0), half(yb, 0), half(ya, 1), half(yb, 1), pb0, pb1);
+            for (int mi = 0; mi < KS; mi += 2) {
+                uint32_t y[4];                       // dims 16 mi .. + 7, + 8 .., 16 (mi + 1) .., + 8 ..
+                ldmatrix_x4(addr + b * TILE + mi * 256, y[0], y[1], y[2], y[3]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t ya = y[2 * x], yb = y[2 * x + 1];
+                    mma_f16_16816(o[mi + x], half(ya, 0), half(yb, 0), half(ya, 1), half(yb, 1), pb[b][0], pb[b][1]);
+                }
             }
         }
     }
+    __device__ __forceinline__ void reset() {}
     __device__ __forceinline__ void finish(Running& run, float (&)[KS][4]) {
         run.l0 *= kPScale;                       // the products carry the same factor
         run.l1 *= kPScale;
     }
 };
 
+// The first product of a sum: D = A B.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // MXFP4 records: codes become f16 in registers (exact).
 //   K: the scale varies along the dot product, so each 32-dim block of it is a product of
 //   its own, times the token's scale, summed in fp32.
 //   V: the scale varies along the tokens, so it multiplies the probabilities: block b's dims
-//   take P_b = p 2^(e_b(t) - 127) c_b with c_b = 2^(135 - R_b), R_b the largest scale code of
-//   block b so far (raised, and the block's accumulators rescaled, when a tile brings a
-//   larger one), so that P_b stays at most 2^8, in f16's range.
+//   take P_b = p 2^(e_b(t) - 127) c_b with c_b = 2^(135 - R_b), R_b at least the largest scale
+//   code of block b so far (raised, and the block's accumulators rescaled, when a pair brings
+//   a larger one), so that P_b stays at most 2^8, in f16's range.
 template <int D>
 struct Fp4Cache {
+    using Out = __nv_bfloat16;
     static constexpr int TILE = 8 * D + D / 2;
     static constexpr int KS = D / 16;
+    static constexpr int SCRATCH = 0;
     static constexpr int NB = D / 32;                         // scale blocks of a row
     uint32_t qb[KS][2];
-    int ref[NB];
     float cb[NB];
-    uint32_t ref_packed = 0;
+    uint32_t ref_packed;                                      // the R_b, a byte each
     int lane, r, c;
-    __device__ __forceinline__ Fp4Cache(int lane_) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {
+    __device__ __forceinline__ Fp4Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {
+        reset();
+    }
+    __device__ __forceinline__ void reset() {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            ref[b] = 0;
-            cb[b] = exp2i(127);
-        }
+        for (int b = 0; b < NB; ++b) cb[b] = exp2i(127);
+        ref_packed = 0;
     }
     __device__ __forceinline__ int lo() const { return r; }
     __device__ __forceinline__ int hi() const { return r + 8; }
@@ -233,78 +308,103 @@ struct Fp4Cache {
         if constexpr (NB == 4) return *reinterpret_cast<const uint32_t*>(at);
         else return *reinterpret_cast<const uint16_t*>(at);
     }
+    // N adjacent 32-bit words
+    template <int N>
+    static __device__ __forceinline__ void words(const uint8_t* at, uint32_t (&w)[N]) {
+        if constexpr (N % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(at + 4 * i);
+                w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+            }
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
+            w[0] = v.x; w[1] = v.y;
+        }
+    }
     // scale byte b of w: 2^(code - 127) (the code is the exponent field; code 0 gives 0)
     static __device__ __forceinline__ float scale_value(uint32_t w, int b) {
         return __uint_as_float(((w >> (8 * b)) & 0xffu) << 23);
     }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[4]) const {
-        uint32_t k0[NB], k1[NB];
+    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
 #pragma unroll
-        for (int w = 0; w < NB; ++w) {
-            k0[w] = *reinterpret_cast<const uint32_t*>(kt + r * (D / 2) + c * (D / 8) + 4 * w);
-            k1[w] = *reinterpret_cast<const uint32_t*>(kt + (r + 8) * (D / 2) + c * (D / 8) + 4 * w);
-        }
-        const uint32_t e0 = scale_bytes(kt + 8 * D + r * NB), e1 = scale_bytes(kt + 8 * D + (r + 8) * NB);
-        s[0] = s[1] = s[2] = s[3] = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uint32_t a[4], a8[4];
-            e2m1x8_to_f16x2x4(k0[b], a);
-            e2m1x8_to_f16x2x4(k1[b], a8);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(acc, a[0], a8[0], a[1], a8[1], qb[2 * b][0], qb[2 * b][1]);
-            mma_f16_16816(acc, a[2], a8[2], a[3], a8[3], qb[2 * b + 1][0], qb[2 * b + 1][1]);
-            const float f0 = scale_value(e0, b) * scale, f1 = scale_value(e1, b) * scale;
-            s[0] = fmaf(acc[0], f0, s[0]);
-            s[1] = fmaf(acc[1], f0, s[1]);
-            s[2] = fmaf(acc[2], f1, s[2]);
-            s[3] = fmaf(acc[3], f1, s[3]);
-        }
-    }
-    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[4], uint32_t, bool ok0, bool ok1,
-                                       Running& run, float al0, float al1, bool rescale, float (&o)[KS][4]) {
-        run.l0 = run.l0 * al0 + (pr[0] + pr[2]);
-        run.l1 = run.l1 * al1 + (pr[1] + pr[3]);
-        // hidden slots count with scale code 0 (their codes are finite whatever they are)
-        const uint32_t e0 = ok0 ? scale_bytes(vt + 8 * D + r * NB) : 0u;
-        const uint32_t e1 = ok1 ? scale_bytes(vt + 8 * D + (r + 8) * NB) : 0u;
-        uint32_t top = __vmaxu4(e0, e1);
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, x));
-        if (__vmaxu4(top, ref_packed) != ref_packed) {        // warp-uniform, rare after the first tile
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t* k = kt + t * TILE;
+            uint32_t k0[NB], k1[NB];
+            words<NB>(k + r * (D / 2) + c * (D / 8), k0);
+            words<NB>(k + (r + 8) * (D / 2) + c * (D / 8), k1);
+            const uint32_t e0 = scale_bytes(k + 8 * D + r * NB), e1 = scale_bytes(k + 8 * D + (r + 8) * NB);
+            s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int eb = (int)((top >> (8 * b)) & 0xffu);
-                if (eb > ref[b]) {
-                    const float cn = exp2i(min(135 - eb, 127)), f = cn / cb[b];    // a power of two: exact
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        o[2 * b][x] *= f;
-                        o[2 * b + 1][x] *= f;
-                    }
-                    ref[b] = eb;
-                    cb[b] = cn;
-                }
+                uint32_t a[4], a8[4];
+                e2m1x8_to_f16x2x4(k0[b], a);
+                e2m1x8_to_f16x2x4(k1[b], a8);
+                float acc[4];
+                mma_f16_zero(acc, a[0], a8[0], a[1], a8[1], qb[2 * b][0], qb[2 * b][1]);
+                mma_f16_16816(acc, a[2], a8[2], a[3], a8[3], qb[2 * b + 1][0], qb[2 * b + 1][1]);
+                const float f0 = scale_value(e0, b), f1 = scale_value(e1, b);
+                s[t][0] = fmaf(acc[0], f0, s[t][0]);
+                s[t][1] = fmaf(acc[1], f0, s[t][1]);
+                s[t][2] = fmaf(acc[2], f1, s[t][2]);
+                s[t][3] = fmaf(acc[3], f1, s[t][3]);
             }
-            ref_packed = __vmaxu4(top, ref_packed);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][i] *= scale;
         }
-        if (rescale) {
+    }
+    // Hidden slots count with scale code 0 (their codes are finite whatever they are).
+    __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
+        if (lane < kBlockTokens && !((vis >> lane) & 1u))
 #pragma unroll
-            for (int mi = 0; mi < KS; ++mi) { o[mi][0] *= al0; o[mi][1] *= al1; o[mi][2] *= al0; o[mi][3] *= al1; }
+            for (int b = 0; b < NB; ++b) vt[8 * D + lane * NB + b] = 0;
+    }
+    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[2][4], Running& run,
+                                       float (&o)[KS][4]) {
+        run.l0 = run.l0 * run.al0 + ((pr[0][0] + pr[0][2]) + (pr[1][0] + pr[1][2]));
+        run.l1 = run.l1 * run.al1 + ((pr[0][1] + pr[0][3]) + (pr[1][1] + pr[1][3]));
+        uint32_t e0[2], e1[2], top = 0u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t* sc = vt + t * TILE + 8 * D;
+            e0[t] = scale_bytes(sc + r * NB);
+            e1[t] = scale_bytes(sc + (r + 8) * NB);
+            top = __vmaxu4(top, __vmaxu4(e0[t], e1[t]));
         }
-        uint32_t vw[KS];
 #pragma unroll
-        for (int w = 0; w < KS; ++w) vw[w] = *reinterpret_cast<const uint32_t*>(vt + (r * 4 + c) * (KS * 4) + 4 * w);
+        for (int x = 4; x < 32; x <<= 1) top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, x));
+        if (__vmaxu4(top, ref_packed) != ref_packed) {        // warp-uniform, rare after a part's first pair
+            // (three octaves above the largest seen, so that the next ones hardly raise it again)
+            const uint32_t raised = __vmaxu4(__vaddus4(top, 0x03030303u), ref_packed);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const float g0 = scale_value(e0, b) * cb[b], g1 = scale_value(e1, b) * cb[b];
-            const uint32_t pb0 = movmatrix_trans(pack_f16x2(pr[0] * g0, pr[1] * g0));
-            const uint32_t pb1 = movmatrix_trans(pack_f16x2(pr[2] * g1, pr[3] * g1));
+            for (int b = 0; b < NB; ++b) {
+                const int eb = (int)((raised >> (8 * b)) & 0xffu);
+                const float cn = exp2i(min(135 - eb, 127)), f = cn / cb[b];        // a power of two: exact
 #pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-                uint32_t a[4];
-                e2m1x8_to_f16x2x4(vw[2 * b + h2], a);
-                mma_f16_16816(o[2 * b + h2], a[0], a[2], a[1], a[3], pb0, pb1);
+                for (int x = 0; x < 4; ++x) {
+                    o[2 * b][x] *= f;
+                    o[2 * b + 1][x] *= f;
+                }
+                cb[b] = cn;
+            }
+            ref_packed = raised;
+        }
+        if (run.rescale) rescale_rows(run, o);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t vw[KS];
+            words<KS>(vt + t * TILE + (r * 4 + c) * (KS * 4), vw);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float g0 = scale_value(e0[t], b) * cb[b], g1 = scale_value(e1[t], b) * cb[b];
+                const uint32_t pb0 = movmatrix_trans(pack_f16x2(pr[t][0] * g0, pr[t][1] * g0));
+                const uint32_t pb1 = movmatrix_trans(pack_f16x2(pr[t][2] * g1, pr[t][3] * g1));
+#pragma unroll
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    uint32_t a[4];
+                    e2m1x8_to_f16x2x4(vw[2 * b + h2], a);
+                    mma_f16_16816(o[2 * b + h2], a[0], a[2], a[1], a[3], pb0, pb1);
+                }
             }
         }
     }
@@ -321,34 +421,153 @@ struct Fp4Cache {
     }
 };
 
-// Shared memory: the stage rings (reused at the end by the warps' results: 8 rows of D + 4
-// floats each, their maxima and sums), then the barriers.
-template <int D, int TILE, int NW, int NST>
-struct Layout {
-    static constexpr int OS = D + 4;
-    static constexpr int RING = NW * NST * 2 * TILE;
-    static constexpr int MERGE = NW * 8 * (OS + 2) * 4;
-    static constexpr int BAR = ((RING > MERGE ? RING : MERGE) + 15) / 16 * 16;
-    static constexpr int BYTES = BAR + NW * NST * 8;
+// f32 tiles: each operand x is split into two tf32 numbers, h (x rounded) and l (x - h
+// rounded), and a product is h h' + h l' + l h' on the tensor cores: the dropped l l' and the
+// roundings of l are 2^-21 of the product at most, near fp32's own rounding, and the work does
+// not grow with G as with FMAs.  K and V fragments are plain 32-bit reads of the tiles (K's
+// are free of bank conflicts, V's two-way); the probabilities pass through 512 bytes of
+// shared memory per warp to reach the B operand's order.
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+    uint32_t y;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+    return y;
+}
+struct Split { uint32_t h, l; };
+__device__ __forceinline__ Split split_tf32(float x) {
+    Split s;
+    s.h = tf32_of(x);
+    s.l = tf32_of(x - __uint_as_float(s.h));
+    return s;
+}
+__device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += a b over 8 of the contraction's elements, a in fp32 (4 per lane), b split
+__device__ __forceinline__ void mma_split(float (&d)[4], const float (&a)[4], Split b0, Split b1) {
+    Split x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = split_tf32(a[i]);
+    mma_tf32_1688(d, x[0].l, x[1].l, x[2].l, x[3].l, b0.h, b1.h);
+    mma_tf32_1688(d, x[0].h, x[1].h, x[2].h, x[3].h, b0.l, b1.l);
+    mma_tf32_1688(d, x[0].h, x[1].h, x[2].h, x[3].h, b0.h, b1.h);
+}
+
+template <int D>
+struct F32Cache {
+    using Out = float;
+    static constexpr int TILE = kBlockTokens * D * 4;
+    static constexpr int KS = D / 16;
+    static constexpr int SCRATCH = 32 * 8 * 4;                // a warp's probabilities, [32 tokens][8 heads]
+    float q[D / 8][2];
+    float* sp;
+    int lane, r, c;
+    __device__ __forceinline__ F32Cache(int lane_, float* scratch) : sp(scratch), lane(lane_), r(lane_ >> 2), c(lane_ & 3) {}
+    __device__ __forceinline__ int lo() const { return r; }
+    __device__ __forceinline__ int hi() const { return r + 8; }
+    __device__ __forceinline__ void load_q(const void* q_, size_t row0, int G) {
+        const float* qrow = static_cast<const float*>(q_) + (row0 + (r < G ? r : 0)) * D;
+#pragma unroll
+        for (int kk = 0; kk < D / 8; ++kk) {
+            q[kk][0] = r < G ? qrow[8 * kk + c] : 0.f;
+            q[kk][1] = r < G ? qrow[8 * kk + 4 + c] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
+        const float* k = reinterpret_cast<const float*>(kt);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 8; ++kk) {
+            const Split b0 = split_tf32(q[kk][0]), b1 = split_tf32(q[kk][1]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float* at = k + b * (TILE / 4) + (2 * kk * kBlockTokens + r) * 4 + c;
+                const float a[4] = {at[0], at[32], at[64], at[96]};
+                mma_split(s[b], a, b0, b1);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[b][i] *= scale;
+    }
+    // (as for bf16)
+    __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
+        for (int i = lane; i < TILE / 16; i += 32)
+            if (!((vis >> (i % kBlockTokens)) & 1u)) *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[2][4], Running& run,
+                                       float (&o)[KS][4]) {
+        run.l0 = run.l0 * run.al0 + ((pr[0][0] + pr[0][2]) + (pr[1][0] + pr[1][2]));
+        run.l1 = run.l1 * run.al1 + ((pr[0][1] + pr[0][3]) + (pr[1][1] + pr[1][3]));
+        __syncwarp();                                         // (the last pair's reads are done)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            *reinterpret_cast<float2*>(sp + (16 * b + r) * 8 + 2 * c) = make_float2(pr[b][0], pr[b][1]);
+            *reinterpret_cast<float2*>(sp + (16 * b + r + 8) * 8 + 2 * c) = make_float2(pr[b][2], pr[b][3]);
+        }
+        __syncwarp();
+        if (run.rescale) rescale_rows(run, o);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {                      // 8 tokens at a time: c and c + 4 of them
+            const int t0 = 8 * (kk & 1) + c, b = kk >> 1;
+            const Split b0 = split_tf32(sp[(16 * b + t0) * 8 + r]), b1 = split_tf32(sp[(16 * b + t0 + 4) * 8 + r]);
+            const float* v = reinterpret_cast<const float*>(vt) + b * (TILE / 4) + ((r >> 2) * kBlockTokens + t0) * 4 + (r & 3);
+#pragma unroll
+            for (int mi = 0; mi < KS; ++mi) {
+                const float* at = v + mi * (4 * kBlockTokens * 4);
+                const float a[4] = {at[0], at[2 * kBlockTokens * 4], at[16], at[2 * kBlockTokens * 4 + 16]};
+                mma_split(o[mi], a, b0, b1);
+            }
+        }
+    }
+    __device__ __forceinline__ void reset() {}
+    __device__ __forceinline__ void finish(Running&, float (&)[KS][4]) {}
 };
 
-// The listed blocks of one sequence as one warp walks them: entry i of this warp is listed
-// block first + i * NW, and the table entries are read 32 at a time.
+// Shared memory: the warps' stages, each the K tiles then the V tiles of a pair of blocks;
+// the warps' scratch; the barriers, two per stage; and the warps' folded results: G rows of
+// D + 4 floats, then their maxima and sums.
+template <class C, int D, int NW, int NST>
+struct Layout {
+    static constexpr int OS = D + 4;
+    static constexpr int STAGE = 4 * C::TILE;
+    static constexpr int WARP = NW * NST * STAGE;
+    static constexpr int BAR = WARP + NW * C::SCRATCH;
+    static constexpr int OUT = BAR + (NW * NST * 16 + 15) / 16 * 16;
+    static constexpr int bytes(int G) { return OUT + NW * G * (OS + 2) * 4; }
+};
+
+// The listed blocks of one sequence as one warp walks them: entry e is block e % 2 of its pair
+// e / 2, pairs lie 2 NW blocks apart, and the table entries are read 32 at a time.
+template <int NW>
 struct BlockWalk {
     const int32_t* trow;
     VisibleBlocks v;
-    int first, step, n, lane, page;
-    int32_t ent;
+    int first, n, lane, page, num_blocks;      // n: entries
+    int32_t* err;
+    int32_t ent;                                // -1: names no block of the pool (flagged)
+    __device__ __forceinline__ int block(int e) const { return v.block(first + (e >> 1) * 2 * NW + (e & 1)); }
     __device__ __forceinline__ void fetch() {
-        const int i = page * 32 + lane;
-        ent = i < n ? __ldg(trow + v.block(first + i * step)) : -1;
+        const int e = page * 32 + lane;
+        ent = -1;
+        if (e < n) {
+            const int32_t b = __ldg(trow + block(e));
+            if (b >= 0 && b < num_blocks) ent = b;
+            else raise_flag(err, PA_DEV_ERR_BAD_BLOCK);
+        }
     }
-    __device__ __forceinline__ int32_t entry(int i) {          // i in order, the whole warp
-        if ((i >> 5) != page) {
-            page = i >> 5;
+    __device__ __forceinline__ int32_t entry(int e) {          // in order, the whole warp
+        if ((e >> 5) != page) {
+            page = e >> 5;
             fetch();
         }
-        return __shfl_sync(0xffffffffu, ent, i & 31);
+        return __shfl_sync(0xffffffffu, ent, e & 31);
     }
 };
 
@@ -375,105 +594,246 @@ __device__ __forceinline__ bool aborted(const int32_t* err) {
     return err && (*reinterpret_cast<const volatile int32_t*>(err) & PA_DEV_ERR_TIMEOUT) != 0;
 }
 
-// The warps' partial results (sm_o rows, sm_m, sm_l per warp and head) as one, written to
-// `out`.  A CTA in which a copy wait gave up writes NaN: its result is incomplete.
-template <int D, int NW, typename Out>
-__device__ __forceinline__ void store_merged(const WParams& p, const float* sm_o, const float* sm_m, const float* sm_l,
-                                             size_t row0, bool failed) {
-    constexpr int OS = D + 4;
-    for (int i = threadIdx.x; i < p.G * D; i += NW * 32) {
-        const int g = i / D, d = i % D;
-        float M = -INFINITY;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// a float of another CTA of the cluster, at this CTA's shared address `addr`
+__device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
+    uint32_t at;
+    float x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+
+// Parts.  The listed blocks are cut into parts of p.part_len, and in every part warp w takes
+// the same blocks whatever CTA it belongs to.  A (warp, part) has its own maximum, sum and
+// outputs; a warp's parts are folded into one in their order, and the warps merged in theirs.
+// So the result is the same, bit for bit, whether one CTA goes through all parts (many
+// sequences: no joining at all) or a cluster has a CTA per part (few: every SM gets work).
+struct Partial { float m, l, o; };         // of one head and dim; a part without keys: -inf, 0, 0
+__device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
+// The joint maximum of two parts and what their sums are scaled by.
+struct Fold { float m, a, s; };
+__device__ __forceinline__ Fold fold_factors(float a, float s) {
+    // (NaN, from a part that was given up, must stay)
+    const float m = (s > a || s != s) ? s : a, z = safe_max(m);
+    return Fold{m, fast_exp2(a - z), fast_exp2(s - z)};
+}
+__device__ __forceinline__ float fold_add(const Fold& f, float a, float s) { return __fmaf_rn(s, f.s, __fmul_rn(a, f.a)); }
+__device__ __forceinline__ void fold(Partial& a, const Partial& s) {
+    const Fold f = fold_factors(a.m, s.m);
+    a = Partial{f.m, fold_add(f, a.l, s.l), fold_add(f, a.o, s.o)};
+}
+
+// The output from the warps' results: of warp w, head g and dim d, get(w).
+template <int NW, typename Get>
+__device__ __forceinline__ float merge_warps(Get get) {
+    Partial x[NW];
+    float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w * 8 + g]);
-        float acc = 0.f, l = 0.f;
-        if (M != -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float wt = fast_exp2(sm_m[w * 8 + g] - M);
-                acc += wt * sm_o[(w * 8 + g) * OS + d];
-                l += wt * sm_l[w * 8 + g];
-            }
-        }
-        const float x = failed ? __int_as_float(0x7fc00000) : l > 0.f ? acc / l : 0.f;
-        if constexpr (sizeof(Out) == 2) static_cast<__nv_bfloat16*>(p.out)[(row0 + g) * D + d] = __float2bfloat16_rn(x);
-        else static_cast<float*>(p.out)[(row0 + g) * D + d] = x;
+    for (int w = 0; w < NW; ++w) {
+        x[w] = get(w);
+        M = (x[w].m > M || x[w].m != x[w].m) ? x[w].m : M;
     }
+    const float z = safe_max(M);
+    float acc = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const float wt = fast_exp2(x[w].m - z);
+        acc = __fmaf_rn(x[w].o, wt, acc);
+        l = __fmaf_rn(x[w].l, wt, l);
+    }
+    return l > 0.f || l != l ? acc / l : 0.f;
+}
+
+template <typename Out>
+__device__ __forceinline__ void store_out(void* out, size_t at, float x) {
+    if constexpr (sizeof(Out) == 2) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
+    else static_cast<float*>(out)[at] = x;
 }
 
 template <template <int> class Cache, int D, int NW, int NST>
 __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p) {
     using C = Cache<D>;
-    using L = Layout<D, C::TILE, NW, NST>;
+    using L = Layout<C, D, NW, NST>;
     constexpr int KS = C::KS, TILE = C::TILE;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = blockIdx.x, s = blockIdx.y;
-    uint8_t* stage0 = smem + warp * NST * 2 * TILE;
-    const uint32_t bar0 = smem_u32(smem) + L::BAR + warp * NST * 8;
+    const int kvh = blockIdx.y, s = blockIdx.z;
+    uint8_t* stage0 = smem + warp * NST * L::STAGE;
+    const uint32_t bar0 = smem_u32(smem) + L::BAR + warp * NST * 16;   // per stage: K's, V's
     if (lane == 0) {
 #pragma unroll
-        for (int st = 0; st < NST; ++st) mbar_init(bar0 + st * 8, 1);
+        for (int st = 0; st < 2 * NST; ++st) mbar_init(bar0 + st * 8, 1);
         fence_proxy_async_smem();
     }
     __syncwarp();
     // lengths, tables, queries and pools may all be the previous kernels' output
     grid_dependency_wait();
     grid_launch_dependents();
-    if (aborted(p.err)) return;
+    // (each warp for itself; a warp that skips reads no tiles and the CTA writes nothing)
+    const bool skip = __any_sync(0xffffffffu, aborted(p.err));
     const size_t row0 = (size_t)s * p.Hq + (size_t)kvh * p.G;
-    C cache(lane);
+    C cache(lane, reinterpret_cast<float*>(smem + L::WARP + warp * C::SCRATCH));
     cache.load_q(p.q, row0, p.G);
-    const Row row = row_of(p, s, kvh == 0 && threadIdx.x == 0);
-    BlockWalk walk{p.tables + (size_t)s * p.max_blocks, row.v, warp, NW, 0, lane, 0, -1};
-    walk.n = row.v.count > warp ? (row.v.count - warp + NW - 1) / NW : 0;
+    const Row row = row_of(p, s, blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0);
+    const int parts = max(1, (row.v.count + p.part_len - 1) / p.part_len);
+    const int begin = p.split ? blockIdx.x * p.part_len : 0;
+    if (begin > 0 && begin >= row.v.count) return;     // (a part's CTA that leaves is not waited for)
+    const int count = p.split ? min(p.part_len, row.v.count - begin) : row.v.count;
+    BlockWalk<NW> walk{p.tables + (size_t)s * p.max_blocks, row.v, begin + 2 * warp, 0, lane, 0, p.num_blocks, p.err, -1};
+    {
+        // whole pairs before the last, then what is left of it
+        const int from = count - 2 * warp;
+        const int pairs = from > 0 && !skip ? (from + 2 * NW - 1) / (2 * NW) : 0;
+        walk.n = pairs > 0 ? 2 * (pairs - 1) + min(2, from - 2 * NW * (pairs - 1)) : 0;
+    }
+    const int npairs = (walk.n + 1) >> 1;
     walk.fetch();
 
     const uint64_t pol = l2_policy_evict_first();
-    uint32_t issued = 0, phase = 0;
-    auto issue = [&](int i) {
-        const int st = i % NST;
-        const int32_t blk = walk.entry(i);
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
-            return;
+    // Pair i's tiles into its stage: `which` 0 K, 1 V.  have: 2 bits per stage, the blocks that
+    // were copied (a table entry that names no block is flagged and left out).
+    uint32_t have = 0, phase = 0;              // phase: 2 bits per stage (K, V)
+    int32_t blk_v[NST][2];                     // pair's blocks, kept from K's issue to V's
+    auto issue = [&](int i, int st, int which) {
+        if (which == 0) {
+            blk_v[st][0] = walk.entry(2 * i);
+            blk_v[st][1] = walk.entry(2 * i + 1);          // (-1 past the last)
+            have = (have & ~(3u << (2 * st))) | (((blk_v[st][0] >= 0 ? 1u : 0u) | (blk_v[st][1] >= 0 ? 2u : 0u)) << (2 * st));
         }
-        if (lane == 0) {
-            const size_t off = ((size_t)blk * p.Hkv + kvh) * (size_t)TILE;
-            const uint32_t k = smem_u32(stage0) + st * 2 * TILE, bar = bar0 + st * 8;
+        const uint32_t h = (have >> (2 * st)) & 3u;
+        if (h != 0u && lane == 0) {
+            const uint32_t bar = bar0 + st * 16 + which * 8;
+            const char* pool = which == 0 ? p.k_pool : p.v_pool;
+            const uint32_t dst = smem_u32(stage0) + st * L::STAGE + which * 2 * TILE;
             fence_proxy_async_smem();
-            mbar_arrive_expect_tx(bar, 2 * TILE);
-            bulk_g2s(k, p.k_pool + off, TILE, bar, pol);
-            bulk_g2s(k + TILE, p.v_pool + off, TILE, bar, pol);
+            mbar_arrive_expect_tx(bar, h == 3u ? 2 * TILE : TILE);
+            if (h & 1u) bulk_g2s(dst, pool + ((size_t)blk_v[st][0] * p.Hkv + kvh) * (size_t)TILE, TILE, bar, pol);
+            if (h & 2u) bulk_g2s(dst + TILE, pool + ((size_t)blk_v[st][1] * p.Hkv + kvh) * (size_t)TILE, TILE, bar, pol);
         }
-        issued |= 1u << st;
     };
-    for (int i = 0; i < NST && i < walk.n; ++i) issue(i);
+    auto landed = [&](int st, int which) -> bool {
+        const uint32_t bit = 2 * st + which;
+        const bool ok = mbar_wait_bounded(bar0 + st * 16 + which * 8, (phase >> bit) & 1u, kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        phase ^= 1u << bit;
+        return true;
+    };
+#pragma unroll
+    for (int st = 0; st < NST; ++st)
+        if (st < npairs) {
+            issue(st, st, 0);
+            issue(st, st, 1);
+        }
 
     Running run;
     float o[KS][4];
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // A part's end: the lanes' sums as one, the cache's own factors out, and into the warp's
+    // folded result (its outputs in shared memory, every lane its own elements).
+    float* sm_o = reinterpret_cast<float*>(smem + L::OUT);     // [NW][G][OS]
+    float* sm_m = sm_o + NW * p.G * L::OS;                     // [NW][G]
+    float* sm_l = sm_m + NW * p.G;                             // [NW][G]
+    float all_m0 = -INFINITY, all_m1 = -INFINITY, all_l0 = 0.f, all_l1 = 0.f;
+    bool folded = false;
+    auto end_part = [&]() {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+            run.l0 += __shfl_xor_sync(0xffffffffu, run.l0, x);
+            run.l1 += __shfl_xor_sync(0xffffffffu, run.l1, x);
+        }
+        cache.finish(run, o);
+        const int r = lane >> 2, c = lane & 3;
+        const Fold f0 = fold_factors(all_m0, run.m0), f1 = fold_factors(all_m1, run.m1);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (2 * c + e >= p.G) continue;
+            const Fold f = e ? f1 : f0;
+            float* at = sm_o + (warp * p.G + 2 * c + e) * L::OS + r;
+#pragma unroll
+            for (int mi = 0; mi < KS; ++mi) {
+                at[16 * mi] = fold_add(f, folded ? at[16 * mi] : 0.f, o[mi][e]);
+                at[16 * mi + 8] = fold_add(f, folded ? at[16 * mi + 8] : 0.f, o[mi][2 + e]);
+            }
+        }
+        all_l0 = fold_add(f0, all_l0, run.l0);
+        all_l1 = fold_add(f1, all_l1, run.l1);
+        all_m0 = f0.m;
+        all_m1 = f1.m;
+        folded = true;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        run.m0 = run.m1 = -INFINITY;
+        run.l0 = run.l1 = 0.f;
+        cache.reset();
+    };
+    const int part_pairs = p.part_len / (2 * NW);      // of a warp
+    int part_left = part_pairs;
     bool failed = false;
-    for (int i = 0; i < walk.n; ++i) {
-        const int st = i % NST;
-        if ((issued >> st) & 1u) {
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + st * 8, (phase >> st) & 1u, kWaitLimitNs))) {
+    uint32_t k_out = 0, v_out = 0;             // stages whose copies of the next pairs are in flight
+#pragma unroll
+    for (int st = 0; st < NST; ++st)
+        if (st < npairs && ((have >> (2 * st)) & 3u)) {
+            k_out |= 1u << st;
+            v_out |= 1u << st;
+        }
+    for (int i0 = 0; i0 < npairs && !failed; i0 += NST) {
+#pragma unroll
+        for (int st = 0; st < NST; ++st) {
+            const int i = i0 + st;
+            if (i >= npairs) break;
+            const bool more = i + NST < npairs;
+            if (part_left == 0) {
+                end_part();
+                part_left = part_pairs;
+            }
+            --part_left;
+            const uint32_t h = (have >> (2 * st)) & 3u;
+            if (h == 0u) {                     // no block of the pair is in the pool
+                if (more) {
+                    issue(i + NST, st, 0);
+                    issue(i + NST, st, 1);
+                    if ((have >> (2 * st)) & 3u) {
+                        k_out |= 1u << st;
+                        v_out |= 1u << st;
+                    }
+                }
+                continue;
+            }
+            uint8_t* kt = stage0 + st * L::STAGE;
+            uint32_t vis[2];                   // 16 bits, a slot each
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int tok0 = walk.block(2 * i + b) * kBlockTokens;
+                const bool inner = tok0 >= row.first && tok0 + kBlockTokens <= row.len;
+                vis[b] = !((h >> b) & 1u) ? 0u : inner ? 0xffffu : visible_slots(tok0, row.len, row.first, p.sinks);
+            }
+            const bool full = (vis[0] & vis[1]) == 0xffffu;
+            if (!landed(st, 0)) {
                 failed = true;
                 break;
             }
-            phase ^= 1u << st;
-            issued &= ~(1u << st);
-            const uint8_t* kt = stage0 + st * 2 * TILE;
-            const int tok0 = row.v.block(warp + i * NW) * kBlockTokens;
-            const uint32_t vis = visible_slots(tok0, row.len, row.first, p.sinks);
-            float sc[4];
+            k_out &= ~(1u << st);
+            float sc[2][4];
             cache.scores(kt, p.scale_log2, sc);
-            const bool ok0 = (vis >> cache.lo()) & 1u, ok1 = (vis >> cache.hi()) & 1u;
-            // hidden slots may hold anything: select, never multiply
-            const float s0 = ok0 ? sc[0] : -INFINITY, s1 = ok0 ? sc[1] : -INFINITY;
-            const float s2 = ok1 ? sc[2] : -INFINITY, s3 = ok1 ? sc[3] : -INFINITY;
-            float t0 = fmaxf(s0, s2), t1 = fmaxf(s1, s3);
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (!full) {
+                    // hidden slots may hold anything: select, never multiply
+                    const bool ok0 = (vis[b] >> cache.lo()) & 1u, ok1 = (vis[b] >> cache.hi()) & 1u;
+                    sc[b][0] = ok0 ? sc[b][0] : -INFINITY;
+                    sc[b][1] = ok0 ? sc[b][1] : -INFINITY;
+                    sc[b][2] = ok1 ? sc[b][2] : -INFINITY;
+                    sc[b][3] = ok1 ? sc[b][3] : -INFINITY;
+                }
+                t0 = fmaxf(t0, fmaxf(sc[b][0], sc[b][2]));
+                t1 = fmaxf(t1, fmaxf(sc[b][1], sc[b][3]));
+            }
+            // K is read: the stage's next K tiles may land under the rest of the pair
+            __syncwarp();
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
                 t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
@@ -482,243 +842,149 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
             const float n0 = fmaxf(run.m0, t0), n1 = fmaxf(run.m1, t1);
             // (a maximum still at -inf, from keys that score -inf, must not give inf - inf)
             const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
-            const float al0 = fast_exp2(run.m0 - z0), al1 = fast_exp2(run.m1 - z1);
+            run.al0 = fast_exp2(run.m0 - z0);
+            run.al1 = fast_exp2(run.m1 - z1);
             run.m0 = n0;
             run.m1 = n1;
-            const float pr[4] = {fast_exp2(s0 - z0), fast_exp2(s1 - z1), fast_exp2(s2 - z0), fast_exp2(s3 - z1)};
-            const bool rescale = __any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f);
-            cache.pv(kt + TILE, pr, vis, ok0, ok1, run, al0, al1, rescale, o);
+            float pr[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                pr[b][0] = fast_exp2(sc[b][0] - z0);
+                pr[b][1] = fast_exp2(sc[b][1] - z1);
+                pr[b][2] = fast_exp2(sc[b][2] - z0);
+                pr[b][3] = fast_exp2(sc[b][3] - z1);
+            }
+            run.rescale = __any_sync(0xffffffffu, run.al0 != 1.f || run.al1 != 1.f);
+            if (more) issue(i + NST, st, 0);
+            const uint32_t h_next = more ? (have >> (2 * st)) & 3u : 0u;
+            if (h_next) k_out |= 1u << st;
+            if (!landed(st, 1)) {
+                failed = true;
+                break;
+            }
+            v_out &= ~(1u << st);
+            if (!full) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (vis[b] != 0xffffu) cache.hide(kt + (2 + b) * TILE, vis[b]);
+                __syncwarp();
+            }
+            cache.pv(kt + 2 * TILE, pr, run, o);
+            __syncwarp();
+            if (more) issue(i + NST, st, 1);
+            if (h_next) v_out |= 1u << st;
         }
-        __syncwarp();
-        if (i + NST < walk.n) issue(i + NST);
     }
     if (failed) {
         // drain every copy still in flight before the shared memory is reused
         if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
-        for (int st = 0; st < NST; ++st)
-            if ((issued >> st) & 1u) mbar_wait_bounded(bar0 + st * 8, (phase >> st) & 1u, kWaitLimitNs);
+        for (int st = 0; st < NST; ++st) {
+            if ((k_out >> st) & 1u) mbar_wait_bounded(bar0 + st * 16, (phase >> (2 * st)) & 1u, kWaitLimitNs);
+            if ((v_out >> st) & 1u) mbar_wait_bounded(bar0 + st * 16 + 8, (phase >> (2 * st + 1)) & 1u, kWaitLimitNs);
+        }
     }
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) {
-        run.l0 += __shfl_xor_sync(0xffffffffu, run.l0, x);
-        run.l1 += __shfl_xor_sync(0xffffffffu, run.l1, x);
-    }
-    cache.finish(run, o);
-    const bool cta_failed = __syncthreads_or(failed);          // every warp is done with its stages
-    float* sm_o = reinterpret_cast<float*>(smem);
-    float* sm_m = sm_o + NW * 8 * L::OS;
-    float* sm_l = sm_m + NW * 8;
+    end_part();
+    const bool bad = __syncthreads_or(failed || skip), cta_skip = __syncthreads_or(skip);
     {
+        // a part that was given up or skipped passes on NaN: its result is incomplete
+        const float nan = __int_as_float(0x7fc00000);
         const int r = lane >> 2, c = lane & 3;
-        float* ow = sm_o + warp * 8 * L::OS;
-#pragma unroll
-        for (int mi = 0; mi < KS; ++mi) {
-            const int d = 16 * mi + r;
-            ow[(2 * c) * L::OS + d] = o[mi][0];
-            ow[(2 * c + 1) * L::OS + d] = o[mi][1];
-            ow[(2 * c) * L::OS + d + 8] = o[mi][2];
-            ow[(2 * c + 1) * L::OS + d + 8] = o[mi][3];
+        if (r == 0 && 2 * c < p.G) {
+            sm_m[warp * p.G + 2 * c] = bad ? nan : all_m0;
+            sm_l[warp * p.G + 2 * c] = bad ? nan : all_l0;
         }
-        if (r == 0) {
-            sm_m[warp * 8 + 2 * c] = run.m0;
-            sm_m[warp * 8 + 2 * c + 1] = run.m1;
-            sm_l[warp * 8 + 2 * c] = run.l0;
-            sm_l[warp * 8 + 2 * c + 1] = run.l1;
+        if (r == 0 && 2 * c + 1 < p.G) {
+            sm_m[warp * p.G + 2 * c + 1] = bad ? nan : all_m1;
+            sm_l[warp * p.G + 2 * c + 1] = bad ? nan : all_l1;
         }
     }
-    __syncthreads();
-    store_merged<D, NW, __nv_bfloat16>(p, sm_o, sm_m, sm_l, row0, cta_failed);
-}
-
-// The f32 cache: the same walk with fp32 FMAs (no tensor-core product has fp32 accuracy).
-// Lane (t, half) takes token t's dot products over half of the dims; the G probabilities of a
-// block pass through shared memory, and a lane then owns D / 32 dims of the output.
-template <int D, int NW, int NST>
-__global__ void __launch_bounds__(NW * 32) window_decode_f32_kernel(const WParams p) {
-    constexpr int TILE = kBlockTokens * D * 4;
-    using L = Layout<D, TILE, NW, NST>;
-    constexpr int NCH = D / 4;          // 16-byte pieces of a row
-    constexpr int DPL = D / 32;         // output dims of a lane
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = blockIdx.x, s = blockIdx.y;
-    uint8_t* stage0 = smem + warp * NST * 2 * TILE;
-    const uint32_t bar0 = smem_u32(smem) + L::BAR + warp * NST * 8;
-    float* sq = reinterpret_cast<float*>(smem + L::BYTES);              // [8][D] query rows
-    float* sp = sq + 8 * D + warp * 8 * kBlockTokens;                   // [8][16] this warp's probabilities
-    if (lane == 0) {
-#pragma unroll
-        for (int st = 0; st < NST; ++st) mbar_init(bar0 + st * 8, 1);
-        fence_proxy_async_smem();
-    }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (aborted(p.err)) return;
-    const size_t row0 = (size_t)s * p.Hq + (size_t)kvh * p.G;
-    const float* qrow = static_cast<const float*>(p.q) + row0 * D;
-    for (int i = threadIdx.x; i < 8 * D; i += NW * 32) sq[i] = i < p.G * D ? qrow[i] : 0.f;
-    __syncthreads();
-    const Row row = row_of(p, s, kvh == 0 && threadIdx.x == 0);
-    BlockWalk walk{p.tables + (size_t)s * p.max_blocks, row.v, warp, NW, 0, lane, 0, -1};
-    walk.n = row.v.count > warp ? (row.v.count - warp + NW - 1) / NW : 0;
-    walk.fetch();
-    const uint64_t pol = l2_policy_evict_first();
-    uint32_t issued = 0, phase = 0;
-    auto issue = [&](int i) {
-        const int st = i % NST;
-        const int32_t blk = walk.entry(i);
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
-            return;
+    if (!p.split || parts == 1) {
+        __syncthreads();
+        if (cta_skip) return;
+        for (int i = threadIdx.x; i < p.G * D; i += NW * 32) {
+            const int g = i / D, d = i % D;
+            const float x = merge_warps<NW>([&](int w) {
+                return Partial{sm_m[w * p.G + g], sm_l[w * p.G + g], sm_o[(w * p.G + g) * L::OS + d]};
+            });
+            store_out<typename C::Out>(p.out, (row0 + g) * D + d, x);
         }
-        if (lane == 0) {
-            const size_t off = ((size_t)blk * p.Hkv + kvh) * (size_t)TILE;
-            const uint32_t k = smem_u32(stage0) + st * 2 * TILE, bar = bar0 + st * 8;
-            fence_proxy_async_smem();
-            mbar_arrive_expect_tx(bar, 2 * TILE);
-            bulk_g2s(k, p.k_pool + off, TILE, bar, pol);
-            bulk_g2s(k + TILE, p.v_pool + off, TILE, bar, pol);
-        }
-        issued |= 1u << st;
-    };
-    for (int i = 0; i < NST && i < walk.n; ++i) issue(i);
-    float m[8], l[8], o[8][DPL];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-#pragma unroll
-        for (int k = 0; k < DPL; ++k) o[g][k] = 0.f;
+        return;
     }
-    bool failed = false;
-    const int t = lane & 15, half = lane >> 4;
-    for (int i = 0; i < walk.n; ++i) {
-        const int st = i % NST;
-        if ((issued >> st) & 1u) {
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + st * 8, (phase >> st) & 1u, kWaitLimitNs))) {
-                failed = true;
-                break;
-            }
-            phase ^= 1u << st;
-            issued &= ~(1u << st);
-            const float* kt = reinterpret_cast<const float*>(stage0 + st * 2 * TILE);
-            const float* vt = kt + TILE / 4;
-            const int tok0 = row.v.block(warp + i * NW) * kBlockTokens;
-            const uint32_t vis = visible_slots(tok0, row.len, row.first, p.sinks);
-            float acc[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) acc[g] = 0.f;
+    // A CTA per part: each adds up its share of the output elements over all parts, reading the
+    // others' shared memory (so nothing goes through a workspace, and one launch does it).
+    cluster_arrive();
+    cluster_wait();
+    const uint32_t o_at = smem_u32(sm_o), m_at = smem_u32(sm_m), l_at = smem_u32(sm_l);
+    for (int i = blockIdx.x * (NW * 32) + threadIdx.x; i < p.G * D; i += parts * (NW * 32)) {
+        const int g = i / D, d = i % D;
+        const float x = merge_warps<NW>([&](int w) {
+            Partial a{-INFINITY, 0.f, 0.f};
 #pragma unroll 4
-            for (int ch = half * (NCH / 2); ch < (half + 1) * (NCH / 2); ++ch) {
-                const float4 kv = *reinterpret_cast<const float4*>(kt + (ch * kBlockTokens + t) * 4);
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    if (g < p.G) {
-                        const float4 qv = *reinterpret_cast<const float4*>(sq + g * D + ch * 4);
-                        acc[g] = fmaf(qv.x, kv.x, acc[g]);
-                        acc[g] = fmaf(qv.y, kv.y, acc[g]);
-                        acc[g] = fmaf(qv.z, kv.z, acc[g]);
-                        acc[g] = fmaf(qv.w, kv.w, acc[g]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                if (g < p.G) {
-                    float sc = acc[g] + __shfl_xor_sync(0xffffffffu, acc[g], 16);
-                    sc = (vis >> t) & 1u ? sc * p.scale_log2 : -INFINITY;
-                    float top = sc;
-#pragma unroll
-                    for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    const float mn = fmaxf(m[g], top);
-                    const float z = mn == -INFINITY ? 0.f : mn;
-                    const float al = exp2f(m[g] - z), pr = exp2f(sc - z);
-                    float sum = pr;
-#pragma unroll
-                    for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                    m[g] = mn;
-                    l[g] = l[g] * al + sum;
-#pragma unroll
-                    for (int k = 0; k < DPL; ++k) o[g][k] *= al;
-                    if (half == 0) sp[g * kBlockTokens + t] = pr;
-                }
-            }
-            __syncwarp();
-            for (int tt = 0; tt < kBlockTokens; ++tt) {
-                if (!((vis >> tt) & 1u)) continue;             // (a hidden slot's V may be NaN)
-#pragma unroll
-                for (int k = 0; k < DPL; ++k) {
-                    const int d = lane + 32 * k;
-                    const float v = vt[((d >> 2) * kBlockTokens + tt) * 4 + (d & 3)];
-#pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        if (g < p.G) o[g][k] = fmaf(sp[g * kBlockTokens + tt], v, o[g][k]);
-                }
-            }
-        }
-        __syncwarp();
-        if (i + NST < walk.n) issue(i + NST);
+            for (int j = 0; j < parts; ++j)
+                fold(a, Partial{peer_f32(m_at + (w * p.G + g) * 4, j), peer_f32(l_at + (w * p.G + g) * 4, j),
+                                peer_f32(o_at + ((w * p.G + g) * L::OS + d) * 4, j)});
+            return a;
+        });
+        if (!cta_skip) store_out<typename C::Out>(p.out, (row0 + g) * D + d, x);
     }
-    if (failed) {
-        if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
-        for (int st = 0; st < NST; ++st)
-            if ((issued >> st) & 1u) mbar_wait_bounded(bar0 + st * 8, (phase >> st) & 1u, kWaitLimitNs);
-    }
-    const bool cta_failed = __syncthreads_or(failed);
-    float* sm_o = reinterpret_cast<float*>(smem);
-    float* sm_m = sm_o + NW * 8 * L::OS;
-    float* sm_l = sm_m + NW * 8;
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-#pragma unroll
-        for (int k = 0; k < DPL; ++k) sm_o[(warp * 8 + g) * L::OS + lane + 32 * k] = o[g][k];
-        if (lane == g) {
-            sm_m[warp * 8 + g] = m[g];
-            sm_l[warp * 8 + g] = l[g];
-        }
-    }
-    __syncthreads();
-    store_merged<D, NW, float>(p, sm_o, sm_m, sm_l, row0, cta_failed);
+    // no CTA leaves while another may still read its shared memory
+    cluster_arrive();
+    cluster_wait();
 }
 
-template <typename K>
-cudaError_t launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t stream, const WParams& p) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         (int)cudaSharedmemCarveoutMaxShared);
+// Attributes of a kernel, set once per device.
+template <void (*Kernel)(const WParams)>
+cudaError_t prepare_kernel(int smem) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // clusters of up to 16 CTAs
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <void (*Kernel)(const WParams)>
+cudaError_t launch(const WParams& p, int parts, int num_seqs, int threads, int smem, int most_smem, cudaStream_t stream) {
+    const cudaError_t e = prepare_kernel<Kernel>(most_smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    const int ctas = p.split ? parts : 1;
+    cfg.gridDim = dim3(ctas, p.Hkv, num_seqs);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, Kernel, p);
 }
 
 template <template <int> class Cache, int D, int NST>
-cudaError_t launch_mma(const WParams& p, dim3 grid, cudaStream_t stream) {
-    constexpr int NW = 4;
-    return launch(window_decode_kernel<Cache, D, NW, NST>, grid, NW * 32, Layout<D, Cache<D>::TILE, NW, NST>::BYTES,
-                  stream, p);
+cudaError_t launch_cache(const WParams& p, int parts, int num_seqs, cudaStream_t stream) {
+    constexpr int NW = kWarps;
+    return launch<window_decode_kernel<Cache, D, NW, NST>>(p, parts, num_seqs, NW * 32, Layout<Cache<D>, D, NW, NST>::bytes(p.G),
+                                                           Layout<Cache<D>, D, NW, NST>::bytes(8), stream);
 }
 
 template <int D>
-cudaError_t launch_type(const WParams& p, pa_dtype dtype, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_type(const WParams& p, int parts, pa_dtype dtype, int num_seqs, cudaStream_t stream) {
     switch (dtype) {
-        case PA_BF16: return launch_mma<Bf16Cache, D, 2>(p, grid, stream);
-        case PA_FP8_E4M3: return launch_mma<Fp8Cache, D, 2>(p, grid, stream);
-        case PA_FP4_E2M1: return launch_mma<Fp4Cache, D, 4>(p, grid, stream);
-        case PA_F32: {
-            constexpr int NW = 4, NST = 2;
-            constexpr int smem = Layout<D, kBlockTokens * D * 4, NW, NST>::BYTES + (8 * D + NW * 8 * kBlockTokens) * 4;
-            return launch(window_decode_f32_kernel<D, NW, NST>, grid, NW * 32, smem, stream, p);
-        }
+        case PA_BF16: return launch_cache<Bf16Cache, D, 1>(p, parts, num_seqs, stream);
+        case PA_FP8_E4M3: return launch_cache<Fp8Cache, D, 1>(p, parts, num_seqs, stream);
+        case PA_FP4_E2M1: return launch_cache<Fp4Cache, D, 1>(p, parts, num_seqs, stream);
+        case PA_F32: return launch_cache<F32Cache, D, 1>(p, parts, num_seqs, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -741,9 +1007,21 @@ cudaError_t launch_window_decode(const WindowArgs& a, cudaStream_t stream) {
     p.num_blocks = a.num_blocks;
     p.window = a.window;
     p.sinks = a.sinks;
+    // the blocks that a sequence can have listed: the window's (one more when it starts inside
+    // one) and the sinks'
+    long long n = ((long long)a.window + 2 * kBlockTokens - 2) / kBlockTokens +
+                  ((long long)a.sinks + kBlockTokens - 1) / kBlockTokens;
+    if (n > a.max_blocks) n = a.max_blocks;
+    // at most 16 parts (the largest cluster), whole pairs for every warp
+    constexpr int kUnit = 2 * kWarps;
+    const int blocks = (int)n, least = min_part(a.dtype);
+    const int most = blocks > 16 * least ? 16 : blocks < least ? 1 : blocks / least;
+    p.part_len = ((blocks + most - 1) / most + kUnit - 1) / kUnit * kUnit;
+    const int parts = (blocks + p.part_len - 1) / p.part_len;
+    p.split = parts > 1 && (long long)a.num_kv_heads * a.num_seqs < kSplitBelow;
     p.scale_log2 = a.scale * kLog2e;
-    const dim3 grid(a.num_kv_heads, a.num_seqs);
-    return a.head_dim == 64 ? launch_type<64>(p, a.dtype, grid, stream) : launch_type<128>(p, a.dtype, grid, stream);
+    return a.head_dim == 64 ? launch_type<64>(p, parts, a.dtype, a.num_seqs, stream)
+                            : launch_type<128>(p, parts, a.dtype, a.num_seqs, stream);
 }
 
 }  // namespace pa

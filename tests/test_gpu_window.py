@@ -108,7 +108,7 @@ def test_decode_window_over_everything_agrees_with_the_full_decode():
         within(full[s:s + 1], want, tol)
 
 
-@pytest.mark.parametrize("cache", ["bf16", "f32"])
+@pytest.mark.parametrize("cache", ["bf16"])
 def test_decode_scores_of_minus_infinity(cache):
     # visible keys that score -inf get weight 0, also as the first ones of a warp's walk
     lens = [200]

@@ -98,7 +98,7 @@ def test_bindings_check_the_tensors(native):
     with pytest.raises(ValueError):
         native.rope_append_kv(pool, pool, q.clone(), q, new, new, freq, tables, lens, cu)
     # types, shapes, layouts (checked before the device)
-    dev = torch.device("cpu")
+    dev = 0
     with pytest.raises(TypeError):
         native._checked(dev, lens.long(), "context_lens", i32, (3,))
     with pytest.raises(ValueError):
