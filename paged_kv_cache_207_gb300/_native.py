@@ -422,7 +422,35 @@ def prefill_attention(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, sca
         _dtype_code(q), None if err_flag is None else _i32(err_flag, "err_flag"), _stream(stream)))
 
 
-_POOL_F32, _POOL_BF16, _POOL_FP8, _POOL_FP4 = 0, 1, 2, 3
+# Bindings of the rotary append and of the windowed attention.  A decode step calls them once per
+# layer, and a short step waits for them rather than for the GPU: each tensor is checked in one
+# expression, and only a refused one is looked at again for the reason.
+_PLAIN_CODE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
+_I32 = torch.int32
+_cuda_device = torch.cuda.current_device
+
+
+def _plain_pool(k_pool):
+    """Blocks, kv heads, head_dim, pool code and the type of rows, q and out."""
+    try:
+        nb, hkv, pieces, slots, x = k_pool.shape
+    except ValueError:
+        slots = 0
+    if slots != BLOCK_SIZE:
+        raise ValueError("pools must have shape [num_blocks][Hkv][D/X][16][X]")
+    dtype = k_pool.dtype
+    code = _PLAIN_CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported element type {dtype}")
+    return nb, hkv, pieces * x, code, dtype
+
+
+def _fp8_pool(k_pool):
+    return *_fp8_dims(k_pool), 2, torch.bfloat16
+
+
+def _fp4_pool(k_pool):
+    return *_fp4_dims(k_pool), 3, torch.bfloat16
 
 
 def _bound(x) -> int:
@@ -430,14 +458,13 @@ def _bound(x) -> int:
     return min(int(x), 2**31 - 1)
 
 
-def _call_on(dev: int, stream, fn, args) -> None:
+def _call_on(dev: int, stream, fn, *args) -> None:
     """Calls a library function on device `dev`, on its current stream by default."""
-    if dev != torch.cuda.current_device():
+    if dev != _cuda_device():
         with torch.cuda.device(dev):
-            return _call_on(dev, stream, fn, args)
+            return _call_on(dev, stream, fn, *args)
     # (the raw handle: building a Stream object costs as much as the launch)
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    status = fn(*args, raw)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status != PA_OK:
         check(fn.__name__, status)
 
@@ -467,45 +494,40 @@ def _rows(dev, t, name, dtype, shape):
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == dev >= 0):
         _refuse(dev, t, name, dtype, shape)
+    row, head, one = t.stride()
     n, heads, d = shape
-    stride = t.stride()
-    if n and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+    if n and (one != 1 or (heads > 1 and head != d)):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.data_ptr(), (stride[0] if n > 1 else heads * d)
+    return t.data_ptr(), (row if n > 1 else heads * d)
 
 
 def _flag(dev, err_flag):
-    if err_flag is None:
-        return None
-    return _checked(dev, err_flag, "err_flag", torch.int32, err_flag.shape)
+    return None if err_flag is None else _checked(dev, err_flag, "err_flag", _I32, err_flag.shape)
 
 
-def _pools(k_pool, v_pool, dims):
-    nb, hkv, d = dims(k_pool)
-    dev, shape = k_pool.get_device(), k_pool.shape
-    return (dev, nb, hkv, d, _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
-            _checked(dev, v_pool, "v_pool", k_pool.dtype, shape))
-
-
-def _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
-                 cu_new_tokens, interleaved, err_flag, stream, dims, code, rows) -> None:
-    dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, dims)
-    n, s = k_new.shape[0], start_pos.shape[0]
-    hq = 0 if q is None else q.shape[1]
-    kn, ks = _rows(dev, k_new, "k_new", rows, (n, hkv, d))
-    vn, vs = _rows(dev, v_new, "v_new", rows, (n, hkv, d))
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    qi, qs = (None, 0) if q is None else _rows(dev, q, "q", rows, (n, hq, d))
-    qo, qos = (None, 0) if q is None else _rows(dev, q_out, "q_out", rows, (n, hq, d))
-    freq = _checked(dev, inv_freq, "inv_freq", torch.float64, (inv_freq.shape[0],))
-    width = block_tables.shape[1]
-    _call_on(dev, stream, lib().pa_rope_append_kv, (
-        kp, vp, qo, qi, kn, vn, qos, qs, ks, vs, freq, 2 * inv_freq.shape[0], int(bool(interleaved)),
-        _checked(dev, block_tables, "block_tables", torch.int32, (s, width)), width,
-        _checked(dev, start_pos, "start_pos", torch.int32, (s,)),
-        _checked(dev, cu_new_tokens, "cu_new_tokens", torch.int32, (s + 1,)), s, n, nb, hq, hkv, d, code,
-        _flag(dev, err_flag)))
+def _rope_append(pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
+                 cu_new_tokens, interleaved, err_flag, stream) -> None:
+    nb, hkv, d, code, rows = pool(k_pool)
+    dev, shape, half = k_pool.get_device(), k_pool.shape, inv_freq.shape[0]
+    s, width = block_tables.shape
+    kv = (k_new.shape[0], hkv, d)
+    kn, ks = _rows(dev, k_new, "k_new", rows, kv)
+    vn, vs = _rows(dev, v_new, "v_new", rows, kv)
+    if q is None or q_out is None:
+        if q is not q_out:
+            raise ValueError("q and q_out come together")
+        hq, qi, qs, qo, qos = 0, None, 0, None, 0
+    else:
+        hq = q.shape[1]
+        qi, qs = _rows(dev, q, "q", rows, (kv[0], hq, d))
+        qo, qos = _rows(dev, q_out, "q_out", rows, (kv[0], hq, d))
+    _call_on(dev, stream, lib().pa_rope_append_kv, _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
+             _checked(dev, v_pool, "v_pool", k_pool.dtype, shape), qo, qi, kn, vn, qos, qs, ks, vs,
+             _checked(dev, inv_freq, "inv_freq", torch.float64, (half,)), 2 * half, 1 if interleaved else 0,
+             _checked(dev, block_tables, "block_tables", _I32, (s, width)), width,
+             _checked(dev, start_pos, "start_pos", _I32, (s,)),
+             _checked(dev, cu_new_tokens, "cu_new_tokens", _I32, (s + 1,)), s, kv[0], nb, hq, hkv, d,
+             code, _flag(dev, err_flag))
 
 
 def rope_append_kv(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
@@ -514,59 +536,59 @@ def rope_append_kv(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_table
     are turned by (start_pos[s] + i) * inv_freq (float64 [rotary_dim / 2] on the device), keys
     and values go to the pools, the turned queries to q_out (which may be q; both None: no
     queries).  Rows [tokens][heads][D] may be column ranges of a wider tensor."""
-    code = _dtype_code(k_pool)
-    _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
-                 cu_new_tokens, interleaved, err_flag, stream, _pool_dims, code, k_pool.dtype)
+    _rope_append(_plain_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
+                 start_pos, cu_new_tokens, interleaved, err_flag, stream)
 
 
 def rope_append_kv_fp8(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
                        cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
     """rope_append_kv of bf16 rows into FP8 pools."""
-    _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
-                 cu_new_tokens, interleaved, err_flag, stream, _fp8_dims, _POOL_FP8, torch.bfloat16)
+    _rope_append(_fp8_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
+                 start_pos, cu_new_tokens, interleaved, err_flag, stream)
 
 
 def rope_append_kv_fp4(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
                        cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
     """rope_append_kv of bf16 rows into MXFP4 pools."""
-    _rope_append(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
-                 cu_new_tokens, interleaved, err_flag, stream, _fp4_dims, _POOL_FP4, torch.bfloat16)
+    _rope_append(_fp4_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
+                 start_pos, cu_new_tokens, interleaved, err_flag, stream)
 
 
-def _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
-                   err_flag, stream, dims, code, rows) -> None:
-    dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, dims)
-    s, hq = q.shape[0], q.shape[1]
-    width = block_tables.shape[1]
-    _call_on(dev, stream, lib().pa_decode_attention_window, (
-        _checked(dev, out, "out", rows, (s, hq, d)), _checked(dev, q, "q", rows, (s, hq, d)), kp, vp,
-        _checked(dev, block_tables, "block_tables", torch.int32, (s, width)),
-        _checked(dev, context_lens, "context_lens", torch.int32, (s,)), s, hq, hkv, d, width, nb,
-        _bound(window), _bound(num_sinks), float(scale), code,
-        _flag(dev, err_flag)))
+def _decode_window(pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
+                   err_flag, stream) -> None:
+    nb, hkv, d, code, rows = pool(k_pool)
+    dev, shape, of_q = k_pool.get_device(), k_pool.shape, q.shape
+    s, width = block_tables.shape
+    if len(of_q) != 3 or of_q[0] != s or of_q[2] != d:
+        raise ValueError("q must have shape [num_seqs][num_q_heads][head_dim]")
+    _call_on(dev, stream, lib().pa_decode_attention_window, _checked(dev, out, "out", rows, of_q),
+             _checked(dev, q, "q", rows, of_q), _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
+             _checked(dev, v_pool, "v_pool", k_pool.dtype, shape),
+             _checked(dev, block_tables, "block_tables", _I32, (s, width)),
+             _checked(dev, context_lens, "context_lens", _I32, (s,)), s, of_q[1], hkv, d, width, nb,
+             _bound(window), _bound(num_sinks), float(scale), code, _flag(dev, err_flag))
 
 
 def decode_attention_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window: int,
                             num_sinks: int = 0, err_flag=None, stream=None) -> None:
     """decode_attention over the last ``window`` positions and the first ``num_sinks``; table
     entries of blocks that hold none of them are not read."""
-    code = _dtype_code(k_pool)
-    _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
-                   err_flag, stream, _pool_dims, code, k_pool.dtype)
+    _decode_window(_plain_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
+                   num_sinks, err_flag, stream)
 
 
 def decode_attention_window_fp8(out, q, k_pool, v_pool, block_tables, context_lens, scale,
                                 window: int, num_sinks: int = 0, err_flag=None, stream=None) -> None:
     """decode_attention_window over FP8 pools (bf16 q and out)."""
-    _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
-                   err_flag, stream, _fp8_dims, _POOL_FP8, torch.bfloat16)
+    _decode_window(_fp8_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
+                   num_sinks, err_flag, stream)
 
 
 def decode_attention_window_fp4(out, q, k_pool, v_pool, block_tables, context_lens, scale,
                                 window: int, num_sinks: int = 0, err_flag=None, stream=None) -> None:
     """decode_attention_window over MXFP4 pools (bf16 q and out)."""
-    _decode_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
-                   err_flag, stream, _fp4_dims, _POOL_FP4, torch.bfloat16)
+    _decode_window(_fp4_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
+                   num_sinks, err_flag, stream)
 
 
 def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, scale,
@@ -574,17 +596,18 @@ def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu
                              stream=None) -> None:
     """prefill_attention with every row limited to the last ``window`` positions up to its own
     and the first ``num_sinks`` (bf16)."""
-    dev, nb, hkv, d, kp, vp = _pools(k_pool, v_pool, _pool_dims)
-    code = _dtype_code(k_pool)
-    n, hq, s = q.shape[0], q.shape[1], start_pos.shape[0]
-    width = block_tables.shape[1]
-    _call_on(dev, stream, lib().pa_prefill_attention_window, (
-        _checked(dev, out, "out", k_pool.dtype, (n, hq, d)), _checked(dev, q, "q", k_pool.dtype, (n, hq, d)),
-        kp, vp, _checked(dev, block_tables, "block_tables", torch.int32, (s, width)), width,
-        _checked(dev, start_pos, "start_pos", torch.int32, (s,)),
-        _checked(dev, cu_q, "cu_q", torch.int32, (s + 1,)), s, n, _bound(max_chunk), hq, hkv, d, nb,
-        _bound(window), _bound(num_sinks), float(scale), code,
-        _flag(dev, err_flag)))
+    nb, hkv, d, code, rows = _plain_pool(k_pool)
+    dev, shape, of_q = k_pool.get_device(), k_pool.shape, q.shape
+    s, width = block_tables.shape
+    if len(of_q) != 3 or of_q[2] != d:
+        raise ValueError("q must have shape [total_q][num_q_heads][head_dim]")
+    _call_on(dev, stream, lib().pa_prefill_attention_window, _checked(dev, out, "out", rows, of_q),
+             _checked(dev, q, "q", rows, of_q), _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
+             _checked(dev, v_pool, "v_pool", k_pool.dtype, shape),
+             _checked(dev, block_tables, "block_tables", _I32, (s, width)), width,
+             _checked(dev, start_pos, "start_pos", _I32, (s,)),
+             _checked(dev, cu_q, "cu_q", _I32, (s + 1,)), s, of_q[0], _bound(max_chunk), of_q[1], hkv, d,
+             nb, _bound(window), _bound(num_sinks), float(scale), code, _flag(dev, err_flag))
 
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024

@@ -232,6 +232,8 @@ __device__ __forceinline__ int32_t fetch_window(const int32_t* trow, const Visib
     const int b = 32 * w + lane;
     return b < lim ? __ldg(trow + (WIN ? v.block(b) : b)) : -1;
 }
+// x as a shift count: 0 below 0, all out from 16 on.
+__device__ __forceinline__ int clamp_shift(int x) { return min(max(x, 0), kBlockTokens); }
 // Table entry of block `lane` of key tile j from the window holding it (-1 for lanes past
 // the tile's blocks or the CTA's last block).
 __device__ __forceinline__ int32_t window_block(int32_t win, int j, int lane, int nblk) {
@@ -930,7 +932,8 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
     const uint32_t tl_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     // without a tile b, tile a's S alternates between both S buffers (see the MMA warp)
     const uint32_t ocol = kColO + (uint32_t)(h * kKeyTok);
-    const float cs = fabsf(p.scale_log2);              // a negative scale was moved into Q
+    // a negative scale was moved into Q; (WIN: a hidden key's -inf stays -inf under a scale of 0)
+    const float cs = WIN ? fmaxf(fabsf(p.scale_log2), 1.17549435e-38f) : fabsf(p.scale_log2);
     const bool active = h == 0 || has_b;
     bool ok = true;
     int t0 = 0, ic = 0;                                // tiles and items of the earlier items
@@ -966,7 +969,29 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             }
             const bool full = __all_sync(0xffffffffu, row_full);
             float mx;
-            if (full) {
+            if constexpr (WIN) {
+                if (!full) {
+                    // hidden keys score -inf (a select: unread or stale columns may hold NaN); the
+                    // visible ones of 32 columns, two listed blocks, are the bits of a word, two
+                    // instructions per score
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t see = 0u;
+#pragma unroll
+                        for (int hb = 0; hb < 2; ++hb) {
+                            const int b = j * kKeyBlocks + 2 * c + hb;
+                            const int tok = b * kBlockTokens + (b >= near_from ? near_off : 0);
+                            const int past = max(pos + 1 - tok, 0);           // slots below it are not after the row
+                            const uint32_t vis = (0xffffu << clamp_shift(past - p.window)) | ~(0xffffu << clamp_shift(p.sinks - tok));
+                            see |= (vis & ~(0xffffu << clamp_shift(past)) & 0xffffu) << (16 * hb);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see >> i) & 1u)) sr[c][i] = 0xff800000u;
+                    }
+                }
+            }
+            if (WIN || full) {
                 // the row maximum of the unscaled scores (c >= 0), four independent chains
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -978,20 +1003,6 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             } else {
                 // scale and causal mask (select: unread or stale columns may hold NaN)
                 mx = -INFINITY;
-                if constexpr (WIN) {
-                    const int far = min(p.sinks, pos + 1);       // sinks up to the row itself
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int b = j * kKeyBlocks + 2 * c + i / kBlockTokens;
-                            const int tok = tok0 + 32 * c + i + (b >= near_from ? near_off : 0);
-                            const bool see = (uint32_t)(pos - tok) < (uint32_t)p.window || tok < far;
-                            const float x = see ? __uint_as_float(sr[c][i]) * cs : -INFINITY;
-                            sr[c][i] = __float_as_uint(x);
-                            mx = fmaxf(mx, x);
-                        }
-                } else
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -1033,7 +1044,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             // -inf, and their probabilities must be 0, not exp2(-inf + inf))
             const float m_sub = WIN && m_used == -INFINITY ? 0.f : m_used;
             float sum;
-            if (full) {
+            if (WIN || full) {
                 const uint64_t c2 = pack_f32x2(cs, cs), nm2 = pack_f32x2(-m_sub, -m_sub);
                 uint64_t sum2[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
 #pragma unroll
@@ -1057,8 +1068,8 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float e0 = fast_exp2(__uint_as_float(sr[c][i]) - m_sub);
-                        const float e1 = fast_exp2(__uint_as_float(sr[c][i + 1]) - m_sub);
+                        const float e0 = fast_exp2(__uint_as_float(sr[c][i]) - m_used);
+                        const float e1 = fast_exp2(__uint_as_float(sr[c][i + 1]) - m_used);
                         sum += e0 + e1;
                         pk[i >> 1] = pack_bf16x2(e0, e1);
                     }

@@ -43,6 +43,8 @@ struct RParams {
 };
 
 constexpr int kThreads = 256;
+constexpr int kTileMinRows = 4;        // rows per sequence from which a call goes tile by tile
+constexpr int kTileHeads = 3;          // heads of a thread that are loaded together (four spill)
 
 // A frequency in radians per position as turns * 2^64, modulo 2^64.
 __device__ __forceinline__ uint64_t fixed_turns(double inv_freq) {
@@ -131,6 +133,117 @@ __device__ __forceinline__ int item_of_piece(int y, int half, bool split, bool& 
     return y >> 1;
 }
 
+// Turns the planes of item u: `cs` the cosines and sines of its row's frequencies.
+template <int E, bool INTERLEAVED>
+__device__ __forceinline__ void turn_item(Piece<E>& a, Piece<E>& b, const float2 (&c)[E]) {
+    if constexpr (INTERLEAVED) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 ca = c[e / 2], cb = c[E / 2 + e / 2];
+            const float a0 = a.x[e], a1 = a.x[e + 1], b0 = b.x[e], b1 = b.x[e + 1];
+            a.x[e] = a0 * ca.x - a1 * ca.y;
+            a.x[e + 1] = a1 * ca.x + a0 * ca.y;
+            b.x[e] = b0 * cb.x - b1 * cb.y;
+            b.x[e + 1] = b1 * cb.x + b0 * cb.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float x1 = a.x[e], x2 = b.x[e];
+            a.x[e] = x1 * c[e].x - x2 * c[e].y;
+            b.x[e] = x2 * c[e].x + x1 * c[e].y;
+        }
+    }
+}
+// Item u's E cosines and sines: its planes are u E .. u E + E - 1 of the row's.
+template <int E>
+__device__ __forceinline__ void item_turns(const float2* cs, int u, float2 (&c)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const float4 v = *reinterpret_cast<const float4*>(cs + u * E + e);
+        c[e] = make_float2(v.x, v.y);
+        c[e + 1] = make_float2(v.z, v.w);
+    }
+}
+
+// One item of a key or value row into a quantised pool (u-adjacent lanes hold a head's items;
+// every lane of the warp calls it).
+template <int D, pa_dtype T>
+__device__ __forceinline__ void put_quantised(const RParams& p, char* pool, int32_t blk, int h, int slot, bool is_k,
+                                              bool live, int u, Pair at, bool split, const Piece<8>& a,
+                                              const Piece<8>& b) {
+    constexpr int E = 8, PH = D / 16;
+    if constexpr (T == PA_FP8_E4M3) {
+        float m = fmaxf(max_abs<E>(a), max_abs<E>(b));
+#pragma unroll
+        for (int x = 1; x < PH; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        if (live) {
+            const float scale = __fdiv_rn(m, 448.f);
+            char* rec = pool + ((size_t)blk * p.Hkv + h) * fp8_record_bytes(D);
+            const uint2 ca = e4m3_codes(a, scale), cb = e4m3_codes(b, scale);
+            if (is_k) {
+                *reinterpret_cast<uint2*>(rec + ((at.a >> 1) * kBlockTokens + slot) * 16 + (at.a & 1) * 8) = ca;
+                *reinterpret_cast<uint2*>(rec + ((at.b >> 1) * kBlockTokens + slot) * 16 + (at.b & 1) * 8) = cb;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    rec[(at.a * 8 + e) * kBlockTokens + slot] = (char)((e < 4 ? ca.x : ca.y) >> (8 * (e & 3)));
+                    rec[(at.b * 8 + e) * kBlockTokens + slot] = (char)((e < 4 ? cb.x : cb.y) >> (8 * (e & 3)));
+                }
+            }
+            if (u == 0) *reinterpret_cast<float*>(rec + (size_t)16 * D + 4 * slot) = scale;
+        }
+    } else {
+        // the largest magnitude of each piece's 32-value block: its four pieces' maxima,
+        // wherever in the head's lanes they are
+        const float ma = max_abs<E>(a), mb = max_abs<E>(b);
+        const int lane = threadIdx.x & 31, base = lane - u;
+        char* rec = pool + ((size_t)blk * p.Hkv + h) * fp4_record_bytes(D);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int pc = k ? at.b : at.a;
+            float m = 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                bool second;
+                const int from = base + item_of_piece<E>((pc & ~3) + y, p.half, split, second);
+                const float va = __shfl_sync(0xffffffffu, ma, from), vb = __shfl_sync(0xffffffffu, mb, from);
+                m = fmaxf(m, second ? vb : va);
+            }
+            if (!live) continue;
+            const int code = m > 0.f ? max((int)(__float_as_uint(m) >> 23) - 2, 0) : 0;
+            const float inv = exp2i(127 - code);                  // 1 / scale, exact
+            const Piece<E>& x = k ? b : a;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t two = m > 0.f ? pack_e2m1x2(x.x[2 * c] * inv, x.x[2 * c + 1] * inv) : 0u;
+                if (is_k) {
+                    rec[(size_t)slot * (D / 2) + c * (D / 8) + pc] = (char)two;
+                } else {
+                    // a byte holds two slots of one dim, and rows of one call may share it
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int at_byte = (((2 * c + e) * 4 + (slot % 8) / 2) * (D / 16) + pc / 2) * 4 +
+                                            (pc & 1) * 2 + slot / 8;
+                        unsigned int* word = reinterpret_cast<unsigned int*>(rec + (at_byte & ~3));
+                        const int shift = (at_byte & 3) * 8 + (slot & 1) * 4;
+                        atomicAnd(word, ~(0xfu << shift));
+                        atomicOr(word, ((two >> (4 * e)) & 0xfu) << shift);
+                    }
+                }
+            }
+            if ((pc & 3) == 0) rec[8 * D + slot * (D / 32) + (pc >> 2)] = (char)code;
+        }
+    }
+}
+
+// Flags cu_new_tokens where it is not a prefix sum that ends at the rows (one CTA's threads).
+__device__ __forceinline__ void check_cu(const RParams& p) {
+    bool bad = threadIdx.x == 0 && (__ldg(p.cu) != 0 || __ldg(p.cu + p.S) != p.total);
+    for (int s = threadIdx.x; s < p.S; s += kThreads) bad |= __ldg(p.cu + s) > __ldg(p.cu + s + 1);
+    if (bad) raise_flag(p.err, PA_DEV_ERR_BAD_CU);
+}
+
 // One CTA per row: its frequencies' cosines and sines once, then every (head, item) of the
 // keys, values and queries, a thread an item at a time: two 16-byte loads, two stores.
 // T: the pool's type.
@@ -138,13 +251,12 @@ template <int D, pa_dtype T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RParams p) {
     constexpr int E = T == PA_F32 ? 4 : 8;       // elements of a piece (the rows are f32 or bf16)
     constexpr int PH = D / (2 * E);              // items of a head
-    __shared__ float2 cs[D / 2];
+    __shared__ __align__(16) float2 cs[D / 2];
     // the rows may come from the kernel before (a projection), and the pools be in use by it
     grid_dependency_wait();
     grid_launch_dependents();
     const int row = blockIdx.x, tid = threadIdx.x;
-    if (row == 0 && tid == 0 && (__ldg(p.cu) != 0 || __ldg(p.cu + p.S) != p.total))
-        raise_flag(p.err, PA_DEV_ERR_BAD_CU);
+    if (row == 0) check_cu(p);
     int s, pos = 0;
     int32_t blk = 0;
     if (!locate_row(p, row, tid == 0, s, pos, blk)) return;      // the same in every thread
@@ -172,25 +284,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RParams p) 
         }
         Piece<E> a = unpack<E>(ra), b = unpack<E>(rb);
         if (turn) {
-            if constexpr (INTERLEAVED) {
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 ca = cs[u * E + e / 2], cb = cs[u * E + E / 2 + e / 2];
-                    const float a0 = a.x[e], a1 = a.x[e + 1], b0 = b.x[e], b1 = b.x[e + 1];
-                    a.x[e] = a0 * ca.x - a1 * ca.y;
-                    a.x[e + 1] = a1 * ca.x + a0 * ca.y;
-                    b.x[e] = b0 * cb.x - b1 * cb.y;
-                    b.x[e + 1] = b1 * cb.x + b0 * cb.y;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float2 c = cs[u * E + e];
-                    const float x1 = a.x[e], x2 = b.x[e];
-                    a.x[e] = x1 * c.x - x2 * c.y;
-                    b.x[e] = x2 * c.x + x1 * c.y;
-                }
-            }
+            float2 c[E];
+            item_turns<E>(cs, u, c);
+            turn_item<E, INTERLEAVED>(a, b, c);
         }
         if (live && !is_k && !is_v) {
             char* dst = p.q_out + row * p.q_out_stride + (size_t)h * (PH * 32);
@@ -204,75 +300,292 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RParams p) 
                 *reinterpret_cast<uint4*>(dst + at.a * 256) = pack<E>(a);
                 *reinterpret_cast<uint4*>(dst + at.b * 256) = pack<E>(b);
             }
-        } else if constexpr (T == PA_FP8_E4M3) {
-            float m = fmaxf(max_abs<E>(a), max_abs<E>(b));
+        } else {
+            put_quantised<D, T>(p, pool, blk, h, slot, is_k, live && (is_k || is_v), u, at, split, a, b);
+        }
+    }
+}
+
+// Chunks.  A CTA takes a tile: the rows of one sequence that fall into one block, at most 16,
+// so that a pool's tile is written in whole runs and the place is looked up once.  Tile t
+// belongs to the last sequence s with cu[s] / 16 + 2 s <= t (a sequence of n rows touches at
+// most n / 16 + 2 blocks, so its tiles stay below the next one's): no counts are summed, and a
+// 256-way search finds s.  blockIdx.y picks a share of the heads.
+//
+// A thread keeps one item index u of one row, with its cosines and sines in registers, and
+// goes through the heads of its share: keys with the rows on adjacent lanes (16 slots of a
+// piece are 256 bytes of a pool tile), queries with the items on adjacent lanes.  FP8 values
+// are transposed through shared memory: a warp takes a head's 16 rows, and every lane stores
+// whole 16-slot runs of four dims.
+constexpr int kTileRows = kBlockTokens;
+
+struct Tile {
+    int32_t row0;            // first row of the new rows, of slot `lo`
+    int pos0;                // position of the block's slot 0
+    int lo, hi;              // slots lo .. hi - 1
+    int32_t blk;             // as read from the table
+};
+
+__device__ __forceinline__ int tile_base(const RParams& p, int s) {
+    return (__ldg(p.cu + s) >> 4) + 2 * s;        // (arithmetic shift: also of a bad negative entry)
+}
+
+// The CTA's tile, the same in every thread; false: none, or at no position of the table
+// (flagged).  The block is checked by the caller, when its load has had time to land.
+__device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
+    const int tid = threadIdx.x;
+    // last s in [lo, lo + n) with tile_base(s) <= t: 256 probes narrow it 256 times
+    int lo = 0, n = p.S;
+    while (n > 1) {
+        const int step = (n + kThreads - 1) / kThreads;
+        const int s = lo + tid * step;
+        const int hits = __syncthreads_count(tid * step < n && tile_base(p, s) <= t);
+        const int k = hits > 0 ? hits - 1 : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    const int first = __ldg(p.cu + lo), next = __ldg(p.cu + lo + 1);
+    const bool report = tid == 0 && blockIdx.y == 0;
+    if (first < 0 || next > p.total || next < first) {
+        if (report) raise_flag(p.err, PA_DEV_ERR_BAD_CU);
+        return false;
+    }
+    const long long start = __ldg(p.start_pos + lo);
+    const long long from = start >> 4;                              // block of the first row
+    const long long b = from + (t - ((first >> 4) + 2 * lo));
+    const long long begin = max(start, b * kTileRows), end = min(start + (next - first), (b + 1) * kTileRows);
+    if (b < from || begin >= end) return false;                     // (a gap between sequences)
+    if (b < 0 || b >= p.max_blocks) {
+        if (report) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+        return false;
+    }
+    out.blk = __ldg(p.tables + (size_t)lo * p.max_blocks + (int)b);
+    out.pos0 = (int)(b * kTileRows);
+    out.lo = (int)(begin - b * kTileRows);
+    out.hi = (int)(end - b * kTileRows);
+    out.row0 = first + (int)(begin - start);
+    return true;
+}
+
+// FP8 values of one head: lane = (slot, half of the dims).  `sm`: D / 4 x 16 words of the warp.
+template <int D>
+__device__ __forceinline__ void put_fp8_values(const RParams& p, const Tile& tile, int h, uint32_t* sm) {
+    constexpr int NP = D / 16;                  // 16-byte pieces of half a row
+    const int lane = threadIdx.x & 31, slot = lane & 15, half = lane >> 4;
+    const bool live = slot >= tile.lo && slot < tile.hi;
+    uint4 v[NP];
+    const char* src = p.v_new + (long long)(tile.row0 + slot - tile.lo) * p.v_stride + (size_t)h * (2 * D) + half * D;
 #pragma unroll
-            for (int x = 1; x < PH; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            if (live && (is_k || is_v)) {
-                const float scale = __fdiv_rn(m, 448.f);
-                char* rec = pool + ((size_t)blk * p.Hkv + h) * fp8_record_bytes(D);
-                const uint2 ca = e4m3_codes(a, scale), cb = e4m3_codes(b, scale);
-                if (is_k) {
-                    *reinterpret_cast<uint2*>(rec + ((at.a >> 1) * kBlockTokens + slot) * 16 + (at.a & 1) * 8) = ca;
-                    *reinterpret_cast<uint2*>(rec + ((at.b >> 1) * kBlockTokens + slot) * 16 + (at.b & 1) * 8) = cb;
+    for (int i = 0; i < NP; ++i)
+        v[i] = live ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) m = fmaxf(m, max_abs<8>(unpack<8>(v[i])));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    const float scale = __fdiv_rn(m, 448.f);
+    __syncwarp();                               // (the last head's reads are done)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint2 c = e4m3_codes(unpack<8>(v[i]), scale);
+        const int d4 = half * (D / 8) + 2 * i;
+        sm[d4 * 16 + slot] = c.x;
+        sm[(d4 + 1) * 16 + slot] = c.y;
+    }
+    __syncwarp();
+    char* rec = p.v_pool + ((size_t)tile.blk * p.Hkv + h) * fp8_record_bytes(D);
+    for (int d4 = lane; d4 < D / 4; d4 += 32) {
+        uint32_t y[4][4];                       // [dim][four slots]
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sm + d4 * 16 + 4 * w);
+            const uint32_t a = __byte_perm(x.x, x.y, 0x5140), b = __byte_perm(x.z, x.w, 0x5140);
+            const uint32_t c = __byte_perm(x.x, x.y, 0x7362), d = __byte_perm(x.z, x.w, 0x7362);
+            y[0][w] = __byte_perm(a, b, 0x5410);
+            y[1][w] = __byte_perm(a, b, 0x7632);
+            y[2][w] = __byte_perm(c, d, 0x5410);
+            y[3][w] = __byte_perm(c, d, 0x7632);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            char* dst = rec + (4 * d4 + j) * 16;
+            if (tile.lo == 0 && tile.hi == kTileRows) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+                continue;
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (4 * w >= tile.lo && 4 * w + 4 <= tile.hi) {
+                    *reinterpret_cast<uint32_t*>(dst + 4 * w) = y[j][w];
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        rec[(at.a * 8 + e) * kBlockTokens + slot] = (char)((e < 4 ? ca.x : ca.y) >> (8 * (e & 3)));
-                        rec[(at.b * 8 + e) * kBlockTokens + slot] = (char)((e < 4 ? cb.x : cb.y) >> (8 * (e & 3)));
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        if (4 * w + k >= tile.lo && 4 * w + k < tile.hi) dst[4 * w + k] = (char)(y[j][w] >> (8 * k));
                 }
-                if (u == 0) *reinterpret_cast<float*>(rec + (size_t)16 * D + 4 * slot) = scale;
             }
-        } else {
-            // the largest magnitude of each piece's 32-value block: its four pieces' maxima,
-            // wherever in the head's lanes they are
-            const float ma = max_abs<E>(a), mb = max_abs<E>(b);
-            const int lane = tid & 31, base = lane - u;
-            char* rec = pool + ((size_t)blk * p.Hkv + h) * fp4_record_bytes(D);
+        }
+    }
+    if (live && half == 0) *reinterpret_cast<float*>(rec + (size_t)16 * D + 4 * slot) = scale;
+}
+
+template <int D, pa_dtype T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RParams p) {
+    constexpr int E = T == PA_F32 ? 4 : 8;
+    constexpr int PH = D / (2 * E);
+    constexpr int GROUPS = kThreads / (kTileRows * PH);      // threads of a (row, item), a share of the heads each
+    constexpr int PAD = D / 2 + 2;                           // (rows on different banks)
+    __shared__ __align__(16) float2 cs[kTileRows * PAD];
+    __shared__ uint64_t turns[D / 2];
+    __shared__ __align__(16) uint32_t sm_v[T == PA_FP8_E4M3 ? 8 * (D / 4) * 16 : 1];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p);
+    if (tid < p.half) turns[tid] = fixed_turns(p.inv_freq[tid]);
+    Tile tile;
+    if (!find_tile(p, blockIdx.x, tile)) return;
+    const int share = blockIdx.y * GROUPS, stride = gridDim.y * GROUPS;
+    auto row_at = [&](int slot) { return (long long)(tile.row0 + slot - tile.lo); };
+    // Queries: items on adjacent lanes.  N heads are loaded while the N before them are turned
+    // and stored (q_out may be q, so the compiler would not move loads past stores); the first
+    // ones are under way while the cosines are made.
+    constexpr int N = kTileHeads;
+    const int qu = tid % PH, qslot = (tid / PH) % kTileRows, qg = share + tid / (PH * kTileRows);
+    const bool q_here = p.Hq > 0 && qslot >= tile.lo && qslot < tile.hi;
+    const Pair qat = pieces_of<E>(qu, p.half, !INTERLEAVED);
+    // (a row's heads span less than 2^26 bytes: 32-bit offsets)
+    const char* q_src = p.q + row_at(qslot) * p.q_stride + qat.a * 16 + (uint32_t)(qg * (PH * 32));
+    const int q_ab = (qat.b - qat.a) * 16, q_step = stride * (PH * 32);
+    const int q_heads = q_here && qg < p.Hq ? (p.Hq - qg + stride - 1) / stride : 0;     // of this thread
+    // its heads first .. first + N - 1
+    auto load_q = [&](int first, uint4 (&ra)[N], uint4 (&rb)[N]) {
+        const char* s = q_src + (uint32_t)(first * q_step);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int pc = k ? at.b : at.a;
-                float m = 0.f;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    bool second;
-                    const int from = base + item_of_piece<E>((pc & ~3) + y, p.half, split, second);
-                    const float va = __shfl_sync(0xffffffffu, ma, from), vb = __shfl_sync(0xffffffffu, mb, from);
-                    m = fmaxf(m, second ? vb : va);
-                }
-                if (!live || (!is_k && !is_v)) continue;
-                const int code = m > 0.f ? max((int)(__float_as_uint(m) >> 23) - 2, 0) : 0;
-                const float inv = exp2i(127 - code);                  // 1 / scale, exact
-                const Piece<E>& x = k ? b : a;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t two = m > 0.f ? pack_e2m1x2(x.x[2 * c] * inv, x.x[2 * c + 1] * inv) : 0u;
-                    if (is_k) {
-                        rec[(size_t)slot * (D / 2) + c * (D / 8) + pc] = (char)two;
-                    } else {
-                        // a byte holds two slots of one dim, and rows of one call may share it
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int at_byte = (((2 * c + e) * 4 + (slot % 8) / 2) * (D / 16) + pc / 2) * 4 +
-                                                (pc & 1) * 2 + slot / 8;
-                            unsigned int* word = reinterpret_cast<unsigned int*>(rec + (at_byte & ~3));
-                            const int shift = (at_byte & 3) * 8 + (slot & 1) * 4;
-                            atomicAnd(word, ~(0xfu << shift));
-                            atomicOr(word, ((two >> (4 * e)) & 0xfu) << shift);
-                        }
-                    }
-                }
-                if ((pc & 3) == 0) rec[8 * D + slot * (D / 32) + (pc >> 2)] = (char)code;
+        for (int i = 0; i < N; ++i)
+            if (first + i < q_heads) {
+                ra[i] = *reinterpret_cast<const uint4*>(s + i * q_step);
+                rb[i] = *reinterpret_cast<const uint4*>(s + i * q_step + q_ab);
             }
+    };
+    uint4 a0[N], b0[N];
+    load_q(0, a0, b0);
+    __syncthreads();
+    const int rows = tile.hi - tile.lo;
+    for (int i = tid; i < rows * p.half; i += kThreads) {
+        const int r = i / p.half, f = i - r * p.half;
+        cs[(tile.lo + r) * PAD + f] = cos_sin(turns[f] * (uint64_t)(tile.pos0 + tile.lo + r));
+    }
+    if (tile.blk < 0 || tile.blk >= p.num_blocks) {        // no place: the tile is skipped
+        if (tid == 0 && blockIdx.y == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+        return;
+    }
+    __syncthreads();
+    if (q_heads > 0) {
+        const bool turn = qu < p.half / E;
+        float2 c[E];
+        if (turn) item_turns<E>(cs + qslot * PAD, qu, c);
+        char* q_dst = p.q_out + row_at(qslot) * p.q_out_stride + qat.a * 16 + (uint32_t)(qg * (PH * 32));
+        auto store_q = [&](int first, const uint4 (&ra)[N], const uint4 (&rb)[N]) {
+            char* d = q_dst + (uint32_t)(first * q_step);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (first + i < q_heads) {
+                    Piece<E> a = unpack<E>(ra[i]), b = unpack<E>(rb[i]);
+                    if (turn) turn_item<E, INTERLEAVED>(a, b, c);
+                    *reinterpret_cast<uint4*>(d + i * q_step) = pack<E>(a);
+                    *reinterpret_cast<uint4*>(d + i * q_step + q_ab) = pack<E>(b);
+                }
+        };
+        uint4 a1[N], b1[N];
+        for (int i = 0; i < q_heads; i += 2 * N) {
+            load_q(i + N, a1, b1);
+            store_q(i, a0, b0);
+            load_q(i + 2 * N, a0, b0);
+            store_q(i + N, a1, b1);
+        }
+    }
+    if constexpr (T == PA_F32 || T == PA_BF16) {
+        // keys and values: rows on adjacent lanes
+        const int slot = tid % kTileRows, u = (tid / kTileRows) % PH, g = share + tid / (PH * kTileRows);
+        if (slot < tile.lo || slot >= tile.hi) return;
+        const Pair at = pieces_of<E>(u, p.half, !INTERLEAVED);
+        const bool turn = u < p.half / E;
+        float2 c[E];
+        if (turn) item_turns<E>(cs + slot * PAD, u, c);
+        const char* ks = p.k_new + row_at(slot) * p.k_stride;
+        const char* vs = p.v_new + row_at(slot) * p.v_stride;
+        constexpr int NK = 2;
+        for (int h0 = g; h0 < p.Hkv; h0 += NK * stride) {
+            uint4 ra[NK], rb[NK], va[NK], vb[NK];
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                const size_t off = (size_t)(h0 + i * stride) * (PH * 32);
+                if (h0 + i * stride < p.Hkv) {
+                    ra[i] = *reinterpret_cast<const uint4*>(ks + off + at.a * 16);
+                    rb[i] = *reinterpret_cast<const uint4*>(ks + off + at.b * 16);
+                    va[i] = *reinterpret_cast<const uint4*>(vs + off + u * 32);
+                    vb[i] = *reinterpret_cast<const uint4*>(vs + off + u * 32 + 16);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                const int h = h0 + i * stride;
+                if (h < p.Hkv) {
+                    Piece<E> a = unpack<E>(ra[i]), b = unpack<E>(rb[i]);
+                    if (turn) turn_item<E, INTERLEAVED>(a, b, c);
+                    const size_t to = ((((size_t)tile.blk * p.Hkv + h) * (2 * PH)) * kBlockTokens + slot) * 16;
+                    *reinterpret_cast<uint4*>(p.k_pool + to + at.a * 256) = pack<E>(a);
+                    *reinterpret_cast<uint4*>(p.k_pool + to + at.b * 256) = pack<E>(b);
+                    *reinterpret_cast<uint4*>(p.v_pool + to + u * 512) = va[i];
+                    *reinterpret_cast<uint4*>(p.v_pool + to + u * 512 + 256) = vb[i];
+                }
+            }
+        }
+    } else {
+        // keys (and FP4 values): a head's items on adjacent lanes, which share its maxima
+        const int u = tid % PH, slot = (tid / PH) % kTileRows, g = share + tid / (PH * kTileRows);
+        const bool here = slot >= tile.lo && slot < tile.hi;
+        const bool turn = u < p.half / E;
+        float2 c[E];
+        if (turn && here) item_turns<E>(cs + slot * PAD, u, c);
+        constexpr int KINDS = T == PA_FP8_E4M3 ? 1 : 2;
+        for (int h0 = share; h0 < p.Hkv; h0 += stride) {             // (the same trips in every lane)
+            const int h = h0 + (g - share);
+#pragma unroll
+            for (int kind = 0; kind < KINDS; ++kind) {
+                const bool split = !INTERLEAVED && kind == 0, live = here && h < p.Hkv;
+                const Pair at = pieces_of<E>(u, p.half, split);
+                const char* src = (kind == 0 ? p.k_new + row_at(slot) * p.k_stride : p.v_new + row_at(slot) * p.v_stride) +
+                                  (size_t)h * (PH * 32);
+                uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
+                if (live) {
+                    ra = *reinterpret_cast<const uint4*>(src + at.a * 16);
+                    rb = *reinterpret_cast<const uint4*>(src + at.b * 16);
+                }
+                Piece<E> a = unpack<E>(ra), b = unpack<E>(rb);
+                if (kind == 0 && turn && live) turn_item<E, INTERLEAVED>(a, b, c);
+                put_quantised<D, T>(p, kind == 0 ? p.k_pool : p.v_pool, tile.blk, live ? h : 0, slot, kind == 0, live, u, at,
+                                    split, a, b);
+            }
+        }
+        if constexpr (T == PA_FP8_E4M3) {
+            const int warp = tid >> 5;
+            for (int h = blockIdx.y * 8 + warp; h < p.Hkv; h += gridDim.y * 8)
+                put_fp8_values<D>(p, tile, h, sm_v + warp * (D / 4) * 16);
         }
     }
 }
 
 template <int D, pa_dtype T, bool INTERLEAVED>
 cudaError_t launch_rope(const RParams& p, cudaStream_t stream) {
+    // Rows of few tokens per sequence (a decode step) go row by row, chunks tile by tile.
+    const bool tiles = p.total >= kTileMinRows * (long long)p.S;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.total);
+    // A tile's heads are shared by several CTAs while that still finds idle SMs (two CTAs fit on
+    // one): 512 full tiles of 32 + 16 heads of 128 take 35.6 us with one CTA each, 37.7 with two;
+    // 185 ragged ones into FP8 pools 25.9 and 22.4 us.
+    const int full = p.total / kTileRows > 0 ? p.total / kTileRows : 1;
+    const int shares = full >= 304 ? 1 : full >= 38 ? (304 + full - 1) / full : 8;
+    cfg.gridDim = tiles ? dim3((unsigned)(p.total / kTileRows + 2ll * p.S), shares) : dim3((unsigned)p.total);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -280,7 +593,8 @@ cudaError_t launch_rope(const RParams& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, T, INTERLEAVED>, p);
+    return tiles ? cudaLaunchKernelEx(&cfg, rope_append_tile_kernel<D, T, INTERLEAVED>, p)
+                 : cudaLaunchKernelEx(&cfg, rope_append_kernel<D, T, INTERLEAVED>, p);
 }
 
 template <int D, bool INTERLEAVED>

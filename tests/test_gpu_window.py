@@ -291,6 +291,41 @@ def test_rope_append_skips_rows_without_a_place():
     assert [bool(out[r].isnan().any()) for r in range(8)] == [False] * 3 + [True] * 5
 
 
+@pytest.mark.parametrize("cache", CACHES)
+def test_rope_append_of_chunks_skips_what_has_no_place(cache):
+    # chunks (block by block): a block without a table entry, positions before 0 and past the
+    # table; every other row as if alone
+    heads, counts, starts = (4, 2, 64), [20, 40, 30, 9], [0, 5, -7, 50]
+    (q, k, v), (dq, dk, dv) = rope_inputs(cache, counts, heads, True, seed=8)
+    tables = torch.arange(16, dtype=torch.int32).view(4, 4)
+    tables[1, 1] = 16                                            # positions 16 .. 31 of sequence 1
+    kp, vp, out, err = pool_for(cache, 16, 2, 64), pool_for(cache, 16, 2, 64), nan_like(dq.contiguous()), err_flag()
+    args = (frequencies(64), tables.cuda(), i32(starts), cu_of(counts))
+    rope_call(cache)(kp, vp, out, dq, dk, dv, *args, err_flag=err)
+    assert int(err) == pk.DEV_ERR_BAD_BLOCK | pk.DEV_ERR_BAD_POS
+    ok = [a + i >= 0 and a + i < 64 and not (s == 1 and 16 <= a + i < 32)
+          for s, (a, n) in enumerate(zip(starts, counts)) for i in range(n)]
+    assert [not bool(out[r].isnan().any()) for r in range(sum(counts))] == ok
+    # one row per call and sequence gives the same pools and queries, bit for bit
+    k2, v2, out2 = pool_for(cache, 16, 2, 64), pool_for(cache, 16, 2, 64), nan_like(out)
+    for i in range(max(counts)):
+        at = [(s, sum(counts[:s]) + i) for s in range(4) if i < counts[s]]
+        rows = torch.tensor([r for _, r in at], device="cuda")
+        one = torch.empty_like(out[rows])
+        one.copy_(out2[rows])
+        rope_call(cache)(k2, v2, one, dq[rows], dk[rows], dv[rows], frequencies(64),
+                         tables[[s for s, _ in at]].contiguous().cuda(), i32([starts[s] + i for s, _ in at]), cu_of([1] * len(at)))
+        out2[rows] = one
+    assert torch.equal(kp, k2) and torch.equal(vp, v2)
+    assert torch.equal(out.nan_to_num(7.0), out2.nan_to_num(7.0))
+    # a prefix sum that does not end at the rows, or runs backwards
+    for cu in ([0, 20, 60, 90, 98], [0, 20, 60, 90, 100], [0, 60, 20, 90, 99], [0, -4, 60, 90, 99]):
+        err.zero_()
+        out = nan_like(out)
+        rope_call(cache)(kp, vp, out, dq, dk, dv, frequencies(64), tables.cuda(), i32([0, 5, 0, 40]), i32(cu), err_flag=err)
+        assert int(err) & pk.DEV_ERR_BAD_CU
+
+
 # ---------------------------------------------------------------------------- prefill
 def run_prefill(c, starts, counts, q, window, sinks, scale, err=None, max_chunk=None, cu=None):
     out = nan_like(q.cuda())

@@ -97,6 +97,14 @@ def test_bindings_check_the_tensors(native):
         native.prefill_attention_window(q.clone(), q, pool, pool, tables, lens, cu, 0.1, 1, 8)
     with pytest.raises(ValueError):
         native.rope_append_kv(pool, pool, q.clone(), q, new, new, freq, tables, lens, cu)
+    with pytest.raises(ValueError):
+        native.decode_attention_window(q.clone(), q[:2], pool, pool, tables, lens, 0.1, 8)
+    with pytest.raises(ValueError):
+        native.decode_attention_window(q.clone(), q, pool[0], pool[0], tables, lens, 0.1, 8)
+    with pytest.raises(TypeError):
+        native.decode_attention_window(q.clone(), q, pool.half(), pool.half(), tables, lens, 0.1, 8)
+    with pytest.raises(ValueError):
+        native.rope_append_kv(pool, pool, None, q, new, new, freq, tables, lens, cu)
     # types, shapes, layouts (checked before the device)
     dev = 0
     with pytest.raises(TypeError):
