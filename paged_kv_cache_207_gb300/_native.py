@@ -423,8 +423,8 @@ def prefill_attention(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, sca
 
 
 # Bindings of the rotary append and of the windowed attention.  A decode step calls them once per
-# layer, and a short step waits for them rather than for the GPU: each tensor is checked in one
-# expression, and only a refused one is looked at again for the reason.
+# layer, and a short step waits for them rather than for the GPU: all tensors are checked in one
+# expression, and only when it is false each is looked at again for the reason.
 _PLAIN_CODE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
 _I32 = torch.int32
 _cuda_device = torch.cuda.current_device
@@ -508,26 +508,58 @@ def _flag(dev, err_flag):
 def _rope_append(pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
                  cu_new_tokens, interleaved, err_flag, stream) -> None:
     nb, hkv, d, code, rows = pool(k_pool)
-    dev, shape, half = k_pool.get_device(), k_pool.shape, inv_freq.shape[0]
-    s, width = block_tables.shape
-    kv = (k_new.shape[0], hkv, d)
-    kn, ks = _rows(dev, k_new, "k_new", rows, kv)
-    vn, vs = _rows(dev, v_new, "v_new", rows, kv)
     if q is None or q_out is None:
         if q is not q_out:
             raise ValueError("q and q_out come together")
-        hq, qi, qs, qo, qos = 0, None, 0, None, 0
+        q = q_out = k_new                               # (checked once more, not used)
+        with_q = False
     else:
+        with_q = True
+    try:
+        dev, shape, kind = k_pool.get_device(), k_pool.shape, k_pool.dtype
+        (half,) = inv_freq.shape
+        s, width = block_tables.shape
+        n, hq, _ = of_q = q.shape
+        of_k = (n, hkv, d)
+        q_row, q_head, q_one = q.stride()
+        o_row, o_head, o_one = q_out.stride()
+        k_row, k_head, k_one = k_new.stride()
+        v_row, v_head, v_one = v_new.stride()
+        fine = (q.dtype is rows and q_out.dtype is rows and k_new.dtype is rows and v_new.dtype is rows
+                and of_q[2] == d and q_out.shape == of_q and k_new.shape == of_k and v_new.shape == of_k
+                and q_one == o_one == k_one == v_one == 1 and q_head == o_head == k_head == v_head == d
+                and v_pool.dtype is kind and v_pool.shape == shape and inv_freq.dtype is torch.float64
+                and block_tables.dtype is _I32 and start_pos.dtype is _I32 and cu_new_tokens.dtype is _I32
+                and start_pos.shape == (s,) and cu_new_tokens.shape == (s + 1,)
+                and q.get_device() == q_out.get_device() == k_new.get_device() == v_new.get_device()
+                == v_pool.get_device() == inv_freq.get_device() == block_tables.get_device()
+                == start_pos.get_device() == cu_new_tokens.get_device() == dev >= 0
+                and k_pool.is_contiguous() and v_pool.is_contiguous() and inv_freq.is_contiguous()
+                and block_tables.is_contiguous() and start_pos.is_contiguous() and cu_new_tokens.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        # one by one, for the reason (or none: a single head's stride, or no rows, say nothing)
+        dev, shape, kind = k_pool.get_device(), k_pool.shape, k_pool.dtype
+        n = k_new.shape[0]
+        _, k_row = _rows(dev, k_new, "k_new", rows, (n, hkv, d))
+        _, v_row = _rows(dev, v_new, "v_new", rows, (n, hkv, d))
         hq = q.shape[1]
-        qi, qs = _rows(dev, q, "q", rows, (kv[0], hq, d))
-        qo, qos = _rows(dev, q_out, "q_out", rows, (kv[0], hq, d))
-    _call_on(dev, stream, lib().pa_rope_append_kv, _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
-             _checked(dev, v_pool, "v_pool", k_pool.dtype, shape), qo, qi, kn, vn, qos, qs, ks, vs,
-             _checked(dev, inv_freq, "inv_freq", torch.float64, (half,)), 2 * half, 1 if interleaved else 0,
-             _checked(dev, block_tables, "block_tables", _I32, (s, width)), width,
-             _checked(dev, start_pos, "start_pos", _I32, (s,)),
-             _checked(dev, cu_new_tokens, "cu_new_tokens", _I32, (s + 1,)), s, kv[0], nb, hq, hkv, d,
-             code, _flag(dev, err_flag))
+        _, q_row = _rows(dev, q, "q", rows, (n, hq, d))
+        _, o_row = _rows(dev, q_out, "q_out", rows, (n, hq, d))
+        s, width, half = block_tables.shape[0], block_tables.shape[1], inv_freq.shape[0]
+        _checked(dev, k_pool, "k_pool", kind, shape)
+        _checked(dev, v_pool, "v_pool", kind, shape)
+        _checked(dev, inv_freq, "inv_freq", torch.float64, (half,))
+        _checked(dev, block_tables, "block_tables", _I32, (s, width))
+        _checked(dev, start_pos, "start_pos", _I32, (s,))
+        _checked(dev, cu_new_tokens, "cu_new_tokens", _I32, (s + 1,))
+    _call_on(dev, stream, lib().pa_rope_append_kv, k_pool.data_ptr(), v_pool.data_ptr(),
+             q_out.data_ptr() if with_q else None, q.data_ptr() if with_q else None, k_new.data_ptr(),
+             v_new.data_ptr(), o_row, q_row, k_row, v_row, inv_freq.data_ptr(), 2 * half,
+             1 if interleaved else 0, block_tables.data_ptr(), width, start_pos.data_ptr(),
+             cu_new_tokens.data_ptr(), s, n, nb, hq if with_q else 0, hkv, d, code,
+             None if err_flag is None else _flag(dev, err_flag))
 
 
 def rope_append_kv(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
@@ -557,16 +589,33 @@ def rope_append_kv_fp4(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_t
 def _decode_window(pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
                    err_flag, stream) -> None:
     nb, hkv, d, code, rows = pool(k_pool)
-    dev, shape, of_q = k_pool.get_device(), k_pool.shape, q.shape
-    s, width = block_tables.shape
-    if len(of_q) != 3 or of_q[0] != s or of_q[2] != d:
-        raise ValueError("q must have shape [num_seqs][num_q_heads][head_dim]")
-    _call_on(dev, stream, lib().pa_decode_attention_window, _checked(dev, out, "out", rows, of_q),
-             _checked(dev, q, "q", rows, of_q), _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
-             _checked(dev, v_pool, "v_pool", k_pool.dtype, shape),
-             _checked(dev, block_tables, "block_tables", _I32, (s, width)),
-             _checked(dev, context_lens, "context_lens", _I32, (s,)), s, of_q[1], hkv, d, width, nb,
-             _bound(window), _bound(num_sinks), float(scale), code, _flag(dev, err_flag))
+    try:
+        dev, shape, kind = k_pool.get_device(), k_pool.shape, k_pool.dtype
+        s, width = block_tables.shape
+        n, hq, dq = of_q = q.shape
+        fine = (n == s and dq == d and q.dtype is rows and out.dtype is rows and out.shape == of_q
+                and v_pool.dtype is kind and v_pool.shape == shape and block_tables.dtype is _I32
+                and context_lens.dtype is _I32 and context_lens.shape == (s,)
+                and q.get_device() == out.get_device() == v_pool.get_device() == block_tables.get_device()
+                == context_lens.get_device() == dev >= 0
+                and q.is_contiguous() and out.is_contiguous() and k_pool.is_contiguous()
+                and v_pool.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:                                        # one by one, for the reason
+        s, width = block_tables.shape[0], block_tables.shape[1]
+        hq = q.shape[1]
+        for t, name, dtype, of_t in ((q, "q", rows, (s, hq, d)), (out, "out", rows, (s, hq, d)),
+                                     (k_pool, "k_pool", k_pool.dtype, k_pool.shape),
+                                     (v_pool, "v_pool", k_pool.dtype, k_pool.shape),
+                                     (block_tables, "block_tables", _I32, (s, width)),
+                                     (context_lens, "context_lens", _I32, (s,))):
+            _checked(k_pool.get_device(), t, name, dtype, of_t)
+        raise ValueError("arguments of different shapes, types or devices")
+    _call_on(dev, stream, lib().pa_decode_attention_window, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
+             v_pool.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), s, hq, hkv, d, width, nb,
+             _bound(window), _bound(num_sinks), float(scale), code,
+             None if err_flag is None else _flag(dev, err_flag))
 
 
 def decode_attention_window(out, q, k_pool, v_pool, block_tables, context_lens, scale, window: int,
@@ -597,17 +646,35 @@ def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu
     """prefill_attention with every row limited to the last ``window`` positions up to its own
     and the first ``num_sinks`` (bf16)."""
     nb, hkv, d, code, rows = _plain_pool(k_pool)
-    dev, shape, of_q = k_pool.get_device(), k_pool.shape, q.shape
-    s, width = block_tables.shape
-    if len(of_q) != 3 or of_q[2] != d:
-        raise ValueError("q must have shape [total_q][num_q_heads][head_dim]")
-    _call_on(dev, stream, lib().pa_prefill_attention_window, _checked(dev, out, "out", rows, of_q),
-             _checked(dev, q, "q", rows, of_q), _checked(dev, k_pool, "k_pool", k_pool.dtype, shape),
-             _checked(dev, v_pool, "v_pool", k_pool.dtype, shape),
-             _checked(dev, block_tables, "block_tables", _I32, (s, width)), width,
-             _checked(dev, start_pos, "start_pos", _I32, (s,)),
-             _checked(dev, cu_q, "cu_q", _I32, (s + 1,)), s, of_q[0], _bound(max_chunk), of_q[1], hkv, d,
-             nb, _bound(window), _bound(num_sinks), float(scale), code, _flag(dev, err_flag))
+    try:
+        dev, shape, kind = k_pool.get_device(), k_pool.shape, k_pool.dtype
+        s, width = block_tables.shape
+        n, hq, dq = of_q = q.shape
+        fine = (dq == d and q.dtype is rows and out.dtype is rows and out.shape == of_q
+                and v_pool.dtype is kind and v_pool.shape == shape and block_tables.dtype is _I32
+                and start_pos.dtype is _I32 and start_pos.shape == (s,)
+                and cu_q.dtype is _I32 and cu_q.shape == (s + 1,)
+                and q.get_device() == out.get_device() == v_pool.get_device() == block_tables.get_device()
+                == start_pos.get_device() == cu_q.get_device() == dev >= 0
+                and q.is_contiguous() and out.is_contiguous() and k_pool.is_contiguous()
+                and v_pool.is_contiguous() and block_tables.is_contiguous() and start_pos.is_contiguous()
+                and cu_q.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:                                        # one by one, for the reason
+        s, width = block_tables.shape[0], block_tables.shape[1]
+        n, hq = q.shape[0], q.shape[1]
+        for t, name, dtype, of_t in ((q, "q", rows, (n, hq, d)), (out, "out", rows, (n, hq, d)),
+                                     (k_pool, "k_pool", k_pool.dtype, k_pool.shape),
+                                     (v_pool, "v_pool", k_pool.dtype, k_pool.shape),
+                                     (block_tables, "block_tables", _I32, (s, width)),
+                                     (start_pos, "start_pos", _I32, (s,)), (cu_q, "cu_q", _I32, (s + 1,))):
+            _checked(k_pool.get_device(), t, name, dtype, of_t)
+        raise ValueError("arguments of different shapes, types or devices")
+    _call_on(dev, stream, lib().pa_prefill_attention_window, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
+             v_pool.data_ptr(), block_tables.data_ptr(), width, start_pos.data_ptr(), cu_q.data_ptr(), s, n,
+             _bound(max_chunk), hq, hkv, d, nb, _bound(window), _bound(num_sinks), float(scale), code,
+             None if err_flag is None else _flag(dev, err_flag))
 
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024

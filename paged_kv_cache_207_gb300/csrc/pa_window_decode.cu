@@ -324,7 +324,12 @@ struct Fp4Cache {
     }
     // scale byte b of w: 2^(code - 127) (the code is the exponent field; code 0 gives 0)
     static __device__ __forceinline__ float scale_value(uint32_t w, int b) {
-        return __uint_as_float(((w >> (8 * b)) & 0xffu) << 23);
+        const int left = 23 - 8 * b;                          // (a constant where this is inlined)
+        return __uint_as_float((left >= 0 ? w << left : w >> -left) & 0x7f800000u);
+    }
+    // log2 of a block's c_b, from its R_b: 135 - R_b, at most 127
+    static __device__ __forceinline__ int c_exp(uint32_t refs, int b) {
+        return min(135 - (int)((refs >> (8 * b)) & 0xffu), 127);
     }
     __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
 #pragma unroll
@@ -378,14 +383,14 @@ struct Fp4Cache {
             const uint32_t raised = __vmaxu4(__vaddus4(top, 0x03030303u), ref_packed);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int eb = (int)((raised >> (8 * b)) & 0xffu);
-                const float cn = exp2i(min(135 - eb, 127)), f = cn / cb[b];        // a power of two: exact
+                const int en = c_exp(raised, b);
+                const float f = exp2i(en - c_exp(ref_packed, b));                  // exact
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     o[2 * b][x] *= f;
                     o[2 * b + 1][x] *= f;
                 }
-                cb[b] = cn;
+                cb[b] = exp2i(en);
             }
             ref_packed = raised;
         }
@@ -411,7 +416,7 @@ struct Fp4Cache {
     __device__ __forceinline__ void finish(Running&, float (&o)[KS][4]) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const float f = 1.f / cb[b];
+            const float f = exp2i(-c_exp(ref_packed, b));
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 o[2 * b][x] *= f;
