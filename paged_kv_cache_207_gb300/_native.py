@@ -61,10 +61,11 @@ class BmStats(ctypes.Structure):
 
 
 _lib = None
+_quick = None                   # csrc/pa_binding.c, where it was built: see the bindings that use it
 
 
 def lib() -> ctypes.CDLL:
-    global _lib
+    global _lib, _quick
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
@@ -144,6 +145,15 @@ def lib() -> ctypes.CDLL:
               "pa_bm_seq_len", "pa_bm_refcount", "pa_bm_stats"):
         getattr(L, n).restype = ctypes.c_int
     _lib = L
+    try:
+        from . import _quick as quick
+    except ImportError:
+        return L
+    quick.bind(*(ctypes.cast(f, p).value for f in (L.pa_rope_append_kv, L.pa_decode_attention_window,
+                                                   L.pa_prefill_attention_window)),
+               torch.Tensor, torch.float32, torch.bfloat16, torch.uint8, torch.int32, torch.float64,
+               torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    _quick = quick
     return L
 
 
@@ -423,8 +433,10 @@ def prefill_attention(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, sca
 
 
 # Bindings of the rotary append and of the windowed attention.  A decode step calls them once per
-# layer, and a short step waits for them rather than for the GPU: all tensors are checked in one
-# expression, and only when it is false each is looked at again for the reason.
+# layer, and a short step waits for them rather than for the GPU: a call whose arguments are all
+# as they should be, on the current device and stream, goes through csrc/pa_binding.c, which
+# makes the same checks.  Where that answers -1 (or was not built), the tensors are checked here,
+# in one expression, and only when it is false each is looked at again for the reason.
 _PLAIN_CODE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
 _I32 = torch.int32
 _cuda_device = torch.cuda.current_device
@@ -568,22 +580,40 @@ def rope_append_kv(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_table
     are turned by (start_pos[s] + i) * inv_freq (float64 [rotary_dim / 2] on the device), keys
     and values go to the pools, the turned queries to q_out (which may be q; both None: no
     queries).  Rows [tokens][heads][D] may be column ranges of a wider tensor."""
-    _rope_append(_plain_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
-                 start_pos, cu_new_tokens, interleaved, err_flag, stream)
+    status = -1 if _quick is None else _quick.rope_append(
+        0, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos, cu_new_tokens,
+        interleaved, err_flag, stream)
+    if status == -1:
+        _rope_append(_plain_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
+                     start_pos, cu_new_tokens, interleaved, err_flag, stream)
+    elif status:
+        check("pa_rope_append_kv", status)
 
 
 def rope_append_kv_fp8(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
                        cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
     """rope_append_kv of bf16 rows into FP8 pools."""
-    _rope_append(_fp8_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
-                 start_pos, cu_new_tokens, interleaved, err_flag, stream)
+    status = -1 if _quick is None else _quick.rope_append(
+        2, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos, cu_new_tokens,
+        interleaved, err_flag, stream)
+    if status == -1:
+        _rope_append(_fp8_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
+                     start_pos, cu_new_tokens, interleaved, err_flag, stream)
+    elif status:
+        check("pa_rope_append_kv", status)
 
 
 def rope_append_kv_fp4(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
                        cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
     """rope_append_kv of bf16 rows into MXFP4 pools."""
-    _rope_append(_fp4_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
-                 start_pos, cu_new_tokens, interleaved, err_flag, stream)
+    status = -1 if _quick is None else _quick.rope_append(
+        3, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos, cu_new_tokens,
+        interleaved, err_flag, stream)
+    if status == -1:
+        _rope_append(_fp4_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables,
+                     start_pos, cu_new_tokens, interleaved, err_flag, stream)
+    elif status:
+        check("pa_rope_append_kv", status)
 
 
 def _decode_window(pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
@@ -622,22 +652,37 @@ def decode_attention_window(out, q, k_pool, v_pool, block_tables, context_lens, 
                             num_sinks: int = 0, err_flag=None, stream=None) -> None:
     """decode_attention over the last ``window`` positions and the first ``num_sinks``; table
     entries of blocks that hold none of them are not read."""
-    _decode_window(_plain_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
-                   num_sinks, err_flag, stream)
+    status = -1 if _quick is None else _quick.decode_window(
+        0, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks, err_flag, stream)
+    if status == -1:
+        _decode_window(_plain_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
+                       num_sinks, err_flag, stream)
+    elif status:
+        check("pa_decode_attention_window", status)
 
 
 def decode_attention_window_fp8(out, q, k_pool, v_pool, block_tables, context_lens, scale,
                                 window: int, num_sinks: int = 0, err_flag=None, stream=None) -> None:
     """decode_attention_window over FP8 pools (bf16 q and out)."""
-    _decode_window(_fp8_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
-                   num_sinks, err_flag, stream)
+    status = -1 if _quick is None else _quick.decode_window(
+        2, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks, err_flag, stream)
+    if status == -1:
+        _decode_window(_fp8_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
+                       num_sinks, err_flag, stream)
+    elif status:
+        check("pa_decode_attention_window", status)
 
 
 def decode_attention_window_fp4(out, q, k_pool, v_pool, block_tables, context_lens, scale,
                                 window: int, num_sinks: int = 0, err_flag=None, stream=None) -> None:
     """decode_attention_window over MXFP4 pools (bf16 q and out)."""
-    _decode_window(_fp4_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
-                   num_sinks, err_flag, stream)
+    status = -1 if _quick is None else _quick.decode_window(
+        3, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks, err_flag, stream)
+    if status == -1:
+        _decode_window(_fp4_pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window,
+                       num_sinks, err_flag, stream)
+    elif status:
+        check("pa_decode_attention_window", status)
 
 
 def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, scale,
@@ -645,6 +690,18 @@ def prefill_attention_window(out, q, k_pool, v_pool, block_tables, start_pos, cu
                              stream=None) -> None:
     """prefill_attention with every row limited to the last ``window`` positions up to its own
     and the first ``num_sinks`` (bf16)."""
+    status = -1 if _quick is None else _quick.prefill_window(
+        out, q, k_pool, v_pool, block_tables, start_pos, cu_q, scale, max_chunk, window, num_sinks, err_flag,
+        stream)
+    if status == -1:
+        _prefill_window(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, scale, max_chunk, window,
+                        num_sinks, err_flag, stream)
+    elif status:
+        check("pa_prefill_attention_window", status)
+
+
+def _prefill_window(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, scale, max_chunk, window,
+                    num_sinks, err_flag, stream) -> None:
     nb, hkv, d, code, rows = _plain_pool(k_pool)
     try:
         dev, shape, kind = k_pool.get_device(), k_pool.shape, k_pool.dtype

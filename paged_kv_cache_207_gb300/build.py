@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpaged_kv.so")
+# the quick way through the Python bindings (csrc/pa_binding.c), for this interpreter
+QUICK = os.path.join(PKG, "_quick.so")
+PYTHON_INCLUDE = sysconfig.get_paths()["include"]
 
 SOURCES = ["pa_api.cu", "pa_decode.cu", "pa_append.cu", "pa_prefill.cu", "pa_noalloc.cu",
            "pa_rope.cu", "pa_window_decode.cu", "pa_block_manager.cpp"]
@@ -39,10 +43,15 @@ def _inputs():
     return files
 
 
+def _has_python_h() -> bool:
+    return os.path.exists(os.path.join(PYTHON_INCLUDE, "Python.h"))
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    made = [LIB] + ([QUICK] if _has_python_h() else [])
+    if not all(os.path.exists(f) for f in made):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(f) for f in made)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -64,6 +73,19 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
     return obj
 
 
+def _compile_quick() -> None:
+    """csrc/pa_binding.c with the C compiler; without Python's headers the bindings do without."""
+    if not _has_python_h():
+        return
+    tmp = QUICK + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-fPIC", "-shared", "-I", INCLUDE, "-I", PYTHON_INCLUDE,
+           os.path.join(CSRC, "pa_binding.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on pa_binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, QUICK)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and not ptxas_verbose and not _stale():
         return LIB
@@ -77,6 +99,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _compile_quick()
     return LIB
 
 

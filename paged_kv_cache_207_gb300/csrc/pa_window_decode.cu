@@ -427,11 +427,13 @@ struct Fp4Cache {
 };
 
 // f32 tiles: each operand x is split into two tf32 numbers, h (x rounded) and l (x - h
-// rounded), and a product is h h' + h l' + l h' on the tensor cores: the dropped l l' and the
+// rounded), and a product is h h' + (h l' + l h') on the tensor cores: the dropped l l' and the
 // roundings of l are 2^-21 of the product at most, near fp32's own rounding, and the work does
-// not grow with G as with FMAs.  K and V fragments are plain 32-bit reads of the tiles (K's
-// are free of bank conflicts, V's two-way); the probabilities pass through 512 bytes of
-// shared memory per warp to reach the B operand's order.
+// not grow with G as with FMAs.  The tensor cores' own sums are cut, not rounded, at each step,
+// so they are kept short: h h' and the small products apart, a few steps each, added in fp32
+// (the outputs' relative error: 2.5e-7 to 3.5e-7; with one long sum 8e-7).
+// K and V fragments are plain 32-bit reads of the tiles (K's are free of bank conflicts, V's
+// two-way); the probabilities pass through shared memory to reach the B operand's order.
 __device__ __forceinline__ uint32_t tf32_of(float x) {
     uint32_t y;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
@@ -452,14 +454,14 @@ __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d += a b over 8 of the contraction's elements, a in fp32 (4 per lane), b split
-__device__ __forceinline__ void mma_split(float (&d)[4], const float (&a)[4], Split b0, Split b1) {
+// large += h h', small += h l' + l h' over 8 of the contraction's elements, a in fp32, b split
+__device__ __forceinline__ void mma_split(float (&large)[4], float (&small)[4], const float (&a)[4], Split b0, Split b1) {
     Split x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = split_tf32(a[i]);
-    mma_tf32_1688(d, x[0].l, x[1].l, x[2].l, x[3].l, b0.h, b1.h);
-    mma_tf32_1688(d, x[0].h, x[1].h, x[2].h, x[3].h, b0.l, b1.l);
-    mma_tf32_1688(d, x[0].h, x[1].h, x[2].h, x[3].h, b0.h, b1.h);
+    mma_tf32_1688(large, x[0].h, x[1].h, x[2].h, x[3].h, b0.h, b1.h);
+    mma_tf32_1688(small, x[0].l, x[1].l, x[2].l, x[3].l, b0.h, b1.h);
+    mma_tf32_1688(small, x[0].h, x[1].h, x[2].h, x[3].h, b0.l, b1.l);
 }
 
 template <int D>
@@ -484,8 +486,7 @@ struct F32Cache {
     }
     __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
         const float* k = reinterpret_cast<const float*>(kt);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
+        float large[2][2][4] = {}, small[2][4] = {};          // two sums of h h' per block, of every other step
 #pragma unroll
         for (int kk = 0; kk < D / 8; ++kk) {
             const Split b0 = split_tf32(q[kk][0]), b1 = split_tf32(q[kk][1]);
@@ -493,13 +494,13 @@ struct F32Cache {
             for (int b = 0; b < 2; ++b) {
                 const float* at = k + b * (TILE / 4) + (2 * kk * kBlockTokens + r) * 4 + c;
                 const float a[4] = {at[0], at[32], at[64], at[96]};
-                mma_split(s[b], a, b0, b1);
+                mma_split(large[b][kk & 1], small[b], a, b0, b1);
             }
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][i] *= scale;
+            for (int i = 0; i < 4; ++i) s[b][i] = (large[b][0][i] + large[b][1][i] + small[b][i]) * scale;
     }
     // (as for bf16)
     __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
@@ -518,17 +519,24 @@ struct F32Cache {
         }
         __syncwarp();
         if (run.rescale) rescale_rows(run, o);
+        Split p0[4], p1[4];                                   // of tokens c and c + 4 of 8, four times
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {                      // 8 tokens at a time: c and c + 4 of them
-            const int t0 = 8 * (kk & 1) + c, b = kk >> 1;
-            const Split b0 = split_tf32(sp[(16 * b + t0) * 8 + r]), b1 = split_tf32(sp[(16 * b + t0 + 4) * 8 + r]);
-            const float* v = reinterpret_cast<const float*>(vt) + b * (TILE / 4) + ((r >> 2) * kBlockTokens + t0) * 4 + (r & 3);
+        for (int kk = 0; kk < 4; ++kk) {
+            p0[kk] = split_tf32(sp[(8 * kk + c) * 8 + r]);
+            p1[kk] = split_tf32(sp[(8 * kk + c + 4) * 8 + r]);
+        }
+        const float* v = reinterpret_cast<const float*>(vt) + ((r >> 2) * kBlockTokens + c) * 4 + (r & 3);
 #pragma unroll
-            for (int mi = 0; mi < KS; ++mi) {
-                const float* at = v + mi * (4 * kBlockTokens * 4);
+        for (int mi = 0; mi < KS; ++mi) {
+            float large[4] = {}, small[4] = {};
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const float* at = v + (kk >> 1) * (TILE / 4) + mi * (4 * kBlockTokens * 4) + (kk & 1) * 32;
                 const float a[4] = {at[0], at[2 * kBlockTokens * 4], at[16], at[2 * kBlockTokens * 4 + 16]};
-                mma_split(o[mi], a, b0, b1);
+                mma_split(large, small, a, p0[kk], p1[kk]);
             }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[mi][x] += large[x] + small[x];
         }
     }
     __device__ __forceinline__ void reset() {}

@@ -532,6 +532,70 @@ def test_captured_step_follows_its_inputs():
     assert int(m.err) == 0
 
 
+def test_bindings_take_the_same_calls_both_ways(monkeypatch):
+    # the compiled way and the Python one: the same results, the same refusals
+    from paged_kv_cache_207_gb300 import _native
+    pk.lib()
+    assert _native._quick is not None
+    m = Model("bf16", (8, 2, 128), 40, 3, 2, 100, seed=5)
+    q, k, v = (torch.randn(50, h, 128, generator=m.g).to(torch.bfloat16).cuda() for h in (8, 2, 2))
+    starts, cu, lens, err = i32([0, 5]), cu_of([30, 20]), i32([30, 25]), err_flag()
+    dq = torch.randn(2, 8, 128, generator=m.g).to(torch.bfloat16).cuda()
+
+    def calls(**more):
+        kp, vp, out, att, dec = m.kp.clone(), m.vp.clone(), nan_like(q), nan_like(q), nan_like(dq)
+        pk.rope_append_kv(kp, vp, out, q, k, v, m.freq, m.tables, starts, cu, True, err, **more)
+        pk.prefill_attention_window(att, out, kp, vp, m.tables, starts, cu, 0.1, 30, 2**40, 3, err, **more)
+        pk.decode_attention_window(dec, dq, kp, vp, m.tables, lens, 1, 12, err_flag=err, **more)
+        return kp, vp, out, att, dec
+
+    quick = calls()
+    for a, b in zip(quick, calls(stream=torch.cuda.current_stream())):     # an explicit stream: the Python way
+        assert torch.equal(a, b)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        got = calls()
+    other.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(quick, got))
+    fp8, f32 = pool_for("fp8", 4, 2, 128), pool_for("f32", 4, 2, 128)
+
+    def refused():
+        bad = [
+            (TypeError, lambda: pk.decode_attention_window(dq.float(), dq, m.kp, m.vp, m.tables, lens, 0.1, 4)),
+            (TypeError, lambda: pk.decode_attention_window(dq, dq, m.kp, m.vp, m.tables.long(), lens, 0.1, 4)),
+            (ValueError, lambda: pk.decode_attention_window(dq, dq, m.kp, m.vp, m.tables, lens[:1], 0.1, 4)),
+            (ValueError, lambda: pk.decode_attention_window(dq, dq, m.kp, m.vp[:3], m.tables, lens, 0.1, 4)),
+            (ValueError, lambda: pk.decode_attention_window(dq.cpu(), dq, m.kp, m.vp, m.tables, lens, 0.1, 4)),
+            (ValueError, lambda: pk.decode_attention_window(dq, q[::25], m.kp, m.vp, m.tables, lens, 0.1, 4)),
+            (TypeError, lambda: pk.decode_attention_window(dq, dq, f32, f32, m.tables, lens, 0.1, 4)),
+            (pk.PagedKVError, lambda: pk.decode_attention_window(dq, dq, m.kp, m.vp, m.tables, lens, 0.1, 0)),
+            (pk.PagedKVError, lambda: pk.decode_attention_window(dq, dq, m.kp, m.vp, m.tables, lens, float("nan"), 4)),
+            (ValueError, lambda: pk.decode_attention_window_fp8(dq, dq, m.kp, m.vp, m.tables, lens, 0.1, 4)),
+            (ValueError, lambda: pk.rope_append_kv(m.kp, m.vp, None, q, k, v, m.freq, m.tables, starts, cu)),
+            (TypeError, lambda: pk.rope_append_kv(m.kp, m.vp, q, q, k, v, m.freq.float(), m.tables, starts, cu)),
+            (ValueError, lambda: pk.rope_append_kv(m.kp, m.vp, q, q, k, v[:49], m.freq, m.tables, starts, cu)),
+            (ValueError, lambda: pk.rope_append_kv(m.kp, m.vp, q, q, k.transpose(1, 2).contiguous().transpose(1, 2), v, m.freq,
+                                                   m.tables, starts, cu)),
+            (pk.PagedKVError, lambda: pk.rope_append_kv(m.kp, m.vp, q, q, k, v, m.freq[:12], m.tables, starts, cu)),
+            (TypeError, lambda: pk.rope_append_kv_fp8(fp8, fp8, q.float(), q, k, v, m.freq, m.tables, starts, cu)),
+            (TypeError, lambda: pk.rope_append_kv(m.kp, m.vp, q, q, k, None, m.freq, m.tables, starts, cu)),
+            (pk.PagedKVError, lambda: pk.prefill_attention_window(q.float(), q.float(), f32, f32, m.tables, starts, cu, 0.1, 30, 4)),
+            (ValueError, lambda: pk.prefill_attention_window(q, q, m.kp, m.vp, m.tables, starts, cu[:2], 0.1, 30, 4)),
+        ]
+        for n, (kind, call) in enumerate(bad):
+            with pytest.raises(kind):
+                call()
+
+    refused()
+    monkeypatch.setattr(_native, "_quick", None)
+    for a, b in zip(quick, calls()):
+        assert torch.equal(a, b)
+    refused()
+    torch.cuda.synchronize()
+    assert int(err) == 0
+
+
 def test_offsets_past_32_bits():
     # pools of over 4 GiB each; the blocks in use are the last ones
     heads, blocks = (8, 8, 128), 140000
