@@ -273,6 +273,9 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 //   take P_b = p 2^(e_b(t) - 127) c_b with c_b = 2^(135 - R_b), R_b at least the largest scale
 //   code of block b so far (raised, and the block's accumulators rescaled, when a pair brings
 //   a larger one), so that P_b stays at most 2^8, in f16's range.
+// The bound is the integer pipe (conversions, selections, packing: half the rate of FMAs), so
+// scale codes are read as bytes (their fp32 is one multiply away, on the other pipe), and lane
+// c watches the codes of block c alone for a raise.
 template <int D>
 struct Fp4Cache {
     using Out = __nv_bfloat16;
@@ -282,7 +285,7 @@ struct Fp4Cache {
     static constexpr int NB = D / 32;                         // scale blocks of a row
     uint32_t qb[KS][2];
     float cb[NB];
-    uint32_t ref_packed;                                      // the R_b, a byte each
+    int ref;                                                  // R_b of b = c % NB
     int lane, r, c;
     __device__ __forceinline__ Fp4Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {
         reset();
@@ -290,7 +293,7 @@ struct Fp4Cache {
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int b = 0; b < NB; ++b) cb[b] = exp2i(127);
-        ref_packed = 0;
+        ref = 0;
     }
     __device__ __forceinline__ int lo() const { return r; }
     __device__ __forceinline__ int hi() const { return r + 8; }
@@ -303,10 +306,6 @@ struct Fp4Cache {
             qb[kk][0] = pack_f16x2(bf16_lo_to_f32(u0), bf16_hi_to_f32(u0));
             qb[kk][1] = pack_f16x2(bf16_lo_to_f32(u1), bf16_hi_to_f32(u1));
         }
-    }
-    static __device__ __forceinline__ uint32_t scale_bytes(const uint8_t* at) {
-        if constexpr (NB == 4) return *reinterpret_cast<const uint32_t*>(at);
-        else return *reinterpret_cast<const uint16_t*>(at);
     }
     // N adjacent 32-bit words
     template <int N>
@@ -322,15 +321,10 @@ struct Fp4Cache {
             w[0] = v.x; w[1] = v.y;
         }
     }
-    // scale byte b of w: 2^(code - 127) (the code is the exponent field; code 0 gives 0)
-    static __device__ __forceinline__ float scale_value(uint32_t w, int b) {
-        const int left = 23 - 8 * b;                          // (a constant where this is inlined)
-        return __uint_as_float((left >= 0 ? w << left : w >> -left) & 0x7f800000u);
-    }
-    // log2 of a block's c_b, from its R_b: 135 - R_b, at most 127
-    static __device__ __forceinline__ int c_exp(uint32_t refs, int b) {
-        return min(135 - (int)((refs >> (8 * b)) & 0xffu), 127);
-    }
+    // 2^(code - 127): the code is the exponent field (code 0 gives 0)
+    static __device__ __forceinline__ float scale_value(uint8_t code) { return __uint_as_float((uint32_t)code * 0x800000u); }
+    // log2 of a block's c_b, from its R_b: at most 127
+    static __device__ __forceinline__ int c_exp(int R) { return min(135 - R, 127); }
     __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -338,7 +332,8 @@ struct Fp4Cache {
             uint32_t k0[NB], k1[NB];
             words<NB>(k + r * (D / 2) + c * (D / 8), k0);
             words<NB>(k + (r + 8) * (D / 2) + c * (D / 8), k1);
-            const uint32_t e0 = scale_bytes(k + 8 * D + r * NB), e1 = scale_bytes(k + 8 * D + (r + 8) * NB);
+            const uint8_t* e0 = k + 8 * D + r * NB;
+            const uint8_t* e1 = e0 + 8 * NB;
             s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -348,7 +343,7 @@ struct Fp4Cache {
                 float acc[4];
                 mma_f16_zero(acc, a[0], a8[0], a[1], a8[1], qb[2 * b][0], qb[2 * b][1]);
                 mma_f16_16816(acc, a[2], a8[2], a[3], a8[3], qb[2 * b + 1][0], qb[2 * b + 1][1]);
-                const float f0 = scale_value(e0, b), f1 = scale_value(e1, b);
+                const float f0 = scale_value(e0[b]), f1 = scale_value(e1[b]);
                 s[t][0] = fmaf(acc[0], f0, s[t][0]);
                 s[t][1] = fmaf(acc[1], f0, s[t][1]);
                 s[t][2] = fmaf(acc[2], f1, s[t][2]);
@@ -368,23 +363,20 @@ struct Fp4Cache {
                                        float (&o)[KS][4]) {
         run.l0 = run.l0 * run.al0 + ((pr[0][0] + pr[0][2]) + (pr[1][0] + pr[1][2]));
         run.l1 = run.l1 * run.al1 + ((pr[0][1] + pr[0][3]) + (pr[1][1] + pr[1][3]));
-        uint32_t e0[2], e1[2], top = 0u;
+        const uint8_t* sc = vt + 8 * D + r * NB;              // scale codes of token r, then r + 8
+        int top = 0;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint8_t* sc = vt + t * TILE + 8 * D;
-            e0[t] = scale_bytes(sc + r * NB);
-            e1[t] = scale_bytes(sc + (r + 8) * NB);
-            top = __vmaxu4(top, __vmaxu4(e0[t], e1[t]));
-        }
+        for (int t = 0; t < 2; ++t)
+            top = max(top, max((int)sc[t * TILE + c % NB], (int)sc[t * TILE + 8 * NB + c % NB]));
+        if (__any_sync(0xffffffffu, top > ref)) {             // rare after a part's first pair
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top = __vmaxu4(top, __shfl_xor_sync(0xffffffffu, top, x));
-        if (__vmaxu4(top, ref_packed) != ref_packed) {        // warp-uniform, rare after a part's first pair
+            for (int x = 4; x < 32; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
             // (three octaves above the largest seen, so that the next ones hardly raise it again)
-            const uint32_t raised = __vmaxu4(__vaddus4(top, 0x03030303u), ref_packed);
+            const int raised = top > ref ? min(top + 3, 255) : ref;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int en = c_exp(raised, b);
-                const float f = exp2i(en - c_exp(ref_packed, b));                  // exact
+                const int en = c_exp(__shfl_sync(0xffffffffu, raised, b)), eo = c_exp(__shfl_sync(0xffffffffu, ref, b));
+                const float f = exp2i(en - eo);               // exact
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     o[2 * b][x] *= f;
@@ -392,7 +384,7 @@ struct Fp4Cache {
                 }
                 cb[b] = exp2i(en);
             }
-            ref_packed = raised;
+            ref = raised;
         }
         if (run.rescale) rescale_rows(run, o);
 #pragma unroll
@@ -401,7 +393,7 @@ struct Fp4Cache {
             words<KS>(vt + t * TILE + (r * 4 + c) * (KS * 4), vw);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float g0 = scale_value(e0[t], b) * cb[b], g1 = scale_value(e1[t], b) * cb[b];
+                const float g0 = scale_value(sc[t * TILE + b]) * cb[b], g1 = scale_value(sc[t * TILE + 8 * NB + b]) * cb[b];
                 const uint32_t pb0 = movmatrix_trans(pack_f16x2(pr[t][0] * g0, pr[t][1] * g0));
                 const uint32_t pb1 = movmatrix_trans(pack_f16x2(pr[t][2] * g1, pr[t][3] * g1));
 #pragma unroll
@@ -416,7 +408,7 @@ struct Fp4Cache {
     __device__ __forceinline__ void finish(Running&, float (&o)[KS][4]) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const float f = exp2i(-c_exp(ref_packed, b));
+            const float f = exp2i(-c_exp(__shfl_sync(0xffffffffu, ref, b)));
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 o[2 * b][x] *= f;
@@ -434,16 +426,12 @@ struct Fp4Cache {
 // (the outputs' relative error: 2.5e-7 to 3.5e-7; with one long sum 8e-7).
 // K and V fragments are plain 32-bit reads of the tiles (K's are free of bank conflicts, V's
 // two-way); the probabilities pass through shared memory to reach the B operand's order.
-__device__ __forceinline__ uint32_t tf32_of(float x) {
-    uint32_t y;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
-    return y;
-}
 struct Split { uint32_t h, l; };
 __device__ __forceinline__ Split split_tf32(float x) {
+    // (integer operations: the conversion instruction runs at a fraction of their rate)
     Split s;
-    s.h = tf32_of(x);
-    s.l = tf32_of(x - __uint_as_float(s.h));
+    s.h = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    s.l = __float_as_uint(x - __uint_as_float(s.h)) & 0xffffe000u;
     return s;
 }
 __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
