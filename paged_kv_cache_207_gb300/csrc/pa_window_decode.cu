@@ -35,14 +35,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 4;
 // Blocks of a part, at least.  A part's end costs a warp about as much as two blocks (FP4:
 // four, with its scale references to set again), so longer parts are cheaper where one CTA
-// goes through all of them and shorter ones faster where each has its own CTA.  On GB300, 32
-// against 64 blocks at 32 / 8 heads of 128: bf16, one sequence, window 4096: 9.9 / 12.4 us;
-// FP4, 128 sequences, window 2047: 97.5 / 91.0 us.
-constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 64 : 32; }
-// (sequence, kv head) pairs below which each part gets a CTA of its own.  At 32 / 8 heads of
-// 128, bf16, window 4096, a CTA per part against one for all: 9.9 / 40.1 us for one sequence,
-// 16.9 / 41.0 for 4, but 55.5 / 46.7 for 16 and 692 / 581 for 256 (a cluster's CTAs start
-// together and wait for one another); with window 2048 and 8 sequences 16.0 / 22.9.
+// goes through all of them and shorter ones faster where each has its own CTA.  On GB300, heads
+// 32 / 8 of 128: bf16, one sequence, window 4096, parts of at least 16 / 32 / 64 blocks: 9.9 /
+// 11.2 / 12.4 us (four sequences 18.0 / 17.6 / 16.0); FP4, 128 sequences, window 2047, 32 / 64
+// blocks: 97.5 / 91.0 us; f32, one sequence, 16 / 32 blocks: 16.6 / 21.6 us.
+constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 64 : t == PA_F32 ? 16 : 32; }
+// (sequence, kv head) pairs below which each part gets a CTA of its own.  bf16, window 4096, a
+// CTA per part against one for all: 9.9 / 40.1 us for one sequence, 16.9 / 41.0 for 4, but 55.5
+// / 46.7 for 16 and 692 / 581 for 256 (a cluster's CTAs start together and wait for one
+// another); with window 2048 and 8 sequences 16.0 / 22.9.
 constexpr int kSplitBelow = 65;
 
 struct WParams {
