@@ -491,7 +491,8 @@ pa_status pa_decode_attention_window(void* out, const void* q, const void* k_poo
  * j < num_sinks, i.e. it equals pa_decode_attention_window of that query with context
  * length p + 1.  Only the blocks of the sinks and of the chunk's windows are read.
  * A chunk outside rows 0 .. total_q sets PA_DEV_ERR_BAD_CU and is skipped; rows of a
- * chunk past max_chunk set PA_DEV_ERR_HINT and are not computed.  A value that is not
+ * chunk past max_chunk set PA_DEV_ERR_HINT and are not computed; rows of q and out past
+ * cu_q[num_seqs] (a padded batch) are neither read nor written.  A value that is not
  * finite reaches, besides the rows that see it, at most rows of the same chunk near them
  * (within 256 tokens), never rows when it is hidden from the whole chunk.
  */

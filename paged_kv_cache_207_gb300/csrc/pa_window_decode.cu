@@ -869,6 +869,7 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
                     if (vis[b] != 0xffffu) cache.hide(kt + (2 + b) * TILE, vis[b]);
+                fence_proxy_async_smem();      // (before the stage's next copy)
                 __syncwarp();
             }
             cache.pv(kt + 2 * TILE, pr, run, o);
@@ -970,7 +971,15 @@ cudaError_t launch(const WParams& p, int parts, int num_seqs, int threads, int s
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, Kernel, p);
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, Kernel, p);
+    if (launched == cudaSuccess || ctas == 1) return launched;
+    // a GPU (or a part of one) without room for the cluster: one CTA for all parts, the same result
+    cudaGetLastError();
+    WParams whole = p;
+    whole.split = 0;
+    cfg.gridDim.x = 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, Kernel, whole);
 }
 
 template <template <int> class Cache, int D, int NST>

@@ -72,6 +72,50 @@ def test_decode_over_many_partitions(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("heads", [(8, 1, 128), (8, 8, 64)])
+def test_decode_over_the_most_partitions(cache, heads):
+    # a window that takes the largest cluster, in one and in many CTAs (the same bits)
+    n, window = 12500, 12000
+    c = Cache(cache, [n], heads, seed=12)
+    q = c.queries(1)
+    alone = run_decode(c, [n], q, window, 20, 0.1)
+    check_decode(c, [n], q, window, 20, 0.1, alone)
+    many = 80
+    out = nan_like(q.repeat(many, 1, 1).cuda())
+    decode_call(cache)(out, q.repeat(many, 1, 1).cuda(), c.kp, c.vp, c.tables.repeat(many, 1).cuda(), i32([n] * many), 0.1,
+                       window, 20)
+    assert bool((out == alone).all())
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_decode_on_two_streams_and_in_two_graphs_at_once(cache):
+    lens = [1500, 700]
+    c = Cache(cache, lens, (8, 2, 128), seed=13)
+    q, other = c.queries(2), c.queries(2)
+    want = [run_decode(c, lens, x, 1024, 4, 0.1) for x in (q, other)]
+    args = (c.kp, c.vp, c.tables.cuda(), i32(lens), 0.1, 1024, 4)
+    outs, qs = [nan_like(w) for w in want], [q.cuda(), other.cuda()]
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for x, o, s in zip(qs, outs, streams):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                decode_call(cache)(o, x, *args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    for x, o, g in zip(qs, outs, graphs):
+        o.fill_(float("nan"))
+        with torch.cuda.graph(g):
+            decode_call(cache)(o, x, *args)
+    for _ in range(10):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("cache", CACHES)
 def test_decode_batched_equals_alone_and_repeats(cache):
     lens = [700, 5, 1300, 64, 0, 2000]
     c = Cache(cache, lens, (14, 2, 64), seed=5)
@@ -392,6 +436,18 @@ def test_prefill_rows_agree_with_decode():
         within(out[row:row + 1], want, tol)
 
 
+def test_prefill_leaves_the_rows_of_a_padded_batch():
+    starts, counts = [10, 0], [40, 25]
+    c = Cache("bf16", [50, 25], (8, 2, 128), seed=5)
+    q = c.queries(65)
+    good, err = run_prefill(c, starts, counts, q, 30, 4, 0.1), err_flag()
+    padded = torch.full((100, 8, 128), float("nan")).to(torch.bfloat16)
+    padded[:65] = q
+    c.tables = torch.cat((c.tables, torch.full_like(c.tables, -1)))
+    out = run_prefill(c, starts + [7, 9], counts, padded, 30, 4, 0.1, err, max_chunk=100, cu=i32([0, 40, 65, 65, 65]))
+    assert int(err) == 0 and torch.equal(out[:65], good) and bool(out[65:].isnan().all())
+
+
 def test_prefill_flags_bad_data():
     starts, counts = [10, 20, 30], [40, 40, 40]
     c = Cache("bf16", [50, 60, 70], (8, 2, 128), seed=6)
@@ -485,11 +541,12 @@ def test_serving_run_in_chunks_and_tokens(cache):
     assert int(m.err) == 0
 
 
-def test_captured_step_follows_its_inputs():
+@pytest.mark.parametrize("window,first", [(40, [70, 5, 33, 50]), (1100, [1300, 5, 900, 1500])])
+def test_captured_step_follows_its_inputs(window, first):
     # one graph of append + attention, replayed as lengths grow; beside it the same on a
     # side stream without a graph
-    m = Model("bf16", (8, 2, 128), 40, 3, 4, 300, seed=2)
-    m.step([70, 5, 33, 50])
+    m = Model("bf16", (8, 2, 128), window, 3, 4, max(first) + 40, seed=2)
+    m.step(first)
     n, rows = 4, [torch.zeros(4, h, 128, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2)]
     starts, lens, cu = i32([0] * n), i32([0] * n), cu_of([1] * n)
     q, out = torch.empty_like(rows[0]), torch.empty_like(rows[0])
