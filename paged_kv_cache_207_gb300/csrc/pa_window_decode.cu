@@ -32,7 +32,13 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 200000000ull;   // 200 ms: a real tile copy takes microseconds
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 4;
+// Warps of a CTA.  At head_dim 64 a block is half the work and eight warps keep a CTA as short
+// as four at 128 (128 sequences of 14 / 2 heads, window 2048, eight against four: bf16 24.0 /
+// 25.5 us, FP8 18.6 / 24.8, FP4 18.8 / 25.5; one sequence, window 512: 5.5 / 7.2); f32 tiles
+// leave room for one such CTA on an SM (16 sequences of 12 heads 12.1 / 9.0 us).  At 128, eight
+// are better for FP8 with 16 or 256 sequences (window 4096: 29.8 / 45.1, 325 / 338 us) and worse
+// with 64 (window 1024: 29.2 / 25.2), where the CTAs no longer fit the SMs at once; FP4 alike.
+constexpr int warps_for(pa_dtype t, int head_dim) { return head_dim == 64 && t != PA_F32 ? 8 : 4; }
 // Blocks of a part, at least.  A part's end costs a warp about as much as two blocks (FP4:
 // four, with its scale references to set again), so longer parts are cheaper where one CTA
 // goes through all of them and shorter ones faster where each has its own CTA.  On GB300, heads
@@ -43,8 +49,10 @@ constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 64 : t == PA_F32 
 // (sequence, kv head) pairs below which each part gets a CTA of its own.  bf16, window 4096, a
 // CTA per part against one for all: 9.9 / 40.1 us for one sequence, 16.9 / 41.0 for 4, but 55.5
 // / 46.7 for 16 and 692 / 581 for 256 (a cluster's CTAs start together and wait for one
-// another); with window 2048 and 8 sequences 16.0 / 22.9.
-constexpr int kSplitBelow = 65;
+// another); with window 2048 and 8 sequences 16.0 / 22.9.  FP8 and FP4 tiles bind an SM's
+// instruction slots sooner, so that it pays up to one pair for each of 152 SMs: 16 sequences
+// 36.0 / 45.2 us and 27.5 / 47.9, 19 sequences 38.6 / 45.7 and 39.7 / 47.8.
+constexpr int split_below(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_FP4_E2M1 ? 153 : 65; }
 
 struct WParams {
     void* out;
@@ -83,6 +91,7 @@ __device__ __forceinline__ void rescale_rows(const Running& run, float (&o)[KS][
 
 template <int D>
 struct Bf16Cache {
+    static constexpr pa_dtype TYPE = PA_BF16;
     using Out = __nv_bfloat16;
     static constexpr int TILE = kBlockTokens * D * 2;         // bytes of a (block, kv head) tile
     static constexpr int KS = D / 16;
@@ -161,6 +170,7 @@ struct Bf16Cache {
 //   to keep the product in f16's normal range (taken out of the sums at the end).
 template <int D>
 struct Fp8Cache {
+    static constexpr pa_dtype TYPE = PA_FP8_E4M3;
     using Out = __nv_bfloat16;
     static constexpr int TILE = 16 * D + 64;
     static constexpr int KS = D / 16;
@@ -279,6 +289,7 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 // c watches the codes of block c alone for a raise.
 template <int D>
 struct Fp4Cache {
+    static constexpr pa_dtype TYPE = PA_FP4_E2M1;
     using Out = __nv_bfloat16;
     static constexpr int TILE = 8 * D + D / 2;
     static constexpr int KS = D / 16;
@@ -455,6 +466,7 @@ __device__ __forceinline__ void mma_split(float (&large)[4], float (&small)[4], 
 
 template <int D>
 struct F32Cache {
+    static constexpr pa_dtype TYPE = PA_F32;
     using Out = float;
     static constexpr int TILE = kBlockTokens * D * 4;
     static constexpr int KS = D / 16;
@@ -984,7 +996,7 @@ cudaError_t launch(const WParams& p, int parts, int num_seqs, int threads, int s
 
 template <template <int> class Cache, int D, int NST>
 cudaError_t launch_cache(const WParams& p, int parts, int num_seqs, cudaStream_t stream) {
-    constexpr int NW = kWarps;
+    constexpr int NW = warps_for(Cache<D>::TYPE, D);
     return launch<window_decode_kernel<Cache, D, NW, NST>>(p, parts, num_seqs, NW * 32, Layout<Cache<D>, D, NW, NST>::bytes(p.G),
                                                            Layout<Cache<D>, D, NW, NST>::bytes(8), stream);
 }
@@ -1024,12 +1036,12 @@ cudaError_t launch_window_decode(const WindowArgs& a, cudaStream_t stream) {
                   ((long long)a.sinks + kBlockTokens - 1) / kBlockTokens;
     if (n > a.max_blocks) n = a.max_blocks;
     // at most 16 parts (the largest cluster), whole pairs for every warp
-    constexpr int kUnit = 2 * kWarps;
+    const int unit = 2 * warps_for(a.dtype, a.head_dim);
     const int blocks = (int)n, least = min_part(a.dtype);
     const int most = blocks > 16 * least ? 16 : blocks < least ? 1 : blocks / least;
-    p.part_len = ((blocks + most - 1) / most + kUnit - 1) / kUnit * kUnit;
+    p.part_len = ((blocks + most - 1) / most + unit - 1) / unit * unit;
     const int parts = (blocks + p.part_len - 1) / p.part_len;
-    p.split = parts > 1 && (long long)a.num_kv_heads * a.num_seqs < kSplitBelow;
+    p.split = parts > 1 && (long long)a.num_kv_heads * a.num_seqs < split_below(a.dtype);
     p.scale_log2 = a.scale * kLog2e;
     return a.head_dim == 64 ? launch_type<64>(p, parts, a.dtype, a.num_seqs, stream)
                             : launch_type<128>(p, parts, a.dtype, a.num_seqs, stream);
