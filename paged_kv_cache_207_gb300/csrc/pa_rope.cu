@@ -334,8 +334,16 @@ __device__ __forceinline__ int tile_base(const RParams& p, int s) {
 // (flagged).  The block is checked by the caller, when its load has had time to land.
 __device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
     const int tid = threadIdx.x;
-    // last s in [lo, lo + n) with tile_base(s) <= t: 256 probes narrow it 256 times
-    int lo = 0, n = p.S;
+    // the sequence if all have as many rows, and its place with it: often right, one round trip
+    int lo = min(t / (p.total / (kTileRows * p.S) + 2), p.S - 1), n = 1;
+    int first = __ldg(p.cu + lo), next = __ldg(p.cu + lo + 1);
+    long long start = __ldg(p.start_pos + lo);
+    if (t < (first >> 4) + 2 * lo || (lo + 1 < p.S && t >= (next >> 4) + 2 * (lo + 1))) {
+        lo = 0;
+        n = p.S;
+    }
+    const bool guessed = n == 1;
+    // else the last s in [lo, lo + n) with tile_base(s) <= t: 256 probes narrow it 256 times
     while (n > 1) {
         const int step = (n + kThreads - 1) / kThreads;
         const int s = lo + tid * step;
@@ -344,13 +352,16 @@ __device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
         lo += k * step;
         n = min(step, n - k * step);
     }
-    const int first = __ldg(p.cu + lo), next = __ldg(p.cu + lo + 1);
+    if (!guessed) {
+        first = __ldg(p.cu + lo);
+        next = __ldg(p.cu + lo + 1);
+        start = __ldg(p.start_pos + lo);
+    }
     const bool report = tid == 0 && blockIdx.y == 0;
     if (first < 0 || next > p.total || next < first) {
         if (report) raise_flag(p.err, PA_DEV_ERR_BAD_CU);
         return false;
     }
-    const long long start = __ldg(p.start_pos + lo);
     const long long from = start >> 4;                              // block of the first row
     const long long b = from + (t - ((first >> 4) + 2 * lo));
     const long long begin = max(start, b * kTileRows), end = min(start + (next - first), (b + 1) * kTileRows);
