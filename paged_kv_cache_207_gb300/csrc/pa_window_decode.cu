@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include "pa_ptx.cuh"
@@ -32,27 +33,40 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 200000000ull;   // 200 ms: a real tile copy takes microseconds
 constexpr float kLog2e = 1.4426950408889634f;
+// Times below are of one call on GB300, inputs in L2 or not as they come in turn.  "A": 32 / 8
+// heads of 128, "B": 14 / 2 heads of 64.
+//
 // Warps of a CTA.  At head_dim 64 a block is half the work and eight warps keep a CTA as short
-// as four at 128 (128 sequences of 14 / 2 heads, window 2048, eight against four: bf16 24.0 /
-// 25.5 us, FP8 18.6 / 24.8, FP4 18.8 / 25.5; one sequence, window 512: 5.5 / 7.2); f32 tiles
-// leave room for one such CTA on an SM (16 sequences of 12 heads 12.1 / 9.0 us).  At 128, eight
-// are better for FP8 with 16 or 256 sequences (window 4096: 29.8 / 45.1, 325 / 338 us) and worse
-// with 64 (window 1024: 29.2 / 25.2), where the CTAs no longer fit the SMs at once; FP4 alike.
+// as four at 128 (B, window 2048, 128 sequences, eight against four: bf16 23.8 / 25.6 us, FP8
+// 19.9 / 25.3, FP4 20.0 / 23.0; one sequence, window 512: 5.3 / 6.7).  At 128, eight win with
+// many blocks for each and many CTAs (A, window 4096: FP8, 256 sequences, 321 / 336; bf16, 16
+// sequences, 41.6 / 45.6) and lose elsewhere (window 1024: one sequence 8.8 / 7.2, 32 of them
+// 26.1 / 23.3; FP4, window 2047, 128 sequences, 90.5 / 81.0).
 constexpr int warps_for(pa_dtype t, int head_dim) { return head_dim == 64 && t != PA_F32 ? 8 : 4; }
-// Blocks of a part, at least.  A part's end costs a warp about as much as two blocks (FP4:
-// four, with its scale references to set again), so longer parts are cheaper where one CTA
-// goes through all of them and shorter ones faster where each has its own CTA.  On GB300, heads
-// 32 / 8 of 128: bf16, one sequence, window 4096, parts of at least 16 / 32 / 64 blocks: 9.9 /
-// 11.2 / 12.4 us (four sequences 18.0 / 17.6 / 16.0); FP4, 128 sequences, window 2047, 32 / 64
-// blocks: 97.5 / 91.0 us; f32, one sequence, 16 / 32 blocks: 16.6 / 21.6 us.
-constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 64 : t == PA_F32 ? 16 : 32; }
-// (sequence, kv head) pairs below which each part gets a CTA of its own.  bf16, window 4096, a
-// CTA per part against one for all: 9.9 / 40.1 us for one sequence, 16.9 / 41.0 for 4, but 55.5
-// / 46.7 for 16 and 692 / 581 for 256 (a cluster's CTAs start together and wait for one
-// another); with window 2048 and 8 sequences 16.0 / 22.9.  FP8 and FP4 tiles bind an SM's
-// instruction slots sooner, so that it pays up to one pair for each of 152 SMs: 16 sequences
-// 36.0 / 45.2 us and 27.5 / 47.9, 19 sequences 38.6 / 45.7 and 39.7 / 47.8.
-constexpr int split_below(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_FP4_E2M1 ? 153 : 65; }
+// CTAs that an SM is to hold, which bounds the registers: as many as shared memory allows for
+// bf16 and f32 (A, f32, window 4096, 12 sequences: 90.6 us with 251 registers, one CTA,
+// against 116 with 168), four of FP8 and FP4, whose conversions want the warps more than the
+// registers (four against three: a mixed FP8 batch of 96 sequences 25.3 / 30.0 us, FP4 with 128
+// sequences 81.7 / 91.6).
+constexpr int ctas_for(pa_dtype t, int head_dim) {
+    return t == PA_F32 ? (head_dim == 64 ? 3 : 1) : head_dim == 64 ? 2 : t == PA_BF16 ? 3 : 4;
+}
+// Blocks of a part, at least.  A part's end costs a warp about as much as a block or two (FP4:
+// two to four, with its scale references to set again), so longer parts are cheaper where one
+// CTA goes through all of them and shorter ones faster where CTAs share them (16 / 32 blocks, A,
+// window 1024, one sequence: bf16 7.2 / 10.7 us, FP8 8.0 / 11.5, f32 12.0 / 17.7; 64 sequences,
+// FP8: 25.4 / 24.7.  FP4, 32 / 64 blocks: window 2048, one sequence, 11.4 / 17.6, 128 of them
+// 81.0 / 77.1).
+constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 32 : 16; }
+// Pairs of blocks for each warp below which a sequence is one part, since joining parts costs
+// about 1.3 us (6 against 4, A, window 512, one sequence: bf16 7.5 / 8.4 us, FP8 8.4 / 9.1, but
+// f32 14.6 / 13.0).
+constexpr int min_pairs(pa_dtype t) { return t == PA_F32 ? 4 : 6; }
+// Parts, at most.  Clusters of up to 8 find room in every part of the GPU; 16 pay only where an
+// SM holds three CTAs that are long (16 against 8: f32, 12 heads of 64, window 4096, one
+// sequence 14.2 / 15.6 us; A, window 4096, 8 sequences: bf16 27.8 / 25.5, f32 54.5 / 50.5;
+// FP8, 16 sequences, 38.4 / 29.1).
+constexpr int most_parts(pa_dtype t, int head_dim) { return t == PA_F32 && head_dim == 64 ? 16 : 8; }
 
 struct WParams {
     void* out;
@@ -64,8 +78,8 @@ struct WParams {
     int32_t* err;
     int Hq, Hkv, G, max_blocks, num_blocks;
     int window, sinks;
-    int part_len;            // listed blocks of a part
-    int split;               // a CTA per part, in clusters; else a CTA goes through all parts
+    int parts, part_len;     // at most so many, of so many listed blocks (the last takes what is left too)
+    int per;                 // parts of a cluster's CTA, each kept by itself; 0: a CTA alone folds all parts
     float scale_log2;
 };
 
@@ -545,16 +559,20 @@ struct F32Cache {
 };
 
 // Shared memory: the warps' stages, each the K tiles then the V tiles of a pair of blocks;
-// the warps' scratch; the barriers, two per stage; and the warps' folded results: G rows of
-// D + 4 floats, then their maxima and sums.
+// the warps' scratch; the barriers, two per stage; and the warps' folded results.  A result is
+// the outputs as the lanes hold them (per pair of heads, 16 dims and r: a float4, dims r and
+// r + 8 of one head, then of the other; CS floats for a pair of heads, no two lanes in the same banks), then the
+// heads' maxima and sums.
 template <class C, int D, int NW, int NST>
 struct Layout {
-    static constexpr int OS = D + 4;
     static constexpr int STAGE = 4 * C::TILE;
     static constexpr int WARP = NW * NST * STAGE;
     static constexpr int BAR = WARP + NW * C::SCRATCH;
     static constexpr int OUT = BAR + (NW * NST * 16 + 15) / 16 * 16;
-    static constexpr int bytes(int G) { return OUT + NW * G * (OS + 2) * 4; }
+    static constexpr int CS = 2 * D + 8;
+    static __host__ __device__ constexpr int outs(int G) { return CS * ((G + 1) / 2); }         // floats of a warp
+    static __host__ __device__ constexpr int result(int G) { return NW * (outs(G) + 2 * G); }   // and of all
+    static constexpr int bytes(int G, int results) { return OUT + results * result(G) * 4; }
 };
 
 // The listed blocks of one sequence as one warp walks them: entry e is block e % 2 of its pair
@@ -619,11 +637,12 @@ __device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
     return x;
 }
 
-// Parts.  The listed blocks are cut into parts of p.part_len, and in every part warp w takes
-// the same blocks whatever CTA it belongs to.  A (warp, part) has its own maximum, sum and
-// outputs; a warp's parts are folded into one in their order, and the warps merged in theirs.
-// So the result is the same, bit for bit, whether one CTA goes through all parts (many
-// sequences: no joining at all) or a cluster has a CTA per part (few: every SM gets work).
+// Parts.  The listed blocks are cut into parts of p.part_len (the last takes what is left), and
+// in every part warp w takes the same blocks whatever CTA it belongs to.  A (warp, part) has
+// its own maximum, sum and outputs; a warp's parts are folded into one in their order, and the
+// warps merged in theirs.  So the result is the same, bit for bit, whether one CTA goes through
+// all parts (many sequences: no joining at all) or a cluster of CTAs has p.per parts each (few:
+// every SM gets work), and a sequence's result does not depend on the batch.
 struct Partial { float m, l, o; };         // of one head and dim; a part without keys: -inf, 0, 0
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.f : m; }
 // The joint maximum of two parts and what their sums are scaled by.
@@ -639,26 +658,29 @@ __device__ __forceinline__ void fold(Partial& a, const Partial& s) {
     a = Partial{f.m, fold_add(f, a.l, s.l), fold_add(f, a.o, s.o)};
 }
 
-// The output from the warps' results: of warp w, head g and dim d, get(w).
-template <int NW, typename Get>
-__device__ __forceinline__ float merge_warps(Get get) {
-    Partial x[NW];
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        x[w] = get(w);
-        M = (x[w].m > M || x[w].m != x[w].m) ? x[w].m : M;
+// The warps' results of one head as one: their maxima and sums first, then each output.
+template <int NW>
+struct Merge {
+    float m[NW], l[NW], sum;          // m: after weigh(), the warps' weights
+    __device__ __forceinline__ void set(int w, float m_, float l_) {
+        m[w] = m_;
+        l[w] = l_;
     }
-    const float z = safe_max(M);
-    float acc = 0.f, l = 0.f;
+    __device__ __forceinline__ void weigh() {
+        float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        const float wt = fast_exp2(x[w].m - z);
-        acc = __fmaf_rn(x[w].o, wt, acc);
-        l = __fmaf_rn(x[w].l, wt, l);
+        for (int w = 0; w < NW; ++w) M = (m[w] > M || m[w] != m[w]) ? m[w] : M;
+        const float z = safe_max(M);
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            m[w] = fast_exp2(m[w] - z);
+            sum = __fmaf_rn(l[w], m[w], sum);
+        }
     }
-    return l > 0.f || l != l ? acc / l : 0.f;
-}
+    __device__ __forceinline__ float add(float acc, int w, float o) const { return __fmaf_rn(o, m[w], acc); }
+    __device__ __forceinline__ float result(float acc) const { return sum > 0.f || sum != sum ? acc / sum : 0.f; }
+};
 
 template <typename Out>
 __device__ __forceinline__ void store_out(void* out, size_t at, float x) {
@@ -667,7 +689,7 @@ __device__ __forceinline__ void store_out(void* out, size_t at, float x) {
 }
 
 template <template <int> class Cache, int D, int NW, int NST>
-__global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p) {
+__global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : ctas_for(Cache<D>::TYPE, D)) window_decode_kernel(const WParams p) {
     using C = Cache<D>;
     using L = Layout<C, D, NW, NST>;
     constexpr int KS = C::KS, TILE = C::TILE;
@@ -691,10 +713,12 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
     C cache(lane, reinterpret_cast<float*>(smem + L::WARP + warp * C::SCRATCH));
     cache.load_q(p.q, row0, p.G);
     const Row row = row_of(p, s, blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0);
-    const int parts = max(1, (row.v.count + p.part_len - 1) / p.part_len);
-    const int begin = p.split ? blockIdx.x * p.part_len : 0;
-    if (begin > 0 && begin >= row.v.count) return;     // (a part's CTA that leaves is not waited for)
-    const int count = p.split ? min(p.part_len, row.v.count - begin) : row.v.count;
+    const int parts = max(1, min(p.parts, (row.v.count + p.part_len - 1) / p.part_len));
+    const int begin = blockIdx.x * p.per * p.part_len;
+    if (p.per && (int)blockIdx.x * p.per >= parts) return;     // (a CTA that leaves is not waited for)
+    // this CTA's parts and listed blocks
+    const int mine = p.per ? min(p.per, parts - (int)blockIdx.x * p.per) : parts;
+    const int count = (p.per && (int)(blockIdx.x + 1) * p.per < parts ? begin + p.per * p.part_len : row.v.count) - begin;
     BlockWalk<NW> walk{p.tables + (size_t)s * p.max_blocks, row.v, begin + 2 * warp, 0, lane, 0, p.num_blocks, p.err, -1};
     {
         // whole pairs before the last, then what is left of it
@@ -746,12 +770,26 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     // A part's end: the lanes' sums as one, the cache's own factors out, and into the warp's
-    // folded result (its outputs in shared memory, every lane its own elements).
-    float* sm_o = reinterpret_cast<float*>(smem + L::OUT);     // [NW][G][OS]
-    float* sm_m = sm_o + NW * p.G * L::OS;                     // [NW][G]
+    // folded result (its outputs in shared memory, every lane its own elements); in a cluster,
+    // where parts before this CTA's are still to be folded, into a result of the part's own.
+    const int slot = L::result(p.G), outs = L::outs(p.G), G2 = (p.G + 1) / 2;
+    float* sm_o = reinterpret_cast<float*>(smem + L::OUT);     // [NW][G2][KS][8][4]
+    float* sm_m = sm_o + NW * outs;                            // [NW][G]
     float* sm_l = sm_m + NW * p.G;                             // [NW][G]
+    int at_slot = 0;                                           // floats from the first result
     float all_m0 = -INFINITY, all_m1 = -INFINITY, all_l0 = 0.f, all_l1 = 0.f;
     bool folded = false;
+    auto put_sums = [&](float m0, float m1, float l0, float l1) {
+        const int r = lane >> 2, g = 2 * (lane & 3), at = at_slot + warp * p.G + g;
+        if (r == 0 && g < p.G) {
+            sm_m[at] = m0;
+            sm_l[at] = l0;
+        }
+        if (r == 0 && g + 1 < p.G) {
+            sm_m[at + 1] = m1;
+            sm_l[at + 1] = l1;
+        }
+    };
     auto end_part = [&]() {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -761,15 +799,13 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
         cache.finish(run, o);
         const int r = lane >> 2, c = lane & 3;
         const Fold f0 = fold_factors(all_m0, run.m0), f1 = fold_factors(all_m1, run.m1);
+        if (c < G2) {
+            float4* at = reinterpret_cast<float4*>(sm_o + at_slot + warp * outs + c * L::CS) + r;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (2 * c + e >= p.G) continue;
-            const Fold f = e ? f1 : f0;
-            float* at = sm_o + (warp * p.G + 2 * c + e) * L::OS + r;
-#pragma unroll
-            for (int mi = 0; mi < KS; ++mi) {
-                at[16 * mi] = fold_add(f, folded ? at[16 * mi] : 0.f, o[mi][e]);
-                at[16 * mi + 8] = fold_add(f, folded ? at[16 * mi + 8] : 0.f, o[mi][2 + e]);
+            for (int mi = 0; mi < KS; ++mi, at += 8) {
+                const float4 was = folded ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                *at = make_float4(fold_add(f0, was.x, o[mi][0]), fold_add(f0, was.y, o[mi][2]),
+                                  fold_add(f1, was.z, o[mi][1]), fold_add(f1, was.w, o[mi][3]));
             }
         }
         all_l0 = fold_add(f0, all_l0, run.l0);
@@ -777,6 +813,13 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
         all_m0 = f0.m;
         all_m1 = f1.m;
         folded = true;
+        if (p.per) {
+            put_sums(all_m0, all_m1, all_l0, all_l1);
+            at_slot += slot;
+            all_m0 = all_m1 = -INFINITY;
+            all_l0 = all_l1 = 0.f;
+            folded = false;
+        }
 #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         run.m0 = run.m1 = -INFINITY;
@@ -784,7 +827,7 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
         cache.reset();
     };
     const int part_pairs = p.part_len / (2 * NW);      // of a warp
-    int part_left = part_pairs;
+    int part_left = mine > 1 ? part_pairs : INT_MAX, ends = mine - 1;
     bool failed = false;
     uint32_t k_out = 0, v_out = 0;             // stages whose copies of the next pairs are in flight
 #pragma unroll
@@ -801,7 +844,7 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
             const bool more = i + NST < npairs;
             if (part_left == 0) {
                 end_part();
-                part_left = part_pairs;
+                part_left = --ends > 0 ? part_pairs : INT_MAX;
             }
             --part_left;
             const uint32_t h = (have >> (2 * st)) & 3u;
@@ -898,49 +941,79 @@ __global__ void __launch_bounds__(NW * 32) window_decode_kernel(const WParams p)
             if ((v_out >> st) & 1u) mbar_wait_bounded(bar0 + st * 16 + 8, (phase >> (2 * st + 1)) & 1u, kWaitLimitNs);
         }
     }
-    end_part();
+    const int results = p.per ? mine : 1;
+    do end_part();                             // (a warp without blocks in the last parts: empty ones)
+    while (p.per && at_slot < results * slot);
     const bool bad = __syncthreads_or(failed || skip), cta_skip = __syncthreads_or(skip);
-    {
-        // a part that was given up or skipped passes on NaN: its result is incomplete
+    if (!p.per) put_sums(all_m0, all_m1, all_l0, all_l1);
+    if (bad) {
+        // what was given up or skipped passes on NaN: its result is incomplete
         const float nan = __int_as_float(0x7fc00000);
-        const int r = lane >> 2, c = lane & 3;
-        if (r == 0 && 2 * c < p.G) {
-            sm_m[warp * p.G + 2 * c] = bad ? nan : all_m0;
-            sm_l[warp * p.G + 2 * c] = bad ? nan : all_l0;
-        }
-        if (r == 0 && 2 * c + 1 < p.G) {
-            sm_m[warp * p.G + 2 * c + 1] = bad ? nan : all_m1;
-            sm_l[warp * p.G + 2 * c + 1] = bad ? nan : all_l1;
-        }
+        for (at_slot = 0; at_slot < results * slot; at_slot += slot) put_sums(nan, nan, nan, nan);
     }
-    if (!p.split || parts == 1) {
+    if (!p.per || parts == 1) {
         __syncthreads();
         if (cta_skip) return;
-        for (int i = threadIdx.x; i < p.G * D; i += NW * 32) {
-            const int g = i / D, d = i % D;
-            const float x = merge_warps<NW>([&](int w) {
-                return Partial{sm_m[w * p.G + g], sm_l[w * p.G + g], sm_o[(w * p.G + g) * L::OS + d]};
-            });
-            store_out<typename C::Out>(p.out, (row0 + g) * D + d, x);
+        // two outputs of HT heads a thread
+        constexpr int HT = NW == 8 ? 1 : 2;
+        for (int i = threadIdx.x; i < G2 * KS * 16 / HT; i += NW * 32) {
+            const int x = i * HT / 2, c = x / (KS * 8), d = x / 8 % KS * 16 + x % 8;
+            const float* at = sm_o + c * L::CS + x % (KS * 8) * 4;
+#pragma unroll
+            for (int e = 0; e < HT; ++e) {
+                const int h = HT == 2 ? e : i & 1, g = 2 * c + h;
+                if (g >= p.G) continue;
+                Merge<NW> m;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) m.set(w, sm_m[w * p.G + g], sm_l[w * p.G + g]);
+                m.weigh();
+                float lo = 0.f, hi = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const float2 o2 = *reinterpret_cast<const float2*>(at + w * outs + 2 * h);
+                    lo = m.add(lo, w, o2.x);
+                    hi = m.add(hi, w, o2.y);
+                }
+                store_out<typename C::Out>(p.out, (row0 + g) * D + d, m.result(lo));
+                store_out<typename C::Out>(p.out, (row0 + g) * D + d + 8, m.result(hi));
+            }
         }
         return;
     }
-    // A CTA per part: each adds up its share of the output elements over all parts, reading the
+    // In a cluster each CTA adds up its share of the output elements over all parts, reading the
     // others' shared memory (so nothing goes through a workspace, and one launch does it).
     cluster_arrive();
     cluster_wait();
+    const int ctas = (parts + p.per - 1) / p.per;
     const uint32_t o_at = smem_u32(sm_o), m_at = smem_u32(sm_m), l_at = smem_u32(sm_l);
-    for (int i = blockIdx.x * (NW * 32) + threadIdx.x; i < p.G * D; i += parts * (NW * 32)) {
-        const int g = i / D, d = i % D;
-        const float x = merge_warps<NW>([&](int w) {
+    for (int i = blockIdx.x * (NW * 32) + threadIdx.x; i < G2 * KS * 32; i += ctas * (NW * 32)) {
+        const int c = i / (KS * 32), g = 2 * c + (i >> 1 & 1), d = i / 32 % KS * 16 + i / 4 % 8 + (i & 1) * 8;
+        const uint32_t at = o_at + (c * L::CS + i % (KS * 32)) * 4;
+        if (g >= p.G) continue;
+        Merge<NW> m;
+        float o_w[NW];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
             Partial a{-INFINITY, 0.f, 0.f};
+            int rank = 0, k = 0;
 #pragma unroll 4
-            for (int j = 0; j < parts; ++j)
-                fold(a, Partial{peer_f32(m_at + (w * p.G + g) * 4, j), peer_f32(l_at + (w * p.G + g) * 4, j),
-                                peer_f32(o_at + ((w * p.G + g) * L::OS + d) * 4, j)});
-            return a;
-        });
-        if (!cta_skip) store_out<typename C::Out>(p.out, (row0 + g) * D + d, x);
+            for (int j = 0; j < parts; ++j) {
+                const uint32_t from = k * slot * 4;
+                fold(a, Partial{peer_f32(m_at + from + (w * p.G + g) * 4, rank), peer_f32(l_at + from + (w * p.G + g) * 4, rank),
+                                peer_f32(at + from + w * outs * 4, rank)});
+                if (++k == p.per) {
+                    k = 0;
+                    ++rank;
+                }
+            }
+            m.set(w, a.m, a.l);
+            o_w[w] = a.o;
+        }
+        m.weigh();
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) x = m.add(x, w, o_w[w]);
+        if (!cta_skip) store_out<typename C::Out>(p.out, (row0 + g) * D + d, m.result(x));
     }
     // no CTA leaves while another may still read its shared memory
     cluster_arrive();
@@ -951,9 +1024,8 @@ constexpr int kSmemMax = 232448;       // shared memory of an SM that one CTA ca
 
 // Attributes of a kernel, set once per device; and the device's SMs.
 template <void (*Kernel)(const WParams)>
-cudaError_t prepare_kernel(int& sms) {
+cudaError_t prepare_kernel(int& dev, int& sms) {
     static std::atomic<uint64_t> done{0};
-    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -967,23 +1039,67 @@ cudaError_t prepare_kernel(int& sms) {
     return e;
 }
 
+// Clusters of `ctas` CTAs that the (empty) GPU runs at once.  What the runtime answers is kept,
+// one answer for each number of CTAs, with what it was asked for.
 template <void (*Kernel)(const WParams)>
-cudaError_t launch(const WParams& p, int parts, int num_seqs, int threads, int smem, cudaStream_t stream) {
-    int sms = 1;
-    const cudaError_t e = prepare_kernel<Kernel>(sms);
-    if (e != cudaSuccess) return e;
+long long clusters_at_once(int dev, int ctas, int threads, int smem) {
+    static std::atomic<uint64_t> kept[17];         // device + 1, bytes, answer
+    const uint64_t key = (uint64_t)(dev + 1) << 48 | (uint64_t)smem << 16;
+    const uint64_t was = kept[ctas].load(std::memory_order_relaxed);
+    if ((was & ~0xffffull) == key) return (long long)(was & 0xffff);
     cudaLaunchConfig_t cfg = {};
-    const int ctas = p.split ? parts : 1;
-    cfg.gridDim = dim3(ctas, p.Hkv, num_seqs);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    n = n < 0xffff ? n : 0xffff;
+    kept[ctas].store(key | (uint64_t)n, std::memory_order_relaxed);
+    return n;
+}
+
+template <void (*Kernel)(const WParams)>
+cudaError_t launch(WParams p, int num_seqs, int threads, int smem, int smem_result, cudaStream_t stream) {
+    const int parts = p.parts;
+    int dev = 0, sms = 1;
+    const cudaError_t e = prepare_kernel<Kernel>(dev, sms);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    const long long pairs = (long long)p.Hkv * num_seqs;
+    // As many CTAs for a sequence's parts as the GPU has room for at once (clusters' CTAs start
+    // together, and what does not fit waits for a whole cluster to end).  bf16, window 4096, 1, 4,
+    // 8 and 16 sequences of 32 / 8 heads of 128: 10.2, 17.3, 25.5 and 45.6 us, against 37.6,
+    // 38.3, 39.4 and 46.5 with a CTA for each (sequence, kv head); FP8, 16 sequences: 29.1 / 43.1.
+    // Clusters of more CTAs than fit: f32, 2 sequences, window 2048, 24.6 / 18.3.
+    p.per = 0;
+    for (int per = 1; per < parts; per *= 2) {
+        const int bytes = smem + (per - 1) * smem_result;
+        if (bytes > kSmemMax) break;
+        if (pairs <= clusters_at_once<Kernel>(dev, (parts + per - 1) / per, threads, bytes)) {
+            p.per = per;
+            break;
+        }
+    }
+    const int ctas = p.per ? (parts + p.per - 1) / p.per : 1;
+    cfg.gridDim = dim3(ctas, p.Hkv, num_seqs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = p.per ? smem + (p.per - 1) * smem_result : smem;
     // No more CTAs on an SM than the grid has for each: a grid of less than the GPU holds would
     // fill some SMs and leave others empty, so its CTAs ask for the memory that keeps them apart
     // (32 sequences of 32 / 8 heads of 128, bf16, window 1024: 27.2 -> 23.8 us).  Not so for
-    // clusters of over 8, which may not find as many SMs together.
-    const long long per_sm = ((long long)ctas * p.Hkv * num_seqs + sms - 1) / sms;
-    const long long apart = kSmemMax / (per_sm + 1) + 1;
-    if (ctas <= 8 && apart > smem && apart <= kSmemMax / per_sm - 1024) cfg.dynamicSmemBytes = (size_t)(apart + 15) / 16 * 16;
+    // clusters, which may not find as many SMs together.
+    const long long per_sm = (pairs + sms - 1) / sms, apart = kSmemMax / (per_sm + 1) + 1;
+    if (ctas == 1 && apart > smem && apart <= kSmemMax / per_sm - 1024) cfg.dynamicSmemBytes = (size_t)(apart + 15) / 16 * 16;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -998,27 +1114,27 @@ cudaError_t launch(const WParams& p, int parts, int num_seqs, int threads, int s
     if (launched == cudaSuccess || ctas == 1) return launched;
     // a GPU (or a part of one) without room for the cluster: one CTA for all parts, the same result
     cudaGetLastError();
-    WParams whole = p;
-    whole.split = 0;
+    p.per = 0;
     cfg.gridDim.x = 1;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, Kernel, whole);
+    return cudaLaunchKernelEx(&cfg, Kernel, p);
 }
 
 template <template <int> class Cache, int D, int NST>
-cudaError_t launch_cache(const WParams& p, int parts, int num_seqs, cudaStream_t stream) {
+cudaError_t launch_cache(const WParams& p, int num_seqs, cudaStream_t stream) {
     constexpr int NW = warps_for(Cache<D>::TYPE, D);
-    return launch<window_decode_kernel<Cache, D, NW, NST>>(p, parts, num_seqs, NW * 32, Layout<Cache<D>, D, NW, NST>::bytes(p.G),
-                                                           stream);
+    using L = Layout<Cache<D>, D, NW, NST>;
+    return launch<window_decode_kernel<Cache, D, NW, NST>>(p, num_seqs, NW * 32, L::bytes(p.G, 1),
+                                                           L::bytes(p.G, 2) - L::bytes(p.G, 1), stream);
 }
 
 template <int D>
-cudaError_t launch_type(const WParams& p, int parts, pa_dtype dtype, int num_seqs, cudaStream_t stream) {
+cudaError_t launch_type(const WParams& p, pa_dtype dtype, int num_seqs, cudaStream_t stream) {
     switch (dtype) {
-        case PA_BF16: return launch_cache<Bf16Cache, D, 1>(p, parts, num_seqs, stream);
-        case PA_FP8_E4M3: return launch_cache<Fp8Cache, D, 1>(p, parts, num_seqs, stream);
-        case PA_FP4_E2M1: return launch_cache<Fp4Cache, D, 1>(p, parts, num_seqs, stream);
-        case PA_F32: return launch_cache<F32Cache, D, 1>(p, parts, num_seqs, stream);
+        case PA_BF16: return launch_cache<Bf16Cache, D, 1>(p, num_seqs, stream);
+        case PA_FP8_E4M3: return launch_cache<Fp8Cache, D, 1>(p, num_seqs, stream);
+        case PA_FP4_E2M1: return launch_cache<Fp4Cache, D, 1>(p, num_seqs, stream);
+        case PA_F32: return launch_cache<F32Cache, D, 1>(p, num_seqs, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -1046,16 +1162,19 @@ cudaError_t launch_window_decode(const WindowArgs& a, cudaStream_t stream) {
     long long n = ((long long)a.window + 2 * kBlockTokens - 2) / kBlockTokens +
                   ((long long)a.sinks + kBlockTokens - 1) / kBlockTokens;
     if (n > a.max_blocks) n = a.max_blocks;
-    // at most 16 parts (the largest cluster), whole pairs for every warp
-    const int unit = 2 * warps_for(a.dtype, a.head_dim);
-    const int blocks = (int)n, least = min_part(a.dtype);
-    const int most = blocks > 16 * least ? 16 : blocks < least ? 1 : blocks / least;
-    p.part_len = ((blocks + most - 1) / most + unit - 1) / unit * unit;
-    const int parts = (blocks + p.part_len - 1) / p.part_len;
-    p.split = parts > 1 && (long long)a.num_kv_heads * a.num_seqs < split_below(a.dtype);
+    const int unit = 2 * warps_for(a.dtype, a.head_dim);       // blocks: a pair for every warp
+    const int blocks = (int)n, least = min_part(a.dtype), limit = most_parts(a.dtype, a.head_dim);
+    p.parts = 1;
+    while (blocks >= min_pairs(a.dtype) * unit && 2 * p.parts <= limit && 2 * p.parts * least <= blocks) p.parts *= 2;
+    p.part_len = blocks / p.parts / unit * unit;
+    if (p.part_len == 0 || blocks - p.parts * p.part_len > unit) {
+        p.part_len += unit;
+        p.parts = (blocks + p.part_len - 1) / p.part_len;
+    }
+    p.per = 0;
     p.scale_log2 = a.scale * kLog2e;
-    return a.head_dim == 64 ? launch_type<64>(p, parts, a.dtype, a.num_seqs, stream)
-                            : launch_type<128>(p, parts, a.dtype, a.num_seqs, stream);
+    return a.head_dim == 64 ? launch_type<64>(p, a.dtype, a.num_seqs, stream)
+                            : launch_type<128>(p, a.dtype, a.num_seqs, stream);
 }
 
 }  // namespace pa

@@ -129,6 +129,21 @@ def test_decode_batched_equals_alone_and_repeats(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("heads", [(32, 8, 128), (15, 3, 128), (14, 2, 64)])
+def test_decode_is_the_same_in_batches_of_every_size(cache, heads):
+    # (a CTA takes one, two, four or all of a sequence's parts, as the batch grows)
+    lens = [2300, 2020, 900, 1300, 17, 0]
+    c = Cache(cache, lens, heads, seed=31)
+    q = c.queries(len(lens))
+    out = run_decode(c, lens, q, 2040, 20, 0.1)
+    check_decode(c, lens, q, 2040, 20, 0.1, out)
+    for n in (1, 2, 3, 5, 8, 12, 16, 24, 40, 75, 160):
+        at = torch.arange(n) % len(lens)
+        many = run_decode(c, [lens[i] for i in at], q[at], 2040, 20, 0.1, tables=c.tables[at])
+        assert torch.equal(many, out[at.cuda()]), n
+
+
+@pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 8.0])
 def test_decode_scales(cache, scale):
     lens = [90, 33]
