@@ -16,6 +16,7 @@
 // a turn, goes to sincospif, so that sine and cosine carry about one fp32 rounding each.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "pa_ptx.cuh"
@@ -42,15 +43,37 @@ struct RParams {
     int max_blocks, S, total, num_blocks, Hq, Hkv, half;       // half = rotary_dim / 2
 };
 
-constexpr int kThreads = 256;
-constexpr int kTileMinRows = 4;        // rows per sequence from which a call goes tile by tile
+constexpr int kThreads = 256;         // of a tile's CTA
+constexpr int kRowThreads = 128;      // of a row's
+// A call goes row by row (a CTA each, no row waits for another) or tile by tile (a pool's tile
+// is written in whole runs).  Rows are faster for few of them, and for short chunks, whose
+// tiles are mostly empty; runs matter more where a value is a byte.  Rows against tiles, 32 / 8
+// heads of 128, us: one chunk of 256 bf16 2.9 / 3.7, FP8 6.2 / 7.3; of 1000 bf16 7.1 / 5.8, FP8
+// 16.4 / 10.0; 256 chunks of 8, 12.5 / 19.0 and 27.3 / 31.0; 64 of 16, 7.0 / 8.3 and 16.3 / 15.3;
+// 100 of 1 to 40, 11.3 / 16.0 and 28.1 / 22.0; 16 of 512, 40.3 / 36.2 and 99.4 / 40.6.
+constexpr int kRowsAlone = 512;        // up to so many rows in all
+constexpr int kTileMinRows = 32;       // and below so many per sequence, of bf16 and f32
+constexpr int kTileMinRowsQuantised = 16;
 constexpr int kTileHeads = 3;          // heads of a thread that are loaded together (four spill)
 
-// A frequency in radians per position as turns * 2^64, modulo 2^64.
+// A frequency in radians per position as turns * 2^64, modulo 2^64.  Below 1024 in integers
+// (FP64 instructions take 64 times as long here): x = m 2^e with a 53-bit m, and 2^64 x / (2 pi)
+// is m (2^66 / (2 pi)) 2^(e - 2), good to less than 2^10 / 2^64 turns.
 __device__ __forceinline__ uint64_t fixed_turns(double inv_freq) {
-    double t = inv_freq * 0.15915494309189533577;              // 1 / (2 pi)
-    t -= rint(t);
-    return (uint64_t)__double2ll_rn(t * 18446744073709551616.0);
+    const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
+    const int e = (int)(bits >> 52 & 0x7ff);                   // x = m 2^(e - 1075)
+    uint64_t t;
+    if (e < 1023 + 10) {
+        const uint64_t m = e > 0 ? (bits & ((1ull << 52) - 1)) | 1ull << 52 : 0;    // (denormal: none)
+        const uint64_t hi = __umul64hi(m, 0xa2f9836e4e44152aull), lo = m * 0xa2f9836e4e44152aull;
+        const int sh = 1077 - e;                               // from 45 on
+        t = sh < 64 ? lo >> sh | hi << (64 - sh) : sh == 64 ? hi : sh < 128 ? hi >> (sh - 64) : 0;
+    } else {
+        double r = fabs(inv_freq) * 0.15915494309189533577;    // 1 / (2 pi)
+        r -= rint(r);
+        t = (uint64_t)__double2ll_rn(r * 18446744073709551616.0);
+    }
+    return bits >> 63 ? 0 - t : t;
 }
 
 // cos and sin of `phase` / 2^64 turns.
@@ -101,14 +124,41 @@ __device__ __forceinline__ float max_abs(const Piece<E>& r) {
     return m;
 }
 
+// x / scale, correctly rounded, for one scale and many x: with the correctly rounded reciprocal
+// y, q = x y and two steps q + (x - q scale) y, the remainders exact by fused multiply-add, give
+// the quotient's rounding (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990) while nothing underflows.  At scales from 2^-80 the remainders
+// of quotients that round to a code above 0 do not; other scales (infinity too) divide.
+struct Divisor {
+    float scale, y;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float s) {
+        scale = s;
+        y = __frcp_rn(s);
+        plain = !(s >= 0x1p-80f && s <= 0x1p80f);
+    }
+    __device__ __forceinline__ float quotient(float x) const {
+        float q = __fmul_rn(x, y);
+        q = __fmaf_rn(__fmaf_rn(-q, scale, x), y, q);
+        return __fmaf_rn(__fmaf_rn(-q, scale, x), y, q);
+    }
+};
+
 // Eight E4M3 codes of x / scale, in the order of the dims (scale 0: an all-zero row).
-__device__ __forceinline__ uint2 e4m3_codes(const Piece<8>& r, float scale) {
-    if (!(scale > 0.f)) return make_uint2(0u, 0u);
+__device__ __forceinline__ uint2 e4m3_codes(const Piece<8>& r, const Divisor& by) {
+    if (!(by.scale > 0.f)) return make_uint2(0u, 0u);
+    float q[8];
+    if (by.plain) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(r.x[i], by.scale);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = by.quotient(r.x[i]);
+    }
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        w[i] = (uint32_t)pack_e4m3x2(__fdiv_rn(r.x[4 * i], scale), __fdiv_rn(r.x[4 * i + 1], scale)) |
-               (uint32_t)pack_e4m3x2(__fdiv_rn(r.x[4 * i + 2], scale), __fdiv_rn(r.x[4 * i + 3], scale)) << 16;
+        w[i] = (uint32_t)pack_e4m3x2(q[4 * i], q[4 * i + 1]) | (uint32_t)pack_e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16;
     return make_uint2(w[0], w[1]);
 }
 
@@ -180,7 +230,8 @@ __device__ __forceinline__ void put_quantised(const RParams& p, char* pool, int3
         if (live) {
             const float scale = __fdiv_rn(m, 448.f);
             char* rec = pool + ((size_t)blk * p.Hkv + h) * fp8_record_bytes(D);
-            const uint2 ca = e4m3_codes(a, scale), cb = e4m3_codes(b, scale);
+            const Divisor by(scale);
+            const uint2 ca = e4m3_codes(a, by), cb = e4m3_codes(b, by);
             if (is_k) {
                 *reinterpret_cast<uint2*>(rec + ((at.a >> 1) * kBlockTokens + slot) * 16 + (at.a & 1) * 8) = ca;
                 *reinterpret_cast<uint2*>(rec + ((at.b >> 1) * kBlockTokens + slot) * 16 + (at.b & 1) * 8) = cb;
@@ -237,71 +288,138 @@ __device__ __forceinline__ void put_quantised(const RParams& p, char* pool, int3
     }
 }
 
-// Flags cu_new_tokens where it is not a prefix sum that ends at the rows (one CTA's threads).
+// Flags cu_new_tokens where it is not a prefix sum that ends at the rows (one CTA's N threads).
+template <int N>
 __device__ __forceinline__ void check_cu(const RParams& p) {
     bool bad = threadIdx.x == 0 && (__ldg(p.cu) != 0 || __ldg(p.cu + p.S) != p.total);
-    for (int s = threadIdx.x; s < p.S; s += kThreads) bad |= __ldg(p.cu + s) > __ldg(p.cu + s + 1);
+    for (int s = threadIdx.x; s < p.S; s += N) bad |= __ldg(p.cu + s) > __ldg(p.cu + s + 1);
     if (bad) raise_flag(p.err, PA_DEV_ERR_BAD_CU);
 }
 
+// The last of n sequences from lo on whose first unit (from(s), not falling) is at most x, found
+// by all N threads of the CTA: a probe each narrows the range N times.
+template <int N, typename From>
+__device__ __forceinline__ int last_from(int lo, int n, int x, From from) {
+    while (n > 1) {
+        const int step = (n + N - 1) / N, at = threadIdx.x * step;
+        const int hits = __syncthreads_count(at < n && from(lo + at) <= x);
+        const int k = hits > 0 ? hits - 1 : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return lo;
+}
+
+// The place of new row `row`, the same in every thread; false: it has none (flagged).
+__device__ __forceinline__ bool find_row(const RParams& p, int row, int& pos_out, int32_t& blk_out) {
+    // its sequence if all append as many rows (a decode step), with its place in the same round trip
+    int s = min((int)((long long)row * p.S / p.total), p.S - 1);
+    int first = __ldg(p.cu + s), next = __ldg(p.cu + s + 1);
+    long long start = __ldg(p.start_pos + s);
+    const bool report = threadIdx.x == 0;
+    if (row < first || row >= next) {
+        s = last_from<kRowThreads>(0, p.S, row, [&](int x) { return __ldg(p.cu + x); });
+        first = __ldg(p.cu + s);
+        next = __ldg(p.cu + s + 1);
+        start = __ldg(p.start_pos + s);
+        if (row < first || row >= next) {
+            if (report) raise_flag(p.err, PA_DEV_ERR_BAD_CU);
+            return false;
+        }
+    }
+    const long long pos = start + (row - first);
+    if (pos < 0 || pos >= (long long)p.max_blocks * kBlockTokens) {
+        if (report) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+        return false;
+    }
+    const int32_t blk = __ldg(p.tables + (size_t)s * p.max_blocks + (int)(pos / kBlockTokens));
+    pos_out = (int)pos;
+    blk_out = blk;
+    return true;
+}
+
 // One CTA per row: its frequencies' cosines and sines once, then every (head, item) of the
-// keys, values and queries, a thread an item at a time: two 16-byte loads, two stores.
-// T: the pool's type.
+// keys, values and queries, a thread an item at a time: two 16-byte loads, two stores.  The
+// row's data do not depend on its place, so the first N items of a thread are under way while
+// the place is looked up.  T: the pool's type.
 template <int D, pa_dtype T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RParams p) {
+__global__ void __launch_bounds__(kRowThreads) rope_append_kernel(const RParams p) {
     constexpr int E = T == PA_F32 ? 4 : 8;       // elements of a piece (the rows are f32 or bf16)
     constexpr int PH = D / (2 * E);              // items of a head
+    constexpr int N = 3;
     __shared__ __align__(16) float2 cs[D / 2];
     // the rows may come from the kernel before (a projection), and the pools be in use by it
     grid_dependency_wait();
     grid_launch_dependents();
     const int row = blockIdx.x, tid = threadIdx.x;
-    if (row == 0) check_cu(p);
-    int s, pos = 0;
+    const int items = (2 * p.Hkv + p.Hq) * PH;
+    struct Item { int h, u; bool live, is_k, is_v; Pair at; };
+    auto item = [&](int i) {
+        Item x;
+        const int head = i / PH;
+        x.live = i < items;
+        x.u = i % PH;
+        x.is_k = head < p.Hkv;
+        x.is_v = !x.is_k && head < 2 * p.Hkv;
+        x.h = x.is_k ? head : x.is_v ? head - p.Hkv : head - 2 * p.Hkv;
+        x.at = pieces_of<E>(x.u, p.half, !INTERLEAVED && !x.is_v);
+        return x;
+    };
+    uint4 ra[N], rb[N];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const Item x = item(i0 + j * kRowThreads + tid);
+            ra[j] = rb[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (!x.live) continue;
+            const char* src = (x.is_k ? p.k_new + row * p.k_stride : x.is_v ? p.v_new + row * p.v_stride
+                                                                            : p.q + row * p.q_stride) + (size_t)x.h * (PH * 32);
+            ra[j] = *reinterpret_cast<const uint4*>(src + x.at.a * 16);
+            rb[j] = *reinterpret_cast<const uint4*>(src + x.at.b * 16);
+        }
+    };
+    load(0);
+    if (row == 0) check_cu<kRowThreads>(p);
+    int pos = 0;
     int32_t blk = 0;
-    if (!locate_row(p, row, tid == 0, s, pos, blk)) return;      // the same in every thread
-    for (int f = tid; f < p.half; f += kThreads) cs[f] = cos_sin(fixed_turns(p.inv_freq[f]) * (uint64_t)pos);
+    if (!find_row(p, row, pos, blk)) return;
+    for (int f = tid; f < p.half; f += kRowThreads) cs[f] = cos_sin(fixed_turns(p.inv_freq[f]) * (uint64_t)pos);
+    if (blk < 0 || blk >= p.num_blocks) {        // no place: the row is skipped
+        if (tid == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+        return;
+    }
     __syncthreads();
     const int slot = pos % kBlockTokens;
-    const int heads = 2 * p.Hkv + p.Hq;
-    const int items = heads * PH;
     // every lane runs every iteration: the quantised types share maxima by shuffles
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-        const int i = i0 + tid;
-        const bool live = i < items;
-        const int head = live ? i / PH : 0, u = i % PH;
-        const bool is_k = head < p.Hkv, is_v = !is_k && head < 2 * p.Hkv;
-        const int h = is_k ? head : is_v ? head - p.Hkv : head - 2 * p.Hkv;
-        const bool split = !INTERLEAVED && !is_v;
-        const bool turn = !is_v && u < p.half / E;
-        const Pair at = pieces_of<E>(u, p.half, split);
-        const char* src = (is_k ? p.k_new + row * p.k_stride : is_v ? p.v_new + row * p.v_stride : p.q + row * p.q_stride) +
-                          (size_t)h * (PH * 32);
-        uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
-        if (live) {
-            ra = *reinterpret_cast<const uint4*>(src + at.a * 16);
-            rb = *reinterpret_cast<const uint4*>(src + at.b * 16);
-        }
-        Piece<E> a = unpack<E>(ra), b = unpack<E>(rb);
-        if (turn) {
-            float2 c[E];
-            item_turns<E>(cs, u, c);
-            turn_item<E, INTERLEAVED>(a, b, c);
-        }
-        if (live && !is_k && !is_v) {
-            char* dst = p.q_out + row * p.q_out_stride + (size_t)h * (PH * 32);
-            *reinterpret_cast<uint4*>(dst + at.a * 16) = pack<E>(a);
-            *reinterpret_cast<uint4*>(dst + at.b * 16) = pack<E>(b);
-        }
-        char* pool = is_v ? p.v_pool : p.k_pool;
-        if constexpr (T == PA_F32 || T == PA_BF16) {
-            if (live && (is_k || is_v)) {
-                char* dst = pool + ((((size_t)blk * p.Hkv + h) * (2 * PH)) * kBlockTokens + slot) * 16;
-                *reinterpret_cast<uint4*>(dst + at.a * 256) = pack<E>(a);
-                *reinterpret_cast<uint4*>(dst + at.b * 256) = pack<E>(b);
+    for (int i0 = 0; i0 < items; i0 += N * kRowThreads) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (i0 + j * kRowThreads >= items) break;
+            const Item x = item(i0 + j * kRowThreads + tid);
+            const Pair at = x.at;
+            Piece<E> a = unpack<E>(ra[j]), b = unpack<E>(rb[j]);
+            if (!x.is_v && x.u < p.half / E) {
+                float2 c[E];
+                item_turns<E>(cs, x.u, c);
+                turn_item<E, INTERLEAVED>(a, b, c);
             }
-        } else {
-            put_quantised<D, T>(p, pool, blk, h, slot, is_k, live && (is_k || is_v), u, at, split, a, b);
+            const bool to_pool = x.live && (x.is_k || x.is_v);
+            if (x.live && !to_pool) {
+                char* dst = p.q_out + row * p.q_out_stride + (size_t)x.h * (PH * 32);
+                *reinterpret_cast<uint4*>(dst + at.a * 16) = pack<E>(a);
+                *reinterpret_cast<uint4*>(dst + at.b * 16) = pack<E>(b);
+            }
+            char* pool = x.is_v ? p.v_pool : p.k_pool;
+            if constexpr (T == PA_F32 || T == PA_BF16) {
+                if (to_pool) {
+                    char* dst = pool + ((((size_t)blk * p.Hkv + x.h) * (2 * PH)) * kBlockTokens + slot) * 16;
+                    *reinterpret_cast<uint4*>(dst + at.a * 256) = pack<E>(a);
+                    *reinterpret_cast<uint4*>(dst + at.b * 256) = pack<E>(b);
+                }
+            } else if (__any_sync(0xffffffffu, to_pool)) {
+                put_quantised<D, T>(p, pool, blk, to_pool ? x.h : 0, slot, x.is_k, to_pool, x.u, at, !INTERLEAVED && !x.is_v, a, b);
+            }
         }
     }
 }
@@ -335,24 +453,12 @@ __device__ __forceinline__ int tile_base(const RParams& p, int s) {
 __device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
     const int tid = threadIdx.x;
     // the sequence if all have as many rows, and its place with it: often right, one round trip
-    int lo = min(t / (p.total / (kTileRows * p.S) + 2), p.S - 1), n = 1;
+    int lo = min(t / (p.total / (kTileRows * p.S) + 2), p.S - 1);
     int first = __ldg(p.cu + lo), next = __ldg(p.cu + lo + 1);
     long long start = __ldg(p.start_pos + lo);
-    if (t < (first >> 4) + 2 * lo || (lo + 1 < p.S && t >= (next >> 4) + 2 * (lo + 1))) {
-        lo = 0;
-        n = p.S;
-    }
-    const bool guessed = n == 1;
-    // else the last s in [lo, lo + n) with tile_base(s) <= t: 256 probes narrow it 256 times
-    while (n > 1) {
-        const int step = (n + kThreads - 1) / kThreads;
-        const int s = lo + tid * step;
-        const int hits = __syncthreads_count(tid * step < n && tile_base(p, s) <= t);
-        const int k = hits > 0 ? hits - 1 : 0;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
+    const bool guessed = t >= (first >> 4) + 2 * lo && (lo + 1 == p.S || t < (next >> 4) + 2 * (lo + 1));
     if (!guessed) {
+        lo = last_from<kThreads>(0, p.S, t, [&](int s) { return tile_base(p, s); });
         first = __ldg(p.cu + lo);
         next = __ldg(p.cu + lo + 1);
         start = __ldg(p.start_pos + lo);
@@ -378,26 +484,33 @@ __device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
     return true;
 }
 
-// FP8 values of one head: lane = (slot, half of the dims).  `sm`: D / 4 x 16 words of the warp.
+// FP8 values of one head: lane = (slot, half of the dims), D / 16 pieces of its row.
 template <int D>
-__device__ __forceinline__ void put_fp8_values(const RParams& p, const Tile& tile, int h, uint32_t* sm) {
-    constexpr int NP = D / 16;                  // 16-byte pieces of half a row
+__device__ __forceinline__ void load_values(const RParams& p, const Tile& tile, int h, uint4 (&v)[D / 16]) {
     const int lane = threadIdx.x & 31, slot = lane & 15, half = lane >> 4;
-    const bool live = slot >= tile.lo && slot < tile.hi;
-    uint4 v[NP];
+    const bool live = h < p.Hkv && slot >= tile.lo && slot < tile.hi;
     const char* src = p.v_new + (long long)(tile.row0 + slot - tile.lo) * p.v_stride + (size_t)h * (2 * D) + half * D;
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+    for (int i = 0; i < D / 16; ++i)
         v[i] = live ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+}
+// ... and into the pool.  `sm`: D / 4 x 16 words of the warp.
+template <int D>
+__device__ __forceinline__ void put_fp8_values(const RParams& p, const Tile& tile, int h, const uint4 (&v)[D / 16],
+                                               uint32_t* sm) {
+    constexpr int NP = D / 16;
+    const int lane = threadIdx.x & 31, slot = lane & 15, half = lane >> 4;
+    const bool live = slot >= tile.lo && slot < tile.hi;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) m = fmaxf(m, max_abs<8>(unpack<8>(v[i])));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
     const float scale = __fdiv_rn(m, 448.f);
+    const Divisor by(scale);
     __syncwarp();                               // (the last head's reads are done)
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const uint2 c = e4m3_codes(unpack<8>(v[i]), scale);
+        const uint2 c = e4m3_codes(unpack<8>(v[i]), by);
         const int d4 = half * (D / 8) + 2 * i;
         sm[d4 * 16 + slot] = c.x;
         sm[(d4 + 1) * 16 + slot] = c.y;
@@ -450,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RPa
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu(p);
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu<kThreads>(p);
     if (tid < p.half) turns[tid] = fixed_turns(p.inv_freq[tid]);
     Tile tile;
     if (!find_tile(p, blockIdx.x, tile)) return;
@@ -558,46 +671,61 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RPa
         const bool turn = u < p.half / E;
         float2 c[E];
         if (turn && here) item_turns<E>(cs + slot * PAD, u, c);
-        constexpr int KINDS = T == PA_FP8_E4M3 ? 1 : 2;
-        for (int h0 = share; h0 < p.Hkv; h0 += stride) {             // (the same trips in every lane)
-            const int h = h0 + (g - share);
+        constexpr bool FP8 = T == PA_FP8_E4M3;
+        // FP8 values: by warps, from the last share on, loaded while the keys are turned
+        const int warp = tid >> 5;
+        int vh = (gridDim.y - 1 - blockIdx.y) * 8 + warp;
+        uint4 v[D / 16];
+        if constexpr (FP8) load_values<D>(p, tile, vh, v);
 #pragma unroll
-            for (int kind = 0; kind < KINDS; ++kind) {
-                const bool split = !INTERLEAVED && kind == 0, live = here && h < p.Hkv;
-                const Pair at = pieces_of<E>(u, p.half, split);
-                const char* src = (kind == 0 ? p.k_new + row_at(slot) * p.k_stride : p.v_new + row_at(slot) * p.v_stride) +
-                                  (size_t)h * (PH * 32);
-                uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
-                if (live) {
-                    ra = *reinterpret_cast<const uint4*>(src + at.a * 16);
-                    rb = *reinterpret_cast<const uint4*>(src + at.b * 16);
+        for (int kind = 0; kind < (FP8 ? 1 : 2); ++kind) {
+            const bool split = !INTERLEAVED && kind == 0;
+            const Pair at = pieces_of<E>(u, p.half, split);
+            const char* src = kind == 0 ? p.k_new + row_at(slot) * p.k_stride : p.v_new + row_at(slot) * p.v_stride;
+            constexpr int NK = 4;                 // heads of a thread that are loaded together
+            uint4 ra[NK], rb[NK];
+            for (int h0 = share; h0 < p.Hkv; h0 += NK * stride) {        // (the same trips in every lane)
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    const int h = h0 + (g - share) + i * stride;
+                    ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (!here || h >= p.Hkv) continue;
+                    ra[i] = *reinterpret_cast<const uint4*>(src + (size_t)h * (PH * 32) + at.a * 16);
+                    rb[i] = *reinterpret_cast<const uint4*>(src + (size_t)h * (PH * 32) + at.b * 16);
                 }
-                Piece<E> a = unpack<E>(ra), b = unpack<E>(rb);
-                if (kind == 0 && turn && live) turn_item<E, INTERLEAVED>(a, b, c);
-                put_quantised<D, T>(p, kind == 0 ? p.k_pool : p.v_pool, tile.blk, live ? h : 0, slot, kind == 0, live, u, at,
-                                    split, a, b);
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    if (h0 + i * stride >= p.Hkv) break;
+                    const int h = h0 + (g - share) + i * stride;
+                    const bool live = here && h < p.Hkv;
+                    Piece<E> a = unpack<E>(ra[i]), b = unpack<E>(rb[i]);
+                    if (kind == 0 && turn && live) turn_item<E, INTERLEAVED>(a, b, c);
+                    put_quantised<D, T>(p, kind == 0 ? p.k_pool : p.v_pool, tile.blk, live ? h : 0, slot, kind == 0, live, u,
+                                        at, split, a, b);
+                }
             }
         }
-        if constexpr (T == PA_FP8_E4M3) {
-            const int warp = tid >> 5;
-            for (int h = blockIdx.y * 8 + warp; h < p.Hkv; h += gridDim.y * 8)
-                put_fp8_values<D>(p, tile, h, sm_v + warp * (D / 4) * 16);
+        if constexpr (FP8) {
+            for (; vh < p.Hkv; vh += gridDim.y * 8) {
+                put_fp8_values<D>(p, tile, vh, v, sm_v + warp * (D / 4) * 16);
+                load_values<D>(p, tile, vh + gridDim.y * 8, v);
+            }
         }
     }
 }
 
 template <int D, pa_dtype T, bool INTERLEAVED>
 cudaError_t launch_rope(const RParams& p, cudaStream_t stream) {
-    // Rows of few tokens per sequence (a decode step) go row by row, chunks tile by tile.
-    const bool tiles = p.total >= kTileMinRows * (long long)p.S;
+    const int least = T == PA_F32 || T == PA_BF16 ? kTileMinRows : kTileMinRowsQuantised;
+    const bool tiles = p.total > kRowsAlone && p.total >= least * (long long)p.S;
     cudaLaunchConfig_t cfg = {};
-    // A tile's heads are shared by several CTAs while that still finds idle SMs (two CTAs fit on
-    // one): 512 full tiles of 32 + 16 heads of 128 take 35.6 us with one CTA each, 37.7 with two;
-    // 185 ragged ones into FP8 pools 25.9 and 22.4 us.
-    const int full = p.total / kTileRows > 0 ? p.total / kTileRows : 1;
-    const int shares = full >= 304 ? 1 : full >= 38 ? (304 + full - 1) / full : 8;
+    // A tile's heads are shared by several CTAs while that finds idle SMs (two CTAs fit on one):
+    // 512 full tiles of 32 + 16 heads of 128 take 35.6 us with one CTA each and 37.7 with two; 153,
+    // 16.7, 12.5 with two and 14.5 with three (FP8 19.1, 15.3, 18.5).
+    const long long touched = (p.total + (kTileRows - 1ll) * p.S) / kTileRows;      // of chunks that begin anywhere
+    const int shares = (int)std::max(1ll, std::min(8ll, 308 / touched));
     cfg.gridDim = tiles ? dim3((unsigned)(p.total / kTileRows + 2ll * p.S), shares) : dim3((unsigned)p.total);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(tiles ? kThreads : kRowThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -403,6 +403,70 @@ def check_prefill(c, starts, counts, q, window, sinks, scale, out, every=1):
         row += n
 
 
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("heads,rotary", [((4, 2, 64), 64), ((15, 3, 128), 112), ((2, 18, 64), 48)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_append_of_long_chunks_is_that_of_their_rows(cache, heads, rotary, interleaved):
+    # 658 rows in one call go block by block, in calls of at most 350 row by row: the same queries,
+    # pools and flags, also where a block has no table entry, before position 0 and past the table
+    hq, hkv, d = heads
+    counts, starts = [0, 300, 33, 1, 150, 64, 110], [5, 3, 0, 17, 70000, -9, 70199]
+    (q, k, v), (dq, dk, dv) = rope_inputs(cache, counts, heads, True, seed=17)
+    tables, _, _, blocks = place([max(0, x) for x in starts], counts)
+    tables = tables[:, :4394].contiguous()                              # (70304 positions)
+    tables[4, 70032 // BLOCK] = blocks
+    freq, dt = frequencies(rotary), tables.cuda()
+    got, flags = [], []
+    for calls in ([range(7)], [[1, 2], [0, 3, 4], [5, 6]]):
+        kp, vp = pool_for(cache, blocks, hkv, d), pool_for(cache, blocks, hkv, d)
+        out, err = nan_like(dq.contiguous()), err_flag()
+        for seqs in calls:
+            seqs = list(seqs)
+            a, b = sum(counts[:seqs[0]]), sum(counts[:seqs[-1] + 1])
+            if seqs == [0, 3, 4]:                                       # (its rows lie apart: those of 3 and 4)
+                a = sum(counts[:3])
+            rope_call(cache)(kp, vp, out[a:b], dq[a:b], dk[a:b], dv[a:b], freq, dt[seqs], i32([starts[x] for x in seqs]),
+                             cu_of([counts[x] for x in seqs]), interleaved, err_flag=err)
+        got.append((kp, vp, out))
+        flags.append(int(err))
+    assert flags[0] == flags[1] == pk.DEV_ERR_BAD_BLOCK | pk.DEV_ERR_BAD_POS
+    for x, y in zip(*got):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    ok = torch.tensor([0 <= a + i < 70304 and not (s == 4 and 70032 <= a + i < 70048)
+                       for s, (a, n) in enumerate(zip(starts, counts)) for i in range(n)])
+    out = got[0][2]
+    assert torch.equal(out.isnan().any(-1).any(-1).cpu(), ~ok)
+    at = torch.tensor([a + i for a, n in zip(starts, counts) for i in range(n)])
+    want, size = rotated(q, at, freq.cpu(), interleaved)
+    within(out[ok.cuda()], want[ok], (half_step(q.dtype) * want.abs() + 5e-7 * size + 1e-30)[ok], "queries")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_append_fp8_codes_are_those_of_the_plain_append(d):
+    # magnitudes over bf16's range, from row to row and within a row; infinities, NaN and zeros among the values
+    g = torch.Generator().manual_seed(41)
+    n, hkv = 1200, 2
+    k, v = ((torch.randn(n, hkv, d, generator=g) * 2.0 ** torch.randint(-126, 120, (n, hkv, 1), generator=g)
+             * 2.0 ** torch.randint(-12, 1, (n, hkv, d), generator=g)).bfloat16() for _ in range(2))
+    v[5, 0], v[6, 1, 3], v[7, 0, 9], v[8, 1, 0] = 0.0, float("inf"), float("nan"), -float("inf")
+    dk, dv = k.cuda(), v.cuda()
+    for counts in ([1] * n, [n]):                                       # row by row, block by block
+        blocks = sum((x + BLOCK - 1) // BLOCK for x in counts)
+        tables = torch.arange(blocks, dtype=torch.int32).view(len(counts), -1).cuda()
+        starts, cu = i32([0] * len(counts)), cu_of(counts)
+        pools = [[pool_for("fp8", blocks, hkv, d) for _ in (0, 1)] for _ in (0, 1)]
+        pk.rope_append_kv_fp8(*pools[0], None, None, dk, dv, frequencies(d), tables, starts, cu)
+        pk.append_kv_fp8(*pools[1], dk, dv, tables, starts, cu)
+        assert torch.equal(pools[0][1], pools[1][1])
+        if len(counts) == n:
+            # position 0 turns nothing: x1 1 - x2 0 is x1, but for an x1 of -0 (of the smallest
+            # magnitudes here, rounded to bf16), which becomes +0 where x2 0 is -0
+            for pool in (pools[0][0], pools[1][0]):
+                codes = pool[..., :BLOCK * d]
+                codes[codes == 0x80] = 0
+            assert bool((k == 0).any()) and torch.equal(pools[0][0], pools[1][0])
+
+
 @pytest.mark.parametrize("heads", HEADS)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (5, 1), (16, 0), (33, 4), (100, 17), (128, 70), (300, 0), (10**9, 0)])
 def test_prefill_sees_the_window_and_the_sinks_only(heads, window, sinks):
