@@ -61,7 +61,7 @@ class BmStats(ctypes.Structure):
 
 
 _lib = None
-_quick = None                   # csrc/pa_binding.c, where it was built: see the bindings that use it
+_quick = None                   # csrc/pa_binding.cpp, where it was built: see the bindings that use it
 
 
 def lib() -> ctypes.CDLL:
@@ -149,10 +149,10 @@ def lib() -> ctypes.CDLL:
         from . import _quick as quick
     except ImportError:
         return L
+    if quick.torch_version != torch.__version__:        # compiled for another torch: its tensors are laid out otherwise
+        return L
     quick.bind(*(ctypes.cast(f, p).value for f in (L.pa_rope_append_kv, L.pa_decode_attention_window,
-                                                   L.pa_prefill_attention_window)),
-               torch.Tensor, torch.float32, torch.bfloat16, torch.uint8, torch.int32, torch.float64,
-               torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+                                                   L.pa_prefill_attention_window)))
     _quick = quick
     return L
 
@@ -434,7 +434,7 @@ def prefill_attention(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, sca
 
 # Bindings of the rotary append and of the windowed attention.  A decode step calls them once per
 # layer, and a short step waits for them rather than for the GPU: a call whose arguments are all
-# as they should be, on the current device and stream, goes through csrc/pa_binding.c, which
+# as they should be, on the current device and stream, goes through csrc/pa_binding.cpp, which
 # makes the same checks.  Where that answers -1 (or was not built), the tensors are checked here,
 # in one expression, and only when it is false each is looked at again for the reason.
 _PLAIN_CODE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}

@@ -8,7 +8,9 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -20,9 +22,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpaged_kv.so")
-# the quick way through the Python bindings (csrc/pa_binding.c), for this interpreter
+# the quick way through the Python bindings (csrc/pa_binding.cpp), for this interpreter
 QUICK = os.path.join(PKG, "_quick.so")
 PYTHON_INCLUDE = sysconfig.get_paths()["include"]
+_torch = importlib.util.find_spec("torch")
+TORCH = _torch.submodule_search_locations[0] if _torch and _torch.submodule_search_locations else None
 
 SOURCES = ["pa_api.cu", "pa_decode.cu", "pa_append.cu", "pa_prefill.cu", "pa_noalloc.cu",
            "pa_rope.cu", "pa_window_decode.cu", "pa_block_manager.cpp"]
@@ -40,15 +44,25 @@ def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "pa.h"))
     files.append(os.path.abspath(__file__))
+    if TORCH is not None:
+        files.append(os.path.join(TORCH, "version.py"))      # (_quick.so is compiled for one torch)
     return files
 
 
-def _has_python_h() -> bool:
-    return os.path.exists(os.path.join(PYTHON_INCLUDE, "Python.h"))
+def _has_headers() -> bool:
+    """Those that csrc/pa_binding.cpp is compiled with: Python's and torch's."""
+    return TORCH is not None and all(os.path.exists(f) for f in (
+        os.path.join(PYTHON_INCLUDE, "Python.h"), os.path.join(TORCH, "include", "torch", "csrc", "autograd", "python_variable.h"),
+        os.path.join(TORCH, "lib", "libc10_cuda.so")))
+
+
+def _torch_version() -> str:
+    with open(os.path.join(TORCH, "version.py")) as f:
+        return re.search(r"__version__ = ['\"](.+?)['\"]", f.read()).group(1)
 
 
 def _stale() -> bool:
-    made = [LIB] + ([QUICK] if _has_python_h() else [])
+    made = [LIB] + ([QUICK] if _has_headers() else [])
     if not all(os.path.exists(f) for f in made):
         return True
     t = min(os.path.getmtime(f) for f in made)
@@ -74,15 +88,20 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
 
 
 def _compile_quick() -> None:
-    """csrc/pa_binding.c with the C compiler; without Python's headers the bindings do without."""
-    if not _has_python_h():
+    """csrc/pa_binding.cpp with the C++ compiler; without the headers the bindings do without."""
+    if not _has_headers():
         return
     tmp = QUICK + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-fPIC", "-shared", "-I", INCLUDE, "-I", PYTHON_INCLUDE,
-           os.path.join(CSRC, "pa_binding.c"), "-o", tmp]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f'-DPA_TORCH_VERSION="{_torch_version()}"', "-I", INCLUDE,
+           "-I", PYTHON_INCLUDE, "-isystem", os.path.join(TORCH, "include"),
+           "-isystem", os.path.join(TORCH, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+           os.path.join(CSRC, "pa_binding.cpp"), "-L", os.path.join(TORCH, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on pa_binding.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on pa_binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, QUICK)
 
 
@@ -91,7 +110,8 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        quick = ex.submit(_compile_quick)
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [_nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
@@ -99,7 +119,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _compile_quick()
+    quick.result()
     return LIB
 
 
