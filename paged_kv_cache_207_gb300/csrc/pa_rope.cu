@@ -43,17 +43,25 @@ struct RParams {
     int max_blocks, S, total, num_blocks, Hq, Hkv, half;       // half = rotary_dim / 2
 };
 
-constexpr int kThreads = 256;         // of a tile's CTA
+// Threads of a tile's CTA: its 16 rows times a head's items, or more.  128 against 256, 32 / 8
+// heads of 128: 37 chunks of 1 to 131, bf16 14.0 / 17.5 us and FP8 17.2 / 22.0; 16 of 512, 34.8 /
+// 36.2 and 38.4 / 40.6 (the SMs' loads come out more even).
+constexpr int tile_threads(pa_dtype t, int head_dim) { return t == PA_F32 && head_dim == 128 ? 256 : 128; }
 constexpr int kRowThreads = 128;      // of a row's
 // A call goes row by row (a CTA each, no row waits for another) or tile by tile (a pool's tile
 // is written in whole runs).  Rows are faster for few of them, and for short chunks, whose
 // tiles are mostly empty; runs matter more where a value is a byte.  Rows against tiles, 32 / 8
-// heads of 128, us: one chunk of 256 bf16 2.9 / 3.7, FP8 6.2 / 7.3; of 1000 bf16 7.1 / 5.8, FP8
-// 16.4 / 10.0; 256 chunks of 8, 12.5 / 19.0 and 27.3 / 31.0; 64 of 16, 7.0 / 8.3 and 16.3 / 15.3;
-// 100 of 1 to 40, 11.3 / 16.0 and 28.1 / 22.0; 16 of 512, 40.3 / 36.2 and 99.4 / 40.6.
-constexpr int kRowsAlone = 512;        // up to so many rows in all
-constexpr int kTileMinRows = 32;       // and below so many per sequence, of bf16 and f32
-constexpr int kTileMinRowsQuantised = 16;
+// heads of 128, us: one chunk of 256 bf16 3.0 / 3.5, FP8 6.3 / 6.3; of 500 bf16 5.0 / 4.3, FP8
+// 13.2 / 6.5; 256 chunks of 8, 12.6 / 17.6 and 27.2 / 28.1; 64 of 16, 7.0 / 7.7 and 16.2 / 13.3;
+// 100 of 1 to 40, 11.2 / 14.2 and 27.2 / 19.3; 256 of 16, 24.5 / 24.1 and 51.6 / 34.8; 16 of 512,
+// 40.3 / 34.8 and 99.4 / 38.4.
+constexpr bool quantised(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_FP4_E2M1; }
+constexpr int rows_alone(pa_dtype t) { return quantised(t) ? 256 : 512; }     // up to so many rows in all
+constexpr int tile_min_rows(pa_dtype t) { return quantised(t) ? 16 : 32; }    // and below so many per sequence
+// Heads of a tile's thread, at least and at most (four against two and six, 14 / 2 heads of 64,
+// FP8, 37 chunks of 1 to 131: 6.5, 7.3 and 6.8 us; 16 chunks of 512, 32 / 8 of 128, bf16, 24
+// and 48 heads: 34.8 and 39.2).
+constexpr int kLeastHeads = 4, kMostHeads = 36;
 constexpr int kTileHeads = 3;          // heads of a thread that are loaded together (four spill)
 
 // A frequency in radians per position as turns * 2^64, modulo 2^64.  Below 1024 in integers
@@ -450,6 +458,7 @@ __device__ __forceinline__ int tile_base(const RParams& p, int s) {
 
 // The CTA's tile, the same in every thread; false: none, or at no position of the table
 // (flagged).  The block is checked by the caller, when its load has had time to land.
+template <int NT>
 __device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
     const int tid = threadIdx.x;
     // the sequence if all have as many rows, and its place with it: often right, one round trip
@@ -458,7 +467,7 @@ __device__ __forceinline__ bool find_tile(const RParams& p, int t, Tile& out) {
     long long start = __ldg(p.start_pos + lo);
     const bool guessed = t >= (first >> 4) + 2 * lo && (lo + 1 == p.S || t < (next >> 4) + 2 * (lo + 1));
     if (!guessed) {
-        lo = last_from<kThreads>(0, p.S, t, [&](int s) { return tile_base(p, s); });
+        lo = last_from<NT>(0, p.S, t, [&](int s) { return tile_base(p, s); });
         first = __ldg(p.cu + lo);
         next = __ldg(p.cu + lo + 1);
         start = __ldg(p.start_pos + lo);
@@ -552,21 +561,22 @@ __device__ __forceinline__ void put_fp8_values(const RParams& p, const Tile& til
 }
 
 template <int D, pa_dtype T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RParams p) {
+__global__ void __launch_bounds__(tile_threads(T, D), 512 / tile_threads(T, D)) rope_append_tile_kernel(const RParams p) {
     constexpr int E = T == PA_F32 ? 4 : 8;
     constexpr int PH = D / (2 * E);
-    constexpr int GROUPS = kThreads / (kTileRows * PH);      // threads of a (row, item), a share of the heads each
+    constexpr int NT = tile_threads(T, D), NW = NT / 32;
+    constexpr int GROUPS = NT / (kTileRows * PH);      // threads of a (row, item), a share of the heads each
     constexpr int PAD = D / 2 + 2;                           // (rows on different banks)
     __shared__ __align__(16) float2 cs[kTileRows * PAD];
     __shared__ uint64_t turns[D / 2];
-    __shared__ __align__(16) uint32_t sm_v[T == PA_FP8_E4M3 ? 8 * (D / 4) * 16 : 1];
+    __shared__ __align__(16) uint32_t sm_v[T == PA_FP8_E4M3 ? NW * (D / 4) * 16 : 1];
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x;
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu<kThreads>(p);
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_cu<NT>(p);
     if (tid < p.half) turns[tid] = fixed_turns(p.inv_freq[tid]);
     Tile tile;
-    if (!find_tile(p, blockIdx.x, tile)) return;
+    if (!find_tile<NT>(p, blockIdx.x, tile)) return;
     const int share = blockIdx.y * GROUPS, stride = gridDim.y * GROUPS;
     auto row_at = [&](int slot) { return (long long)(tile.row0 + slot - tile.lo); };
     // Queries: items on adjacent lanes.  N heads are loaded while the N before them are turned
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RPa
     load_q(0, a0, b0);
     __syncthreads();
     const int rows = tile.hi - tile.lo;
-    for (int i = tid; i < rows * p.half; i += kThreads) {
+    for (int i = tid; i < rows * p.half; i += NT) {
         const int r = i / p.half, f = i - r * p.half;
         cs[(tile.lo + r) * PAD + f] = cos_sin(turns[f] * (uint64_t)(tile.pos0 + tile.lo + r));
     }
@@ -675,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RPa
         constexpr bool FP8 = T == PA_FP8_E4M3;
         // FP8 values: by warps, from the last share on, loaded while the keys are turned
         const int warp = tid >> 5;
-        int vh = (gridDim.y - 1 - blockIdx.y) * 8 + warp;
+        int vh = (gridDim.y - 1 - blockIdx.y) * NW + warp;
         uint4 v[D / 16];
         if constexpr (FP8) load_values<D>(p, tile, vh, v);
 #pragma unroll
@@ -701,9 +711,9 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RPa
             }
         }
         if constexpr (FP8) {
-            for (; vh < p.Hkv; vh += gridDim.y * 8) {
+            for (; vh < p.Hkv; vh += gridDim.y * NW) {
                 put_fp8_values<D>(p, tile, vh, v, sm_v + warp * (D / 4) * 16);
-                load_values<D>(p, tile, vh + gridDim.y * 8, v);
+                load_values<D>(p, tile, vh + gridDim.y * NW, v);
             }
         }
     }
@@ -711,16 +721,18 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_tile_kernel(const RPa
 
 template <int D, pa_dtype T, bool INTERLEAVED>
 cudaError_t launch_rope(const RParams& p, cudaStream_t stream) {
-    const int least = T == PA_F32 || T == PA_BF16 ? kTileMinRows : kTileMinRowsQuantised;
-    const bool tiles = p.total > kRowsAlone && p.total >= least * (long long)p.S;
+    const bool tiles = p.total > rows_alone(T) && p.total >= tile_min_rows(T) * (long long)p.S;
     cudaLaunchConfig_t cfg = {};
-    // A tile's heads are shared by several CTAs while that finds idle SMs (two CTAs fit on one):
-    // 512 full tiles of 32 + 16 heads of 128 take 35.6 us with one CTA each and 37.7 with two; 153,
-    // 16.7, 12.5 with two and 14.5 with three (FP8 19.1, 15.3, 18.5).
+    // A tile's heads are shared by several CTAs while all of them fit the GPU (512 threads of an
+    // SM) and a thread keeps kLeastHeads; by two where a thread of 128 had more than kMostHeads.
+    constexpr int NT = tile_threads(T, D), GROUPS = NT / (kTileRows * (D / (T == PA_F32 ? 8 : 16)));
     const long long touched = (p.total + (kTileRows - 1ll) * p.S) / kTileRows;      // of chunks that begin anywhere
-    const int shares = (int)std::max(1ll, std::min(8ll, 308 / touched));
+    const int heads = (p.Hq + 2 * p.Hkv) / GROUPS;                                  // of a thread that has a share alone
+    const long long most = std::max(1, std::min(8, heads / kLeastHeads));
+    const long long at_once = 308ll * 256 / NT / touched, least = NT == 128 && heads > kMostHeads ? 2 : 1;
+    const int shares = (int)std::max(least, std::min(most, at_once));
     cfg.gridDim = tiles ? dim3((unsigned)(p.total / kTileRows + 2ll * p.S), shares) : dim3((unsigned)p.total);
-    cfg.blockDim = dim3(tiles ? kThreads : kRowThreads);
+    cfg.blockDim = dim3(tiles ? tile_threads(T, D) : kRowThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
