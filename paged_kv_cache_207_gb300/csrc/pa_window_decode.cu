@@ -59,9 +59,14 @@ constexpr int ctas_for(pa_dtype t, int head_dim) {
 // 81.0 / 77.1).
 constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 32 : 16; }
 // Pairs of blocks for each warp below which a sequence is one part, since joining parts costs
-// about 1.3 us (6 against 4, A, window 512, one sequence: bf16 7.5 / 8.4 us, FP8 8.4 / 9.1, but
-// f32 14.6 / 13.0).
-constexpr int min_pairs(pa_dtype t) { return t == PA_F32 ? 4 : 6; }
+// about 1 us (4 against 5 and 6: A, bf16, window 512, one sequence 7.3 / 7.6, 16 sequences 10.3 /
+// 8.2; window 700, one sequence 7.5 / 7.5 / 8.8; f32, window 512, one sequence 13.0 / 14.6).
+constexpr int min_pairs(pa_dtype t) { return t == PA_F32 ? 4 : 5; }
+// Whether clusters are to leave an SM to each CTA: one of eight warps fills it (B, window 2048, 24
+// sequences, an SM each against as many as fit: bf16 13.0 / 14.7 us, FP8 13.4 / 15.0; 32 / 8 heads
+// of 64, window 4096, bf16, 16 sequences, 25.1 / 29.2; but FP4, window 8192, 48 sequences of B, 46.7
+// / 38.4).
+constexpr bool one_each(pa_dtype t, int head_dim) { return head_dim == 64 && (t == PA_BF16 || t == PA_FP8_E4M3); }
 // Parts, at most.  Clusters of up to 8 find room in every part of the GPU; 16 pay only where an
 // SM holds three CTAs that are long (16 against 8: f32, 12 heads of 64, window 4096, one
 // sequence 14.2 / 15.6 us; A, window 4096, 8 sequences: bf16 27.8 / 25.5, f32 54.5 / 50.5;
@@ -628,11 +633,14 @@ __device__ __forceinline__ bool aborted(const int32_t* err) {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// a float of another CTA of the cluster, at this CTA's shared address `addr`
-__device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
+// another CTA's address of what this CTA has at shared address `addr`, and a float there
+__device__ __forceinline__ uint32_t peer_at(uint32_t addr, int rank) {
     uint32_t at;
-    float x;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float peer_f32(uint32_t at) {
+    float x;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
     return x;
 }
@@ -689,7 +697,7 @@ __device__ __forceinline__ void store_out(void* out, size_t at, float x) {
 }
 
 template <template <int> class Cache, int D, int NW, int NST>
-__global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : ctas_for(Cache<D>::TYPE, D)) window_decode_kernel(const WParams p) {
+__global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_decode_kernel(const WParams p) {
     using C = Cache<D>;
     using L = Layout<C, D, NW, NST>;
     constexpr int KS = C::KS, TILE = C::TILE;
@@ -732,7 +740,11 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
     const uint64_t pol = l2_policy_evict_first();
     // Pair i's tiles into its stage: `which` 0 K, 1 V.  have: 2 bits per stage, the blocks that
     // were copied (a table entry that names no block is flagged and left out).
-    uint32_t have = 0, phase = 0;              // phase: 2 bits per stage (K, V)
+    // state: 2 bits per stage (K, V), the phase that its barrier's next copy ends; from bit 16 and
+    // from bit 24 on a bit per stage, whether such a copy of K, of V is in flight.
+    uint32_t have = 0, state = 0;
+    auto k_out = [](int st) { return 1u << (16 + st); };
+    auto v_out = [](int st) { return 1u << (24 + st); };
     int32_t blk_v[NST][2];                     // pair's blocks, kept from K's issue to V's
     auto issue = [&](int i, int st, int which) {
         if (which == 0) {
@@ -753,9 +765,9 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
     };
     auto landed = [&](int st, int which) -> bool {
         const uint32_t bit = 2 * st + which;
-        const bool ok = mbar_wait_bounded(bar0 + st * 16 + which * 8, (phase >> bit) & 1u, kWaitLimitNs);
+        const bool ok = mbar_wait_bounded(bar0 + st * 16 + which * 8, (state >> bit) & 1u, kWaitLimitNs);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        phase ^= 1u << bit;
+        state ^= 1u << bit;
         return true;
     };
 #pragma unroll
@@ -827,14 +839,13 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
         cache.reset();
     };
     const int part_pairs = p.part_len / (2 * NW);      // of a warp
-    int part_left = mine > 1 ? part_pairs : INT_MAX, ends = mine - 1;
+    const int last_end = (mine - 1) * part_pairs;
+    int end_at = mine > 1 ? part_pairs : INT_MAX;      // pair before which a part ends (the last one: never)
     bool failed = false;
-    uint32_t k_out = 0, v_out = 0;             // stages whose copies of the next pairs are in flight
 #pragma unroll
     for (int st = 0; st < NST; ++st)
         if (st < npairs && ((have >> (2 * st)) & 3u)) {
-            k_out |= 1u << st;
-            v_out |= 1u << st;
+            state |= k_out(st) | v_out(st);
         }
     for (int i0 = 0; i0 < npairs && !failed; i0 += NST) {
 #pragma unroll
@@ -842,19 +853,17 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
             const int i = i0 + st;
             if (i >= npairs) break;
             const bool more = i + NST < npairs;
-            if (part_left == 0) {
+            if (i == end_at) {
                 end_part();
-                part_left = --ends > 0 ? part_pairs : INT_MAX;
+                end_at = end_at < last_end ? end_at + part_pairs : INT_MAX;
             }
-            --part_left;
             const uint32_t h = (have >> (2 * st)) & 3u;
             if (h == 0u) {                     // no block of the pair is in the pool
                 if (more) {
                     issue(i + NST, st, 0);
                     issue(i + NST, st, 1);
                     if ((have >> (2 * st)) & 3u) {
-                        k_out |= 1u << st;
-                        v_out |= 1u << st;
+                        state |= k_out(st) | v_out(st);
                     }
                 }
                 continue;
@@ -872,7 +881,7 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
                 failed = true;
                 break;
             }
-            k_out &= ~(1u << st);
+            state &= ~k_out(st);
             float sc[2][4];
             cache.scores(kt, p.scale_log2, sc);
             float t0 = -INFINITY, t1 = -INFINITY;
@@ -914,12 +923,12 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
             run.rescale = __any_sync(0xffffffffu, run.al0 != 1.f || run.al1 != 1.f);
             if (more) issue(i + NST, st, 0);
             const uint32_t h_next = more ? (have >> (2 * st)) & 3u : 0u;
-            if (h_next) k_out |= 1u << st;
+            if (h_next) state |= k_out(st);
             if (!landed(st, 1)) {
                 failed = true;
                 break;
             }
-            v_out &= ~(1u << st);
+            state &= ~v_out(st);
             if (!full) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -930,18 +939,18 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
             cache.pv(kt + 2 * TILE, pr, run, o);
             __syncwarp();
             if (more) issue(i + NST, st, 1);
-            if (h_next) v_out |= 1u << st;
+            if (h_next) state |= v_out(st);
         }
     }
     if (failed) {
         // drain every copy still in flight before the shared memory is reused
         if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         for (int st = 0; st < NST; ++st) {
-            if ((k_out >> st) & 1u) mbar_wait_bounded(bar0 + st * 16, (phase >> (2 * st)) & 1u, kWaitLimitNs);
-            if ((v_out >> st) & 1u) mbar_wait_bounded(bar0 + st * 16 + 8, (phase >> (2 * st + 1)) & 1u, kWaitLimitNs);
+            if (state & k_out(st)) mbar_wait_bounded(bar0 + st * 16, (state >> (2 * st)) & 1u, kWaitLimitNs);
+            if (state & v_out(st)) mbar_wait_bounded(bar0 + st * 16 + 8, (state >> (2 * st + 1)) & 1u, kWaitLimitNs);
         }
     }
-    const int results = p.per ? mine : 1;
+    const int results = p.per ? min(p.per, parts - (int)blockIdx.x * p.per) : 1;
     do end_part();                             // (a warp without blocks in the last parts: empty ones)
     while (p.per && at_slot < results * slot);
     const bool bad = __syncthreads_or(failed || skip), cta_skip = __syncthreads_or(skip);
@@ -985,35 +994,46 @@ __global__ void __launch_bounds__(NW * 32, Cache<D>::TYPE == PA_FP4_E2M1 ? 0 : c
     cluster_arrive();
     cluster_wait();
     const int ctas = (parts + p.per - 1) / p.per;
-    const uint32_t o_at = smem_u32(sm_o), m_at = smem_u32(sm_m), l_at = smem_u32(sm_l);
+    // (the loads of JB parts are under way together: 2 of 8 round trips, a call 0.9 us shorter)
+    constexpr int JB = (C::TYPE == PA_FP4_E2M1 ? 8 : 16) / NW;       // (FP4: registers)
+    const uint32_t m_from = NW * outs * 4, l_from = m_from + NW * p.G * 4;
     for (int i = blockIdx.x * (NW * 32) + threadIdx.x; i < G2 * KS * 32; i += ctas * (NW * 32)) {
         const int c = i / (KS * 32), g = 2 * c + (i >> 1 & 1), d = i / 32 % KS * 16 + i / 4 % 8 + (i & 1) * 8;
-        const uint32_t at = o_at + (c * L::CS + i % (KS * 32)) * 4;
         if (g >= p.G) continue;
-        Merge<NW> m;
-        float o_w[NW];
+        Partial a[NW];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            Partial a{-INFINITY, 0.f, 0.f};
-            int rank = 0, k = 0;
-#pragma unroll 4
-            for (int j = 0; j < parts; ++j) {
-                const uint32_t from = k * slot * 4;
-                fold(a, Partial{peer_f32(m_at + from + (w * p.G + g) * 4, rank), peer_f32(l_at + from + (w * p.G + g) * 4, rank),
-                                peer_f32(at + from + w * outs * 4, rank)});
+        for (int w = 0; w < NW; ++w) a[w] = Partial{-INFINITY, 0.f, 0.f};
+        int rank = 0, k = 0;
+        for (int j = 0; j < parts; j += JB) {
+            Partial x[JB][NW];
+#pragma unroll
+            for (int jj = 0; jj < JB; ++jj) {
+                const uint32_t at = peer_at(smem_u32(sm_o), rank) + k * slot * 4;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    x[jj][w] = Partial{-INFINITY, 0.f, 0.f};
+                    if (j + jj < parts)
+                        x[jj][w] = Partial{peer_f32(at + m_from + (w * p.G + g) * 4), peer_f32(at + l_from + (w * p.G + g) * 4),
+                                           peer_f32(at + (w * outs + c * L::CS + i % (KS * 32)) * 4)};
+                }
                 if (++k == p.per) {
                     k = 0;
-                    ++rank;
+                    rank = min(rank + 1, ctas - 1);
                 }
             }
-            m.set(w, a.m, a.l);
-            o_w[w] = a.o;
-        }
-        m.weigh();
-        float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) x = m.add(x, w, o_w[w]);
-        if (!cta_skip) store_out<typename C::Out>(p.out, (row0 + g) * D + d, m.result(x));
+            for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+                for (int w = 0; w < NW; ++w) fold(a[w], x[jj][w]);
+        }
+        Merge<NW> m;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) m.set(w, a[w].m, a[w].l);
+        m.weigh();
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) y = m.add(y, w, a[w].o);
+        if (!cta_skip) store_out<typename C::Out>(p.out, (row0 + g) * D + d, m.result(y));
     }
     // no CTA leaves while another may still read its shared memory
     cluster_arrive();
@@ -1069,7 +1089,7 @@ long long clusters_at_once(int dev, int ctas, int threads, int smem) {
 }
 
 template <void (*Kernel)(const WParams)>
-cudaError_t launch(WParams p, int num_seqs, int threads, int smem, int smem_result, cudaStream_t stream) {
+cudaError_t launch(WParams p, int num_seqs, int threads, bool one_each, int smem, int smem_result, cudaStream_t stream) {
     const int parts = p.parts;
     int dev = 0, sms = 1;
     const cudaError_t e = prepare_kernel<Kernel>(dev, sms);
@@ -1085,7 +1105,8 @@ cudaError_t launch(WParams p, int num_seqs, int threads, int smem, int smem_resu
     for (int per = 1; per < parts; per *= 2) {
         const int bytes = smem + (per - 1) * smem_result;
         if (bytes > kSmemMax) break;
-        if (pairs <= clusters_at_once<Kernel>(dev, (parts + per - 1) / per, threads, bytes)) {
+        const int ctas = (parts + per - 1) / per;
+        if ((!one_each || pairs * ctas <= sms) && pairs <= clusters_at_once<Kernel>(dev, ctas, threads, bytes)) {
             p.per = per;
             break;
         }
@@ -1124,7 +1145,7 @@ template <template <int> class Cache, int D, int NST>
 cudaError_t launch_cache(const WParams& p, int num_seqs, cudaStream_t stream) {
     constexpr int NW = warps_for(Cache<D>::TYPE, D);
     using L = Layout<Cache<D>, D, NW, NST>;
-    return launch<window_decode_kernel<Cache, D, NW, NST>>(p, num_seqs, NW * 32, L::bytes(p.G, 1),
+    return launch<window_decode_kernel<Cache, D, NW, NST>>(p, num_seqs, NW * 32, one_each(Cache<D>::TYPE, D), L::bytes(p.G, 1),
                                                            L::bytes(p.G, 2) - L::bytes(p.G, 1), stream);
 }
 
