@@ -1,5 +1,9 @@
 """The rotary append and the sliding-window attention against a plain 64-bit implementation
 (tests/_window_common.py, which derives the tolerances)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -113,6 +117,40 @@ def test_decode_on_two_streams_and_in_two_graphs_at_once(cache):
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+FIRST_IN_A_CAPTURE = """
+import sys, torch
+sys.path.insert(0, "tests")
+import paged_kv_cache_207_gb300 as pk
+from _window_common import Cache, nan_like
+c = Cache("bf16", [2000, 700], (8, 2, 128), seed=3)
+q, lens = c.queries(2).cuda(), torch.tensor([2000, 700], dtype=torch.int32, device="cuda")
+kn, vn = torch.randn(2, 2, 2, 128, device="cuda").bfloat16()
+start, cu = lens - 1, torch.arange(3, dtype=torch.int32, device="cuda")
+freq = 10000.0 ** (-torch.arange(0, 128, 2, dtype=torch.float64, device="cuda") / 128)
+tables, out, turned = c.tables.cuda(), nan_like(q), torch.empty_like(q)
+def step():
+    pk.rope_append_kv(c.kp, c.vp, turned, q, kn, vn, freq, tables, start, cu)
+    pk.decode_attention_window(out, turned, c.kp, c.vp, tables, lens, 0.1, 1500, 4)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+out.fill_(float("nan"))
+step()
+torch.cuda.synchronize()
+assert torch.equal(out, got) and not bool(got.isnan().any())
+"""
+
+
+def test_first_call_of_a_process_is_captured():
+    # (what the library asks the runtime once, clusters' room among it, is asked within the capture)
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_CAPTURE], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("cache", CACHES)
