@@ -994,7 +994,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
     cluster_arrive();
     cluster_wait();
     const int ctas = (parts + p.per - 1) / p.per;
-    // (the loads of JB parts are under way together: 2 of 8 round trips, a call 0.9 us shorter)
+    // (the loads of JB parts of all warps are under way together: 14 / 2 heads of 64, window 1500, one
+    // sequence 8.5 -> 7.2 us)
     constexpr int JB = (C::TYPE == PA_FP4_E2M1 ? 8 : 16) / NW;       // (FP4: registers)
     const uint32_t m_from = NW * outs * 4, l_from = m_from + NW * p.G * 4;
     for (int i = blockIdx.x * (NW * 32) + threadIdx.x; i < G2 * KS * 32; i += ctas * (NW * 32)) {
