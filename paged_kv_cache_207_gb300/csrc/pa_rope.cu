@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_append_kernel(const RParams 
 // so that a pool's tile is written in whole runs and the place is looked up once.  Tile t
 // belongs to the last sequence s with cu[s] / 16 + 2 s <= t (a sequence of n rows touches at
 // most n / 16 + 2 blocks, so its tiles stay below the next one's): no counts are summed, and a
-// 256-way search finds s.  blockIdx.y picks a share of the heads.
+// search by all threads finds s.  blockIdx.y picks a share of the heads.
 //
 // A thread keeps one item index u of one row, with its cosines and sines in registers, and
 // goes through the heads of its share: keys with the rows on adjacent lanes (16 slots of a
