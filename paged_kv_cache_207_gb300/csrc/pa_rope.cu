@@ -48,12 +48,17 @@ struct RParams {
 // 36.2 and 38.4 / 40.6 (the SMs' loads come out more even).
 constexpr int tile_threads(pa_dtype t, int head_dim) { return t == PA_F32 && head_dim == 128 ? 256 : 128; }
 constexpr int kRowThreads = 128;      // of a row's
+// Items of a row's thread that are loaded together (32 / 8 heads of 128 have three for each; two
+// leave the quantised types' registers), and CTAs of an SM that the registers are bounded for (7
+// against what comes of it, 6 or 9: 1024 rows of 32 / 8 heads, bf16 5.5 / 7.0 us, f32 9.5 / 10.6).
+constexpr int row_items(pa_dtype t, int head_dim) { return head_dim == 64 || (t != PA_F32 && t != PA_BF16) ? 2 : 3; }
+constexpr int kRowCtas = 7;
 // A call goes row by row (a CTA each, no row waits for another) or tile by tile (a pool's tile
 // is written in whole runs).  Rows are faster for few of them, and for short chunks, whose
 // tiles are mostly empty; runs matter more where a value is a byte.  Rows against tiles, 32 / 8
-// heads of 128, us: one chunk of 256 bf16 3.0 / 3.5, FP8 6.3 / 6.3; of 500 bf16 5.0 / 4.3, FP8
-// 13.2 / 6.5; 256 chunks of 8, 12.6 / 17.6 and 27.2 / 28.1; 64 of 16, 7.0 / 7.7 and 16.2 / 13.3;
-// 100 of 1 to 40, 11.2 / 14.2 and 27.2 / 19.3; 256 of 16, 24.5 / 24.1 and 51.6 / 34.8; 16 of 512,
+// heads of 128, us: one chunk of 256 bf16 3.0 / 3.5, FP8 6.3 / 6.3; of 500 bf16 4.1 / 4.3, FP8
+// 13.2 / 6.5; 256 chunks of 8, 11.6 / 17.6 and 27.4 / 28.2; 64 of 16, 5.5 / 7.7 and 16.2 / 13.4;
+// 100 of 1 to 40, 11.0 / 14.2 and 27.2 / 19.1; 256 of 16, 24.0 / 24.2 and 51.6 / 34.8; 16 of 512,
 // 40.3 / 34.8 and 99.4 / 38.4.
 constexpr bool quantised(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_FP4_E2M1; }
 constexpr int rows_alone(pa_dtype t) { return quantised(t) ? 256 : 512; }     // up to so many rows in all
@@ -351,10 +356,10 @@ __device__ __forceinline__ bool find_row(const RParams& p, int row, int& pos_out
 // row's data do not depend on its place, so the first N items of a thread are under way while
 // the place is looked up.  T: the pool's type.
 template <int D, pa_dtype T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRowThreads) rope_append_kernel(const RParams p) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) rope_append_kernel(const RParams p) {
     constexpr int E = T == PA_F32 ? 4 : 8;       // elements of a piece (the rows are f32 or bf16)
     constexpr int PH = D / (2 * E);              // items of a head
-    constexpr int N = 3;
+    constexpr int N = row_items(T, D);
     __shared__ __align__(16) float2 cs[D / 2];
     // the rows may come from the kernel before (a projection), and the pools be in use by it
     grid_dependency_wait();
