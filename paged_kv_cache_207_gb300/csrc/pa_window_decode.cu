@@ -106,7 +106,7 @@ __device__ __forceinline__ void rescale_rows(const Running& run, float (&o)[KS][
 
 // The cache types.  A lane is r = lane / 4, c = lane % 4; of each block it holds the scores of
 // two tokens, lo() and hi(), for heads 2c and 2c + 1: s[0..1] and s[2..3].  o[mi] accumulates
-// dims 16 mi + r, + 8 of the same heads.
+// dims 16 mi + r, + 8 of the same heads.  finish() gives the factor that is left on o.
 
 template <int D>
 struct Bf16Cache {
@@ -178,15 +178,19 @@ struct Bf16Cache {
         }
     }
     __device__ __forceinline__ void reset() {}
-    __device__ __forceinline__ void finish(Running&, float (&)[KS][4]) {}
+    __device__ __forceinline__ float finish(float (&)[KS][4]) const { return 1.f; }
 };
 
 // E4M3 records: codes become f16 in registers (exact), the products run in f16.
 //   K: ldmatrix gives a lane 4 consecutive dims of one token, so the dot product's index is
 //   permuted alike in the query; the tokens come in the order lo() = 4 (r / 2) + r % 2,
 //   hi() = lo() + 2, which lines the transposed probabilities up with V's 16-token rows.
-//   The key's scale multiplies its scores; the value's multiplies its probability, with 2^8
-//   to keep the product in f16's normal range (taken out of the sums at the end).
+//   The key's scale multiplies its scores; the value's multiplies its probability, with a power
+//   of two c that keeps the product in f16's range whatever the values' size: below 2^12 at the
+//   largest scale of the part's first pair, so that three octaves more need no other c (a pair
+//   with a larger scale lowers c and rescales the accumulators).  f16 because its 11 bits keep
+//   a product eight times as exact as bf16 would; one below its normal range is off by at most
+//   2^-25 / c, 2^-36 of the largest scale so far.
 template <int D>
 struct Fp8Cache {
     static constexpr pa_dtype TYPE = PA_FP8_E4M3;
@@ -194,10 +198,10 @@ struct Fp8Cache {
     static constexpr int TILE = 16 * D + 64;
     static constexpr int KS = D / 16;
     static constexpr int SCRATCH = 0;
-    static constexpr float kPScale = 256.f;
     uint32_t qb[KS][2];
+    float unit;                                               // c; 0: the part has no pair yet
     int lane, r, c;
-    __device__ __forceinline__ Fp8Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) {}
+    __device__ __forceinline__ Fp8Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) { reset(); }
     __device__ __forceinline__ int lo() const { return 4 * (r >> 1) + (r & 1); }
     __device__ __forceinline__ int hi() const { return lo() + 2; }
     __device__ __forceinline__ void load_q(const void* q, size_t row0, int G) {
@@ -256,10 +260,32 @@ struct Fp8Cache {
         uint32_t pb[2][2];
         run.l0 = run.l0 * run.al0 + ((pr[0][0] + pr[0][2]) + (pr[1][0] + pr[1][2]));
         run.l1 = run.l1 * run.al1 + ((pr[0][1] + pr[0][3]) + (pr[1][1] + pr[1][3]));
+        float v[2][2];                                        // the scales of the lane's tokens
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const float* vs = reinterpret_cast<const float*>(vt + b * TILE + 16 * D);
-            const float v0 = vs[lo()] * kPScale, v1 = vs[hi()] * kPScale;
+            v[b][0] = vs[lo()];
+            v[b][1] = vs[hi()];
+        }
+        float top = fmaxf(fmaxf(fabsf(v[0][0]), fabsf(v[0][1])), fmaxf(fabsf(v[1][0]), fabsf(v[1][1])));
+        if (__any_sync(0xffffffffu, unit == 0.f || top * unit >= 32768.f)) {       // rare after a part's first pair
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            // 2^(e - 127) <= top < 2^(e - 126): top c from 2^11 on, below 2^12
+            const int e = (int)(__float_as_uint(top) >> 23);
+            const float was = unit;
+            unit = exp2i(min(138 - e, 127));
+            if (was > 0.f) {
+                const float f = exp2i(exponent(unit) - exponent(was));       // exact
+#pragma unroll
+                for (int mi = 0; mi < KS; ++mi)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[mi][x] *= f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float v0 = v[b][0] * unit, v1 = v[b][1] * unit;
             pb[b][0] = movmatrix_trans(pack_f16x2(pr[b][0] * v0, pr[b][1] * v0));
             pb[b][1] = movmatrix_trans(pack_f16x2(pr[b][2] * v1, pr[b][3] * v1));
         }
@@ -279,11 +305,10 @@ struct Fp8Cache {
             }
         }
     }
-    __device__ __forceinline__ void reset() {}
-    __device__ __forceinline__ void finish(Running& run, float (&)[KS][4]) {
-        run.l0 *= kPScale;                       // the products carry the same factor
-        run.l1 *= kPScale;
-    }
+    // log2 of a power of two
+    static __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+    __device__ __forceinline__ void reset() { unit = 0.f; }
+    __device__ __forceinline__ float finish(float (&)[KS][4]) const { return unit > 0.f ? exp2i(-exponent(unit)) : 1.f; }
 };
 
 // The first product of a sum: D = A B.
@@ -436,7 +461,7 @@ struct Fp4Cache {
             }
         }
     }
-    __device__ __forceinline__ void finish(Running&, float (&o)[KS][4]) {
+    __device__ __forceinline__ float finish(float (&o)[KS][4]) const {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const float f = exp2i(-c_exp(__shfl_sync(0xffffffffu, ref, b)));
@@ -446,6 +471,7 @@ struct Fp4Cache {
                 o[2 * b + 1][x] *= f;
             }
         }
+        return 1.f;
     }
 };
 
@@ -560,7 +586,7 @@ struct F32Cache {
         }
     }
     __device__ __forceinline__ void reset() {}
-    __device__ __forceinline__ void finish(Running&, float (&)[KS][4]) {}
+    __device__ __forceinline__ float finish(float (&)[KS][4]) const { return 1.f; }
 };
 
 // Shared memory: the warps' stages, each the K tiles then the V tiles of a pair of blocks;
@@ -808,16 +834,17 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
             run.l0 += __shfl_xor_sync(0xffffffffu, run.l0, x);
             run.l1 += __shfl_xor_sync(0xffffffffu, run.l1, x);
         }
-        cache.finish(run, o);
+        const float factor = cache.finish(o);
         const int r = lane >> 2, c = lane & 3;
         const Fold f0 = fold_factors(all_m0, run.m0), f1 = fold_factors(all_m1, run.m1);
+        const Fold o0{f0.m, f0.a, f0.s * factor}, o1{f1.m, f1.a, f1.s * factor};
         if (c < G2) {
             float4* at = reinterpret_cast<float4*>(sm_o + at_slot + warp * outs + c * L::CS) + r;
 #pragma unroll
             for (int mi = 0; mi < KS; ++mi, at += 8) {
                 const float4 was = folded ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-                *at = make_float4(fold_add(f0, was.x, o[mi][0]), fold_add(f0, was.y, o[mi][2]),
-                                  fold_add(f1, was.z, o[mi][1]), fold_add(f1, was.w, o[mi][3]));
+                *at = make_float4(fold_add(o0, was.x, o[mi][0]), fold_add(o0, was.y, o[mi][2]),
+                                  fold_add(o1, was.z, o[mi][1]), fold_add(o1, was.w, o[mi][3]));
             }
         }
         all_l0 = fold_add(f0, all_l0, run.l0);

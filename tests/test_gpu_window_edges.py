@@ -1,0 +1,83 @@
+"""The rotary append and the sliding-window attention where values leave the usual range, where
+rows go by tiles, and where a sequence's parts do not divide evenly (tolerances: see
+_window_common.py, and beside each test what it adds)."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_207_gb300 as pk
+from _window_common import (Cache, attention, visible, within)
+from test_gpu_window import i32, run_decode
+
+pytestmark = pytest.mark.gpu
+
+
+def refill(c, k, v):
+    """Other rows [tokens][Hkv][D] into the cache, in the order of the sequences."""
+    append = {"fp8": pk.append_kv_fp8, "fp4": pk.append_kv_fp4}.get(c.cache, pk.append_kv)
+    append(c.kp, c.vp, k.to(c.wide).cuda(), v.to(c.wide).cuda(), c.tables.cuda(), i32([0] * len(c.lens)), i32(c.cu))
+    c.refresh()
+
+
+def check_range(c, q, window, sinks, scale, out):
+    """Outputs of the 8- and 4-bit caches with a tolerance that follows the values.
+
+    A probability times its value's scale is brought to f16 by a power of two that takes the
+    largest scale so far to between 2^11 and 2^15, so what rounds below f16's normal range is off
+    by at most 2^-25 of that unit: 2^-36 of the largest scale, times the largest code at most
+    2^-36 max |v| for each key."""
+    for s, n in enumerate(c.lens):
+        see = visible(torch.tensor([n - 1]), n, window, sinks)
+        want, tol = attention(q[s:s + 1], c.k[s], c.v[s], see, scale, "f16", q.dtype)
+        G = c.hq // c.hkv
+        for h in range(c.hkv):
+            tol[:, h * G:(h + 1) * G] += n * 2.0 ** -36 * float(c.v[s][see[0], h].abs().max())
+        within(out[s:s + 1], want, tol, f"sequence {s} of length {n}")
+
+
+# ---------------------------------------------------------------------------- decode: values
+def sizes(kind, n, hkv, g):
+    """Factors of the value rows [tokens][Hkv][1]."""
+    if kind == "mixed":                # from row to row, eleven orders of magnitude
+        return 10.0 ** (torch.rand(n, hkv, 1, generator=g) * 11 - 5.5)
+    if kind == "rising":               # raised again and again, within a part and from part to part
+        return torch.logspace(-20, 20, n).view(n, 1, 1).expand(n, hkv, 1)
+    if kind == "falling":
+        return torch.logspace(20, -20, n).view(n, 1, 1).expand(n, hkv, 1)
+    return torch.full((n, hkv, 1), float(kind))
+
+
+@pytest.mark.parametrize("cache", ["fp8", "fp4"])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (14, 2, 64)])
+@pytest.mark.parametrize("kind", ["1e-20", "1e-5", "1e-2", "1", "2e5", "1e30", "mixed", "rising", "falling"])
+def test_decode_of_values_of_any_size(cache, heads, kind):
+    lens = [1, 40, 700, 2600]
+    c = Cache(cache, lens, heads, seed=51)
+    g = torch.Generator().manual_seed(52)
+    n = sum(lens)
+    refill(c, torch.randn(n, heads[1], heads[2], generator=g),
+           torch.randn(n, heads[1], heads[2], generator=g) * sizes(kind, n, heads[1], g))
+    q = c.queries(len(lens))
+    for window, sinks in ((2500, 4), (33, 0)):
+        check_range(c, q, window, sinks, 0.1, run_decode(c, lens, q, window, sinks, 0.1))
+
+
+def small_values_beside_a_hidden_weight(cache, d, small):
+    # the first key has the largest value and no weight (a score 60 or more below the others'): what the
+    # others' probabilities lose beside its scale stays within the tolerance
+    lens, heads = [4], (2, 2, d)
+    c = Cache(cache, lens, heads, seed=54)
+    g = torch.Generator().manual_seed(d - round(math.log2(small)))
+    q = torch.randn(1, 2, d, generator=g).to(c.wide)
+    k, v = torch.randn(4, 2, d, generator=g), torch.randn(4, 2, d, generator=g)
+    k[0] = -8 * q[0].float()
+    v[1:] *= small
+    refill(c, k, v)
+    check_range(c, q, 100, 0, d ** -0.5, run_decode(c, lens, q, 100, 0, d ** -0.5))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("small", [2.0 ** -22, 2.0 ** -26, 2.0 ** -30])
+def test_fp8_decode_of_small_values_beside_a_hidden_weight(d, small):
+    small_values_beside_a_hidden_weight("fp8", d, small)
