@@ -128,6 +128,7 @@ struct Bf16Cache {
             qb[kk][1] = r < G ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8 + 2 * c) : 0u;
         }
     }
+    __device__ __forceinline__ void set_q(float) {}
     __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
         const uint32_t addr = smem_u32(kt) + lane * 16;
         float acc[2][4] = {};
@@ -181,6 +182,30 @@ struct Bf16Cache {
     __device__ __forceinline__ float finish(float (&)[KS][4]) const { return 1.f; }
 };
 
+// Query rows of the 8- and 4-bit caches, bf16 in q and f16 for the tensor cores: each row times
+// the power of two that takes its largest magnitude to 2^4 .. 2^5, which the row's scores give
+// back.  So no element overflows f16, and one loses bits only where it is 2^18 below its row's
+// largest: at most 2^-29 of that, less than the sum's fp32.  (Not higher: FP4's sums over a scale
+// block are multiplied with scales of up to 2^114 before the row's power of two.)  `qb`: the
+// fragments, bf16 on entry; s0, s1: what the scores of heads 2c and 2c + 1 are multiplied with.
+template <int KS>
+__device__ __forceinline__ void rows_to_f16(uint32_t (&qb)[KS][2], float scale, int c, float& s0, float& s1) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) top = __vmaxu2(top, __vmaxu2(qb[kk][0] & 0x7fff7fffu, qb[kk][1] & 0x7fff7fffu));
+    top = max(top & 0xffffu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int shift = min(131 - (int)(top >> 7), 110);        // (2^110 makes bf16's smallest an f16)
+    const float f = exp2i(shift), back = scale * exp2i(-shift);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) qb[kk][i] = pack_f16x2(bf16_lo_to_f32(qb[kk][i]) * f, bf16_hi_to_f32(qb[kk][i]) * f);
+    s0 = __shfl_sync(0xffffffffu, back, 8 * c);
+    s1 = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+}
+
 // E4M3 records: codes become f16 in registers (exact), the products run in f16.
 //   K: ldmatrix gives a lane 4 consecutive dims of one token, so the dot product's index is
 //   permuted alike in the query; the tokens come in the order lo() = 4 (r / 2) + r % 2,
@@ -199,6 +224,7 @@ struct Fp8Cache {
     static constexpr int KS = D / 16;
     static constexpr int SCRATCH = 0;
     uint32_t qb[KS][2];
+    float q0, q1;                                             // factors of the scores
     float unit;                                               // c; 0: the part has no pair yet
     int lane, r, c;
     __device__ __forceinline__ Fp8Cache(int lane_, float*) : lane(lane_), r(lane_ >> 2), c(lane_ & 3) { reset(); }
@@ -209,14 +235,15 @@ struct Fp8Cache {
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
             const uint2 u = r < G ? *reinterpret_cast<const uint2*>(qrow + 16 * kk + 4 * c) : make_uint2(0u, 0u);
-            qb[kk][0] = pack_f16x2(bf16_lo_to_f32(u.x), bf16_hi_to_f32(u.x));
-            qb[kk][1] = pack_f16x2(bf16_lo_to_f32(u.y), bf16_hi_to_f32(u.y));
+            qb[kk][0] = u.x;
+            qb[kk][1] = u.y;
         }
     }
+    __device__ __forceinline__ void set_q(float scale) { rows_to_f16<KS>(qb, scale, c, q0, q1); }
     static __device__ __forceinline__ uint32_t half(uint32_t x, int i) {
         return e4m3x2_to_f16x2((uint16_t)(i ? x >> 16 : x & 0xffffu));
     }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, float, float (&s)[2][4]) const {
         const int km = lane >> 3, kr = lane & 7;
         const int tok = 4 * (kr >> 1) + (kr & 1) + ((km & 1) ? 2 : 0);
         const uint32_t addr = smem_u32(kt) + (uint32_t)(((km >> 1) * kBlockTokens + tok) * 16);
@@ -233,11 +260,11 @@ struct Fp8Cache {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const float* ks = reinterpret_cast<const float*>(kt + b * TILE + 16 * D);
-            const float s0 = ks[lo()] * scale, s1 = ks[hi()] * scale;
-            s[b][0] = acc[b][0] * s0;
-            s[b][1] = acc[b][1] * s0;
-            s[b][2] = acc[b][2] * s1;
-            s[b][3] = acc[b][3] * s1;
+            const float k0 = ks[lo()], k1 = ks[hi()];
+            s[b][0] = acc[b][0] * (k0 * q0);
+            s[b][1] = acc[b][1] * (k0 * q1);
+            s[b][2] = acc[b][2] * (k1 * q0);
+            s[b][3] = acc[b][3] * (k1 * q1);
         }
     }
     // Hidden slots may hold anything (NaN codes, scales of inf): a dim's 16 slots are 16 bytes.
@@ -340,6 +367,7 @@ struct Fp4Cache {
     static constexpr int SCRATCH = 0;
     static constexpr int NB = D / 32;                         // scale blocks of a row
     uint32_t qb[KS][2];
+    float q0, q1;                                             // factors of the scores
     float cb[NB];
     int ref;                                                  // R_b of b = c % NB
     int lane, r, c;
@@ -357,12 +385,11 @@ struct Fp4Cache {
         const uint16_t* qrow = static_cast<const uint16_t*>(q) + (row0 + (r < G ? r : 0)) * D;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
-            const uint32_t u0 = r < G ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * c) : 0u;
-            const uint32_t u1 = r < G ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8 + 2 * c) : 0u;
-            qb[kk][0] = pack_f16x2(bf16_lo_to_f32(u0), bf16_hi_to_f32(u0));
-            qb[kk][1] = pack_f16x2(bf16_lo_to_f32(u1), bf16_hi_to_f32(u1));
+            qb[kk][0] = r < G ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 2 * c) : 0u;
+            qb[kk][1] = r < G ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8 + 2 * c) : 0u;
         }
     }
+    __device__ __forceinline__ void set_q(float scale) { rows_to_f16<KS>(qb, scale, c, q0, q1); }
     // N adjacent 32-bit words
     template <int N>
     static __device__ __forceinline__ void words(const uint8_t* at, uint32_t (&w)[N]) {
@@ -381,7 +408,7 @@ struct Fp4Cache {
     static __device__ __forceinline__ float scale_value(uint8_t code) { return __uint_as_float((uint32_t)code * 0x800000u); }
     // log2 of a block's c_b, from its R_b: at most 127
     static __device__ __forceinline__ int c_exp(int R) { return min(135 - R, 127); }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, float, float (&s)[2][4]) const {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint8_t* k = kt + t * TILE;
@@ -406,7 +433,7 @@ struct Fp4Cache {
                 s[t][3] = fmaf(acc[3], f1, s[t][3]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[t][i] *= scale;
+            for (int i = 0; i < 4; ++i) s[t][i] *= (i & 1) ? q1 : q0;
         }
     }
     // Hidden slots count with scale code 0 (their codes are finite whatever they are).
@@ -530,6 +557,7 @@ struct F32Cache {
             q[kk][1] = r < G ? qrow[8 * kk + 4 + c] : 0.f;
         }
     }
+    __device__ __forceinline__ void set_q(float) {}
     __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
         const float* k = reinterpret_cast<const float*>(kt);
         float large[2][2][4] = {}, small[2][4] = {};          // two sums of h h' per block, of every other step
@@ -802,6 +830,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
             issue(st, st, 0);
             issue(st, st, 1);
         }
+    cache.set_q(p.scale_log2);                 // (the queries are waited for with the copies under way)
 
     Running run;
     float o[KS][4];

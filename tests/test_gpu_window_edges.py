@@ -81,3 +81,23 @@ def small_values_beside_a_hidden_weight(cache, d, small):
 @pytest.mark.parametrize("small", [2.0 ** -22, 2.0 ** -26, 2.0 ** -30])
 def test_fp8_decode_of_small_values_beside_a_hidden_weight(d, small):
     small_values_beside_a_hidden_weight("fp8", d, small)
+
+
+# ---------------------------------------------------------------------------- decode: queries
+@pytest.mark.parametrize("cache", ["fp8", "fp4"])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (14, 2, 64)])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 7e4, 1e30])
+def test_decode_of_queries_of_any_size(cache, heads, size):
+    lens = [20, 700]
+    c = Cache(cache, lens, heads, seed=53)
+    q = (c.queries(2).float() * size).to(c.wide)
+    check_range(c, q, 600, 4, 0.1 / size, run_decode(c, lens, q, 600, 4, 0.1 / size))
+    # heads of one group apart by fourteen orders of magnitude; and a head of zeros
+    q = c.queries(2).float()
+    q[:, 0] *= 1e7
+    q[:, 1] *= 1e-7
+    q[:, 2] = 0
+    q = q.to(c.wide)
+    for scale in (1e-8, 1e6):
+        # (scores beyond fp32's exponent of the others are still finite: the weights of a few keys)
+        check_range(c, q, 600, 4, scale, run_decode(c, lens, q, 600, 4, scale))
