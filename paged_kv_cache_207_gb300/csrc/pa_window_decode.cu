@@ -352,9 +352,11 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 //   K: the scale varies along the dot product, so each 32-dim block of it is a product of
 //   its own, times the token's scale, summed in fp32.
 //   V: the scale varies along the tokens, so it multiplies the probabilities: block b's dims
-//   take P_b = p 2^(e_b(t) - 127) c_b with c_b = 2^(135 - R_b), R_b at least the largest scale
+//   take P_b = p 2^(e_b(t) - 127) c_b with c_b = 2^(142 - R_b), R_b at least the largest scale
 //   code of block b so far (raised, and the block's accumulators rescaled, when a pair brings
-//   a larger one), so that P_b stays at most 2^8, in f16's range.
+//   a larger one), so that P_b stays at most 2^15, in f16's range.  As with FP8, f16 for its 11
+//   bits; R_b lies up to three octaves above the largest code, so a P_b below f16's normal range
+//   is off by at most 2^-25 / c_b, 2^-37 of the largest scale.
 // The bound is the integer pipe (conversions, selections, packing: half the rate of FMAs), so
 // scale codes are read as bytes (their fp32 is one multiply away, on the other pipe), and lane
 // c watches the codes of block c alone for a raise.
@@ -407,7 +409,7 @@ struct Fp4Cache {
     // 2^(code - 127): the code is the exponent field (code 0 gives 0)
     static __device__ __forceinline__ float scale_value(uint8_t code) { return __uint_as_float((uint32_t)code * 0x800000u); }
     // log2 of a block's c_b, from its R_b: at most 127
-    static __device__ __forceinline__ int c_exp(int R) { return min(135 - R, 127); }
+    static __device__ __forceinline__ int c_exp(int R) { return min(142 - R, 127); }
     __device__ __forceinline__ void scores(const uint8_t* kt, float, float (&s)[2][4]) const {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {

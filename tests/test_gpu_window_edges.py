@@ -83,6 +83,12 @@ def test_fp8_decode_of_small_values_beside_a_hidden_weight(d, small):
     small_values_beside_a_hidden_weight("fp8", d, small)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("small", [2.0 ** -22, 2.0 ** -26, 2.0 ** -30])
+def test_fp4_decode_of_small_values_beside_a_hidden_weight(d, small):
+    small_values_beside_a_hidden_weight("fp4", d, small)
+
+
 # ---------------------------------------------------------------------------- decode: queries
 @pytest.mark.parametrize("cache", ["fp8", "fp4"])
 @pytest.mark.parametrize("heads", [(8, 2, 128), (14, 2, 64)])
