@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -88,6 +89,11 @@ struct WParams {
     float scale_log2;
 };
 
+struct Row {
+    int len, first;          // context length (clamped to the table), oldest window position
+    VisibleBlocks v;
+};
+
 // Running maxima (log2 units) and this lane's share of the sums of heads 2c, 2c + 1, and the
 // factors that the last pair's maxima put on what was summed before.
 struct Running {
@@ -129,7 +135,7 @@ struct Bf16Cache {
         }
     }
     __device__ __forceinline__ void set_q(float) {}
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, const WParams& p, float (&s)[2][4]) const {
         const uint32_t addr = smem_u32(kt) + lane * 16;
         float acc[2][4] = {};
 #pragma unroll
@@ -143,7 +149,7 @@ struct Bf16Cache {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][i] = acc[b][i] * scale;
+            for (int i = 0; i < 4; ++i) s[b][i] = acc[b][i] * p.scale_log2;
     }
     // Hidden slots of a V tile may hold anything (even NaN): zero them, 16-byte pieces of 16 slots.
     __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
@@ -243,7 +249,7 @@ struct Fp8Cache {
     static __device__ __forceinline__ uint32_t half(uint32_t x, int i) {
         return e4m3x2_to_f16x2((uint16_t)(i ? x >> 16 : x & 0xffffu));
     }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float, float (&s)[2][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, const WParams&, float (&s)[2][4]) const {
         const int km = lane >> 3, kr = lane & 7;
         const int tok = 4 * (kr >> 1) + (kr & 1) + ((km & 1) ? 2 : 0);
         const uint32_t addr = smem_u32(kt) + (uint32_t)(((km >> 1) * kBlockTokens + tok) * 16);
@@ -410,7 +416,7 @@ struct Fp4Cache {
     static __device__ __forceinline__ float scale_value(uint8_t code) { return __uint_as_float((uint32_t)code * 0x800000u); }
     // log2 of a block's c_b, from its R_b: at most 127
     static __device__ __forceinline__ int c_exp(int R) { return min(142 - R, 127); }
-    __device__ __forceinline__ void scores(const uint8_t* kt, float, float (&s)[2][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, const WParams&, float (&s)[2][4]) const {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint8_t* k = kt + t * TILE;
@@ -512,6 +518,11 @@ struct Fp4Cache {
 // (the outputs' relative error: 2.5e-7 to 3.5e-7; with one long sum 8e-7).
 // K and V fragments are plain 32-bit reads of the tiles (K's are free of bank conflicts, V's
 // two-way); the probabilities pass through shared memory to reach the B operand's order.
+// An infinity has no such two numbers (its l is NaN), and the rounding of h takes finite numbers
+// within 2^-12 of the largest to infinity.  Either leaves its mark on the part: a score that is
+// NaN on the part's sum, a value on its outputs, which come out NaN or infinite.  Such a part of a
+// warp is done again with fp32 FMAs, token by token (a check of each pair's results instead: 20 to
+// 35 % of the time).
 struct Split { uint32_t h, l; };
 __device__ __forceinline__ Split split_tf32(float x) {
     // (integer operations: the conversion instruction runs at a fraction of their rate)
@@ -560,7 +571,7 @@ struct F32Cache {
         }
     }
     __device__ __forceinline__ void set_q(float) {}
-    __device__ __forceinline__ void scores(const uint8_t* kt, float scale, float (&s)[2][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t* kt, const WParams& p, float (&s)[2][4]) const {
         const float* k = reinterpret_cast<const float*>(kt);
         float large[2][2][4] = {}, small[2][4] = {};          // two sums of h h' per block, of every other step
 #pragma unroll
@@ -576,7 +587,7 @@ struct F32Cache {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[b][i] = (large[b][0][i] + large[b][1][i] + small[b][i]) * scale;
+            for (int i = 0; i < 4; ++i) s[b][i] = (large[b][0][i] + large[b][1][i] + small[b][i]) * p.scale_log2;
     }
     // (as for bf16)
     __device__ __forceinline__ void hide(uint8_t* vt, uint32_t vis) const {
@@ -617,6 +628,58 @@ struct F32Cache {
     }
     __device__ __forceinline__ void reset() {}
     __device__ __forceinline__ float finish(float (&)[KS][4]) const { return 1.f; }
+    // The part of entries first .. last - 1 of a walk again, from the pools: its maxima and outputs,
+    // and its whole sums in every lane.
+    template <typename Walk>
+    __device__ __forceinline__ void again(const WParams& p, const Walk& walk, const Row& row, int first, int last, Running& run,
+                                          float (&o)[KS][4]) const {
+        const size_t row0 = (size_t)blockIdx.z * p.Hq + (size_t)blockIdx.y * p.G;
+        // (lanes of heads past G: the first head's, which nothing stores)
+        const float* q0 = static_cast<const float*>(p.q) + (row0 + (2 * c < p.G ? 2 * c : 0)) * D;
+        const float* q1 = static_cast<const float*>(p.q) + (row0 + (2 * c + 1 < p.G ? 2 * c + 1 : 0)) * D;
+        run.m0 = run.m1 = -INFINITY;
+        run.l0 = run.l1 = 0.f;
+#pragma unroll
+        for (int mi = 0; mi < KS; ++mi) o[mi][0] = o[mi][1] = o[mi][2] = o[mi][3] = 0.f;
+#pragma unroll 1
+        for (int e = first; e < last; ++e) {
+            const int at = walk.block(e);
+            const int32_t blk = __ldg(walk.trow + at);
+            if (blk < 0 || blk >= p.num_blocks) continue;
+            const uint32_t vis = visible_slots(at * kBlockTokens, row.len, row.first, p.sinks);
+            const size_t tile = ((size_t)blk * p.Hkv + blockIdx.y) * TILE;
+#pragma unroll 1
+            for (int t = 0; t < kBlockTokens; ++t) {
+                if (!((vis >> t) & 1u)) continue;
+                const float* k = reinterpret_cast<const float*>(p.k_pool + tile) + t * 4;
+                const float* v = reinterpret_cast<const float*>(p.v_pool + tile) + t * 4;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+                for (int d = 0; d < D; ++d) {
+                    const float x = k[(d >> 2) * (kBlockTokens * 4) + (d & 3)];
+                    s0 = __fmaf_rn(q0[d], x, s0);
+                    s1 = __fmaf_rn(q1[d], x, s1);
+                }
+                s0 *= p.scale_log2;
+                s1 *= p.scale_log2;
+                const float n0 = fmaxf(run.m0, s0), n1 = fmaxf(run.m1, s1);
+                const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+                const float a0 = fast_exp2(run.m0 - z0), a1 = fast_exp2(run.m1 - z1);
+                const float w0 = fast_exp2(s0 - z0), w1 = fast_exp2(s1 - z1);
+                run.m0 = n0;
+                run.m1 = n1;
+                run.l0 = __fmaf_rn(run.l0, a0, w0);
+                run.l1 = __fmaf_rn(run.l1, a1, w1);
+#pragma unroll
+                for (int mi = 0; mi < KS; ++mi)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int d = 16 * mi + r + (x >> 1) * 8;
+                        o[mi][x] = __fmaf_rn((x & 1) ? w1 : w0, v[(d >> 2) * (kBlockTokens * 4) + (d & 3)], o[mi][x] * ((x & 1) ? a1 : a0));
+                    }
+            }
+        }
+    }
 };
 
 // Shared memory: the warps' stages, each the K tiles then the V tiles of a pair of blocks;
@@ -664,10 +727,6 @@ struct BlockWalk {
     }
 };
 
-struct Row {
-    int len, first;          // context length (clamped to the table), oldest window position
-    VisibleBlocks v;
-};
 __device__ __forceinline__ Row row_of(const WParams& p, int s, bool report) {
     Row x;
     x.len = __ldg(p.lens + s);
@@ -859,11 +918,19 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
             sm_l[at + 1] = l1;
         }
     };
-    auto end_part = [&]() {
+    auto end_part = [&](int from, int to) {                    // (of the pairs from .. to - 1)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
             run.l0 += __shfl_xor_sync(0xffffffffu, run.l0, x);
             run.l1 += __shfl_xor_sync(0xffffffffu, run.l1, x);
+        }
+        if constexpr (C::TYPE == PA_F32) {
+            bool fine = run.l0 == run.l0 && run.l1 == run.l1;
+#pragma unroll
+            for (int mi = 0; mi < KS; ++mi)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) fine = fine && fabsf(o[mi][x]) <= FLT_MAX;
+            if (!__all_sync(0xffffffffu, fine)) cache.again(p, walk, row, 2 * from, min(2 * to, walk.n), run, o);
         }
         const float factor = cache.finish(o);
         const int r = lane >> 2, c = lane & 3;
@@ -912,7 +979,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
             if (i >= npairs) break;
             const bool more = i + NST < npairs;
             if (i == end_at) {
-                end_part();
+                end_part(i - part_pairs, i);
                 end_at = end_at < last_end ? end_at + part_pairs : INT_MAX;
             }
             const uint32_t h = (have >> (2 * st)) & 3u;
@@ -941,7 +1008,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
             }
             state &= ~k_out(st);
             float sc[2][4];
-            cache.scores(kt, p.scale_log2, sc);
+            cache.scores(kt, p, sc);
             float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -1009,8 +1076,11 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
         }
     }
     const int results = p.per ? min(p.per, parts - (int)blockIdx.x * p.per) : 1;
-    do end_part();                             // (a warp without blocks in the last parts: empty ones)
-    while (p.per && at_slot < results * slot);
+    int from = end_at == INT_MAX ? last_end : end_at - part_pairs;
+    do {                                       // (a warp without blocks in the last parts: empty ones)
+        end_part(from, npairs);
+        from = npairs;
+    } while (p.per && at_slot < results * slot);
     const bool bad = __syncthreads_or(failed || skip), cta_skip = __syncthreads_or(skip);
     if (!p.per) put_sums(all_m0, all_m1, all_l0, all_l1);
     if (bad) {

@@ -107,3 +107,36 @@ def test_decode_of_queries_of_any_size(cache, heads, size):
     for scale in (1e-8, 1e6):
         # (scores beyond fp32's exponent of the others are still finite: the weights of a few keys)
         check_range(c, q, 600, 4, scale, run_decode(c, lens, q, 600, 4, scale))
+
+
+# ---------------------------------------------------------------------------- decode: f32
+@pytest.mark.parametrize("heads", [(4, 4, 64), (8, 2, 128)])
+def test_f32_decode_of_infinities_and_the_largest_values(heads):
+    hq, hkv, d = heads
+    lens = [200, 1, 900]
+    c = Cache("f32", lens, heads, seed=55)
+    k, v = (torch.cat(x).float() for x in (c.k, c.v))
+    last = torch.finfo(torch.float32).max
+    # keys that score -inf get weight 0, also as the first ones of a warp's walk
+    away = list(range(64)) + [100, 199]
+    k[away, :, 0] = float("-inf")
+    # a value that is not finite reaches its dim alone; the largest one stays what it is
+    v[120, :, 5] = float("inf")
+    v[200, :, 7] = last
+    # the largest keys, and queries that bring them back
+    k[201 + 50, :, 3] = last
+    refill(c, k, v)
+    q = torch.rand(3, hq, d, generator=c.g) + 0.1
+    q[2, :, 3] = 8.0 / last
+    out = run_decode(c, lens, q, 1000, 0, 0.125).cpu()
+    assert bool((out[0, :, 5] == float("inf")).all())
+    out[0, :, 5] = 0
+    c.k[0][away], c.v[0][120, :, 5] = 0, 0
+    for s, n in enumerate(lens):
+        see = torch.ones(1, n, dtype=torch.bool)
+        if s == 0:
+            see[0, away] = False
+        want, tol = attention(q[s:s + 1], c.k[s], c.v[s], see, 0.125, "f32", q.dtype)
+        if s == 0:
+            want[:, :, 5] = 0
+        within(out[s:s + 1], want, tol, f"sequence {s}")
