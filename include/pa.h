@@ -476,7 +476,7 @@ pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void*
  * context gives zeros.  A sequence's result does not depend on the rest of the batch (for
  * the same table width).  For f32 pools the products run on the tensor cores with every
  * factor as a sum of two tf32 numbers (2^-21 of a product); stretches of a sequence that hold
- * infinities or numbers near the largest go through fp32 FMAs (about a hundred times slower).
+ * infinities or numbers near the largest go through fp32 FMAs, more slowly.
  */
 pa_status pa_decode_attention_window(void* out, const void* q, const void* k_pool,
                                      const void* v_pool, const int32_t* block_tables,
