@@ -141,7 +141,8 @@ __device__ __forceinline__ float max_abs(const Piece<E>& r) {
 // y, q = x y and two steps q + (x - q scale) y, the remainders exact by fused multiply-add, give
 // the quotient's rounding (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990) while nothing underflows.  At scales from 2^-80 the remainders
-// of quotients that round to a code above 0 do not; other scales (infinity too) divide.
+// of quotients that round to a code above 0 do not; other scales (infinity too) divide.  The
+// steps make +0 of a quotient of -0 (and may of one that underflows): x gives the sign.
 struct Divisor {
     float scale, y;
     bool plain;
@@ -153,7 +154,7 @@ struct Divisor {
     __device__ __forceinline__ float quotient(float x) const {
         float q = __fmul_rn(x, y);
         q = __fmaf_rn(__fmaf_rn(-q, scale, x), y, q);
-        return __fmaf_rn(__fmaf_rn(-q, scale, x), y, q);
+        return copysignf(__fmaf_rn(__fmaf_rn(-q, scale, x), y, q), x);
     }
 };
 

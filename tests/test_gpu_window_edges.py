@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import paged_kv_cache_207_gb300 as pk
-from _window_common import (Cache, attention, visible, within)
-from test_gpu_window import i32, run_decode
+from _window_common import (BLOCK, Cache, attention, pool_for, visible, within)
+from test_gpu_window import cu_of, frequencies, i32, run_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,22 @@ def test_f32_decode_of_infinities_and_the_largest_values(heads):
         if s == 0:
             want[:, :, 5] = 0
         within(out[s:s + 1], want, tol, f"sequence {s}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_append_fp8_keeps_the_sign_of_zeros(d):
+    # values are never turned: the plain append's bytes, -0 among them, row by row and by tiles
+    g = torch.Generator().manual_seed(63)
+    n, hkv = 1200, 2
+    v = torch.randn(n, hkv, d, generator=g)
+    v[torch.rand(n, hkv, d, generator=g) < 0.1] = -0.0
+    v[torch.rand(n, hkv, d, generator=g) < 0.1] = 0.0
+    dk, dv = (torch.randn(n, hkv, d, generator=g).bfloat16().cuda(), v.bfloat16().cuda())
+    for counts in ([1] * n, [n]):
+        blocks = sum((x + BLOCK - 1) // BLOCK for x in counts)
+        tables = torch.arange(blocks, dtype=torch.int32).view(len(counts), -1).cuda()
+        starts, cu = i32([0] * len(counts)), cu_of(counts)
+        pools = [[pool_for("fp8", blocks, hkv, d) for _ in (0, 1)] for _ in (0, 1)]
+        pk.rope_append_kv_fp8(*pools[0], None, None, dk, dv, frequencies(d), tables, starts, cu)
+        pk.append_kv_fp8(*pools[1], dk, dv, tables, starts, cu)
+        assert bool((pools[1][1][..., :BLOCK * d] == 0x80).any()) and torch.equal(pools[0][1], pools[1][1])
