@@ -466,8 +466,9 @@ def _fp4_pool(k_pool):
 
 
 def _bound(x) -> int:
-    """A window, sink count or chunk bound: anything past int32 is as good as the largest."""
-    return min(int(x), 2**31 - 1)
+    """A window, sink count or chunk bound as an int32: anything past its ends is as good as the
+    end (ctypes would take it modulo 2^32)."""
+    return max(-2**31, min(int(x), 2**31 - 1))
 
 
 def _call_on(dev: int, stream, fn, *args) -> None:
@@ -568,7 +569,7 @@ def _rope_append(pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_t
         _checked(dev, cu_new_tokens, "cu_new_tokens", _I32, (s + 1,))
     _call_on(dev, stream, lib().pa_rope_append_kv, k_pool.data_ptr(), v_pool.data_ptr(),
              q_out.data_ptr() if with_q else None, q.data_ptr() if with_q else None, k_new.data_ptr(),
-             v_new.data_ptr(), o_row, q_row, k_row, v_row, inv_freq.data_ptr(), 2 * half,
+             v_new.data_ptr(), o_row, q_row, k_row, v_row, inv_freq.data_ptr(), _bound(2 * half),
              1 if interleaved else 0, block_tables.data_ptr(), width, start_pos.data_ptr(),
              cu_new_tokens.data_ptr(), s, n, nb, hq if with_q else 0, hkv, d, code,
              None if err_flag is None else _flag(dev, err_flag))

@@ -159,3 +159,14 @@ def test_rope_append_fp8_keeps_the_sign_of_zeros(d):
         pk.rope_append_kv_fp8(*pools[0], None, None, dk, dv, frequencies(d), tables, starts, cu)
         pk.append_kv_fp8(*pools[1], dk, dv, tables, starts, cu)
         assert bool((pools[1][1][..., :BLOCK * d] == 0x80).any()) and torch.equal(pools[0][1], pools[1][1])
+
+
+def test_bounds_far_below_are_refused_both_ways():
+    c = Cache("bf16", [40], (4, 2, 64), seed=65)
+    q = c.queries(1).cuda()
+    call = lambda w, n, **kw: pk.decode_attention_window(torch.empty_like(q), q, c.kp, c.vp, c.tables.cuda(), i32([40]), 0.1, w, n, **kw)
+    for kw in ({}, {"stream": torch.cuda.current_stream()}):
+        for w, n in ((-2**32 + 5, 0), (-2**63, 0), (5, -2**32 + 1), (-2**100, 3)):
+            with pytest.raises(pk.PagedKVError):
+                call(w, n, **kw)
+        call(2**32 + 5, 2**33, **kw)
