@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import importlib.util
 import os
 import re
+import shlex
 import shutil
 import subprocess
 import sys
@@ -61,11 +62,10 @@ def _torch_version() -> str:
         return re.search(r"__version__ = ['\"](.+?)['\"]", f.read()).group(1)
 
 
-def _stale() -> bool:
-    made = [LIB] + ([QUICK] if _has_headers() else [])
-    if not all(os.path.exists(f) for f in made):
+def _stale(made: str) -> bool:
+    if not os.path.exists(made):
         return True
-    t = min(os.path.getmtime(f) for f in made)
+    t = os.path.getmtime(made)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -87,39 +87,53 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
     return obj
 
 
-def _compile_quick() -> None:
-    """csrc/pa_binding.cpp with the C++ compiler; without the headers the bindings do without."""
-    if not _has_headers():
-        return
-    tmp = QUICK + f".tmp{os.getpid()}"
+def _compile_quick() -> str | None:
+    """csrc/pa_binding.cpp with the C++ compiler (``CXX`` may be a command with arguments), as a
+    file to be renamed to QUICK.  None where that does not work, which is said on stderr: the
+    bindings do without."""
+    tmp = os.path.join(BUILD, f"_quick{os.getpid()}.so")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f'-DPA_TORCH_VERSION="{_torch_version()}"', "-I", INCLUDE,
-           "-I", PYTHON_INCLUDE, "-isystem", os.path.join(TORCH, "include"),
-           "-isystem", os.path.join(TORCH, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
-           os.path.join(CSRC, "pa_binding.cpp"), "-L", os.path.join(TORCH, "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda", "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on pa_binding.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, QUICK)
+    cmd = shlex.split(os.environ.get("CXX", "")) or ["g++"]
+    cmd += ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f'-DPA_TORCH_VERSION="{_torch_version()}"', "-I", INCLUDE,
+            "-I", PYTHON_INCLUDE, "-isystem", os.path.join(TORCH, "include"),
+            "-isystem", os.path.join(TORCH, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+            os.path.join(CSRC, "pa_binding.cpp"), "-L", os.path.join(TORCH, "lib"), "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-o", tmp]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = f"{r.stdout}\n{r.stderr}" if r.returncode != 0 else ""
+    except OSError as e:
+        why = str(e)
+    if why:
+        sys.stderr.write(f"{cmd[0]} failed on pa_binding.cpp, calls go through Python:\n{why}\n")
+        return None
+    return tmp
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
-    if not force and not ptxas_verbose and not _stale():
+    lib = force or ptxas_verbose or _stale(LIB)
+    short_cut = _has_headers() and (force or ptxas_verbose or _stale(QUICK))
+    if not lib and not short_cut:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    srcs = [os.path.join(CSRC, s) for s in SOURCES] if lib else []
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        quick = ex.submit(_compile_quick)
+        quick = ex.submit(_compile_quick) if short_cut else None
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    quick.result()
+    if lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [_nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if quick is not None:
+        made = quick.result()
+        if made is not None:
+            os.replace(made, QUICK)
+        elif os.path.exists(QUICK):
+            os.remove(QUICK)                     # (of other sources: it must not meet this library)
     return LIB
 
 
