@@ -2,13 +2,14 @@
 rows go by tiles, and where a sequence's parts do not divide evenly (tolerances: see
 _window_common.py, and beside each test what it adds)."""
 import math
+import warnings
 
 import pytest
 import torch
 
 import paged_kv_cache_207_gb300 as pk
-from _window_common import (BLOCK, Cache, attention, pool_for, visible, within)
-from test_gpu_window import cu_of, frequencies, i32, run_decode
+from _window_common import (BLOCK, Cache, attention, half_step, nan_like, pool_for, rope_call, rotated, visible, within)
+from test_gpu_window import cu_of, err_flag, frequencies, i32, place, rope_inputs, run_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -140,6 +141,131 @@ def test_f32_decode_of_infinities_and_the_largest_values(heads):
         if s == 0:
             want[:, :, 5] = 0
         within(out[s:s + 1], want, tol, f"sequence {s}")
+
+
+# ---------------------------------------------------------------------------- decode: parts
+@pytest.mark.parametrize("cache,heads,windows", [
+    ("bf16", (32, 8, 128), (2276, 2150)),                # 7 and 6 parts
+    ("bf16", (14, 2, 64), (2276, 1250)),                 # 5 and 3
+    ("fp8", (32, 8, 128), (2276, 2150)),
+    ("fp8", (14, 2, 64), (2600,)),                       # 6
+    ("fp4", (32, 8, 128), (4300,)),                      # 7
+    ("f32", (12, 12, 64), (2276, 4300, 4600, 5400)),     # 7, 12, 13 and 15
+    ("f32", (15, 3, 128), (2276,)),                      # 7
+])
+def test_decode_is_the_same_where_parts_do_not_divide_evenly(cache, heads, windows):
+    lens = [6300, 2290, 4700, 17]
+    c = Cache(cache, lens, heads, seed=57)
+    q = c.queries(len(lens))
+    for window in windows:
+        out = run_decode(c, lens, q, window, 4, 0.1)
+        for s, n in enumerate(lens):
+            want, tol = attention(q[s:s + 1], c.k[s], c.v[s], visible(torch.tensor([n - 1]), n, window, 4), 0.1, cache, q.dtype)
+            within(out[s:s + 1], want, tol, f"sequence {s} of length {n}")
+        for n in (1, 2, 3, 5, 8, 12, 16, 24, 40, 75, 160):
+            at = torch.arange(n) % len(lens)
+            many = run_decode(c, [lens[i] for i in at], q[at], window, 4, 0.1, tables=c.tables[at])
+            assert torch.equal(many, out[at.cuda()]), (window, n)
+
+
+# ---------------------------------------------------------------------------- rotary append
+def captured(call, tmp_path):
+    """What the runtime says of the kernels that `call` launches."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    graph.enable_debug_mode()
+    with torch.cuda.graph(graph):
+        call()
+    at = tmp_path / "graph.dot"
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")
+        graph.debug_dump(str(at))
+    return at.read_text()
+
+
+def kernels_of(call, tmp_path):
+    """The rotary append's kernels that `call` launches, by name."""
+    text = captured(call, tmp_path)
+    return {name for name in ("rope_append_kernel", "rope_append_tile_kernel") if name in text}
+
+
+CACHES = ["bf16", "f32", "fp8", "fp4"]
+
+
+def test_rope_append_goes_by_rows_and_by_tiles(tmp_path):
+    for cache in CACHES:
+        most = 512 if cache in ("bf16", "f32") else 256
+        for counts, want in (([most], "rope_append_kernel"), ([most + 1], "rope_append_tile_kernel"),
+                             ([8] * 200, "rope_append_kernel"), ([40] * 20, "rope_append_tile_kernel")):
+            _, (dq, dk, dv) = rope_inputs(cache, counts, (4, 2, 64), False, seed=1)
+            tables, _, _, blocks = place([3] * len(counts), counts)
+            args = (pool_for(cache, blocks, 2, 64), pool_for(cache, blocks, 2, 64), nan_like(dq), dq, dk, dv, frequencies(64),
+                    tables.cuda(), i32([3] * len(counts)), cu_of(counts))
+            assert kernels_of(lambda: rope_call(cache)(*args), tmp_path) == {want}, (cache, counts[0])
+
+
+# 712 rows of six sequences, 32 and more on average: tiles for every type of pool
+TILE_COUNTS, TILE_STARTS = [160, 33, 0, 250, 200, 69], [0, 5, 9, 50, 31, 130]
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 3, 128), (26, 1, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_append_of_tiles_in_place_and_without_queries(cache, heads, interleaved, tmp_path):
+    hq, hkv, d = heads
+    (q, k, v), (dq, dk, dv) = rope_inputs(cache, TILE_COUNTS, heads, True, seed=61)
+    tables, pos, blk, blocks = place(TILE_STARTS, TILE_COUNTS)
+    freq = frequencies(d)
+    args = (freq, tables.cuda(), i32(TILE_STARTS), cu_of(TILE_COUNTS), interleaved)
+    pools = [[pool_for(cache, blocks, hkv, d) for _ in (0, 1)] for _ in range(3)]
+    out = nan_like(dq.contiguous())
+    assert kernels_of(lambda: rope_call(cache)(*pools[0], out, dq, dk, dv, *args), tmp_path) == {"rope_append_tile_kernel"}
+    rope_call(cache)(*pools[0], out, dq, dk, dv, *args)
+    rope_call(cache)(*pools[1], None, None, dk, dv, *args)
+    rope_call(cache)(*pools[2], dq, dq, dk, dv, *args)             # queries turned where they are
+    want, size = rotated(q, pos, freq.cpu(), interleaved)
+    within(out, want, half_step(q.dtype) * want.abs() + 5e-7 * size + 1e-30, "queries")
+    assert torch.equal(dq, out)
+    for a in pools[1:]:
+        for x, y in zip(a, pools[0]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+# prefix sums over the 712 rows: a wrong end, backwards, negative, past the rows, not from 0
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("cu", [[0, 160, 193, 193, 443, 643, 700], [0, 160, 193, 193, 443, 643, 800],
+                                [0, 193, 160, 193, 443, 643, 712], [0, -40, 193, 193, 443, 643, 712],
+                                [0, 160, 193, 193, 900, 643, 712], [16, 160, 193, 193, 443, 643, 712],
+                                [0, 2**31 - 1, -2**31, 193, 443, 643, 712], [712, 643, 443, 193, 193, 160, 0]])
+def test_rope_append_of_tiles_flags_bad_prefix_sums(cache, cu, tmp_path):
+    heads = (4, 2, 64)
+    (q, k, v), (dq, dk, dv) = rope_inputs(cache, TILE_COUNTS, heads, True, seed=62)
+    tables = torch.arange(6 * 24, dtype=torch.int32).view(6, 24)
+    freq, starts = frequencies(64), TILE_STARTS
+    kp, vp = pool_for(cache, 6 * 24, 2, 64), pool_for(cache, 6 * 24, 2, 64)
+    out, err = nan_like(dq.contiguous()), err_flag()
+    args = (freq, tables.cuda(), i32(starts), i32(cu))
+    call = lambda: rope_call(cache)(kp, vp, out, dq, dk, dv, *args, err_flag=err)
+    assert kernels_of(call, tmp_path) == {"rope_append_tile_kernel"}
+    call()
+    assert int(err) & pk.DEV_ERR_BAD_CU
+    # every row that lies in one sequence alone, one within the rows, is turned by its place there
+    claims = torch.zeros(712, dtype=torch.int64)
+    at = torch.zeros(712, dtype=torch.int64)
+    for s in range(6):
+        a, b = cu[s], cu[s + 1]
+        if 0 <= a <= b <= 712:
+            claims[a:b] += 1
+            at[a:b] = starts[s] + torch.arange(b - a)
+    rising = all(a <= b for a, b in zip(cu, cu[1:]))
+    done = ~out.isnan().any(-1).any(-1).cpu()
+    assert not bool(done[claims == 0].any())
+    ok = (claims == 1) & (at < 24 * BLOCK)
+    if rising:
+        assert torch.equal(done, ok)
+    else:
+        ok &= done                                        # (the search may miss sequences of sums that fall)
+    want, size = rotated(q, at, freq.cpu(), False)
+    within(out[ok.cuda()], want[ok], (half_step(q.dtype) * want.abs() + 5e-7 * size + 1e-30)[ok], "queries")
 
 
 @pytest.mark.parametrize("d", [64, 128])
