@@ -67,6 +67,11 @@ constexpr int tile_min_rows(pa_dtype t) { return quantised(t) ? 16 : 32; }    //
 // FP8, 37 chunks of 1 to 131: 6.5, 7.3 and 6.8 us; 16 chunks of 512, 32 / 8 of 128, bf16, 24
 // and 48 heads: 34.8 and 39.2).
 constexpr int kLeastHeads = 4, kMostHeads = 36;
+// Threads of tiles' CTAs for each SM while their shares are picked.  An SM holds 512; a handful of
+// CTAs more cost less than a whole share fewer for every tile (4 chunks of 600, 153 tiles, 32 / 8
+// heads of 128, 520 against 512, four shares against three: bf16 11.9 / 13.9 us, FP8 14.4 / 15.8;
+// f32, two against one, 21.7 / 26.9).
+constexpr int kTileRoom = 520;
 constexpr int kTileHeads = 3;          // heads of a thread that are loaded together (four spill)
 
 // A frequency in radians per position as turns * 2^64, modulo 2^64.  Below 1024 in integers
@@ -729,13 +734,20 @@ template <int D, pa_dtype T, bool INTERLEAVED>
 cudaError_t launch_rope(const RParams& p, cudaStream_t stream) {
     const bool tiles = p.total > rows_alone(T) && p.total >= tile_min_rows(T) * (long long)p.S;
     cudaLaunchConfig_t cfg = {};
-    // A tile's heads are shared by several CTAs while all of them fit the GPU (512 threads of an
-    // SM) and a thread keeps kLeastHeads; by two where a thread of 128 had more than kMostHeads.
+    // A tile's heads are shared by several CTAs while all of them find room on the GPU (kTileRoom)
+    // and a thread keeps kLeastHeads; by two where a thread of 128 had more than kMostHeads.
     constexpr int NT = tile_threads(T, D), GROUPS = NT / (kTileRows * (D / (T == PA_F32 ? 8 : 16)));
     const long long touched = (p.total + (kTileRows - 1ll) * p.S) / kTileRows;      // of chunks that begin anywhere
     const int heads = (p.Hq + 2 * p.Hkv) / GROUPS;                                  // of a thread that has a share alone
     const long long most = std::max(1, std::min(8, heads / kLeastHeads));
-    const long long at_once = 308ll * 256 / NT / touched, least = NT == 128 && heads > kMostHeads ? 2 : 1;
+    int sms = 1;
+    if (tiles) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    const long long at_once = (long long)sms * kTileRoom / NT / touched, least = NT == 128 && heads > kMostHeads ? 2 : 1;
     const int shares = (int)std::max(least, std::min(most, at_once));
     cfg.gridDim = tiles ? dim3((unsigned)(p.total / kTileRows + 2ll * p.S), shares) : dim3((unsigned)p.total);
     cfg.blockDim = dim3(tiles ? tile_threads(T, D) : kRowThreads);

@@ -2,6 +2,7 @@
 rows go by tiles, and where a sequence's parts do not divide evenly (tolerances: see
 _window_common.py, and beside each test what it adds)."""
 import math
+import re
 import warnings
 
 import pytest
@@ -201,6 +202,20 @@ def test_rope_append_goes_by_rows_and_by_tiles(tmp_path):
             args = (pool_for(cache, blocks, 2, 64), pool_for(cache, blocks, 2, 64), nan_like(dq), dq, dk, dv, frequencies(64),
                     tables.cuda(), i32([3] * len(counts)), cu_of(counts))
             assert kernels_of(lambda: rope_call(cache)(*args), tmp_path) == {want}, (cache, counts[0])
+
+
+@pytest.mark.parametrize("cache,threads", [("bf16", 128), ("fp8", 128), ("f32", 256)])
+def test_rope_append_shares_tiles_as_the_gpu_has_room(cache, threads, tmp_path):
+    # 154 tiles in as many shares as 520 threads for each SM allow
+    n, (hq, hkv, d) = 154 * BLOCK, (32, 8, 128)
+    _, (dq, dk, dv) = rope_inputs(cache, [n], (hq, hkv, d), False, seed=64)
+    tables = torch.arange(154, dtype=torch.int32).view(1, 154).cuda()
+    args = (pool_for(cache, 154, hkv, d), pool_for(cache, 154, hkv, d), nan_like(dq), dq, dk, dv, frequencies(d), tables,
+            i32([0]), cu_of([n]))
+    # (a grid of one share has one dimension)
+    grid = re.search(r"rope_append_tile_kernel\S*?<\\<(?:\\\{\d+,(\d+)\\\}|\d+),(\d+)", captured(lambda: rope_call(cache)(*args), tmp_path))
+    shares, room = int(grid[1] or 1), torch.cuda.get_device_properties(0).multi_processor_count * 520 // threads
+    assert int(grid[2]) == threads and shares == max(1, room // 154)
 
 
 # 712 rows of six sequences, 32 and more on average: tiles for every type of pool
