@@ -14,11 +14,14 @@
 // block src goes to block dst in both pools; 16-byte vector loads and stores.
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
-#include "pa_rows.cuh"
 
 namespace pa {
 
 namespace {
+
+__device__ __forceinline__ void raise_flag(int32_t* err, int bits) {
+    if (err) atomicOr(err, bits);
+}
 
 struct AParams {
     char* k_pool;
@@ -33,6 +36,49 @@ struct AParams {
     long long items;                                      // (FP8 / FP4) total * Hkv warps; (plain)
                                                           // groups of 16 rows x Hkv x piece pairs x 32
 };
+
+// Sequence, position and physical block of new row `row` (reads only cu, start_pos
+// and the tables, which no kernel of this library writes).  Flags and returns false
+// when the row has no valid destination; `report` selects the thread that flags.
+__device__ __forceinline__ bool locate_row(const AParams& p, int row, bool report, int& s_out,
+                                           int& slot_out, int32_t& blk_out) {
+    // sequence owning this row: cu[s] <= row < cu[s+1].  Guess by proportion (exact
+    // when every sequence appends the same number of rows, e.g. one per decode step),
+    // then fall back to a binary search.
+    int s = (int)(((long long)row * p.S) / (p.total > 0 ? p.total : 1));
+    if (s >= p.S) s = p.S - 1;
+    int first = __ldg(p.cu + s);
+    int next = __ldg(p.cu + s + 1);
+    if (!(first <= row && row < next)) {
+        int lo = 0, hi = p.S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (__ldg(p.cu + mid) <= row) lo = mid;
+            else hi = mid - 1;
+        }
+        s = lo;
+        first = __ldg(p.cu + s);
+        next = __ldg(p.cu + s + 1);
+        if (row < first || row >= next) {
+            if (report) raise_flag(p.err, PA_DEV_ERR_BAD_CU);
+            return false;
+        }
+    }
+    const long long pos = (long long)__ldg(p.start_pos + s) + (row - first);
+    if (pos < 0 || pos >= (long long)p.max_blocks * kBlockTokens) {
+        if (report) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+        return false;
+    }
+    const int32_t blk = __ldg(p.tables + (size_t)s * p.max_blocks + (int)(pos / kBlockTokens));
+    if (blk < 0 || blk >= p.num_blocks) {
+        if (report) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+        return false;
+    }
+    s_out = s;
+    slot_out = (int)(pos % kBlockTokens);
+    blk_out = blk;
+    return true;
+}
 
 __global__ void __launch_bounds__(256) append_kernel(const AParams p) {
     // a decode launched after this kernel may start its set-up now; it waits for this
@@ -49,18 +95,17 @@ __global__ void __launch_bounds__(256) append_kernel(const AParams p) {
     const int h = (int)(gh % p.Hkv);
     const int row = (int)(gh / p.Hkv) * 16 + (int)(item & 15);
     const int ch = 2 * pr + (int)((item >> 4) & 1);
-    int s, pos = 0;
+    int s, slot;
     int32_t blk;
     // (the two lanes of a row both look it up; the piece-0 lane reports a failure)
     const bool ok = item < p.items && row < p.total && ch < p.chunks &&
-                    locate_row(p, row, ch == 0, s, pos, blk);
+                    locate_row(p, row, ch == 0, s, slot, blk);
 
     // The address chain above read only inputs.  The pools (and, in principle, the new
     // rows) may still be in use by the previous kernel of the stream: wait for it.  Every
     // thread waits before it exits, so this grid never completes before that kernel.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!ok) return;
-    const int slot = pos % kBlockTokens;
     const size_t src = (((size_t)row * p.Hkv + h) * p.chunks + ch) * 16;
     const uint4 kv = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
     const uint4 vv = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
@@ -85,12 +130,11 @@ __global__ void __launch_bounds__(256) append_fp8_kernel(const AParams p) {
     }
     const int h = (int)(wid % p.Hkv);
     const int row = (int)(wid / p.Hkv);
-    int s, pos = 0;
+    int s, slot;
     int32_t blk;
-    const bool ok = wid < (long long)p.total * p.Hkv && locate_row(p, row, lane == 0, s, pos, blk);
+    const bool ok = wid < (long long)p.total * p.Hkv && locate_row(p, row, lane == 0, s, slot, blk);
     asm volatile("griddepcontrol.wait;" ::: "memory");           // as in append_kernel
     if (!ok) return;                                              // warp-uniform
-    const int slot = pos % kBlockTokens;
     const size_t src = ((size_t)row * p.Hkv + h) * D * 2;          // bytes of bf16 rows
     uint32_t kw, vw;
     float ks, vs;
@@ -125,12 +169,11 @@ __global__ void __launch_bounds__(256) append_fp4_kernel(const AParams p) {
     }
     const int h = (int)(wid % p.Hkv);
     const int row = (int)(wid / p.Hkv);
-    int s, pos = 0;
+    int s, slot;
     int32_t blk;
-    const bool ok = wid < (long long)p.total * p.Hkv && locate_row(p, row, lane == 0, s, pos, blk);
+    const bool ok = wid < (long long)p.total * p.Hkv && locate_row(p, row, lane == 0, s, slot, blk);
     asm volatile("griddepcontrol.wait;" ::: "memory");           // as in append_kernel
     if (!ok) return;                                              // warp-uniform
-    const int slot = pos % kBlockTokens;
 
     const size_t src = ((size_t)row * p.Hkv + h) * D + (size_t)lane * VPL;
     float kx[VPL], vx[VPL];

@@ -19,8 +19,8 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "pa_flags.cuh"
 #include "pa_ptx.cuh"
-#include "pa_rows.cuh"
 #include "pa_window.h"
 
 namespace pa {

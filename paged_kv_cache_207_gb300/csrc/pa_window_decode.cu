@@ -24,8 +24,8 @@
 #include <climits>
 #include <cmath>
 
+#include "pa_flags.cuh"
 #include "pa_ptx.cuh"
-#include "pa_rows.cuh"
 #include "pa_window.h"
 
 namespace pa {
