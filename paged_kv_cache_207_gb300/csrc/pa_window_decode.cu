@@ -9,9 +9,9 @@
 // free the blocks between; hidden slots of a listed block are masked, whatever they hold.
 //
 // One warp-level pass over the keys with a running maximum and sum (fp32): the listed blocks
-// go to the warps in pairs, through private shared-memory stages filled by bulk copies.  A
-// stage's K half and V half have an mbarrier each: K is refilled as soon as the scores are
-// taken, V after the products.  Scores of 32 tokens x 8 heads (the kv head's G <= 8 query
+// go to the warps in pairs, through a stage of shared memory of the warp's own that bulk copies
+// fill.  Its K half and V half have an mbarrier each: K is refilled as soon as the scores are
+// taken, V after the products (more stages gained nothing: the CTAs of an SM hide the copies).  Scores of 32 tokens x 8 heads (the kv head's G <= 8 query
 // heads) come from the tensor cores (mma.sync, tokens on M), the probabilities are transposed
 // in registers and multiplied with V on the tensor cores again.  Two blocks at a time because
 // the chain scores -> maximum -> probabilities -> products is what a warp waits for when few
@@ -683,16 +683,16 @@ struct F32Cache {
 };
 
 // Shared memory: the warps' stages, each the K tiles then the V tiles of a pair of blocks;
-// the warps' scratch; the barriers, two per stage; and the warps' folded results.  A result is
+// the warps' scratch; the barriers, two of each warp; and the warps' folded results.  A result is
 // the outputs as the lanes hold them (per pair of heads, 16 dims and r: a float4, dims r and
 // r + 8 of one head, then of the other; CS floats for a pair of heads, no two lanes in the same banks), then the
 // heads' maxima and sums.
-template <class C, int D, int NW, int NST>
+template <class C, int D, int NW>
 struct Layout {
     static constexpr int STAGE = 4 * C::TILE;
-    static constexpr int WARP = NW * NST * STAGE;
+    static constexpr int WARP = NW * STAGE;
     static constexpr int BAR = WARP + NW * C::SCRATCH;
-    static constexpr int OUT = BAR + (NW * NST * 16 + 15) / 16 * 16;
+    static constexpr int OUT = BAR + NW * 16;
     static constexpr int CS = 2 * D + 8;
     static __host__ __device__ constexpr int outs(int G) { return CS * ((G + 1) / 2); }         // floats of a warp
     static __host__ __device__ constexpr int result(int G) { return NW * (outs(G) + 2 * G); }   // and of all
@@ -811,19 +811,19 @@ __device__ __forceinline__ void store_out(void* out, size_t at, float x) {
     else static_cast<float*>(out)[at] = x;
 }
 
-template <template <int> class Cache, int D, int NW, int NST>
+template <template <int> class Cache, int D, int NW>
 __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_decode_kernel(const WParams p) {
     using C = Cache<D>;
-    using L = Layout<C, D, NW, NST>;
+    using L = Layout<C, D, NW>;
     constexpr int KS = C::KS, TILE = C::TILE;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kvh = blockIdx.y, s = blockIdx.z;
-    uint8_t* stage0 = smem + warp * NST * L::STAGE;
-    const uint32_t bar0 = smem_u32(smem) + L::BAR + warp * NST * 16;   // per stage: K's, V's
+    uint8_t* const stage = smem + warp * L::STAGE;
+    const uint32_t bars = smem_u32(smem) + L::BAR + warp * 16;         // K's, V's
     if (lane == 0) {
-#pragma unroll
-        for (int st = 0; st < 2 * NST; ++st) mbar_init(bar0 + st * 8, 1);
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
         fence_proxy_async_smem();
     }
     __syncwarp();
@@ -853,44 +853,39 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
     walk.fetch();
 
     const uint64_t pol = l2_policy_evict_first();
-    // Pair i's tiles into its stage: `which` 0 K, 1 V.  have: 2 bits per stage, the blocks that
-    // were copied (a table entry that names no block is flagged and left out).
-    // state: 2 bits per stage (K, V), the phase that its barrier's next copy ends; from bit 16 and
-    // from bit 24 on a bit per stage, whether such a copy of K, of V is in flight.
-    uint32_t have = 0, state = 0;
-    auto k_out = [](int st) { return 1u << (16 + st); };
-    auto v_out = [](int st) { return 1u << (24 + st); };
-    int32_t blk_v[NST][2];                     // pair's blocks, kept from K's issue to V's
-    auto issue = [&](int i, int st, int which) {
-        if (which == 0) {
-            blk_v[st][0] = walk.entry(2 * i);
-            blk_v[st][1] = walk.entry(2 * i + 1);          // (-1 past the last)
-            have = (have & ~(3u << (2 * st))) | (((blk_v[st][0] >= 0 ? 1u : 0u) | (blk_v[st][1] >= 0 ? 2u : 0u)) << (2 * st));
+    // Pair i's tiles into the stage, HALF 0 K, 1 V (a table entry that names no block is flagged
+    // and left out).
+    uint32_t have = 0;                         // of the pair whose K was issued last, a bit a block: it is copied
+    uint32_t phase = 0, in_flight = 0;         // a bit a half: the phase that its next copy ends; it has a copy under way
+    int32_t blk[2];                            // that pair's blocks, kept from K's issue to V's
+    auto issue = [&](int i, int half) {
+        if (half == 0) {
+            blk[0] = walk.entry(2 * i);
+            blk[1] = walk.entry(2 * i + 1);                    // (-1 past the last)
+            have = (blk[0] >= 0 ? 1u : 0u) | (blk[1] >= 0 ? 2u : 0u);
         }
-        const uint32_t h = (have >> (2 * st)) & 3u;
-        if (h != 0u && lane == 0) {
-            const uint32_t bar = bar0 + st * 16 + which * 8;
-            const char* pool = which == 0 ? p.k_pool : p.v_pool;
-            const uint32_t dst = smem_u32(stage0) + st * L::STAGE + which * 2 * TILE;
+        if (have == 0u) return;
+        in_flight |= 1u << half;
+        if (lane == 0) {
+            const uint32_t bar = bars + half * 8, dst = smem_u32(stage) + half * 2 * TILE;
+            const char* pool = half == 0 ? p.k_pool : p.v_pool;
             fence_proxy_async_smem();
-            mbar_arrive_expect_tx(bar, h == 3u ? 2 * TILE : TILE);
-            if (h & 1u) bulk_g2s(dst, pool + ((size_t)blk_v[st][0] * p.Hkv + kvh) * (size_t)TILE, TILE, bar, pol);
-            if (h & 2u) bulk_g2s(dst + TILE, pool + ((size_t)blk_v[st][1] * p.Hkv + kvh) * (size_t)TILE, TILE, bar, pol);
+            mbar_arrive_expect_tx(bar, have == 3u ? 2 * TILE : TILE);
+            if (have & 1u) bulk_g2s(dst, pool + ((size_t)blk[0] * p.Hkv + kvh) * (size_t)TILE, TILE, bar, pol);
+            if (have & 2u) bulk_g2s(dst + TILE, pool + ((size_t)blk[1] * p.Hkv + kvh) * (size_t)TILE, TILE, bar, pol);
         }
     };
-    auto landed = [&](int st, int which) -> bool {
-        const uint32_t bit = 2 * st + which;
-        const bool ok = mbar_wait_bounded(bar0 + st * 16 + which * 8, (state >> bit) & 1u, kWaitLimitNs);
+    auto landed = [&](int half) -> bool {
+        const bool ok = mbar_wait_bounded(bars + half * 8, (phase >> half) & 1u, kWaitLimitNs);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        state ^= 1u << bit;
+        phase ^= 1u << half;
+        in_flight &= ~(1u << half);
         return true;
     };
-#pragma unroll
-    for (int st = 0; st < NST; ++st)
-        if (st < npairs) {
-            issue(st, st, 0);
-            issue(st, st, 1);
-        }
+    if (npairs > 0) {
+        issue(0, 0);
+        issue(0, 1);
+    }
     cache.set_q(p.scale_log2);                 // (the queries are waited for with the copies under way)
 
     Running run;
@@ -967,113 +962,92 @@ __global__ void __launch_bounds__(NW * 32, ctas_for(Cache<D>::TYPE, D)) window_d
     const int last_end = (mine - 1) * part_pairs;
     int end_at = mine > 1 ? part_pairs : INT_MAX;      // pair before which a part ends (the last one: never)
     bool failed = false;
-#pragma unroll
-    for (int st = 0; st < NST; ++st)
-        if (st < npairs && ((have >> (2 * st)) & 3u)) {
-            state |= k_out(st) | v_out(st);
+    for (int i = 0; i < npairs; ++i) {
+        const bool more = i + 1 < npairs;
+        if (i == end_at) {
+            end_part(i - part_pairs, i);
+            end_at = end_at < last_end ? end_at + part_pairs : INT_MAX;
         }
-    for (int i0 = 0; i0 < npairs && !failed; i0 += NST) {
+        const uint32_t h = have;
+        if (h == 0u) {                         // no block of the pair is in the pool
+            if (more) {
+                issue(i + 1, 0);
+                issue(i + 1, 1);
+            }
+            continue;
+        }
+        uint32_t vis[2];                       // 16 bits, a slot each
 #pragma unroll
-        for (int st = 0; st < NST; ++st) {
-            const int i = i0 + st;
-            if (i >= npairs) break;
-            const bool more = i + NST < npairs;
-            if (i == end_at) {
-                end_part(i - part_pairs, i);
-                end_at = end_at < last_end ? end_at + part_pairs : INT_MAX;
-            }
-            const uint32_t h = (have >> (2 * st)) & 3u;
-            if (h == 0u) {                     // no block of the pair is in the pool
-                if (more) {
-                    issue(i + NST, st, 0);
-                    issue(i + NST, st, 1);
-                    if ((have >> (2 * st)) & 3u) {
-                        state |= k_out(st) | v_out(st);
-                    }
-                }
-                continue;
-            }
-            uint8_t* kt = stage0 + st * L::STAGE;
-            uint32_t vis[2];                   // 16 bits, a slot each
+        for (int b = 0; b < 2; ++b) {
+            const int tok0 = walk.block(2 * i + b) * kBlockTokens;
+            const bool inner = tok0 >= row.first && tok0 + kBlockTokens <= row.len;
+            vis[b] = !((h >> b) & 1u) ? 0u : inner ? 0xffffu : visible_slots(tok0, row.len, row.first, p.sinks);
+        }
+        const bool full = (vis[0] & vis[1]) == 0xffffu;
+        if (!landed(0)) {
+            failed = true;
+            break;
+        }
+        float sc[2][4];
+        cache.scores(stage, p, sc);
+        float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int tok0 = walk.block(2 * i + b) * kBlockTokens;
-                const bool inner = tok0 >= row.first && tok0 + kBlockTokens <= row.len;
-                vis[b] = !((h >> b) & 1u) ? 0u : inner ? 0xffffu : visible_slots(tok0, row.len, row.first, p.sinks);
-            }
-            const bool full = (vis[0] & vis[1]) == 0xffffu;
-            if (!landed(st, 0)) {
-                failed = true;
-                break;
-            }
-            state &= ~k_out(st);
-            float sc[2][4];
-            cache.scores(kt, p, sc);
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (!full) {
-                    // hidden slots may hold anything: select, never multiply
-                    const bool ok0 = (vis[b] >> cache.lo()) & 1u, ok1 = (vis[b] >> cache.hi()) & 1u;
-                    sc[b][0] = ok0 ? sc[b][0] : -INFINITY;
-                    sc[b][1] = ok0 ? sc[b][1] : -INFINITY;
-                    sc[b][2] = ok1 ? sc[b][2] : -INFINITY;
-                    sc[b][3] = ok1 ? sc[b][3] : -INFINITY;
-                }
-                t0 = fmaxf(t0, fmaxf(sc[b][0], sc[b][2]));
-                t1 = fmaxf(t1, fmaxf(sc[b][1], sc[b][3]));
-            }
-            // K is read: the stage's next K tiles may land under the rest of the pair
-            __syncwarp();
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-            }
-            const float n0 = fmaxf(run.m0, t0), n1 = fmaxf(run.m1, t1);
-            // (a maximum still at -inf, from keys that score -inf, must not give inf - inf)
-            const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
-            run.al0 = fast_exp2(run.m0 - z0);
-            run.al1 = fast_exp2(run.m1 - z1);
-            run.m0 = n0;
-            run.m1 = n1;
-            float pr[2][4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                pr[b][0] = fast_exp2(sc[b][0] - z0);
-                pr[b][1] = fast_exp2(sc[b][1] - z1);
-                pr[b][2] = fast_exp2(sc[b][2] - z0);
-                pr[b][3] = fast_exp2(sc[b][3] - z1);
-            }
-            run.rescale = __any_sync(0xffffffffu, run.al0 != 1.f || run.al1 != 1.f);
-            if (more) issue(i + NST, st, 0);
-            const uint32_t h_next = more ? (have >> (2 * st)) & 3u : 0u;
-            if (h_next) state |= k_out(st);
-            if (!landed(st, 1)) {
-                failed = true;
-                break;
-            }
-            state &= ~v_out(st);
+        for (int b = 0; b < 2; ++b) {
             if (!full) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (vis[b] != 0xffffu) cache.hide(kt + (2 + b) * TILE, vis[b]);
-                fence_proxy_async_smem();      // (before the stage's next copy)
-                __syncwarp();
+                // hidden slots may hold anything: select, never multiply
+                const bool ok0 = (vis[b] >> cache.lo()) & 1u, ok1 = (vis[b] >> cache.hi()) & 1u;
+                sc[b][0] = ok0 ? sc[b][0] : -INFINITY;
+                sc[b][1] = ok0 ? sc[b][1] : -INFINITY;
+                sc[b][2] = ok1 ? sc[b][2] : -INFINITY;
+                sc[b][3] = ok1 ? sc[b][3] : -INFINITY;
             }
-            cache.pv(kt + 2 * TILE, pr, run, o);
-            __syncwarp();
-            if (more) issue(i + NST, st, 1);
-            if (h_next) state |= v_out(st);
+            t0 = fmaxf(t0, fmaxf(sc[b][0], sc[b][2]));
+            t1 = fmaxf(t1, fmaxf(sc[b][1], sc[b][3]));
         }
+        // K is read: the stage's next K tiles may land under the rest of the pair
+        __syncwarp();
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+        }
+        const float n0 = fmaxf(run.m0, t0), n1 = fmaxf(run.m1, t1);
+        // (a maximum still at -inf, from keys that score -inf, must not give inf - inf)
+        const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+        run.al0 = fast_exp2(run.m0 - z0);
+        run.al1 = fast_exp2(run.m1 - z1);
+        run.m0 = n0;
+        run.m1 = n1;
+        float pr[2][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            pr[b][0] = fast_exp2(sc[b][0] - z0);
+            pr[b][1] = fast_exp2(sc[b][1] - z1);
+            pr[b][2] = fast_exp2(sc[b][2] - z0);
+            pr[b][3] = fast_exp2(sc[b][3] - z1);
+        }
+        run.rescale = __any_sync(0xffffffffu, run.al0 != 1.f || run.al1 != 1.f);
+        if (more) issue(i + 1, 0);
+        if (!landed(1)) {
+            failed = true;
+            break;
+        }
+        if (!full) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                if (vis[b] != 0xffffu) cache.hide(stage + (2 + b) * TILE, vis[b]);
+            fence_proxy_async_smem();      // (before the stage's next copy)
+            __syncwarp();
+        }
+        cache.pv(stage + 2 * TILE, pr, run, o);
+        __syncwarp();
+        if (more) issue(i + 1, 1);
     }
     if (failed) {
         // drain every copy still in flight before the shared memory is reused
         if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
-        for (int st = 0; st < NST; ++st) {
-            if (state & k_out(st)) mbar_wait_bounded(bar0 + st * 16, (state >> (2 * st)) & 1u, kWaitLimitNs);
-            if (state & v_out(st)) mbar_wait_bounded(bar0 + st * 16 + 8, (state >> (2 * st + 1)) & 1u, kWaitLimitNs);
-        }
+        for (int half = 0; half < 2; ++half)
+            if ((in_flight >> half) & 1u) mbar_wait_bounded(bars + half * 8, (phase >> half) & 1u, kWaitLimitNs);
     }
     const int results = p.per ? min(p.per, parts - (int)blockIdx.x * p.per) : 1;
     int from = end_at == INT_MAX ? last_end : end_at - part_pairs;
@@ -1270,21 +1244,21 @@ cudaError_t launch(WParams p, int num_seqs, int threads, bool one_each, int smem
     return cudaLaunchKernelEx(&cfg, Kernel, p);
 }
 
-template <template <int> class Cache, int D, int NST>
+template <template <int> class Cache, int D>
 cudaError_t launch_cache(const WParams& p, int num_seqs, cudaStream_t stream) {
     constexpr int NW = warps_for(Cache<D>::TYPE, D);
-    using L = Layout<Cache<D>, D, NW, NST>;
-    return launch<window_decode_kernel<Cache, D, NW, NST>>(p, num_seqs, NW * 32, one_each(Cache<D>::TYPE, D), L::bytes(p.G, 1),
+    using L = Layout<Cache<D>, D, NW>;
+    return launch<window_decode_kernel<Cache, D, NW>>(p, num_seqs, NW * 32, one_each(Cache<D>::TYPE, D), L::bytes(p.G, 1),
                                                            L::bytes(p.G, 2) - L::bytes(p.G, 1), stream);
 }
 
 template <int D>
 cudaError_t launch_type(const WParams& p, pa_dtype dtype, int num_seqs, cudaStream_t stream) {
     switch (dtype) {
-        case PA_BF16: return launch_cache<Bf16Cache, D, 1>(p, num_seqs, stream);
-        case PA_FP8_E4M3: return launch_cache<Fp8Cache, D, 1>(p, num_seqs, stream);
-        case PA_FP4_E2M1: return launch_cache<Fp4Cache, D, 1>(p, num_seqs, stream);
-        case PA_F32: return launch_cache<F32Cache, D, 1>(p, num_seqs, stream);
+        case PA_BF16: return launch_cache<Bf16Cache, D>(p, num_seqs, stream);
+        case PA_FP8_E4M3: return launch_cache<Fp8Cache, D>(p, num_seqs, stream);
+        case PA_FP4_E2M1: return launch_cache<Fp4Cache, D>(p, num_seqs, stream);
+        case PA_F32: return launch_cache<F32Cache, D>(p, num_seqs, stream);
     }
     return cudaErrorInvalidValue;
 }
