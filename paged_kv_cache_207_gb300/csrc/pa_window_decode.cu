@@ -217,9 +217,9 @@ __device__ __forceinline__ void rows_to_f16(uint32_t (&qb)[KS][2], float scale, 
 //   permuted alike in the query; the tokens come in the order lo() = 4 (r / 2) + r % 2,
 //   hi() = lo() + 2, which lines the transposed probabilities up with V's 16-token rows.
 //   The key's scale multiplies its scores; the value's multiplies its probability, with a power
-//   of two c that keeps the product in f16's range whatever the values' size: below 2^12 at the
-//   largest scale of the part's first pair, so that three octaves more need no other c (a pair
-//   with a larger scale lowers c and rescales the accumulators).  f16 because its 11 bits keep
+//   of two c that keeps the product in f16's range whatever the values' size: below 2^12 at one
+//   scale of the part's first pair, so that three octaves more need no other c (a pair with a
+//   larger scale lowers c and rescales the accumulators).  f16 because its 11 bits keep
 //   a product eight times as exact as bf16 would; one below its normal range is off by at most
 //   2^-25 / c, 2^-36 of the largest scale so far.
 template <int D>
@@ -301,20 +301,18 @@ struct Fp8Cache {
             v[b][1] = vs[hi()];
         }
         float top = fmaxf(fmaxf(fabsf(v[0][0]), fabsf(v[0][1])), fmaxf(fabsf(v[1][0]), fabsf(v[1][1])));
-        if (__any_sync(0xffffffffu, unit == 0.f || top * unit >= 32768.f)) {       // rare after a part's first pair
+        // (a part's first pair: by its first scale, which every lane reads, as good as any)
+        if (unit == 0.f) unit = unit_for(*reinterpret_cast<const float*>(vt + 16 * D));
+        if (__any_sync(0xffffffffu, top * unit >= 32768.f)) {                      // rare
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            // 2^(e - 127) <= top < 2^(e - 126): top c from 2^11 on, below 2^12
-            const int e = (int)(__float_as_uint(top) >> 23);
             const float was = unit;
-            unit = exp2i(min(138 - e, 127));
-            if (was > 0.f) {
-                const float f = exp2i(exponent(unit) - exponent(was));       // exact
+            unit = unit_for(top);
+            const float f = exp2i(exponent(unit) - exponent(was));                 // exact
 #pragma unroll
-                for (int mi = 0; mi < KS; ++mi)
+            for (int mi = 0; mi < KS; ++mi)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) o[mi][x] *= f;
-            }
+                for (int x = 0; x < 4; ++x) o[mi][x] *= f;
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -338,6 +336,8 @@ struct Fp8Cache {
             }
         }
     }
+    // c for a largest scale in 2^(e - 127) .. 2^(e - 126): their product from 2^11 on, below 2^12
+    static __device__ __forceinline__ float unit_for(float top) { return exp2i(min(138 - (int)(__float_as_uint(fabsf(top)) >> 23), 127)); }
     // log2 of a power of two
     static __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
     __device__ __forceinline__ void reset() { unit = 0.f; }
