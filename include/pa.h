@@ -19,7 +19,9 @@
  * Conventions for every call
  *   - All array arguments are DEVICE pointers unless the name says "host";
  *     the caller owns and allocates every buffer.  Nothing is allocated,
- *     freed, synchronised or kept between calls by the GPU entry points.
+ *     freed or synchronised by the GPU entry points, and nothing of a call's
+ *     data is kept for the next (only the runtime's answers about the device
+ *     and the kernels are, such as how many clusters fit it).
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Calls only enqueue work; they return before it runs.
  *   - Device arrays must be 16-byte aligned.
@@ -260,7 +262,11 @@ pa_status pa_append_kv_fp8(void* k_pool, void* v_pool, const void* k_new, const 
 
 /* pa_decode_attention_fp8 -- pa_decode_attention over FP8 pools; q and out are
  * bf16, scores and the softmax in fp32, the products on the tensor cores in f16
- * (every E4M3 code is exact in f16).  Same workspace, partitions, errors. */
+ * (every E4M3 code is exact in f16).  Same workspace, partitions, errors.
+ * Range: queries go to f16 as they are (at most 65504), probabilities times 256
+ * and the value's scale: rows of V with a magnitude above 1.1e5 overflow, and a
+ * key's contribution is off by up to 5.3e-8 however small the values are.
+ * (pa_decode_attention_window has neither limit.) */
 pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, const void* v_pool,
                                   const int32_t* block_tables, const int32_t* context_lens,
                                   int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
@@ -328,7 +334,7 @@ pa_status pa_append_kv_fp4(void* k_pool, void* v_pool, const void* k_new, const 
  * bf16, scores and the softmax in fp32, the products on the tensor cores in f16
  * (every E2M1 code is exact in f16; the scales are applied in fp32, and to the
  * probabilities as powers of two).  Same workspace and errors; 2048-token
- * partitions. */
+ * partitions.  Queries go to f16 as they are (at most 65504). */
 pa_status pa_decode_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
                                   const int32_t* block_tables, const int32_t* context_lens,
                                   int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
@@ -446,11 +452,14 @@ pa_status pa_decode_attention_noalloc(void* out, const void* q, const void* k_po
  *                    the token at position p = start_pos[s] + i of sequence s
  * Plane f of every query and key head of the row is turned by p * inv_freq[f]:
  *   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin;  dims rotary_dim and up pass through.
- * Angles are exact to about 1e-7 radian at any position; the turn is computed in fp32 and
- * rounded once to the destination's type (for FP8 / FP4 pools the fp32 row is quantised
- * by the rules of pa_append_kv_fp8 / _fp4; values are never rotated).
+ * Angles of up to 1 radian per position are exact to about 1e-7 radian at any position; the
+ * turn is computed in fp32 and rounded once to the destination's type (for FP8 / FP4 pools
+ * the fp32 row is quantised by the rules of pa_append_kv_fp8 / _fp4; values are never
+ * rotated).
  * Rows must start on 16-byte boundaries and not overlap.  A row without a valid place
- * (flagged as in pa_append_kv) is skipped: neither the pools nor its q_out row change.
+ * (flagged as in pa_append_kv) is skipped: neither the pools nor its q_out row change.  Of
+ * prefix sums that fall or leave 0 .. total_new_tokens (flagged), a sequence's rows may be
+ * skipped together.
  */
 pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void* q,
                             const void* k_new, const void* v_new, int64_t q_out_stride,
@@ -474,7 +483,11 @@ pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void*
  * blocks that hold a visible position are read: the table entries between the sinks and
  * the window may be anything (blocks freed and given to others, -1).  A zero-length
  * context gives zeros.  A sequence's result does not depend on the rest of the batch (for
- * the same table width).  For f32 pools the products run on the tensor cores with every
+ * the same table width).  Queries and values may have any finite size while a value times
+ * the visible positions stays in fp32, whose sums are divided at the end.  For FP8 and FP4
+ * pools the products run in f16 with powers of two that follow the query rows and the values'
+ * scales: a key's contribution is off by at most 2^-36 of the largest visible value, besides
+ * f16's rounding of its weight.  For f32 pools the products run on the tensor cores with every
  * factor as a sum of two tf32 numbers (2^-21 of a product); stretches of a sequence that hold
  * infinities or numbers near the largest go through fp32 FMAs, more slowly.
  */

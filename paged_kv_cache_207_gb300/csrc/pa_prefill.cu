@@ -1039,7 +1039,10 @@ __global__ void __launch_bounds__(kThreadsTC, 1) prefill_tc_kernel(const PParams
             }
             // probabilities, bf16 pairs, over the first 64 columns of S_h (already read), 16
             // columns per store (32 scores: the fewest registers held beside the row); a full
-            // tile takes s c - m for two keys in one packed FFMA and sums in pairs
+            // tile takes s c - m for two keys in one packed FFMA and sums in pairs.  bf16 because the
+            // tensor cores multiply them with the cache's bf16 values; the sums take them unrounded:
+            // the roundings are of either sign and average out over the keys, and to sum the rounded
+            // ones would be two more instructions for each pair of keys in what bounds the kernel
             // (a row whose window starts in a later tile has no maximum yet: its scores are all
             // -inf, and their probabilities must be 0, not exp2(-inf + inf))
             const float m_sub = WIN && m_used == -INFINITY ? 0.f : m_used;

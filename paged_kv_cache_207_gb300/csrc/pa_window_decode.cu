@@ -39,39 +39,39 @@ constexpr float kLog2e = 1.4426950408889634f;
 //
 // Warps of a CTA.  At head_dim 64 a block is half the work and eight warps keep a CTA as short
 // as four at 128 (B, window 2048, 128 sequences, eight against four: bf16 23.8 / 25.6 us, FP8
-// 19.9 / 25.3, FP4 20.0 / 23.0; one sequence, window 512: 5.3 / 6.7).  At 128, eight win with
-// many blocks for each and many CTAs (A, window 4096: FP8, 256 sequences, 321 / 336; bf16, 16
-// sequences, 41.6 / 45.6) and lose elsewhere (window 1024: one sequence 8.8 / 7.2, 32 of them
-// 26.1 / 23.3; FP4, window 2047, 128 sequences, 90.5 / 81.0).
+// 20.8 / 26.1, FP4 20.0 / 23.0; one sequence, window 512: bf16 5.3 / 6.7, FP8 6.1 / 7.9).  At 128,
+// eight win with many blocks for each and many CTAs (A, window 4096: FP8, 256 sequences, 326 /
+// 333; bf16, 16 sequences, 41.6 / 45.6) and lose elsewhere (window 1024: one sequence, bf16 8.8 /
+// 7.2, FP8 9.7 / 7.8, bf16, 32 of them 26.1 / 23.3; FP4, window 2047, 128 sequences, 90.5 / 81.0).
 constexpr int warps_for(pa_dtype t, int head_dim) { return head_dim == 64 && t != PA_F32 ? 8 : 4; }
 // CTAs that an SM is to hold, which bounds the registers: as many as shared memory allows for
-// bf16 and f32 (A, f32, window 4096, 12 sequences: 90.6 us with 251 registers, one CTA,
-// against 116 with 168), four of FP8 and FP4, whose conversions want the warps more than the
-// registers (four against three: a mixed FP8 batch of 96 sequences 25.3 / 30.0 us, FP4 with 128
-// sequences 81.7 / 91.6).
+// bf16 and f32 (A, f32, window 4096, 12 sequences: 92 us with 255 registers, one CTA, against
+// 137 with 168), four of FP8 and FP4, whose conversions want the warps more than the registers
+// (four against three: FP8, 64 sequences of window 1024, 25.6 / 35.7 us, a mixed batch of 64 25.0 /
+// 29.7, but of 96 43.6 / 38.8; FP4 with 128 sequences 81.7 / 91.6).
 constexpr int ctas_for(pa_dtype t, int head_dim) {
     return t == PA_F32 ? (head_dim == 64 ? 3 : 1) : head_dim == 64 ? 2 : t == PA_BF16 ? 3 : 4;
 }
 // Blocks of a part, at least.  A part's end costs a warp about as much as a block or two (FP4:
 // two to four, with its scale references to set again), so longer parts are cheaper where one
 // CTA goes through all of them and shorter ones faster where CTAs share them (16 / 32 blocks, A,
-// window 1024, one sequence: bf16 7.2 / 10.7 us, FP8 8.0 / 11.5, f32 12.0 / 17.7; 64 sequences,
-// FP8: 25.4 / 24.7.  FP4, 32 / 64 blocks: window 2048, one sequence, 11.4 / 17.6, 128 of them
+// window 1024, one sequence: bf16 7.2 / 10.7 us, FP8 7.8 / 10.7, f32 12.2 / 17.4; 64 sequences,
+// FP8: 25.6 / 24.8; B, window 2048, FP8, 24 sequences 14.2 / 11.9.  FP4, 32 / 64 blocks: window 2048, one sequence, 11.4 / 17.6, 128 of them
 // 81.0 / 77.1).
 constexpr int min_part(pa_dtype t) { return t == PA_FP4_E2M1 ? 32 : 16; }
 // Pairs of blocks for each warp below which a sequence is one part, since joining parts costs
 // about 1 us (4 against 5 and 6: A, bf16, window 512, one sequence 7.3 / 7.6, 16 sequences 10.3 /
-// 8.2; window 700, one sequence 7.5 / 7.5 / 8.8; f32, window 512, one sequence 13.0 / 14.6).
+// 8.2; window 700, one sequence 7.5 / 7.5 / 8.8; f32, window 512, one sequence 12.5 / 15.7).
 constexpr int min_pairs(pa_dtype t) { return t == PA_F32 ? 4 : 5; }
 // Whether clusters are to leave an SM to each CTA: one of eight warps fills it (B, window 2048, 24
-// sequences, an SM each against as many as fit: bf16 13.0 / 14.7 us, FP8 13.4 / 15.0; 32 / 8 heads
+// sequences, an SM each against as many as fit: bf16 13.0 / 14.7 us, FP8 14.2 / 15.5; 32 / 8 heads
 // of 64, window 4096, bf16, 16 sequences, 25.1 / 29.2; but FP4, window 8192, 48 sequences of B, 46.7
 // / 38.4).
 constexpr bool one_each(pa_dtype t, int head_dim) { return head_dim == 64 && (t == PA_BF16 || t == PA_FP8_E4M3); }
 // Parts, at most.  Clusters of up to 8 find room in every part of the GPU; 16 pay only where an
 // SM holds three CTAs that are long (16 against 8: f32, 12 heads of 64, window 4096, one
-// sequence 14.2 / 15.6 us; A, window 4096, 8 sequences: bf16 27.8 / 25.5, f32 54.5 / 50.5;
-// FP8, 16 sequences, 38.4 / 29.1).
+// sequence 13.6 / 14.3 us; A, window 4096, 8 sequences: bf16 27.8 / 25.5, f32 56.0 / 52.4;
+// FP8, 16 sequences, 37.4 / 29.7).
 constexpr int most_parts(pa_dtype t, int head_dim) { return t == PA_F32 && head_dim == 64 ? 16 : 8; }
 
 struct WParams {
@@ -156,8 +156,9 @@ struct Bf16Cache {
         for (int i = lane; i < TILE / 16; i += 32)
             if (!((vis >> (i % kBlockTokens)) & 1u)) *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
-    // Probabilities are rounded to bf16 for the tensor cores, and the sums take the rounded
-    // ones, so that a weighted mean of equal values stays exact.
+    // Probabilities are rounded to bf16 for the tensor cores, whose factors have one type (f16
+    // would need every value converted and scaled), and the sums take the rounded ones, so that
+    // a weighted mean of equal values stays exact.
     __device__ __forceinline__ void pv(const uint8_t* vt, const float (&pr)[2][4], Running& run,
                                        float (&o)[KS][4]) {
         uint32_t pb[2][2];
@@ -363,9 +364,11 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
 //   a larger one), so that P_b stays at most 2^15, in f16's range.  As with FP8, f16 for its 11
 //   bits; R_b lies up to three octaves above the largest code, so a P_b below f16's normal range
 //   is off by at most 2^-25 / c_b, 2^-37 of the largest scale.
-// The bound is the integer pipe (conversions, selections, packing: half the rate of FMAs), so
-// scale codes are read as bytes (their fp32 is one multiply away, on the other pipe), and lane
-// c watches the codes of block c alone for a raise.
+// The bound is latency: an SM's 16 warps fill 60 % of the issue slots (64 sequences of window
+// 2040, 32 / 8 heads of 128), waiting for the chain conversion, product, product, sum of each 32
+// dims.  Conversions, selections and packing run at half the rate of FMAs (that pipe is 45 %
+// busy), so scale codes are read as bytes (their fp32 is one multiply away, on the other pipe),
+// and lane c watches the codes of block c alone for a raise.
 template <int D>
 struct Fp4Cache {
     static constexpr pa_dtype TYPE = PA_FP4_E2M1;
@@ -521,8 +524,8 @@ struct Fp4Cache {
 // An infinity has no such two numbers (its l is NaN), and the rounding of h takes finite numbers
 // within 2^-12 of the largest to infinity.  Either leaves its mark on the part: a score that is
 // NaN on the part's sum, a value on its outputs, which come out NaN or infinite.  Such a part of a
-// warp is done again with fp32 FMAs, token by token (a check of each pair's results instead: 20 to
-// 35 % of the time).
+// warp is done again with fp32 FMAs, token by token (a check of each pair's results instead: 10 to
+// 37 % of the time).
 struct Split { uint32_t h, l; };
 __device__ __forceinline__ Split split_tf32(float x) {
     // (integer operations: the conversion instruction runs at a fraction of their rate)

@@ -10,7 +10,7 @@ import torch
 
 import paged_kv_cache_207_gb300 as pk
 from _window_common import (BLOCK, Cache, attention, half_step, nan_like, pool_for, rope_call, rotated, visible, within)
-from test_gpu_window import cu_of, err_flag, frequencies, i32, place, rope_inputs, run_decode
+from test_gpu_window import cu_of, err_flag, frequencies, i32, place, rope_inputs, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -142,6 +142,28 @@ def test_f32_decode_of_infinities_and_the_largest_values(heads):
         if s == 0:
             want[:, :, 5] = 0
         within(out[s:s + 1], want, tol, f"sequence {s}")
+
+
+# ---------------------------------------------------------------------------- prefill
+@pytest.mark.parametrize("heads", [(4, 4, 64), (8, 2, 128)])
+@pytest.mark.parametrize("window,sinks", [(1000, 0), (70, 4), (300, 140)])
+def test_prefill_of_keys_that_score_minus_infinity(heads, window, sinks):
+    # weight 0, whole tiles of them among others and before a row's first key; rows that see no other key give zeros
+    starts, counts = [0, 300], [200, 260]
+    c = Cache("bf16", [200, 560], heads, seed=56)
+    q = (torch.rand(460, heads[0], heads[2], generator=c.g) + 0.05).to(c.wide)
+    away = [list(range(64)) + [100, 199], list(range(128, 300)) + [310, 420]]
+    for s in (0, 1):
+        for t in away[s]:
+            c.kp[int(c.tables[s, t // BLOCK]), :, :, t % BLOCK, 0] = float("-inf")
+    out = run_prefill(c, starts, counts, q, window, sinks, 0.125)
+    for s, (a, n, row) in enumerate(zip(starts, counts, (0, 200))):
+        see = visible(a + torch.arange(n), a + n, window, sinks)
+        see[:, away[s]] = False
+        k = c.k[s].clone()
+        k[away[s]] = 0
+        want, tol = attention(q[row:row + n], k, c.v[s], see, 0.125, "bf16", q.dtype)
+        within(out[row:row + n], want, tol, f"sequence {s}")
 
 
 # ---------------------------------------------------------------------------- decode: parts
