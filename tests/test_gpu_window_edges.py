@@ -65,6 +65,22 @@ def test_decode_of_values_of_any_size(cache, heads, kind):
         check_range(c, q, window, sinks, 0.1, run_decode(c, lens, q, window, sinks, 0.1))
 
 
+@pytest.mark.parametrize("cache", ["fp8", "fp4"])
+@pytest.mark.parametrize("kind", ["mixed", "rising", "falling"])
+def test_decode_of_values_of_any_size_is_the_same_in_every_batch(cache, kind):
+    # (every part starts with a reference of its own, whatever CTA does it)
+    lens, heads = [2300, 900], (32, 8, 128)
+    c = Cache(cache, lens, heads, seed=58)
+    g = torch.Generator().manual_seed(59)
+    refill(c, torch.randn(3200, 8, 128, generator=g), torch.randn(3200, 8, 128, generator=g) * sizes(kind, 3200, 8, g))
+    q = c.queries(2)
+    out = run_decode(c, lens, q, 2040, 20, 0.1)
+    for n in (1, 3, 8, 16, 40, 160):
+        at = torch.arange(n) % 2
+        many = run_decode(c, [lens[i] for i in at], q[at], 2040, 20, 0.1, tables=c.tables[at])
+        assert torch.equal(many, out[at.cuda()]), n
+
+
 def small_values_beside_a_hidden_weight(cache, d, small):
     # the first key has the largest value and no weight (a score 60 or more below the others'): what the
     # others' probabilities lose beside its scale stays within the tolerance
@@ -142,6 +158,12 @@ def test_f32_decode_of_infinities_and_the_largest_values(heads):
         if s == 0:
             want[:, :, 5] = 0
         within(out[s:s + 1], want, tol, f"sequence {s}")
+    # a part that is done again gives the same bits in batches of every size
+    for n in (1, 2, 8, 30, 200):
+        at = torch.arange(n) % 3
+        many = run_decode(c, [lens[i] for i in at], q[at], 1000, 0, 0.125, tables=c.tables[at])
+        many[at.cuda() == 0, :, 5] = 0
+        assert torch.equal(many, out.cuda()[at.cuda()]), n
 
 
 # ---------------------------------------------------------------------------- prefill
