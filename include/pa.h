@@ -519,6 +519,111 @@ pa_status pa_prefill_attention_window(void* out, const void* q, const void* k_po
                                       int32_t window, int32_t num_sinks, float scale,
                                       pa_dtype dtype, int32_t* dev_err_flag, void* stream);
 
+/*
+ * pa_rope_append_kv_axes -- pa_rope_append_kv whose rows are turned by positions of their own,
+ * on one or more axes, instead of by their place in the sequence.
+ *
+ *   positions        int32 [num_axes][total_new_tokens] (device), any values
+ *   plane_axis       int32 [rotary_dim / 2] (device): the axis of each plane, 0 .. num_axes - 1;
+ *                    may be NULL when num_axes is 1
+ * Plane f of every query and key head of row r is turned by positions[plane_axis[f]][r] *
+ * inv_freq[f]; the row still goes to position start_pos[s] + i of its sequence.  With one axis
+ * that serves the nodes of a drafted tree, which lie one behind the other but turn by their
+ * depth; with three the time, height and width of an image's or a video's tokens.  A plane whose
+ * axis is out of range sets PA_DEV_ERR_BAD_POS and is not turned.  Everything else as
+ * pa_rope_append_kv, whose result this is, bit for bit, when every axis holds the rows' places.
+ */
+pa_status pa_rope_append_kv_axes(void* k_pool, void* v_pool, void* q_out, const void* q,
+                                 const void* k_new, const void* v_new, int64_t q_out_stride,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                                 const int32_t* positions, int32_t num_axes,
+                                 const int32_t* plane_axis, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* start_pos,
+                                 const int32_t* cu_new_tokens, int32_t num_seqs,
+                                 int32_t total_new_tokens, int32_t num_blocks, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                                 int32_t* dev_err_flag, void* stream);
+
+/*
+ * pa_tree_workspace_size -- bytes of device workspace pa_tree_attention needs for trees of at
+ * most max_chunk nodes, whatever the batch and the contexts.
+ */
+size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_chunk);
+
+/*
+ * pa_tree_attention -- attention of a tree of drafted tokens over the paged cache: the nodes of
+ * sequence s have been appended at positions start_pos[s], start_pos[s] + 1, ... (in any order of
+ * the tree), and each sees the context before them and the nodes that its mask names, its ancestors
+ * and itself as a rule.
+ *
+ *   q, out           [total_q][num_q_heads][head_dim], f32 for f32 pools, bf16 otherwise; rows of
+ *                    sequence s are cu_q[s] .. cu_q[s+1]-1, node i is row cu_q[s] + i
+ *   tree_mask        int32 [total_q][mask_words] (device): bit j % 32 of word j / 32 of node i's
+ *                    row is set when it sees node j (any j, later nodes too); bits from the
+ *                    sequence's number of nodes on do not matter
+ *   max_chunk        host bound on the nodes of a sequence, at most 32 * mask_words (or total_q,
+ *                    where that is less)
+ *   dtype            of the pools: PA_F32, PA_BF16, PA_FP8_E4M3 or PA_FP4_E2M1
+ *   workspace        device scratch of at least pa_tree_workspace_size() bytes, 16-byte aligned; its
+ *                    contents on entry do not matter.  Calls sharing a workspace must not overlap
+ *                    on the GPU.
+ * Row (i, h) attends to positions t < start_pos[s] and start_pos[s] + j for the j of its mask:
+ *   out = sum_t softmax_t(scale * <q, K[t][g]>) V[t][g],  g = h / (Hq / Hkv);
+ * a row that sees nothing, or only keys that score -inf, gives zeros.  K and V are read once for
+ * all rows of a kv head (of up to 128 or 256 rows; more share them in groups).  Contexts are split
+ * over the whole GPU at places that follow from all sequences' lengths, so that the last bits of a
+ * sequence's result may depend on the batch; equal calls give equal bits.  A key or value of a node
+ * that is not finite reaches only rows that see the node.
+ * A chunk outside rows 0 .. total_q sets PA_DEV_ERR_BAD_CU and is skipped, one at positions outside
+ * the table PA_DEV_ERR_BAD_POS; nodes past max_chunk set PA_DEV_ERR_HINT: they are not computed, and
+ * not seen.  Rows of q and out past cu_q[num_seqs] (a padded batch) are neither read nor written.
+ * A table entry that is no block of the pool sets PA_DEV_ERR_BAD_BLOCK and leaves the sequence's
+ * outputs undefined.  head_dim 64 or 128; at most 8 query heads per kv head.
+ */
+pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* start_pos, const int32_t* cu_q,
+                            const int32_t* tree_mask, int32_t mask_words, int32_t num_seqs,
+                            int32_t total_q, int32_t max_chunk, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                            float scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_err_flag, void* stream);
+
+/*
+ * pa_compact_kv -- rows of a sequence, moved to consecutive positions: the accepted path of a
+ * drafted tree behind its root, or the tokens that an eviction keeps.
+ *
+ *   src_pos          int32 [total_rows] (device): row i of sequence s comes from position
+ *                    src_pos[cu_rows[s] + i], through block_tables
+ *   dst_start        int32 [num_seqs] (device): and goes to position dst_start[s] + i, through
+ *                    dst_tables
+ *   cu_rows          int32 [num_seqs + 1] (device), not falling, from 0 to at most total_rows;
+ *                    src_pos past cu_rows[num_seqs] is not read, so the counts may be known to the
+ *                    device alone
+ *   dst_tables       int32 [num_seqs][max_dst_blocks_per_seq]; NULL, or block_tables: in place.
+ *   dtype            of the pools: PA_F32, PA_BF16, PA_FP8_E4M3 or PA_FP4_E2M1
+ * Every kv head of both pools takes the row as it is stored, bit for bit (quantised rows with their
+ * scales).  In place, a row may not come from before its destination (src_pos >= dst_start + i, as
+ * increasing positions from dst_start on never do): such a row sets PA_DEV_ERR_BAD_POS and is not
+ * moved; every row is read before another takes its place.  Into other tables, the rows may come in any order
+ * and more than once, and no destination block may be a source of the same call, or the destination
+ * of another sequence.  Blocks that are written must not be shared (refcount > 1); the block
+ * manager's prepare_append gives that, and its truncate frees the blocks behind the kept rows.
+ * A position outside its table sets PA_DEV_ERR_BAD_POS, a table entry that is no block of the pool
+ * PA_DEV_ERR_BAD_BLOCK: that row is not moved (a sequence whose rows would pass its destination's
+ * table: none of it).  A sequence whose rows leave 0 .. total_rows sets PA_DEV_ERR_BAD_CU and is
+ * skipped.  head_dim 64 or 128.
+ */
+pa_status pa_compact_kv(void* k_pool, void* v_pool, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* src_pos,
+                        const int32_t* dst_start, const int32_t* cu_rows,
+                        const int32_t* dst_tables, int32_t max_dst_blocks_per_seq,
+                        int32_t num_seqs, int32_t total_rows, int32_t num_blocks,
+                        int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                        int32_t* dev_err_flag, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Host block manager (no GPU; spindle, "Paging").
  *
@@ -560,6 +665,9 @@ pa_status pa_bm_blocks_needed(const pa_block_manager* bm, int32_t seq, int32_t s
 pa_status pa_bm_prepare_append(pa_block_manager* bm, int32_t seq, int32_t start_pos,
                                int32_t num_tokens, int32_t* pairs_out, int32_t max_pairs,
                                int32_t* num_pairs_out);
+/* Cut the sequence to its first `len` tokens (at most its length): the blocks behind them lose one
+ * reference each, as after a compaction or a rejected draft. */
+pa_status pa_bm_truncate(pa_block_manager* bm, int32_t seq, int32_t len);
 /* Host array row_out (max_blocks entries) receives the block table, -1 padded. */
 pa_status pa_bm_block_table(const pa_block_manager* bm, int32_t seq, int32_t* row_out,
                             int32_t max_blocks, int32_t* num_blocks_out);

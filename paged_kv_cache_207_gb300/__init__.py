@@ -16,6 +16,9 @@ from ._native import (  # noqa: F401
     rope_append_kv, rope_append_kv_fp8, rope_append_kv_fp4,
     decode_attention_window, decode_attention_window_fp8, decode_attention_window_fp4,
     prefill_attention_window,
+    rope_append_kv_axes, rope_append_kv_axes_fp8, rope_append_kv_axes_fp4,
+    tree_attention, tree_attention_fp8, tree_attention_fp4, tree_workspace, tree_workspace_size,
+    compact_kv, compact_kv_fp8, compact_kv_fp4,
     DEV_ERR_BAD_BLOCK, DEV_ERR_BAD_POS, DEV_ERR_HINT, DEV_ERR_BAD_CU, DEV_ERR_TIMEOUT,
     DEV_ERR_BAD_PAIR, DEV_ERR_BAD_PREFIX,
 )

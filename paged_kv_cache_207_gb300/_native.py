@@ -42,7 +42,8 @@ EXPORTED = [
     "pa_append_decode_attention_fp8",
     "pa_append_kv_fp4", "pa_decode_attention_fp4",
     "pa_prefill_attention", "pa_rope_append_kv", "pa_decode_attention_window",
-    "pa_prefill_attention_window", "pa_bm_create", "pa_bm_destroy",
+    "pa_prefill_attention_window", "pa_rope_append_kv_axes", "pa_tree_workspace_size",
+    "pa_tree_attention", "pa_compact_kv", "pa_bm_truncate", "pa_bm_create", "pa_bm_destroy",
     "pa_bm_add_seq", "pa_bm_fork", "pa_bm_free_seq", "pa_bm_blocks_needed",
     "pa_bm_prepare_append", "pa_bm_block_table", "pa_bm_block_tables", "pa_bm_seq_len",
     "pa_bm_refcount", "pa_bm_stats",
@@ -123,6 +124,16 @@ def lib() -> ctypes.CDLL:
     L.pa_prefill_attention_window.argtypes = [p, p, p, p, p, i32, p, p, i32, i32, i32, i32, i32, i32,
                                               i32, i32, i32, ctypes.c_float, ctypes.c_int, p, p]
     L.pa_prefill_attention_window.restype = ctypes.c_int
+    L.pa_rope_append_kv_axes.argtypes = [p, p, p, p, p, p, i64, i64, i64, i64, p, i32, i32, p, i32, p, p, i32, p,
+                                         p, i32, i32, i32, i32, i32, i32, ctypes.c_int, p, p]
+    L.pa_rope_append_kv_axes.restype = ctypes.c_int
+    L.pa_tree_workspace_size.argtypes = [i32, i32, i32, i32]
+    L.pa_tree_workspace_size.restype = sz
+    L.pa_tree_attention.argtypes = [p, p, p, p, p, i32, p, p, p, i32, i32, i32, i32, i32, i32, i32, i32,
+                                    ctypes.c_float, ctypes.c_int, p, sz, p, p]
+    L.pa_tree_attention.restype = ctypes.c_int
+    L.pa_compact_kv.argtypes = [p, p, p, i32, p, p, p, p, i32, i32, i32, i32, i32, i32, ctypes.c_int, p, p]
+    L.pa_compact_kv.restype = ctypes.c_int
     L.pa_decode_attention_noalloc.argtypes = [p, p, p, p, p, p, i32, i32, i32, i32, i32, i32, i32,
                                               ctypes.c_float, ctypes.c_int, p, p]
     L.pa_decode_attention_noalloc.restype = ctypes.c_int
@@ -134,13 +145,14 @@ def lib() -> ctypes.CDLL:
     L.pa_bm_free_seq.argtypes = [p, i32]
     L.pa_bm_blocks_needed.argtypes = [p, i32, i32, i32, ip]
     L.pa_bm_prepare_append.argtypes = [p, i32, i32, i32, ip, i32, ip]
+    L.pa_bm_truncate.argtypes = [p, i32, i32]
     L.pa_bm_block_table.argtypes = [p, i32, ip, i32, ip]
     L.pa_bm_block_tables.argtypes = [p, ip, i32, ip, i32]
     L.pa_bm_seq_len.argtypes = [p, i32, ip]
     L.pa_bm_refcount.argtypes = [p, i32, ip]
     L.pa_bm_stats.argtypes = [p, ctypes.POINTER(BmStats)]
     for n in ("pa_bm_create", "pa_bm_add_seq", "pa_bm_fork", "pa_bm_free_seq",
-              "pa_bm_blocks_needed", "pa_bm_prepare_append", "pa_bm_block_table",
+              "pa_bm_blocks_needed", "pa_bm_prepare_append", "pa_bm_truncate", "pa_bm_block_table",
               "pa_bm_block_tables",
               "pa_bm_seq_len", "pa_bm_refcount", "pa_bm_stats"):
         getattr(L, n).restype = ctypes.c_int
@@ -152,7 +164,8 @@ def lib() -> ctypes.CDLL:
     if quick.torch_version != torch.__version__:        # compiled for another torch: its tensors are laid out otherwise
         return L
     quick.bind(*(ctypes.cast(f, p).value for f in (L.pa_rope_append_kv, L.pa_decode_attention_window,
-                                                   L.pa_prefill_attention_window)))
+                                                   L.pa_prefill_attention_window, L.pa_rope_append_kv_axes,
+                                                   L.pa_tree_attention, L.pa_compact_kv)))
     _quick = quick
     return L
 
@@ -519,7 +532,7 @@ def _flag(dev, err_flag):
 
 
 def _rope_append(pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos,
-                 cu_new_tokens, interleaved, err_flag, stream) -> None:
+                 cu_new_tokens, interleaved, err_flag, stream, axes=None) -> None:
     nb, hkv, d, code, rows = pool(k_pool)
     if q is None or q_out is None:
         if q is not q_out:
@@ -567,10 +580,21 @@ def _rope_append(pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_t
         _checked(dev, block_tables, "block_tables", _I32, (s, width))
         _checked(dev, start_pos, "start_pos", _I32, (s,))
         _checked(dev, cu_new_tokens, "cu_new_tokens", _I32, (s + 1,))
-    _call_on(dev, stream, lib().pa_rope_append_kv, k_pool.data_ptr(), v_pool.data_ptr(),
+    fn, more = lib().pa_rope_append_kv, ()
+    if axes is not None:
+        plane_axis, positions = axes
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 2 or positions.shape[0] < 1:
+            raise ValueError("positions must be an int32 [axes][tokens] tensor")
+        num = positions.shape[0]
+        at = _checked(dev, positions, "positions", _I32, (num, n))
+        if plane_axis is None and num > 1:
+            raise ValueError("plane_axis must name the axis of each plane where there are several")
+        fn, more = lib().pa_rope_append_kv_axes, (
+            at, num, None if plane_axis is None else _checked(dev, plane_axis, "plane_axis", _I32, (half,)))
+    _call_on(dev, stream, fn, k_pool.data_ptr(), v_pool.data_ptr(),
              q_out.data_ptr() if with_q else None, q.data_ptr() if with_q else None, k_new.data_ptr(),
              v_new.data_ptr(), o_row, q_row, k_row, v_row, inv_freq.data_ptr(), _bound(2 * half),
-             1 if interleaved else 0, block_tables.data_ptr(), width, start_pos.data_ptr(),
+             1 if interleaved else 0, *more, block_tables.data_ptr(), width, start_pos.data_ptr(),
              cu_new_tokens.data_ptr(), s, n, nb, hq if with_q else 0, hkv, d, code,
              None if err_flag is None else _flag(dev, err_flag))
 
@@ -615,6 +639,152 @@ def rope_append_kv_fp4(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_t
                      start_pos, cu_new_tokens, interleaved, err_flag, stream)
     elif status:
         check("pa_rope_append_kv", status)
+
+
+def _rope_axes(kind, pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+               start_pos, cu_new_tokens, interleaved, err_flag, stream) -> None:
+    status = -1 if _quick is None else _quick.rope_axes(
+        kind, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables, start_pos,
+        cu_new_tokens, interleaved, err_flag, stream)
+    if status == -1:
+        _rope_append(pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, block_tables, start_pos, cu_new_tokens,
+                     interleaved, err_flag, stream, (plane_axis, positions))
+    elif status:
+        check("pa_rope_append_kv_axes", status)
+
+
+def rope_append_kv_axes(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+                        start_pos, cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
+    """rope_append_kv whose rows are turned by positions of their own: plane f of row r by
+    positions[plane_axis[f], r] * inv_freq[f] (positions int32 [axes][tokens], plane_axis int32
+    [rotary_dim / 2], None for a single axis).  A drafted tree's nodes turn by their depth (one
+    axis), an image's tokens by time, height and width (three)."""
+    _rope_axes(0, _plain_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+               start_pos, cu_new_tokens, interleaved, err_flag, stream)
+
+
+def rope_append_kv_axes_fp8(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+                            start_pos, cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
+    """rope_append_kv_axes of bf16 rows into FP8 pools."""
+    _rope_axes(2, _fp8_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+               start_pos, cu_new_tokens, interleaved, err_flag, stream)
+
+
+def rope_append_kv_axes_fp4(k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+                            start_pos, cu_new_tokens, interleaved: bool = False, err_flag=None, stream=None) -> None:
+    """rope_append_kv_axes of bf16 rows into MXFP4 pools."""
+    _rope_axes(3, _fp4_pool, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, plane_axis, positions, block_tables,
+               start_pos, cu_new_tokens, interleaved, err_flag, stream)
+
+
+def tree_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int, max_chunk: int) -> int:
+    return int(lib().pa_tree_workspace_size(num_q_heads, num_kv_heads, head_dim, _bound(max_chunk)))
+
+
+def tree_workspace(num_q_heads: int, num_kv_heads: int, head_dim: int, max_chunk: int, device="cuda"):
+    """A workspace for tree_attention of trees of at most max_chunk nodes."""
+    return torch.empty(tree_workspace_size(num_q_heads, num_kv_heads, head_dim, max_chunk), dtype=torch.uint8, device=device)
+
+
+def _tree(kind, pool, out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk, workspace,
+          err_flag, stream) -> None:
+    status = -1 if _quick is None else _quick.tree(
+        kind, out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk, workspace, err_flag,
+        stream)
+    if status > 0:
+        check("pa_tree_attention", status)
+    if status != -1:
+        return
+    nb, hkv, d, code, rows = pool(k_pool)
+    dev = k_pool.get_device()
+    for t, name, dims in ((block_tables, "block_tables", 2), (q, "q", 3), (tree_mask, "tree_mask", 2)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name} must be a tensor of {dims} dimensions")
+    (s, width), (n, hq, _), words = block_tables.shape, q.shape, tree_mask.shape[1]
+    for t, name, dtype, of_t in ((q, "q", rows, (n, hq, d)), (out, "out", rows, (n, hq, d)),
+                                 (k_pool, "k_pool", k_pool.dtype, k_pool.shape),
+                                 (v_pool, "v_pool", k_pool.dtype, k_pool.shape),
+                                 (block_tables, "block_tables", _I32, (s, width)), (start_pos, "start_pos", _I32, (s,)),
+                                 (cu_q, "cu_q", _I32, (s + 1,)), (tree_mask, "tree_mask", _I32, (n, words))):
+        _checked(dev, t, name, dtype, of_t)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch tensor (see tree_workspace)")
+    _checked(dev, workspace, "workspace", workspace.dtype, workspace.shape)
+    _call_on(dev, stream, lib().pa_tree_attention, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+             block_tables.data_ptr(), width, start_pos.data_ptr(), cu_q.data_ptr(), tree_mask.data_ptr(), words, s, n,
+             _bound(max_chunk), hq, hkv, d, nb, float(scale), code, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), None if err_flag is None else _flag(dev, err_flag))
+
+
+def tree_attention(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk: int, workspace,
+                   err_flag=None, stream=None) -> None:
+    """Attention of drafted trees: row cu_q[s] + i of q ([total][Hq][D]), node i of sequence s at
+    position start_pos[s] + i, sees the positions before start_pos[s] and the nodes j whose bit
+    (j % 32 of word j / 32) its row of tree_mask (int32 [total][words]) sets.  No tree has more than
+    max_chunk nodes; workspace: see tree_workspace."""
+    _tree(0, _plain_pool, out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk, workspace,
+          err_flag, stream)
+
+
+def tree_attention_fp8(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk: int, workspace,
+                       err_flag=None, stream=None) -> None:
+    """tree_attention over FP8 pools (bf16 q and out)."""
+    _tree(2, _fp8_pool, out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk, workspace,
+          err_flag, stream)
+
+
+def tree_attention_fp4(out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk: int, workspace,
+                       err_flag=None, stream=None) -> None:
+    """tree_attention over MXFP4 pools (bf16 q and out)."""
+    _tree(3, _fp4_pool, out, q, k_pool, v_pool, block_tables, start_pos, cu_q, tree_mask, scale, max_chunk, workspace,
+          err_flag, stream)
+
+
+def _compact(kind, pool, k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables, err_flag, stream) -> None:
+    status = -1 if _quick is None else _quick.compact(
+        kind, k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables, err_flag, stream)
+    if status > 0:
+        check("pa_compact_kv", status)
+    if status != -1:
+        return
+    nb, hkv, d, code, _ = pool(k_pool)
+    dev = k_pool.get_device()
+    for t, name, dims in ((block_tables, "block_tables", 2), (src_pos, "src_pos", 1)) + (
+            () if dst_tables is None else ((dst_tables, "dst_tables", 2),)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name} must be a tensor of {dims} dimensions")
+    (s, width), n = block_tables.shape, src_pos.shape[0]
+    for t, name, dtype, of_t in ((k_pool, "k_pool", k_pool.dtype, k_pool.shape),
+                                 (v_pool, "v_pool", k_pool.dtype, k_pool.shape),
+                                 (block_tables, "block_tables", _I32, (s, width)), (src_pos, "src_pos", _I32, (n,)),
+                                 (dst_start, "dst_start", _I32, (s,)), (cu_rows, "cu_rows", _I32, (s + 1,))):
+        _checked(dev, t, name, dtype, of_t)
+    to = (None, 0) if dst_tables is None else (
+        _checked(dev, dst_tables, "dst_tables", _I32, (s, dst_tables.shape[1])), dst_tables.shape[1])
+    _call_on(dev, stream, lib().pa_compact_kv, k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), width,
+             src_pos.data_ptr(), dst_start.data_ptr(), cu_rows.data_ptr(), *to, s, n, nb, hkv, d, code,
+             None if err_flag is None else _flag(dev, err_flag))
+
+
+def compact_kv(k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables=None, err_flag=None,
+               stream=None) -> None:
+    """Moves rows to consecutive positions: row i of sequence s from position
+    src_pos[cu_rows[s] + i] to dst_start[s] + i.  In place (dst_tables None) a row may not come from
+    before its destination; with dst_tables ([num_seqs][width]) the rows go to blocks that are none
+    of the sources', in any order.  cu_rows may end below src_pos's length."""
+    _compact(0, _plain_pool, k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables, err_flag, stream)
+
+
+def compact_kv_fp8(k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables=None, err_flag=None,
+                   stream=None) -> None:
+    """compact_kv for FP8 pools."""
+    _compact(2, _fp8_pool, k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables, err_flag, stream)
+
+
+def compact_kv_fp4(k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables=None, err_flag=None,
+                   stream=None) -> None:
+    """compact_kv for MXFP4 pools."""
+    _compact(3, _fp4_pool, k_pool, v_pool, block_tables, src_pos, dst_start, cu_rows, dst_tables, err_flag, stream)
 
 
 def _decode_window(pool, out, q, k_pool, v_pool, block_tables, context_lens, scale, window, num_sinks,
@@ -792,6 +962,10 @@ class BlockManager:
         check("pa_bm_prepare_append", lib().pa_bm_prepare_append(
             self._h, seq, start, n, buf, cap, ctypes.byref(npairs)))
         return [(buf[2 * i], buf[2 * i + 1]) for i in range(npairs.value)]
+
+    def truncate(self, seq: int, length: int) -> None:
+        """Cuts the sequence to its first `length` tokens; the blocks behind them are let go."""
+        check("pa_bm_truncate", lib().pa_bm_truncate(self._h, seq, length))
 
     def block_table(self, seq: int, max_blocks: int) -> list:
         buf = (ctypes.c_int32 * max(max_blocks, 1))()

@@ -6,7 +6,9 @@
 #include <cmath>
 #include <cstdint>
 
+#include "pa_compact.h"
 #include "pa_internal.h"
+#include "pa_tree.h"
 #include "pa_window.h"
 
 namespace {
@@ -531,15 +533,15 @@ pa_status pa_prefill_attention(void* out, const void* q, const void* k_pool, con
     return cuda_status(pa::launch_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
-pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void* q,
-                            const void* k_new, const void* v_new, int64_t q_out_stride,
-                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
-                            const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
-                            const int32_t* block_tables, int32_t max_blocks_per_seq,
-                            const int32_t* start_pos, const int32_t* cu_new_tokens,
-                            int32_t num_seqs, int32_t total_new_tokens, int32_t num_blocks,
-                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                            pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
+// pa_rope_append_kv (num_axes 0), and its form with positions on axes.
+static pa_status rope_call(
+    void* k_pool, void* v_pool, void* q_out, const void* q, const void* k_new, const void* v_new,
+    int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride, const double* inv_freq,
+    int32_t rotary_dim, int32_t interleaved, const int32_t* positions, int32_t num_axes, const int32_t* plane_axis,
+    const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* start_pos, const int32_t* cu_new_tokens, int32_t num_seqs,
+    int32_t total_new_tokens, int32_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
     if (!dtype_ok(dtype) && dtype != PA_FP8_E4M3 && dtype != PA_FP4_E2M1) return PA_ERR_INVALID_ARG;
     if (num_seqs < 0 || total_new_tokens < 0 || num_blocks <= 0 || num_kv_heads <= 0 ||
         max_blocks_per_seq <= 0 || rotary_dim <= 0 || rotary_dim > head_dim)
@@ -554,6 +556,8 @@ pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void*
     if (!k_pool || !v_pool || !inv_freq || !block_tables || !start_pos || !cu_new_tokens)
         return PA_ERR_INVALID_ARG;
     if (total_new_tokens > 0 && (!k_new || !v_new)) return PA_ERR_INVALID_ARG;
+    if (num_axes > 0 && ((total_new_tokens > 0 && !positions) || (num_axes > 1 && !plane_axis)))
+        return PA_ERR_INVALID_ARG;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_new) || !aligned16(v_new) ||
         !aligned16(q) || !aligned16(q_out) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
         return PA_ERR_INVALID_ARG;
@@ -594,7 +598,39 @@ pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void*
     a.num_kv_heads = num_kv_heads;
     a.head_dim = head_dim;
     a.dtype = dtype;
-    return cuda_status(pa::launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+    if (num_axes == 0) return cuda_status(pa::launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+    a.positions = positions;
+    a.plane_axis = plane_axis;
+    a.num_axes = num_axes;
+    return cuda_status(pa::launch_rope_append_axes(a, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_rope_append_kv(void* k_pool, void* v_pool, void* q_out, const void* q,
+                            const void* k_new, const void* v_new, int64_t q_out_stride,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* start_pos, const int32_t* cu_new_tokens,
+                            int32_t num_seqs, int32_t total_new_tokens, int32_t num_blocks,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
+    return rope_call(k_pool, v_pool, q_out, q, k_new, v_new, q_out_stride, q_stride, k_stride, v_stride, inv_freq, rotary_dim,
+                     interleaved, nullptr, 0, nullptr, block_tables, max_blocks_per_seq, start_pos, cu_new_tokens, num_seqs,
+                     total_new_tokens, num_blocks, num_q_heads, num_kv_heads, head_dim, dtype, dev_err_flag, stream);
+}
+
+pa_status pa_rope_append_kv_axes(
+    void* k_pool, void* v_pool, void* q_out, const void* q, const void* k_new, const void* v_new,
+    int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride, const double* inv_freq,
+    int32_t rotary_dim, int32_t interleaved, const int32_t* positions, int32_t num_axes, const int32_t* plane_axis,
+    const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* start_pos, const int32_t* cu_new_tokens, int32_t num_seqs,
+    int32_t total_new_tokens, int32_t num_blocks, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    pa_dtype dtype, int32_t* dev_err_flag, void* stream) {
+    if (num_axes <= 0) return PA_ERR_INVALID_ARG;
+    return rope_call(k_pool, v_pool, q_out, q, k_new, v_new, q_out_stride, q_stride, k_stride, v_stride, inv_freq, rotary_dim,
+                     interleaved, positions, num_axes, plane_axis, block_tables, max_blocks_per_seq, start_pos, cu_new_tokens, num_seqs,
+                     total_new_tokens, num_blocks, num_q_heads, num_kv_heads, head_dim, dtype, dev_err_flag, stream);
 }
 
 pa_status pa_decode_attention_window(void* out, const void* q, const void* k_pool,
@@ -680,6 +716,109 @@ pa_status pa_prefill_attention_window(void* out, const void* q, const void* k_po
     a.num_blocks = num_blocks;
     a.scale = scale;
     return cuda_status(pa::launch_prefill_window(a, total_q, window, num_sinks, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_chunk) {
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_chunk <= 0 ||
+        num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > 8)
+        return 0;
+    return pa::tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_chunk);
+}
+
+pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* start_pos, const int32_t* cu_q,
+                            const int32_t* tree_mask, int32_t mask_words, int32_t num_seqs,
+                            int32_t total_q, int32_t max_chunk, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                            float scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_err_flag, void* stream) {
+    if (!dtype_ok(dtype) && dtype != PA_FP8_E4M3 && dtype != PA_FP4_E2M1) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_q < 0 || max_chunk < 0 || mask_words < 0 || num_q_heads <= 0 ||
+        num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || !std::isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > 8) return PA_ERR_UNSUPPORTED;
+    if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q == 0 || max_chunk == 0) return PA_OK;
+    // (no tree has more nodes than there are rows)
+    if (max_chunk > total_q) max_chunk = total_q;
+    if ((long long)mask_words * 32 < max_chunk) return PA_ERR_INVALID_ARG;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !start_pos || !cu_q || !tree_mask)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
+        return PA_ERR_INVALID_ARG;
+    const size_t need = pa::tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_chunk);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+    pa::TreeArgs a;
+    a.out = out;
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.block_tables = block_tables;
+    a.start_pos = start_pos;
+    a.cu_q = cu_q;
+    a.mask = tree_mask;
+    a.err = dev_err_flag;
+    a.workspace = workspace;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.max_chunk = max_chunk;
+    a.mask_words = mask_words;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.scale = scale;
+    a.dtype = dtype;
+    return cuda_status(pa::launch_tree_f32(a, static_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_compact_kv(void* k_pool, void* v_pool, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* src_pos,
+                        const int32_t* dst_start, const int32_t* cu_rows,
+                        const int32_t* dst_tables, int32_t max_dst_blocks_per_seq,
+                        int32_t num_seqs, int32_t total_rows, int32_t num_blocks,
+                        int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype,
+                        int32_t* dev_err_flag, void* stream) {
+    if (!dtype_ok(dtype) && dtype != PA_FP8_E4M3 && dtype != PA_FP4_E2M1) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_rows < 0 || num_blocks <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    const bool in_place = !dst_tables || dst_tables == block_tables;
+    // (the same array read with another width would be another table of the same blocks)
+    if (dst_tables == block_tables && block_tables && max_dst_blocks_per_seq != max_blocks_per_seq)
+        return PA_ERR_INVALID_ARG;
+    const int32_t dst_width = in_place ? max_blocks_per_seq : max_dst_blocks_per_seq;
+    if (dst_width <= 0 || (long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX ||
+        (long long)dst_width * pa::kBlockTokens > INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_rows == 0) return PA_OK;
+    if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (!k_pool || !v_pool || !block_tables || !src_pos || !dst_start || !cu_rows) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_ERR_INVALID_ARG;
+    pa::CompactArgs a;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.block_tables = block_tables;
+    a.dst_tables = in_place ? block_tables : dst_tables;
+    a.src_pos = src_pos;
+    a.dst_start = dst_start;
+    a.cu_rows = cu_rows;
+    a.err = dev_err_flag;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_dst_blocks = dst_width;
+    a.num_seqs = num_seqs;
+    a.total_rows = total_rows;
+    a.num_blocks = num_blocks;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.in_place = in_place;
+    a.dtype = dtype;
+    return cuda_status(pa::launch_compact(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -37,9 +37,23 @@ typedef pa_status (*prefill_fn)(void*, const void*, const void*, const void*, co
                                 const int32_t*, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t,
                                 int32_t, float, pa_dtype, int32_t*, void*);
 
+typedef pa_status (*rope_axes_fn)(void*, void*, void*, const void*, const void*, const void*, int64_t, int64_t, int64_t,
+                                  int64_t, const double*, int32_t, int32_t, const int32_t*, int32_t, const int32_t*,
+                                  const int32_t*, int32_t, const int32_t*, const int32_t*, int32_t, int32_t, int32_t,
+                                  int32_t, int32_t, int32_t, pa_dtype, int32_t*, void*);
+typedef pa_status (*tree_fn)(void*, const void*, const void*, const void*, const int32_t*, int32_t, const int32_t*,
+                             const int32_t*, const int32_t*, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t,
+                             int32_t, float, pa_dtype, void*, size_t, int32_t*, void*);
+typedef pa_status (*compact_fn)(void*, void*, const int32_t*, int32_t, const int32_t*, const int32_t*, const int32_t*,
+                                const int32_t*, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, pa_dtype, int32_t*,
+                                void*);
+
 rope_fn call_rope;
 decode_fn call_decode;
 prefill_fn call_prefill;
+rope_axes_fn call_rope_axes;
+tree_fn call_tree;
+compact_fn call_compact;
 
 struct Address {
     void* at;
@@ -213,13 +227,15 @@ int look_rows(PyObject* t, const Pools* p, int64_t n, int64_t heads, Info* x) {
     return 0;
 }
 
-/* rope_append(kind, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, tables, start, cu, interleaved, flag, stream) */
-PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
+/* rope_append(kind, k_pool, v_pool, q_out, q, k_new, v_new, inv_freq, tables, start, cu, interleaved, flag, stream), and
+ * with AXES rope_axes(.., inv_freq, plane_axis, positions, tables, ..) */
+template <bool AXES>
+PyObject* rope_rows(PyObject* const* a, Py_ssize_t n) {
     Pools p;
-    Info qo, q, k, v, freq, tables, start, cu;
+    Info qo, q, k, v, freq, tables, start, cu, axis, pos;
     int32_t* err;
     void* raw;
-    if (n != 14 || look_pools(a[1], a[2], PyLong_AsLong(a[0]), &p) < 0) return closer();
+    if (n != (AXES ? 16 : 14) || look_pools(a[1], a[2], PyLong_AsLong(a[0]), &p) < 0) return closer();
     const long dev = p.k.device;
     if (look_rows(a[5], &p, -1, p.heads, &k) < 0 || look_rows(a[6], &p, k.shape[0], p.heads, &v) < 0) return closer();
     if (a[4] == Py_None && a[3] == Py_None) {
@@ -228,8 +244,17 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
     } else if (look_rows(a[4], &p, k.shape[0], -1, &q) < 0 || look_rows(a[3], &p, k.shape[0], q.shape[1], &qo) < 0) {
         return closer();
     }
-    if (look(a[7], &freq, false) < 0 || look(a[8], &tables, false) < 0 || look(a[9], &start, false) < 0 || look(a[10], &cu, false) < 0)
-        return closer();
+    if (look(a[7], &freq, false) < 0) return closer();
+    if (AXES) {
+        if (look(a[9], &pos, false) < 0 || pos.dtype != at::kInt || pos.dims != 2 || pos.shape[1] != k.shape[0] ||
+            pos.shape[0] < 1 || !small(pos.shape[0]) || pos.device != dev)
+            return closer();
+        axis.ptr.at = nullptr;
+        if (a[8] == Py_None ? pos.shape[0] != 1 : look(a[8], &axis, false) < 0 || freq.dims != 1 || !is_vector(&axis, at::kInt, freq.shape[0], dev))
+            return closer();
+        a += 2;
+    }
+    if (look(a[8], &tables, false) < 0 || look(a[9], &start, false) < 0 || look(a[10], &cu, false) < 0) return closer();
     if (freq.dims != 1 || freq.shape[0] > 1 << 20 || !is_vector(&freq, at::kDouble, freq.shape[0], dev) || tables.dtype != at::kInt ||
         tables.dims != 2 || !small(tables.shape[0]) || !small(tables.shape[1]) || tables.device != dev ||
         !is_vector(&start, at::kInt, tables.shape[0], dev) || !is_vector(&cu, at::kInt, tables.shape[0] + 1, dev))
@@ -238,10 +263,80 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
     if (interleaved < 0 || look_rest(a[12], a[13], dev, &err, &raw) < 0) return closer();
     pa_status s;
     Py_BEGIN_ALLOW_THREADS
-    s = call_rope(p.k.ptr, p.v.ptr, qo.ptr, q.ptr, k.ptr, v.ptr, qo.stride[0], q.stride[0], k.stride[0], v.stride[0],
-                  freq.ptr, (int32_t)(2 * freq.shape[0]), interleaved, tables.ptr, (int32_t)tables.shape[1], start.ptr,
-                  cu.ptr, (int32_t)tables.shape[0], (int32_t)k.shape[0], p.blocks, (int32_t)q.shape[1], p.heads, p.dim,
-                  p.code, err, raw);
+    if (AXES)
+        s = call_rope_axes(p.k.ptr, p.v.ptr, qo.ptr, q.ptr, k.ptr, v.ptr, qo.stride[0], q.stride[0], k.stride[0], v.stride[0],
+                           freq.ptr, (int32_t)(2 * freq.shape[0]), interleaved, pos.ptr, (int32_t)pos.shape[0], axis.ptr,
+                           tables.ptr, (int32_t)tables.shape[1], start.ptr, cu.ptr, (int32_t)tables.shape[0],
+                           (int32_t)k.shape[0], p.blocks, (int32_t)q.shape[1], p.heads, p.dim, p.code, err, raw);
+    else
+        s = call_rope(p.k.ptr, p.v.ptr, qo.ptr, q.ptr, k.ptr, v.ptr, qo.stride[0], q.stride[0], k.stride[0], v.stride[0],
+                      freq.ptr, (int32_t)(2 * freq.shape[0]), interleaved, tables.ptr, (int32_t)tables.shape[1], start.ptr,
+                      cu.ptr, (int32_t)tables.shape[0], (int32_t)k.shape[0], p.blocks, (int32_t)q.shape[1], p.heads, p.dim,
+                      p.code, err, raw);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(s);
+}
+
+/* tree(kind, out, q, k_pool, v_pool, tables, start, cu, mask, scale, max_chunk, workspace, flag, stream) */
+PyObject* tree(PyObject* const* a, Py_ssize_t n) {
+    Pools p;
+    Info out, q, tables, start, cu, mask, work;
+    int32_t chunk, *err;
+    void* raw;
+    if (n != 14 || look_pools(a[3], a[4], PyLong_AsLong(a[0]), &p) < 0) return closer();
+    const long dev = p.k.device;
+    if (look(a[1], &out, false) < 0 || look(a[2], &q, false) < 0 || look(a[5], &tables, false) < 0 || look(a[6], &start, false) < 0 ||
+        look(a[7], &cu, false) < 0 || look(a[8], &mask, false) < 0 || look(a[11], &work, false) < 0)
+        return closer();
+    if (q.dtype != p.rows || out.dtype != p.rows || q.dims != 3 || out.dims != 3 || q.device != dev || out.device != dev ||
+        work.device != dev || work.dtype != at::kByte)
+        return closer();
+    int64_t bytes = 1;
+    for (int i = 0; i < work.dims; ++i) bytes *= work.shape[i];
+    for (int i = 0; i < 3; ++i)
+        if (out.shape[i] != q.shape[i] || !small(q.shape[i])) return closer();
+    if (q.shape[2] != p.dim || tables.dtype != at::kInt || tables.dims != 2 || !small(tables.shape[0]) ||
+        !small(tables.shape[1]) || tables.device != dev || !is_vector(&start, at::kInt, tables.shape[0], dev) ||
+        !is_vector(&cu, at::kInt, tables.shape[0] + 1, dev) || mask.dtype != at::kInt || mask.dims != 2 ||
+        mask.shape[0] != q.shape[0] || !small(mask.shape[1]) || mask.device != dev)
+        return closer();
+    const double scale = PyFloat_AsDouble(a[9]);
+    if (scale == -1.0 && PyErr_Occurred()) return closer();
+    if (bound_of(a[10], &chunk) < 0 || look_rest(a[12], a[13], dev, &err, &raw) < 0) return closer();
+    pa_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = call_tree(out.ptr, q.ptr, p.k.ptr, p.v.ptr, tables.ptr, (int32_t)tables.shape[1], start.ptr, cu.ptr, mask.ptr,
+                  (int32_t)mask.shape[1], (int32_t)tables.shape[0], (int32_t)q.shape[0], chunk, (int32_t)q.shape[1], p.heads,
+                  p.dim, p.blocks, (float)scale, p.code, work.ptr, (size_t)bytes, err, raw);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(s);
+}
+
+/* compact(kind, k_pool, v_pool, tables, src, dst_start, cu, dst_tables, flag, stream) */
+PyObject* compact(PyObject* const* a, Py_ssize_t n) {
+    Pools p;
+    Info tables, src, start, cu, dst;
+    int32_t* err;
+    void* raw;
+    if (n != 10 || look_pools(a[1], a[2], PyLong_AsLong(a[0]), &p) < 0) return closer();
+    const long dev = p.k.device;
+    if (look(a[3], &tables, false) < 0 || look(a[4], &src, false) < 0 || look(a[5], &start, false) < 0 || look(a[6], &cu, false) < 0)
+        return closer();
+    if (tables.dtype != at::kInt || tables.dims != 2 || !small(tables.shape[0]) || !small(tables.shape[1]) ||
+        tables.device != dev || src.dims != 1 || !small(src.shape[0]) || !is_vector(&src, at::kInt, src.shape[0], dev) ||
+        !is_vector(&start, at::kInt, tables.shape[0], dev) || !is_vector(&cu, at::kInt, tables.shape[0] + 1, dev))
+        return closer();
+    dst.ptr.at = nullptr;
+    dst.shape[1] = 0;
+    if (a[7] != Py_None && (look(a[7], &dst, false) < 0 || dst.dtype != at::kInt || dst.dims != 2 ||
+                            dst.shape[0] != tables.shape[0] || !small(dst.shape[1]) || dst.device != dev))
+        return closer();
+    if (look_rest(a[8], a[9], dev, &err, &raw) < 0) return closer();
+    pa_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = call_compact(p.k.ptr, p.v.ptr, tables.ptr, (int32_t)tables.shape[1], src.ptr, start.ptr, cu.ptr, dst.ptr,
+                     (int32_t)dst.shape[1], (int32_t)tables.shape[0], (int32_t)src.shape[0], p.blocks, p.heads, p.dim, p.code,
+                     err, raw);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(s);
 }
@@ -257,14 +352,14 @@ PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-/* bind(rope, decode, prefill): the addresses of the library's functions, once, before any other call. */
+/* bind(rope, decode, prefill, rope with axes, tree, compact): the addresses of the library's functions, once, before any other call. */
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* at[3];
-    if (n != 3) {
-        PyErr_SetString(PyExc_TypeError, "bind: three addresses");
+    void* at[6];
+    if (n != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind: six addresses");
         return nullptr;
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 6; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i]);
         if (!at[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
@@ -273,6 +368,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     call_decode = reinterpret_cast<decode_fn>(at[1]);
     call_prefill = reinterpret_cast<prefill_fn>(at[2]);
+    call_rope_axes = reinterpret_cast<rope_axes_fn>(at[3]);
+    call_tree = reinterpret_cast<tree_fn>(at[4]);
+    call_compact = reinterpret_cast<compact_fn>(at[5]);
     call_rope = reinterpret_cast<rope_fn>(at[0]);
     Py_RETURN_NONE;
 }
@@ -282,7 +380,10 @@ PyCFunction fast(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f));
 }
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
-                         {"rope_append", fast(guarded<rope_append>), METH_FASTCALL, nullptr},
+                         {"rope_append", fast(guarded<rope_rows<false>>), METH_FASTCALL, nullptr},
+                         {"rope_axes", fast(guarded<rope_rows<true>>), METH_FASTCALL, nullptr},
+                         {"tree", fast(guarded<tree>), METH_FASTCALL, nullptr},
+                         {"compact", fast(guarded<compact>), METH_FASTCALL, nullptr},
                          {"decode_window", fast(guarded<decode_window>), METH_FASTCALL, nullptr},
                          {"prefill_window", fast(guarded<prefill_window>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -151,6 +151,21 @@ pa_status pa_bm_prepare_append(pa_block_manager* bm, int32_t seq, int32_t start_
     return PA_OK;
 }
 
+pa_status pa_bm_truncate(pa_block_manager* bm, int32_t seq, int32_t len) {
+    if (!bm || len < 0) return PA_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq);
+    if (it == bm->seqs.end() || len > it->second.len) return PA_ERR_INVALID_ARG;
+    pa_block_manager::Seq& q = it->second;
+    const size_t keep = ((size_t)len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
+    while (q.table.size() > keep) {
+        bm->drop(q.table.back());
+        q.table.pop_back();
+    }
+    bm->logical_tokens -= q.len - len;
+    q.len = len;
+    return PA_OK;
+}
+
 pa_status pa_bm_block_table(const pa_block_manager* bm, int32_t seq, int32_t* row_out,
                             int32_t max_blocks, int32_t* num_blocks_out) {
     if (!bm || max_blocks < 0 || (max_blocks > 0 && !row_out)) return PA_ERR_INVALID_ARG;

@@ -1,0 +1,338 @@
+// pa_tree.cu -- attention of a tree of drafted tokens over the paged cache, f32 arithmetic.
+//
+// Row (i, h) of sequence s, the query of node i and query head h, sees the positions before
+// start_pos[s] and those nodes j, at positions start_pos[s] + j, whose bit its mask row sets:
+//   out = sum_t softmax_t(scale <q, K[t][g]>) V[t][g] over the visible t,  g = h / G.
+//
+// One pass over the keys with a running maximum and sum (f32).  A CTA keeps 32 query rows of one kv
+// head (tokens x G) in shared memory and goes through key tiles of 64 tokens: scores by register
+// tiles of 4 rows x 4 keys, the probabilities through shared memory, outputs by register tiles of
+// 4 rows x D / 16 dims, all in packed pairs of fp32 FMAs.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <type_traits>
+
+#include "pa_tc.cuh"
+#include "pa_tree.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRows = kTreeF32Rows, kKeys = 64, kThreads = 128, kMinTiles = 2;
+
+// Packed pairs of fp32: the first in the low 32 bits.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float pair_lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float pair_hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+struct Quad { uint64_t a, b; };
+__device__ __forceinline__ Quad quad_at(const float* p) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    return Quad{v.x, v.y};
+}
+
+// Four dims (4 d4 ..) of a key or value, as numbers.
+template <pa_dtype T, int D>
+__device__ __forceinline__ float4 cached(const char* rec, int slot, int d4, bool keys) {
+    float x[4];
+    if constexpr (T == PA_BF16) {
+        const uint2 v = *reinterpret_cast<const uint2*>(rec + ((d4 / 2) * kBlockTokens + slot) * 16 + (d4 & 1) * 8);
+        x[0] = bf16_lo_to_f32(v.x); x[1] = bf16_hi_to_f32(v.x);
+        x[2] = bf16_lo_to_f32(v.y); x[3] = bf16_hi_to_f32(v.y);
+    } else if constexpr (T == PA_FP8_E4M3) {
+        const float scale = *reinterpret_cast<const float*>(rec + 16 * D + 4 * slot);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int d = 4 * d4 + e;
+            const uint8_t code = keys ? rec[(d / 16) * 256 + slot * 16 + d % 16] : rec[d * 16 + slot];
+            const uint32_t h = e4m3x2_to_f16x2(code);
+            float y;
+            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(y) : "r"(h));
+            x[e] = y * scale;
+        }
+    } else {
+        const float scale = __uint_as_float((uint32_t)(uint8_t)rec[8 * D + slot * (D / 32) + d4 / 8] << 23);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int d = 4 * d4 + e;
+            uint32_t code;
+            if (keys) {
+                code = (uint8_t)rec[slot * (D / 2) + (d % 8) / 2 * (D / 8) + 2 * (d / 16) + (d % 16) / 8] >> (4 * (d & 1));
+            } else {
+                const int at = ((4 * (d % 8) + (slot % 8) / 2) * (D / 16) + d / 16) * 4 + 2 * ((d % 16) / 8) + slot / 8;
+                code = (uint8_t)rec[at] >> (4 * (slot & 1));
+            }
+            const uint32_t m = code & 7u;
+            const float mag = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
+            x[e] = ((code & 8u) ? -mag : mag) * scale;
+        }
+    }
+    return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+template <int D>
+struct F32Layout {
+    static constexpr int KS = kKeys + 1;                  // 16-byte pieces from one d4 to the next
+    static constexpr int K = 0;                           // [D / 4][KS][4]
+    static constexpr int V = K + D / 4 * KS * 16;
+    static constexpr int Q = V + D / 4 * KS * 16;         // [D / 4][kRows + 1][4]
+    static constexpr int P = Q + D / 4 * (kRows + 1) * 16;   // [kKeys][kRows]
+    static constexpr int SM = P + kKeys * kRows * 4;
+    static constexpr int BYTES = SM + (kThreads / 32 + 4) * 8;
+};
+
+template <int D, pa_dtype T>
+__global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) {
+    using L = F32Layout<D>;
+    constexpr int ND = D / 64;                            // float4 of outputs per row and thread
+    constexpr size_t REC = T == PA_F32 ? 64 * D : T == PA_BF16 ? 32 * D : T == PA_FP8_E4M3 ? 16 * D + 64 : 8 * D + D / 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* const sK = reinterpret_cast<float*>(smem + L::K);
+    float* const sV = reinterpret_cast<float*>(smem + L::V);
+    float* const sQ = reinterpret_cast<float*>(smem + L::Q);
+    float* const sP = reinterpret_cast<float*>(smem + L::P);
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    Cursor cur{};
+    const Line line = tree_locate<kThreads, kKeys, kMinTiles>(
+        p, reinterpret_cast<long long*>(smem + L::SM), blockIdx.x == 0,
+        [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
+    if ((int)blockIdx.x >= line.ctas || tree_aborted(p.err)) return;
+    long long left = line.begin(blockIdx.x + 1) - line.begin(blockIdx.x);
+    for (bool first_piece = true; left > 0; first_piece = false) {
+        const int j0 = cur.j, j1 = (int)min((long long)cur.q.tiles, cur.j + left);
+        const int tokens = item_tokens(p, cur), rows = tokens * p.G;
+        const int qrow = cur.q.q0 + cur.rt * p.TQ, end = cur.q.start + cur.q.n;
+        const int32_t* trow = p.tables + (size_t)cur.s * p.max_blocks;
+        // the query rows, zeros past the last
+        __syncthreads();
+        for (int i = tid; i < D / 4 * kRows; i += kThreads) {
+            const int d4 = i % (D / 4), r = i / (D / 4), tok = r / p.G, g = r - tok * p.G;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const size_t at = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D + 4 * d4;
+                if constexpr (T == PA_F32) {
+                    v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at);
+                    v = make_float4(bf16_lo_to_f32(u.x), bf16_hi_to_f32(u.x), bf16_lo_to_f32(u.y), bf16_hi_to_f32(u.y));
+                }
+            }
+            *reinterpret_cast<float4*>(sQ + (d4 * (kRows + 1) + r) * 4) = v;
+        }
+        float m[4], l[4];
+        uint64_t o[4][2 * ND];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 2 * ND; ++x) o[r][x] = 0ull;
+        }
+        for (int j = j0; j < j1; ++j) {
+            const int tok0 = j * kKeys;
+            // thread t: slot t % 16 of blocks t / 16 % 4, pieces from t / 64 on; keys past the last
+            // and those of a bad block count as zeros, and no row sees them
+            const int slot = tid & 15, b = (tid >> 4) & 3;
+            int32_t blk = -1;
+            if (tok0 + b * kBlockTokens < end) {
+                blk = __ldg(trow + tok0 / kBlockTokens + b);
+                if (blk < 0 || blk >= p.num_blocks) {
+                    if (slot == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+                    blk = -1;
+                }
+            }
+            const bool live = blk >= 0 && tok0 + b * kBlockTokens + slot < end;
+            const char* krec = p.k_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * REC;
+            const char* vrec = p.v_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * REC;
+            __syncthreads();                              // (the last tile's reads are done)
+#pragma unroll 4
+            for (int d4 = tid >> 6; d4 < D / 4; d4 += 2) {
+                float* k = sK + (d4 * L::KS + b * 16 + slot) * 4;
+                float* v = sV + (d4 * L::KS + b * 16 + slot) * 4;
+                if (!live) {
+                    *reinterpret_cast<float4*>(k) = *reinterpret_cast<float4*>(v) = make_float4(0.f, 0.f, 0.f, 0.f);
+                } else if constexpr (T == PA_F32) {
+                    cp_async_16(smem_u32(k), krec + (d4 * kBlockTokens + slot) * 16);
+                    cp_async_16(smem_u32(v), vrec + (d4 * kBlockTokens + slot) * 16);
+                } else {
+                    *reinterpret_cast<float4*>(k) = cached<T, D>(krec, slot, d4, true);
+                    *reinterpret_cast<float4*>(v) = cached<T, D>(vrec, slot, d4, false);
+                }
+            }
+            if constexpr (T == PA_F32) {
+                cp_async_commit();
+                cp_async_wait<0>();
+            }
+            __syncthreads();
+            // scores of rows 4 ty .. + 3 and keys tx + 16 i, in pairs of dims
+            uint64_t s2[4][4] = {};
+#pragma unroll 4
+            for (int d4 = 0; d4 < D / 4; ++d4) {
+                Quad q[4], k[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) q[r] = quad_at(sQ + (d4 * (kRows + 1) + 4 * ty + r) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) k[i] = quad_at(sK + (d4 * L::KS + tx + 16 * i) * 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        fma2(s2[r][i], q[r].a, k[i].a);
+                        fma2(s2[r][i], q[r].b, k[i].b);
+                    }
+            }
+            // hidden keys score -inf (a select: they may hold anything)
+            float s[4][4], top[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                top[r] = -INFINITY;
+                const int row = 4 * ty + r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = tok0 + tx + 16 * i;
+                    bool see = key < end;
+                    if (key >= cur.q.start && see)
+                        see = row < rows && ((uint32_t)__ldg(p.mask + (size_t)(qrow + row / p.G) * p.words + (key - cur.q.start) / 32) >>
+                                             ((key - cur.q.start) & 31)) & 1u;
+                    s[r][i] = see ? (pair_lo(s2[r][i]) + pair_hi(s2[r][i])) * p.scale_log2 : -INFINITY;
+                    top[r] = fmaxf(top[r], s[r][i]);
+                }
+            }
+            float al[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], x));
+                const float n = fmaxf(m[r], top[r]), z = n == -INFINITY ? 0.f : n;
+                al[r] = fast_exp2(m[r] - z);
+                m[r] = n;
+                l[r] *= al[r];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[r][i] = fast_exp2(s[r][i] - z);
+                    l[r] += s[r][i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(sP + (tx + 16 * i) * kRows + 4 * ty) = make_float4(s[0][i], s[1][i], s[2][i], s[3][i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint64_t a2 = pair_of(al[r], al[r]);
+#pragma unroll
+                for (int x = 0; x < 2 * ND; ++x) o[r][x] = mul2(o[r][x], a2);
+            }
+            // values of the tree's tokens that are no finite numbers must not reach the rows that do
+            // not see them (0 times an infinity): such a tile takes a select for each product
+            bool odd = false;
+            if (tok0 + kKeys > cur.q.start)
+                for (int i = tid; i < D / 4 * kKeys; i += kThreads) {
+                    const int key = tok0 + i % kKeys;
+                    const float4 v = *reinterpret_cast<const float4*>(sV + (i / kKeys * L::KS + i % kKeys) * 4);
+                    odd |= key >= cur.q.start && !(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX);
+                }
+            odd = __syncthreads_or(odd);                  // (the probabilities are in place)
+#pragma unroll 2
+            for (int k = 0; k < kKeys; ++k) {
+                const float4 pr = *reinterpret_cast<const float4*>(sP + k * kRows + 4 * ty);
+                const float pv[4] = {pr.x, pr.y, pr.z, pr.w};
+#pragma unroll
+                for (int x = 0; x < ND; ++x) {
+                    const Quad v = quad_at(sV + ((tx + 16 * x) * L::KS + k) * 4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (odd && pv[r] == 0.f) continue;
+                        const uint64_t w = pair_of(pv[r], pv[r]);
+                        fma2(o[r][2 * x], w, v.a);
+                        fma2(o[r][2 * x + 1], w, v.b);
+                    }
+                }
+            }
+        }
+        // the lanes' shares of the sums as one
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int x = 1; x < 16; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+        const bool whole = j0 == 0 && j1 == cur.q.tiles;
+        const size_t at_slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * p.slot_rows;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 4 * ty + r;
+            if (row >= rows) continue;
+            const int tok = row / p.G, g = row - tok * p.G;
+            const size_t dst = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D;
+            const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
+#pragma unroll
+            for (int x = 0; x < ND; ++x) {
+                const int d = 4 * (tx + 16 * x);
+                float4 v = make_float4(pair_lo(o[r][2 * x]), pair_hi(o[r][2 * x]), pair_lo(o[r][2 * x + 1]), pair_hi(o[r][2 * x + 1]));
+                if (!whole) {
+                    *reinterpret_cast<float4*>(p.part_o + (at_slot + row) * D + d) = v;
+                    continue;
+                }
+                v = inv != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+                if constexpr (T == PA_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst + d) = v;
+                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + dst + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            }
+            if (!whole && tx == 0) p.part_ml[at_slot + row] = make_float2(m[r], l[r]);
+        }
+        left -= j1 - j0;
+        if (left > 0) next_item<kKeys>(p, cur);
+    }
+}
+
+int tree_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 1;
+    return n;
+}
+
+template <int D, pa_dtype T>
+cudaError_t launch_f32(const TreeArgs& a, cudaStream_t stream) {
+    constexpr int smem = F32Layout<D>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(tree_f32_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(2 * tree_sms(), kTreeF32Ctas);
+    const TParams p = tree_params(a, kRows, ctas);
+    e = tree_launch(tree_f32_kernel<D, T>, dim3(ctas), kThreads, smem, stream, p);
+    if (e != cudaSuccess || ctas == 1) return e;
+    using Out = typename std::conditional<T == PA_F32, float, __nv_bfloat16>::type;
+    return tree_launch(tree_merge_kernel<D, kKeys, kMinTiles, Out>, dim3(ctas - 1, 1), kMergeThreads, 0, stream, p);
+}
+
+}  // namespace
+
+size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_chunk) {
+    const long long G = num_q_heads / num_kv_heads, rows = G * max_chunk;
+    const long long tile = tree_tile_rows(rows) / G * G, tile32 = kTreeF32Rows / G * G;
+    const long long tc = 2ll * kTreeCtas * std::min(rows, tile), f32 = 2ll * kTreeF32Ctas * std::min(rows, tile32);
+    return (size_t)std::max(tc, f32) * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_tree_f32(const TreeArgs& a, cudaStream_t stream) {
+    switch (a.dtype) {
+        case PA_F32: return a.head_dim == 64 ? launch_f32<64, PA_F32>(a, stream) : launch_f32<128, PA_F32>(a, stream);
+        case PA_BF16: return a.head_dim == 64 ? launch_f32<64, PA_BF16>(a, stream) : launch_f32<128, PA_BF16>(a, stream);
+        case PA_FP8_E4M3: return a.head_dim == 64 ? launch_f32<64, PA_FP8_E4M3>(a, stream) : launch_f32<128, PA_FP8_E4M3>(a, stream);
+        case PA_FP4_E2M1: return a.head_dim == 64 ? launch_f32<64, PA_FP4_E2M1>(a, stream) : launch_f32<128, PA_FP4_E2M1>(a, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -14,6 +14,9 @@ struct RopeArgs {
     const void* v_new;
     long long q_out_stride, q_stride, k_stride, v_stride;   // elements from row to row
     const double* inv_freq;  // [rotary_dim / 2], radians per position
+    const int32_t* positions = nullptr;    // of the form with axes: [num_axes][total_new],
+    const int32_t* plane_axis = nullptr;   // [rotary_dim / 2] or null
+    int num_axes = 0;
     const int32_t* block_tables;
     const int32_t* start_pos;
     const int32_t* cu_new;
@@ -24,6 +27,7 @@ struct RopeArgs {
     pa_dtype dtype;          // of the pools
 };
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_append_axes(const RopeArgs& a, cudaStream_t stream);
 
 // Positions of a sequence that stay visible to a row at position L - 1: the first `sinks`
 // and the last `window`.
