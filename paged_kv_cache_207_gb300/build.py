@@ -30,7 +30,8 @@ _torch = importlib.util.find_spec("torch")
 TORCH = _torch.submodule_search_locations[0] if _torch and _torch.submodule_search_locations else None
 
 SOURCES = ["pa_api.cu", "pa_decode.cu", "pa_append.cu", "pa_prefill.cu", "pa_noalloc.cu",
-           "pa_rope.cu", "pa_rope_axes.cu", "pa_window_decode.cu", "pa_tree.cu", "pa_compact.cu",
+           "pa_rope.cu", "pa_rope_axes.cu", "pa_window_decode.cu", "pa_tree.cu", "pa_tree_tc.cu",
+           "pa_compact.cu",
            "pa_block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -774,7 +774,8 @@ pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const 
     a.num_blocks = num_blocks;
     a.scale = scale;
     a.dtype = dtype;
-    return cuda_status(pa::launch_tree_f32(a, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t on = static_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == PA_F32 ? pa::launch_tree_f32(a, on) : pa::launch_tree_tc(a, on));
 }
 
 pa_status pa_compact_kv(void* k_pool, void* v_pool, const int32_t* block_tables,

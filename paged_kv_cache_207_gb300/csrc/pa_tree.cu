@@ -1,4 +1,4 @@
-// pa_tree.cu -- attention of a tree of drafted tokens over the paged cache, f32 arithmetic.
+// pa_tree.cu -- attention of a tree of drafted tokens over an f32 cache (other types: pa_tree_tc.cu).
 //
 // Row (i, h) of sequence s, the query of node i and query head h, sees the positions before
 // start_pos[s] and those nodes j, at positions start_pos[s] + j, whose bit its mask row sets:
@@ -8,11 +8,8 @@
 // head (tokens x G) in shared memory and goes through key tiles of 64 tokens: scores by register
 // tiles of 4 rows x 4 keys, the probabilities through shared memory, outputs by register tiles of
 // 4 rows x D / 16 dims, all in packed pairs of fp32 FMAs.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 #include <cfloat>
-#include <type_traits>
 
 #include "pa_tc.cuh"
 #include "pa_tree.cuh"
@@ -43,45 +40,6 @@ __device__ __forceinline__ Quad quad_at(const float* p) {
     return Quad{v.x, v.y};
 }
 
-// Four dims (4 d4 ..) of a key or value, as numbers.
-template <pa_dtype T, int D>
-__device__ __forceinline__ float4 cached(const char* rec, int slot, int d4, bool keys) {
-    float x[4];
-    if constexpr (T == PA_BF16) {
-        const uint2 v = *reinterpret_cast<const uint2*>(rec + ((d4 / 2) * kBlockTokens + slot) * 16 + (d4 & 1) * 8);
-        x[0] = bf16_lo_to_f32(v.x); x[1] = bf16_hi_to_f32(v.x);
-        x[2] = bf16_lo_to_f32(v.y); x[3] = bf16_hi_to_f32(v.y);
-    } else if constexpr (T == PA_FP8_E4M3) {
-        const float scale = *reinterpret_cast<const float*>(rec + 16 * D + 4 * slot);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int d = 4 * d4 + e;
-            const uint8_t code = keys ? rec[(d / 16) * 256 + slot * 16 + d % 16] : rec[d * 16 + slot];
-            const uint32_t h = e4m3x2_to_f16x2(code);
-            float y;
-            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(y) : "r"(h));
-            x[e] = y * scale;
-        }
-    } else {
-        const float scale = __uint_as_float((uint32_t)(uint8_t)rec[8 * D + slot * (D / 32) + d4 / 8] << 23);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int d = 4 * d4 + e;
-            uint32_t code;
-            if (keys) {
-                code = (uint8_t)rec[slot * (D / 2) + (d % 8) / 2 * (D / 8) + 2 * (d / 16) + (d % 16) / 8] >> (4 * (d & 1));
-            } else {
-                const int at = ((4 * (d % 8) + (slot % 8) / 2) * (D / 16) + d / 16) * 4 + 2 * ((d % 16) / 8) + slot / 8;
-                code = (uint8_t)rec[at] >> (4 * (slot & 1));
-            }
-            const uint32_t m = code & 7u;
-            const float mag = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-            x[e] = ((code & 8u) ? -mag : mag) * scale;
-        }
-    }
-    return make_float4(x[0], x[1], x[2], x[3]);
-}
-
 template <int D>
 struct F32Layout {
     static constexpr int KS = kKeys + 1;                  // 16-byte pieces from one d4 to the next
@@ -93,11 +51,11 @@ struct F32Layout {
     static constexpr int BYTES = SM + (kThreads / 32 + 4) * 8;
 };
 
-template <int D, pa_dtype T>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) {
     using L = F32Layout<D>;
     constexpr int ND = D / 64;                            // float4 of outputs per row and thread
-    constexpr size_t REC = T == PA_F32 ? 64 * D : T == PA_BF16 ? 32 * D : T == PA_FP8_E4M3 ? 16 * D + 64 : 8 * D + D / 2;
+    constexpr size_t TILE = kBlockTokens * D * 4;
     extern __shared__ __align__(16) uint8_t smem[];
     float* const sK = reinterpret_cast<float*>(smem + L::K);
     float* const sV = reinterpret_cast<float*>(smem + L::V);
@@ -124,12 +82,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const size_t at = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D + 4 * d4;
-                if constexpr (T == PA_F32) {
-                    v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at);
-                    v = make_float4(bf16_lo_to_f32(u.x), bf16_hi_to_f32(u.x), bf16_lo_to_f32(u.y), bf16_hi_to_f32(u.y));
-                }
+                v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
             }
             *reinterpret_cast<float4*>(sQ + (d4 * (kRows + 1) + r) * 4) = v;
         }
@@ -156,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                 }
             }
             const bool live = blk >= 0 && tok0 + b * kBlockTokens + slot < end;
-            const char* krec = p.k_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * REC;
-            const char* vrec = p.v_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * REC;
+            const char* krec = p.k_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
+            const char* vrec = p.v_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
             __syncthreads();                              // (the last tile's reads are done)
 #pragma unroll 4
             for (int d4 = tid >> 6; d4 < D / 4; d4 += 2) {
@@ -165,18 +118,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                 float* v = sV + (d4 * L::KS + b * 16 + slot) * 4;
                 if (!live) {
                     *reinterpret_cast<float4*>(k) = *reinterpret_cast<float4*>(v) = make_float4(0.f, 0.f, 0.f, 0.f);
-                } else if constexpr (T == PA_F32) {
+                } else {
                     cp_async_16(smem_u32(k), krec + (d4 * kBlockTokens + slot) * 16);
                     cp_async_16(smem_u32(v), vrec + (d4 * kBlockTokens + slot) * 16);
-                } else {
-                    *reinterpret_cast<float4*>(k) = cached<T, D>(krec, slot, d4, true);
-                    *reinterpret_cast<float4*>(v) = cached<T, D>(vrec, slot, d4, false);
                 }
             }
-            if constexpr (T == PA_F32) {
-                cp_async_commit();
-                cp_async_wait<0>();
-            }
+            cp_async_commit();
+            cp_async_wait<0>();
             __syncthreads();
             // scores of rows 4 ty .. + 3 and keys tx + 16 i, in pairs of dims
             uint64_t s2[4][4] = {};
@@ -286,8 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                     continue;
                 }
                 v = inv != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
-                if constexpr (T == PA_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst + d) = v;
-                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + dst + d) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst + d) = v;
             }
             if (!whole && tx == 0) p.part_ml[at_slot + row] = make_float2(m[r], l[r]);
         }
@@ -296,24 +243,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
     }
 }
 
-int tree_sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 1;
-    return n;
-}
-
-template <int D, pa_dtype T>
+template <int D>
 cudaError_t launch_f32(const TreeArgs& a, cudaStream_t stream) {
     constexpr int smem = F32Layout<D>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(tree_f32_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(tree_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(2 * tree_sms(), kTreeF32Ctas);
     const TParams p = tree_params(a, kRows, ctas);
-    e = tree_launch(tree_f32_kernel<D, T>, dim3(ctas), kThreads, smem, stream, p);
+    e = tree_launch(tree_f32_kernel<D>, dim3(ctas), kThreads, smem, stream, p);
     if (e != cudaSuccess || ctas == 1) return e;
-    using Out = typename std::conditional<T == PA_F32, float, __nv_bfloat16>::type;
-    return tree_launch(tree_merge_kernel<D, kKeys, kMinTiles, Out>, dim3(ctas - 1, 1), kMergeThreads, 0, stream, p);
+    return tree_launch(tree_merge_kernel<D, kKeys, kMinTiles, float>, dim3(ctas - 1, 1), kMergeThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -326,13 +265,7 @@ size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int
 }
 
 cudaError_t launch_tree_f32(const TreeArgs& a, cudaStream_t stream) {
-    switch (a.dtype) {
-        case PA_F32: return a.head_dim == 64 ? launch_f32<64, PA_F32>(a, stream) : launch_f32<128, PA_F32>(a, stream);
-        case PA_BF16: return a.head_dim == 64 ? launch_f32<64, PA_BF16>(a, stream) : launch_f32<128, PA_BF16>(a, stream);
-        case PA_FP8_E4M3: return a.head_dim == 64 ? launch_f32<64, PA_FP8_E4M3>(a, stream) : launch_f32<128, PA_FP8_E4M3>(a, stream);
-        case PA_FP4_E2M1: return a.head_dim == 64 ? launch_f32<64, PA_FP4_E2M1>(a, stream) : launch_f32<128, PA_FP4_E2M1>(a, stream);
-    }
-    return cudaErrorInvalidValue;
+    return a.head_dim == 64 ? launch_f32<64>(a, stream) : launch_f32<128>(a, stream);
 }
 
 }  // namespace pa

@@ -11,6 +11,8 @@
 // calls give equal bits.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "pa_flags.cuh"
 #include "pa_ptx.cuh"
 #include "pa_tree.h"
@@ -256,6 +258,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TParams
             for (int i = 0; i < N; i += 2) to2[i / 2] = pack_bf16x2(o[i], o[i + 1]);
         }
     }
+}
+
+inline int tree_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 1;
+    return n;
 }
 
 // Launches as a programmatic dependent of the previous kernel of the stream.

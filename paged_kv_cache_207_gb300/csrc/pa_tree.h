@@ -32,5 +32,6 @@ inline int tree_tile_rows(long long rows) { return rows > 128 ? 256 : 128; }
 size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_chunk);
 
 cudaError_t launch_tree_f32(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);      // every other type
 
 }  // namespace pa

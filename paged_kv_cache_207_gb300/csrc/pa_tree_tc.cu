@@ -1,0 +1,1063 @@
+// pa_tree_tc.cu -- attention of a tree of drafted tokens over the paged cache on the 5th-generation
+// tensor cores (bf16, FP8 and FP4 pools; the work's order: pa_tree.cuh).
+//
+// A CTA (one per SM) goes through its pieces: the rows of an item, one or two tiles of 128 (token,
+// query head) rows of a kv head, against key tiles of 128 tokens (8 blocks),
+//   S = Q K^T   into TMEM (one M128 N128 K16 MMA per 16 dims),
+//   O += P V    into TMEM (one M128 N=D K16 MMA per block, P from TMEM over S's columns),
+// with a running maximum per row that is raised only when a tile passes it by more than 2^8 (O is then
+// rescaled), one row per softmax thread.  Warps have roles: softmax (four per row tile), copies, the
+// issue of all MMAs; a piece's first copies and scores run while the piece before it ends.  Keys before
+// the tree take no mask; in the tree's own tiles a row's visible keys are its mask words, shifted to the
+// tile, two instructions per score.
+//
+// Where it is bound: a row tile costs a tile of keys 128 exponentials per row and 2 x 128 x 128 x D
+// multiplications whatever its number of rows, less time than the tile's bytes take from HBM, so up
+// to 128 rows (bf16: 256) the keys' bytes are the bound.
+//
+// bf16: K and V tiles come as they are (V's blocks by bulk copies; K's 16-byte pieces each to a
+// place of their own, so that the tile is one operand of 128 rows).
+//
+// FP8 and FP4: the records come by bulk copies and eight warps, one per block of the tile, write K
+// and V as f16 operands.  f16 holds every code exactly.  An FP4 scale is a power of two and is
+// folded in exactly; an FP8 scale is rounded to f16, and its product with a code again, each by
+// 2^-11 of the value, an eighth of what bf16 probabilities would lose: to keep FP8's scales
+// apart would cost the softmax, which is as long as the copies, two more operations per score.  A tile's K carries the power
+// of two that puts its largest scale at 1 .. 2; the tile's scores take it back.  V's power of two is
+// the piece's first tile's and changes, O with it, only when a tile's scales pass it by 2^6.
+// Probabilities are taken times 2^7, at most 2^15, so that one below f16's normal range is off by at most 2^-32 of
+// a weight of 1.  Query rows become f16 times a power of two of their own, their largest element
+// at 2^4 .. 2^5, and the row's scores give it back.
+//
+// Values of the tree's own tokens that are no finite numbers become zeros for the MMA (0 times an
+// infinity would reach the rows that do not see the token); the rows that see them add them at the end.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+
+#include "pa_tc.cuh"
+#include "pa_tree.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr uint64_t kWaitNs = 200000000ull;
+constexpr int kTileRows = 128;
+constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
+constexpr int kMinTiles = 2;
+constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at most
+
+// Warps: softmax 0 .. 4 SW - 1, the copies (bf16: V's; else all records), the MMAs, then K's copies
+// (bf16) or the conversions, filled up to whole warpgroups (setmaxnreg is collective).
+template <pa_dtype T, int SW>
+struct Roles {
+    static constexpr int SOFT = 4 * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
+    static constexpr int FEEDS = T == PA_BF16 ? (SW == 1 ? 4 : 2) : kKeyBlocks;
+    static constexpr int OTHERS = (2 + FEEDS + 3) / 4 * 4;
+    static constexpr int THREADS = (SOFT + OTHERS) * 32;
+};
+
+template <int D, pa_dtype T, int SW>
+struct Layout {
+    static constexpr int TILE = kBlockTokens * D * 2;                  // a block's K or V as an operand
+    static constexpr int KTILE = kKeyBlocks * TILE;
+    static constexpr int QTILE = kTileRows * D * 2;                    // [D/8][16][8 rows][16 B]
+    static constexpr bool RAW = T != PA_BF16;
+    static constexpr int REC = T == PA_BF16 ? TILE : T == PA_FP8_E4M3 ? 16 * D + 64 : 8 * D + D / 2;
+    static constexpr int KST = RAW ? 2 : 3, VST = RAW ? 2 : (SW == 1 || D == 64) ? 3 : 2;
+    static constexpr int RST = !RAW ? 0 : D == 64 ? 4 : T == PA_FP8_E4M3 ? 2 : 3;   // stages of records, K's then V's
+    static constexpr int Q = 0;
+    static constexpr int K = Q + SW * QTILE;
+    static constexpr int V = K + KST * KTILE;
+    static constexpr int R = V + VST * KTILE;
+    static constexpr int BAR = R + RST * 2 * kKeyBlocks * REC;
+    static constexpr int NBAR = 36;
+    // what the MMA warp passes on beside the results, and the search's scratch (once, before)
+    static constexpr int SLOT = BAR + NBAR * 8;       // TMEM address
+    static constexpr int ODD = SLOT + 16;             // [2] of a piece: values that are no finite numbers
+    static constexpr int EXPS = ODD + 16;             // [8] (K, V) exponents of a tile, as the conversions leave them
+    static constexpr int PASSED = EXPS + 64;          // [8] as the MMA warp passes them on
+    static constexpr int SEEN = PASSED + 64;          // [8][8] a tile's block has such values
+    static constexpr int BYTES0 = SEEN + 64;
+    static_assert(BYTES0 <= 232448, "shared memory of one CTA");
+    static_assert((Roles<T, SW>::THREADS / 32 + 4) * 8 <= QTILE, "the search's scratch");
+    // one CTA (and its 512 TMEM columns) to an SM
+    static constexpr int BYTES = BYTES0 < 122880 ? 122880 : BYTES0;
+};
+
+// barriers
+constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kRFull = 16, kREmpty = 20, kSFull = 24, kPFull = 26,
+              kODone = 28, kPVDone = 30, kQFull = 31, kOFree = 33, kDone = 34;
+
+constexpr uint32_t kColS = 0, kColO = 2 * kKeys;
+
+constexpr uint32_t idesc(bool f16, int N, int b_mn_major) {
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(kTileRows >> 4) << 24);
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint2 v) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float pair_lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float pair_hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Bits of the halves of a 16-bit pair whose exponent is all ones.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x, uint32_t exponent) {
+    const uint32_t e = x & exponent;
+    return ((e & 0xffffu) == (exponent & 0xffffu) ? 0xffffu : 0u) | ((e >> 16) == (exponent >> 16) ? 0xffff0000u : 0u);
+}
+
+// A run of key tiles of one item, as every role walks them.
+struct Piece {
+    Cursor c;
+    int j0, j1;              // its key tiles
+    int tokens, rows;        // of the row tile
+    int qrow;                // row of q of its first token
+    int end;                 // keys of the sequence
+    int nblk;                // blocks of them
+};
+__device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor& c, long long left) {
+    Piece x;
+    x.c = c;
+    x.j0 = c.j;
+    x.j1 = (int)min((long long)c.q.tiles, c.j + left);
+    x.tokens = item_tokens(p, c);
+    x.rows = x.tokens * p.G;
+    x.qrow = c.q.q0 + c.rt * p.TQ;
+    x.end = c.q.start + c.q.n;
+    x.nblk = (x.end + kBlockTokens - 1) / kBlockTokens;
+    return x;
+}
+struct Walk {
+    Cursor c;
+    long long left;          // tiles from the cursor on
+    __device__ __forceinline__ void next(const TParams& p, const Piece& x) {
+        left -= x.j1 - x.j0;
+        if (left > 0) next_item<kKeys>(p, c);
+    }
+};
+
+// The table of a piece in windows of 32 entries, one per lane, a window ahead of its use (read tile
+// by tile, every tile would wait for a load).
+struct Table {
+    const int32_t* row;
+    int first, nblk, lane, at;
+    int32_t now, ahead;
+    __device__ __forceinline__ int32_t fetch(int w) const {
+        const int b = first + 32 * w + lane;
+        return b < nblk ? __ldg(row + b) : -1;
+    }
+    __device__ __forceinline__ Table(const TParams& p, const Piece& x, int lane_) {
+        row = p.tables + (size_t)x.c.s * p.max_blocks;
+        first = x.j0 * kKeyBlocks;
+        nblk = x.nblk;
+        lane = lane_;
+        at = 0;
+        now = fetch(0);
+        ahead = fetch(1);
+    }
+    // Entry of block `lane % 8` of the piece's i-th tile (in order); -1: past the last, or no block of
+    // the pool (flagged).  The whole warp.
+    __device__ __forceinline__ int32_t block(const TParams& p, int i) {
+        while (i / 4 > at) {
+            now = ahead;
+            ++at;
+            ahead = fetch(at + 1);
+        }
+        const int b = lane & (kKeyBlocks - 1);
+        int32_t blk = __shfl_sync(0xffffffffu, now, (i % 4) * kKeyBlocks + b);
+        if (first + i * kKeyBlocks + b >= nblk) return -1;
+        if (blk < 0 || blk >= p.num_blocks) {
+            if (lane < kKeyBlocks) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+            blk = -1;
+        }
+        return blk;
+    }
+};
+
+// The conversions of one block of a tile by one warp: K to [D/8][8 blocks][16 slots][8 dims], V to
+// [16 token groups of 8][D/8][8 dims][8 tokens], f16.  `live`: its tokens that are keys; `own`: those of the tree.
+template <int D, pa_dtype T>
+struct Convert;
+
+template <int D>
+struct Convert<D, PA_FP8_E4M3> {
+    // Largest biased exponents of the tile's finite scales, K's and V's (keys only).
+    static __device__ __forceinline__ void exponents(uint32_t raw, uint32_t vraw, int rec, int keys, int lane, int& ek, int& ev) {
+        const uint32_t at = (lane >> 2) * rec + 16 * D + (lane & 3) * 16;
+        const uint4 k = ld_shared_v4(raw + at), v = ld_shared_v4(vraw + at);
+        const int n = keys - 4 * lane;                                     // keys of this lane's four
+        auto top = [&](uint4 x) {
+            auto e = [&](uint32_t y, int i) {
+                const uint32_t z = (y >> 23) & 0xffu;
+                return n > i && z != 0xffu ? z : 0u;
+            };
+            return max(max(e(x.x, 0), e(x.y, 1)), max(e(x.z, 2), e(x.w, 3)));
+        };
+        ek = (int)__reduce_max_sync(0xffffffffu, top(k));
+        ev = (int)__reduce_max_sync(0xffffffffu, top(v));
+    }
+    static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int ek, int lane) {
+        const int slot = lane & 15;
+        const float f = exp2i(127 - ek);
+        const float s = __uint_as_float(ld_shared_u32(raw + 16 * D + 4 * slot)) * f;
+        const uint32_t h = pack_f16x2(s, s);
+#pragma unroll
+        for (int d16 = lane >> 4; d16 < D / 16; d16 += 2) {
+            const uint4 c = ld_shared_v4(raw + (d16 * kBlockTokens + slot) * 16);
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu)), h);
+                o[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[i] >> 16)), h);
+            }
+            const uint32_t to = dst + 2 * d16 * (kKeyBlocks * 256) + slot * 16;
+            st_shared_v4(to, make_uint4(o[0], o[1], o[2], o[3]));
+            st_shared_v4(to + kKeyBlocks * 256, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+    }
+    static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, int rv, int lane, uint32_t live, uint32_t own) {
+        const float f = exp2i(127 - rv);
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 s = ld_shared_v4(raw + 16 * D + 16 * i);
+            h[2 * i] = pack_f16x2(__uint_as_float(s.x) * f, __uint_as_float(s.y) * f);
+            h[2 * i + 1] = pack_f16x2(__uint_as_float(s.z) * f, __uint_as_float(s.w) * f);
+        }
+        const bool plain = live == 0xffffu && own == 0u;
+        bool odd = false;
+#pragma unroll
+        for (int d = lane; d < D; d += 32) {
+            const uint4 c = ld_shared_v4(raw + d * 16);
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu)), h[i]);
+            if (!plain) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t bad = not_finite(o[i], 0x7c007c00u);
+                    const uint32_t mine = ((own >> (2 * i)) & 1u ? 0xffffu : 0u) | ((own >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+                    const uint32_t key = ((live >> (2 * i)) & 1u ? 0xffffu : 0u) | ((live >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+                    odd |= (bad & mine) != 0u;
+                    o[i] &= key & ~(bad & mine);
+                }
+            }
+            st_shared_v4(dst + d * 16, make_uint4(o[0], o[1], o[2], o[3]));
+            st_shared_v4(dst + D * 16 + d * 16, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+        return odd;
+    }
+};
+
+// 2^x as f16: 0 below its range, infinity above
+__device__ __forceinline__ uint32_t f16_power(int x) {
+    return x >= -14 ? (uint32_t)min(x + 15, 31) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+}
+
+template <int D>
+struct Convert<D, PA_FP4_E2M1> {
+    static constexpr int NB = D / 32;
+    static __device__ __forceinline__ void exponents(uint32_t raw, uint32_t vraw, int rec, int keys, int lane, int& ek, int& ev) {
+        // a lane has the scale codes of four tokens, NB bytes each; code 255 is no number
+        const uint32_t at = (lane >> 2) * rec + 8 * D + (lane & 3) * (4 * NB);
+        const int n = keys - 4 * lane;
+        auto bytes = [&](uint32_t x, bool key) {
+            x &= ~__vcmpeq4(x, 0xffffffffu);
+            return key ? x : 0u;
+        };
+        auto top = [&](uint32_t from) {
+            uint32_t m;
+            if constexpr (NB == 4) {
+                const uint4 x = ld_shared_v4(from + at);
+                m = __vmaxu4(__vmaxu4(bytes(x.x, n > 0), bytes(x.y, n > 1)), __vmaxu4(bytes(x.z, n > 2), bytes(x.w, n > 3)));
+            } else {
+                const uint2 x = ld_shared_v2(from + at);
+                const uint32_t lo = n > 1 ? 0xffffffffu : n > 0 ? 0xffffu : 0u, hi = n > 3 ? 0xffffffffu : n > 2 ? 0xffffu : 0u;
+                m = __vmaxu4(bytes(x.x, true) & lo, bytes(x.y, true) & hi);
+            }
+            m = __vmaxu4(m, m >> 16);
+            return max(m & 0xffu, (m >> 8) & 0xffu);
+        };
+        ek = (int)__reduce_max_sync(0xffffffffu, top(raw));
+        ev = (int)__reduce_max_sync(0xffffffffu, top(vraw));
+    }
+    static __device__ __forceinline__ uint32_t code_at(uint32_t addr) {
+        uint32_t v;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+        return v;
+    }
+    // the power of two of scale code e against the reference r (code 255: infinity)
+    static __device__ __forceinline__ uint32_t power(uint32_t e, int r) { return e == 255u ? 0x7c00u : f16_power((int)e - r); }
+    static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int ek, int lane) {
+        const int slot = lane & 15;
+#pragma unroll
+        for (int w = lane >> 4; w < NB; w += 2) {
+            const uint32_t e = power(code_at(raw + 8 * D + slot * NB + w), ek), h = e | e << 16;
+            uint32_t o[4][4];                                  // [c][piece]: dims 8 piece + 2 c, + 1
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                e2m1x8_to_f16x2x4(ld_shared_u32(raw + slot * (D / 2) + c * (D / 8) + 4 * w), o[c]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[c][i] = mul_f16x2(o[c][i], h);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                st_shared_v4(dst + (4 * w + i) * (kKeyBlocks * 256) + slot * 16, make_uint4(o[0][i], o[1][i], o[2][i], o[3][i]));
+        }
+    }
+    static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, int rv, int lane, uint32_t live, uint32_t own) {
+        const int r = lane & 7;
+        const bool plain = live == 0xffffu && own == 0u;
+        bool odd = false;
+#pragma unroll
+        for (int mi = lane >> 3; mi < D / 16; mi += 4) {
+            uint32_t o[4][4];                                  // [c][dh, half]: tokens 2 c + 8 half, + 1 of dim 16 mi + 8 dh + r
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                e2m1x8_to_f16x2x4(ld_shared_u32(raw + ((4 * r + c) * (D / 16) + mi) * 4), o[c]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int t = 2 * c + 8 * half;
+                    const uint32_t at = raw + 8 * D + t * NB + mi / 2;
+                    const uint32_t e0 = code_at(at), e1 = code_at(at + NB);
+                    uint32_t h = power(e0, rv) | power(e1, rv) << 16;
+                    if (!plain) {
+                        const bool b0 = e0 == 255u && ((own >> t) & 1u), b1 = e1 == 255u && ((own >> (t + 1)) & 1u);
+                        odd |= b0 || b1;
+                        if (b0 || !((live >> t) & 1u)) h &= 0xffff0000u;
+                        if (b1 || !((live >> (t + 1)) & 1u)) h &= 0xffffu;
+                    }
+                    o[c][half] = mul_f16x2(o[c][half], h);
+                    o[c][2 + half] = mul_f16x2(o[c][2 + half], h);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                st_shared_v4(dst + (x & 1) * (D * 16) + (16 * mi + 8 * (x >> 1) + r) * 16,
+                             make_uint4(o[0][x], o[1][x], o[2][x], o[3][x]));
+        }
+        return odd;
+    }
+};
+
+// One element of a value as a number, from the pool.
+template <int D, pa_dtype T>
+__device__ __noinline__ float value_at(const char* rec, int slot, int d) {
+    if constexpr (T == PA_BF16) {
+        return bf16_lo_to_f32(*reinterpret_cast<const uint16_t*>(rec + ((d / 8) * kBlockTokens + slot) * 16 + (d % 8) * 2));
+    } else if constexpr (T == PA_FP8_E4M3) {
+        const uint32_t code = (uint8_t)rec[d * 16 + slot];
+        // (what is asked is whether it is finite, and which infinity else)
+        const float scale = *reinterpret_cast<const float*>(rec + 16 * D + 4 * slot);
+        const float unit = (code & 0x7fu) == 0x7fu ? __int_as_float(0x7fc00000) : (code & 0x7fu) ? 1.f : 0.f;
+        return (code & 0x80u ? -unit : unit) * scale;
+    } else {
+        const uint32_t e = (uint8_t)rec[8 * D + slot * (D / 32) + d / 32];
+        if (e != 255u) return 0.f;
+        const int at = ((4 * (d % 8) + (slot % 8) / 2) * (D / 16) + d / 16) * 4 + 2 * ((d % 16) / 8) + slot / 8;
+        const uint32_t code = (uint8_t)rec[at] >> (4 * (slot & 1));
+        return (code & 7u) == 0u ? __int_as_float(0x7fc00000) : __int_as_float(code & 8u ? 0xff800000 : 0x7f800000);
+    }
+}
+
+template <int D, pa_dtype T, int SW>
+__global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const TParams p) {
+    using L = Layout<D, T, SW>;
+    using W = Roles<T, SW>;
+    constexpr bool RAW = L::RAW;
+    constexpr int TILE = L::TILE, KTILE = L::KTILE, KST = L::KST, VST = L::VST, REC = L::REC;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + L::BAR + 8u * (uint32_t)i; };
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < KST; ++i) {
+            mbar_init(bar(kKFull + i), W::FEEDS);
+            mbar_init(bar(kKEmpty + i), 1);
+        }
+#pragma unroll
+        for (int i = 0; i < VST; ++i) {
+            mbar_init(bar(kVFull + i), RAW ? W::FEEDS : 1);
+            mbar_init(bar(kVEmpty + i), 1);
+        }
+#pragma unroll
+        for (int i = 0; i < L::RST; ++i) {
+            mbar_init(bar(kRFull + i), 1);
+            mbar_init(bar(kREmpty + i), W::FEEDS);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kSFull + i), RAW ? 2 : 1);      // (RAW: the MMA warp passes the exponents on)
+            mbar_init(bar(kPFull + i), 4);
+            mbar_init(bar(kODone + i), 2);
+            mbar_init(bar(kQFull + i), 4);
+        }
+        mbar_init(bar(kPVDone), 1);
+        mbar_init(bar(kOFree), W::SOFT);
+        mbar_init(bar(kDone), 1);
+        fence_proxy_async_smem();
+    }
+    // lengths, tables, masks, queries and pools may be the previous kernels' output
+    grid_dependency_wait();
+    grid_launch_dependents();
+    Walk walk;
+    {
+        const Line line = tree_locate<W::THREADS, kKeys, kMinTiles>(
+            p, reinterpret_cast<long long*>(smem + L::Q), blockIdx.x == 0,
+            [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, walk.c);
+        walk.left = (int)blockIdx.x < line.ctas ? line.begin(blockIdx.x + 1) - line.begin(blockIdx.x) : 0;
+    }
+    // (also orders the search's scratch before the queries that take its place)
+    const bool stop = __syncthreads_or(threadIdx.x == 0 && tree_aborted(p.err));
+    if (stop || walk.left == 0) return;
+
+    if (warp >= W::SOFT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+    if (warp == W::COPY) {
+        // ------------------------------------------------------------ bulk copies
+        // bf16: V tiles, lane b block b.  Else the records of both, lane b K's and 8 + b V's.
+        const uint64_t pol = l2_policy_evict_first();
+        constexpr int ST = RAW ? L::RST : VST;
+        const int full0 = RAW ? kRFull : kVFull, empty0 = RAW ? kREmpty : kVEmpty;
+        bool ok = true;
+        int t = 0;
+        while (ok && walk.left > 0) {
+            const Piece x = piece_at(p, walk.c, walk.left);
+            Table table(p, x, lane);
+            for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
+                const int st = t % ST;
+                const int32_t blk = table.block(p, i);
+                if (t >= ST) {
+                    ok = warp_wait(bar(empty0 + st), (t / ST - 1) & 1);
+                    if (!ok) break;
+                }
+                const bool mine = blk >= 0 && lane < (RAW ? 2 * kKeyBlocks : kKeyBlocks);
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * REC;
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(bar(full0 + st), bytes);
+                }
+                __syncwarp();
+                if (mine) {
+                    const char* pool = RAW && lane < kKeyBlocks ? p.k_pool : p.v_pool;
+                    const uint32_t dst = RAW ? L::R + (st * 2 * kKeyBlocks + lane) * REC : L::V + st * KTILE + lane * TILE;
+                    bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC, REC, bar(full0 + st), pol);
+                }
+            }
+            walk.next(p, x);
+        }
+        if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+        // before the CTA ends, every copy has landed
+        if (lane == 0)
+            for (int u = max(0, t - ST); u < t; ++u) mbar_wait_bounded(bar(full0 + u % ST), (u / ST) & 1, kWaitNs);
+    } else if (warp == W::MMA) {
+        // ------------------------------------------------------------ MMA issue
+        // MMAs execute in issue order, so S(t + 2) (or S_h(t + 1) with two row tiles) overwrites
+        // P(t)'s columns only after P V(t) has read them.
+        tmem_alloc<512>(sbase + L::SLOT);
+        tc_fence_before();
+        named_bar_sync(2, 32 * (W::SOFT + 1));
+        tc_fence_after();
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::SLOT);
+        constexpr uint32_t idS = idesc(RAW, kKeys, 0), idO = idesc(RAW, D, RAW ? 0 : 1);
+        bool ok = true;
+        int t0 = 0;
+        for (int ic = 0; ok && walk.left > 0; ++ic) {
+            const Piece x = piece_at(p, walk.c, walk.left);
+            const int n = x.j1 - x.j0;
+            bool odd = false;
+            auto issue_s = [&](int hh, int i) {
+                const int t = t0 + i, buf = SW == 2 ? hh : t & 1;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t qd = umma_desc(sbase + L::Q + hh * L::QTILE, 2048, 128);
+                    const uint64_t kd = umma_desc(sbase + L::K + (t % KST) * KTILE, kKeyBlocks * 256, 128);
+                    const uint32_t dcol = tmem + kColS + (uint32_t)(buf * kKeys);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_ss(dcol, qd + (uint64_t)(ks * 256), kd + (uint64_t)((ks * 2 * kKeyBlocks * 256) >> 4), idS, ks > 0);
+                    umma_commit(bar(kSFull + buf));
+                    if constexpr (RAW) {
+                        st_shared_v2(sbase + L::PASSED + 8 * (t & 7), ld_shared_v2(sbase + L::EXPS + 8 * (t & 7)));
+                        mbar_arrive(bar(kSFull + buf));
+                    }
+                }
+                __syncwarp();
+            };
+            auto k_ready = [&](int i) { ok = warp_wait(bar(kKFull + (t0 + i) % KST), ((t0 + i) / KST) & 1); };
+            auto k_free = [&](int i) {
+                if (lane == 0) umma_commit(bar(kKEmpty + (t0 + i) % KST));
+                __syncwarp();
+            };
+            auto issue_pv = [&](int hh, int i) {
+                const int t = t0 + i, st = t % VST, buf = SW == 2 ? hh : t & 1;
+                ok = SW == 2 ? warp_wait(bar(kPFull + hh), t & 1) : warp_wait(bar(kPFull + buf), (t >> 1) & 1);
+                if (!ok) return;
+                if (i == 0 && hh == 0 && ic > 0) {
+                    ok = warp_wait(bar(kOFree), (ic - 1) & 1);            // the last piece's O is read
+                    if (!ok) return;
+                }
+                const int tok0 = (x.j0 + i) * kKeys, nb = min(kKeyBlocks, x.nblk - (x.j0 + i) * kKeyBlocks);
+                if (hh == 0) {
+                    ok = warp_wait(bar(kVFull + st), (t / VST) & 1);
+                    if (!ok) return;
+                    if constexpr (RAW) {
+                        const uint2 o = ld_shared_v2(sbase + L::SEEN + 8 * (t & 7));
+                        odd |= (o.x | o.y) != 0u;
+                    } else if (tok0 + nb * kBlockTokens > x.c.q.start) {
+                        // slots past the last key may hold anything: zeros; values of the tree's own
+                        // tokens that are no finite numbers too
+                        const int from = max(x.c.q.start - tok0, 0);
+                        for (int e = from / kBlockTokens * (D / 8) * kBlockTokens + lane; e < nb * (D / 8) * kBlockTokens; e += 32) {
+                            const int key = e / ((D / 8) * kBlockTokens) * kBlockTokens + e % kBlockTokens;
+                            if (key < from) continue;
+                            const uint32_t at = sbase + L::V + st * KTILE + e * 16;
+                            if (tok0 + key >= x.end) {
+                                st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
+                                continue;
+                            }
+                            uint4 v = ld_shared_v4(at);
+                            const uint4 bad = make_uint4(not_finite(v.x, 0x7f807f80u), not_finite(v.y, 0x7f807f80u),
+                                                         not_finite(v.z, 0x7f807f80u), not_finite(v.w, 0x7f807f80u));
+                            if ((bad.x | bad.y | bad.z | bad.w) != 0u) {
+                                odd = true;
+                                st_shared_v4(at, make_uint4(v.x & ~bad.x, v.y & ~bad.y, v.z & ~bad.z, v.w & ~bad.w));
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t pcol = tmem + kColS + (uint32_t)(buf * kKeys), ocol = tmem + kColO + (uint32_t)(hh * kKeys);
+                    // bf16: a block as stored, [D/8][16 slots][8 dims]; else [2 groups][D/8][8 dims][8 tokens]
+                    const uint64_t vd = RAW ? umma_desc(sbase + L::V + st * KTILE, D * 16, 128)
+                                            : umma_desc(sbase + L::V + st * KTILE, 128, 256);
+                    for (int b = 0; b < nb; ++b)
+                        umma_ts(ocol, pcol + 8 * b, vd + (uint64_t)((b * TILE) >> 4), idO, (i > 0 || b > 0) ? 1u : 0u);
+                    if (hh == SW - 1) umma_commit(bar(kVEmpty + st));
+                    if (SW == 1) umma_commit(bar(kPVDone));
+                }
+                __syncwarp();
+                if (i == n - 1) {
+                    odd = __any_sync(0xffffffffu, odd);
+                    if (lane == 0) {
+                        umma_commit(bar(kODone + hh));
+                        if (hh == 0) *reinterpret_cast<volatile uint32_t*>(smem + L::ODD + 4 * (ic & 1)) = odd;
+                        mbar_arrive(bar(kODone + hh));
+                    }
+                    __syncwarp();
+                }
+            };
+            if constexpr (SW == 1) {
+                ok = warp_wait(bar(kQFull), ic & 1);
+                for (int i = 0; ok && i < n + 2; ++i) {
+                    // S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
+                    if (i >= 2) issue_pv(0, i - 2);
+                    if (ok && i < n) {
+                        k_ready(i);
+                        if (!ok) break;
+                        issue_s(0, i);
+                        k_free(i);
+                    }
+                }
+            } else {
+                // S_a(0) S_b(0) | PV_a(0) S_a(1) PV_b(0) S_b(1) | ...
+                ok = warp_wait(bar(kQFull), ic & 1);
+                if (ok) k_ready(0);
+                if (ok) issue_s(0, 0);
+                if (ok) ok = warp_wait(bar(kQFull + 1), ic & 1);
+                if (ok) {
+                    issue_s(1, 0);
+                    k_free(0);
+                }
+                for (int i = 0; ok && i < n; ++i) {
+                    const bool more = i + 1 < n;
+                    issue_pv(0, i);
+                    if (ok && more) {
+                        k_ready(i + 1);
+                        if (ok) issue_s(0, i + 1);
+                    }
+                    if (ok) issue_pv(1, i);
+                    if (ok && more) {
+                        issue_s(1, i + 1);
+                        k_free(i + 1);
+                    }
+                }
+            }
+            t0 += n;
+            walk.next(p, x);
+        }
+        if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+        // nothing may still be running on the tensor cores when the TMEM is freed
+        if (lane == 0) umma_commit(bar(kDone));
+        __syncwarp();
+        mbar_wait_bounded(bar(kDone), 0, kWaitNs);
+    } else if (warp < W::FEED + W::FEEDS) {
+        const int f = warp - W::FEED;
+        if constexpr (RAW) {
+            // -------------------------------------------------------- conversions, one block of every tile
+            using C = Convert<D, T>;
+            bool ok = true;
+            int t = 0;
+            while (ok && walk.left > 0) {
+                const Piece x = piece_at(p, walk.c, walk.left);
+                int rv = 0;
+                for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
+                    const int rs = t % L::RST, ks = t % KST, vs = t % VST;
+                    ok = warp_wait(bar(kRFull + rs), (t / L::RST) & 1);
+                    if (!ok) break;
+                    const uint32_t kraw = sbase + L::R + rs * 2 * kKeyBlocks * REC, vraw = kraw + kKeyBlocks * REC;
+                    const int tok0 = (x.j0 + i) * kKeys, first = tok0 + f * kBlockTokens;
+                    int ek, ev;
+                    C::exponents(kraw, vraw, REC, x.end - tok0, lane, ek, ev);
+                    if (i == 0 || ev > rv + 6) rv = ev;
+                    if (f == 0 && lane == 0)
+                        st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
+                    if (t >= KST) {
+                        ok = warp_wait(bar(kKEmpty + ks), (t / KST - 1) & 1);
+                        if (!ok) break;
+                    }
+                    const bool any = first < x.end;
+                    if (any) C::keys(kraw + f * REC, sbase + L::K + ks * KTILE + f * 256, ek, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kKFull + ks));
+                    if (t >= VST) {
+                        ok = warp_wait(bar(kVEmpty + vs), (t / VST - 1) & 1);
+                        if (!ok) break;
+                    }
+                    bool odd = false;
+                    if (any) {
+                        const int keys = min(x.end - first, kBlockTokens), ctx = min(max(x.c.q.start - first, 0), kBlockTokens);
+                        const uint32_t live = (1u << keys) - 1u, own = live & ~((1u << ctx) - 1u);
+                        odd = C::values(vraw + f * REC, sbase + L::V + vs * KTILE + f * TILE, rv, lane, live, own);
+                    }
+                    odd = __any_sync(0xffffffffu, odd);
+                    if (lane == 0) *reinterpret_cast<volatile uint8_t*>(smem + L::SEEN + 8 * (t & 7) + f) = odd;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(kVFull + vs));
+                        mbar_arrive(bar(kREmpty + rs));
+                    }
+                }
+                walk.next(p, x);
+            }
+            if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+        } else {
+            // -------------------------------------------------------- K's pieces
+            // Tiles are published in order, each as soon as its copies have landed; a new one is issued
+            // whenever its stage is free, two ahead at most.
+            static_assert(RAW || KST <= 3, "the landing waits below cover up to two newer tiles");
+            constexpr int PER = kBlockTokens * (D / 8) / (32 * W::FEEDS);     // pieces per thread and block
+            const uint64_t pol = l2_policy_evict_first();
+            const int kt = f * 32 + lane;
+            bool ok = true;
+            int t0 = 0;
+            while (ok && walk.left > 0) {
+                const Piece x = piece_at(p, walk.c, walk.left);
+                const int n = x.j1 - x.j0;
+                Table table(p, x, lane);
+                int next = 0;
+                auto issue = [&]() {
+                    const uint32_t dst = sbase + L::K + (t0 + next) % KST * KTILE;
+                    const int32_t blk = table.block(p, next);
+#pragma unroll
+                    for (int b = 0; b < kKeyBlocks; ++b) {
+                        const int32_t bb = __shfl_sync(0xffffffffu, blk, b);
+                        if (bb < 0) continue;
+                        const char* src = p.k_pool + ((size_t)bb * p.Hkv + x.c.h) * (size_t)TILE;
+#pragma unroll
+                        for (int u = 0; u < PER; ++u) {
+                            const int piece = u * 32 * W::FEEDS + kt;
+                            cp_async_16(dst + (piece >> 4) * (kKeyBlocks * 256) + b * 256 + (piece & 15) * 16, src + piece * 16, pol);
+                        }
+                    }
+                    cp_async_commit();
+                    ++next;
+                };
+                auto free_now = [&](int t) {
+                    return t < KST || __all_sync(0xffffffffu, mbar_test(bar(kKEmpty + t % KST), (t / KST - 1) & 1));
+                };
+                for (int pub = 0; pub < n; ++pub) {
+                    while (next < n && next - pub < 2 && free_now(t0 + next)) issue();
+                    if (next == pub) {
+                        ok = warp_wait(bar(kKEmpty + (t0 + next) % KST), ((t0 + next) / KST - 1) & 1);
+                        if (!ok) break;
+                        issue();
+                    }
+                    if (next - pub - 1 >= 1) cp_async_wait<1>();
+                    else cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kKFull + (t0 + pub) % KST));
+                }
+                t0 += n;
+                walk.next(p, x);
+            }
+            if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+            cp_async_wait<0>();
+        }
+    }
+    } else {
+    // ---------------------------------------------------------------- softmax, a row per thread
+    const int row = threadIdx.x, h = warp >> 2, lr = row & (kTileRows - 1);
+    const int tl = row / p.G, g = row - tl * p.G;                     // token of the row tile, query head
+    const uint32_t qdst = sbase + L::Q + h * L::QTILE + (uint32_t)((lr >> 3) * 128 + (lr & 7) * 16);
+    const float scale = fabsf(p.scale_log2);
+    // a negative scale is applied as |scale| to -q, so that the row's maximum is that of the unscaled scores
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    constexpr int QB = D / 8;
+    // A warp without rows only keeps the barriers going.
+    auto busy = [&](const Piece& x) { return (row & ~31) < x.rows; };
+    auto load_q = [&](const Piece& x) {
+        if (!busy(x)) return;
+        if (tl < x.tokens) {
+            const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
+#pragma unroll
+            for (int u = 0; u < QB; ++u) cp_async_16(qdst + u * 2048, src + 8 * u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < QB; ++u) st_shared_v4(qdst + u * 2048, make_uint4(0u, 0u, 0u, 0u));
+        }
+        cp_async_commit();
+    };
+    float factor = scale;                                             // of the row's scores
+    auto publish_q = [&](const Piece& x) {
+        cp_async_wait<0>();
+        __syncwarp();
+        if (busy(x)) {
+            if constexpr (RAW) {
+                uint32_t top = 0u;
+#pragma unroll
+                for (int u = 0; u < QB; ++u) {
+                    const uint4 v = ld_shared_v4(qdst + u * 2048);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                }
+                top = max(top & 0xffffu, top >> 16);
+                const int shift = min(131 - (int)(top >> 7), 110);    // (2^110 makes bf16's smallest an f16)
+                const float f = exp2i(shift);
+                factor = scale * exp2i(-shift);
+#pragma unroll
+                for (int u = 0; u < QB; ++u) {
+                    const uint4 v = ld_shared_v4(qdst + u * 2048);
+                    auto half = [&](uint32_t w) { return pack_f16x2(bf16_lo_to_f32(w) * f, bf16_hi_to_f32(w) * f) ^ flip; };
+                    st_shared_v4(qdst + u * 2048, make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
+                }
+            } else if (flip) {
+#pragma unroll 1
+                for (int u = 0; u < QB; ++u) {
+                    const uint4 v = ld_shared_v4(qdst + u * 2048);
+                    st_shared_v4(qdst + u * 2048, make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQFull + h));
+    };
+    Piece x = piece_at(p, walk.c, walk.left);
+    load_q(x);
+    tc_fence_before();
+    named_bar_sync(2, 32 * (W::SOFT + 1));
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::SLOT);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t ocol = kColO + (uint32_t)(h * kKeys);
+    constexpr float kLift = RAW ? 7.f : 0.f;                          // (log2) on the probabilities
+    publish_q(x);
+    bool ok = true;
+    int t0 = 0;
+    for (int ic = 0; ok; ++ic) {
+        const int n = x.j1 - x.j0;
+        const bool live = busy(x), valid = tl < x.tokens;
+        const int32_t* mrow = p.mask + (size_t)(x.qrow + (valid ? tl : 0)) * p.words;
+        Walk ahead = walk;
+        ahead.next(p, x);
+        Piece xn = x;
+        if (ahead.left > 0) xn = piece_at(p, ahead.c, ahead.left);
+        float m_used = -INFINITY, l = 0.f;
+        int ev = 0;
+        for (int i = 0; i < n; ++i) {
+            const int t = t0 + i, sb = SW == 2 ? h : t & 1;
+            const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
+            const int tok0 = (x.j0 + i) * kKeys;
+            const bool full = tok0 + kKeys <= x.c.q.start;
+            // the visible keys of 32 columns are the bits of a word: the context's, then the row's mask
+            uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            if (!full && live) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int node = tok0 + 32 * c - x.c.q.start, left = x.c.q.n - node;
+                    uint32_t v;
+                    if (node < 0) {
+                        v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
+                    } else if (left > 0) {
+                        const uint32_t lo = (uint32_t)__ldg(mrow + node / 32);
+                        const uint32_t hi = (node & 31) != 0 && node / 32 + 1 < p.words ? (uint32_t)__ldg(mrow + node / 32 + 1) : 0u;
+                        v = __funnelshift_r(lo, hi, node & 31);
+                    } else {
+                        v = 0u;
+                    }
+                    if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
+                    see[c] = valid ? v : 0u;
+                }
+            }
+            ok = warp_wait(bar(kSFull + sb), SW == 2 ? (t & 1) : ((t >> 1) & 1));
+            if (!ok) break;
+            if (i == n - 1 && ahead.left > 0) load_q(xn);             // (the piece's scores are taken: Q is free)
+            tc_fence_after();
+            if (live) {
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(lanes + scol + 32 * c, sr[c]);
+                tmem_wait_ld();
+                float c1 = factor;
+                float drop = 1.f;                                     // what a raise of V's power of two puts on O
+                if constexpr (RAW) {
+                    const uint2 e = ld_shared_v2(sbase + L::PASSED + 8 * (t & 7));
+                    c1 *= exp2i((int)e.x - 127);
+                    if (i > 0 && (int)e.y != ev) drop = exp2i(ev - (int)e.y);
+                    ev = (int)e.y;
+                }
+                c1 = fmaxf(c1, FLT_MIN);                              // (a hidden key's -inf stays -inf under a scale of 0)
+                if (!full) {
+                    // hidden keys score -inf (a select: unread or stale columns may hold NaN)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!((see[c] >> k) & 1u)) sr[c][k] = 0xff800000u;
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) m4[c] = max3(m4[c], __uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1]));
+                const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
+                float alpha = 1.f;
+                bool raise = drop != 1.f;
+                if (mx > m_used + kRaise) {                           // (the first keys: from -inf)
+                    alpha = fast_exp2(m_used - mx);
+                    raise |= i > 0;
+                    m_used = mx;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+                    // with S double-buffered, S(t) complete does not imply P V(t - 1) complete
+                    if (SW == 1) {
+                        ok = warp_wait(bar(kPVDone), (t - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    const float on_o = alpha * drop;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(lanes + ocol + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * on_o);
+                        tmem_st32(lanes + ocol + 32 * c, o);
+                    }
+                }
+                // probabilities, rounded to the tensor cores' type (the sums take them unrounded: the
+                // roundings are of either sign and average out), over the first half of S's columns
+                const float m_sub = (m_used == -INFINITY ? 0.f : m_used) - kLift;
+                const uint64_t c2 = pair_of(c1, c1), nm2 = pair_of(-m_sub, -m_sub);
+                uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const uint64_t y = fma2(pair_of(__uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1])), c2, nm2);
+                        const float e0 = fast_exp2(pair_lo(y)), e1 = fast_exp2(pair_hi(y));
+                        sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pair_of(e0, e1));
+                        pk[k >> 1] = RAW ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+                    }
+                    tmem_st16(lanes + scol + 16 * c, pk);
+                }
+                const uint64_t sum = add2(sum2[0], sum2[1]);
+                l = l * alpha + (pair_lo(sum) + pair_hi(sum));
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kPFull + sb));
+        }
+        if (!ok) break;
+        ok = warp_wait(bar(kODone + h), ic & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+            const bool odd = *reinterpret_cast<volatile uint32_t*>(smem + L::ODD + 4 * (ic & 1)) != 0u;
+            const bool whole = x.j0 == 0 && x.j1 == x.c.q.tiles;
+            const size_t slot = (size_t)(2 * blockIdx.x + (ic == 0 ? 0 : 1)) * p.slot_rows + row;
+            const size_t orow = ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
+            // what is left on O: V's power of two, the probabilities' lift where the sums do not share it
+            const float back = RAW ? exp2i(ev - 127) : 1.f;
+            const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : exp2i(-(int)kLift);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(lanes + ocol + 32 * c, o);
+                tmem_wait_ld();
+                if (valid) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float y = __uint_as_float(o[k]) * inv;
+                    if (RAW) y *= back;
+                    o[k] = __float_as_uint(inv != 0.f ? y : 0.f);     // (no key that the row sees: O may be anything)
+                }
+                if (odd) {
+                    // the rare values that are no finite numbers, of the tokens that the row sees
+                    const int32_t* trow = p.tables + (size_t)x.c.s * p.max_blocks;
+                    for (int tok = max(x.c.q.start, x.j0 * kKeys); tok < min(x.end, x.j1 * kKeys); ++tok) {
+                        const int node = tok - x.c.q.start;
+                        if (!(((uint32_t)__ldg(mrow + node / 32) >> (node & 31)) & 1u)) continue;
+                        const int32_t blk = __ldg(trow + tok / kBlockTokens);
+                        if (blk < 0 || blk >= p.num_blocks) continue;
+                        const char* rec = p.v_pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float y = value_at<D, T>(rec, tok % kBlockTokens, 32 * c + k);
+                            if (!(fabsf(y) <= FLT_MAX)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+                        }
+                    }
+                }
+                if (whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + 32 * c);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        auto two = [&](int k) { return pack_bf16x2(__uint_as_float(o[8 * v + k]), __uint_as_float(o[8 * v + k + 1])); };
+                        dst[v] = make_uint4(two(0), two(2), two(4), two(6));
+                    }
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * D + 32 * c);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                }
+                }
+                __syncwarp();
+            }
+            if (valid && !whole) p.part_ml[slot] = make_float2(m_used, l * exp2i(-(int)kLift));
+        }
+        // O is read: the next piece's P V may start afresh
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kOFree));
+        t0 += n;
+        walk = ahead;
+        if (walk.left <= 0) break;
+        x = xn;
+        publish_q(x);
+    }
+    if (!ok) {
+        // a wait gave up: the rows of this piece and of the later ones are incomplete and become NaN
+        if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+        for (int ic = 0; walk.left > 0; ++ic) {
+            x = piece_at(p, walk.c, walk.left);
+            if (tl < x.tokens) {
+                const float nan = __int_as_float(0x7fc00000);
+                if (x.j0 != 0 || x.j1 != x.c.q.tiles) {
+                    for (int k = 0; k < 2; ++k) p.part_ml[(size_t)(2 * blockIdx.x + k) * p.slot_rows + row] = make_float2(nan, nan);
+                }
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D);
+                for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+            }
+            walk.next(p, x);
+        }
+    }
+    // (no query copy may still be landing when the CTA ends)
+    cp_async_wait<0>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W::MMA) {
+        tc_fence_after();
+        tmem_dealloc<512>(*reinterpret_cast<volatile uint32_t*>(smem + L::SLOT));
+    }
+}
+
+template <int D, pa_dtype T, int SW>
+cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
+    constexpr int smem = Layout<D, T, SW>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, T, SW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(tree_sms(), kTreeCtas);
+    const TParams p = tree_params(a, SW * kTileRows, ctas);
+    e = tree_launch(tree_tc_kernel<D, T, SW>, dim3(ctas), Roles<T, SW>::THREADS, smem, stream, p);
+    if (e != cudaSuccess || ctas == 1) return e;
+    return tree_launch(tree_merge_kernel<D, kKeys, kMinTiles, __nv_bfloat16>, dim3(ctas - 1, 2), kMergeThreads, 0, stream, p);
+}
+
+template <int D>
+cudaError_t launch_type(const TreeArgs& a, cudaStream_t stream) {
+    switch (a.dtype) {
+        case PA_BF16:
+            return tree_tile_rows((long long)a.num_q_heads / a.num_kv_heads * a.max_chunk) > kTileRows ? launch<D, PA_BF16, 2>(a, stream)
+                                                                                                    : launch<D, PA_BF16, 1>(a, stream);
+        case PA_FP8_E4M3: return launch<D, PA_FP8_E4M3, 1>(a, stream);
+        case PA_FP4_E2M1: return launch<D, PA_FP4_E2M1, 1>(a, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream) {
+    return a.head_dim == 64 ? launch_type<64>(a, stream) : launch_type<128>(a, stream);
+}
+
+}  // namespace pa
