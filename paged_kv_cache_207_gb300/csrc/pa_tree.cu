@@ -48,7 +48,7 @@ struct F32Layout {
     static constexpr int Q = V + D / 4 * KS * 16;         // [D / 4][kRows + 1][4]
     static constexpr int P = Q + D / 4 * (kRows + 1) * 16;   // [kKeys][kRows]
     static constexpr int SM = P + kKeys * kRows * 4;
-    static constexpr int BYTES = SM + (kThreads / 32 + 4) * 8;
+    static constexpr int BYTES = SM + (kThreads / 32 + 6) * 8;
 };
 
 template <int D>
@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
     const Line line = tree_locate<kThreads, kKeys, kMinTiles>(
         p, reinterpret_cast<long long*>(smem + L::SM), blockIdx.x == 0,
         [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
-    if ((int)blockIdx.x >= line.ctas || tree_aborted(p.err)) return;
+    const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
+    if (tid == 0) say_joint(p, line, cur, blockIdx.x, any);
+    if (!any || tree_aborted(p.err)) return;
     long long left = line.begin(blockIdx.x + 1) - line.begin(blockIdx.x);
     for (bool first_piece = true; left > 0; first_piece = false) {
         const int j0 = cur.j, j1 = (int)min((long long)cur.q.tiles, cur.j + left);
@@ -252,7 +254,7 @@ cudaError_t launch_f32(const TreeArgs& a, cudaStream_t stream) {
     const TParams p = tree_params(a, kRows, ctas);
     e = tree_launch(tree_f32_kernel<D>, dim3(ctas), kThreads, smem, stream, p);
     if (e != cudaSuccess || ctas == 1) return e;
-    return tree_launch(tree_merge_kernel<D, kKeys, kMinTiles, float>, dim3(ctas - 1, 1), kMergeThreads, 0, stream, p);
+    return tree_launch(tree_merge_kernel<D, float>, tree_merge_grid(p), kMergeThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -261,7 +263,7 @@ size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int
     const long long G = num_q_heads / num_kv_heads, rows = G * max_chunk;
     const long long tile = tree_tile_rows(rows) / G * G, tile32 = kTreeF32Rows / G * G;
     const long long tc = 2ll * kTreeCtas * std::min(rows, tile), f32 = 2ll * kTreeF32Ctas * std::min(rows, tile32);
-    return (size_t)std::max(tc, f32) * (head_dim + 2) * sizeof(float);
+    return (size_t)std::max(tc, f32) * (head_dim + 2) * sizeof(float) + kTreeF32Ctas * kTreeJointBytes;
 }
 
 cudaError_t launch_tree_f32(const TreeArgs& a, cudaStream_t stream) {

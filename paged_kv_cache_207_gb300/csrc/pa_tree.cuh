@@ -23,6 +23,16 @@ namespace {
 
 constexpr float kTreeLog2e = 1.4426950408889634f;
 
+// What a CTA says of the item that its first tile cuts: the CTAs that have parts of it, from its first
+// (the one before) on, and its rows.  count 0: no item, or an earlier CTA says it.
+struct Joint {
+    int count;               // parts
+    int late;                // the first part is its CTA's last piece, not its first
+    int row0, rows;          // the row of out, of all heads' rows, of its first one; and its rows
+};
+
+static_assert(sizeof(Joint) == kTreeJointBytes, "the workspace's size");
+
 struct TParams {
     void* out;
     const void* q;
@@ -35,6 +45,7 @@ struct TParams {
     int32_t* err;
     float* part_o;           // [2 CTAs][slot_rows][D]
     float2* part_ml;         // [2 CTAs][slot_rows]: maximum (log2 units) and sum
+    Joint* joints;           // [CTAs]
     int slot_rows;
     int S, total_q, max_chunk, words;
     int Hq, Hkv, G, max_blocks, num_blocks;
@@ -87,7 +98,7 @@ struct Line {
 };
 
 // The line, and the place of tile `begin_of(line)` in it where there is one (begin >= 0 and below
-// the total), found by all NT threads.  `sm`: NT / 32 + 4 words of 64 bits.
+// the total), found by all NT threads.  `sm`: NT / 32 + 6 words of 64 bits.
 template <int NT, int KT, int MIN_TILES, typename Begin>
 __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, bool report, Begin begin_of, Cursor& cur) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -122,20 +133,28 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
     long long at = before + incl - mine;
     if (begin >= at && begin < at + mine) {
         int s = s0;
-        for (; s < s1 - 1; ++s) {
-            if (each > 1) one = tree_seq<KT>(p, s);
+        for (; each > 1; ++s) {
+            one = tree_seq<KT>(p, s);
             const long long len = (long long)one.tiles * one.rts * p.Hkv;
-            if (begin < at + len) break;
+            if (begin < at + len || s + 1 >= s1) break;
             at += len;
         }
-        sm[NT / 32] = s;
-        sm[NT / 32 + 1] = begin - at;
+        // (with what is known of the sequence: the others need not read it again)
+        int* to = reinterpret_cast<int*>(sm + NT / 32 + 1);
+        sm[NT / 32] = begin - at;
+        to[0] = s;
+        to[1] = one.q0;
+        to[2] = one.n;
+        to[3] = one.start;
+        to[4] = one.tiles;
+        to[5] = one.rts;
     }
     __syncthreads();
     if (begin >= 0 && begin < total) {
-        cur.s = (int)sm[NT / 32];
-        cur.q = tree_seq<KT>(p, cur.s);
-        const long long off = sm[NT / 32 + 1];
+        const int* from = reinterpret_cast<const int*>(sm + NT / 32 + 1);
+        cur.s = from[0];
+        cur.q = TreeSeq{from[1], from[2], from[3], from[4], from[5], 0};
+        const long long off = sm[NT / 32];
         const int item = (int)(off / cur.q.tiles);
         cur.j = (int)(off - (long long)item * cur.q.tiles);
         cur.h = item / cur.q.rts;
@@ -192,72 +211,103 @@ inline TParams tree_params(const TreeArgs& a, int rows, int ctas) {
     p.scale_log2 = a.scale * kTreeLog2e;
     p.part_o = static_cast<float*>(a.workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * ctas * p.slot_rows * a.head_dim);
+    p.joints = reinterpret_cast<Joint*>(p.part_ml + (size_t)2 * ctas * p.slot_rows);
     return p;
 }
 
-// Joins the partial results of the items that CTA boundaries cut.  Block b takes the item that
-// boundary b lies in, if no earlier boundary does; blockIdx.y a share of its rows.
-constexpr int kMergeThreads = 256;
-template <int D, int KT, int MIN_TILES, typename Out>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TParams p) {
-    __shared__ long long sm[kMergeThreads / 32 + 4];
-    const int b = blockIdx.x + 1;
-    // (the lengths are no output of the kernel before, which waited for what came before it)
-    Cursor cur{};
-    const Line line = tree_locate<kMergeThreads, KT, MIN_TILES>(
-        p, sm, false, [&](const Line& l) { return b < l.ctas ? l.begin(b) : -1ll; }, cur);
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (b >= line.ctas || cur.j == 0 || tree_aborted(p.err)) return;
-    const long long x = line.begin(b), from = x - cur.j, to = from + cur.q.tiles;
-    if (line.begin(b - 1) > from) return;
-    int last = b;
-    while (last + 1 < line.ctas && line.begin(last + 1) < to) ++last;
-    const int first = b - 1, rows = item_tokens(p, cur) * p.G;
-    const size_t slot0 = (size_t)(2 * first + (line.begin(first) < from ? 1 : 0));
-    // a warp a row: lane l has dims of (D / 32) l
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int N = D / 32;
-    for (int r = blockIdx.y * (kMergeThreads / 32) + warp; r < rows; r += gridDim.y * (kMergeThreads / 32)) {
-        float m = -INFINITY;
-        for (int c = first; c <= last; ++c) {
-            const float2 ml = p.part_ml[(c == first ? slot0 : (size_t)2 * c) * p.slot_rows + r];
-            m = (ml.x > m || ml.x != ml.x) ? ml.x : m;      // (NaN stays)
-        }
-        const float z = m == -INFINITY ? 0.f : m;
-        float l = 0.f, o[N] = {};
-        for (int c = first; c <= last; ++c) {
-            const size_t at = (c == first ? slot0 : (size_t)2 * c) * p.slot_rows + r;
-            const float2 ml = p.part_ml[at];
-            const float w = fast_exp2(ml.x - z);
-            if (ml.y == 0.f) continue;               // no key that this row sees (its outputs count for nothing)
-            l = __fmaf_rn(w, ml.y, l);
-            float v[N];
-            if constexpr (N == 4) {
-                const float4 y = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
-                v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
-            } else {
-                const float2 y = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
-                v[0] = y.x; v[1] = y.y;
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = __fmaf_rn(w, v[i], o[i]);
-        }
-        const int tok = r / p.G, g = r - tok * p.G;
-        const size_t dst = ((size_t)(cur.q.q0 + cur.rt * p.TQ + tok) * p.Hq + (size_t)cur.h * p.G + g) * D + lane * N;
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = inv != 0.f ? o[i] * inv : 0.f;
-        if constexpr (sizeof(Out) == 4) {
-            float* to4 = static_cast<float*>(p.out) + dst;
-#pragma unroll
-            for (int i = 0; i < N; i += 2) *reinterpret_cast<float2*>(to4 + i) = make_float2(o[i], o[i + 1]);
-        } else {
-            uint32_t* to2 = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + dst);
-#pragma unroll
-            for (int i = 0; i < N; i += 2) to2[i / 2] = pack_bf16x2(o[i], o[i + 1]);
+// What CTA c says of the item that its begin cuts (one thread of it).
+__device__ __forceinline__ void say_joint(const TParams& p, const Line& line, const Cursor& cur, int c, bool any) {
+    Joint x{0, 0, 0, 0};
+    if (any && cur.j > 0) {
+        const long long from = line.begin(c) - cur.j, to = from + cur.q.tiles;
+        if (line.begin(c - 1) <= from) {
+            int last = c;
+            while (last + 1 < line.ctas && line.begin(last + 1) < to) ++last;
+            x.count = last - c + 2;
+            x.late = line.begin(c - 1) < from ? 1 : 0;
+            x.row0 = (cur.q.q0 + cur.rt * p.TQ) * p.Hq + cur.h * p.G;
+            x.rows = item_tokens(p, cur) * p.G;
         }
     }
+    p.joints[c] = x;
+}
+
+// Joins the partial results of the items that CTA boundaries cut.  Block b takes the item that CTA
+// b + 1 tells of, blockIdx.y eight of its rows, a warp each: the weights of the parts on the lanes,
+// then the parts' outputs, eight loads under way together.
+constexpr int kMergeThreads = 256;
+template <int D, typename Out>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TParams p) {
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const Joint x = p.joints[c];
+    if (r >= x.rows || tree_aborted(p.err)) return;                       // (rows: 0 where nothing is to be joined)
+    // part i: piece 2 (c - 1 + i), the first one perhaps the piece after it
+    auto at = [&](int i) { return (size_t)(2 * (c - 1 + i) + (i == 0 ? x.late : 0)) * p.slot_rows + r; };
+    float m = -INFINITY;
+    for (int i = lane; i < x.count; i += 32) {
+        const float y = p.part_ml[at(i)].x;
+        m = (y > m || y != y) ? y : m;                                    // (NaN stays)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, m, o);
+        m = (y > m || y != y) ? y : m;
+    }
+    const float z = m == -INFINITY ? 0.f : m;
+    constexpr int N = D / 32, B = 8;
+    float l = 0.f, o[N] = {};
+    for (int i0 = 0; i0 < x.count; i0 += 32) {
+        const float2 ml = i0 + lane < x.count ? p.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
+        // a part without a key that the row sees counts for nothing, whatever its outputs are
+        const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - z);
+        const uint32_t with = __ballot_sync(0xffffffffu, ml.y != 0.f);
+        l = __fmaf_rn(w, ml.y, l);
+        const int n = min(32, x.count - i0);
+        for (int i = 0; i < n; i += B) {
+            float v[B][N];
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+                if (i + b < n) {
+                    const float* from = p.part_o + at(i0 + i + b) * D + lane * N;
+                    if constexpr (N == 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(from);
+                        v[b][0] = y.x; v[b][1] = y.y; v[b][2] = y.z; v[b][3] = y.w;
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2*>(from);
+                        v[b][0] = y.x; v[b][1] = y.y;
+                    }
+                }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float wb = __shfl_sync(0xffffffffu, w, (i + b) & 31);
+                if (i + b < n && ((with >> (i + b)) & 1u))
+#pragma unroll
+                    for (int k = 0; k < N; ++k) o[k] = __fmaf_rn(wb, v[b][k], o[k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+    const int tok = r / p.G, g = r - tok * p.G;
+    const size_t dst = ((size_t)(uint32_t)x.row0 + (size_t)tok * p.Hq + g) * D + lane * N;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
+    if constexpr (sizeof(Out) == 4) {
+        float* to = static_cast<float*>(p.out) + dst;
+#pragma unroll
+        for (int k = 0; k < N; k += 2) *reinterpret_cast<float2*>(to + k) = make_float2(o[k], o[k + 1]);
+    } else {
+        uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + dst);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) to[k / 2] = pack_bf16x2(o[k], o[k + 1]);
+    }
+}
+inline dim3 tree_merge_grid(const TParams& p) {
+    return dim3(p.ctas - 1, (p.slot_rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
 }
 
 inline int tree_sms() {

@@ -27,6 +27,7 @@ struct TreeArgs {
 constexpr int kTreeCtas = 160;               // CTAs at most of the tensor-core kernel, one per SM,
 constexpr int kTreeF32Ctas = 2 * kTreeCtas;  // and of the f32 kernel
 constexpr int kTreeF32Rows = 32;             // query rows of an f32 item
+constexpr int kTreeJointBytes = 16;          // of what a CTA says of an item that it shares
 // Query rows of an item of the tensor-core kernel: one or two tiles of 128.
 inline int tree_tile_rows(long long rows) { return rows > 128 ? 256 : 128; }
 size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_chunk);

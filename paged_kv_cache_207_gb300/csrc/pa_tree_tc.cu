@@ -54,9 +54,12 @@ constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at 
 template <pa_dtype T, int SW>
 struct Roles {
     static constexpr int SOFT = 4 * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
-    static constexpr int FEEDS = T == PA_BF16 ? (SW == 1 ? 4 : 2) : kKeyBlocks;
+    static constexpr int FEEDS = T == PA_BF16 ? (SW == 1 ? 4 : 2) : 2 * kKeyBlocks;
+    // registers of a thread: at launch, and how setmaxnreg shares them out (softmax holds a row of S)
+    static constexpr int LAUNCH = T == PA_BF16 ? 168 : 80, OTHER = T == PA_BF16 ? 104 : 56;
     static constexpr int OTHERS = (2 + FEEDS + 3) / 4 * 4;
     static constexpr int THREADS = (SOFT + OTHERS) * 32;
+    static_assert(32 * (SOFT * 200 + OTHERS * OTHER) <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "registers of an SM");
 };
 
 template <int D, pa_dtype T, int SW>
@@ -80,9 +83,10 @@ struct Layout {
     static constexpr int EXPS = ODD + 16;             // [8] (K, V) exponents of a tile, as the conversions leave them
     static constexpr int PASSED = EXPS + 64;          // [8] as the MMA warp passes them on
     static constexpr int SEEN = PASSED + 64;          // [8][8] a tile's block has such values
-    static constexpr int BYTES0 = SEEN + 64;
+    static constexpr int TABLE = SEEN + 64;           // [8] FP4: a block's scales of values
+    static constexpr int BYTES0 = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);
     static_assert(BYTES0 <= 232448, "shared memory of one CTA");
-    static_assert((Roles<T, SW>::THREADS / 32 + 4) * 8 <= QTILE, "the search's scratch");
+    static_assert((Roles<T, SW>::THREADS / 32 + 6) * 8 <= QTILE, "the search's scratch");
     // one CTA (and its 512 TMEM columns) to an SM
     static constexpr int BYTES = BYTES0 < 122880 ? 122880 : BYTES0;
 };
@@ -118,6 +122,14 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs));
+}
+// One lane of the warp, always the same one, in a form that the compiler sees to be one (MMAs issued
+// under `lane == 0` take about 104 clocks each, and 150 in a loop, for the descriptors' way into uniform
+// registers; under this and unrolled, 72 to 105, what the tensor cores take).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -225,20 +237,15 @@ struct Convert;
 
 template <int D>
 struct Convert<D, PA_FP8_E4M3> {
-    // Largest biased exponents of the tile's finite scales, K's and V's (keys only).
-    static __device__ __forceinline__ void exponents(uint32_t raw, uint32_t vraw, int rec, int keys, int lane, int& ek, int& ev) {
-        const uint32_t at = (lane >> 2) * rec + 16 * D + (lane & 3) * 16;
-        const uint4 k = ld_shared_v4(raw + at), v = ld_shared_v4(vraw + at);
+    // Largest biased exponent of the tile's finite scales (of its keys).
+    static __device__ __forceinline__ int exponent(uint32_t raw, int rec, int keys, int lane) {
+        const uint4 x = ld_shared_v4(raw + (lane >> 2) * rec + 16 * D + (lane & 3) * 16);
         const int n = keys - 4 * lane;                                     // keys of this lane's four
-        auto top = [&](uint4 x) {
-            auto e = [&](uint32_t y, int i) {
-                const uint32_t z = (y >> 23) & 0xffu;
-                return n > i && z != 0xffu ? z : 0u;
-            };
-            return max(max(e(x.x, 0), e(x.y, 1)), max(e(x.z, 2), e(x.w, 3)));
+        auto e = [&](uint32_t y, int i) {
+            const uint32_t z = (y >> 23) & 0xffu;
+            return n > i && z != 0xffu ? z : 0u;
         };
-        ek = (int)__reduce_max_sync(0xffffffffu, top(k));
-        ev = (int)__reduce_max_sync(0xffffffffu, top(v));
+        return (int)__reduce_max_sync(0xffffffffu, max(max(e(x.x, 0), e(x.y, 1)), max(e(x.z, 2), e(x.w, 3))));
     }
     static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int ek, int lane) {
         const int slot = lane & 15;
@@ -260,7 +267,7 @@ struct Convert<D, PA_FP8_E4M3> {
             st_shared_v4(to + kKeyBlocks * 256, make_uint4(o[4], o[5], o[6], o[7]));
         }
     }
-    static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, int rv, int lane, uint32_t live, uint32_t own) {
+    static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, uint32_t, int rv, int lane, uint32_t live, uint32_t own) {
         const float f = exp2i(127 - rv);
         uint32_t h[8];
 #pragma unroll
@@ -304,29 +311,25 @@ __device__ __forceinline__ uint32_t f16_power(int x) {
 template <int D>
 struct Convert<D, PA_FP4_E2M1> {
     static constexpr int NB = D / 32;
-    static __device__ __forceinline__ void exponents(uint32_t raw, uint32_t vraw, int rec, int keys, int lane, int& ek, int& ev) {
+    static __device__ __forceinline__ int exponent(uint32_t raw, int rec, int keys, int lane) {
         // a lane has the scale codes of four tokens, NB bytes each; code 255 is no number
-        const uint32_t at = (lane >> 2) * rec + 8 * D + (lane & 3) * (4 * NB);
+        const uint32_t at = raw + (lane >> 2) * rec + 8 * D + (lane & 3) * (4 * NB);
         const int n = keys - 4 * lane;
         auto bytes = [&](uint32_t x, bool key) {
             x &= ~__vcmpeq4(x, 0xffffffffu);
             return key ? x : 0u;
         };
-        auto top = [&](uint32_t from) {
-            uint32_t m;
-            if constexpr (NB == 4) {
-                const uint4 x = ld_shared_v4(from + at);
-                m = __vmaxu4(__vmaxu4(bytes(x.x, n > 0), bytes(x.y, n > 1)), __vmaxu4(bytes(x.z, n > 2), bytes(x.w, n > 3)));
-            } else {
-                const uint2 x = ld_shared_v2(from + at);
-                const uint32_t lo = n > 1 ? 0xffffffffu : n > 0 ? 0xffffu : 0u, hi = n > 3 ? 0xffffffffu : n > 2 ? 0xffffu : 0u;
-                m = __vmaxu4(bytes(x.x, true) & lo, bytes(x.y, true) & hi);
-            }
-            m = __vmaxu4(m, m >> 16);
-            return max(m & 0xffu, (m >> 8) & 0xffu);
-        };
-        ek = (int)__reduce_max_sync(0xffffffffu, top(raw));
-        ev = (int)__reduce_max_sync(0xffffffffu, top(vraw));
+        uint32_t m;
+        if constexpr (NB == 4) {
+            const uint4 x = ld_shared_v4(at);
+            m = __vmaxu4(__vmaxu4(bytes(x.x, n > 0), bytes(x.y, n > 1)), __vmaxu4(bytes(x.z, n > 2), bytes(x.w, n > 3)));
+        } else {
+            const uint2 x = ld_shared_v2(at);
+            const uint32_t lo = n > 1 ? 0xffffffffu : n > 0 ? 0xffffu : 0u, hi = n > 3 ? 0xffffffffu : n > 2 ? 0xffffu : 0u;
+            m = __vmaxu4(bytes(x.x, true) & lo, bytes(x.y, true) & hi);
+        }
+        m = __vmaxu4(m, m >> 16);
+        return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffu, (m >> 8) & 0xffu));
     }
     static __device__ __forceinline__ uint32_t code_at(uint32_t addr) {
         uint32_t v;
@@ -352,37 +355,40 @@ struct Convert<D, PA_FP4_E2M1> {
                 st_shared_v4(dst + (4 * w + i) * (kKeyBlocks * 256) + slot * 16, make_uint4(o[0][i], o[1][i], o[2][i], o[3][i]));
         }
     }
-    static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, int rv, int lane, uint32_t live, uint32_t own) {
+    // `table`: 128 bytes of the warp's, a pair of tokens' powers of two for each 32 dims: [D / 32][8 pairs]
+    static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, uint32_t table, int rv, int lane, uint32_t live,
+                                                  uint32_t own) {
         const int r = lane & 7;
-        const bool plain = live == 0xffffu && own == 0u;
         bool odd = false;
+        if (lane < 8 * NB) {
+            const int t = 2 * r, b = lane >> 3;
+            const uint32_t at = raw + 8 * D + t * NB + b;
+            const uint32_t e0 = code_at(at), e1 = code_at(at + NB);
+            uint32_t h = power(e0, rv) | power(e1, rv) << 16;
+            const bool b0 = e0 == 255u && ((own >> t) & 1u), b1 = e1 == 255u && ((own >> (t + 1)) & 1u);
+            odd = b0 || b1;
+            if (b0 || !((live >> t) & 1u)) h &= 0xffff0000u;
+            if (b1 || !((live >> (t + 1)) & 1u)) h &= 0xffffu;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(table + 4 * lane), "r"(h) : "memory");
+        }
+        __syncwarp();
 #pragma unroll
         for (int mi = lane >> 3; mi < D / 16; mi += 4) {
+            const uint4 lo = ld_shared_v4(table + mi / 2 * 32), hi = ld_shared_v4(table + mi / 2 * 32 + 16);
+            const uint32_t h[2][4] = {{lo.x, lo.y, lo.z, lo.w}, {hi.x, hi.y, hi.z, hi.w}};
             uint32_t o[4][4];                                  // [c][dh, half]: tokens 2 c + 8 half, + 1 of dim 16 mi + 8 dh + r
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 e2m1x8_to_f16x2x4(ld_shared_u32(raw + ((4 * r + c) * (D / 16) + mi) * 4), o[c]);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int t = 2 * c + 8 * half;
-                    const uint32_t at = raw + 8 * D + t * NB + mi / 2;
-                    const uint32_t e0 = code_at(at), e1 = code_at(at + NB);
-                    uint32_t h = power(e0, rv) | power(e1, rv) << 16;
-                    if (!plain) {
-                        const bool b0 = e0 == 255u && ((own >> t) & 1u), b1 = e1 == 255u && ((own >> (t + 1)) & 1u);
-                        odd |= b0 || b1;
-                        if (b0 || !((live >> t) & 1u)) h &= 0xffff0000u;
-                        if (b1 || !((live >> (t + 1)) & 1u)) h &= 0xffffu;
-                    }
-                    o[c][half] = mul_f16x2(o[c][half], h);
-                    o[c][2 + half] = mul_f16x2(o[c][2 + half], h);
-                }
+                for (int x = 0; x < 4; ++x) o[c][x] = mul_f16x2(o[c][x], h[x & 1][c]);
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 st_shared_v4(dst + (x & 1) * (D * 16) + (16 * mi + 8 * (x >> 1) + r) * 16,
                              make_uint4(o[0][x], o[1][x], o[2][x], o[3][x]));
         }
+        __syncwarp();                                          // (the table's reads are done)
         return odd;
     }
 };
@@ -420,12 +426,12 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 0; i < KST; ++i) {
-            mbar_init(bar(kKFull + i), W::FEEDS);
+            mbar_init(bar(kKFull + i), RAW ? kKeyBlocks : W::FEEDS);
             mbar_init(bar(kKEmpty + i), 1);
         }
 #pragma unroll
         for (int i = 0; i < VST; ++i) {
-            mbar_init(bar(kVFull + i), RAW ? W::FEEDS : 1);
+            mbar_init(bar(kVFull + i), RAW ? kKeyBlocks : 1);
             mbar_init(bar(kVEmpty + i), 1);
         }
 #pragma unroll
@@ -453,14 +459,17 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         const Line line = tree_locate<W::THREADS, kKeys, kMinTiles>(
             p, reinterpret_cast<long long*>(smem + L::Q), blockIdx.x == 0,
             [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, walk.c);
-        walk.left = (int)blockIdx.x < line.ctas ? line.begin(blockIdx.x + 1) - line.begin(blockIdx.x) : 0;
+        const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
+        walk.left = any ? line.begin(blockIdx.x + 1) - line.begin(blockIdx.x) : 0;
+        // (said whether or not the call goes on)
+        if (threadIdx.x == 32 * W::FEED) say_joint(p, line, walk.c, blockIdx.x, any);
     }
     // (also orders the search's scratch before the queries that take its place)
     const bool stop = __syncthreads_or(threadIdx.x == 0 && tree_aborted(p.err));
     if (stop || walk.left == 0) return;
 
     if (warp >= W::SOFT) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::OTHER) : "memory");
     if (warp == W::COPY) {
         // ------------------------------------------------------------ bulk copies
         // bf16: V tiles, lane b block b.  Else the records of both, lane b K's and 8 + b V's.
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             auto issue_s = [&](int hh, int i) {
                 const int t = t0 + i, buf = SW == 2 ? hh : t & 1;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t qd = umma_desc(sbase + L::Q + hh * L::QTILE, 2048, 128);
                     const uint64_t kd = umma_desc(sbase + L::K + (t % KST) * KTILE, kKeyBlocks * 256, 128);
                     const uint32_t dcol = tmem + kColS + (uint32_t)(buf * kKeys);
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             };
             auto k_ready = [&](int i) { ok = warp_wait(bar(kKFull + (t0 + i) % KST), ((t0 + i) / KST) & 1); };
             auto k_free = [&](int i) {
-                if (lane == 0) umma_commit(bar(kKEmpty + (t0 + i) % KST));
+                if (elect_one()) umma_commit(bar(kKEmpty + (t0 + i) % KST));
                 __syncwarp();
             };
             auto issue_pv = [&](int hh, int i) {
@@ -577,20 +586,27 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     }
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t pcol = tmem + kColS + (uint32_t)(buf * kKeys), ocol = tmem + kColO + (uint32_t)(hh * kKeys);
                     // bf16: a block as stored, [D/8][16 slots][8 dims]; else [2 groups][D/8][8 dims][8 tokens]
                     const uint64_t vd = RAW ? umma_desc(sbase + L::V + st * KTILE, D * 16, 128)
                                             : umma_desc(sbase + L::V + st * KTILE, 128, 256);
-                    for (int b = 0; b < nb; ++b)
-                        umma_ts(ocol, pcol + 8 * b, vd + (uint64_t)((b * TILE) >> 4), idO, (i > 0 || b > 0) ? 1u : 0u);
+                    const uint32_t more = i > 0 ? 1u : 0u;
+                    if (nb == kKeyBlocks) {
+#pragma unroll
+                        for (int b = 0; b < kKeyBlocks; ++b)
+                            umma_ts(ocol, pcol + 8 * b, vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                    } else {
+                        for (int b = 0; b < nb; ++b)
+                            umma_ts(ocol, pcol + 8 * b, vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                    }
                     if (hh == SW - 1) umma_commit(bar(kVEmpty + st));
                     if (SW == 1) umma_commit(bar(kPVDone));
                 }
                 __syncwarp();
                 if (i == n - 1) {
                     odd = __any_sync(0xffffffffu, odd);
-                    if (lane == 0) {
+                    if (elect_one()) {
                         umma_commit(bar(kODone + hh));
                         if (hh == 0) *reinterpret_cast<volatile uint32_t*>(smem + L::ODD + 4 * (ic & 1)) = odd;
                         mbar_arrive(bar(kODone + hh));
@@ -639,55 +655,55 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         }
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // nothing may still be running on the tensor cores when the TMEM is freed
-        if (lane == 0) umma_commit(bar(kDone));
+        if (elect_one()) umma_commit(bar(kDone));
         __syncwarp();
         mbar_wait_bounded(bar(kDone), 0, kWaitNs);
     } else if (warp < W::FEED + W::FEEDS) {
         const int f = warp - W::FEED;
         if constexpr (RAW) {
-            // -------------------------------------------------------- conversions, one block of every tile
+            // -------------------------------------------------------- conversions, one block of every
+            // tile: warps 0 .. 7 its keys, 8 .. 15 its values (so that the keys of a tile do not wait
+            // for the values of the one before)
             using C = Convert<D, T>;
+            const int b = f % kKeyBlocks;
+            const bool for_v = f >= kKeyBlocks;
             bool ok = true;
             int t = 0;
             while (ok && walk.left > 0) {
                 const Piece x = piece_at(p, walk.c, walk.left);
                 int rv = 0;
                 for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
-                    const int rs = t % L::RST, ks = t % KST, vs = t % VST;
+                    const int rs = t % L::RST, st = for_v ? t % VST : t % KST;
                     ok = warp_wait(bar(kRFull + rs), (t / L::RST) & 1);
                     if (!ok) break;
                     const uint32_t kraw = sbase + L::R + rs * 2 * kKeyBlocks * REC, vraw = kraw + kKeyBlocks * REC;
-                    const int tok0 = (x.j0 + i) * kKeys, first = tok0 + f * kBlockTokens;
-                    int ek, ev;
-                    C::exponents(kraw, vraw, REC, x.end - tok0, lane, ek, ev);
+                    const int tok0 = (x.j0 + i) * kKeys, first = tok0 + b * kBlockTokens;
+                    const int ek = for_v ? 0 : C::exponent(kraw, REC, x.end - tok0, lane);
+                    const int ev = for_v || f == 0 ? C::exponent(vraw, REC, x.end - tok0, lane) : 0;
                     if (i == 0 || ev > rv + 6) rv = ev;
-                    if (f == 0 && lane == 0)
-                        st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
-                    if (t >= KST) {
-                        ok = warp_wait(bar(kKEmpty + ks), (t / KST - 1) & 1);
+                    if (f == 0 && lane == 0) st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
+                    const int use = for_v ? t / VST : t / KST;
+                    if (use > 0) {
+                        ok = warp_wait(bar((for_v ? kVEmpty : kKEmpty) + st), (use - 1) & 1);
                         if (!ok) break;
                     }
-                    const bool any = first < x.end;
-                    if (any) C::keys(kraw + f * REC, sbase + L::K + ks * KTILE + f * 256, ek, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kKFull + ks));
-                    if (t >= VST) {
-                        ok = warp_wait(bar(kVEmpty + vs), (t / VST - 1) & 1);
-                        if (!ok) break;
+                    if (for_v) {
+                        bool odd = false;
+                        if (first < x.end) {
+                            const int keys = min(x.end - first, kBlockTokens), ctx = min(max(x.c.q.start - first, 0), kBlockTokens);
+                            const uint32_t live = (1u << keys) - 1u, own = live & ~((1u << ctx) - 1u);
+                            odd = C::values(vraw + b * REC, sbase + L::V + st * KTILE + b * TILE, sbase + L::TABLE + b * 128, rv, lane,
+                                            live, own);
+                        }
+                        odd = __any_sync(0xffffffffu, odd);
+                        if (lane == 0) *reinterpret_cast<volatile uint8_t*>(smem + L::SEEN + 8 * (t & 7) + b) = odd;
+                    } else if (first < x.end) {
+                        C::keys(kraw + b * REC, sbase + L::K + st * KTILE + b * 256, ek, lane);
                     }
-                    bool odd = false;
-                    if (any) {
-                        const int keys = min(x.end - first, kBlockTokens), ctx = min(max(x.c.q.start - first, 0), kBlockTokens);
-                        const uint32_t live = (1u << keys) - 1u, own = live & ~((1u << ctx) - 1u);
-                        odd = C::values(vraw + f * REC, sbase + L::V + vs * KTILE + f * TILE, rv, lane, live, own);
-                    }
-                    odd = __any_sync(0xffffffffu, odd);
-                    if (lane == 0) *reinterpret_cast<volatile uint8_t*>(smem + L::SEEN + 8 * (t & 7) + f) = odd;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(bar(kVFull + vs));
+                        mbar_arrive(bar((for_v ? kVFull : kKFull) + st));
                         mbar_arrive(bar(kREmpty + rs));
                     }
                 }
@@ -1039,7 +1055,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
     const TParams p = tree_params(a, SW * kTileRows, ctas);
     e = tree_launch(tree_tc_kernel<D, T, SW>, dim3(ctas), Roles<T, SW>::THREADS, smem, stream, p);
     if (e != cudaSuccess || ctas == 1) return e;
-    return tree_launch(tree_merge_kernel<D, kKeys, kMinTiles, __nv_bfloat16>, dim3(ctas - 1, 2), kMergeThreads, 0, stream, p);
+    return tree_launch(tree_merge_kernel<D, __nv_bfloat16>, tree_merge_grid(p), kMergeThreads, 0, stream, p);
 }
 
 template <int D>
