@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
 #pragma unroll
             for (int x = 1; x < 16; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
         const bool whole = j0 == 0 && j1 == cur.q.tiles;
-        const size_t at_slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * p.slot_rows;
+        const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 4 * ty + r;
@@ -232,13 +232,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                 const int d = 4 * (tx + 16 * x);
                 float4 v = make_float4(pair_lo(o[r][2 * x]), pair_hi(o[r][2 * x]), pair_lo(o[r][2 * x + 1]), pair_hi(o[r][2 * x + 1]));
                 if (!whole) {
-                    *reinterpret_cast<float4*>(p.part_o + (at_slot + row) * D + d) = v;
+                    reinterpret_cast<float4*>(p.part_o)[(slot * (D / 4) + d / 4) * p.slot_rows + row] = v;
                     continue;
                 }
                 v = inv != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
                 *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst + d) = v;
             }
-            if (!whole && tx == 0) p.part_ml[at_slot + row] = make_float2(m[r], l[r]);
+            if (!whole && tx == 0) p.part_ml[slot * p.slot_rows + row] = make_float2(m[r], l[r]);
         }
         left -= j1 - j0;
         if (left > 0) next_item<kKeys>(p, cur);
@@ -253,8 +253,7 @@ cudaError_t launch_f32(const TreeArgs& a, cudaStream_t stream) {
     const int ctas = std::min(2 * tree_sms(), kTreeF32Ctas);
     const TParams p = tree_params(a, kRows, ctas);
     e = tree_launch(tree_f32_kernel<D>, dim3(ctas), kThreads, smem, stream, p);
-    if (e != cudaSuccess || ctas == 1) return e;
-    return tree_launch(tree_merge_kernel<D, float>, tree_merge_grid(p), kMergeThreads, 0, stream, p);
+    return e != cudaSuccess ? e : launch_merge<D, float>(p, stream);
 }
 
 }  // namespace

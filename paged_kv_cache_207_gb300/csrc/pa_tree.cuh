@@ -43,7 +43,7 @@ struct TParams {
     const int32_t* cu;
     const int32_t* mask;
     int32_t* err;
-    float* part_o;           // [2 CTAs][slot_rows][D]
+    float* part_o;           // [2 CTAs][D / 4][slot_rows][4]: a thread's row lies beside its neighbours'
     float2* part_ml;         // [2 CTAs][slot_rows]: maximum (log2 units) and sum
     Joint* joints;           // [CTAs]
     int slot_rows;
@@ -90,11 +90,24 @@ struct Cursor {
     TreeSeq q;
 };
 
-// C and the first tile of CTA c.
+// The line: its tiles, C, and the first tile of CTA c.
 struct Line {
-    long long total;
+    long long total, base;   // base = total / ctas
+    uint32_t rest;           // total % ctas
     int ctas;
-    __device__ __forceinline__ long long begin(int c) const { return total / ctas * c + total % ctas * c / ctas; }
+    __device__ __forceinline__ Line(long long tiles, long long most, int limit) {
+        total = tiles;
+        ctas = most < 1 ? 1 : most < limit ? (int)most : limit;
+        // (a division of 64 bits takes as long as a trip to L2)
+        if (tiles < 1ll << 32) {
+            base = (uint32_t)tiles / (uint32_t)ctas;
+            rest = (uint32_t)tiles % (uint32_t)ctas;
+        } else {
+            base = tiles / ctas;
+            rest = (uint32_t)(tiles % ctas);
+        }
+    }
+    __device__ __forceinline__ long long begin(int c) const { return base * c + rest * (uint32_t)c / (uint32_t)ctas; }
 };
 
 // The line, and the place of tile `begin_of(line)` in it where there is one (begin >= 0 and below
@@ -125,10 +138,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
         before += w < warp ? u : 0;
         total += u;
     }
-    Line line;
-    line.total = total;
-    const long long most = (total + MIN_TILES - 1) / MIN_TILES;
-    line.ctas = most < 1 ? 1 : most < p.ctas ? (int)most : p.ctas;
+    const Line line(total, (total + MIN_TILES - 1) / MIN_TILES, p.ctas);
     const long long begin = begin_of(line);
     long long at = before + incl - mine;
     if (begin >= at && begin < at + mine) {
@@ -155,7 +165,8 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
         cur.s = from[0];
         cur.q = TreeSeq{from[1], from[2], from[3], from[4], from[5], 0};
         const long long off = sm[NT / 32];
-        const int item = (int)(off / cur.q.tiles);
+        // (a sequence's own tiles: its heads, row tiles and keys hardly ever pass 2^32)
+        const int item = off < 1ll << 32 ? (int)((uint32_t)off / (uint32_t)cur.q.tiles) : (int)(off / cur.q.tiles);
         cur.j = (int)(off - (long long)item * cur.q.tiles);
         cur.h = item / cur.q.rts;
         cur.rt = item - cur.h * cur.q.rts;
@@ -221,7 +232,10 @@ __device__ __forceinline__ void say_joint(const TParams& p, const Line& line, co
     if (any && cur.j > 0) {
         const long long from = line.begin(c) - cur.j, to = from + cur.q.tiles;
         if (line.begin(c - 1) <= from) {
-            int last = c;
+            // the CTA of the item's last tile: where it would be with even shares, or beside that
+            const long long each = line.base > 0 ? line.base : 1;
+            int last = (int)min((long long)line.ctas - 1, c + (cur.q.tiles - cur.j) / each);
+            while (line.begin(last) >= to) --last;
             while (last + 1 < line.ctas && line.begin(last + 1) < to) ++last;
             x.count = last - c + 2;
             x.late = line.begin(c - 1) < from ? 1 : 0;
@@ -233,83 +247,60 @@ __device__ __forceinline__ void say_joint(const TParams& p, const Line& line, co
 }
 
 // Joins the partial results of the items that CTA boundaries cut.  Block b takes the item that CTA
-// b + 1 tells of, blockIdx.y eight of its rows, a warp each: the weights of the parts on the lanes,
-// then the parts' outputs, eight loads under way together.
-constexpr int kMergeThreads = 256;
+// b + 1 tells of, blockIdx.y eight of its rows: a thread four dims of a row, over the parts in their
+// order with a running maximum, eight parts' loads under way together.
+constexpr int kMergeRows = 8;
 template <int D, typename Out>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TParams p) {
-    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(2 * D) tree_merge_kernel(const TParams p) {
+    const int c = blockIdx.x + 1, unit = threadIdx.x / kMergeRows;
+    const int r = blockIdx.y * kMergeRows + threadIdx.x % kMergeRows;
     grid_dependency_wait();
     grid_launch_dependents();
     const Joint x = p.joints[c];
     if (r >= x.rows || tree_aborted(p.err)) return;                       // (rows: 0 where nothing is to be joined)
     // part i: piece 2 (c - 1 + i), the first one perhaps the piece after it
-    auto at = [&](int i) { return (size_t)(2 * (c - 1 + i) + (i == 0 ? x.late : 0)) * p.slot_rows + r; };
-    float m = -INFINITY;
-    for (int i = lane; i < x.count; i += 32) {
-        const float y = p.part_ml[at(i)].x;
-        m = (y > m || y != y) ? y : m;                                    // (NaN stays)
-    }
+    auto slot = [&](int i) { return (size_t)(2 * (c - 1 + i) + (i == 0 ? x.late : 0)); };
+    constexpr int B = 8;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < x.count; i0 += B) {
+        float2 ml[B];
+        float4 v[B];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, m, o);
-        m = (y > m || y != y) ? y : m;
-    }
-    const float z = m == -INFINITY ? 0.f : m;
-    constexpr int N = D / 32, B = 8;
-    float l = 0.f, o[N] = {};
-    for (int i0 = 0; i0 < x.count; i0 += 32) {
-        const float2 ml = i0 + lane < x.count ? p.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
-        // a part without a key that the row sees counts for nothing, whatever its outputs are
-        const float w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - z);
-        const uint32_t with = __ballot_sync(0xffffffffu, ml.y != 0.f);
-        l = __fmaf_rn(w, ml.y, l);
-        const int n = min(32, x.count - i0);
-        for (int i = 0; i < n; i += B) {
-            float v[B][N];
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-                if (i + b < n) {
-                    const float* from = p.part_o + at(i0 + i + b) * D + lane * N;
-                    if constexpr (N == 4) {
-                        const float4 y = *reinterpret_cast<const float4*>(from);
-                        v[b][0] = y.x; v[b][1] = y.y; v[b][2] = y.z; v[b][3] = y.w;
-                    } else {
-                        const float2 y = *reinterpret_cast<const float2*>(from);
-                        v[b][0] = y.x; v[b][1] = y.y;
-                    }
-                }
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const float wb = __shfl_sync(0xffffffffu, w, (i + b) & 31);
-                if (i + b < n && ((with >> (i + b)) & 1u))
-#pragma unroll
-                    for (int k = 0; k < N; ++k) o[k] = __fmaf_rn(wb, v[b][k], o[k]);
+        for (int b = 0; b < B; ++b) {
+            ml[b] = make_float2(-INFINITY, 0.f);
+            v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + b < x.count) {
+                const size_t at = slot(i0 + b);
+                ml[b] = p.part_ml[at * p.slot_rows + r];
+                v[b] = reinterpret_cast<const float4*>(p.part_o)[(at * (D / 4) + unit) * p.slot_rows + r];
             }
         }
-    }
+        float top = m;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+        for (int b = 0; b < B; ++b) top = (ml[b].x > top || ml[b].x != ml[b].x) ? ml[b].x : top;      // (NaN stays)
+        const float z = top == -INFINITY ? 0.f : top, was = fast_exp2(m - z);
+        m = top;
+        l *= was;
+        o = make_float4(o.x * was, o.y * was, o.z * was, o.w * was);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            // (a part without a key that the row sees counts for nothing, whatever its outputs are)
+            if (ml[b].y == 0.f) continue;
+            const float w = fast_exp2(ml[b].x - z);
+            l = __fmaf_rn(w, ml[b].y, l);
+            o = make_float4(__fmaf_rn(w, v[b].x, o.x), __fmaf_rn(w, v[b].y, o.y), __fmaf_rn(w, v[b].z, o.z), __fmaf_rn(w, v[b].w, o.w));
+        }
+    }
     const int tok = r / p.G, g = r - tok * p.G;
-    const size_t dst = ((size_t)(uint32_t)x.row0 + (size_t)tok * p.Hq + g) * D + lane * N;
+    const size_t dst = ((size_t)(uint32_t)x.row0 + (size_t)tok * p.Hq + g) * D + 4 * unit;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
-    if constexpr (sizeof(Out) == 4) {
-        float* to = static_cast<float*>(p.out) + dst;
-#pragma unroll
-        for (int k = 0; k < N; k += 2) *reinterpret_cast<float2*>(to + k) = make_float2(o[k], o[k + 1]);
-    } else {
-        uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + dst);
-#pragma unroll
-        for (int k = 0; k < N; k += 2) to[k / 2] = pack_bf16x2(o[k], o[k + 1]);
-    }
+    o = inv != 0.f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (sizeof(Out) == 4)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst) = o;
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + dst) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
-inline dim3 tree_merge_grid(const TParams& p) {
-    return dim3(p.ctas - 1, (p.slot_rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
-}
-
 inline int tree_sms() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
@@ -331,6 +322,13 @@ cudaError_t tree_launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, typename Out>
+cudaError_t launch_merge(const TParams& p, cudaStream_t stream) {
+    if (p.ctas == 1) return cudaSuccess;
+    const dim3 grid(p.ctas - 1, (p.slot_rows + kMergeRows - 1) / kMergeRows);
+    return tree_launch(tree_merge_kernel<D, Out>, grid, 2 * D, 0, stream, p);
 }
 
 }  // namespace

@@ -49,17 +49,18 @@ constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
 constexpr int kMinTiles = 2;
 constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at most
 
-// Warps: softmax 0 .. 4 SW - 1, the copies (bf16: V's; else all records), the MMAs, then K's copies
-// (bf16) or the conversions, filled up to whole warpgroups (setmaxnreg is collective).
+// Warps: softmax 0 .. 8 SW - 1, the copies (bf16: V's; else all records), the MMAs, then K's copies
+// (bf16) or the conversions.  All have the registers of a launch of so many threads (128, 96 or 72: what
+// setmaxnreg hands from role to role the compiler does not count on), so the softmax takes a row in
+// pieces of 32 columns, from the TMEM once for the maximum and again for the probabilities.
 template <pa_dtype T, int SW>
 struct Roles {
-    static constexpr int SOFT = 4 * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
-    static constexpr int FEEDS = T == PA_BF16 ? (SW == 1 ? 4 : 2) : 2 * kKeyBlocks;
-    // registers of a thread: at launch, and how setmaxnreg shares them out (softmax holds a row of S)
-    static constexpr int LAUNCH = T == PA_BF16 ? 168 : 80, OTHER = T == PA_BF16 ? 104 : 56;
-    static constexpr int OTHERS = (2 + FEEDS + 3) / 4 * 4;
+    static constexpr bool RAW = T != PA_BF16;
+    static constexpr int SOFT = 8 * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
+    static constexpr int FEEDS = RAW ? 2 * kKeyBlocks : SW == 1 ? 4 : 2;
+    static constexpr int LEAD = FEED + FEEDS;          // (FP8, FP4) two warps that the conversions wait for
+    static constexpr int OTHERS = (2 + FEEDS + (RAW ? 2 : 0) + 3) / 4 * 4;
     static constexpr int THREADS = (SOFT + OTHERS) * 32;
-    static_assert(32 * (SOFT * 200 + OTHERS * OTHER) <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "registers of an SM");
 };
 
 template <int D, pa_dtype T, int SW>
@@ -70,32 +71,38 @@ struct Layout {
     static constexpr bool RAW = T != PA_BF16;
     static constexpr int REC = T == PA_BF16 ? TILE : T == PA_FP8_E4M3 ? 16 * D + 64 : 8 * D + D / 2;
     static constexpr int KST = RAW ? 2 : 3, VST = RAW ? 2 : (SW == 1 || D == 64) ? 3 : 2;
-    static constexpr int RST = !RAW ? 0 : D == 64 ? 4 : T == PA_FP8_E4M3 ? 2 : 3;   // stages of records, K's then V's
+    // stages of records, of K and V in turn: as many as find room, six at most
+    static constexpr int HALF = kKeyBlocks * REC;
+    static constexpr int RST = !RAW ? 0 : T == PA_FP8_E4M3 && D == 128 ? 5 : 6;
+    // query rows: in the TMEM with one row tile, else in shared memory
     static constexpr int Q = 0;
-    static constexpr int K = Q + SW * QTILE;
+    static constexpr int K = Q + (SW == 2 ? SW * QTILE : 0);
     static constexpr int V = K + KST * KTILE;
     static constexpr int R = V + VST * KTILE;
-    static constexpr int BAR = R + RST * 2 * kKeyBlocks * REC;
-    static constexpr int NBAR = 36;
+    static constexpr int BAR = R + RST * HALF;
+    static constexpr int NBAR = 44;
     // what the MMA warp passes on beside the results, and the search's scratch (once, before)
     static constexpr int SLOT = BAR + NBAR * 8;       // TMEM address
     static constexpr int ODD = SLOT + 16;             // [2] of a piece: values that are no finite numbers
     static constexpr int EXPS = ODD + 16;             // [8] (K, V) exponents of a tile, as the conversions leave them
     static constexpr int PASSED = EXPS + 64;          // [8] as the MMA warp passes them on
     static constexpr int SEEN = PASSED + 64;          // [8][8] a tile's block has such values
-    static constexpr int TABLE = SEEN + 64;           // [8] FP4: a block's scales of values
-    static constexpr int BYTES0 = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);
+    static constexpr int TABLE = SEEN + 80;           // [8] FP4: a block's scales of values
+    static constexpr int GONE = TABLE - 8;            // [2] the conversions' lead gave up, K's and V's
+    static constexpr int ROWS = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);   // [row tile][2][128] maxima, sums
+    static constexpr int BYTES0 = ROWS + SW * 2 * kTileRows * 4;
     static_assert(BYTES0 <= 232448, "shared memory of one CTA");
-    static_assert((Roles<T, SW>::THREADS / 32 + 6) * 8 <= QTILE, "the search's scratch");
+    static_assert((Roles<T, SW>::THREADS / 32 + 6) * 8 <= KTILE, "the search's scratch, where the first tile goes");
     // one CTA (and its 512 TMEM columns) to an SM
     static constexpr int BYTES = BYTES0 < 122880 ? 122880 : BYTES0;
 };
 
 // barriers
-constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kRFull = 16, kREmpty = 20, kSFull = 24, kPFull = 26,
-              kODone = 28, kPVDone = 30, kQFull = 31, kOFree = 33, kDone = 34;
+constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kRFull = 16, kREmpty = 22, kSFull = 28, kPFull = 30,
+              kODone = 32, kPVDone = 34, kQFull = 35, kOFree = 37, kDone = 38, kEFull = 39;
 
-constexpr uint32_t kColS = 0, kColO = 2 * kKeys;
+// TMEM columns: two S tiles, O of each row tile; with one row tile, the query rows of two pieces.
+constexpr uint32_t kColS = 0, kColO = 2 * kKeys, kColQ = kColO + 128;
 
 constexpr uint32_t idesc(bool f16, int N, int b_mn_major) {
     return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
@@ -120,8 +127,24 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+// All lanes wait, a fifth of a second at most; the result is the same in all.  (A look costs four
+// instructions: the waiting warps share their issue slots with those that work.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs));
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    bool ok;
+    do {
+        int looks = 64;
+        do ok = mbar_try_wait(bar, parity);
+        while (!ok && --looks > 0);
+    } while (!ok && global_timer_ns() - t0 < kWaitNs);
+    return __all_sync(0xffffffffu, ok);
+}
+// One 32-byte store (the address a multiple of 32).
+__device__ __forceinline__ void st_global_v8(void* addr, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 // One lane of the warp, always the same one, in a form that the compiler sees to be one (MMAs issued
 // under `lane == 0` take about 104 clocks each, and 150 in a loop, for the descriptors' way into uniform
@@ -252,10 +275,14 @@ struct Convert<D, PA_FP8_E4M3> {
         const float f = exp2i(127 - ek);
         const float s = __uint_as_float(ld_shared_u32(raw + 16 * D + 4 * slot)) * f;
         const uint32_t h = pack_f16x2(s, s);
+        // (the loads first: the stores keep their order to later loads)
+        uint4 c[D / 32];
 #pragma unroll
-        for (int d16 = lane >> 4; d16 < D / 16; d16 += 2) {
-            const uint4 c = ld_shared_v4(raw + (d16 * kBlockTokens + slot) * 16);
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        for (int k = 0; k < D / 32; ++k) c[k] = ld_shared_v4(raw + ((2 * k + (lane >> 4)) * kBlockTokens + slot) * 16);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            const int d16 = 2 * k + (lane >> 4);
+            const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -269,6 +296,9 @@ struct Convert<D, PA_FP8_E4M3> {
     }
     static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, uint32_t, int rv, int lane, uint32_t live, uint32_t own) {
         const float f = exp2i(127 - rv);
+        uint4 code[D / 32];
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) code[k] = ld_shared_v4(raw + (32 * k + lane) * 16);
         uint32_t h[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -279,9 +309,9 @@ struct Convert<D, PA_FP8_E4M3> {
         const bool plain = live == 0xffffu && own == 0u;
         bool odd = false;
 #pragma unroll
-        for (int d = lane; d < D; d += 32) {
-            const uint4 c = ld_shared_v4(raw + d * 16);
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        for (int k = 0; k < D / 32; ++k) {
+            const int d = 32 * k + lane;
+            const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -340,13 +370,22 @@ struct Convert<D, PA_FP4_E2M1> {
     static __device__ __forceinline__ uint32_t power(uint32_t e, int r) { return e == 255u ? 0x7c00u : f16_power((int)e - r); }
     static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int ek, int lane) {
         const int slot = lane & 15;
+        uint32_t code[NB / 2][4], scale[NB / 2];
 #pragma unroll
-        for (int w = lane >> 4; w < NB; w += 2) {
-            const uint32_t e = power(code_at(raw + 8 * D + slot * NB + w), ek), h = e | e << 16;
+        for (int k = 0; k < NB / 2; ++k) {
+            const int w = 2 * k + (lane >> 4);
+            scale[k] = code_at(raw + 8 * D + slot * NB + w);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) code[k][c] = ld_shared_u32(raw + slot * (D / 2) + c * (D / 8) + 4 * w);
+        }
+#pragma unroll
+        for (int k = 0; k < NB / 2; ++k) {
+            const int w = 2 * k + (lane >> 4);
+            const uint32_t e = power(scale[k], ek), h = e | e << 16;
             uint32_t o[4][4];                                  // [c][piece]: dims 8 piece + 2 c, + 1
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                e2m1x8_to_f16x2x4(ld_shared_u32(raw + slot * (D / 2) + c * (D / 8) + 4 * w), o[c]);
+                e2m1x8_to_f16x2x4(code[k][c], o[c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[c][i] = mul_f16x2(o[c][i], h);
             }
@@ -360,6 +399,11 @@ struct Convert<D, PA_FP4_E2M1> {
                                                   uint32_t own) {
         const int r = lane & 7;
         bool odd = false;
+        uint32_t code[D / 64][4];
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) code[k][c] = ld_shared_u32(raw + ((4 * r + c) * (D / 16) + 4 * k + (lane >> 3)) * 4);
         if (lane < 8 * NB) {
             const int t = 2 * r, b = lane >> 3;
             const uint32_t at = raw + 8 * D + t * NB + b;
@@ -373,13 +417,14 @@ struct Convert<D, PA_FP4_E2M1> {
         }
         __syncwarp();
 #pragma unroll
-        for (int mi = lane >> 3; mi < D / 16; mi += 4) {
+        for (int k = 0; k < D / 64; ++k) {
+            const int mi = 4 * k + (lane >> 3);
             const uint4 lo = ld_shared_v4(table + mi / 2 * 32), hi = ld_shared_v4(table + mi / 2 * 32 + 16);
             const uint32_t h[2][4] = {{lo.x, lo.y, lo.z, lo.w}, {hi.x, hi.y, hi.z, hi.w}};
             uint32_t o[4][4];                                  // [c][dh, half]: tokens 2 c + 8 half, + 1 of dim 16 mi + 8 dh + r
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                e2m1x8_to_f16x2x4(ld_shared_u32(raw + ((4 * r + c) * (D / 16) + mi) * 4), o[c]);
+                e2m1x8_to_f16x2x4(code[k][c], o[c]);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) o[c][x] = mul_f16x2(o[c][x], h[x & 1][c]);
             }
@@ -392,6 +437,29 @@ struct Convert<D, PA_FP4_E2M1> {
         return odd;
     }
 };
+
+// n arrivals on an mbarrier.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+// A named barrier of n threads that also says whether any of them brought `x`.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id), "r"(n)
+        : "memory");
+    return r != 0u;
+}
+// 16 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 
 // One element of a value as a number, from the pool.
 template <int D, pa_dtype T>
@@ -437,18 +505,22 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
 #pragma unroll
         for (int i = 0; i < L::RST; ++i) {
             mbar_init(bar(kRFull + i), 1);
-            mbar_init(bar(kREmpty + i), W::FEEDS);
+            mbar_init(bar(kREmpty + i), kKeyBlocks + 1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSFull + i), RAW ? 2 : 1);      // (RAW: the MMA warp passes the exponents on)
-            mbar_init(bar(kPFull + i), 4);
+            mbar_init(bar(kPFull + i), 8);
             mbar_init(bar(kODone + i), 2);
-            mbar_init(bar(kQFull + i), 4);
+            mbar_init(bar(kQFull + i), 8);
         }
         mbar_init(bar(kPVDone), 1);
         mbar_init(bar(kOFree), W::SOFT);
         mbar_init(bar(kDone), 1);
+        if (RAW) {
+            for (int i = 0; i < 4; ++i) mbar_init(bar(kEFull + i), 1);
+            for (int i = 0; i < 2; ++i) *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * i) = 0u;
+        }
         fence_proxy_async_smem();
     }
     // lengths, tables, masks, queries and pools may be the previous kernels' output
@@ -469,36 +541,38 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     if (stop || walk.left == 0) return;
 
     if (warp >= W::SOFT) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::OTHER) : "memory");
     if (warp == W::COPY) {
         // ------------------------------------------------------------ bulk copies
-        // bf16: V tiles, lane b block b.  Else the records of both, lane b K's and 8 + b V's.
+        // bf16: V tiles, lane b block b.  Else the records, K's and V's of a tile one after the other.
         const uint64_t pol = l2_policy_evict_first();
-        constexpr int ST = RAW ? L::RST : VST;
+        constexpr int ST = RAW ? L::RST : VST, PER = RAW ? 2 : 1;
         const int full0 = RAW ? kRFull : kVFull, empty0 = RAW ? kREmpty : kVEmpty;
         bool ok = true;
-        int t = 0;
+        int u = 0;                                    // stages filled so far
         while (ok && walk.left > 0) {
             const Piece x = piece_at(p, walk.c, walk.left);
             Table table(p, x, lane);
-            for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
-                const int st = t % ST;
+            for (int i = 0; ok && i < x.j1 - x.j0; ++i) {
                 const int32_t blk = table.block(p, i);
-                if (t >= ST) {
-                    ok = warp_wait(bar(empty0 + st), (t / ST - 1) & 1);
-                    if (!ok) break;
-                }
-                const bool mine = blk >= 0 && lane < (RAW ? 2 * kKeyBlocks : kKeyBlocks);
+                const bool mine = blk >= 0 && lane < kKeyBlocks;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * REC;
-                if (lane == 0) {
-                    fence_proxy_async_smem();
-                    mbar_arrive_expect_tx(bar(full0 + st), bytes);
-                }
-                __syncwarp();
-                if (mine) {
-                    const char* pool = RAW && lane < kKeyBlocks ? p.k_pool : p.v_pool;
-                    const uint32_t dst = RAW ? L::R + (st * 2 * kKeyBlocks + lane) * REC : L::V + st * KTILE + lane * TILE;
-                    bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC, REC, bar(full0 + st), pol);
+#pragma unroll
+                for (int k = 0; k < PER; ++k, ++u) {
+                    const int st = u % ST;
+                    if (u >= ST) {
+                        ok = warp_wait(bar(empty0 + st), (u / ST - 1) & 1);
+                        if (!ok) break;
+                    }
+                    if (lane == 0) {
+                        fence_proxy_async_smem();
+                        mbar_arrive_expect_tx(bar(full0 + st), bytes);
+                    }
+                    __syncwarp();
+                    if (mine) {
+                        const char* pool = RAW && k == 0 ? p.k_pool : p.v_pool;
+                        const uint32_t dst = RAW ? L::R + st * L::HALF + lane * REC : L::V + st * KTILE + lane * TILE;
+                        bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC, REC, bar(full0 + st), pol);
+                    }
                 }
             }
             walk.next(p, x);
@@ -506,7 +580,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // before the CTA ends, every copy has landed
         if (lane == 0)
-            for (int u = max(0, t - ST); u < t; ++u) mbar_wait_bounded(bar(full0 + u % ST), (u / ST) & 1, kWaitNs);
+            for (int f = max(0, u - ST); f < u; ++f) mbar_wait_bounded(bar(full0 + f % ST), (f / ST) & 1, kWaitNs);
     } else if (warp == W::MMA) {
         // ------------------------------------------------------------ MMA issue
         // MMAs execute in issue order, so S(t + 2) (or S_h(t + 1) with two row tiles) overwrites
@@ -529,10 +603,13 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 if (elect_one()) {
                     const uint64_t qd = umma_desc(sbase + L::Q + hh * L::QTILE, 2048, 128);
                     const uint64_t kd = umma_desc(sbase + L::K + (t % KST) * KTILE, kKeyBlocks * 256, 128);
-                    const uint32_t dcol = tmem + kColS + (uint32_t)(buf * kKeys);
+                    const uint32_t dcol = tmem + kColS + (uint32_t)(buf * kKeys), qcol = tmem + kColQ + (uint32_t)((ic & 1) * (D / 2));
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        umma_ss(dcol, qd + (uint64_t)(ks * 256), kd + (uint64_t)((ks * 2 * kKeyBlocks * 256) >> 4), idS, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t kk = kd + (uint64_t)((ks * 2 * kKeyBlocks * 256) >> 4);
+                        if (SW == 1) umma_ts(dcol, qcol + 8 * ks, kk, idS, ks > 0);
+                        else umma_ss(dcol, qd + (uint64_t)(ks * 256), kk, idS, ks > 0);
+                    }
                     umma_commit(bar(kSFull + buf));
                     if constexpr (RAW) {
                         st_shared_v2(sbase + L::PASSED + 8 * (t & 7), ld_shared_v2(sbase + L::EXPS + 8 * (t & 7)));
@@ -564,21 +641,30 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     } else if (tok0 + nb * kBlockTokens > x.c.q.start) {
                         // slots past the last key may hold anything: zeros; values of the tree's own
                         // tokens that are no finite numbers too
-                        const int from = max(x.c.q.start - tok0, 0);
-                        for (int e = from / kBlockTokens * (D / 8) * kBlockTokens + lane; e < nb * (D / 8) * kBlockTokens; e += 32) {
-                            const int key = e / ((D / 8) * kBlockTokens) * kBlockTokens + e % kBlockTokens;
-                            if (key < from) continue;
-                            const uint32_t at = sbase + L::V + st * KTILE + e * 16;
-                            if (tok0 + key >= x.end) {
-                                st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
-                                continue;
+                        const int from = max(x.c.q.start - tok0, 0), to = x.end - tok0;
+                        const uint32_t vt = sbase + L::V + st * KTILE;
+                        constexpr int PIECES = (D / 8) * kBlockTokens;
+                        auto key_of = [&](int e) { return e / PIECES * kBlockTokens + e % kBlockTokens; };
+                        uint32_t top = 0u;                              // largest magnitudes, 16 bits each
+#pragma unroll 4
+                        for (int e = from / kBlockTokens * PIECES + lane; e < nb * PIECES; e += 32) {
+                            const int key = key_of(e);
+                            if (key >= to) {
+                                st_shared_v4(vt + e * 16, make_uint4(0u, 0u, 0u, 0u));
+                            } else if (key >= from) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(smem + L::V + st * KTILE + e * 16);
+                                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                             }
-                            uint4 v = ld_shared_v4(at);
-                            const uint4 bad = make_uint4(not_finite(v.x, 0x7f807f80u), not_finite(v.y, 0x7f807f80u),
-                                                         not_finite(v.z, 0x7f807f80u), not_finite(v.w, 0x7f807f80u));
-                            if ((bad.x | bad.y | bad.z | bad.w) != 0u) {
-                                odd = true;
-                                st_shared_v4(at, make_uint4(v.x & ~bad.x, v.y & ~bad.y, v.z & ~bad.z, v.w & ~bad.w));
+                        }
+                        if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+                            odd = true;
+                            for (int e = from / kBlockTokens * PIECES + lane; e < nb * PIECES; e += 32) {
+                                if (key_of(e) < from || key_of(e) >= to) continue;
+                                const uint4 v = ld_shared_v4(vt + e * 16);
+                                const uint32_t m = 0x7f807f80u;
+                                st_shared_v4(vt + e * 16, make_uint4(v.x & ~not_finite(v.x, m), v.y & ~not_finite(v.y, m),
+                                                                     v.z & ~not_finite(v.z, m), v.w & ~not_finite(v.w, m)));
                             }
                         }
                         fence_proxy_async_smem();
@@ -595,10 +681,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (nb == kKeyBlocks) {
 #pragma unroll
                         for (int b = 0; b < kKeyBlocks; ++b)
-                            umma_ts(ocol, pcol + 8 * b, vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                            umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
                     } else {
                         for (int b = 0; b < nb; ++b)
-                            umma_ts(ocol, pcol + 8 * b, vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                            umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
                     }
                     if (hh == SW - 1) umma_commit(bar(kVEmpty + st));
                     if (SW == 1) umma_commit(bar(kPVDone));
@@ -615,7 +701,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 }
             };
             if constexpr (SW == 1) {
-                ok = warp_wait(bar(kQFull), ic & 1);
+                ok = warp_wait(bar(kQFull + (ic & 1)), (ic >> 1) & 1);
                 for (int i = 0; ok && i < n + 2; ++i) {
                     // S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
                     if (i >= 2) issue_pv(0, i - 2);
@@ -658,6 +744,50 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (elect_one()) umma_commit(bar(kDone));
         __syncwarp();
         mbar_wait_bounded(bar(kDone), 0, kWaitNs);
+    } else if (RAW && warp >= W::LEAD) {
+        // ------------------------------------------------------------ the conversions' lead
+        // One warp for the keys, one for the values waits for a tile's records and for its place and lets
+        // eight warps go at a named barrier, so that they do not poll (28 polling warps took half of
+        // the issue slots).  The first also finds the tile's largest K scale, and V's reference: the
+        // piece's first, raised where a tile's scales pass it by 2^6.
+        if constexpr (RAW) {
+            using C = Convert<D, T>;
+            const bool for_v = warp > W::LEAD;
+            bool ok = true;
+            int t = 0;
+            while (ok && walk.left > 0) {
+                const Piece x = piece_at(p, walk.c, walk.left);
+                int rv = 0;
+                for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
+                    const int uk = 2 * t, uv = 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST;
+                    if (!for_v) {
+                        const int keys = x.end - (x.j0 + i) * kKeys;
+                        ok = warp_wait(bar(kRFull + rk), (uk / L::RST) & 1);
+                        const int ek = C::exponent(sbase + L::R + rk * L::HALF, REC, keys, lane);
+                        ok = ok && warp_wait(bar(kRFull + rs), (uv / L::RST) & 1);
+                        const int ev = C::exponent(sbase + L::R + rs * L::HALF, REC, keys, lane);
+                        if (i == 0 || ev > rv + 6) rv = ev;
+                        if (lane == 0) {
+                            st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
+                            mbar_arrive(bar(kEFull + (t & 3)));
+                            mbar_arrive(bar(kREmpty + rk));
+                            mbar_arrive(bar(kREmpty + rs));
+                        }
+                        if (t >= KST) ok = ok && warp_wait(bar(kKEmpty + t % KST), (t / KST - 1) & 1);
+                    } else {
+                        ok = warp_wait(bar(kEFull + (t & 3)), (t >> 2) & 1);
+                        if (t >= VST) ok = ok && warp_wait(bar(kVEmpty + t % VST), (t / VST - 1) & 1);
+                    }
+                    if (!ok && lane == 0) *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * for_v) = 1u;
+                    __syncwarp();
+                    // (two barriers in turn: a tile's place is free when the conversions two tiles before are done)
+                    named_bar_arrive(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
+                    if (!ok) break;
+                }
+                walk.next(p, x);
+            }
+            if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+        }
     } else if (warp < W::FEED + W::FEEDS) {
         const int f = warp - W::FEED;
         if constexpr (RAW) {
@@ -667,26 +797,22 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             using C = Convert<D, T>;
             const int b = f % kKeyBlocks;
             const bool for_v = f >= kKeyBlocks;
+            const uint32_t smem_r = sbase + L::R;
             bool ok = true;
             int t = 0;
             while (ok && walk.left > 0) {
                 const Piece x = piece_at(p, walk.c, walk.left);
-                int rv = 0;
                 for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
-                    const int rs = t % L::RST, st = for_v ? t % VST : t % KST;
-                    ok = warp_wait(bar(kRFull + rs), (t / L::RST) & 1);
-                    if (!ok) break;
-                    const uint32_t kraw = sbase + L::R + rs * 2 * kKeyBlocks * REC, vraw = kraw + kKeyBlocks * REC;
+                    // (stages of K and V in turn)
+                    const int uk = 2 * t, uv = 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST, st = for_v ? t % VST : t % KST;
+                    const uint32_t kraw = smem_r + rk * L::HALF, vraw = smem_r + rs * L::HALF;
                     const int tok0 = (x.j0 + i) * kKeys, first = tok0 + b * kBlockTokens;
-                    const int ek = for_v ? 0 : C::exponent(kraw, REC, x.end - tok0, lane);
-                    const int ev = for_v || f == 0 ? C::exponent(vraw, REC, x.end - tok0, lane) : 0;
-                    if (i == 0 || ev > rv + 6) rv = ev;
-                    if (f == 0 && lane == 0) st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
-                    const int use = for_v ? t / VST : t / KST;
-                    if (use > 0) {
-                        ok = warp_wait(bar((for_v ? kVEmpty : kKEmpty) + st), (use - 1) & 1);
-                        if (!ok) break;
-                    }
+                    named_bar_sync(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
+                    ok = *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * for_v) == 0u;
+                    if (!ok) break;
+                    mbar_test(bar(kRFull + (for_v ? rs : rk)), ((for_v ? uv : uk) / L::RST) & 1);     // (the copies are seen)
+                    const uint2 e = ld_shared_v2(sbase + L::EXPS + 8 * (t & 7));
+                    const int ek = (int)e.x, rv = (int)e.y;
                     if (for_v) {
                         bool odd = false;
                         if (first < x.end) {
@@ -704,12 +830,11 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar((for_v ? kVFull : kKFull) + st));
-                        mbar_arrive(bar(kREmpty + rs));
+                        mbar_arrive(bar(kREmpty + (for_v ? rs : rk)));
                     }
                 }
                 walk.next(p, x);
             }
-            if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         } else {
             // -------------------------------------------------------- K's pieces
             // Tiles are published in order, each as soon as its copies have landed; a new one is issued
@@ -766,56 +891,88 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         }
     }
     } else {
-    // ---------------------------------------------------------------- softmax, a row per thread
-    const int row = threadIdx.x, h = warp >> 2, lr = row & (kTileRows - 1);
+    // ---------------------------------------------------------------- softmax, a row per pair of threads
+    // Warps w and w + 4 of a row tile's eight reach the TMEM lanes 32 (w % 4) .. and share its rows: the
+    // first takes the tile's keys 0 .. 63, the second 64 .. 127 (half the code and the wait of a warp
+    // that takes them all).  They agree on the row's maximum through shared memory where it rises.
+    const int quarter = warp & 3, half = (warp >> 2) & 1, h = warp >> 3;
+    const int lr = quarter * 32 + lane, row = h * kTileRows + lr;
     const int tl = row / p.G, g = row - tl * p.G;                     // token of the row tile, query head
-    const uint32_t qdst = sbase + L::Q + h * L::QTILE + (uint32_t)((lr >> 3) * 128 + (lr & 7) * 16);
+    const uint32_t lanes_at = (uint32_t)(32 * quarter) << 16;
+    const int pair_bar = 3 + 4 * h + quarter;                         // the pair's named barrier
+    float* const shared_row = reinterpret_cast<float*>(smem + L::ROWS) + (h * 2) * kTileRows + lr;    // [half]
     const float scale = fabsf(p.scale_log2);
     // a negative scale is applied as |scale| to -q, so that the row's maximum is that of the unscaled scores
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     constexpr int QB = D / 8;
     // A warp without rows only keeps the barriers going.
-    auto busy = [&](const Piece& x) { return (row & ~31) < x.rows; };
-    auto load_q = [&](const Piece& x) {
-        if (!busy(x)) return;
-        if (tl < x.tokens) {
-            const uint16_t* src = static_cast<const uint16_t*>(p.q) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
-#pragma unroll
-            for (int u = 0; u < QB; ++u) cp_async_16(qdst + u * 2048, src + 8 * u);
-        } else {
-#pragma unroll
-            for (int u = 0; u < QB; ++u) st_shared_v4(qdst + u * 2048, make_uint4(0u, 0u, 0u, 0u));
-        }
-        cp_async_commit();
+    auto busy = [&](const Piece& x) { return row - lane < x.rows; };
+    auto q_of = [&](const Piece& x) {
+        return static_cast<const uint16_t*>(p.q) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
     };
+    uint32_t tmem = 0u;
     float factor = scale;                                             // of the row's scores
-    auto publish_q = [&](const Piece& x) {
-        cp_async_wait<0>();
-        __syncwarp();
+    // One row tile: the row goes through registers into the TMEM, columns of the piece's parity, half
+    // of them by each thread of the pair.
+    auto put_q = [&](const Piece& x, int ic) -> float {
+        float f = 1.f, f_out = scale;
         if (busy(x)) {
+            const bool valid = tl < x.tokens;
+            const uint4* src = reinterpret_cast<const uint4*>(q_of(x));
             if constexpr (RAW) {
                 uint32_t top = 0u;
-#pragma unroll
+#pragma unroll 8
                 for (int u = 0; u < QB; ++u) {
-                    const uint4 v = ld_shared_v4(qdst + u * 2048);
+                    const uint4 v = valid ? src[u] : make_uint4(0u, 0u, 0u, 0u);
                     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                 }
                 top = max(top & 0xffffu, top >> 16);
                 const int shift = min(131 - (int)(top >> 7), 110);    // (2^110 makes bf16's smallest an f16)
-                const float f = exp2i(shift);
-                factor = scale * exp2i(-shift);
-#pragma unroll
-                for (int u = 0; u < QB; ++u) {
-                    const uint4 v = ld_shared_v4(qdst + u * 2048);
-                    auto half = [&](uint32_t w) { return pack_f16x2(bf16_lo_to_f32(w) * f, bf16_hi_to_f32(w) * f) ^ flip; };
-                    st_shared_v4(qdst + u * 2048, make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
-                }
-            } else if (flip) {
+                f = exp2i(shift);
+                f_out = scale * exp2i(-shift);
+            }
 #pragma unroll 1
-                for (int u = 0; u < QB; ++u) {
-                    const uint4 v = ld_shared_v4(qdst + u * 2048);
-                    st_shared_v4(qdst + u * 2048, make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 v = valid ? src[half * (QB / 2) + 4 * c + u] : make_uint4(0u, 0u, 0u, 0u);
+                    w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
                 }
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    w[k] = (RAW ? pack_f16x2(bf16_lo_to_f32(w[k]) * f, bf16_hi_to_f32(w[k]) * f) : w[k]) ^ flip;
+                tmem_st16(tmem + lanes_at + kColQ + (ic & 1) * (D / 2) + half * (D / 4) + 16 * c, w);
+            }
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQFull + (ic & 1)));
+        return f_out;
+    };
+    // Two: into shared memory by 16-byte copies, and published later.
+    const uint32_t qdst = sbase + L::Q + h * L::QTILE + (uint32_t)((lr >> 3) * 128 + (lr & 7) * 16) + half * (QB / 2) * 2048;
+    auto load_q = [&](const Piece& x) {
+        if (!busy(x)) return;
+        if (tl < x.tokens) {
+            const uint16_t* src = q_of(x) + half * (D / 2);
+#pragma unroll
+            for (int u = 0; u < QB / 2; ++u) cp_async_16(qdst + u * 2048, src + 8 * u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < QB / 2; ++u) st_shared_v4(qdst + u * 2048, make_uint4(0u, 0u, 0u, 0u));
+        }
+        cp_async_commit();
+    };
+    auto publish_q = [&](const Piece& x) {
+        cp_async_wait<0>();
+        __syncwarp();
+        if (flip && busy(x)) {
+#pragma unroll 1
+            for (int u = 0; u < QB / 2; ++u) {
+                const uint4 v = ld_shared_v4(qdst + u * 2048);
+                st_shared_v4(qdst + u * 2048, make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
             }
         }
         fence_proxy_async_smem();
@@ -823,48 +980,55 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (lane == 0) mbar_arrive(bar(kQFull + h));
     };
     Piece x = piece_at(p, walk.c, walk.left);
-    load_q(x);
+    if constexpr (SW == 2) load_q(x);
     tc_fence_before();
     named_bar_sync(2, 32 * (W::SOFT + 1));
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::SLOT);
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
-    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::SLOT);
+    const uint32_t lanes = tmem + lanes_at;
     const uint32_t ocol = kColO + (uint32_t)(h * kKeys);
     constexpr float kLift = RAW ? 7.f : 0.f;                          // (log2) on the probabilities
-    publish_q(x);
+    if constexpr (SW == 2) publish_q(x);
+    else factor = put_q(x, 0);
     bool ok = true;
     int t0 = 0;
     for (int ic = 0; ok; ++ic) {
         const int n = x.j1 - x.j0;
         const bool live = busy(x), valid = tl < x.tokens;
         const int32_t* mrow = p.mask + (size_t)(x.qrow + (valid ? tl : 0)) * p.words;
-        Walk ahead = walk;
-        ahead.next(p, x);
-        Piece xn = x;
-        if (ahead.left > 0) xn = piece_at(p, ahead.c, ahead.left);
-        float m_used = -INFINITY, l = 0.f;
+        float m_used = -INFINITY, l = 0.f, factor_next = scale;
         int ev = 0;
-        for (int i = 0; i < n; ++i) {
+        // the row tile's warps without rows do not go through the keys: its first one arrives for them
+        const int with_rows = 2 * max(0, min(4, (x.rows - h * kTileRows + 31) / 32));
+        const bool leads = (warp & 7) == 0, runs = live || leads;
+        const uint32_t arrivals = leads ? 8 - with_rows + (with_rows > 0 ? 1 : 0) : 1;
+        auto next_q = [&]() {
+            Walk ahead = walk;
+            ahead.next(p, x);
+            if (ahead.left <= 0) return;
+            const Piece y = piece_at(p, ahead.c, ahead.left);
+            if constexpr (SW == 2) load_q(y);
+            else factor_next = put_q(y, ic + 1);
+        };
+        if (SW == 1 && !runs) next_q();
+        for (int i = 0; runs && i < n; ++i) {
             const int t = t0 + i, sb = SW == 2 ? h : t & 1;
             const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
-            const int tok0 = (x.j0 + i) * kKeys;
-            const bool full = tok0 + kKeys <= x.c.q.start;
+            const int first = (x.j0 + i) * kKeys + 64 * half - x.c.q.start;      // this thread's first key, as a node
             // the visible keys of 32 columns are the bits of a word: the context's, then the row's mask
-            uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            const bool full = first + 64 <= 0;
             if (!full && live) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int node = tok0 + 32 * c - x.c.q.start, left = x.c.q.n - node;
-                    uint32_t v;
+                for (int c = 0; c < 2; ++c) {
+                    const int node = first + 32 * c, left = x.c.q.n - node;
+                    uint32_t v = 0u;
                     if (node < 0) {
                         v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
                     } else if (left > 0) {
                         const uint32_t lo = (uint32_t)__ldg(mrow + node / 32);
                         const uint32_t hi = (node & 31) != 0 && node / 32 + 1 < p.words ? (uint32_t)__ldg(mrow + node / 32 + 1) : 0u;
                         v = __funnelshift_r(lo, hi, node & 31);
-                    } else {
-                        v = 0u;
                     }
                     if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
                     see[c] = valid ? v : 0u;
@@ -872,13 +1036,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             }
             ok = warp_wait(bar(kSFull + sb), SW == 2 ? (t & 1) : ((t >> 1) & 1));
             if (!ok) break;
-            if (i == n - 1 && ahead.left > 0) load_q(xn);             // (the piece's scores are taken: Q is free)
-            tc_fence_after();
+            // (two row tiles: this piece's scores are taken, their Q is free)
+            if (SW == 2 && i == n - 1) next_q();
             if (live) {
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(lanes + scol + 32 * c, sr[c]);
-                tmem_wait_ld();
+                tc_fence_after();
                 float c1 = factor;
                 float drop = 1.f;                                     // what a raise of V's power of two puts on O
                 if constexpr (RAW) {
@@ -888,61 +1049,75 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     ev = (int)e.y;
                 }
                 c1 = fmaxf(c1, FLT_MIN);                              // (a hidden key's -inf stays -inf under a scale of 0)
-                if (!full) {
-                    // hidden keys score -inf (a select: unread or stale columns may hold NaN)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!((see[c] >> k) & 1u)) sr[c][k] = 0xff800000u;
-                }
+                const uint32_t mine = lanes + scol + 64 * half;
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t sr[32];
+                    tmem_ld32(mine + 32 * c, sr);
+                    tmem_wait_ld();
+                    if (!full) {
+                        // hidden keys score -inf (a select: unread or stale columns may hold NaN)
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) m4[c] = max3(m4[c], __uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1]));
-                const float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
-                float alpha = 1.f;
-                bool raise = drop != 1.f;
-                if (mx > m_used + kRaise) {                           // (the first keys: from -inf)
-                    alpha = fast_exp2(m_used - mx);
-                    raise |= i > 0;
-                    m_used = mx;
+                        for (int k = 0; k < 32; ++k)
+                            if (!((see[c] >> k) & 1u)) sr[k] = 0xff800000u;
+                        tmem_st32(mine + 32 * c, sr);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        m4[2 * c + (k >> 4)] = max3(m4[2 * c + (k >> 4)], __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
                 }
-                if (__any_sync(0xffffffffu, raise)) {
-                    // with S double-buffered, S(t) complete does not imply P V(t - 1) complete
-                    if (SW == 1) {
-                        ok = warp_wait(bar(kPVDone), (t - 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
+                if (!full) tmem_wait_st();
+                float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
+                // whether a row of the pair of warps rises, or V's power of two
+                const bool rise = named_bar_or(pair_bar, 64, mx > m_used + kRaise || drop != 1.f);
+                float alpha = 1.f;
+                if (rise) {
+                    shared_row[half * kTileRows] = mx;
+                    named_bar_sync(pair_bar, 64);
+                    mx = fmaxf(mx, shared_row[(half ^ 1) * kTileRows]);
+                    if (mx > m_used + kRaise) {                       // (the first keys: from -inf)
+                        alpha = fast_exp2(m_used - mx);
+                        m_used = mx;
                     }
-                    const float on_o = alpha * drop;
+                    if (i > 0) {
+                        // with S double-buffered, S(t) complete does not imply P V(t - 1) complete
+                        if (SW == 1) {
+                            ok = warp_wait(bar(kPVDone), (t - 1) & 1);
+                            tc_fence_after();
+                        }
+                        const float on_o = alpha * drop;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(lanes + ocol + 32 * c, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < D / 32 && ok; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(lanes + ocol + half * (D / 2) + 16 * c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * on_o);
-                        tmem_st32(lanes + ocol + 32 * c, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * on_o);
+                            tmem_st16(lanes + ocol + half * (D / 2) + 16 * c, o);
+                        }
                     }
+                    named_bar_sync(pair_bar, 64);                     // (the maxima are read)
+                    if (!ok) break;
                 }
                 // probabilities, rounded to the tensor cores' type (the sums take them unrounded: the
-                // roundings are of either sign and average out), over the first half of S's columns
+                // roundings are of either sign and average out), over the first columns of this thread's part of S
                 const float m_sub = (m_used == -INFINITY ? 0.f : m_used) - kLift;
                 const uint64_t c2 = pair_of(c1, c1), nm2 = pair_of(-m_sub, -m_sub);
                 uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t sr[32], pk[16];
+                    tmem_ld32(mine + 32 * c, sr);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        const uint64_t y = fma2(pair_of(__uint_as_float(sr[c][k]), __uint_as_float(sr[c][k + 1])), c2, nm2);
+                        const uint64_t y = fma2(pair_of(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
                         const float e0 = fast_exp2(pair_lo(y)), e1 = fast_exp2(pair_hi(y));
                         sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pair_of(e0, e1));
                         pk[k >> 1] = RAW ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
                     }
-                    tmem_st16(lanes + scol + 16 * c, pk);
+                    tmem_st16(mine + 16 * c, pk);
                 }
                 const uint64_t sum = add2(sum2[0], sum2[1]);
                 l = l * alpha + (pair_lo(sum) + pair_hi(sum));
@@ -950,79 +1125,103 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kPFull + sb));
+            if (lane == 0) mbar_arrive_n(bar(kPFull + sb), arrivals);
+            // (the last piece's scores are taken: their Q is free)
+            if (SW == 1 && i == 0) next_q();
         }
         if (!ok) break;
         ok = warp_wait(bar(kODone + h), ic & 1);
         if (!ok) break;
+        if (SW == 2 && !runs) next_q();
         tc_fence_after();
         if (live) {
-            const bool odd = *reinterpret_cast<volatile uint32_t*>(smem + L::ODD + 4 * (ic & 1)) != 0u;
+            // the row's sum, of both halves in their order
+            shared_row[half * kTileRows] = l;
+            named_bar_sync(pair_bar, 64);
+            l = shared_row[0] + shared_row[kTileRows];
             const bool whole = x.j0 == 0 && x.j1 == x.c.q.tiles;
-            const size_t slot = (size_t)(2 * blockIdx.x + (ic == 0 ? 0 : 1)) * p.slot_rows + row;
+            const size_t piece = (size_t)(2 * blockIdx.x + (ic == 0 ? 0 : 1));
             const size_t orow = ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
             // what is left on O: V's power of two, the probabilities' lift where the sums do not share it
             const float back = RAW ? exp2i(ev - 127) : 1.f;
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : exp2i(-(int)kLift);
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0u;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
-                tmem_ld32(lanes + ocol + 32 * c, o);
+                const int col = half * (D / 2) + 32 * c;
+                tmem_ld32(lanes + ocol + col, o);
                 tmem_wait_ld();
                 if (valid) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float y = __uint_as_float(o[k]) * inv;
-                    if (RAW) y *= back;
-                    o[k] = __float_as_uint(inv != 0.f ? y : 0.f);     // (no key that the row sees: O may be anything)
-                }
-                if (odd) {
-                    // the rare values that are no finite numbers, of the tokens that the row sees
-                    const int32_t* trow = p.tables + (size_t)x.c.s * p.max_blocks;
-                    for (int tok = max(x.c.q.start, x.j0 * kKeys); tok < min(x.end, x.j1 * kKeys); ++tok) {
-                        const int node = tok - x.c.q.start;
-                        if (!(((uint32_t)__ldg(mrow + node / 32) >> (node & 31)) & 1u)) continue;
-                        const int32_t blk = __ldg(trow + tok / kBlockTokens);
-                        if (blk < 0 || blk >= p.num_blocks) continue;
-                        const char* rec = p.v_pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC;
+                    for (int k = 0; k < 32; ++k) {
+                        float y = __uint_as_float(o[k]) * inv;
+                        if (RAW) y *= back;
+                        o[k] = __float_as_uint(inv != 0.f ? y : 0.f);     // (no key that the row sees: O may be anything)
+                    }
+                    if (whole) {
+                        uint16_t* dst = static_cast<uint16_t*>(p.out) + orow + col;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float y = value_at<D, T>(rec, tok % kBlockTokens, 32 * c + k);
-                            if (!(fabsf(y) <= FLT_MAX)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+                        for (int v = 0; v < 2; ++v) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * k]), __uint_as_float(o[16 * v + 2 * k + 1]));
+                            if (wide) {
+                                st_global_v8(dst + 16 * v, w);
+                            } else {
+                                reinterpret_cast<uint4*>(dst + 16 * v)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                reinterpret_cast<uint4*>(dst + 16 * v)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
                         }
-                    }
-                }
-                if (whole) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + 32 * c);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (piece * (D / 4) + col / 4) * p.slot_rows + row;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        auto two = [&](int k) { return pack_bf16x2(__uint_as_float(o[8 * v + k]), __uint_as_float(o[8 * v + k + 1])); };
-                        dst[v] = make_uint4(two(0), two(2), two(4), two(6));
+                        for (int v = 0; v < 8; ++v)
+                            dst[(size_t)v * p.slot_rows] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                     }
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot * D + 32 * c);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-                }
                 }
                 __syncwarp();
             }
-            if (valid && !whole) p.part_ml[slot] = make_float2(m_used, l * exp2i(-(int)kLift));
+            if (valid && !whole && half == 0) p.part_ml[piece * p.slot_rows + row] = make_float2(m_used, l * exp2i(-(int)kLift));
+            if (valid && *reinterpret_cast<volatile uint32_t*>(smem + L::ODD + 4 * (ic & 1)) != 0u) {
+                // the rare values that are no finite numbers, of the tokens that the row sees, on what was stored
+                const int32_t* trow = p.tables + (size_t)x.c.s * p.max_blocks;
+                for (int tok = max(x.c.q.start, x.j0 * kKeys); tok < min(x.end, x.j1 * kKeys); ++tok) {
+                    const int node = tok - x.c.q.start;
+                    if (!(((uint32_t)__ldg(mrow + node / 32) >> (node & 31)) & 1u)) continue;
+                    const int32_t blk = __ldg(trow + tok / kBlockTokens);
+                    if (blk < 0 || blk >= p.num_blocks) continue;
+                    const char* rec = p.v_pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC;
+#pragma unroll 1
+                    for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
+                        const float y = value_at<D, T>(rec, tok % kBlockTokens, d);
+                        if (fabsf(y) <= FLT_MAX) continue;
+                        if (whole) {
+                            __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.out) + orow + d;
+                            *at = __float2bfloat16_rn(__bfloat162float(*at) + y);
+                        } else {
+                            p.part_o[((piece * (D / 4) + d / 4) * p.slot_rows + row) * 4 + d % 4] += y;
+                        }
+                    }
+                }
+            }
         }
         // O is read: the next piece's P V may start afresh
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kOFree));
         t0 += n;
-        walk = ahead;
+        walk.next(p, x);
         if (walk.left <= 0) break;
-        x = xn;
-        publish_q(x);
+        x = piece_at(p, walk.c, walk.left);
+        if constexpr (SW == 2) publish_q(x);
+        else factor = factor_next;
     }
     if (!ok) {
         // a wait gave up: the rows of this piece and of the later ones are incomplete and become NaN
         if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
-        for (int ic = 0; walk.left > 0; ++ic) {
+        while (walk.left > 0) {
             x = piece_at(p, walk.c, walk.left);
             if (tl < x.tokens) {
                 const float nan = __int_as_float(0x7fc00000);
@@ -1054,8 +1253,7 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t stream) {
     const int ctas = std::min(tree_sms(), kTreeCtas);
     const TParams p = tree_params(a, SW * kTileRows, ctas);
     e = tree_launch(tree_tc_kernel<D, T, SW>, dim3(ctas), Roles<T, SW>::THREADS, smem, stream, p);
-    if (e != cudaSuccess || ctas == 1) return e;
-    return tree_launch(tree_merge_kernel<D, __nv_bfloat16>, tree_merge_grid(p), kMergeThreads, 0, stream, p);
+    return e != cudaSuccess ? e : launch_merge<D, __nv_bfloat16>(p, stream);
 }
 
 template <int D>
