@@ -72,8 +72,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
     if (tid == 0) say_joint(p, line, cur, blockIdx.x, any);
     if (!any || tree_aborted(p.err)) return;
     long long left = line.begin(blockIdx.x + 1) - line.begin(blockIdx.x);
+    if (left <= kItemCost - cur.at) return;
     for (bool first_piece = true; left > 0; first_piece = false) {
-        const int j0 = cur.j, j1 = (int)min((long long)cur.q.tiles, cur.j + left);
+        const int j0 = Cursor::tile(cur.at), j1 = Cursor::tile((int)min((long long)cur.cost(), cur.at + left));
         const int tokens = item_tokens(p, cur), rows = tokens * p.G;
         const int qrow = cur.q.q0 + cur.rt * p.TQ, end = cur.q.start + cur.q.n;
         const int32_t* trow = p.tables + (size_t)cur.s * p.max_blocks;
@@ -240,8 +241,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
             }
             if (!whole && tx == 0) p.part_ml[slot * p.slot_rows + row] = make_float2(m[r], l[r]);
         }
-        left -= j1 - j0;
-        if (left > 0) next_item<kKeys>(p, cur);
+        left -= cur.cost() - cur.at;
+        if (left <= kItemCost) break;             // (ends before an item's first tile)
+        next_item<kKeys>(p, cur);
     }
 }
 

@@ -1,10 +1,12 @@
 // pa_tree.cuh -- how the work of the tree attention is handed out, for its kernels.
 //
 // An item is (sequence, kv head, row tile): ROWS query rows at most of one kv head, whole tokens,
-// against all keys of the sequence, cut into key tiles.  The items' key tiles, in the order of the
-// sequences, then heads, then row tiles, form one line, and CTA c of C takes the tiles c T / C ..
-// (c + 1) T / C - 1 of its T: contexts may be as uneven as they like, every CTA has the same work,
-// and no lengths are needed on the host.  A CTA's run of tiles of one item is a piece.  A piece that
+// against all keys of the sequence, cut into key tiles.  The items, in the order of the sequences,
+// then heads, then row tiles, form one line, each kItemCost places (what its beginning and end cost,
+// in tiles: 64 sequences of 400 to 7800 tokens, 32 / 8 heads, 32 nodes, 244 us without) and one for every
+// tile, and CTA c of C takes the places c T / C .. (c + 1) T / C - 1 of its T: contexts may be as uneven
+// as they like, every CTA has the same work, and no lengths are needed on the host.  A CTA's run of
+// tiles of one item is a piece.  A piece that
 // is a whole item gives its outputs; others leave partial results (sums, maxima, unnormalised
 // outputs), of which a CTA has two at most, its first and its last piece, and the merge kernel joins
 // those of each item in the order of its keys.  Everything is a function of the lengths, so equal
@@ -20,6 +22,8 @@
 namespace pa {
 
 namespace {
+
+constexpr int kItemCost = 2;
 
 constexpr float kTreeLog2e = 1.4426950408889634f;
 
@@ -84,33 +88,36 @@ __device__ __forceinline__ TreeSeq tree_seq(const TParams& p, int s) {
     return x;
 }
 
-// A place in the line of tiles.
+// A place in the line.
 struct Cursor {
-    int s, h, rt, j;         // sequence, kv head, row tile, key tile
+    int s, h, rt, at;        // sequence, kv head, row tile, place of the item
     TreeSeq q;
+    __device__ __forceinline__ int cost() const { return q.tiles + kItemCost; }
+    // the first key tile from a place on
+    static __device__ __forceinline__ int tile(int at) { return max(at - kItemCost, 0); }
 };
 
-// The line: its tiles, C, and the first tile of CTA c.
+// The line: its places, C, and the first place of CTA c.
 struct Line {
     long long total, base;   // base = total / ctas
     uint32_t rest;           // total % ctas
     int ctas;
-    __device__ __forceinline__ Line(long long tiles, long long most, int limit) {
-        total = tiles;
+    __device__ __forceinline__ Line(long long places, long long most, int limit) {
+        total = places;
         ctas = most < 1 ? 1 : most < limit ? (int)most : limit;
         // (a division of 64 bits takes as long as a trip to L2)
-        if (tiles < 1ll << 32) {
-            base = (uint32_t)tiles / (uint32_t)ctas;
-            rest = (uint32_t)tiles % (uint32_t)ctas;
+        if (places < 1ll << 32) {
+            base = (uint32_t)places / (uint32_t)ctas;
+            rest = (uint32_t)places % (uint32_t)ctas;
         } else {
-            base = tiles / ctas;
-            rest = (uint32_t)(tiles % ctas);
+            base = places / ctas;
+            rest = (uint32_t)(places % ctas);
         }
     }
     __device__ __forceinline__ long long begin(int c) const { return base * c + rest * (uint32_t)c / (uint32_t)ctas; }
 };
 
-// The line, and the place of tile `begin_of(line)` in it where there is one (begin >= 0 and below
+// The line, and the cursor of place `begin_of(line)` in it where there is one (begin >= 0 and below
 // the total), found by all NT threads.  `sm`: NT / 32 + 6 words of 64 bits.
 template <int NT, int KT, int MIN_TILES, typename Begin>
 __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, bool report, Begin begin_of, Cursor& cur) {
@@ -121,7 +128,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
     for (int s = s0; s < s1; ++s) {
         one = tree_seq<KT>(p, s);
         if (report && one.bad) raise_flag(p.err, one.bad);
-        mine += (long long)one.tiles * one.rts * p.Hkv;
+        mine += (long long)(one.tiles + kItemCost) * one.rts * p.Hkv;
     }
     long long incl = mine;
 #pragma unroll
@@ -145,7 +152,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
         int s = s0;
         for (; each > 1; ++s) {
             one = tree_seq<KT>(p, s);
-            const long long len = (long long)one.tiles * one.rts * p.Hkv;
+            const long long len = (long long)(one.tiles + kItemCost) * one.rts * p.Hkv;
             if (begin < at + len || s + 1 >= s1) break;
             at += len;
         }
@@ -165,9 +172,9 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
         cur.s = from[0];
         cur.q = TreeSeq{from[1], from[2], from[3], from[4], from[5], 0};
         const long long off = sm[NT / 32];
-        // (a sequence's own tiles: its heads, row tiles and keys hardly ever pass 2^32)
-        const int item = off < 1ll << 32 ? (int)((uint32_t)off / (uint32_t)cur.q.tiles) : (int)(off / cur.q.tiles);
-        cur.j = (int)(off - (long long)item * cur.q.tiles);
+        // (a sequence's heads, row tiles and keys hardly ever pass 2^32)
+        const int item = off < 1ll << 32 ? (int)((uint32_t)off / (uint32_t)cur.cost()) : (int)(off / cur.cost());
+        cur.at = (int)(off - (long long)item * cur.cost());
         cur.h = item / cur.q.rts;
         cur.rt = item - cur.h * cur.q.rts;
     }
@@ -177,7 +184,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
 // The item after the cursor's (there is one).
 template <int KT>
 __device__ __forceinline__ void next_item(const TParams& p, Cursor& c) {
-    c.j = 0;
+    c.at = 0;
     if (++c.rt < c.q.rts) return;
     c.rt = 0;
     if (++c.h < p.Hkv) return;
@@ -229,12 +236,14 @@ inline TParams tree_params(const TreeArgs& a, int rows, int ctas) {
 // What CTA c says of the item that its begin cuts (one thread of it).
 __device__ __forceinline__ void say_joint(const TParams& p, const Line& line, const Cursor& cur, int c, bool any) {
     Joint x{0, 0, 0, 0};
-    if (any && cur.j > 0) {
-        const long long from = line.begin(c) - cur.j, to = from + cur.q.tiles;
-        if (line.begin(c - 1) <= from) {
+    const int j = Cursor::tile(cur.at);
+    if (any && j > 0) {
+        const long long from = line.begin(c) - cur.at, to = from + cur.cost();
+        // (the CTA before has tiles of the item, and is the first that has)
+        if (line.begin(c - 1) <= from + kItemCost) {
             // the CTA of the item's last tile: where it would be with even shares, or beside that
-            const long long each = line.base > 0 ? line.base : 1;
-            int last = (int)min((long long)line.ctas - 1, c + (cur.q.tiles - cur.j) / each);
+            const uint32_t each = line.base > 0 && line.base < 1ll << 31 ? (uint32_t)line.base : line.base > 0 ? 1u << 31 : 1u;
+            int last = (int)min((long long)line.ctas - 1, c + (long long)((uint32_t)(cur.cost() - cur.at) / each));
             while (line.begin(last) >= to) --last;
             while (last + 1 < line.ctas && line.begin(last + 1) < to) ++last;
             x.count = last - c + 2;

@@ -197,8 +197,8 @@ struct Piece {
 __device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor& c, long long left) {
     Piece x;
     x.c = c;
-    x.j0 = c.j;
-    x.j1 = (int)min((long long)c.q.tiles, c.j + left);
+    x.j0 = Cursor::tile(c.at);
+    x.j1 = Cursor::tile((int)min((long long)c.cost(), c.at + left));
     x.tokens = item_tokens(p, c);
     x.rows = x.tokens * p.G;
     x.qrow = c.q.q0 + c.rt * p.TQ;
@@ -208,10 +208,12 @@ __device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor& c, lon
 }
 struct Walk {
     Cursor c;
-    long long left;          // tiles from the cursor on
-    __device__ __forceinline__ void next(const TParams& p, const Piece& x) {
-        left -= x.j1 - x.j0;
-        if (left > 0) next_item<kKeys>(p, c);
+    long long left;          // places from the cursor on
+    // To the next item with tiles for this CTA (a run that ends before an item's first tile has none).
+    __device__ __forceinline__ void next(const TParams& p) {
+        left -= c.cost() - c.at;
+        if (left > kItemCost) next_item<kKeys>(p, c);
+        else left = 0;
     }
 };
 
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     // lengths, tables, masks, queries and pools may be the previous kernels' output
     grid_dependency_wait();
     grid_launch_dependents();
+    const bool aborted = tree_aborted(p.err);             // (every thread: the load is under way with the lengths')
     Walk walk;
     {
         const Line line = tree_locate<W::THREADS, kKeys, kMinTiles>(
@@ -533,12 +536,11 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, walk.c);
         const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
         walk.left = any ? line.begin(blockIdx.x + 1) - line.begin(blockIdx.x) : 0;
-        // (said whether or not the call goes on)
-        if (threadIdx.x == 32 * W::FEED) say_joint(p, line, walk.c, blockIdx.x, any);
+        if (walk.left <= kItemCost - walk.c.at) walk.left = 0;            // (ends before a first tile)
+        // (said whether or not the call goes on, by the last thread, which has the least to do)
+        if (threadIdx.x == W::THREADS - 1) say_joint(p, line, walk.c, blockIdx.x, any);
     }
-    // (also orders the search's scratch before the queries that take its place)
-    const bool stop = __syncthreads_or(threadIdx.x == 0 && tree_aborted(p.err));
-    if (stop || walk.left == 0) return;
+    if (aborted || walk.left == 0) return;
 
     if (warp >= W::SOFT) {
     if (warp == W::COPY) {
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     }
                 }
             }
-            walk.next(p, x);
+            walk.next(p);
         }
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // before the CTA ends, every copy has landed
@@ -737,7 +739,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 }
             }
             t0 += n;
-            walk.next(p, x);
+            walk.next(p);
         }
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // nothing may still be running on the tensor cores when the TMEM is freed
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     named_bar_arrive(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
                     if (!ok) break;
                 }
-                walk.next(p, x);
+                walk.next(p);
             }
             if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         }
@@ -833,7 +835,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         mbar_arrive(bar(kREmpty + (for_v ? rs : rk)));
                     }
                 }
-                walk.next(p, x);
+                walk.next(p);
             }
         } else {
             // -------------------------------------------------------- K's pieces
@@ -884,7 +886,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (lane == 0) mbar_arrive(bar(kKFull + (t0 + pub) % KST));
                 }
                 t0 += n;
-                walk.next(p, x);
+                walk.next(p);
             }
             if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
             cp_async_wait<0>();
@@ -1004,7 +1006,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         const uint32_t arrivals = leads ? 8 - with_rows + (with_rows > 0 ? 1 : 0) : 1;
         auto next_q = [&]() {
             Walk ahead = walk;
-            ahead.next(p, x);
+            ahead.next(p);
             if (ahead.left <= 0) return;
             const Piece y = piece_at(p, ahead.c, ahead.left);
             if constexpr (SW == 2) load_q(y);
@@ -1212,7 +1214,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kOFree));
         t0 += n;
-        walk.next(p, x);
+        walk.next(p);
         if (walk.left <= 0) break;
         x = piece_at(p, walk.c, walk.left);
         if constexpr (SW == 2) publish_q(x);
@@ -1231,7 +1233,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D);
                 for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
             }
-            walk.next(p, x);
+            walk.next(p);
         }
     }
     // (no query copy may still be landing when the CTA ends)
