@@ -23,7 +23,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 4;
 
 constexpr float kTreeLog2e = 1.4426950408889634f;
 

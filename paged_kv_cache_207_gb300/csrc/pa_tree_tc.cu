@@ -46,7 +46,7 @@ namespace {
 constexpr uint64_t kWaitNs = 200000000ull;
 constexpr int kTileRows = 128;
 constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
-constexpr int kMinTiles = 2;
+constexpr int kMinTiles = 3;             // places of a CTA, at least
 constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at most
 
 // Warps: softmax 0 .. 8 SW - 1, the copies (bf16: V's; else all records), the MMAs, then K's copies
@@ -528,7 +528,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     // lengths, tables, masks, queries and pools may be the previous kernels' output
     grid_dependency_wait();
     grid_launch_dependents();
-    const bool aborted = tree_aborted(p.err);             // (every thread: the load is under way with the lengths')
+    int32_t flag = 0;                                     // (under way with the lengths)
+    if (threadIdx.x == 0 && p.err) flag = *reinterpret_cast<const volatile int32_t*>(p.err);
     Walk walk;
     {
         const Line line = tree_locate<W::THREADS, kKeys, kMinTiles>(
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         // (said whether or not the call goes on, by the last thread, which has the least to do)
         if (threadIdx.x == W::THREADS - 1) say_joint(p, line, walk.c, blockIdx.x, any);
     }
-    if (aborted || walk.left == 0) return;
+    // (the same for all threads, and the search's scratch is free)
+    if (__syncthreads_or(flag & PA_DEV_ERR_TIMEOUT) || walk.left == 0) return;
 
     if (warp >= W::SOFT) {
     if (warp == W::COPY) {
@@ -642,19 +644,22 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         odd |= (o.x | o.y) != 0u;
                     } else if (tok0 + nb * kBlockTokens > x.c.q.start) {
                         // slots past the last key may hold anything: zeros; values of the tree's own
-                        // tokens that are no finite numbers too
+                        // tokens that are no finite numbers too (looked for in all of its blocks)
                         const int from = max(x.c.q.start - tok0, 0), to = x.end - tok0;
-                        const uint32_t vt = sbase + L::V + st * KTILE;
-                        constexpr int PIECES = (D / 8) * kBlockTokens;
-                        auto key_of = [&](int e) { return e / PIECES * kBlockTokens + e % kBlockTokens; };
+                        uint8_t* const vt = smem + L::V + st * KTILE;
+                        constexpr int PIECES = (D / 8) * kBlockTokens;                 // of a block
+                        if (to < nb * kBlockTokens) {
+                            uint8_t* const last = vt + (nb - 1) * TILE;
+                            for (int e = lane; e < PIECES; e += 32)
+                                if ((nb - 1) * kBlockTokens + e % kBlockTokens >= to)
+                                    *reinterpret_cast<uint4*>(last + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            __syncwarp();
+                        }
                         uint32_t top = 0u;                              // largest magnitudes, 16 bits each
-#pragma unroll 4
-                        for (int e = from / kBlockTokens * PIECES + lane; e < nb * PIECES; e += 32) {
-                            const int key = key_of(e);
-                            if (key >= to) {
-                                st_shared_v4(vt + e * 16, make_uint4(0u, 0u, 0u, 0u));
-                            } else if (key >= from) {
-                                const uint4 v = *reinterpret_cast<const uint4*>(smem + L::V + st * KTILE + e * 16);
+                        for (int b = from / kBlockTokens; b < nb; ++b) {
+#pragma unroll
+                            for (int e = 0; e < PIECES / 32; ++e) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(vt + b * TILE + (32 * e + lane) * 16);
                                 top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
                                                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                             }
@@ -662,11 +667,12 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
                             odd = true;
                             for (int e = from / kBlockTokens * PIECES + lane; e < nb * PIECES; e += 32) {
-                                if (key_of(e) < from || key_of(e) >= to) continue;
-                                const uint4 v = ld_shared_v4(vt + e * 16);
+                                const int key = e / PIECES * kBlockTokens + e % kBlockTokens;
+                                if (key < from) continue;
+                                const uint4 v = *reinterpret_cast<const uint4*>(vt + e * 16);
                                 const uint32_t m = 0x7f807f80u;
-                                st_shared_v4(vt + e * 16, make_uint4(v.x & ~not_finite(v.x, m), v.y & ~not_finite(v.y, m),
-                                                                     v.z & ~not_finite(v.z, m), v.w & ~not_finite(v.w, m)));
+                                *reinterpret_cast<uint4*>(vt + e * 16) =
+                                    make_uint4(v.x & ~not_finite(v.x, m), v.y & ~not_finite(v.y, m), v.z & ~not_finite(v.z, m), v.w & ~not_finite(v.w, m));
                             }
                         }
                         fence_proxy_async_smem();
