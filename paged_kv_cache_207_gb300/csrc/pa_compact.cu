@@ -7,8 +7,8 @@
 // destination, so no row is written where a later one still has to be read if rows are read in
 // order, each before what it is read over by is written: a CTA takes all rows of its share of a (sequence, kv
 // head, pool) -- the 16-byte pieces, dims or words that a pool's tile consists of do not mix --
-// chunk by chunk, loads the next chunk into registers, waits for all its threads, and stores the one
-// before.  Into other blocks nothing is in the way, and the rows too are shared out.
+// chunk by chunk, loads chunks ahead into registers, waits for all its threads, and stores the first of
+// them.  Into other blocks nothing is in the way, and the rows too are shared out.
 //
 // Chunks are whole blocks of the destination, so that a block's bytes that hold several slots (the
 // 8- and 4-bit values, transposed in their tiles) have one writer.
@@ -25,10 +25,12 @@ namespace {
 
 constexpr int kCompactThreads = 256;
 constexpr int kBatchBlocks = 64, kBatchRows = kBatchBlocks * kBlockTokens;   // whose places are looked up together
-constexpr int kUnits = 4;                  // 16-byte pieces of a thread under way
+constexpr int kUnits = 2, kDepth = 2;      // 16-byte pieces of a thread's chunk, and chunks under way
+constexpr int kSmCtas = 5;                 // CTAs of an SM, which bound the registers
 
 struct KParams {
-    char* pool[2];
+    char* k_pool;
+    char* v_pool;
     const int32_t* src_tables;
     const int32_t* dst_tables;
     const int32_t* src_pos;
@@ -37,11 +39,13 @@ struct KParams {
     int32_t* err;
     int src_blocks, dst_blocks;            // widths of the tables
     int total, num_blocks, Hkv;
-    int slices, segs;                      // of a (sequence, kv head, pool): shares of its tiles, of its rows
+    int slice_bits, segs;                  // of a (sequence, kv head, pool): 2^slice_bits shares of its tiles, shares of its rows
     bool in_place;
 };
 
-struct From { int32_t blk, slot; };        // where a row comes from; blk -1: it does not move
+// Where a row comes from: its tile's byte offset in the pool (a multiple of 16) and its slot; -1: it does not move.
+using From = int64_t;
+__device__ __forceinline__ int slot_of(From f) { return (int)f & (kBlockTokens - 1); }
 
 // The geometry of a (block, kv head) tile.
 template <pa_dtype T, int D>
@@ -59,60 +63,37 @@ struct Tile {
     }
 };
 
-// One dim's 16 slots of FP8 values, or the four words of 16 dims mi and r of FP4 values.
+// One dim's 16 slots of FP8 values (16 bytes), or the four words of 16 dims mi and r of FP4 values.
 struct Mixed { uint32_t w[4]; };
 
 template <pa_dtype T, int D>
-__device__ __forceinline__ Mixed load_mixed(const char* rec, int u) {
-    Mixed x;
-    if constexpr (T == PA_FP8_E4M3) {
-        const uint4 v = *reinterpret_cast<const uint4*>(rec + u * 16);
-        x.w[0] = v.x; x.w[1] = v.y; x.w[2] = v.z; x.w[3] = v.w;
-    } else {
-        const int r = u / (D / 16), mi = u % (D / 16);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x.w[c] = *reinterpret_cast<const uint32_t*>(rec + ((4 * r + c) * (D / 16) + mi) * 4);
-    }
-    return x;
+__device__ __forceinline__ uint32_t mixed_at(int u, int i) {       // byte offset of word i
+    return T == PA_FP8_E4M3 ? u * 16 + i * 4 : ((4 * (u / (D / 16)) + i) * (D / 16) + u % (D / 16)) * 4;
 }
+// What slot `slot` of a unit holds, at the place of slot t (compile-time) of its word t / 4 (FP8) or t / 2 % 4.
 template <pa_dtype T, int D>
-__device__ __forceinline__ void store_mixed(char* rec, int u, const Mixed& x) {
-    if constexpr (T == PA_FP8_E4M3) {
-        *reinterpret_cast<uint4*>(rec + u * 16) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
-    } else {
-        const int r = u / (D / 16), mi = u % (D / 16);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint32_t*>(rec + ((4 * r + c) * (D / 16) + mi) * 4) = x.w[c];
-    }
+__device__ __forceinline__ uint32_t load_slot(const char* tile, int u, int slot) {
+    if constexpr (T == PA_FP8_E4M3) return *reinterpret_cast<const uint8_t*>(tile + u * 16 + slot);
+    // bytes (dh, half) of word c hold slots 2 c + 8 half, + 1: the two dims' nibbles of a slot
+    else return (*reinterpret_cast<const uint32_t*>(tile + mixed_at<T, D>(u, (slot >> 1) & 3)) >> (8 * (slot >> 3) + 4 * (slot & 1))) & 0x000f000fu;
 }
-__device__ __forceinline__ uint32_t pick(const Mixed& x, int i) {
-    return i & 2 ? (i & 1 ? x.w[3] : x.w[2]) : (i & 1 ? x.w[1] : x.w[0]);
-}
-// Slot t of a unit (compile-time t) becomes slot `from` of another.
 template <pa_dtype T>
-__device__ __forceinline__ void put_slot(Mixed& x, int t, const Mixed& y, int from) {
-    if constexpr (T == PA_FP8_E4M3) {
-        const uint32_t v = (pick(y, from >> 2) >> (8 * (from & 3))) & 0xffu;
-        const int sh = 8 * (t & 3);
-        x.w[t >> 2] = (x.w[t >> 2] & ~(0xffu << sh)) | v << sh;
-    } else {
-        // bytes (dh, half) of word c hold slots 2 c + 8 half, + 1
-        const uint32_t v = (pick(y, (from >> 1) & 3) >> (8 * (from >> 3) + 4 * (from & 1))) & 0x000f000fu;
-        const int sh = 8 * (t >> 3) + 4 * (t & 1);
-        x.w[(t >> 1) & 3] = (x.w[(t >> 1) & 3] & ~(0x000f000fu << sh)) | v << sh;
-    }
+__device__ __forceinline__ void put_slot(Mixed& x, int t, uint32_t v, bool moved) {
+    const int i = T == PA_FP8_E4M3 ? t >> 2 : (t >> 1) & 3, sh = T == PA_FP8_E4M3 ? 8 * (t & 3) : 8 * (t >> 3) + 4 * (t & 1);
+    const uint32_t m = (T == PA_FP8_E4M3 ? 0xffu : 0x000f000fu) << sh;
+    if (moved) x.w[i] = (x.w[i] & ~m) | v << sh;
 }
 
 template <pa_dtype T, int D>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const KParams p) {
+__global__ void __launch_bounds__(kCompactThreads, kSmCtas) compact_kernel(const KParams p) {
     using G = Tile<T, D>;
     __shared__ From from[kBatchRows];
-    __shared__ int32_t to[kBatchBlocks];
+    __shared__ int64_t to[kBatchBlocks];      // byte offsets of the destination's tiles, -1: none
     const int tid = threadIdx.x, s = blockIdx.z, h = blockIdx.y;
     int x = blockIdx.x;
     const int seg = x % p.segs;
     x /= p.segs;
-    const int slice = x % p.slices, which = x / p.slices;
+    const int slice = x & ((1 << p.slice_bits) - 1), which = x >> p.slice_bits;
     grid_dependency_wait();
     grid_launch_dependents();
     const bool report = blockIdx.x == 0 && h == 0 && tid == 0;
@@ -132,113 +113,113 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const KParams 
     const int first = start / kBlockTokens, nblk = (start + n - 1) / kBlockTokens - first + 1;
     const int each = (nblk + p.segs - 1) / p.segs;
     const int b0 = min(seg * each, nblk), b1 = min(b0 + each, nblk);
-    char* const pool = p.pool[which];
+    char* const pool = which ? p.v_pool : p.k_pool;
     const int32_t* strow = p.src_tables + (size_t)s * p.src_blocks;
     const int32_t* dtrow = p.dst_tables + (size_t)s * p.dst_blocks;
-    auto tile = [&](int32_t blk) { return pool + ((size_t)blk * p.Hkv + h) * G::BYTES; };
+    auto tile = [&](int32_t blk) { return ((int64_t)blk * p.Hkv + h) * (int64_t)G::BYTES; };
+    auto source = [&](From f) -> const char* { return pool + (f & ~(int64_t)(kBlockTokens - 1)); };
     const bool flags = h == 0 && which == 0 && slice == 0;
     for (int base = b0; base < b1; base += kBatchBlocks) {
         const int blocks = min(kBatchBlocks, b1 - base);
         __syncthreads();                       // (the last batch's reads of the places are done)
-        for (int i = tid; i < blocks; i += kCompactThreads) {
-            int32_t blk = __ldg(dtrow + first + base + i);
-            if (blk < 0 || blk >= p.num_blocks) {
-                if (flags) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
-                blk = -1;
-            }
-            to[i] = blk;
+        if (tid < blocks) {
+            const int32_t blk = __ldg(dtrow + first + base + tid);
+            const bool ok = blk >= 0 && blk < p.num_blocks;
+            if (!ok && flags) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+            to[tid] = ok ? tile(blk) : -1;
         }
         for (int i = tid; i < blocks * kBlockTokens; i += kCompactThreads) {
             const int pos = (first + base) * kBlockTokens + i, row = pos - start;
-            From f{-1, 0};
+            From f = -1;
             if (row >= 0 && row < n) {
                 const int src = __ldg(p.src_pos + q0 + row);
                 if (src < 0 || src >= src_cap || (p.in_place && src < pos)) {
                     if (flags) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
                 } else if (!(p.in_place && src == pos)) {
-                    f.blk = __ldg(strow + src / kBlockTokens);
-                    f.slot = src % kBlockTokens;
-                    if (f.blk < 0 || f.blk >= p.num_blocks) {
+                    const int32_t blk = __ldg(strow + src / kBlockTokens);
+                    if (blk < 0 || blk >= p.num_blocks) {
                         if (flags) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
-                        f.blk = -1;
+                    } else {
+                        f = tile(blk) | (src % kBlockTokens);
                     }
                 }
             }
             from[i] = f;
         }
         __syncthreads();
-        // (rows without a destination)
-        for (int i = tid; i < blocks * kBlockTokens; i += kCompactThreads)
-            if (to[i / kBlockTokens] < 0) from[i].blk = -1;
-        __syncthreads();
+        // (a row moves if it has both places)
+        auto moves = [&](int row) { return from[row] >= 0 && to[row / kBlockTokens] >= 0; };
         if (!G::VALUES_MIX || which == 0) {
             // pieces: lanes on a block's slots, then the slice's pieces, then blocks
-            const int per = G::PIECES / p.slices, c0 = slice * per;
-            const int units = blocks * per * kBlockTokens, chunk = kUnits * kCompactThreads;
-            auto place = [&](int i, int& row, int& c) {
-                const int y = i / kBlockTokens;
-                c = c0 + y % per;
-                row = y / per * kBlockTokens + i % kBlockTokens;
-            };
+            constexpr int PIECE_BITS = G::PIECES == 2 ? 1 : G::PIECES == 4 ? 2 : G::PIECES == 8 ? 3 : G::PIECES == 16 ? 4 : 5;
+            const int bits = PIECE_BITS - p.slice_bits, c0 = slice << bits;
+            const int units = blocks << (bits + 4), chunk = kUnits * kCompactThreads;
+            auto row_at = [&](int i) { return (i >> (bits + 4)) * kBlockTokens + i % kBlockTokens; };
+            auto piece_at = [&](int i) { return c0 + ((i >> 4) & ((1 << bits) - 1)); };
             auto load = [&](int at, uint4 (&v)[kUnits]) {
 #pragma unroll
                 for (int k = 0; k < kUnits; ++k) {
                     const int i = at + k * kCompactThreads + tid;
-                    if (i >= units) continue;
-                    int row, c;
-                    place(i, row, c);
-                    const From f = from[row];
-                    if (f.blk >= 0) v[k] = *reinterpret_cast<const uint4*>(tile(f.blk) + G::piece(c, f.slot));
+                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < units) {
+                        const From f = from[row_at(i)];
+                        if (f >= 0) v[k] = *reinterpret_cast<const uint4*>(source(f) + G::piece(piece_at(i), slot_of(f)));
+                    }
                 }
             };
             auto store = [&](int at, const uint4 (&v)[kUnits]) {
 #pragma unroll
                 for (int k = 0; k < kUnits; ++k) {
-                    const int i = at + k * kCompactThreads + tid;
-                    if (i >= units) continue;
-                    int row, c;
-                    place(i, row, c);
-                    if (from[row].blk >= 0)
-                        *reinterpret_cast<uint4*>(tile(to[row / kBlockTokens]) + G::piece(c, row % kBlockTokens)) = v[k];
+                    const int i = at + k * kCompactThreads + tid, row = row_at(i);
+                    if (i < units && moves(row))
+                        *reinterpret_cast<uint4*>(pool + to[row / kBlockTokens] + G::piece(piece_at(i), row % kBlockTokens)) = v[k];
                 }
             };
-            uint4 a[kUnits], b[kUnits];
-            load(0, a);
-            for (int at = 0; at < units; at += 2 * chunk) {
-                load(at + chunk, b);
-                __syncthreads();
-                store(at, a);
-                load(at + 2 * chunk, a);
-                __syncthreads();
-                store(at + chunk, b);
+            uint4 v[kDepth][kUnits];
+#pragma unroll
+            for (int d = 0; d + 1 < kDepth; ++d) load(d * chunk, v[d]);
+            for (int at = 0; at < units; at += kDepth * chunk) {
+#pragma unroll
+                for (int d = 0; d < kDepth; ++d) {
+                    // (chunks past the last: nothing is loaded or stored, the barrier is passed by all)
+                    load(at + (d + kDepth - 1) * chunk, v[(d + kDepth - 1) % kDepth]);
+                    if (p.in_place) __syncthreads();
+                    store(at + d * chunk, v[d]);
+                }
             }
         } else {
-            // units that hold all slots of a block: gathered slot by slot, from few blocks as a rule
-            const int per = G::MIXED / p.slices, u0 = slice * per, units = blocks * per;
+            // units that hold all slots of a block: gathered slot by slot, sixteen small loads under way
+            const int per = G::MIXED >> p.slice_bits, u0 = slice * per, units = blocks * per;
             for (int at = 0; at < units; at += kCompactThreads) {
-                const int i = at + tid, b = i / per, u = u0 + i % per;
+                const int i = at + tid, b = i < units ? i / per : 0, u = u0 + i % per;
+                const From* f = from + b * kBlockTokens;
                 Mixed got{};
                 uint32_t moved = 0u;
                 if (i < units && to[b] >= 0) {
-                    const From* f = from + b * kBlockTokens;
-#pragma unroll
-                    for (int t = 0; t < kBlockTokens; ++t) moved |= f[t].blk >= 0 ? 1u << t : 0u;
-                    if (moved != 0u && moved != 0xffffu) got = load_mixed<T, D>(tile(to[b]), u);
-                    Mixed was{};
-                    int32_t last = -1;
+                    uint32_t v[kBlockTokens];
 #pragma unroll
                     for (int t = 0; t < kBlockTokens; ++t) {
-                        const From y = f[t];
-                        if (y.blk < 0) continue;
-                        if (y.blk != last) {
-                            was = load_mixed<T, D>(tile(y.blk), u);
-                            last = y.blk;
+                        v[t] = 0u;
+                        if (f[t] >= 0) {
+                            v[t] = load_slot<T, D>(source(f[t]), u, slot_of(f[t]));
+                            moved |= 1u << t;
                         }
-                        put_slot<T>(got, t, was, y.slot);
                     }
+                    if (moved != 0u && moved != 0xffffu)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) got.w[w] = *reinterpret_cast<const uint32_t*>(pool + to[b] + mixed_at<T, D>(u, w));
+#pragma unroll
+                    for (int t = 0; t < kBlockTokens; ++t) put_slot<T>(got, t, v[t], (moved >> t) & 1u);
                 }
-                __syncthreads();
-                if (moved != 0u) store_mixed<T, D>(tile(to[b]), u, got);
+                if (p.in_place) __syncthreads();
+                if (moved != 0u) {
+                    char* dst = pool + to[b];
+                    if constexpr (T == PA_FP8_E4M3)
+                        *reinterpret_cast<uint4*>(dst + u * 16) = make_uint4(got.w[0], got.w[1], got.w[2], got.w[3]);
+                    else
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) *reinterpret_cast<uint32_t*>(dst + mixed_at<T, D>(u, w)) = got.w[w];
+                }
             }
         }
         if constexpr (G::SCALE > 0) {
@@ -247,16 +228,16 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const KParams 
 #pragma unroll
                 for (int k = 0; k < kBatchRows / kCompactThreads; ++k) {
                     const int i = k * kCompactThreads + tid;
-                    if (i >= blocks * kBlockTokens || from[i].blk < 0) continue;
-                    const char* at = tile(from[i].blk) + G::CODES + from[i].slot * G::SCALE;
+                    if (i >= blocks * kBlockTokens || from[i] < 0) continue;
+                    const char* at = source(from[i]) + G::CODES + slot_of(from[i]) * G::SCALE;
                     v[k] = G::SCALE == 4 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
                 }
                 __syncthreads();
 #pragma unroll
                 for (int k = 0; k < kBatchRows / kCompactThreads; ++k) {
                     const int i = k * kCompactThreads + tid;
-                    if (i >= blocks * kBlockTokens || from[i].blk < 0) continue;
-                    char* at = tile(to[i / kBlockTokens]) + G::CODES + i % kBlockTokens * G::SCALE;
+                    if (i >= blocks * kBlockTokens || !moves(i)) continue;
+                    char* at = pool + to[i / kBlockTokens] + G::CODES + i % kBlockTokens * G::SCALE;
                     if constexpr (G::SCALE == 4) *reinterpret_cast<uint32_t*>(at) = v[k];
                     else *reinterpret_cast<uint16_t*>(at) = (uint16_t)v[k];
                 }
@@ -273,16 +254,17 @@ cudaError_t launch(KParams p, int num_seqs, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // CTAs for the whole GPU: in place by shares of the tiles, else by shares of the rows
-    const long long pairs = 2ll * p.Hkv * num_seqs;
-    p.slices = p.segs = 1;
+    const long long pairs = 2ll * p.Hkv * num_seqs, room = (long long)kSmCtas * sms;
+    p.slice_bits = 0;
+    p.segs = 1;
     if (p.in_place) {
-        while (2 * p.slices <= std::min(G::PIECES, 8) && pairs * p.slices < 2ll * sms) p.slices *= 2;
+        while ((2 << p.slice_bits) <= std::min(G::PIECES, 8) && (pairs << p.slice_bits) * 2 <= room) ++p.slice_bits;
     } else {
         const long long blocks = (p.total / num_seqs + kBlockTokens - 1) / kBlockTokens;
-        p.segs = (int)std::max(1ll, std::min((blocks + 3) / 4, 8ll * sms / pairs));
+        p.segs = (int)std::max(1ll, std::min((blocks + 3) / 4, 4 * room / pairs));
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * p.slices * p.segs, p.Hkv, num_seqs);
+    cfg.gridDim = dim3((2 << p.slice_bits) * p.segs, p.Hkv, num_seqs);
     cfg.blockDim = dim3(kCompactThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -308,8 +290,8 @@ cudaError_t launch_type(const KParams& p, pa_dtype dtype, int num_seqs, cudaStre
 
 cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
     KParams p;
-    p.pool[0] = static_cast<char*>(a.k_pool);
-    p.pool[1] = static_cast<char*>(a.v_pool);
+    p.k_pool = static_cast<char*>(a.k_pool);
+    p.v_pool = static_cast<char*>(a.v_pool);
     p.src_tables = a.block_tables;
     p.dst_tables = a.dst_tables;
     p.src_pos = a.src_pos;

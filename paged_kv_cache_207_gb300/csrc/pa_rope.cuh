@@ -113,12 +113,16 @@ __device__ __forceinline__ float2 cos_sin(uint64_t phase) {
     return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b);
 }
 
-// The position that plane f of row `row` turns by where it has its own; false: the plane has no axis.
-__device__ __forceinline__ bool own_position(const RParams& p, int row, int f, int32_t& pos) {
+// The axis of plane f where rows have positions of their own, -1 (flagged by `report`): it has none.
+__device__ __forceinline__ int plane_axis(const RParams& p, int f, bool report) {
     const int axis = p.plane_axis ? __ldg(p.plane_axis + f) : 0;
     const bool ok = axis >= 0 && axis < p.axes;
-    pos = ok ? __ldg(p.positions + (size_t)axis * p.total + row) : 0;
-    return ok;
+    if (!ok && report) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+    return ok ? axis : -1;
+}
+// The position of row `row` on an axis; a plane without one does not turn.
+__device__ __forceinline__ int32_t own_position(const RParams& p, int row, int axis) {
+    return axis >= 0 ? __ldg(p.positions + (size_t)axis * p.total + row) : 0;
 }
 
 // Elements of one 16-byte piece of a row.
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rope_append_kernel(cons
     // (at most one plane a thread, whose position does not depend on the row's place either)
     static_assert(D / 2 <= kRowThreads, "a thread has one plane");
     int32_t own = 0;
-    if (AXES && tid < p.half && !own_position(p, row, tid, own)) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
+    if (AXES && tid < p.half) own = own_position(p, row, plane_axis(p, tid, true));
     if (row == 0) check_cu<kRowThreads>(p);
     int pos = 0;
     int32_t blk = 0;
@@ -603,12 +607,15 @@ __global__ void __launch_bounds__(tile_threads(T, D), 512 / tile_threads(T, D)) 
     constexpr int PAD = D / 2 + 2;                           // (rows on different banks)
     __shared__ __align__(16) float2 cs[kTileRows * PAD];
     __shared__ uint64_t turns[D / 2];
+    __shared__ int axis[AXES ? D / 2 : 1];
     __shared__ __align__(16) uint32_t sm_v[T == PA_FP8_E4M3 ? NW * (D / 4) * 16 : 1];
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_cu<NT>(p);
     if (tid < p.half) turns[tid] = fixed_turns(p.inv_freq[tid]);
+    if constexpr (AXES)
+        if (tid < p.half) axis[tid] = plane_axis(p, tid, blockIdx.y == 0);
     Tile tile;
     if (!find_tile<NT>(p, blockIdx.x, tile)) return;
     const int share = blockIdx.y * GROUPS, stride = gridDim.y * GROUPS;
@@ -641,9 +648,7 @@ __global__ void __launch_bounds__(tile_threads(T, D), 512 / tile_threads(T, D)) 
     for (int i = tid; i < rows * p.half; i += NT) {
         const int r = i / p.half, f = i - r * p.half;
         if constexpr (AXES) {
-            int32_t own;
-            if (!own_position(p, tile.row0 + r, f, own)) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
-            cs[(tile.lo + r) * PAD + f] = cos_sin(turns[f] * (uint64_t)(int64_t)own);
+            cs[(tile.lo + r) * PAD + f] = cos_sin(turns[f] * (uint64_t)(int64_t)own_position(p, tile.row0 + r, axis[f]));
         } else {
             cs[(tile.lo + r) * PAD + f] = cos_sin(turns[f] * (uint64_t)(tile.pos0 + tile.lo + r));
         }
