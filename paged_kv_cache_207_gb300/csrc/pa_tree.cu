@@ -19,6 +19,7 @@ namespace pa {
 namespace {
 
 constexpr int kRows = kTreeF32Rows, kKeys = 64, kThreads = 128, kMinTiles = 2;
+constexpr int f32_ctas(int D) { return D == 64 ? 3 : 2; }      // of an SM: what shared memory (91 KB at 128) and registers allow
 
 // Packed pairs of fp32: the first in the low 32 bits.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
@@ -52,7 +53,7 @@ struct F32Layout {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) {
+__global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const TParams p) {
     using L = F32Layout<D>;
     constexpr int ND = D / 64;                            // float4 of outputs per row and thread
     constexpr size_t TILE = kBlockTokens * D * 4;
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     grid_dependency_wait();
     grid_launch_dependents();
-    Cursor cur{};
+    Cursor<kKeys> cur{};
     const Line line = tree_locate<kThreads, kKeys, kMinTiles>(
         p, reinterpret_cast<long long*>(smem + L::SM), blockIdx.x == 0,
         [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
@@ -72,9 +73,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
     if (tid == 0) say_joint(p, line, cur, blockIdx.x, any);
     if (!any || tree_aborted(p.err)) return;
     long long left = line.begin(blockIdx.x + 1) - line.begin(blockIdx.x);
-    if (left <= kItemCost - cur.at) return;
+    if (left <= item_cost(kKeys) - cur.at) return;
     for (bool first_piece = true; left > 0; first_piece = false) {
-        const int j0 = Cursor::tile(cur.at), j1 = Cursor::tile((int)min((long long)cur.cost(), cur.at + left));
+        const int j0 = cur.tile(cur.at), j1 = cur.tile((int)min((long long)cur.cost(), cur.at + left));
         const int tokens = item_tokens(p, cur), rows = tokens * p.G;
         const int qrow = cur.q.q0 + cur.rt * p.TQ, end = cur.q.start + cur.q.n;
         const int32_t* trow = p.tables + (size_t)cur.s * p.max_blocks;
@@ -98,37 +99,37 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
 #pragma unroll
             for (int x = 0; x < 2 * ND; ++x) o[r][x] = 0ull;
         }
-        for (int j = j0; j < j1; ++j) {
-            const int tok0 = j * kKeys;
-            // thread t: slot t % 16 of blocks t / 16 % 4, pieces from t / 64 on; keys past the last
-            // and those of a bad block count as zeros, and no row sees them
-            const int slot = tid & 15, b = (tid >> 4) & 3;
-            int32_t blk = -1;
-            if (tok0 + b * kBlockTokens < end) {
-                blk = __ldg(trow + tok0 / kBlockTokens + b);
-                if (blk < 0 || blk >= p.num_blocks) {
-                    if (slot == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
-                    blk = -1;
-                }
-            }
-            const bool live = blk >= 0 && tok0 + b * kBlockTokens + slot < end;
-            const char* krec = p.k_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
-            const char* vrec = p.v_pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
-            __syncthreads();                              // (the last tile's reads are done)
-#pragma unroll 4
-            for (int d4 = tid >> 6; d4 < D / 4; d4 += 2) {
-                float* k = sK + (d4 * L::KS + b * 16 + slot) * 4;
-                float* v = sV + (d4 * L::KS + b * 16 + slot) * 4;
-                if (!live) {
-                    *reinterpret_cast<float4*>(k) = *reinterpret_cast<float4*>(v) = make_float4(0.f, 0.f, 0.f, 0.f);
-                } else {
-                    cp_async_16(smem_u32(k), krec + (d4 * kBlockTokens + slot) * 16);
-                    cp_async_16(smem_u32(v), vrec + (d4 * kBlockTokens + slot) * 16);
-                }
+        // Thread t copies slot t % 16 of blocks t / 16 % 4, pieces from t / 64 on; keys past the last and
+        // those of a bad block count as zeros, and no row sees them.  A tile's keys come under the products
+        // with the values of the tile before, its values under its scores.
+        const int slot = tid & 15, b = (tid >> 4) & 3;
+        auto block_of = [&](int j) -> int32_t {
+            const int tok = j * kKeys + b * kBlockTokens;
+            if (j >= j1 || tok >= end) return -1;
+            const int32_t blk = __ldg(trow + tok / kBlockTokens);
+            if (blk >= 0 && blk < p.num_blocks) return blk;
+            if (slot == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+            return -1;
+        };
+        auto copy = [&](int j, int32_t blk, const char* pool, float* to) {
+            const bool live = blk >= 0 && j * kKeys + b * kBlockTokens + slot < end;
+            const char* rec = pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
+#pragma unroll 8
+            for (int d4 = tid >> 6; d4 < D / 4 && j < j1; d4 += 2) {
+                float* at = to + (d4 * L::KS + b * 16 + slot) * 4;
+                if (live) cp_async_16(smem_u32(at), rec + (d4 * kBlockTokens + slot) * 16);
+                else *reinterpret_cast<float4*>(at) = make_float4(0.f, 0.f, 0.f, 0.f);
             }
             cp_async_commit();
-            cp_async_wait<0>();
-            __syncthreads();
+        };
+        int32_t blk = block_of(j0);
+        copy(j0, blk, p.k_pool, sK);
+        for (int j = j0; j < j1; ++j) {
+            const int tok0 = j * kKeys;
+            copy(j, blk, p.v_pool, sV);
+            blk = block_of(j + 1);
+            cp_async_wait<1>();
+            __syncthreads();                              // (the keys, and before the first tile the queries)
             // scores of rows 4 ty .. + 3 and keys tx + 16 i, in pairs of dims
             uint64_t s2[4][4] = {};
 #pragma unroll 4
@@ -146,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                         fma2(s2[r][i], q[r].b, k[i].b);
                     }
             }
+            __syncthreads();                              // (the keys are read)
+            copy(j + 1, blk, p.k_pool, sK);
             // hidden keys score -inf (a select: they may hold anything)
             float s[4][4], top[4];
 #pragma unroll
@@ -187,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
 #pragma unroll
                 for (int x = 0; x < 2 * ND; ++x) o[r][x] = mul2(o[r][x], a2);
             }
+            cp_async_wait<1>();
+            __syncthreads();                              // (the values)
             // values of the tree's tokens that are no finite numbers must not reach the rows that do
             // not see them (0 times an infinity): such a tile takes a select for each product
             bool odd = false;
@@ -213,14 +218,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                     }
                 }
             }
+            __syncthreads();                              // (the values and the probabilities are read)
         }
+        cp_async_wait<0>();
         // the lanes' shares of the sums as one
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int x = 1; x < 16; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
         const bool whole = j0 == 0 && j1 == cur.q.tiles;
-        const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1));
+        const size_t part = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 4 * ty + r;
@@ -233,16 +240,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(const TParams p) 
                 const int d = 4 * (tx + 16 * x);
                 float4 v = make_float4(pair_lo(o[r][2 * x]), pair_hi(o[r][2 * x]), pair_lo(o[r][2 * x + 1]), pair_hi(o[r][2 * x + 1]));
                 if (!whole) {
-                    reinterpret_cast<float4*>(p.part_o)[(slot * (D / 4) + d / 4) * p.slot_rows + row] = v;
+                    reinterpret_cast<float4*>(p.part_o)[(part * (D / 4) + d / 4) * p.slot_rows + row] = v;
                     continue;
                 }
                 v = inv != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
                 *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst + d) = v;
             }
-            if (!whole && tx == 0) p.part_ml[slot * p.slot_rows + row] = make_float2(m[r], l[r]);
+            if (!whole && tx == 0) p.part_ml[part * p.slot_rows + row] = make_float2(m[r], l[r]);
         }
         left -= cur.cost() - cur.at;
-        if (left <= kItemCost) break;             // (ends before an item's first tile)
+        if (left <= item_cost(kKeys)) break;             // (ends before an item's first tile)
         next_item<kKeys>(p, cur);
     }
 }
@@ -252,7 +259,7 @@ cudaError_t launch_f32(const TreeArgs& a, cudaStream_t stream) {
     constexpr int smem = F32Layout<D>::BYTES;
     cudaError_t e = cudaFuncSetAttribute(tree_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(2 * tree_sms(), kTreeF32Ctas);
+    const int ctas = std::min(f32_ctas(D) * tree_sms(), kTreeF32Ctas);
     const TParams p = tree_params(a, kRows, ctas);
     e = tree_launch(tree_f32_kernel<D>, dim3(ctas), kThreads, smem, stream, p);
     return e != cudaSuccess ? e : launch_merge<D, float>(p, stream);

@@ -2,7 +2,7 @@
 //
 // An item is (sequence, kv head, row tile): ROWS query rows at most of one kv head, whole tokens,
 // against all keys of the sequence, cut into key tiles.  The items, in the order of the sequences,
-// then heads, then row tiles, form one line, each kItemCost places (what its beginning and end cost,
+// then heads, then row tiles, form one line, each item_cost() places (what its beginning and end cost,
 // in tiles: 64 sequences of 400 to 7800 tokens, 32 / 8 heads, 32 nodes, 244 us without) and one for every
 // tile, and CTA c of C takes the places c T / C .. (c + 1) T / C - 1 of its T: contexts may be as uneven
 // as they like, every CTA has the same work, and no lengths are needed on the host.  A CTA's run of
@@ -23,7 +23,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kItemCost = 4;
+// (in tiles of 128 keys on the tensor cores, of 64 on the FMA units)
+constexpr int item_cost(int KT) { return KT == 128 ? 4 : 1; }
 
 constexpr float kTreeLog2e = 1.4426950408889634f;
 
@@ -89,12 +90,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TParams& p, int s) {
 }
 
 // A place in the line.
+template <int KT>
 struct Cursor {
+    static constexpr int COST = item_cost(KT);
     int s, h, rt, at;        // sequence, kv head, row tile, place of the item
     TreeSeq q;
-    __device__ __forceinline__ int cost() const { return q.tiles + kItemCost; }
+    __device__ __forceinline__ int cost() const { return q.tiles + COST; }
     // the first key tile from a place on
-    static __device__ __forceinline__ int tile(int at) { return max(at - kItemCost, 0); }
+    static __device__ __forceinline__ int tile(int at) { return max(at - COST, 0); }
 };
 
 // The line: its places, C, and the first place of CTA c.
@@ -120,7 +123,7 @@ struct Line {
 // The line, and the cursor of place `begin_of(line)` in it where there is one (begin >= 0 and below
 // the total), found by all NT threads.  `sm`: NT / 32 + 6 words of 64 bits.
 template <int NT, int KT, int MIN_TILES, typename Begin>
-__device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, bool report, Begin begin_of, Cursor& cur) {
+__device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, bool report, Begin begin_of, Cursor<KT>& cur) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (p.S + NT - 1) / NT, s0 = min(tid * each, p.S), s1 = min(s0 + each, p.S);
     long long mine = 0;
@@ -128,7 +131,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
     for (int s = s0; s < s1; ++s) {
         one = tree_seq<KT>(p, s);
         if (report && one.bad) raise_flag(p.err, one.bad);
-        mine += (long long)(one.tiles + kItemCost) * one.rts * p.Hkv;
+        mine += (long long)(one.tiles + item_cost(KT)) * one.rts * p.Hkv;
     }
     long long incl = mine;
 #pragma unroll
@@ -152,7 +155,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
         int s = s0;
         for (; each > 1; ++s) {
             one = tree_seq<KT>(p, s);
-            const long long len = (long long)(one.tiles + kItemCost) * one.rts * p.Hkv;
+            const long long len = (long long)(one.tiles + item_cost(KT)) * one.rts * p.Hkv;
             if (begin < at + len || s + 1 >= s1) break;
             at += len;
         }
@@ -183,7 +186,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
 
 // The item after the cursor's (there is one).
 template <int KT>
-__device__ __forceinline__ void next_item(const TParams& p, Cursor& c) {
+__device__ __forceinline__ void next_item(const TParams& p, Cursor<KT>& c) {
     c.at = 0;
     if (++c.rt < c.q.rts) return;
     c.rt = 0;
@@ -194,7 +197,8 @@ __device__ __forceinline__ void next_item(const TParams& p, Cursor& c) {
 }
 
 // The rows of an item: its tokens.
-__device__ __forceinline__ int item_tokens(const TParams& p, const Cursor& c) { return min(c.q.n - c.rt * p.TQ, p.TQ); }
+template <int KT>
+__device__ __forceinline__ int item_tokens(const TParams& p, const Cursor<KT>& c) { return min(c.q.n - c.rt * p.TQ, p.TQ); }
 
 // True when some CTA has already given up on a wait (nothing is written from then on).
 __device__ __forceinline__ bool tree_aborted(const int32_t* err) {
@@ -234,13 +238,14 @@ inline TParams tree_params(const TreeArgs& a, int rows, int ctas) {
 }
 
 // What CTA c says of the item that its begin cuts (one thread of it).
-__device__ __forceinline__ void say_joint(const TParams& p, const Line& line, const Cursor& cur, int c, bool any) {
+template <int KT>
+__device__ __forceinline__ void say_joint(const TParams& p, const Line& line, const Cursor<KT>& cur, int c, bool any) {
     Joint x{0, 0, 0, 0};
-    const int j = Cursor::tile(cur.at);
+    const int j = cur.tile(cur.at);
     if (any && j > 0) {
         const long long from = line.begin(c) - cur.at, to = from + cur.cost();
         // (the CTA before has tiles of the item, and is the first that has)
-        if (line.begin(c - 1) <= from + kItemCost) {
+        if (line.begin(c - 1) <= from + item_cost(KT)) {
             // the CTA of the item's last tile: where it would be with even shares, or beside that
             const uint32_t each = line.base > 0 && line.base < 1ll << 31 ? (uint32_t)line.base : line.base > 0 ? 1u << 31 : 1u;
             int last = (int)min((long long)line.ctas - 1, c + (long long)((uint32_t)(cur.cost() - cur.at) / each));

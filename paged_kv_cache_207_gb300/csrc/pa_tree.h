@@ -25,7 +25,7 @@ struct TreeArgs {
 // Work is handed out in key tiles, evenly over the CTAs (pa_tree.cuh), so that at most two items
 // of a CTA are incomplete: their partial results are what the workspace holds.
 constexpr int kTreeCtas = 160;               // CTAs at most of the tensor-core kernel, one per SM,
-constexpr int kTreeF32Ctas = 2 * kTreeCtas;  // and of the f32 kernel
+constexpr int kTreeF32Ctas = 3 * kTreeCtas;  // and of the f32 kernel
 constexpr int kTreeF32Rows = 32;             // query rows of an f32 item
 constexpr int kTreeJointBytes = 16;          // of what a CTA says of an item that it shares
 // Query rows of an item of the tensor-core kernel: one or two tiles of 128.

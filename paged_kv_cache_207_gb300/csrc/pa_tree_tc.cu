@@ -187,18 +187,18 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x, uint32_t exponent) {
 
 // A run of key tiles of one item, as every role walks them.
 struct Piece {
-    Cursor c;
+    Cursor<kKeys> c;
     int j0, j1;              // its key tiles
     int tokens, rows;        // of the row tile
     int qrow;                // row of q of its first token
     int end;                 // keys of the sequence
     int nblk;                // blocks of them
 };
-__device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor& c, long long left) {
+__device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor<kKeys>& c, long long left) {
     Piece x;
     x.c = c;
-    x.j0 = Cursor::tile(c.at);
-    x.j1 = Cursor::tile((int)min((long long)c.cost(), c.at + left));
+    x.j0 = c.tile(c.at);
+    x.j1 = c.tile((int)min((long long)c.cost(), c.at + left));
     x.tokens = item_tokens(p, c);
     x.rows = x.tokens * p.G;
     x.qrow = c.q.q0 + c.rt * p.TQ;
@@ -207,12 +207,12 @@ __device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor& c, lon
     return x;
 }
 struct Walk {
-    Cursor c;
+    Cursor<kKeys> c;
     long long left;          // places from the cursor on
     // To the next item with tiles for this CTA (a run that ends before an item's first tile has none).
     __device__ __forceinline__ void next(const TParams& p) {
         left -= c.cost() - c.at;
-        if (left > kItemCost) next_item<kKeys>(p, c);
+        if (left > item_cost(kKeys)) next_item<kKeys>(p, c);
         else left = 0;
     }
 };
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, walk.c);
         const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
         walk.left = any ? line.begin(blockIdx.x + 1) - line.begin(blockIdx.x) : 0;
-        if (walk.left <= kItemCost - walk.c.at) walk.left = 0;            // (ends before a first tile)
+        if (walk.left <= item_cost(kKeys) - walk.c.at) walk.left = 0;            // (ends before a first tile)
         // (said whether or not the call goes on, by the last thread, which has the least to do)
         if (threadIdx.x == W::THREADS - 1) say_joint(p, line, walk.c, blockIdx.x, any);
     }
