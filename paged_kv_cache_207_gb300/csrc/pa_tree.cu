@@ -18,8 +18,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kRows = kTreeF32Rows, kKeys = 64, kThreads = 128, kMinTiles = 2;
-constexpr int f32_ctas(int D) { return D == 64 ? 3 : 2; }      // of an SM: what shared memory (91 KB at 128) and registers allow
+constexpr int kRows = kTreeF32Rows, kThreads = 128, kWarps = kThreads / 32, kKeys = kWarps * kBlockTokens, kMinTiles = 2;
+constexpr int f32_ctas(int D) { return D == 64 ? 3 : 2; }      // of an SM: what registers (168) and shared memory (94 KB) allow
 
 // Packed pairs of fp32: the first in the low 32 bits.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
@@ -43,26 +43,244 @@ __device__ __forceinline__ Quad quad_at(const float* p) {
 
 template <int D>
 struct F32Layout {
-    static constexpr int KS = kKeys + 1;                  // 16-byte pieces from one d4 to the next
-    static constexpr int K = 0;                           // [D / 4][KS][4]
-    static constexpr int V = K + D / 4 * KS * 16;
-    static constexpr int Q = V + D / 4 * KS * 16;         // [D / 4][kRows + 1][4]
-    static constexpr int P = Q + D / 4 * (kRows + 1) * 16;   // [kKeys][kRows]
-    static constexpr int SM = P + kKeys * kRows * 4;
-    static constexpr int BYTES = SM + (kThreads / 32 + 6) * 8;
+    static constexpr int KS = kBlockTokens + 1;           // 16-byte pieces from one d4 to the next
+    static constexpr int HALF = D / 4 * KS * 16;          // a block's keys or values: [D / 4][KS][4]
+    static constexpr int OS = D / 4 + 1;                  // pieces from row to row of a warp's outputs (over its keys and values)
+    static_assert(kRows * OS * 16 <= 2 * HALF, "a warp's outputs, where its keys and values were");
+    static constexpr int KV = 0;                          // [warp][keys, values]
+    static constexpr int Q = KV + kWarps * 2 * HALF;      // [D / 4][kRows][4]
+    static constexpr int P = Q + D / 4 * kRows * 16;      // [warp][16 keys][8][4]: rows ty + 8 r
+    static constexpr int ML = P + kWarps * kBlockTokens * kRows * 4;   // [warp][kRows]
+    static constexpr int SM = ML + kWarps * kRows * 8;
+    static constexpr int BYTES = SM + (kWarps + 6) * 8;
 };
+
+// One piece: tiles j0 .. j1 - 1 of the cursor's item, by rows ty + 8 r, r < NR.
+template <int D, int NR>
+__device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kKeys>& cur, uint8_t* smem, int j0, int j1, bool first_piece) {
+    using L = F32Layout<D>;
+    constexpr int NX = D / 16;                            // float4 of outputs per row and thread
+    constexpr size_t TILE = kBlockTokens * D * 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = lane & 3, ty = lane >> 2;
+    float* const sK = reinterpret_cast<float*>(smem + L::KV + warp * 2 * L::HALF);
+    float* const sV = reinterpret_cast<float*>(smem + L::KV + warp * 2 * L::HALF + L::HALF);
+    float* const sQ = reinterpret_cast<float*>(smem + L::Q);
+    float* const sP = reinterpret_cast<float*>(smem + L::P) + warp * (kBlockTokens * kRows);
+    float2* const sML = reinterpret_cast<float2*>(smem + L::ML);
+    const int tokens = item_tokens(p, cur), rows = tokens * p.G;
+    const int qrow = cur.q.q0 + cur.rt * p.TQ, end = cur.q.start + cur.q.n;
+    const int32_t* trow = p.tables + (size_t)cur.s * p.max_blocks;
+    // the warp's block of tile j; -1: past the last key, or no block of the pool (flagged)
+    auto block_of = [&](int j) -> int32_t {
+        const int tok = j * kKeys + warp * kBlockTokens;
+        if (j >= j1 || tok >= end) return -1;
+        const int32_t blk = __ldg(trow + tok / kBlockTokens);
+        if (blk >= 0 && blk < p.num_blocks) return blk;
+        if (lane == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
+        return -1;
+    };
+    // keys past the last and those of a bad block count as zeros, and no row sees the former
+    auto copy = [&](int j, int32_t blk, const char* pool, float* to) {
+        const int slot = lane & 15, tok = j * kKeys + warp * kBlockTokens;
+        const bool live = blk >= 0 && tok + slot < end;
+        const char* rec = pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
+        if (j < j1 && tok < end) {
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u) {
+                const int d4 = 2 * u + (lane >> 4);
+                float* at = to + (d4 * L::KS + slot) * 4;
+                if (live) cp_async_16(smem_u32(at), rec + (d4 * kBlockTokens + slot) * 16);
+                else *reinterpret_cast<float4*>(at) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        cp_async_commit();
+    };
+    __syncthreads();                                      // (the piece before has read its outputs)
+    int32_t blk = block_of(j0);
+    copy(j0, blk, p.k_pool, sK);
+    // the query rows, zeros past the last
+    for (int i = tid; i < D / 4 * 8 * NR; i += kThreads) {
+        const int d4 = i % (D / 4), r = i / (D / 4), tok = r / p.G, g = r - tok * p.G;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            const size_t at = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D + 4 * d4;
+            v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
+        }
+        *reinterpret_cast<float4*>(sQ + (d4 * kRows + r) * 4) = v;
+    }
+    __syncthreads();
+    const int32_t* mrow[NR];                              // the rows' mask words; null: no row
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int row = ty + 8 * r;
+        mrow[r] = row < rows ? p.mask + (size_t)(qrow + row / p.G) * p.words : nullptr;
+    }
+    float m[NR], l[NR];
+    uint64_t o[NR][2 * NX];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2 * NX; ++x) o[r][x] = 0ull;
+    }
+    for (int j = j0; j < j1; ++j) {
+        const int tok0 = j * kKeys + warp * kBlockTokens, node0 = tok0 - cur.q.start, left = end - tok0;
+        if (left <= 0) break;                             // (the warp's blocks end)
+        copy(j, blk, p.v_pool, sV);
+        blk = block_of(j + 1);
+        // the keys that a row sees: 16 bits
+        uint32_t see[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            see[r] = 0xffffu;
+            if (node0 > -kBlockTokens) {
+                uint32_t v = 0u;
+                if (mrow[r]) {
+                    if (node0 < 0) {
+                        v = ~(0xffffffffu << -node0) | (uint32_t)__ldg(mrow[r]) << -node0;
+                    } else {
+                        const uint32_t lo = (uint32_t)__ldg(mrow[r] + node0 / 32);
+                        const uint32_t hi = (node0 & 31) > 16 && node0 / 32 + 1 < p.words ? (uint32_t)__ldg(mrow[r] + node0 / 32 + 1) : 0u;
+                        v = __funnelshift_r(lo, hi, node0 & 31);
+                    }
+                }
+                see[r] = left < kBlockTokens ? v & ~(0xffffffffu << left) : v;
+            }
+        }
+        cp_async_wait<1>();
+        __syncwarp();                                     // (the keys)
+        // scores of rows ty + 8 r and keys tx + 4 i, in pairs of dims
+        uint64_t s2[NR][4] = {};
+#pragma unroll 2
+        for (int d4 = 0; d4 < D / 4; ++d4) {
+            Quad q[NR], k[4];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) q[r] = quad_at(sQ + (d4 * kRows + ty + 8 * r) * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = quad_at(sK + (d4 * L::KS + tx + 4 * i) * 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    fma2(s2[r][i], q[r].a, k[i].a);
+                    fma2(s2[r][i], q[r].b, k[i].b);
+                }
+        }
+        __syncwarp();                                     // (the keys are read)
+        copy(j + 1, blk, p.k_pool, sK);
+        // hidden keys score -inf (a select: they may hold anything)
+        float s[4][4] = {};
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[r][i] = (see[r] >> (tx + 4 * i)) & 1u ? (pair_lo(s2[r][i]) + pair_hi(s2[r][i])) * p.scale_log2 : -INFINITY;
+                top = fmaxf(top, s[r][i]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float n = fmaxf(m[r], top), z = n == -INFINITY ? 0.f : n;
+            const float al = fast_exp2(m[r] - z);
+            m[r] = n;
+            l[r] *= al;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[r][i] = fast_exp2(s[r][i] - z);
+                l[r] += s[r][i];
+            }
+            if (al != 1.f) {
+                const uint64_t a2 = pair_of(al, al);
+#pragma unroll
+                for (int x = 0; x < 2 * NX; ++x) o[r][x] = mul2(o[r][x], a2);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(sP + ((tx + 4 * i) * 8 + ty) * 4) = make_float4(s[0][i], s[1][i], s[2][i], s[3][i]);
+        cp_async_wait<1>();
+        __syncwarp();                                     // (the values, and the probabilities)
+        // values of the tree's tokens that are no finite numbers must not reach the rows that do
+        // not see them (0 times an infinity): such a block takes a select for each product
+        bool odd = false;
+        if (node0 > -kBlockTokens) {
+            const int slot = lane & 15;
+            for (int u = 0; u < D / 8; ++u) {
+                const float4 v = *reinterpret_cast<const float4*>(sV + ((2 * u + (lane >> 4)) * L::KS + slot) * 4);
+                odd |= !(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX);
+            }
+            odd = __any_sync(0xffffffffu, odd && node0 + slot >= 0);
+        }
+#pragma unroll 2
+        for (int k = 0; k < kBlockTokens; ++k) {
+            const float4 pr = *reinterpret_cast<const float4*>(sP + (k * 8 + ty) * 4);
+            const float pv[4] = {pr.x, pr.y, pr.z, pr.w};
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                const Quad v = quad_at(sV + ((tx + 4 * x) * L::KS + k) * 4);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    if (odd && pv[r] == 0.f) continue;
+                    const uint64_t w = pair_of(pv[r], pv[r]);
+                    fma2(o[r][2 * x], w, v.a);
+                    fma2(o[r][2 * x + 1], w, v.b);
+                }
+            }
+        }
+        __syncwarp();                                     // (the values and the probabilities are read)
+    }
+    // the warps' rows as one
+    cp_async_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int row = ty + 8 * r;
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (tx == 0) sML[warp * kRows + row] = make_float2(m[r], l[r]);
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+            *reinterpret_cast<ulonglong2*>(sK + (row * L::OS + tx + 4 * x) * 4) = make_ulonglong2(o[r][2 * x], o[r][2 * x + 1]);
+    }
+    __syncthreads();
+    const bool whole = j0 == 0 && j1 == cur.q.tiles;
+    const size_t part = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1));
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int d4 = i % (D / 4), row = i / (D / 4), tok = row / p.G, g = row - tok * p.G;
+        float top = -INFINITY, sum = 0.f;
+        float2 ml[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            ml[w] = sML[w * kRows + row];
+            top = fmaxf(top, ml[w].x);
+        }
+        const float z = top == -INFINITY ? 0.f : top;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = fast_exp2(ml[w].x - z);
+            if (ml[w].x == -INFINITY && ml[w].y == ml[w].y) continue;      // (sees none of the warp's keys)
+            const float4 y = *reinterpret_cast<const float4*>(smem + L::KV + w * 2 * L::HALF + (row * L::OS + d4) * 16);
+            sum += ml[w].y * f;
+            v = make_float4(v.x + y.x * f, v.y + y.y * f, v.z + y.z * f, v.w + y.w * f);
+        }
+        if (!whole) {
+            reinterpret_cast<float4*>(p.part_o)[(part * (D / 4) + d4) * p.slot_rows + row] = v;
+            if (d4 == 0) p.part_ml[part * p.slot_rows + row] = make_float2(top, sum);
+            continue;
+        }
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        v = inv != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const size_t dst = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D + 4 * d4;
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst) = v;
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const TParams p) {
     using L = F32Layout<D>;
-    constexpr int ND = D / 64;                            // float4 of outputs per row and thread
-    constexpr size_t TILE = kBlockTokens * D * 4;
     extern __shared__ __align__(16) uint8_t smem[];
-    float* const sK = reinterpret_cast<float*>(smem + L::K);
-    float* const sV = reinterpret_cast<float*>(smem + L::V);
-    float* const sQ = reinterpret_cast<float*>(smem + L::Q);
-    float* const sP = reinterpret_cast<float*>(smem + L::P);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     grid_dependency_wait();
     grid_launch_dependents();
     Cursor<kKeys> cur{};
@@ -70,183 +288,17 @@ __global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const T
         p, reinterpret_cast<long long*>(smem + L::SM), blockIdx.x == 0,
         [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
     const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
-    if (tid == 0) say_joint(p, line, cur, blockIdx.x, any);
-    if (!any || tree_aborted(p.err)) return;
+    if (threadIdx.x == 0) say_joint(p, line, cur, blockIdx.x, any);
+    if (__syncthreads_or(!any || (threadIdx.x == 0 && tree_aborted(p.err)))) return;
     long long left = line.begin(blockIdx.x + 1) - line.begin(blockIdx.x);
     if (left <= item_cost(kKeys) - cur.at) return;
     for (bool first_piece = true; left > 0; first_piece = false) {
         const int j0 = cur.tile(cur.at), j1 = cur.tile((int)min((long long)cur.cost(), cur.at + left));
-        const int tokens = item_tokens(p, cur), rows = tokens * p.G;
-        const int qrow = cur.q.q0 + cur.rt * p.TQ, end = cur.q.start + cur.q.n;
-        const int32_t* trow = p.tables + (size_t)cur.s * p.max_blocks;
-        // the query rows, zeros past the last
-        __syncthreads();
-        for (int i = tid; i < D / 4 * kRows; i += kThreads) {
-            const int d4 = i % (D / 4), r = i / (D / 4), tok = r / p.G, g = r - tok * p.G;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows) {
-                const size_t at = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D + 4 * d4;
-                v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-            }
-            *reinterpret_cast<float4*>(sQ + (d4 * (kRows + 1) + r) * 4) = v;
-        }
-        float m[4], l[4];
-        uint64_t o[4][2 * ND];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-#pragma unroll
-            for (int x = 0; x < 2 * ND; ++x) o[r][x] = 0ull;
-        }
-        // Thread t copies slot t % 16 of blocks t / 16 % 4, pieces from t / 64 on; keys past the last and
-        // those of a bad block count as zeros, and no row sees them.  A tile's keys come under the products
-        // with the values of the tile before, its values under its scores.
-        const int slot = tid & 15, b = (tid >> 4) & 3;
-        auto block_of = [&](int j) -> int32_t {
-            const int tok = j * kKeys + b * kBlockTokens;
-            if (j >= j1 || tok >= end) return -1;
-            const int32_t blk = __ldg(trow + tok / kBlockTokens);
-            if (blk >= 0 && blk < p.num_blocks) return blk;
-            if (slot == 0) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
-            return -1;
-        };
-        auto copy = [&](int j, int32_t blk, const char* pool, float* to) {
-            const bool live = blk >= 0 && j * kKeys + b * kBlockTokens + slot < end;
-            const char* rec = pool + ((size_t)(live ? blk : 0) * p.Hkv + cur.h) * TILE;
-#pragma unroll 8
-            for (int d4 = tid >> 6; d4 < D / 4 && j < j1; d4 += 2) {
-                float* at = to + (d4 * L::KS + b * 16 + slot) * 4;
-                if (live) cp_async_16(smem_u32(at), rec + (d4 * kBlockTokens + slot) * 16);
-                else *reinterpret_cast<float4*>(at) = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            cp_async_commit();
-        };
-        int32_t blk = block_of(j0);
-        copy(j0, blk, p.k_pool, sK);
-        for (int j = j0; j < j1; ++j) {
-            const int tok0 = j * kKeys;
-            copy(j, blk, p.v_pool, sV);
-            blk = block_of(j + 1);
-            cp_async_wait<1>();
-            __syncthreads();                              // (the keys, and before the first tile the queries)
-            // scores of rows 4 ty .. + 3 and keys tx + 16 i, in pairs of dims
-            uint64_t s2[4][4] = {};
-#pragma unroll 4
-            for (int d4 = 0; d4 < D / 4; ++d4) {
-                Quad q[4], k[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) q[r] = quad_at(sQ + (d4 * (kRows + 1) + 4 * ty + r) * 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) k[i] = quad_at(sK + (d4 * L::KS + tx + 16 * i) * 4);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        fma2(s2[r][i], q[r].a, k[i].a);
-                        fma2(s2[r][i], q[r].b, k[i].b);
-                    }
-            }
-            __syncthreads();                              // (the keys are read)
-            copy(j + 1, blk, p.k_pool, sK);
-            // hidden keys score -inf (a select: they may hold anything)
-            float s[4][4], top[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                top[r] = -INFINITY;
-                const int row = 4 * ty + r;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = tok0 + tx + 16 * i;
-                    bool see = key < end;
-                    if (key >= cur.q.start && see)
-                        see = row < rows && ((uint32_t)__ldg(p.mask + (size_t)(qrow + row / p.G) * p.words + (key - cur.q.start) / 32) >>
-                                             ((key - cur.q.start) & 31)) & 1u;
-                    s[r][i] = see ? (pair_lo(s2[r][i]) + pair_hi(s2[r][i])) * p.scale_log2 : -INFINITY;
-                    top[r] = fmaxf(top[r], s[r][i]);
-                }
-            }
-            float al[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                for (int x = 1; x < 16; x <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], x));
-                const float n = fmaxf(m[r], top[r]), z = n == -INFINITY ? 0.f : n;
-                al[r] = fast_exp2(m[r] - z);
-                m[r] = n;
-                l[r] *= al[r];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[r][i] = fast_exp2(s[r][i] - z);
-                    l[r] += s[r][i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(sP + (tx + 16 * i) * kRows + 4 * ty) = make_float4(s[0][i], s[1][i], s[2][i], s[3][i]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint64_t a2 = pair_of(al[r], al[r]);
-#pragma unroll
-                for (int x = 0; x < 2 * ND; ++x) o[r][x] = mul2(o[r][x], a2);
-            }
-            cp_async_wait<1>();
-            __syncthreads();                              // (the values)
-            // values of the tree's tokens that are no finite numbers must not reach the rows that do
-            // not see them (0 times an infinity): such a tile takes a select for each product
-            bool odd = false;
-            if (tok0 + kKeys > cur.q.start)
-                for (int i = tid; i < D / 4 * kKeys; i += kThreads) {
-                    const int key = tok0 + i % kKeys;
-                    const float4 v = *reinterpret_cast<const float4*>(sV + (i / kKeys * L::KS + i % kKeys) * 4);
-                    odd |= key >= cur.q.start && !(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX);
-                }
-            odd = __syncthreads_or(odd);                  // (the probabilities are in place)
-#pragma unroll 2
-            for (int k = 0; k < kKeys; ++k) {
-                const float4 pr = *reinterpret_cast<const float4*>(sP + k * kRows + 4 * ty);
-                const float pv[4] = {pr.x, pr.y, pr.z, pr.w};
-#pragma unroll
-                for (int x = 0; x < ND; ++x) {
-                    const Quad v = quad_at(sV + ((tx + 16 * x) * L::KS + k) * 4);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (odd && pv[r] == 0.f) continue;
-                        const uint64_t w = pair_of(pv[r], pv[r]);
-                        fma2(o[r][2 * x], w, v.a);
-                        fma2(o[r][2 * x + 1], w, v.b);
-                    }
-                }
-            }
-            __syncthreads();                              // (the values and the probabilities are read)
-        }
-        cp_async_wait<0>();
-        // the lanes' shares of the sums as one
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int x = 1; x < 16; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
-        const bool whole = j0 == 0 && j1 == cur.q.tiles;
-        const size_t part = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 4 * ty + r;
-            if (row >= rows) continue;
-            const int tok = row / p.G, g = row - tok * p.G;
-            const size_t dst = ((size_t)(qrow + tok) * p.Hq + (size_t)cur.h * p.G + g) * D;
-            const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
-#pragma unroll
-            for (int x = 0; x < ND; ++x) {
-                const int d = 4 * (tx + 16 * x);
-                float4 v = make_float4(pair_lo(o[r][2 * x]), pair_hi(o[r][2 * x]), pair_lo(o[r][2 * x + 1]), pair_hi(o[r][2 * x + 1]));
-                if (!whole) {
-                    reinterpret_cast<float4*>(p.part_o)[(part * (D / 4) + d / 4) * p.slot_rows + row] = v;
-                    continue;
-                }
-                v = inv != 0.f ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst + d) = v;
-            }
-            if (!whole && tx == 0) p.part_ml[part * p.slot_rows + row] = make_float2(m[r], l[r]);
+        switch ((item_tokens(p, cur) * p.G + 7) / 8) {
+            case 1: tree_f32_piece<D, 1>(p, cur, smem, j0, j1, first_piece); break;
+            case 2: tree_f32_piece<D, 2>(p, cur, smem, j0, j1, first_piece); break;
+            case 3: tree_f32_piece<D, 3>(p, cur, smem, j0, j1, first_piece); break;
+            default: tree_f32_piece<D, 4>(p, cur, smem, j0, j1, first_piece); break;
         }
         left -= cur.cost() - cur.at;
         if (left <= item_cost(kKeys)) break;             // (ends before an item's first tile)
