@@ -55,11 +55,11 @@ constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at 
 // pieces of 32 columns, from the TMEM once for the maximum and again for the probabilities.
 template <pa_dtype T, int SW>
 struct Roles {
-    static constexpr bool RAW = T != PA_BF16;
     static constexpr int SOFT = 8 * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
-    static constexpr int FEEDS = RAW ? 2 * kKeyBlocks : SW == 1 ? 4 : 2;
-    static constexpr int LEAD = FEED + FEEDS;          // (FP8, FP4) two warps that the conversions wait for
-    static constexpr int OTHERS = (2 + FEEDS + (RAW ? 2 : 0) + 3) / 4 * 4;
+    static constexpr int FEEDS = T == PA_FP4_E2M1 ? 2 * kKeyBlocks : T == PA_FP8_E4M3 ? kKeyBlocks : SW == 1 ? 4 : 2;
+    static constexpr int LEAD = FEED + FEEDS;          // (FP8, FP4) warps that the conversions wait for
+    static constexpr int LEADS = T == PA_FP4_E2M1 ? 2 : T == PA_FP8_E4M3 ? 1 : 0;
+    static constexpr int OTHERS = (2 + FEEDS + LEADS + 3) / 4 * 4;
     static constexpr int THREADS = (SOFT + OTHERS) * 32;
 };
 
@@ -68,16 +68,18 @@ struct Layout {
     static constexpr int TILE = kBlockTokens * D * 2;                  // a block's K or V as an operand
     static constexpr int KTILE = kKeyBlocks * TILE;
     static constexpr int QTILE = kTileRows * D * 2;                    // [D/8][16][8 rows][16 B]
-    static constexpr bool RAW = T != PA_BF16;
+    static constexpr bool RAW = T != PA_BF16;                          // values are converted
+    static constexpr bool NAT = T == PA_FP8_E4M3;                      // keys are operands as they are
     static constexpr int REC = T == PA_BF16 ? TILE : T == PA_FP8_E4M3 ? 16 * D + 64 : 8 * D + D / 2;
-    static constexpr int KST = RAW ? 2 : 3, VST = RAW ? 2 : (SW == 1 || D == 64) ? 3 : 2;
-    // stages of records, of K and V in turn: as many as find room, six at most
+    static constexpr int KST = NAT ? 4 : RAW ? 2 : 3, VST = RAW ? 2 : (SW == 1 || D == 64) ? 3 : 2;
+    // stages of records (FP8: V's; FP4: K's and V's in turn): as many as find room, six at most
     static constexpr int HALF = kKeyBlocks * REC;
-    static constexpr int RST = !RAW ? 0 : T == PA_FP8_E4M3 && D == 128 ? 5 : 6;
+    static constexpr int KSTAGE = NAT ? HALF : KTILE;
+    static constexpr int RST = !RAW ? 0 : NAT && D == 128 ? 5 : 6;
     // query rows: in the TMEM with one row tile, else in shared memory
     static constexpr int Q = 0;
     static constexpr int K = Q + (SW == 2 ? SW * QTILE : 0);
-    static constexpr int V = K + KST * KTILE;
+    static constexpr int V = K + KST * KSTAGE;
     static constexpr int R = V + VST * KTILE;
     static constexpr int BAR = R + RST * HALF;
     static constexpr int NBAR = 44;
@@ -85,8 +87,10 @@ struct Layout {
     static constexpr int SLOT = BAR + NBAR * 8;       // TMEM address
     static constexpr int ODD = SLOT + 16;             // [2] of a piece: values that are no finite numbers
     static constexpr int EXPS = ODD + 16;             // [8] (K, V) exponents of a tile, as the conversions leave them
-    static constexpr int PASSED = EXPS + 64;          // [8] as the MMA warp passes them on
-    static constexpr int SEEN = PASSED + 64;          // [8][8] a tile's block has such values
+    // as the MMA warp passes them on: FP4: [8]; FP8: [S tile][the columns' scales, V's exponent]
+    static constexpr int PASS = kKeys * 4 + 16;
+    static constexpr int PASSED = EXPS + 64;
+    static constexpr int SEEN = PASSED + (NAT ? 2 * PASS : 64);      // [8][8] a tile's block has such values
     static constexpr int TABLE = SEEN + 80;           // [8] FP4: a block's scales of values
     static constexpr int GONE = TABLE - 8;            // [2] the conversions' lead gave up, K's and V's
     static constexpr int ROWS = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);   // [row tile][2][128] maxima, sums
@@ -272,30 +276,6 @@ struct Convert<D, PA_FP8_E4M3> {
         };
         return (int)__reduce_max_sync(0xffffffffu, max(max(e(x.x, 0), e(x.y, 1)), max(e(x.z, 2), e(x.w, 3))));
     }
-    static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int ek, int lane) {
-        const int slot = lane & 15;
-        const float f = exp2i(127 - ek);
-        const float s = __uint_as_float(ld_shared_u32(raw + 16 * D + 4 * slot)) * f;
-        const uint32_t h = pack_f16x2(s, s);
-        // (the loads first: the stores keep their order to later loads)
-        uint4 c[D / 32];
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) c[k] = ld_shared_v4(raw + ((2 * k + (lane >> 4)) * kBlockTokens + slot) * 16);
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-            const int d16 = 2 * k + (lane >> 4);
-            const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[2 * i] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[i] & 0xffffu)), h);
-                o[2 * i + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[i] >> 16)), h);
-            }
-            const uint32_t to = dst + 2 * d16 * (kKeyBlocks * 256) + slot * 16;
-            st_shared_v4(to, make_uint4(o[0], o[1], o[2], o[3]));
-            st_shared_v4(to + kKeyBlocks * 256, make_uint4(o[4], o[5], o[6], o[7]));
-        }
-    }
     static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, uint32_t, int rv, int lane, uint32_t live, uint32_t own) {
         const float f = exp2i(127 - rv);
         uint4 code[D / 32];
@@ -329,7 +309,7 @@ struct Convert<D, PA_FP8_E4M3> {
                 }
             }
             st_shared_v4(dst + d * 16, make_uint4(o[0], o[1], o[2], o[3]));
-            st_shared_v4(dst + D * 16 + d * 16, make_uint4(o[4], o[5], o[6], o[7]));
+            st_shared_v4(dst + kKeyBlocks * (D * 16) + d * 16, make_uint4(o[4], o[5], o[6], o[7]));
         }
         return odd;
     }
@@ -454,6 +434,34 @@ __device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
         : "memory");
     return r != 0u;
 }
+// The same of E4M3 operands, 32 of K at a time.
+__device__ __forceinline__ void umma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(id), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// 8 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // 16 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -487,8 +495,8 @@ template <int D, pa_dtype T, int SW>
 __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const TParams p) {
     using L = Layout<D, T, SW>;
     using W = Roles<T, SW>;
-    constexpr bool RAW = L::RAW;
-    constexpr int TILE = L::TILE, KTILE = L::KTILE, KST = L::KST, VST = L::VST, REC = L::REC;
+    constexpr bool RAW = L::RAW, NAT = L::NAT;
+    constexpr int TILE = L::TILE, KTILE = L::KTILE, KSTAGE = L::KSTAGE, KST = L::KST, VST = L::VST, REC = L::REC;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 0; i < KST; ++i) {
-            mbar_init(bar(kKFull + i), RAW ? kKeyBlocks : W::FEEDS);
+            mbar_init(bar(kKFull + i), NAT ? 1 : RAW ? kKeyBlocks : W::FEEDS);
             mbar_init(bar(kKEmpty + i), 1);
         }
 #pragma unroll
@@ -547,12 +555,13 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     if (warp >= W::SOFT) {
     if (warp == W::COPY) {
         // ------------------------------------------------------------ bulk copies
-        // bf16: V tiles, lane b block b.  Else the records, K's and V's of a tile one after the other.
+        // Lane b block b.  bf16: V tiles; FP8: K tiles and V's records; FP4: the records, K's and V's of
+        // a tile one after the other.
         const uint64_t pol = l2_policy_evict_first();
         constexpr int ST = RAW ? L::RST : VST, PER = RAW ? 2 : 1;
         const int full0 = RAW ? kRFull : kVFull, empty0 = RAW ? kREmpty : kVEmpty;
         bool ok = true;
-        int u = 0;                                    // stages filled so far
+        int u = 0, uk = 0;                            // stages filled so far (K's own: FP8)
         while (ok && walk.left > 0) {
             const Piece x = piece_at(p, walk.c, walk.left);
             Table table(p, x, lane);
@@ -561,30 +570,36 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 const bool mine = blk >= 0 && lane < kKeyBlocks;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * REC;
 #pragma unroll
-                for (int k = 0; k < PER; ++k, ++u) {
-                    const int st = u % ST;
-                    if (u >= ST) {
-                        ok = warp_wait(bar(empty0 + st), (u / ST - 1) & 1);
+                for (int k = 0; k < PER; ++k) {
+                    const bool to_k = NAT && k == 0;
+                    int& at = to_k ? uk : u;
+                    const int ring = to_k ? KST : ST, st = at % ring;
+                    const uint32_t full = bar((to_k ? kKFull : full0) + st);
+                    if (at >= ring) {
+                        ok = warp_wait(bar((to_k ? kKEmpty : empty0) + st), (at / ring - 1) & 1);
                         if (!ok) break;
                     }
                     if (lane == 0) {
                         fence_proxy_async_smem();
-                        mbar_arrive_expect_tx(bar(full0 + st), bytes);
+                        mbar_arrive_expect_tx(full, bytes);
                     }
                     __syncwarp();
                     if (mine) {
                         const char* pool = RAW && k == 0 ? p.k_pool : p.v_pool;
-                        const uint32_t dst = RAW ? L::R + st * L::HALF + lane * REC : L::V + st * KTILE + lane * TILE;
-                        bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC, REC, bar(full0 + st), pol);
+                        const uint32_t dst = to_k ? L::K + st * KSTAGE + lane * REC : RAW ? L::R + st * L::HALF + lane * REC : L::V + st * KTILE + lane * TILE;
+                        bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC, REC, full, pol);
                     }
+                    ++at;
                 }
             }
             walk.next(p);
         }
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // before the CTA ends, every copy has landed
-        if (lane == 0)
+        if (lane == 0) {
             for (int f = max(0, u - ST); f < u; ++f) mbar_wait_bounded(bar(full0 + f % ST), (f / ST) & 1, kWaitNs);
+            for (int f = max(0, uk - KST); f < uk; ++f) mbar_wait_bounded(bar(kKFull + f % KST), (f / KST) & 1, kWaitNs);
+        }
     } else if (warp == W::MMA) {
         // ------------------------------------------------------------ MMA issue
         // MMAs execute in issue order, so S(t + 2) (or S_h(t + 1) with two row tiles) overwrites
@@ -594,7 +609,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         named_bar_sync(2, 32 * (W::SOFT + 1));
         tc_fence_after();
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::SLOT);
-        constexpr uint32_t idS = idesc(RAW, kKeys, 0), idO = idesc(RAW, D, RAW ? 0 : 1);
+        constexpr uint32_t idS = idesc(RAW, NAT ? kKeys / 2 : kKeys, 0), idO = idesc(RAW, D, RAW ? 0 : 1);
         bool ok = true;
         int t0 = 0;
         for (int ic = 0; ok && walk.left > 0; ++ic) {
@@ -606,21 +621,43 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t qd = umma_desc(sbase + L::Q + hh * L::QTILE, 2048, 128);
-                    const uint64_t kd = umma_desc(sbase + L::K + (t % KST) * KTILE, kKeyBlocks * 256, 128);
                     const uint32_t dcol = tmem + kColS + (uint32_t)(buf * kKeys), qcol = tmem + kColQ + (uint32_t)((ic & 1) * (D / 2));
+                    if constexpr (NAT) {
+                        // eight slots of a block are eight rows of the operand, 16 dims each: the blocks' first
+                        // eight, a record apart, are one operand of 64 rows, their last eight another
+                        const uint64_t kd = umma_desc(sbase + L::K + (t % KST) * KSTAGE, 256, REC);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t kk = kd + (uint64_t)((ks * 2 * kKeyBlocks * 256) >> 4);
-                        if (SW == 1) umma_ts(dcol, qcol + 8 * ks, kk, idS, ks > 0);
-                        else umma_ss(dcol, qd + (uint64_t)(ks * 256), kk, idS, ks > 0);
+                        for (int m = 0; m < D / 8; ++m) {              // [slots' half][part of q][32 dims]
+                            const int hf = m / (D / 16), a = m % (D / 16), ks = a % (D / 32);
+                            umma_ts_f8(dcol + 64 * hf, qcol + 8 * a, kd + (uint64_t)((hf * 128 + ks * 512) >> 4), idS, a > 0);
+                        }
+                    } else {
+                        const uint64_t kd = umma_desc(sbase + L::K + (t % KST) * KSTAGE, kKeyBlocks * 256, 128);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint64_t kk = kd + (uint64_t)((ks * 2 * kKeyBlocks * 256) >> 4);
+                            if (SW == 1) umma_ts(dcol, qcol + 8 * ks, kk, idS, ks > 0);
+                            else umma_ss(dcol, qd + (uint64_t)(ks * 256), kk, idS, ks > 0);
+                        }
                     }
                     umma_commit(bar(kSFull + buf));
-                    if constexpr (RAW) {
+                    if constexpr (RAW && !NAT) {
                         st_shared_v2(sbase + L::PASSED + 8 * (t & 7), ld_shared_v2(sbase + L::EXPS + 8 * (t & 7)));
                         mbar_arrive(bar(kSFull + buf));
                     }
                 }
                 __syncwarp();
+                if constexpr (NAT) {
+                    // the columns' scales in their order: a lane has four slots of a block
+                    const uint32_t to = sbase + L::PASSED + buf * L::PASS;
+                    const uint4 sk = ld_shared_v4(sbase + L::K + (t % KST) * KSTAGE + (lane >> 2) * REC + 16 * D + (lane & 3) * 16);
+                    st_shared_v4(to + ((lane >> 1) & 1) * 256 + (lane >> 2) * 32 + (lane & 1) * 16, sk);
+                    ok = warp_wait(bar(kEFull + (t & 3)), (t >> 2) & 1);
+                    if (lane == 0) st_shared_v2(to + kKeys * 4, ld_shared_v2(sbase + L::EXPS + 8 * (t & 7)));
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive(bar(kSFull + buf));
+                    __syncwarp();
+                }
             };
             auto k_ready = [&](int i) { ok = warp_wait(bar(kKFull + (t0 + i) % KST), ((t0 + i) / KST) & 1); };
             auto k_free = [&](int i) {
@@ -682,7 +719,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t pcol = tmem + kColS + (uint32_t)(buf * kKeys), ocol = tmem + kColO + (uint32_t)(hh * kKeys);
-                    // bf16: a block as stored, [D/8][16 slots][8 dims]; else [2 groups][D/8][8 dims][8 tokens]
+                    // bf16: a block as stored, [D/8][16 slots][8 dims]; else [2 groups][D/8][8 dims][8 tokens], FP8's
+                    // groups the blocks' first eight slots, then their last eight, as the columns of S are
                     const uint64_t vd = RAW ? umma_desc(sbase + L::V + st * KTILE, D * 16, 128)
                                             : umma_desc(sbase + L::V + st * KTILE, 128, 256);
                     const uint32_t more = i > 0 ? 1u : 0u;
@@ -691,8 +729,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         for (int b = 0; b < kKeyBlocks; ++b)
                             umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
                     } else {
-                        for (int b = 0; b < nb; ++b)
-                            umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                        for (int b = 0; b < kKeyBlocks; ++b)
+                            if ((NAT ? 2 * (b % 4) : b) < nb) umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
                     }
                     if (hh == SW - 1) umma_commit(bar(kVEmpty + st));
                     if (SW == 1) umma_commit(bar(kPVDone));
@@ -752,7 +790,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (elect_one()) umma_commit(bar(kDone));
         __syncwarp();
         mbar_wait_bounded(bar(kDone), 0, kWaitNs);
-    } else if (RAW && warp >= W::LEAD) {
+    } else if (RAW && warp >= W::LEAD && warp < W::LEAD + W::LEADS) {
         // ------------------------------------------------------------ the conversions' lead
         // One warp for the keys, one for the values waits for a tile's records and for its place and lets
         // eight warps go at a named barrier, so that they do not poll (28 polling warps took half of
@@ -760,31 +798,37 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         // piece's first, raised where a tile's scales pass it by 2^6.
         if constexpr (RAW) {
             using C = Convert<D, T>;
-            const bool for_v = warp > W::LEAD;
+            const bool for_v = NAT || warp > W::LEAD;
             bool ok = true;
             int t = 0;
             while (ok && walk.left > 0) {
                 const Piece x = piece_at(p, walk.c, walk.left);
                 int rv = 0;
                 for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
-                    const int uk = 2 * t, uv = 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST;
-                    if (!for_v) {
-                        const int keys = x.end - (x.j0 + i) * kKeys;
-                        ok = warp_wait(bar(kRFull + rk), (uk / L::RST) & 1);
-                        const int ek = C::exponent(sbase + L::R + rk * L::HALF, REC, keys, lane);
+                    const int uk = 2 * t, uv = NAT ? t : 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST;
+                    const int keys = x.end - (x.j0 + i) * kKeys;
+                    if (NAT || !for_v) {
+                        int ek = 0;
+                        if (!NAT) {
+                            ok = warp_wait(bar(kRFull + rk), (uk / L::RST) & 1);
+                            ek = C::exponent(sbase + L::R + rk * L::HALF, REC, keys, lane);
+                        }
                         ok = ok && warp_wait(bar(kRFull + rs), (uv / L::RST) & 1);
                         const int ev = C::exponent(sbase + L::R + rs * L::HALF, REC, keys, lane);
                         if (i == 0 || ev > rv + 6) rv = ev;
                         if (lane == 0) {
                             st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
                             mbar_arrive(bar(kEFull + (t & 3)));
-                            mbar_arrive(bar(kREmpty + rk));
+                            if (!NAT) mbar_arrive(bar(kREmpty + rk));
                             mbar_arrive(bar(kREmpty + rs));
                         }
-                        if (t >= KST) ok = ok && warp_wait(bar(kKEmpty + t % KST), (t / KST - 1) & 1);
                     } else {
                         ok = warp_wait(bar(kEFull + (t & 3)), (t >> 2) & 1);
+                    }
+                    if (for_v) {
                         if (t >= VST) ok = ok && warp_wait(bar(kVEmpty + t % VST), (t / VST - 1) & 1);
+                    } else {
+                        if (t >= KST) ok = ok && warp_wait(bar(kKEmpty + t % KST), (t / KST - 1) & 1);
                     }
                     if (!ok && lane == 0) *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * for_v) = 1u;
                     __syncwarp();
@@ -804,7 +848,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             // for the values of the one before)
             using C = Convert<D, T>;
             const int b = f % kKeyBlocks;
-            const bool for_v = f >= kKeyBlocks;
+            const bool for_v = NAT || f >= kKeyBlocks;
             const uint32_t smem_r = sbase + L::R;
             bool ok = true;
             int t = 0;
@@ -812,27 +856,28 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 const Piece x = piece_at(p, walk.c, walk.left);
                 for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
                     // (stages of K and V in turn)
-                    const int uk = 2 * t, uv = 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST, st = for_v ? t % VST : t % KST;
-                    const uint32_t kraw = smem_r + rk * L::HALF, vraw = smem_r + rs * L::HALF;
+                    const int uk = 2 * t, uv = NAT ? t : 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST, st = for_v ? t % VST : t % KST;
+                    const uint32_t vraw = smem_r + rs * L::HALF;
                     const int tok0 = (x.j0 + i) * kKeys, first = tok0 + b * kBlockTokens;
                     named_bar_sync(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
                     ok = *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * for_v) == 0u;
                     if (!ok) break;
                     mbar_test(bar(kRFull + (for_v ? rs : rk)), ((for_v ? uv : uk) / L::RST) & 1);     // (the copies are seen)
                     const uint2 e = ld_shared_v2(sbase + L::EXPS + 8 * (t & 7));
-                    const int ek = (int)e.x, rv = (int)e.y;
+                    const int rv = (int)e.y;
                     if (for_v) {
                         bool odd = false;
-                        if (first < x.end) {
-                            const int keys = min(x.end - first, kBlockTokens), ctx = min(max(x.c.q.start - first, 0), kBlockTokens);
+                        // (FP8: an odd last block has the next one's zeros beside it)
+                        if (first < x.end || (NAT && (b & 1) && first - kBlockTokens < x.end)) {
+                            const int keys = min(max(x.end - first, 0), kBlockTokens), ctx = min(max(x.c.q.start - first, 0), kBlockTokens);
                             const uint32_t live = (1u << keys) - 1u, own = live & ~((1u << ctx) - 1u);
-                            odd = C::values(vraw + b * REC, sbase + L::V + st * KTILE + b * TILE, sbase + L::TABLE + b * 128, rv, lane,
+                            odd = C::values(vraw + b * REC, sbase + L::V + st * KTILE + b * (NAT ? D * 16 : TILE), sbase + L::TABLE + b * 128, rv, lane,
                                             live, own);
                         }
                         odd = __any_sync(0xffffffffu, odd);
                         if (lane == 0) *reinterpret_cast<volatile uint8_t*>(smem + L::SEEN + 8 * (t & 7) + b) = odd;
-                    } else if (first < x.end) {
-                        C::keys(kraw + b * REC, sbase + L::K + st * KTILE + b * 256, ek, lane);
+                    } else if constexpr (!NAT) {
+                        if (first < x.end) C::keys(smem_r + rk * L::HALF + b * REC, sbase + L::K + st * KTILE + b * 256, (int)e.x, lane);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -935,7 +980,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                 }
                 top = max(top & 0xffffu, top >> 16);
-                const int shift = min(131 - (int)(top >> 7), 110);    // (2^110 makes bf16's smallest an f16)
+                const int shift = min((NAT ? 134 : 131) - (int)(top >> 7), 110);     // (2^110 makes bf16's smallest an f16)
                 f = exp2i(shift);
                 f_out = scale * exp2i(-shift);
             }
@@ -948,9 +993,26 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
                 }
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    w[k] = (RAW ? pack_f16x2(bf16_lo_to_f32(w[k]) * f, bf16_hi_to_f32(w[k]) * f) : w[k]) ^ flip;
-                tmem_st16(tmem + lanes_at + kColQ + (ic & 1) * (D / 2) + half * (D / 4) + 16 * c, w);
+                for (int k = 0; k < 16; ++k) {
+                    // (0 times an infinity makes a NaN of it, for E4M3, which has none)
+                    const float a = bf16_lo_to_f32(w[k]), b = bf16_hi_to_f32(w[k]);
+                    w[k] = (NAT ? pack_f16x2(fmaf(a, f, a * 0.f), fmaf(b, f, b * 0.f)) : RAW ? pack_f16x2(a * f, b * f) : w[k]) ^ flip;
+                }
+                const uint32_t to = tmem + lanes_at + kColQ + (ic & 1) * (D / 2);
+                if constexpr (NAT) {
+                    uint32_t part[2][8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t a = f16x2_to_e4m3x2(w[2 * k]), b = f16x2_to_e4m3x2(w[2 * k + 1]);
+                        part[0][k] = a | b << 16;
+                        part[1][k] = f16x2_to_e4m3x2(sub_f16x2(w[2 * k], e4m3x2_to_f16x2((uint16_t)a))) |
+                                     f16x2_to_e4m3x2(sub_f16x2(w[2 * k + 1], e4m3x2_to_f16x2((uint16_t)b))) << 16;
+                    }
+                    tmem_st8(to + half * (D / 8) + 8 * c, part[0]);
+                    tmem_st8(to + D / 4 + half * (D / 8) + 8 * c, part[1]);
+                } else {
+                    tmem_st16(to + half * (D / 4) + 16 * c, w);
+                }
             }
             tmem_wait_st();
         }
@@ -1022,14 +1084,14 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         for (int i = 0; runs && i < n; ++i) {
             const int t = t0 + i, sb = SW == 2 ? h : t & 1;
             const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
-            const int first = (x.j0 + i) * kKeys + 64 * half - x.c.q.start;      // this thread's first key, as a node
+            // The first key as a node, of this thread's 64; FP8, whose columns are every other eight, of the tile's 128.
+            const int first = (x.j0 + i) * kKeys + (NAT ? 0 : 64 * half) - x.c.q.start;
             // the visible keys of 32 columns are the bits of a word: the context's, then the row's mask
             uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            const bool full = first + 64 <= 0;
+            const bool full = first + (NAT ? 128 : 64) <= 0;
             if (!full && live) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int node = first + 32 * c, left = x.c.q.n - node;
+                auto word = [&](int node) -> uint32_t {
+                    const int left = x.c.q.n - node;
                     uint32_t v = 0u;
                     if (node < 0) {
                         v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
@@ -1039,8 +1101,11 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         v = __funnelshift_r(lo, hi, node & 31);
                     }
                     if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
-                    see[c] = valid ? v : 0u;
-                }
+                    return valid ? v : 0u;
+                };
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    see[c] = NAT ? __byte_perm(word(first + 64 * c), word(first + 64 * c + 32), half ? 0x7531 : 0x6420) : word(first + 32 * c);
             }
             ok = warp_wait(bar(kSFull + sb), SW == 2 ? (t & 1) : ((t >> 1) & 1));
             if (!ok) break;
@@ -1051,8 +1116,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 float c1 = factor;
                 float drop = 1.f;                                     // what a raise of V's power of two puts on O
                 if constexpr (RAW) {
-                    const uint2 e = ld_shared_v2(sbase + L::PASSED + 8 * (t & 7));
-                    c1 *= exp2i((int)e.x - 127);
+                    const uint2 e = ld_shared_v2(sbase + L::PASSED + (NAT ? sb * L::PASS + kKeys * 4 : 8 * (t & 7)));
+                    if (!NAT) c1 *= exp2i((int)e.x - 127);
                     if (i > 0 && (int)e.y != ev) drop = exp2i(ev - (int)e.y);
                     ev = (int)e.y;
                 }
@@ -1064,18 +1129,30 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     uint32_t sr[32];
                     tmem_ld32(mine + 32 * c, sr);
                     tmem_wait_ld();
+                    if constexpr (NAT) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const uint4 sk = ld_shared_v4(sbase + L::PASSED + sb * L::PASS + 256 * half + 128 * c + 4 * k);
+                            const uint64_t a = mul2((uint64_t)sr[k + 1] << 32 | sr[k], (uint64_t)sk.y << 32 | sk.x);
+                            const uint64_t b = mul2((uint64_t)sr[k + 3] << 32 | sr[k + 2], (uint64_t)sk.w << 32 | sk.z);
+                            sr[k] = (uint32_t)a;
+                            sr[k + 1] = (uint32_t)(a >> 32);
+                            sr[k + 2] = (uint32_t)b;
+                            sr[k + 3] = (uint32_t)(b >> 32);
+                        }
+                    }
                     if (!full) {
                         // hidden keys score -inf (a select: unread or stale columns may hold NaN)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (!((see[c] >> k) & 1u)) sr[k] = 0xff800000u;
-                        tmem_st32(mine + 32 * c, sr);
                     }
+                    if (NAT || !full) tmem_st32(mine + 32 * c, sr);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2)
                         m4[2 * c + (k >> 4)] = max3(m4[2 * c + (k >> 4)], __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
                 }
-                if (!full) tmem_wait_st();
+                if (NAT || !full) tmem_wait_st();
                 float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
                 // whether a row of the pair of warps rises, or V's power of two
                 const bool rise = named_bar_or(pair_bar, 64, mx > m_used + kRaise || drop != 1.f);
