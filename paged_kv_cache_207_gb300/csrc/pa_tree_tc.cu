@@ -47,6 +47,7 @@ constexpr uint64_t kWaitNs = 200000000ull;
 constexpr int kTileRows = 128;
 constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
 constexpr int kMinTiles = 3;             // places of a CTA, at least
+constexpr int kPieces = 4;                // records of pieces
 constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at most
 
 // Warps: softmax 0 .. 8 SW - 1, the copies (bf16: V's; else all records), the MMAs, then K's copies
@@ -55,12 +56,14 @@ constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at 
 // pieces of 32 columns, from the TMEM once for the maximum and again for the probabilities.
 template <pa_dtype T, int SW>
 struct Roles {
-    static constexpr int SOFT = 8 * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
+    static constexpr int PARTS = T == PA_FP8_E4M3 ? 4 : 2;       // warps that share 32 rows
+    static constexpr int SOFT = 4 * PARTS * SW, COPY = SOFT, MMA = SOFT + 1, FEED = SOFT + 2;
     static constexpr int FEEDS = T == PA_FP4_E2M1 ? 2 * kKeyBlocks : T == PA_FP8_E4M3 ? kKeyBlocks : SW == 1 ? 4 : 2;
     static constexpr int LEAD = FEED + FEEDS;          // (FP8, FP4) warps that the conversions wait for
     static constexpr int LEADS = T == PA_FP4_E2M1 ? 2 : T == PA_FP8_E4M3 ? 1 : 0;
     static constexpr int OTHERS = (2 + FEEDS + LEADS + 3) / 4 * 4;
     static constexpr int THREADS = (SOFT + OTHERS) * 32;
+    static constexpr int READERS = SOFT + 1 + FEEDS + LEADS;       // of a piece's record: all but the copies' warp
 };
 
 template <int D, pa_dtype T, int SW>
@@ -71,18 +74,18 @@ struct Layout {
     static constexpr bool RAW = T != PA_BF16;                          // values are converted
     static constexpr bool NAT = T == PA_FP8_E4M3;                      // keys are operands as they are
     static constexpr int REC = T == PA_BF16 ? TILE : T == PA_FP8_E4M3 ? 16 * D + 64 : 8 * D + D / 2;
-    static constexpr int KST = NAT ? 4 : RAW ? 2 : 3, VST = RAW ? 2 : (SW == 1 || D == 64) ? 3 : 2;
+    static constexpr int KST = RAW && !NAT ? 2 : 3, VST = RAW ? 2 : (SW == 1 || D == 64) ? 3 : 2;
     // stages of records (FP8: V's; FP4: K's and V's in turn): as many as find room, six at most
     static constexpr int HALF = kKeyBlocks * REC;
     static constexpr int KSTAGE = NAT ? HALF : KTILE;
-    static constexpr int RST = !RAW ? 0 : NAT && D == 128 ? 5 : 6;
-    // query rows: in the TMEM with one row tile, else in shared memory
+    static constexpr int RST = !RAW ? 0 : NAT && D == 128 ? 4 : 6;
+    // query rows: two row tiles: operands; one: on their way to the TMEM, [row][D / 8 pieces, turned by the row]
     static constexpr int Q = 0;
-    static constexpr int K = Q + (SW == 2 ? SW * QTILE : 0);
+    static constexpr int K = Q + SW * QTILE;
     static constexpr int V = K + KST * KSTAGE;
     static constexpr int R = V + VST * KTILE;
     static constexpr int BAR = R + RST * HALF;
-    static constexpr int NBAR = 44;
+    static constexpr int NBAR = 52;
     // what the MMA warp passes on beside the results, and the search's scratch (once, before)
     static constexpr int SLOT = BAR + NBAR * 8;       // TMEM address
     static constexpr int ODD = SLOT + 16;             // [2] of a piece: values that are no finite numbers
@@ -93,8 +96,12 @@ struct Layout {
     static constexpr int SEEN = PASSED + (NAT ? 2 * PASS : 64);      // [8][8] a tile's block has such values
     static constexpr int TABLE = SEEN + 80;           // [8] FP4: a block's scales of values
     static constexpr int GONE = TABLE - 8;            // [2] the conversions' lead gave up, K's and V's
-    static constexpr int ROWS = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);   // [row tile][2][128] maxima, sums
-    static constexpr int BYTES0 = ROWS + SW * 2 * kTileRows * 4;
+    static constexpr int RECORDS = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);      // [kPieces] pieces
+    static constexpr int FIRST = RECORDS + kPieces * 32;               // the CTA's first place, for a call that gives up
+    static constexpr int ROWS = FIRST + 64;                            // [row tile][part][128] maxima, sums
+    static constexpr int TOPS = ROWS + SW * Roles<T, SW>::PARTS * kTileRows * 4;     // [part][128] the queries' largest
+    static constexpr int BYTES0 = TOPS + (RAW ? Roles<T, SW>::PARTS * kTileRows * 4 : 0);
+    static_assert(RECORDS % 16 == 0);
     static_assert(BYTES0 <= 232448, "shared memory of one CTA");
     static_assert((Roles<T, SW>::THREADS / 32 + 6) * 8 <= KTILE, "the search's scratch, where the first tile goes");
     // one CTA (and its 512 TMEM columns) to an SM
@@ -103,7 +110,8 @@ struct Layout {
 
 // barriers
 constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kRFull = 16, kREmpty = 22, kSFull = 28, kPFull = 30,
-              kODone = 32, kPVDone = 34, kQFull = 35, kOFree = 37, kDone = 38, kEFull = 39;
+              kODone = 32, kPVDone = 34, kQFull = 35, kOFree = 37, kDone = 38, kEFull = 39,
+              kXFull = 44, kXEmpty = 48;
 
 // TMEM columns: two S tiles, O of each row tile; with one row tile, the query rows of two pieces.
 constexpr uint32_t kColS = 0, kColO = 2 * kKeys, kColQ = kColO + 128;
@@ -133,8 +141,7 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 }
 // All lanes wait, a fifth of a second at most; the result is the same in all.  (A look costs four
 // instructions: the waiting warps share their issue slots with those that work.)
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = global_timer_ns();
     bool ok;
     do {
@@ -143,6 +150,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
         while (!ok && --looks > 0);
     } while (!ok && global_timer_ns() - t0 < kWaitNs);
     return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) ? true : warp_wait_long(bar, parity);
 }
 // One 32-byte store (the address a multiple of 32).
 __device__ __forceinline__ void st_global_v8(void* addr, const uint32_t (&w)[8]) {
@@ -189,30 +199,35 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x, uint32_t exponent) {
     return ((e & 0xffffu) == (exponent & 0xffffu) ? 0xffffu : 0u) | ((e >> 16) == (exponent >> 16) ? 0xffff0000u : 0u);
 }
 
-// A run of key tiles of one item, as every role walks them.
+// A run of key tiles of one item.
 struct Piece {
-    Cursor<kKeys> c;
-    int j0, j1;              // its key tiles
-    int tokens, rows;        // of the row tile
-    int qrow;                // row of q of its first token
-    int end;                 // keys of the sequence
-    int nblk;                // blocks of them
+    int j0, n;               // its first key tile, and how many; none: the CTA's work has ended
+    int tokens, qrow;        // of the row tile, and the row of q of its first
+    int start, nodes;        // of the sequence
+    int s, h;                // sequence, kv head
+    bool whole;              // all tiles of the item
+    __device__ __forceinline__ int end() const { return start + nodes; }
+    __device__ __forceinline__ int blocks() const { return (start + nodes + kBlockTokens - 1) / kBlockTokens; }
 };
-__device__ __forceinline__ Piece piece_at(const TParams& p, const Cursor<kKeys>& c, long long left) {
-    Piece x;
-    x.c = c;
-    x.j0 = c.tile(c.at);
-    x.j1 = c.tile((int)min((long long)c.cost(), c.at + left));
-    x.tokens = item_tokens(p, c);
-    x.rows = x.tokens * p.G;
-    x.qrow = c.q.q0 + c.rt * p.TQ;
-    x.end = c.q.start + c.q.n;
-    x.nblk = (x.end + kBlockTokens - 1) / kBlockTokens;
-    return x;
-}
+// The copies' warp goes through the places and leaves each piece as a record, one ahead of its own; the
+// others read them (to find the next item costs a few hundred instructions and, at times, a load).
 struct Walk {
     Cursor<kKeys> c;
     long long left;          // places from the cursor on
+    __device__ __forceinline__ Piece piece(const TParams& p) const {
+        Piece x;
+        x.j0 = c.tile(c.at);
+        const int j1 = c.tile((int)min((long long)c.cost(), c.at + left));
+        x.n = left > 0 ? j1 - x.j0 : 0;
+        x.tokens = item_tokens(p, c);
+        x.qrow = c.q.q0 + c.rt * p.TQ;
+        x.start = c.q.start;
+        x.nodes = c.q.n;
+        x.s = c.s;
+        x.h = c.h;
+        x.whole = x.j0 == 0 && j1 == c.q.tiles;
+        return x;
+    }
     // To the next item with tiles for this CTA (a run that ends before an item's first tile has none).
     __device__ __forceinline__ void next(const TParams& p) {
         left -= c.cost() - c.at;
@@ -220,6 +235,8 @@ struct Walk {
         else left = 0;
     }
 };
+
+static_assert(sizeof(Walk) <= 64, "its place in shared memory");
 
 // The table of a piece in windows of 32 entries, one per lane, a window ahead of its use (read tile
 // by tile, every tile would wait for a load).
@@ -232,9 +249,9 @@ struct Table {
         return b < nblk ? __ldg(row + b) : -1;
     }
     __device__ __forceinline__ Table(const TParams& p, const Piece& x, int lane_) {
-        row = p.tables + (size_t)x.c.s * p.max_blocks;
+        row = p.tables + (size_t)x.s * p.max_blocks;
         first = x.j0 * kKeyBlocks;
-        nblk = x.nblk;
+        nblk = x.blocks();
         lane = lane_;
         at = 0;
         now = fetch(0);
@@ -456,19 +473,34 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// 8 consecutive 32-bit columns of this thread's lane.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// N consecutive 32-bit columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32);
+    if constexpr (N == 4) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else if constexpr (N == 16) {
+        tmem_st16(taddr, r);
+    } else {
+        tmem_st32(taddr, r);
+    }
 }
-// 16 consecutive 32-bit columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 16 || N == 32);
+    if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+    } else {
+        tmem_ld32(taddr, r);
+    }
 }
 
 // One element of a value as a number, from the pool.
@@ -520,9 +552,13 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSFull + i), RAW ? 2 : 1);      // (RAW: the MMA warp passes the exponents on)
-            mbar_init(bar(kPFull + i), 8);
+            mbar_init(bar(kPFull + i), 4 * W::PARTS);
             mbar_init(bar(kODone + i), 2);
-            mbar_init(bar(kQFull + i), 8);
+            mbar_init(bar(kQFull + i), 4 * W::PARTS);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(kXFull + i), 1);
+            mbar_init(bar(kXEmpty + i), W::READERS);
         }
         mbar_init(bar(kPVDone), 1);
         mbar_init(bar(kOFree), W::SOFT);
@@ -549,8 +585,29 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         // (said whether or not the call goes on, by the last thread, which has the least to do)
         if (threadIdx.x == W::THREADS - 1) say_joint(p, line, walk.c, blockIdx.x, any);
     }
+    if (threadIdx.x == 0) *reinterpret_cast<Walk*>(smem + L::FIRST) = walk;
     // (the same for all threads, and the search's scratch is free)
     if (__syncthreads_or(flag & PA_DEV_ERR_TIMEOUT) || walk.left == 0) return;
+    // the ic-th piece of the CTA
+    auto piece = [&](int ic, Piece& x) -> bool {
+        if (!warp_wait(bar(kXFull + ic % kPieces), (ic / kPieces) & 1)) return false;
+        const uint32_t at = sbase + L::RECORDS + (ic % kPieces) * 32;
+        const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 16);
+        x.j0 = (int)a.x;
+        x.n = (int)a.y;
+        x.tokens = (int)a.z;
+        x.qrow = (int)a.w;
+        x.start = (int)b.x;
+        x.nodes = (int)b.y;
+        x.s = (int)b.z;
+        x.h = (int)(b.w & 0x7fffffffu);
+        x.whole = b.w >> 31;
+        return true;
+    };
+    auto piece_done = [&](int ic) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kXEmpty + ic % kPieces));
+    };
 
     if (warp >= W::SOFT) {
     if (warp == W::COPY) {
@@ -562,10 +619,25 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         const int full0 = RAW ? kRFull : kVFull, empty0 = RAW ? kREmpty : kVEmpty;
         bool ok = true;
         int u = 0, uk = 0;                            // stages filled so far (K's own: FP8)
-        while (ok && walk.left > 0) {
-            const Piece x = piece_at(p, walk.c, walk.left);
+        Piece ahead = walk.piece(p);
+        auto put = [&](int ic) {
+            if (ic >= kPieces) ok = ok && warp_wait(bar(kXEmpty + ic % kPieces), (ic / kPieces - 1) & 1);
+            if (ok && lane == 0) {
+                const uint32_t at = sbase + L::RECORDS + (ic % kPieces) * 32;
+                st_shared_v4(at, make_uint4(ahead.j0, ahead.n, ahead.tokens, ahead.qrow));
+                st_shared_v4(at + 16, make_uint4(ahead.start, ahead.nodes, ahead.s, (uint32_t)ahead.h | (ahead.whole ? 1u << 31 : 0u)));
+                mbar_arrive(bar(kXFull + ic % kPieces));
+            }
+            __syncwarp();
+        };
+        put(0);
+        for (int ic = 0; ok && ahead.n > 0; ++ic) {
+            const Piece x = ahead;
+            walk.next(p);
+            ahead = walk.piece(p);
+            put(ic + 1);
             Table table(p, x, lane);
-            for (int i = 0; ok && i < x.j1 - x.j0; ++i) {
+            for (int i = 0; ok && i < x.n; ++i) {
                 const int32_t blk = table.block(p, i);
                 const bool mine = blk >= 0 && lane < kKeyBlocks;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * REC;
@@ -587,12 +659,11 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (mine) {
                         const char* pool = RAW && k == 0 ? p.k_pool : p.v_pool;
                         const uint32_t dst = to_k ? L::K + st * KSTAGE + lane * REC : RAW ? L::R + st * L::HALF + lane * REC : L::V + st * KTILE + lane * TILE;
-                        bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC, REC, full, pol);
+                        bulk_g2s(sbase + dst, pool + ((size_t)blk * p.Hkv + x.h) * (size_t)REC, REC, full, pol);
                     }
                     ++at;
                 }
             }
-            walk.next(p);
         }
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // before the CTA ends, every copy has landed
@@ -612,9 +683,11 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         constexpr uint32_t idS = idesc(RAW, NAT ? kKeys / 2 : kKeys, 0), idO = idesc(RAW, D, RAW ? 0 : 1);
         bool ok = true;
         int t0 = 0;
-        for (int ic = 0; ok && walk.left > 0; ++ic) {
-            const Piece x = piece_at(p, walk.c, walk.left);
-            const int n = x.j1 - x.j0;
+        for (int ic = 0; ok; ++ic) {
+            Piece x;
+            ok = piece(ic, x);
+            if (!ok || x.n == 0) break;
+            const int n = x.n, nblk = x.blocks();
             bool odd = false;
             auto issue_s = [&](int hh, int i) {
                 const int t = t0 + i, buf = SW == 2 ? hh : t & 1;
@@ -672,17 +745,17 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     ok = warp_wait(bar(kOFree), (ic - 1) & 1);            // the last piece's O is read
                     if (!ok) return;
                 }
-                const int tok0 = (x.j0 + i) * kKeys, nb = min(kKeyBlocks, x.nblk - (x.j0 + i) * kKeyBlocks);
+                const int tok0 = (x.j0 + i) * kKeys, nb = min(kKeyBlocks, nblk - (x.j0 + i) * kKeyBlocks);
                 if (hh == 0) {
                     ok = warp_wait(bar(kVFull + st), (t / VST) & 1);
                     if (!ok) return;
                     if constexpr (RAW) {
                         const uint2 o = ld_shared_v2(sbase + L::SEEN + 8 * (t & 7));
                         odd |= (o.x | o.y) != 0u;
-                    } else if (tok0 + nb * kBlockTokens > x.c.q.start) {
+                    } else if (tok0 + nb * kBlockTokens > x.start) {
                         // slots past the last key may hold anything: zeros; values of the tree's own
                         // tokens that are no finite numbers too (looked for in all of its blocks)
-                        const int from = max(x.c.q.start - tok0, 0), to = x.end - tok0;
+                        const int from = max(x.start - tok0, 0), to = x.end() - tok0;
                         uint8_t* const vt = smem + L::V + st * KTILE;
                         constexpr int PIECES = (D / 8) * kBlockTokens;                 // of a block
                         if (to < nb * kBlockTokens) {
@@ -724,13 +797,14 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     const uint64_t vd = RAW ? umma_desc(sbase + L::V + st * KTILE, D * 16, 128)
                                             : umma_desc(sbase + L::V + st * KTILE, 128, 256);
                     const uint32_t more = i > 0 ? 1u : 0u;
+                    constexpr int PB = kKeyBlocks / W::PARTS;           // each part of the rows' threads begins at its own columns
                     if (nb == kKeyBlocks) {
 #pragma unroll
                         for (int b = 0; b < kKeyBlocks; ++b)
-                            umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                            umma_ts(ocol, pcol + kKeys / W::PARTS * (b / PB) + 8 * (b % PB), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
                     } else {
                         for (int b = 0; b < kKeyBlocks; ++b)
-                            if ((NAT ? 2 * (b % 4) : b) < nb) umma_ts(ocol, pcol + 8 * b + (b < kKeyBlocks / 2 ? 0 : 32), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                            if ((NAT ? 2 * (b % 4) : b) < nb) umma_ts(ocol, pcol + kKeys / W::PARTS * (b / PB) + 8 * (b % PB), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
                     }
                     if (hh == SW - 1) umma_commit(bar(kVEmpty + st));
                     if (SW == 1) umma_commit(bar(kPVDone));
@@ -783,7 +857,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 }
             }
             t0 += n;
-            walk.next(p);
+            piece_done(ic);
         }
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // nothing may still be running on the tensor cores when the TMEM is freed
@@ -801,12 +875,14 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             const bool for_v = NAT || warp > W::LEAD;
             bool ok = true;
             int t = 0;
-            while (ok && walk.left > 0) {
-                const Piece x = piece_at(p, walk.c, walk.left);
+            for (int ic = 0; ok; ++ic) {
+                Piece x;
+                ok = piece(ic, x);
+                if (!ok || x.n == 0) break;
                 int rv = 0;
-                for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
+                for (int i = 0; i < x.n; ++i, ++t) {
                     const int uk = 2 * t, uv = NAT ? t : 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST;
-                    const int keys = x.end - (x.j0 + i) * kKeys;
+                    const int keys = x.end() - (x.j0 + i) * kKeys;
                     if (NAT || !for_v) {
                         int ek = 0;
                         if (!NAT) {
@@ -836,7 +912,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     named_bar_arrive(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
                     if (!ok) break;
                 }
-                walk.next(p);
+                piece_done(ic);
             }
             if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         }
@@ -852,9 +928,12 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             const uint32_t smem_r = sbase + L::R;
             bool ok = true;
             int t = 0;
-            while (ok && walk.left > 0) {
-                const Piece x = piece_at(p, walk.c, walk.left);
-                for (int i = 0; i < x.j1 - x.j0; ++i, ++t) {
+            for (int ic = 0; ok; ++ic) {
+                Piece x;
+                ok = piece(ic, x);
+                if (!ok || x.n == 0) break;
+                const int end = x.end();
+                for (int i = 0; i < x.n; ++i, ++t) {
                     // (stages of K and V in turn)
                     const int uk = 2 * t, uv = NAT ? t : 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST, st = for_v ? t % VST : t % KST;
                     const uint32_t vraw = smem_r + rs * L::HALF;
@@ -868,8 +947,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (for_v) {
                         bool odd = false;
                         // (FP8: an odd last block has the next one's zeros beside it)
-                        if (first < x.end || (NAT && (b & 1) && first - kBlockTokens < x.end)) {
-                            const int keys = min(max(x.end - first, 0), kBlockTokens), ctx = min(max(x.c.q.start - first, 0), kBlockTokens);
+                        if (first < end || (NAT && (b & 1) && first - kBlockTokens < end)) {
+                            const int keys = min(max(end - first, 0), kBlockTokens), ctx = min(max(x.start - first, 0), kBlockTokens);
                             const uint32_t live = (1u << keys) - 1u, own = live & ~((1u << ctx) - 1u);
                             odd = C::values(vraw + b * REC, sbase + L::V + st * KTILE + b * (NAT ? D * 16 : TILE), sbase + L::TABLE + b * 128, rv, lane,
                                             live, own);
@@ -877,7 +956,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         odd = __any_sync(0xffffffffu, odd);
                         if (lane == 0) *reinterpret_cast<volatile uint8_t*>(smem + L::SEEN + 8 * (t & 7) + b) = odd;
                     } else if constexpr (!NAT) {
-                        if (first < x.end) C::keys(smem_r + rk * L::HALF + b * REC, sbase + L::K + st * KTILE + b * 256, (int)e.x, lane);
+                        if (first < end) C::keys(smem_r + rk * L::HALF + b * REC, sbase + L::K + st * KTILE + b * 256, (int)e.x, lane);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -886,7 +965,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         mbar_arrive(bar(kREmpty + (for_v ? rs : rk)));
                     }
                 }
-                walk.next(p);
+                piece_done(ic);
             }
         } else {
             // -------------------------------------------------------- K's pieces
@@ -898,9 +977,11 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             const int kt = f * 32 + lane;
             bool ok = true;
             int t0 = 0;
-            while (ok && walk.left > 0) {
-                const Piece x = piece_at(p, walk.c, walk.left);
-                const int n = x.j1 - x.j0;
+            for (int ic = 0; ok; ++ic) {
+                Piece x;
+                ok = piece(ic, x);
+                if (!ok || x.n == 0) break;
+                const int n = x.n;
                 Table table(p, x, lane);
                 int next = 0;
                 auto issue = [&]() {
@@ -910,7 +991,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     for (int b = 0; b < kKeyBlocks; ++b) {
                         const int32_t bb = __shfl_sync(0xffffffffu, blk, b);
                         if (bb < 0) continue;
-                        const char* src = p.k_pool + ((size_t)bb * p.Hkv + x.c.h) * (size_t)TILE;
+                        const char* src = p.k_pool + ((size_t)bb * p.Hkv + x.h) * (size_t)TILE;
 #pragma unroll
                         for (int u = 0; u < PER; ++u) {
                             const int piece = u * 32 * W::FEEDS + kt;
@@ -937,7 +1018,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (lane == 0) mbar_arrive(bar(kKFull + (t0 + pub) % KST));
                 }
                 t0 += n;
-                walk.next(p);
+                piece_done(ic);
             }
             if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
             cp_async_wait<0>();
@@ -948,72 +1029,96 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     // Warps w and w + 4 of a row tile's eight reach the TMEM lanes 32 (w % 4) .. and share its rows: the
     // first takes the tile's keys 0 .. 63, the second 64 .. 127 (half the code and the wait of a warp
     // that takes them all).  They agree on the row's maximum through shared memory where it rises.
-    const int quarter = warp & 3, half = (warp >> 2) & 1, h = warp >> 3;
+    constexpr int PARTS = W::PARTS, COLS = kKeys / PARTS, NC = COLS / 32, DP = D / PARTS;
+    const int quarter = warp & 3, part = (warp >> 2) % PARTS, h = warp / (4 * PARTS);
     const int lr = quarter * 32 + lane, row = h * kTileRows + lr;
     const int tl = row / p.G, g = row - tl * p.G;                     // token of the row tile, query head
     const uint32_t lanes_at = (uint32_t)(32 * quarter) << 16;
-    const int pair_bar = 3 + 4 * h + quarter;                         // the pair's named barrier
-    float* const shared_row = reinterpret_cast<float*>(smem + L::ROWS) + (h * 2) * kTileRows + lr;    // [half]
+    const int row_bar = 3 + 4 * h + quarter;                          // the named barrier of the warps with the same rows
+    float* const shared_row = reinterpret_cast<float*>(smem + L::ROWS) + (h * PARTS) * kTileRows + lr;    // [part]
     const float scale = fabsf(p.scale_log2);
     // a negative scale is applied as |scale| to -q, so that the row's maximum is that of the unscaled scores
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     constexpr int QB = D / 8;
     // A warp without rows only keeps the barriers going.
-    auto busy = [&](const Piece& x) { return row - lane < x.rows; };
-    auto q_of = [&](const Piece& x) {
-        return static_cast<const uint16_t*>(p.q) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
+    auto busy = [&](const Piece& x) { return row - lane < x.tokens * p.G; };
+    // row r of the row tile
+    auto q_of = [&](const Piece& x, int token, int head) {
+        return static_cast<const uint16_t*>(p.q) + ((size_t)(x.qrow + token) * p.Hq + (size_t)x.h * p.G + head) * D;
     };
     uint32_t tmem = 0u;
     float factor = scale;                                             // of the row's scores
-    // One row tile: the row goes through registers into the TMEM, columns of the piece's parity, half
-    // of them by each thread of the pair.
+    // One row tile: the rows of the warps come to shared memory by whole rows (a thread that loads its
+    // own row touches 32 lines at a time: 12000 clocks a piece), 16-byte piece u of row r at place u ^ r % 8,
+    // and each goes through registers into the TMEM, columns of the piece's parity, a part of them by
+    // each of the row's threads.
+    auto stage_q = [&](const Piece& x) {
+        if (busy(x)) {
+#pragma unroll 1
+            for (int k = part; k < QB; k += PARTS) {
+                const int e = 32 * k + lane, r = 32 * quarter + e / QB, u = e % QB, token = r / p.G;
+                const uint32_t to = sbase + L::Q + r * (2 * D) + (uint32_t)((u ^ (r & 7)) * 16);
+                if (token < x.tokens) cp_async_16(to, q_of(x, token, r - token * p.G) + 8 * u);
+                else st_shared_v4(to, make_uint4(0u, 0u, 0u, 0u));
+            }
+        }
+        cp_async_commit();
+    };
     auto put_q = [&](const Piece& x, int ic) -> float {
         float f = 1.f, f_out = scale;
+        cp_async_wait<0>();
         if (busy(x)) {
-            const bool valid = tl < x.tokens;
-            const uint4* src = reinterpret_cast<const uint4*>(q_of(x));
+            named_bar_sync(row_bar, 32 * PARTS);                      // (the rows)
+            auto at = [&](int u) { return ld_shared_v4(sbase + L::Q + lr * (2 * D) + (uint32_t)(((part * (DP / 8) + u) ^ (lr & 7)) * 16)); };
             if constexpr (RAW) {
                 uint32_t top = 0u;
-#pragma unroll 8
-                for (int u = 0; u < QB; ++u) {
-                    const uint4 v = valid ? src[u] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int u = 0; u < DP / 8; ++u) {
+                    const uint4 v = at(u);
                     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                 }
-                top = max(top & 0xffffu, top >> 16);
+                uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + L::TOPS) + lr;
+                tops[part * kTileRows] = max(top & 0xffffu, top >> 16);
+                named_bar_sync(row_bar, 32 * PARTS);
+                top = tops[0];
+#pragma unroll
+                for (int k = 1; k < PARTS; ++k) top = max(top, tops[k * kTileRows]);
                 const int shift = min((NAT ? 134 : 131) - (int)(top >> 7), 110);     // (2^110 makes bf16's smallest an f16)
                 f = exp2i(shift);
                 f_out = scale * exp2i(-shift);
             }
+            constexpr int NW = DP < 32 ? DP / 2 : 16;                 // words of two dims at a time
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t w[16];
+            for (int c = 0; c < DP / (2 * NW); ++c) {
+                uint32_t w[NW];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint4 v = valid ? src[half * (QB / 2) + 4 * c + u] : make_uint4(0u, 0u, 0u, 0u);
+                for (int u = 0; u < NW / 4; ++u) {
+                    const uint4 v = at(NW / 4 * c + u);
                     w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
                 }
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < NW; ++k) {
                     // (0 times an infinity makes a NaN of it, for E4M3, which has none)
                     const float a = bf16_lo_to_f32(w[k]), b = bf16_hi_to_f32(w[k]);
                     w[k] = (NAT ? pack_f16x2(fmaf(a, f, a * 0.f), fmaf(b, f, b * 0.f)) : RAW ? pack_f16x2(a * f, b * f) : w[k]) ^ flip;
                 }
                 const uint32_t to = tmem + lanes_at + kColQ + (ic & 1) * (D / 2);
                 if constexpr (NAT) {
-                    uint32_t part[2][8];
+                    uint32_t hi[NW / 2], lo[NW / 2];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < NW / 2; ++k) {
                         const uint32_t a = f16x2_to_e4m3x2(w[2 * k]), b = f16x2_to_e4m3x2(w[2 * k + 1]);
-                        part[0][k] = a | b << 16;
-                        part[1][k] = f16x2_to_e4m3x2(sub_f16x2(w[2 * k], e4m3x2_to_f16x2((uint16_t)a))) |
-                                     f16x2_to_e4m3x2(sub_f16x2(w[2 * k + 1], e4m3x2_to_f16x2((uint16_t)b))) << 16;
+                        hi[k] = a | b << 16;
+                        lo[k] = f16x2_to_e4m3x2(sub_f16x2(w[2 * k], e4m3x2_to_f16x2((uint16_t)a))) |
+                                f16x2_to_e4m3x2(sub_f16x2(w[2 * k + 1], e4m3x2_to_f16x2((uint16_t)b))) << 16;
                     }
-                    tmem_st8(to + half * (D / 8) + 8 * c, part[0]);
-                    tmem_st8(to + D / 4 + half * (D / 8) + 8 * c, part[1]);
+                    tmem_st(to + part * (DP / 4) + NW / 2 * c, hi);
+                    tmem_st(to + D / 4 + part * (DP / 4) + NW / 2 * c, lo);
                 } else {
-                    tmem_st16(to + half * (D / 4) + 16 * c, w);
+                    tmem_st(to + part * (DP / 2) + NW * c, w);
                 }
             }
+            named_bar_sync(row_bar, 32 * PARTS);                      // (the rows are read)
             tmem_wait_st();
         }
         tc_fence_before();
@@ -1021,17 +1126,17 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (lane == 0) mbar_arrive(bar(kQFull + (ic & 1)));
         return f_out;
     };
-    // Two: into shared memory by 16-byte copies, and published later.
-    const uint32_t qdst = sbase + L::Q + h * L::QTILE + (uint32_t)((lr >> 3) * 128 + (lr & 7) * 16) + half * (QB / 2) * 2048;
+    // Two: as operands, eight rows' 16-byte pieces side by side, and published later by the threads that
+    // loaded them: lanes are 8 rows by 4 pieces.
+    const uint32_t qdst = sbase + L::Q + h * L::QTILE + (uint32_t)(quarter * 512 + (lane & 7) * 16 + (lane >> 3) * 2048);
     auto load_q = [&](const Piece& x) {
         if (!busy(x)) return;
-        if (tl < x.tokens) {
-            const uint16_t* src = q_of(x) + half * (D / 2);
-#pragma unroll
-            for (int u = 0; u < QB / 2; ++u) cp_async_16(qdst + u * 2048, src + 8 * u);
-        } else {
-#pragma unroll
-            for (int u = 0; u < QB / 2; ++u) st_shared_v4(qdst + u * 2048, make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll 1
+        for (int k = part; k < QB; k += PARTS) {                      // [8 rows of 32][4 pieces]
+            const int r8 = k & 3, u = k & ~3, r = h * kTileRows + 32 * quarter + 8 * r8 + (lane & 7), token = r / p.G;
+            const uint32_t to = qdst + r8 * 128 + u * 2048;
+            if (token < x.tokens) cp_async_16(to, q_of(x, token, r - token * p.G) + 8 * (u + (lane >> 3)));
+            else st_shared_v4(to, make_uint4(0u, 0u, 0u, 0u));
         }
         cp_async_commit();
     };
@@ -1040,17 +1145,20 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         __syncwarp();
         if (flip && busy(x)) {
 #pragma unroll 1
-            for (int u = 0; u < QB / 2; ++u) {
-                const uint4 v = ld_shared_v4(qdst + u * 2048);
-                st_shared_v4(qdst + u * 2048, make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
+            for (int k = part; k < QB; k += PARTS) {
+                const uint32_t to = qdst + (k & 3) * 128 + (k & ~3) * 2048;
+                const uint4 v = ld_shared_v4(to);
+                st_shared_v4(to, make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
             }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQFull + h));
     };
-    Piece x = piece_at(p, walk.c, walk.left);
+    Piece x{};
+    bool ok = piece(0, x);
     if constexpr (SW == 2) load_q(x);
+    else stage_q(x);
     tc_fence_before();
     named_bar_sync(2, 32 * (W::SOFT + 1));
     tc_fence_after();
@@ -1060,38 +1168,36 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     constexpr float kLift = RAW ? 7.f : 0.f;                          // (log2) on the probabilities
     if constexpr (SW == 2) publish_q(x);
     else factor = put_q(x, 0);
-    bool ok = true;
-    int t0 = 0;
-    for (int ic = 0; ok; ++ic) {
-        const int n = x.j1 - x.j0;
+    int t0 = 0, ic = 0;
+    for (; ok; ++ic) {
+        const int n = x.n, rows = x.tokens * p.G;
         const bool live = busy(x), valid = tl < x.tokens;
         const int32_t* mrow = p.mask + (size_t)(x.qrow + (valid ? tl : 0)) * p.words;
+        Piece y;
+        ok = piece(ic + 1, y);
+        if (!ok) break;
+        if (SW == 1 && y.n > 0) stage_q(y);
         float m_used = -INFINITY, l = 0.f, factor_next = scale;
         int ev = 0;
         // the row tile's warps without rows do not go through the keys: its first one arrives for them
-        const int with_rows = 2 * max(0, min(4, (x.rows - h * kTileRows + 31) / 32));
-        const bool leads = (warp & 7) == 0, runs = live || leads;
-        const uint32_t arrivals = leads ? 8 - with_rows + (with_rows > 0 ? 1 : 0) : 1;
-        auto next_q = [&]() {
-            Walk ahead = walk;
-            ahead.next(p);
-            if (ahead.left <= 0) return;
-            const Piece y = piece_at(p, ahead.c, ahead.left);
-            if constexpr (SW == 2) load_q(y);
-            else factor_next = put_q(y, ic + 1);
-        };
-        if (SW == 1 && !runs) next_q();
-        for (int i = 0; runs && i < n; ++i) {
+        const int with_rows = PARTS * max(0, min(4, (rows - h * kTileRows + 31) / 32));
+        const bool leads = warp % (4 * PARTS) == 0, runs = live || leads;
+        const uint32_t arrivals = leads ? 4 * PARTS - with_rows + (with_rows > 0 ? 1 : 0) : 1;
+        // (the first tile by itself: the next piece's queries then follow outside the loop, which stays short)
+        for (int lo = 0; ok && lo < n;) {
+        const int hi = SW == 1 && lo == 0 ? 1 : n;
+#pragma unroll 1
+        for (int i = lo; runs && i < hi; ++i) {
             const int t = t0 + i, sb = SW == 2 ? h : t & 1;
             const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
-            // The first key as a node, of this thread's 64; FP8, whose columns are every other eight, of the tile's 128.
-            const int first = (x.j0 + i) * kKeys + (NAT ? 0 : 64 * half) - x.c.q.start;
+            // The first key as a node, of this thread's; FP8, whose columns are every other eight, of the tile's 128.
+            const int first = (x.j0 + i) * kKeys + (NAT ? 0 : COLS * part) - x.start;
             // the visible keys of 32 columns are the bits of a word: the context's, then the row's mask
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            const bool full = first + (NAT ? 128 : 64) <= 0;
-            if (!full && live) {
+            uint32_t see[NC];
+            const bool full = first + (NAT ? kKeys : COLS) <= 0;
+            if (live && !full) {
                 auto word = [&](int node) -> uint32_t {
-                    const int left = x.c.q.n - node;
+                    const int left = x.nodes - node;
                     uint32_t v = 0u;
                     if (node < 0) {
                         v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
@@ -1104,13 +1210,14 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     return valid ? v : 0u;
                 };
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    see[c] = NAT ? __byte_perm(word(first + 64 * c), word(first + 64 * c + 32), half ? 0x7531 : 0x6420) : word(first + 32 * c);
+                for (int c = 0; c < NC; ++c) {
+                    const int at = part * NC + c;                     // of the tile's four: FP8: [slots' half][blocks' half]
+                    see[c] = NAT ? __byte_perm(word(first + 64 * (at & 1)), word(first + 64 * (at & 1) + 32), at & 2 ? 0x7531 : 0x6420)
+                                 : word(first + 32 * c);
+                }
             }
             ok = warp_wait(bar(kSFull + sb), SW == 2 ? (t & 1) : ((t >> 1) & 1));
             if (!ok) break;
-            // (two row tiles: this piece's scores are taken, their Q is free)
-            if (SW == 2 && i == n - 1) next_q();
             if (live) {
                 tc_fence_after();
                 float c1 = factor;
@@ -1122,45 +1229,53 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     ev = (int)e.y;
                 }
                 c1 = fmaxf(c1, FLT_MIN);                              // (a hidden key's -inf stays -inf under a scale of 0)
-                const uint32_t mine = lanes + scol + 64 * half;
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t sr[32];
+                const uint32_t mine = lanes + scol + COLS * part;
+                uint32_t sr[32];
+                // 32 of the thread's columns, hidden keys' -inf (a select: unread or stale columns may hold NaN)
+                auto scores = [&](int c) {
                     tmem_ld32(mine + 32 * c, sr);
+                    uint4 sk[NAT ? 8 : 1];
+                    if constexpr (NAT) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) sk[k] = ld_shared_v4(sbase + L::PASSED + sb * L::PASS + 4 * (COLS * part + 32 * c + 4 * k));
+                    }
                     tmem_wait_ld();
                     if constexpr (NAT) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
-                            const uint4 sk = ld_shared_v4(sbase + L::PASSED + sb * L::PASS + 256 * half + 128 * c + 4 * k);
-                            const uint64_t a = mul2((uint64_t)sr[k + 1] << 32 | sr[k], (uint64_t)sk.y << 32 | sk.x);
-                            const uint64_t b = mul2((uint64_t)sr[k + 3] << 32 | sr[k + 2], (uint64_t)sk.w << 32 | sk.z);
+                            const uint64_t a = mul2((uint64_t)sr[k + 1] << 32 | sr[k], (uint64_t)sk[k / 4].y << 32 | sk[k / 4].x);
+                            const uint64_t b = mul2((uint64_t)sr[k + 3] << 32 | sr[k + 2], (uint64_t)sk[k / 4].w << 32 | sk[k / 4].z);
                             sr[k] = (uint32_t)a;
                             sr[k + 1] = (uint32_t)(a >> 32);
                             sr[k + 2] = (uint32_t)b;
                             sr[k + 3] = (uint32_t)(b >> 32);
                         }
                     }
+                };
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    scores(c);
                     if (!full) {
-                        // hidden keys score -inf (a select: unread or stale columns may hold NaN)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (!((see[c] >> k) & 1u)) sr[k] = 0xff800000u;
+                        if (NC > 1) tmem_st32(mine + 32 * c, sr);
                     }
-                    if (NAT || !full) tmem_st32(mine + 32 * c, sr);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2)
-                        m4[2 * c + (k >> 4)] = max3(m4[2 * c + (k >> 4)], __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
+                        m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
                 }
-                if (NAT || !full) tmem_wait_st();
+                if (NC > 1 && !full) tmem_wait_st();
                 float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
                 // whether a row of the pair of warps rises, or V's power of two
-                const bool rise = named_bar_or(pair_bar, 64, mx > m_used + kRaise || drop != 1.f);
+                const bool rise = named_bar_or(row_bar, 32 * PARTS, mx > m_used + kRaise || drop != 1.f);
                 float alpha = 1.f;
                 if (rise) {
-                    shared_row[half * kTileRows] = mx;
-                    named_bar_sync(pair_bar, 64);
-                    mx = fmaxf(mx, shared_row[(half ^ 1) * kTileRows]);
+                    shared_row[part * kTileRows] = mx;
+                    named_bar_sync(row_bar, 32 * PARTS);
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k) mx = fmaxf(mx, shared_row[k * kTileRows]);
                     if (mx > m_used + kRaise) {                       // (the first keys: from -inf)
                         alpha = fast_exp2(m_used - mx);
                         m_used = mx;
@@ -1173,16 +1288,16 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         }
                         const float on_o = alpha * drop;
 #pragma unroll 1
-                        for (int c = 0; c < D / 32 && ok; ++c) {
+                        for (int c = 0; c < DP / 16 && ok; ++c) {
                             uint32_t o[16];
-                            tmem_ld16(lanes + ocol + half * (D / 2) + 16 * c, o);
+                            tmem_ld(lanes + ocol + part * DP + 16 * c, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * on_o);
-                            tmem_st16(lanes + ocol + half * (D / 2) + 16 * c, o);
+                            tmem_st(lanes + ocol + part * DP + 16 * c, o);
                         }
                     }
-                    named_bar_sync(pair_bar, 64);                     // (the maxima are read)
+                    named_bar_sync(row_bar, 32 * PARTS);                     // (the maxima are read)
                     if (!ok) break;
                 }
                 // probabilities, rounded to the tensor cores' type (the sums take them unrounded: the
@@ -1190,11 +1305,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 const float m_sub = (m_used == -INFINITY ? 0.f : m_used) - kLift;
                 const uint64_t c2 = pair_of(c1, c1), nm2 = pair_of(-m_sub, -m_sub);
                 uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t sr[32], pk[16];
-                    tmem_ld32(mine + 32 * c, sr);
-                    tmem_wait_ld();
+#pragma unroll (RAW ? 1 : 2)
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t pk[16];
+                    if constexpr (NC > 1) scores(c);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
                         const uint64_t y = fma2(pair_of(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
@@ -1211,35 +1325,41 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_n(bar(kPFull + sb), arrivals);
-            // (the last piece's scores are taken: their Q is free)
-            if (SW == 1 && i == 0) next_q();
+        }
+        // (one row tile: the last piece's scores are taken, their Q is free)
+        if (SW == 1 && ok && lo == 0 && y.n > 0) factor_next = put_q(y, ic + 1);
+        lo = hi;
         }
         if (!ok) break;
+        // (two: this piece's scores are taken, their Q is free)
+        if (SW == 2 && y.n > 0) load_q(y);
         ok = warp_wait(bar(kODone + h), ic & 1);
         if (!ok) break;
-        if (SW == 2 && !runs) next_q();
         tc_fence_after();
         if (live) {
             // the row's sum, of both halves in their order
-            shared_row[half * kTileRows] = l;
-            named_bar_sync(pair_bar, 64);
-            l = shared_row[0] + shared_row[kTileRows];
-            const bool whole = x.j0 == 0 && x.j1 == x.c.q.tiles;
+            shared_row[part * kTileRows] = l;
+            named_bar_sync(row_bar, 32 * PARTS);
+            l = shared_row[0];
+#pragma unroll
+            for (int k = 1; k < PARTS; ++k) l += shared_row[k * kTileRows];
+            const bool whole = x.whole;
             const size_t piece = (size_t)(2 * blockIdx.x + (ic == 0 ? 0 : 1));
-            const size_t orow = ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D;
+            const size_t orow = ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.h * p.G + g) * D;
             // what is left on O: V's power of two, the probabilities' lift where the sums do not share it
             const float back = RAW ? exp2i(ev - 127) : 1.f;
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : exp2i(-(int)kLift);
+            constexpr int EC = DP < 32 ? DP : 32;
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0u;
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t o[32];
-                const int col = half * (D / 2) + 32 * c;
-                tmem_ld32(lanes + ocol + col, o);
+            for (int c = 0; c < DP / EC; ++c) {
+                uint32_t o[EC];
+                const int col = part * DP + EC * c;
+                tmem_ld(lanes + ocol + col, o);
                 tmem_wait_ld();
                 if (valid) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < EC; ++k) {
                         float y = __uint_as_float(o[k]) * inv;
                         if (RAW) y *= back;
                         o[k] = __float_as_uint(inv != 0.f ? y : 0.f);     // (no key that the row sees: O may be anything)
@@ -1247,7 +1367,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (whole) {
                         uint16_t* dst = static_cast<uint16_t*>(p.out) + orow + col;
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
+                        for (int v = 0; v < EC / 16; ++v) {
                             uint32_t w[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
@@ -1262,24 +1382,24 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     } else {
                         uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (piece * (D / 4) + col / 4) * p.slot_rows + row;
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
+                        for (int v = 0; v < EC / 4; ++v)
                             dst[(size_t)v * p.slot_rows] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                     }
                 }
                 __syncwarp();
             }
-            if (valid && !whole && half == 0) p.part_ml[piece * p.slot_rows + row] = make_float2(m_used, l * exp2i(-(int)kLift));
+            if (valid && !whole && part == 0) p.part_ml[piece * p.slot_rows + row] = make_float2(m_used, l * exp2i(-(int)kLift));
             if (valid && *reinterpret_cast<volatile uint32_t*>(smem + L::ODD + 4 * (ic & 1)) != 0u) {
                 // the rare values that are no finite numbers, of the tokens that the row sees, on what was stored
-                const int32_t* trow = p.tables + (size_t)x.c.s * p.max_blocks;
-                for (int tok = max(x.c.q.start, x.j0 * kKeys); tok < min(x.end, x.j1 * kKeys); ++tok) {
-                    const int node = tok - x.c.q.start;
+                const int32_t* trow = p.tables + (size_t)x.s * p.max_blocks;
+                for (int tok = max(x.start, x.j0 * kKeys); tok < min(x.end(), (x.j0 + n) * kKeys); ++tok) {
+                    const int node = tok - x.start;
                     if (!(((uint32_t)__ldg(mrow + node / 32) >> (node & 31)) & 1u)) continue;
                     const int32_t blk = __ldg(trow + tok / kBlockTokens);
                     if (blk < 0 || blk >= p.num_blocks) continue;
-                    const char* rec = p.v_pool + ((size_t)blk * p.Hkv + x.c.h) * (size_t)REC;
+                    const char* rec = p.v_pool + ((size_t)blk * p.Hkv + x.h) * (size_t)REC;
 #pragma unroll 1
-                    for (int d = half * (D / 2); d < (half + 1) * (D / 2); ++d) {
+                    for (int d = part * DP; d < (part + 1) * DP; ++d) {
                         const float y = value_at<D, T>(rec, tok % kBlockTokens, d);
                         if (fabsf(y) <= FLT_MAX) continue;
                         if (whole) {
@@ -1296,27 +1416,26 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kOFree));
+        piece_done(ic);
         t0 += n;
-        walk.next(p);
-        if (walk.left <= 0) break;
-        x = piece_at(p, walk.c, walk.left);
+        if (y.n == 0) break;
+        x = y;
         if constexpr (SW == 2) publish_q(x);
         else factor = factor_next;
     }
     if (!ok) {
         // a wait gave up: the rows of this piece and of the later ones are incomplete and become NaN
         if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
-        while (walk.left > 0) {
-            x = piece_at(p, walk.c, walk.left);
-            if (tl < x.tokens) {
-                const float nan = __int_as_float(0x7fc00000);
-                if (x.j0 != 0 || x.j1 != x.c.q.tiles) {
-                    for (int k = 0; k < 2; ++k) p.part_ml[(size_t)(2 * blockIdx.x + k) * p.slot_rows + row] = make_float2(nan, nan);
-                }
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.c.h * p.G + g) * D);
-                for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        walk = *reinterpret_cast<const Walk*>(smem + L::FIRST);
+        for (int k = 0; walk.left > 0; ++k, walk.next(p)) {
+            x = walk.piece(p);
+            if (k < ic || tl >= x.tokens) continue;
+            const float nan = __int_as_float(0x7fc00000);
+            if (!x.whole) {
+                for (int i = 0; i < 2; ++i) p.part_ml[(size_t)(2 * blockIdx.x + i) * p.slot_rows + row] = make_float2(nan, nan);
             }
-            walk.next(p);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.h * p.G + g) * D);
+            for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
         }
     }
     // (no query copy may still be landing when the CTA ends)
