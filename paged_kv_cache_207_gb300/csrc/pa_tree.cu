@@ -18,7 +18,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kRows = kTreeF32Rows, kThreads = 128, kWarps = kThreads / 32, kKeys = kWarps * kBlockTokens, kMinTiles = 2;
+constexpr int kRows = kTreeF32Rows, kThreads = 128, kWarps = kThreads / 32, kKeys = kWarps * kBlockTokens;
 constexpr int f32_ctas(int D) { return D == 64 ? 3 : 2; }      // of an SM: what registers (168) and shared memory (94 KB) allow
 
 // Packed pairs of fp32: the first in the low 32 bits.
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const T
     grid_dependency_wait();
     grid_launch_dependents();
     Cursor<kKeys> cur{};
-    const Line line = tree_locate<kThreads, kKeys, kMinTiles>(
+    const Line line = tree_locate<kThreads, kKeys>(
         p, reinterpret_cast<long long*>(smem + L::SM), blockIdx.x == 0,
         [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
     const bool any = (int)blockIdx.x < line.ctas && line.total > 0;

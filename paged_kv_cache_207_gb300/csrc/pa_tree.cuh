@@ -55,7 +55,7 @@ struct TParams {
     int S, total_q, max_chunk, words;
     int Hq, Hkv, G, max_blocks, num_blocks;
     int TQ;                  // tokens of a row tile
-    int ctas;                // C, before the least number of tiles
+    int ctas;                // C, before the number of places
     float scale_log2;
 };
 
@@ -105,9 +105,11 @@ struct Line {
     long long total, base;   // base = total / ctas
     uint32_t rest;           // total % ctas
     int ctas;
-    __device__ __forceinline__ Line(long long places, long long most, int limit) {
+    // (short lines: a place to a CTA, as many as there are: a tree of 8 nodes after 600 tokens 8.9 us, with
+    // three places to a CTA 10.9)
+    __device__ __forceinline__ Line(long long places, int limit) {
         total = places;
-        ctas = most < 1 ? 1 : most < limit ? (int)most : limit;
+        ctas = places < 1 ? 1 : places < limit ? (int)places : limit;
         // (a division of 64 bits takes as long as a trip to L2)
         if (places < 1ll << 32) {
             base = (uint32_t)places / (uint32_t)ctas;
@@ -122,7 +124,7 @@ struct Line {
 
 // The line, and the cursor of place `begin_of(line)` in it where there is one (begin >= 0 and below
 // the total), found by all NT threads.  `sm`: NT / 32 + 6 words of 64 bits.
-template <int NT, int KT, int MIN_TILES, typename Begin>
+template <int NT, int KT, typename Begin>
 __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, bool report, Begin begin_of, Cursor<KT>& cur) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (p.S + NT - 1) / NT, s0 = min(tid * each, p.S), s1 = min(s0 + each, p.S);
@@ -148,7 +150,7 @@ __device__ __forceinline__ Line tree_locate(const TParams& p, long long* sm, boo
         before += w < warp ? u : 0;
         total += u;
     }
-    const Line line(total, (total + MIN_TILES - 1) / MIN_TILES, p.ctas);
+    const Line line(total, p.ctas);
     const long long begin = begin_of(line);
     long long at = before + incl - mine;
     if (begin >= at && begin < at + mine) {

@@ -46,7 +46,6 @@ namespace {
 constexpr uint64_t kWaitNs = 200000000ull;
 constexpr int kTileRows = 128;
 constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
-constexpr int kMinTiles = 3;             // places of a CTA, at least
 constexpr int kPieces = 4;                // records of pieces
 constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at most
 
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     if (threadIdx.x == 0 && p.err) flag = *reinterpret_cast<const volatile int32_t*>(p.err);
     Walk walk;
     {
-        const Line line = tree_locate<W::THREADS, kKeys, kMinTiles>(
+        const Line line = tree_locate<W::THREADS, kKeys>(
             p, reinterpret_cast<long long*>(smem + L::Q), blockIdx.x == 0,
             [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, walk.c);
         const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
