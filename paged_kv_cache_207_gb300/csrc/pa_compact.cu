@@ -14,6 +14,7 @@
 // 8- and 4-bit values, transposed in their tiles) have one writer.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_compact.h"
 #include "pa_flags.cuh"
@@ -26,7 +27,10 @@ namespace {
 constexpr int kCompactThreads = 256;
 constexpr int kBatchBlocks = 64, kBatchRows = kBatchBlocks * kBlockTokens;   // whose places are looked up together
 constexpr int kUnits = 2, kDepth = 2;      // 16-byte pieces of a thread's chunk, and chunks under way
-constexpr int kSmCtas = 5;                 // CTAs of an SM, which bound the registers
+// CTAs of an SM, which bound the registers: 48, or 64 where units of several slots are put together
+// (16 windows of 4100 FP8 tokens, 8 heads: 140 us, with five CTAs 160; 64 gathers of bf16 rows, 2 heads: 10.7 with
+// five, 11.9 with four).
+constexpr int sm_ctas(bool mix) { return mix ? 4 : 5; }
 
 struct KParams {
     char* k_pool;
@@ -70,22 +74,76 @@ template <pa_dtype T, int D>
 __device__ __forceinline__ uint32_t mixed_at(int u, int i) {       // byte offset of word i
     return T == PA_FP8_E4M3 ? u * 16 + i * 4 : ((4 * (u / (D / 16)) + i) * (D / 16) + u % (D / 16)) * 4;
 }
-// What slot `slot` of a unit holds, at the place of slot t (compile-time) of its word t / 4 (FP8) or t / 2 % 4.
 template <pa_dtype T, int D>
-__device__ __forceinline__ uint32_t load_slot(const char* tile, int u, int slot) {
-    if constexpr (T == PA_FP8_E4M3) return *reinterpret_cast<const uint8_t*>(tile + u * 16 + slot);
-    // bytes (dh, half) of word c hold slots 2 c + 8 half, + 1: the two dims' nibbles of a slot
-    else return (*reinterpret_cast<const uint32_t*>(tile + mixed_at<T, D>(u, (slot >> 1) & 3)) >> (8 * (slot >> 3) + 4 * (slot & 1))) & 0x000f000fu;
+__device__ __forceinline__ Mixed load_mixed(const char* tile, int u) {
+    Mixed x;
+    if constexpr (T == PA_FP8_E4M3) {
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + u * 16);
+        x = Mixed{{v.x, v.y, v.z, v.w}};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.w[i] = *reinterpret_cast<const uint32_t*>(tile + mixed_at<T, D>(u, i));
+    }
+    return x;
 }
+template <pa_dtype T, int D>
+__device__ __forceinline__ void store_mixed(char* tile, int u, const Mixed& x) {
+    if constexpr (T == PA_FP8_E4M3)
+        *reinterpret_cast<uint4*>(tile + u * 16) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(tile + mixed_at<T, D>(u, i)) = x.w[i];
+}
+// Slot t (compile-time) of x becomes slot `slot` (the same in the warp, as a rule) of y.
 template <pa_dtype T>
-__device__ __forceinline__ void put_slot(Mixed& x, int t, uint32_t v, bool moved) {
-    const int i = T == PA_FP8_E4M3 ? t >> 2 : (t >> 1) & 3, sh = T == PA_FP8_E4M3 ? 8 * (t & 3) : 8 * (t >> 3) + 4 * (t & 1);
-    const uint32_t m = (T == PA_FP8_E4M3 ? 0xffu : 0x000f000fu) << sh;
-    if (moved) x.w[i] = (x.w[i] & ~m) | v << sh;
+__device__ __forceinline__ void move_slot(Mixed& x, int t, const Mixed& y, int slot) {
+    const int i = T == PA_FP8_E4M3 ? slot >> 2 : (slot >> 1) & 3;
+    const uint32_t w = i & 2 ? (i & 1 ? y.w[3] : y.w[2]) : (i & 1 ? y.w[1] : y.w[0]);
+    if constexpr (T == PA_FP8_E4M3) {
+        const int sh = 4 * (t & 3);
+        x.w[t >> 2] = __byte_perm(x.w[t >> 2], w, (0x3210u & ~(0xfu << sh)) | (4u + (slot & 3)) << sh);
+    } else {
+        // bytes (dh, half) of word c hold slots 2 c + 8 half, + 1: the two dims' nibbles of a slot
+        const int sh = 8 * (t >> 3) + 4 * (t & 1);
+        const uint32_t v = (w >> (8 * (slot >> 3) + 4 * (slot & 1))) & 0x000f000fu;
+        x.w[(t >> 1) & 3] = (x.w[(t >> 1) & 3] & ~(0x000f000fu << sh)) | v << sh;
+    }
+}
+// Units u of a destination's tile from the rows f, and which of its slots move.  A source's tile
+// is read as whole units, once for the rows in turn that come from it: rows mostly lie in few blocks.
+template <pa_dtype T, int D, int NU>
+__device__ __forceinline__ uint32_t gather_mixed(const char* pool, const From* f, const char* dst, const int (&u)[NU], Mixed (&got)[NU]) {
+    Mixed have[NU];
+    From at = -1;
+    uint32_t moved = 0u;
+#pragma unroll
+    for (int t = 0; t < kBlockTokens; ++t) {
+        const From x = f[t];
+        if (x < 0) continue;
+        if ((x & ~(From)(kBlockTokens - 1)) != at) {
+            at = x & ~(From)(kBlockTokens - 1);
+#pragma unroll
+            for (int k = 0; k < NU; ++k) have[k] = load_mixed<T, D>(pool + at, u[k]);
+        }
+        moved |= 1u << t;
+#pragma unroll
+        for (int k = 0; k < NU; ++k) move_slot<T>(got[k], t, have[k], slot_of(x));
+    }
+    if (moved != 0u && moved != 0xffffu) {
+#pragma unroll
+        for (int k = 0; k < NU; ++k) have[k] = load_mixed<T, D>(dst, u[k]);
+#pragma unroll
+        for (int t = 0; t < kBlockTokens; ++t)
+            if (!((moved >> t) & 1u)) {
+#pragma unroll
+                for (int k = 0; k < NU; ++k) move_slot<T>(got[k], t, have[k], t);
+            }
+    }
+    return moved;
 }
 
 template <pa_dtype T, int D>
-__global__ void __launch_bounds__(kCompactThreads, kSmCtas) compact_kernel(const KParams p) {
+__global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MIX)) compact_kernel(const KParams p) {
     using G = Tile<T, D>;
     __shared__ From from[kBatchRows];
     __shared__ int64_t to[kBatchBlocks];      // byte offsets of the destination's tiles, -1: none
@@ -188,39 +246,28 @@ __global__ void __launch_bounds__(kCompactThreads, kSmCtas) compact_kernel(const
                 }
             }
         } else {
-            // units that hold all slots of a block: gathered slot by slot, sixteen small loads under way
-            const int per = G::MIXED >> p.slice_bits, u0 = slice * per, units = blocks * per;
-            for (int at = 0; at < units; at += kCompactThreads) {
-                const int i = at + tid, b = i < units ? i / per : 0, u = u0 + i % per;
-                const From* f = from + b * kBlockTokens;
-                Mixed got{};
-                uint32_t moved = 0u;
-                if (i < units && to[b] >= 0) {
-                    uint32_t v[kBlockTokens];
+            // units that hold all slots of a block, of a slice's where they are many two to a thread
+            const int per = G::MIXED >> p.slice_bits;
+            auto run = [&](auto number) {
+                constexpr int NU = decltype(number)::value;
+                const int groups = per / NU, units = blocks * groups;
+                for (int at = 0; at < units; at += kCompactThreads) {
+                    const int i = at + tid, b = i < units ? i / groups : 0, j = i % groups;
+                    int u[NU];
 #pragma unroll
-                    for (int t = 0; t < kBlockTokens; ++t) {
-                        v[t] = 0u;
-                        if (f[t] >= 0) {
-                            v[t] = load_slot<T, D>(source(f[t]), u, slot_of(f[t]));
-                            moved |= 1u << t;
-                        }
+                    for (int k = 0; k < NU; ++k) u[k] = slice * per + (NU == 1 ? j : (j / 32 * NU + k) * 32 + j % 32);
+                    Mixed got[NU] = {};
+                    uint32_t moved = 0u;
+                    if (i < units && to[b] >= 0) moved = gather_mixed<T, D>(pool, from + b * kBlockTokens, pool + to[b], u, got);
+                    if (p.in_place) __syncthreads();
+                    if (moved != 0u) {
+#pragma unroll
+                        for (int k = 0; k < NU; ++k) store_mixed<T, D>(pool + to[b], u[k], got[k]);
                     }
-                    if (moved != 0u && moved != 0xffffu)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) got.w[w] = *reinterpret_cast<const uint32_t*>(pool + to[b] + mixed_at<T, D>(u, w));
-#pragma unroll
-                    for (int t = 0; t < kBlockTokens; ++t) put_slot<T>(got, t, v[t], (moved >> t) & 1u);
                 }
-                if (p.in_place) __syncthreads();
-                if (moved != 0u) {
-                    char* dst = pool + to[b];
-                    if constexpr (T == PA_FP8_E4M3)
-                        *reinterpret_cast<uint4*>(dst + u * 16) = make_uint4(got.w[0], got.w[1], got.w[2], got.w[3]);
-                    else
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) *reinterpret_cast<uint32_t*>(dst + mixed_at<T, D>(u, w)) = got.w[w];
-                }
-            }
+            };
+            if (per % 64 == 0) run(std::integral_constant<int, 2>{});
+            else run(std::integral_constant<int, 1>{});
         }
         if constexpr (G::SCALE > 0) {
             if (slice == 0) {
@@ -254,7 +301,7 @@ cudaError_t launch(KParams p, int num_seqs, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // CTAs for the whole GPU: in place by shares of the tiles, else by shares of the rows
-    const long long pairs = 2ll * p.Hkv * num_seqs, room = (long long)kSmCtas * sms;
+    const long long pairs = 2ll * p.Hkv * num_seqs, room = (long long)sm_ctas(G::VALUES_MIX) * sms;
     p.slice_bits = 0;
     p.segs = 1;
     if (p.in_place) {
