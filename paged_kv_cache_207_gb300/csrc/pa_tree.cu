@@ -4,10 +4,17 @@
 // start_pos[s] and those nodes j, at positions start_pos[s] + j, whose bit its mask row sets:
 //   out = sum_t softmax_t(scale <q, K[t][g]>) V[t][g] over the visible t,  g = h / G.
 //
-// One pass over the keys with a running maximum and sum (f32).  A CTA keeps 32 query rows of one kv
-// head (tokens x G) in shared memory and goes through key tiles of 64 tokens: scores by register
-// tiles of 4 rows x 4 keys, the probabilities through shared memory, outputs by register tiles of
-// 4 rows x D / 16 dims, all in packed pairs of fp32 FMAs.
+// One pass over the keys with running maxima and sums (f32).  A CTA keeps up to 32 query rows of one kv
+// head (tokens x G) in shared memory; a warp takes every fourth block of 16 keys with maxima, sums and
+// outputs of its own, which the CTA joins at a piece's end: no barrier between blocks, and each
+// warp copies its own, the next block's keys under the products with the values, a block's values under its
+// scores.  Scores are register tiles of up to 4 rows by 4 keys, outputs of up to 4 rows by D / 4 dims,
+// rows in steps of eight (a piece of 8 rows costs a quarter of one of 32).
+//
+// Where it is bound: by the FMA units once 32 rows share the keys (32 sequences of 2048 tokens, 32 / 8
+// heads of 128, 8 nodes: 238 us, 36 of 74 TFLOP/s; packed pairs of fp32 FMAs, whose six operands come
+// from the registers at half the pace, 320 us; four warps on one tile of 64 keys with barriers between, 366),
+// else by latency: 8 sequences of 20 to 1000 tokens, 12 heads of 64, up to 21 nodes, 20 us.
 #include <algorithm>
 #include <cfloat>
 
@@ -21,24 +28,9 @@ namespace {
 constexpr int kRows = kTreeF32Rows, kThreads = 128, kWarps = kThreads / 32, kKeys = kWarps * kBlockTokens;
 constexpr int f32_ctas(int D) { return D == 64 ? 3 : 2; }      // of an SM: what registers (168) and shared memory (94 KB) allow
 
-// Packed pairs of fp32: the first in the low 32 bits.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-    return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-}
-__device__ __forceinline__ float pair_lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float pair_hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-struct Quad { uint64_t a, b; };
-__device__ __forceinline__ Quad quad_at(const float* p) {
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
-    return Quad{v.x, v.y};
+__device__ __forceinline__ float4 quad_at(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void fma4(float4& acc, float a, const float4& b) {
+    acc = make_float4(fmaf(a, b.x, acc.x), fmaf(a, b.y, acc.y), fmaf(a, b.z, acc.z), fmaf(a, b.w, acc.w));
 }
 
 template <int D>
@@ -116,13 +108,13 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
         mrow[r] = row < rows ? p.mask + (size_t)(qrow + row / p.G) * p.words : nullptr;
     }
     float m[NR], l[NR];
-    uint64_t o[NR][2 * NX];
+    float4 o[NR][NX];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2 * NX; ++x) o[r][x] = 0ull;
+        for (int x = 0; x < NX; ++x) o[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int j = j0; j < j1; ++j) {
         const int tok0 = j * kKeys + warp * kBlockTokens, node0 = tok0 - cur.q.start, left = end - tok0;
@@ -150,11 +142,11 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
         }
         cp_async_wait<1>();
         __syncwarp();                                     // (the keys)
-        // scores of rows ty + 8 r and keys tx + 4 i, in pairs of dims
-        uint64_t s2[NR][4] = {};
-#pragma unroll 2
+        // scores of rows ty + 8 r and keys tx + 4 i
+        float s[4][4] = {};
+#pragma unroll 4
         for (int d4 = 0; d4 < D / 4; ++d4) {
-            Quad q[NR], k[4];
+            float4 q[NR], k[4];
 #pragma unroll
             for (int r = 0; r < NR; ++r) q[r] = quad_at(sQ + (d4 * kRows + ty + 8 * r) * 4);
 #pragma unroll
@@ -162,21 +154,18 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
 #pragma unroll
             for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    fma2(s2[r][i], q[r].a, k[i].a);
-                    fma2(s2[r][i], q[r].b, k[i].b);
-                }
+                for (int i = 0; i < 4; ++i)
+                    s[r][i] = fmaf(q[r].w, k[i].w, fmaf(q[r].z, k[i].z, fmaf(q[r].y, k[i].y, fmaf(q[r].x, k[i].x, s[r][i]))));
         }
         __syncwarp();                                     // (the keys are read)
         copy(j + 1, blk, p.k_pool, sK);
         // hidden keys score -inf (a select: they may hold anything)
-        float s[4][4] = {};
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[r][i] = (see[r] >> (tx + 4 * i)) & 1u ? (pair_lo(s2[r][i]) + pair_hi(s2[r][i])) * p.scale_log2 : -INFINITY;
+                s[r][i] = (see[r] >> (tx + 4 * i)) & 1u ? s[r][i] * p.scale_log2 : -INFINITY;
                 top = fmaxf(top, s[r][i]);
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -191,9 +180,8 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
                 l[r] += s[r][i];
             }
             if (al != 1.f) {
-                const uint64_t a2 = pair_of(al, al);
 #pragma unroll
-                for (int x = 0; x < 2 * NX; ++x) o[r][x] = mul2(o[r][x], a2);
+                for (int x = 0; x < NX; ++x) o[r][x] = make_float4(o[r][x].x * al, o[r][x].y * al, o[r][x].z * al, o[r][x].w * al);
             }
         }
 #pragma unroll
@@ -212,19 +200,17 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
             }
             odd = __any_sync(0xffffffffu, odd && node0 + slot >= 0);
         }
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < kBlockTokens; ++k) {
             const float4 pr = *reinterpret_cast<const float4*>(sP + (k * 8 + ty) * 4);
             const float pv[4] = {pr.x, pr.y, pr.z, pr.w};
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
-                const Quad v = quad_at(sV + ((tx + 4 * x) * L::KS + k) * 4);
+                const float4 v = quad_at(sV + ((tx + 4 * x) * L::KS + k) * 4);
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     if (odd && pv[r] == 0.f) continue;
-                    const uint64_t w = pair_of(pv[r], pv[r]);
-                    fma2(o[r][2 * x], w, v.a);
-                    fma2(o[r][2 * x + 1], w, v.b);
+                    fma4(o[r][x], pv[r], v);
                 }
             }
         }
@@ -241,7 +227,7 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
         if (tx == 0) sML[warp * kRows + row] = make_float2(m[r], l[r]);
 #pragma unroll
         for (int x = 0; x < NX; ++x)
-            *reinterpret_cast<ulonglong2*>(sK + (row * L::OS + tx + 4 * x) * 4) = make_ulonglong2(o[r][2 * x], o[r][2 * x + 1]);
+            *reinterpret_cast<float4*>(sK + (row * L::OS + tx + 4 * x) * 4) = o[r][x];
     }
     __syncthreads();
     const bool whole = j0 == 0 && j1 == cur.q.tiles;
