@@ -3,8 +3,8 @@
 // An item is (sequence, kv head, row tile): ROWS query rows at most of one kv head, whole tokens,
 // against all keys of the sequence, cut into key tiles.  The items, in the order of the sequences,
 // then heads, then row tiles, form one line, each item_cost() places (what its beginning and end cost,
-// in tiles: 64 sequences of 400 to 7800 tokens, 32 / 8 heads, 32 nodes, 244 us without) and one for every
-// tile, and CTA c of C takes the places c T / C .. (c + 1) T / C - 1 of its T: contexts may be as uneven
+// in tiles: 64 sequences of 400 to 7800 tokens, 32 / 8 heads, 32 nodes, 244 us without, 179 with four) and one
+// for every tile, and CTA c of C takes the places c T / C .. (c + 1) T / C - 1 of its T: contexts may be as uneven
 // as they like, every CTA has the same work, and no lengths are needed on the host.  A CTA's run of
 // tiles of one item is a piece.  A piece that
 // is a whole item gives its outputs; others leave partial results (sums, maxima, unnormalised
@@ -264,10 +264,10 @@ __device__ __forceinline__ void say_joint(const TParams& p, const Line& line, co
 
 // Joins the partial results of the items that CTA boundaries cut.  Block b takes the item that CTA
 // b + 1 tells of, blockIdx.y eight of its rows: a thread four dims of a row, over the parts in their
-// order with a running maximum, eight parts' loads under way together.
+// order with a running maximum, B parts' loads under way together (which is what registers go to).
 constexpr int kMergeRows = 8;
-template <int D, typename Out>
-__global__ void __launch_bounds__(2 * D) tree_merge_kernel(const TParams p) {
+template <int D, typename Out, int B>
+__global__ void __launch_bounds__(2 * D, (B == 8 ? 768 : 1536) / (2 * D)) tree_merge_kernel(const TParams p) {
     const int c = blockIdx.x + 1, unit = threadIdx.x / kMergeRows;
     const int r = blockIdx.y * kMergeRows + threadIdx.x % kMergeRows;
     grid_dependency_wait();
@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(2 * D) tree_merge_kernel(const TParams p) {
     if (r >= x.rows || tree_aborted(p.err)) return;                       // (rows: 0 where nothing is to be joined)
     // part i: piece 2 (c - 1 + i), the first one perhaps the piece after it
     auto slot = [&](int i) { return (size_t)(2 * (c - 1 + i) + (i == 0 ? x.late : 0)); };
-    constexpr int B = 8;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < x.count; i0 += B) {
@@ -344,7 +343,12 @@ template <int D, typename Out>
 cudaError_t launch_merge(const TParams& p, cudaStream_t stream) {
     if (p.ctas == 1) return cudaSuccess;
     const dim3 grid(p.ctas - 1, (p.slot_rows + kMergeRows - 1) / kMergeRows);
-    return tree_launch(tree_merge_kernel<D, Out>, grid, 2 * D, 0, stream, p);
+    // Two parts at a time and six blocks an SM where an item has few parts (at least a third as many items
+    // as CTAs), else eight and three: 16 sequences of 2500 tokens, 64 nodes, 53.3 us, with eight 60.0; one of
+    // 32768, two kv heads, 8 nodes, 18.9 us, with two 28.3.
+    const long long items = (long long)p.S * p.Hkv * ((p.max_chunk + p.TQ - 1) / p.TQ);
+    return 3 * items >= p.ctas ? tree_launch(tree_merge_kernel<D, Out, 2>, grid, 2 * D, 0, stream, p)
+                               : tree_launch(tree_merge_kernel<D, Out, 8>, grid, 2 * D, 0, stream, p);
 }
 
 }  // namespace
