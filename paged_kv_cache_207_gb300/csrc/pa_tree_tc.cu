@@ -6,28 +6,40 @@
 //   S = Q K^T   into TMEM (one M128 N128 K16 MMA per 16 dims),
 //   O += P V    into TMEM (one M128 N=D K16 MMA per block, P from TMEM over S's columns),
 // with a running maximum per row that is raised only when a tile passes it by more than 2^8 (O is then
-// rescaled), one row per softmax thread.  Warps have roles: softmax (four per row tile), copies, the
-// issue of all MMAs; a piece's first copies and scores run while the piece before it ends.  Keys before
-// the tree take no mask; in the tree's own tiles a row's visible keys are its mask words, shifted to the
-// tile, two instructions per score.
+// rescaled).  A row belongs to two softmax threads (FP8: four) in warps of their own, each with a part of
+// its columns.  Other warps make the bulk copies, issue all MMAs, copy K's pieces (bf16) or convert; a
+// piece's first copies and scores run while the piece before it ends.  Keys before the tree take no mask;
+// in the tree's own tiles a row's visible keys are its mask words, shifted to the tile, two instructions
+// per score.
 //
-// Where it is bound: a row tile costs a tile of keys 128 exponentials per row and 2 x 128 x 128 x D
-// multiplications whatever its number of rows, less time than the tile's bytes take from HBM, so up
-// to 128 rows (bf16: 256) the keys' bytes are the bound.
+// Where it is bound.  bf16 to 128 rows: by the keys' bytes (64 sequences of 4096 tokens, 32 / 8 heads of
+// 128: 1 node 166 us, 6.5 TB/s, 32 nodes 178).  bf16 with 256 rows: a key tile's MMAs take 1.5 us of the
+// 2.0 that pass (64 nodes 227 us): scores of one row tile wait for its products with the values, as the TMEM
+// holds one S tile per row tile.  FP8 (8 nodes 164, 32 nodes 171; four sequences of 80000: 182) and FP4 (191,
+// 200): 1.4 and 1.7 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
+// agreement, exponentials, publication), takes beside the conversions on the same issue slots; without
+// conversions 1.25, with the copies alone 1.05.
 //
 // bf16: K and V tiles come as they are (V's blocks by bulk copies; K's 16-byte pieces each to a
 // place of their own, so that the tile is one operand of 128 rows).
 //
-// FP8 and FP4: the records come by bulk copies and eight warps, one per block of the tile, write K
-// and V as f16 operands.  f16 holds every code exactly.  An FP4 scale is a power of two and is
-// folded in exactly; an FP8 scale is rounded to f16, and its product with a code again, each by
-// 2^-11 of the value, an eighth of what bf16 probabilities would lose: to keep FP8's scales
-// apart would cost the softmax, which is as long as the copies, two more operations per score.  A tile's K carries the power
+// FP8: a record's keys are an E4M3 operand as they are stored, and a query row, eight significant bits,
+// is the sum of two E4M3 numbers, exactly, but for elements below 2^-10 of the row's largest, which are off by 2^-17 of
+// that at most: S takes two E4M3 MMAs for each one of 16-bit types, at twice the rate, nothing is converted, and a score
+// is multiplied by its key's scale (against keys written as f16 operands: 187 us instead of 201 for four sequences of
+// 30000 to 131000).  Probabilities do not fit E4M3 (flat rows of 10^5 keys lie below its range), so values are
+// converted as FP4's are.
+//
+// FP4, and FP8's values: the records come by bulk copies and eight warps, one per block of the tile, write
+// f16 operands (FP4: eight for K and eight for V).  f16 holds every code exactly.  An FP4 scale is a power
+// of two and is folded in exactly; an FP8 scale is rounded to f16, and its product with a code again, each
+// by 2^-11 of the value, an eighth of what bf16 probabilities would lose: to keep the scales of values
+// apart would cost the softmax a product per probability.  An FP4 tile's K carries the power
 // of two that puts its largest scale at 1 .. 2; the tile's scores take it back.  V's power of two is
 // the piece's first tile's and changes, O with it, only when a tile's scales pass it by 2^6.
 // Probabilities are taken times 2^7, at most 2^15, so that one below f16's normal range is off by at most 2^-32 of
-// a weight of 1.  Query rows become f16 times a power of two of their own, their largest element
-// at 2^4 .. 2^5, and the row's scores give it back.
+// a weight of 1.  FP4's query rows become f16 times a power of two of their own, their largest element
+// at 2^4 .. 2^5 (FP8: at 2^7 .. 2^8), and the row's scores give it back.
 //
 // Values of the tree's own tokens that are no finite numbers become zeros for the MMA (0 times an
 // infinity would reach the rows that do not see the token); the rows that see them add them at the end.
@@ -49,10 +61,12 @@ constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
 constexpr int kPieces = 4;                // records of pieces
 constexpr float kRaise = 8.f;            // (log2) that a row's maximum lags at most
 
-// Warps: softmax 0 .. 8 SW - 1, the copies (bf16: V's; else all records), the MMAs, then K's copies
-// (bf16) or the conversions.  All have the registers of a launch of so many threads (128, 96 or 72: what
-// setmaxnreg hands from role to role the compiler does not count on), so the softmax takes a row in
-// pieces of 32 columns, from the TMEM once for the maximum and again for the probabilities.
+// Warps: the softmax, the copies (bf16: V's; else all records), the MMAs, then K's copies (bf16) or the
+// conversions.  All have the registers of a launch of so many threads (128, 96 or 72: what setmaxnreg
+// hands from role to role the compiler does not count on), so the softmax takes a row in pieces of 32
+// columns: with two threads to a row from the TMEM once for the maximum and again for the
+// probabilities, with four (FP8: 164 us instead of 183 for 64 sequences of 4096 tokens, 8 nodes) kept between.
+// Four are too many warps beside FP4's conversions and two row tiles, and bf16 loses 1% to 2%.
 template <pa_dtype T, int SW>
 struct Roles {
     static constexpr int PARTS = T == PA_FP8_E4M3 ? 4 : 2;       // warps that share 32 rows
@@ -89,7 +103,7 @@ struct Layout {
     static constexpr int SLOT = BAR + NBAR * 8;       // TMEM address
     static constexpr int ODD = SLOT + 16;             // [2] of a piece: values that are no finite numbers
     static constexpr int EXPS = ODD + 16;             // [8] (K, V) exponents of a tile, as the conversions leave them
-    // as the MMA warp passes them on: FP4: [8]; FP8: [S tile][the columns' scales, V's exponent]
+    // as the MMA warp passes them on: FP4: [8]; FP8: [S tile][the columns' scales, the exponents]
     static constexpr int PASS = kKeys * 4 + 16;
     static constexpr int PASSED = EXPS + 64;
     static constexpr int SEEN = PASSED + (NAT ? 2 * PASS : 64);      // [8][8] a tile's block has such values
@@ -720,12 +734,17 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 }
                 __syncwarp();
                 if constexpr (NAT) {
-                    // the columns' scales in their order: a lane has four slots of a block
-                    const uint32_t to = sbase + L::PASSED + buf * L::PASS;
-                    const uint4 sk = ld_shared_v4(sbase + L::K + (t % KST) * KSTAGE + (lane >> 2) * REC + 16 * D + (lane & 3) * 16);
-                    st_shared_v4(to + ((lane >> 1) & 1) * 256 + (lane >> 2) * 32 + (lane & 1) * 16, sk);
+                    // the columns' scales in their order, against the largest's power of two (so that no score
+                    // overflows that does not with the row's factor): a lane has four slots of a block
+                    const uint32_t to = sbase + L::PASSED + buf * L::PASS, at = sbase + L::K + (t % KST) * KSTAGE;
+                    const int ek = Convert<D, T>::exponent(at, REC, x.end() - (x.j0 + i) * kKeys, lane);
+                    const uint4 sk = ld_shared_v4(at + (lane >> 2) * REC + 16 * D + (lane & 3) * 16);
+                    const float f = exp2i(127 - ek);
+                    st_shared_v4(to + ((lane >> 1) & 1) * 256 + (lane >> 2) * 32 + (lane & 1) * 16,
+                                 make_uint4(__float_as_uint(__uint_as_float(sk.x) * f), __float_as_uint(__uint_as_float(sk.y) * f),
+                                            __float_as_uint(__uint_as_float(sk.z) * f), __float_as_uint(__uint_as_float(sk.w) * f)));
                     ok = warp_wait(bar(kEFull + (t & 3)), (t >> 2) & 1);
-                    if (lane == 0) st_shared_v2(to + kKeys * 4, ld_shared_v2(sbase + L::EXPS + 8 * (t & 7)));
+                    if (lane == 0) st_shared_v2(to + kKeys * 4, make_uint2((uint32_t)ek, ld_shared_u32(sbase + L::EXPS + 8 * (t & 7) + 4)));
                     __syncwarp();
                     if (elect_one()) mbar_arrive(bar(kSFull + buf));
                     __syncwarp();
@@ -797,13 +816,15 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                                             : umma_desc(sbase + L::V + st * KTILE, 128, 256);
                     const uint32_t more = i > 0 ? 1u : 0u;
                     constexpr int PB = kKeyBlocks / W::PARTS;           // each part of the rows' threads begins at its own columns
+                    auto pv = [&](int b) {
+                        umma_ts(ocol, pcol + kKeys / W::PARTS * (b / PB) + 8 * (b % PB), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                    };
                     if (nb == kKeyBlocks) {
 #pragma unroll
-                        for (int b = 0; b < kKeyBlocks; ++b)
-                            umma_ts(ocol, pcol + kKeys / W::PARTS * (b / PB) + 8 * (b % PB), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                        for (int b = 0; b < kKeyBlocks; ++b) pv(b);
                     } else {
                         for (int b = 0; b < kKeyBlocks; ++b)
-                            if ((NAT ? 2 * (b % 4) : b) < nb) umma_ts(ocol, pcol + kKeys / W::PARTS * (b / PB) + 8 * (b % PB), vd + (uint64_t)((b * TILE) >> 4), idO, b > 0 ? 1u : more);
+                            if ((NAT ? 2 * (b % 4) : b) < nb) pv(b);
                     }
                     if (hh == SW - 1) umma_commit(bar(kVEmpty + st));
                     if (SW == 1) umma_commit(bar(kPVDone));
@@ -1024,10 +1045,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         }
     }
     } else {
-    // ---------------------------------------------------------------- softmax, a row per pair of threads
-    // Warps w and w + 4 of a row tile's eight reach the TMEM lanes 32 (w % 4) .. and share its rows: the
-    // first takes the tile's keys 0 .. 63, the second 64 .. 127 (half the code and the wait of a warp
-    // that takes them all).  They agree on the row's maximum through shared memory where it rises.
+    // ---------------------------------------------------------------- softmax, a row to PARTS threads
+    // Warps w, w + 4, .. of a row tile's reach the TMEM lanes 32 (w % 4) .. and share its rows, each with
+    // its part of the tile's columns (less code and waiting than a warp that takes them all).  They agree
+    // on the row's maximum through shared memory where it rises.
     constexpr int PARTS = W::PARTS, COLS = kKeys / PARTS, NC = COLS / 32, DP = D / PARTS;
     const int quarter = warp & 3, part = (warp >> 2) % PARTS, h = warp / (4 * PARTS);
     const int lr = quarter * 32 + lane, row = h * kTileRows + lr;
@@ -1046,7 +1067,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         return static_cast<const uint16_t*>(p.q) + ((size_t)(x.qrow + token) * p.Hq + (size_t)x.h * p.G + head) * D;
     };
     uint32_t tmem = 0u;
-    float factor = scale;                                             // of the row's scores
+    int shift = 0;                                                    // (log2) of what the row of q carries
     // One row tile: the rows of the warps come to shared memory by whole rows (a thread that loads its
     // own row touches 32 lines at a time: 12000 clocks a piece), 16-byte piece u of row r at place u ^ r % 8,
     // and each goes through registers into the TMEM, columns of the piece's parity, a part of them by
@@ -1063,8 +1084,9 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         }
         cp_async_commit();
     };
-    auto put_q = [&](const Piece& x, int ic) -> float {
-        float f = 1.f, f_out = scale;
+    auto put_q = [&](const Piece& x, int ic) -> int {
+        float f = 1.f;
+        int shift = 0;
         cp_async_wait<0>();
         if (busy(x)) {
             named_bar_sync(row_bar, 32 * PARTS);                      // (the rows)
@@ -1082,9 +1104,9 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 top = tops[0];
 #pragma unroll
                 for (int k = 1; k < PARTS; ++k) top = max(top, tops[k * kTileRows]);
-                const int shift = min((NAT ? 134 : 131) - (int)(top >> 7), 110);     // (2^110 makes bf16's smallest an f16)
+                // (E4M3's smallest step is 2^-9, f16's 2^-24: bf16's smallest number times 2^125 or 2^110 is one still)
+                shift = NAT ? min(134 - (int)(top >> 7), 125) : min(131 - (int)(top >> 7), 110);
                 f = exp2i(shift);
-                f_out = scale * exp2i(-shift);
             }
             constexpr int NW = DP < 32 ? DP / 2 : 16;                 // words of two dims at a time
 #pragma unroll 1
@@ -1123,7 +1145,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQFull + (ic & 1)));
-        return f_out;
+        return shift;
     };
     // Two: as operands, eight rows' 16-byte pieces side by side, and published later by the threads that
     // loaded them: lanes are 8 rows by 4 pieces.
@@ -1166,7 +1188,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     const uint32_t ocol = kColO + (uint32_t)(h * kKeys);
     constexpr float kLift = RAW ? 7.f : 0.f;                          // (log2) on the probabilities
     if constexpr (SW == 2) publish_q(x);
-    else factor = put_q(x, 0);
+    else shift = put_q(x, 0);
     int t0 = 0, ic = 0;
     for (; ok; ++ic) {
         const int n = x.n, rows = x.tokens * p.G;
@@ -1176,158 +1198,161 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         ok = piece(ic + 1, y);
         if (!ok) break;
         if (SW == 1 && y.n > 0) stage_q(y);
-        float m_used = -INFINITY, l = 0.f, factor_next = scale;
+        float m_used = -INFINITY, l = 0.f;
+        int shift_next = 0;
         int ev = 0;
         // the row tile's warps without rows do not go through the keys: its first one arrives for them
         const int with_rows = PARTS * max(0, min(4, (rows - h * kTileRows + 31) / 32));
         const bool leads = warp % (4 * PARTS) == 0, runs = live || leads;
         const uint32_t arrivals = leads ? 4 * PARTS - with_rows + (with_rows > 0 ? 1 : 0) : 1;
-        // (the first tile by itself: the next piece's queries then follow outside the loop, which stays short)
+        // The first tile by itself: the next piece's queries then follow outside the loop, which stays short
+        // (with them in it, the instructions come too slowly: 64 ragged FP8 sequences of 4096 tokens, 32 nodes,
+        // 189 us instead of 180; for the same reason a wait that does not end at once is a function, FP4 215 to 199).
         for (int lo = 0; ok && lo < n;) {
-        const int hi = SW == 1 && lo == 0 ? 1 : n;
+            const int hi = SW == 1 && lo == 0 ? 1 : n;
 #pragma unroll 1
-        for (int i = lo; runs && i < hi; ++i) {
-            const int t = t0 + i, sb = SW == 2 ? h : t & 1;
-            const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
-            // The first key as a node, of this thread's; FP8, whose columns are every other eight, of the tile's 128.
-            const int first = (x.j0 + i) * kKeys + (NAT ? 0 : COLS * part) - x.start;
-            // the visible keys of 32 columns are the bits of a word: the context's, then the row's mask
-            uint32_t see[NC];
-            const bool full = first + (NAT ? kKeys : COLS) <= 0;
-            if (live && !full) {
-                auto word = [&](int node) -> uint32_t {
-                    const int left = x.nodes - node;
-                    uint32_t v = 0u;
-                    if (node < 0) {
-                        v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
-                    } else if (left > 0) {
-                        const uint32_t lo = (uint32_t)__ldg(mrow + node / 32);
-                        const uint32_t hi = (node & 31) != 0 && node / 32 + 1 < p.words ? (uint32_t)__ldg(mrow + node / 32 + 1) : 0u;
-                        v = __funnelshift_r(lo, hi, node & 31);
-                    }
-                    if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
-                    return valid ? v : 0u;
-                };
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int at = part * NC + c;                     // of the tile's four: FP8: [slots' half][blocks' half]
-                    see[c] = NAT ? __byte_perm(word(first + 64 * (at & 1)), word(first + 64 * (at & 1) + 32), at & 2 ? 0x7531 : 0x6420)
-                                 : word(first + 32 * c);
-                }
-            }
-            ok = warp_wait(bar(kSFull + sb), SW == 2 ? (t & 1) : ((t >> 1) & 1));
-            if (!ok) break;
-            if (live) {
-                tc_fence_after();
-                float c1 = factor;
-                float drop = 1.f;                                     // what a raise of V's power of two puts on O
-                if constexpr (RAW) {
-                    const uint2 e = ld_shared_v2(sbase + L::PASSED + (NAT ? sb * L::PASS + kKeys * 4 : 8 * (t & 7)));
-                    if (!NAT) c1 *= exp2i((int)e.x - 127);
-                    if (i > 0 && (int)e.y != ev) drop = exp2i(ev - (int)e.y);
-                    ev = (int)e.y;
-                }
-                c1 = fmaxf(c1, FLT_MIN);                              // (a hidden key's -inf stays -inf under a scale of 0)
-                const uint32_t mine = lanes + scol + COLS * part;
-                uint32_t sr[32];
-                // 32 of the thread's columns, hidden keys' -inf (a select: unread or stale columns may hold NaN)
-                auto scores = [&](int c) {
-                    tmem_ld32(mine + 32 * c, sr);
-                    uint4 sk[NAT ? 8 : 1];
-                    if constexpr (NAT) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) sk[k] = ld_shared_v4(sbase + L::PASSED + sb * L::PASS + 4 * (COLS * part + 32 * c + 4 * k));
-                    }
-                    tmem_wait_ld();
-                    if constexpr (NAT) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const uint64_t a = mul2((uint64_t)sr[k + 1] << 32 | sr[k], (uint64_t)sk[k / 4].y << 32 | sk[k / 4].x);
-                            const uint64_t b = mul2((uint64_t)sr[k + 3] << 32 | sr[k + 2], (uint64_t)sk[k / 4].w << 32 | sk[k / 4].z);
-                            sr[k] = (uint32_t)a;
-                            sr[k + 1] = (uint32_t)(a >> 32);
-                            sr[k + 2] = (uint32_t)b;
-                            sr[k + 3] = (uint32_t)(b >> 32);
+            for (int i = lo; runs && i < hi; ++i) {
+                const int t = t0 + i, sb = SW == 2 ? h : t & 1;
+                const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
+                // The first key as a node, of this thread's; FP8, whose columns are every other eight, of the tile's 128.
+                const int first = (x.j0 + i) * kKeys + (NAT ? 0 : COLS * part) - x.start;
+                // the visible keys of 32 columns are the bits of a word: the context's, then the row's mask
+                uint32_t see[NC];
+                const bool full = first + (NAT ? kKeys : COLS) <= 0;
+                if (live && !full) {
+                    auto word = [&](int node) -> uint32_t {
+                        const int left = x.nodes - node;
+                        uint32_t v = 0u;
+                        if (node < 0) {
+                            v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
+                        } else if (left > 0) {
+                            const uint32_t lo = (uint32_t)__ldg(mrow + node / 32);
+                            const uint32_t hi = (node & 31) != 0 && node / 32 + 1 < p.words ? (uint32_t)__ldg(mrow + node / 32 + 1) : 0u;
+                            v = __funnelshift_r(lo, hi, node & 31);
                         }
+                        if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
+                        return valid ? v : 0u;
+                    };
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int at = part * NC + c;                     // of the tile's four: FP8: [slots' half][blocks' half]
+                        see[c] = NAT ? __byte_perm(word(first + 64 * (at & 1)), word(first + 64 * (at & 1) + 32), at & 2 ? 0x7531 : 0x6420)
+                                     : word(first + 32 * c);
                     }
-                };
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    scores(c);
-                    if (!full) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!((see[c] >> k) & 1u)) sr[k] = 0xff800000u;
-                        if (NC > 1) tmem_st32(mine + 32 * c, sr);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-                        m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
                 }
-                if (NC > 1 && !full) tmem_wait_st();
-                float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
-                // whether a row of the pair of warps rises, or V's power of two
-                const bool rise = named_bar_or(row_bar, 32 * PARTS, mx > m_used + kRaise || drop != 1.f);
-                float alpha = 1.f;
-                if (rise) {
-                    shared_row[part * kTileRows] = mx;
-                    named_bar_sync(row_bar, 32 * PARTS);
-#pragma unroll
-                    for (int k = 0; k < PARTS; ++k) mx = fmaxf(mx, shared_row[k * kTileRows]);
-                    if (mx > m_used + kRaise) {                       // (the first keys: from -inf)
-                        alpha = fast_exp2(m_used - mx);
-                        m_used = mx;
+                ok = warp_wait(bar(kSFull + sb), SW == 2 ? (t & 1) : ((t >> 1) & 1));
+                if (!ok) break;
+                if (live) {
+                    tc_fence_after();
+                    float c1 = scale;
+                    float drop = 1.f;                                     // what a raise of V's power of two puts on O
+                    if constexpr (RAW) {
+                        const uint2 e = ld_shared_v2(sbase + L::PASSED + (NAT ? sb * L::PASS + kKeys * 4 : 8 * (t & 7)));
+                        c1 *= exp2i(max(min((int)e.x - 127 - shift, 127), -126));
+                        if (i > 0 && (int)e.y != ev) drop = exp2i(ev - (int)e.y);
+                        ev = (int)e.y;
                     }
-                    if (i > 0) {
-                        // with S double-buffered, S(t) complete does not imply P V(t - 1) complete
-                        if (SW == 1) {
-                            ok = warp_wait(bar(kPVDone), (t - 1) & 1);
-                            tc_fence_after();
+                    c1 = fmaxf(c1, FLT_MIN);                              // (a hidden key's -inf stays -inf under a scale of 0)
+                    const uint32_t mine = lanes + scol + COLS * part;
+                    uint32_t sr[32];
+                    // 32 of the thread's columns, hidden keys' -inf (a select: unread or stale columns may hold NaN)
+                    auto scores = [&](int c) {
+                        tmem_ld32(mine + 32 * c, sr);
+                        uint4 sk[NAT ? 8 : 1];
+                        if constexpr (NAT) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) sk[k] = ld_shared_v4(sbase + L::PASSED + sb * L::PASS + 4 * (COLS * part + 32 * c + 4 * k));
                         }
-                        const float on_o = alpha * drop;
+                        tmem_wait_ld();
+                        if constexpr (NAT) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const uint64_t a = mul2((uint64_t)sr[k + 1] << 32 | sr[k], (uint64_t)sk[k / 4].y << 32 | sk[k / 4].x);
+                                const uint64_t b = mul2((uint64_t)sr[k + 3] << 32 | sr[k + 2], (uint64_t)sk[k / 4].w << 32 | sk[k / 4].z);
+                                sr[k] = (uint32_t)a;
+                                sr[k + 1] = (uint32_t)(a >> 32);
+                                sr[k + 2] = (uint32_t)b;
+                                sr[k + 3] = (uint32_t)(b >> 32);
+                            }
+                        }
+                    };
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        scores(c);
+                        if (!full) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((see[c] >> k) & 1u)) sr[k] = 0xff800000u;
+                            if (NC > 1) tmem_st32(mine + 32 * c, sr);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(sr[k]), __uint_as_float(sr[k + 1]));
+                    }
+                    if (NC > 1 && !full) tmem_wait_st();
+                    float mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c1;
+                    // whether a row of the warps rises, or V's power of two
+                    const bool rise = named_bar_or(row_bar, 32 * PARTS, mx > m_used + kRaise || drop != 1.f);
+                    float alpha = 1.f;
+                    if (rise) {
+                        shared_row[part * kTileRows] = mx;
+                        named_bar_sync(row_bar, 32 * PARTS);
+#pragma unroll
+                        for (int k = 0; k < PARTS; ++k) mx = fmaxf(mx, shared_row[k * kTileRows]);
+                        if (mx > m_used + kRaise) {                       // (the first keys: from -inf)
+                            alpha = fast_exp2(m_used - mx);
+                            m_used = mx;
+                        }
+                        if (i > 0) {
+                            // with S double-buffered, S(t) complete does not imply P V(t - 1) complete
+                            if (SW == 1) {
+                                ok = warp_wait(bar(kPVDone), (t - 1) & 1);
+                                tc_fence_after();
+                            }
+                            const float on_o = alpha * drop;
 #pragma unroll 1
-                        for (int c = 0; c < DP / 16 && ok; ++c) {
-                            uint32_t o[16];
-                            tmem_ld(lanes + ocol + part * DP + 16 * c, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < DP / 16 && ok; ++c) {
+                                uint32_t o[16];
+                                tmem_ld(lanes + ocol + part * DP + 16 * c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * on_o);
-                            tmem_st(lanes + ocol + part * DP + 16 * c, o);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * on_o);
+                                tmem_st(lanes + ocol + part * DP + 16 * c, o);
+                            }
                         }
+                        named_bar_sync(row_bar, 32 * PARTS);                     // (the maxima are read)
+                        if (!ok) break;
                     }
-                    named_bar_sync(row_bar, 32 * PARTS);                     // (the maxima are read)
-                    if (!ok) break;
-                }
-                // probabilities, rounded to the tensor cores' type (the sums take them unrounded: the
-                // roundings are of either sign and average out), over the first columns of this thread's part of S
-                const float m_sub = (m_used == -INFINITY ? 0.f : m_used) - kLift;
-                const uint64_t c2 = pair_of(c1, c1), nm2 = pair_of(-m_sub, -m_sub);
-                uint64_t sum2[2] = {0ull, 0ull};
+                    // probabilities, rounded to the tensor cores' type (the sums take them unrounded: the
+                    // roundings are of either sign and average out), over the first columns of this thread's part of S
+                    const float m_sub = (m_used == -INFINITY ? 0.f : m_used) - kLift;
+                    const uint64_t c2 = pair_of(c1, c1), nm2 = pair_of(-m_sub, -m_sub);
+                    uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll (RAW ? 1 : 2)
-                for (int c = 0; c < NC; ++c) {
-                    uint32_t pk[16];
-                    if constexpr (NC > 1) scores(c);
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t pk[16];
+                        if constexpr (NC > 1) scores(c);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const uint64_t y = fma2(pair_of(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
-                        const float e0 = fast_exp2(pair_lo(y)), e1 = fast_exp2(pair_hi(y));
-                        sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pair_of(e0, e1));
-                        pk[k >> 1] = RAW ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+                        for (int k = 0; k < 32; k += 2) {
+                            const uint64_t y = fma2(pair_of(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, nm2);
+                            const float e0 = fast_exp2(pair_lo(y)), e1 = fast_exp2(pair_hi(y));
+                            sum2[(k >> 1) & 1] = add2(sum2[(k >> 1) & 1], pair_of(e0, e1));
+                            pk[k >> 1] = RAW ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+                        }
+                        tmem_st16(mine + 16 * c, pk);
                     }
-                    tmem_st16(mine + 16 * c, pk);
+                    const uint64_t sum = add2(sum2[0], sum2[1]);
+                    l = l * alpha + (pair_lo(sum) + pair_hi(sum));
+                    tmem_wait_st();
                 }
-                const uint64_t sum = add2(sum2[0], sum2[1]);
-                l = l * alpha + (pair_lo(sum) + pair_hi(sum));
-                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(bar(kPFull + sb), arrivals);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_n(bar(kPFull + sb), arrivals);
-        }
-        // (one row tile: the last piece's scores are taken, their Q is free)
-        if (SW == 1 && ok && lo == 0 && y.n > 0) factor_next = put_q(y, ic + 1);
-        lo = hi;
+            // (one row tile: the last piece's scores are taken, their Q is free)
+            if (SW == 1 && ok && lo == 0 && y.n > 0) shift_next = put_q(y, ic + 1);
+            lo = hi;
         }
         if (!ok) break;
         // (two: this piece's scores are taken, their Q is free)
@@ -1336,7 +1361,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (!ok) break;
         tc_fence_after();
         if (live) {
-            // the row's sum, of both halves in their order
+            // the row's sum, of its parts in their order
             shared_row[part * kTileRows] = l;
             named_bar_sync(row_bar, 32 * PARTS);
             l = shared_row[0];
@@ -1420,7 +1445,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (y.n == 0) break;
         x = y;
         if constexpr (SW == 2) publish_q(x);
-        else factor = factor_next;
+        else shift = shift_next;
     }
     if (!ok) {
         // a wait gave up: the rows of this piece and of the later ones are incomplete and become NaN

@@ -8,14 +8,15 @@ with A = sum w |v| / sum w.  d is the probability's rounding (bf16 for bf16 pool
 A score is a dot of D products summed in fp32: D u(f32) of size = max_t sum |q k| scale.  The sums
 over n keys add n u(f32) A, the output one rounding.  Beyond that, where keys and values become f16
 for the tensor cores:
-* FP8: a code times its scale, the scale rounded to f16 and the product again: 2 u(f16) of each key
-  element (so of size) and of each value (so of A).
+* FP8: a value's code times its scale, the scale rounded to f16 and the product again: 2 u(f16) of A.
+  Keys are taken as they are; a query element is two E4M3 numbers, the row's largest at 2^7 at least, exact
+  but for what lies below E4M3's smallest step of 2^-9: 2^-17 of the largest.
 * FP8 and FP4: a scale times the power of two that puts its tile's largest at 1 .. 2 (V: to 2^7, never
   below 1) is off by at most 2^-25 where it is below f16's normal range, and its code is at most 448,
   or 6, while max |k| is at least 448 or 4 of the largest scale's units: 1.5 2^-25 max |k|, with the product's
   own rounding taken as 2^-24 max |k| (and max |v|).
 * a probability times 2^7 likewise, while the sum of the weights is at least 1: 2^-32 max |v| a key.
-* a query element, its row's largest at 2^4 at least: 2^-29 of the largest.
+* a query element of FP4's, its row's largest at 2^4 at least: 2^-29 of the largest.
 Pools whose largest magnitudes belong to rows outside the sequence are not used with these.
 """
 from __future__ import annotations
@@ -86,7 +87,8 @@ def attention(q, k, v, see, scale, cache, out_dtype):
         size = torch.where(see, Q.abs() @ K.abs().T * abs(scale), 0.0).amax(1, keepdim=True)
         score = D * U32 * size
         if cache == "fp8":
-            score = score + 2 * u16 * size
+            k1 = torch.where(see, K.abs().sum(1)[None], 0.0).amax(1, keepdim=True)
+            score = score + abs(scale) * Q.abs().amax(1, keepdim=True) * k1 * 2.0 ** -17
         if quantised:
             kmax, qmax = float(K.abs().max()), Q.abs().amax(1, keepdim=True)
             score = score + abs(scale) * (Q.abs().sum(1, keepdim=True) * kmax * 2.0 ** -24 + D * qmax * kmax * 2.0 ** -29)

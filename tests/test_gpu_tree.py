@@ -653,3 +653,134 @@ def test_a_drafting_step(cache):
                 for pool, keys in ((kp, True), (vp, False)))
     want, tol = attention(turned[at].cpu(), k64, v64, visible(base, torch.ones(len(path), len(path)).tril().bool()), d ** -0.5, cache, wide)
     within(out[at], want, tol)
+
+
+# ---------------------------------------------------------------------------- the ends of the ranges
+@pytest.mark.parametrize("cache", CACHES)
+def test_more_sequences_than_threads(cache):
+    rng = rng_of("1100", cache)
+    ctx = [rng.randint(0, 40) for _ in range(1100)]
+    counts = [rng.choice([0, 1, 1, 2]) for _ in ctx]
+    sees = trees(counts, "1100", cache)
+    c = Cache(cache, [a + n for a, n in zip(ctx, counts)], (2, 1, 64), seed=40)
+    q = c.queries(sum(counts))
+    out = run_tree(c, ctx, sees, q, 0.125)
+    check_tree(c, ctx, sees, q, 0.125, out)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+def test_large_keys_and_small_queries(cache):
+    # scores of ordinary size from factors that are not, in keys whose scales differ by 2^20
+    ctx, counts, heads = [300], [9], (4, 2, 128)
+    c = Cache(cache, [309], heads, seed=41)
+    g = torch.Generator().manual_seed(42)
+    k = (torch.randn(309, 2, 128, generator=g) * torch.exp2(100 + torch.linspace(0, 20, 309))[:, None, None]).to(torch.bfloat16)
+    v = torch.randn(309, 2, 128, generator=g).to(torch.bfloat16)
+    append = {"fp8": pk.append_kv_fp8, "fp4": pk.append_kv_fp4}.get(cache, pk.append_kv)
+    append(c.kp, c.vp, k.cuda(), v.cuda(), c.tables.cuda(), i32([0]), i32([0, 309]))
+    c.refresh()
+    sees = trees(counts, "large")
+    q = (c.queries(9).float() * 2.0 ** -120).to(torch.bfloat16)
+    out = run_tree(c, ctx, sees, q, 0.1)
+    check_tree(c, ctx, sees, q, 0.1, out)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_calls_at_once(cache):
+    # two streams, each with a workspace of its own
+    ctx, counts = [2500, 40, 700], [20, 3, 11]
+    sees = trees(counts, "at once")
+    c = Cache(cache, [a + n for a, n in zip(ctx, counts)], (8, 2, 64), seed=43)
+    q = c.queries(sum(counts)).cuda()
+    want = run_tree(c, ctx, sees, q, 0.1)
+    rest = (c.tables.cuda(), i32(ctx), i32(cumulated(counts)), packed(sees).cuda(), 0.1, 20)
+    runs = [(torch.cuda.Stream(), pk.tree_workspace(8, 2, 64, 20), nan_like(q)) for _ in (0, 1)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for stream, ws, out in runs:
+            with torch.cuda.stream(stream):
+                tree_call(cache)(out, q, c.kp, c.vp, *rest, ws)
+    torch.cuda.synchronize()
+    for _, _, out in runs:
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "f32"])
+def test_outputs_on_a_16_byte_boundary(cache):
+    ctx, counts = [130, 5], [7, 40]
+    sees = trees(counts, "odd start")
+    c = Cache(cache, [a + n for a, n in zip(ctx, counts)], (6, 2, 64), seed=44)
+    q = c.queries(47).cuda()
+    e = 16 // q.element_size()
+    room = torch.full((q.numel() + 2 * e,), 7.0, dtype=q.dtype, device="cuda")
+    out = room[e:-e].view_as(q)
+    assert out.data_ptr() % 32 == 16
+    run_tree(c, ctx, sees, q, 0.1, out=out)
+    check_tree(c, ctx, sees, q.cpu(), 0.1, out)
+    assert bool((room[:e] == 7.0).all()) and bool((room[-e:] == 7.0).all())
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_pools_past_32_bits(cache):
+    # the sequences' blocks at both ends of pools of more than 4 GB
+    ctx, counts, heads = [70, 200], [6, 17], (4, 2, 128)
+    sees = trees(counts, "far blocks")
+    c = Cache(cache, [a + n for a, n in zip(ctx, counts)], heads, seed=45)
+    q = c.queries(23)
+    each = c.kp[0].numel() * c.kp.element_size()
+    blocks = 2**32 // each + 2 * c.blocks
+    far = []
+    for pool in (c.kp, c.vp):
+        t = torch.empty((blocks,) + tuple(pool.shape[1:]), dtype=pool.dtype, device="cuda")
+        t[-c.blocks:] = pool
+        far.append(t)
+    tables = torch.where(c.tables >= 0, c.tables + (blocks - c.blocks), -1).cuda()
+    want, out = run_tree(c, ctx, sees, q, 0.1), nan_like(q.cuda())
+    ws = pk.tree_workspace(4, 2, 128, 17)
+    tree_call(cache)(out, q.cuda(), far[0], far[1], tables, i32(ctx), i32(cumulated(counts)), packed(sees).cuda(), 0.1, 17, ws)
+    assert torch.equal(out, want)
+    # kept rows to the first blocks, then in place at the far end
+    src, start, cu = i32([69, 3, 40, 100, 215]), i32([0, 2]), i32([0, 3, 5])
+    compact_call(cache)(far[0], far[1], tables, src, start, cu, dst_tables=i32([0, 1]).view(2, 1))
+    compact_call(cache)(c.kp, c.vp, c.tables.cuda(), i32([3, 40, 69, 100, 215]), start, cu)
+    compact_call(cache)(far[0], far[1], tables, i32([3, 40, 69, 100, 215]), start, cu)
+    for pool, t in zip((c.kp, c.vp), far):
+        assert torch.equal(pool.view(torch.uint8), t[-c.blocks:].view(torch.uint8))
+    rows, near = (unpacked(cache, t, 128, True) for t in (far[0][-c.blocks:], far[0][:2]))
+    first = c.tables[:, 0].tolist()
+    assert torch.equal(near[0, 1], rows[first[0], 0]) and torch.equal(near[0, 2], rows[first[0], 1]) and torch.equal(near[0, 0], rows[first[0], 2])
+    assert torch.equal(near[1, 2], rows[first[1], 2]) and torch.equal(near[1, 3], rows[first[1], 3])
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_axes_in_a_graph(cache):
+    # captured on a side stream, replayed over other positions, lengths and rows
+    c = Cache(cache, [60, 90], (4, 2, 64), seed=46)
+    x = torch.randn(20, 8, 64, generator=c.g).to(c.wide).cuda()
+    q, k, v = torch.split(x, (4, 2, 2), dim=1)
+    plane, places = i32([f % 3 for f in range(32)]), torch.randint(0, 5000, (3, 20), dtype=torch.int32, device="cuda")
+    tables, start, cu = c.tables.cuda(), i32([50, 70]), i32([0, 8, 20])
+    out = nan_like(q.contiguous())
+
+    def call(kp, vp, o):
+        axes_call(cache)(kp, vp, o, q, k, v, frequencies(64), plane, places, tables, start, cu)
+
+    freq = frequencies(64)
+    kp, vp = c.kp.clone(), c.vp.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        axes_call(cache)(kp, vp, out, q, k, v, freq, plane, places, tables, start, cu)
+    for turn in range(2):
+        places.random_(0, 9000)
+        start.copy_(i32([50 - turn, 70 + turn]))
+        x.normal_()
+        kp.copy_(c.kp)
+        vp.copy_(c.vp)
+        kp2, vp2, out2 = c.kp.clone(), c.vp.clone(), nan_like(out)
+        g.replay()
+        call(kp2, vp2, out2)
+        torch.cuda.synchronize()
+        for a, b in ((kp, kp2), (vp, vp2), (out, out2)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
