@@ -264,15 +264,27 @@ __device__ __forceinline__ void tree_f32_piece(const TParams& p, const Cursor<kK
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const TParams p) {
+__global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const TParams given) {
     using L = F32Layout<D>;
     extern __shared__ __align__(16) uint8_t smem[];
     grid_dependency_wait();
     grid_launch_dependents();
     Cursor<kKeys> cur{};
-    const Line line = tree_locate<kThreads, kKeys>(
-        p, reinterpret_cast<long long*>(smem + L::SM), blockIdx.x == 0,
-        [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
+    TParams p = given;
+    auto locate = [&](bool report) {
+        return tree_locate<kThreads, kKeys>(
+            p, reinterpret_cast<long long*>(smem + L::SM), report,
+            [&](const Line& l) { return (int)blockIdx.x < l.ctas ? l.begin(blockIdx.x) : l.total; }, cur);
+    };
+    Line line = locate(blockIdx.x == 0);
+    // a line that leaves half of the CTAs without a tile shares out rows too, 16 or 8 to an item: four warps
+    // take 4 us for 32 rows of head dim 128 against 64 keys (9 sequences of 600 tokens, 32 rows 20.2 -> 16.3 us, 33 of 40
+    // with 64 rows 18.6 -> 14.6; three of 500 with 36, head dim 64, 11.6 -> 12.0)
+    if (2 * line.total <= p.ctas && p.TQ * p.G > 8) {
+        p.TQ = max(1, (4 * line.total <= p.ctas ? 8 : 16) / p.G);
+        __syncthreads();
+        line = locate(false);
+    }
     const bool any = (int)blockIdx.x < line.ctas && line.total > 0;
     if (threadIdx.x == 0) say_joint(p, line, cur, blockIdx.x, any);
     if (__syncthreads_or(!any || (threadIdx.x == 0 && tree_aborted(p.err)))) return;
