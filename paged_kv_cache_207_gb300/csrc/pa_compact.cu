@@ -28,7 +28,7 @@ constexpr int kCompactThreads = 256;
 constexpr int kBatchBlocks = 64, kBatchRows = kBatchBlocks * kBlockTokens;   // whose places are looked up together
 constexpr int kUnits = 2, kDepth = 2;      // 16-byte pieces of a thread's chunk, and chunks under way
 // CTAs of an SM, which bound the registers: 48, or 64 where units of several slots are put together
-// (16 windows of 4100 FP8 tokens, 8 heads: 140 us, with five CTAs 160; 64 gathers of bf16 rows, 2 heads: 10.7 with
+// (16 windows of 4100 FP8 tokens, 8 heads: 93 us, with five CTAs 110; 64 gathers of bf16 rows, 2 heads: 10.7 with
 // five, 11.9 with four).
 constexpr int sm_ctas(bool mix) { return mix ? 4 : 5; }
 
@@ -44,7 +44,6 @@ struct KParams {
     int src_blocks, dst_blocks;            // widths of the tables
     int total, num_blocks, Hkv;
     int slice_bits, segs;                  // of a (sequence, kv head, pool): 2^slice_bits shares of its tiles, shares of its rows
-    bool in_place;
 };
 
 // Where a row comes from: its tile's byte offset in the pool (a multiple of 16) and its slot; -1: it does not move.
@@ -142,11 +141,53 @@ __device__ __forceinline__ uint32_t gather_mixed(const char* pool, const From* f
     return moved;
 }
 
-template <pa_dtype T, int D>
+// FP8: what one source tile gives the units of a destination's, as byte permutations: word w takes
+// (x, y, z) of words 0 and 1, of words 2 and 3, and of those two results, under the mask w.
+constexpr int kRuns = 2;                  // tiles that a block's rows come from in turn, at most; more go slot by slot
+struct Runs {
+    uint4 word[kRuns][4];
+    From tile[kRuns];
+    uint16_t count, moves;                 // how many there are, and the slots that move
+};
+template <int D, int NU>
+__device__ __forceinline__ void gather_runs(const char* pool, const Runs& x, const char* dst, const int (&u)[NU], Mixed (&got)[NU]) {
+    constexpr pa_dtype T = PA_FP8_E4M3;
+    Mixed have[kRuns][NU];
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r)
+        if (r < x.count) {
+            const char* tile = pool + x.tile[r];
+#pragma unroll
+            for (int k = 0; k < NU; ++k) have[r][k] = load_mixed<T, D>(tile, u[k]);
+        }
+    if (x.moves != 0xffffu) {
+#pragma unroll
+        for (int k = 0; k < NU; ++k) got[k] = load_mixed<T, D>(dst, u[k]);
+    }
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r)
+        if (r < x.count) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint4 q = x.word[r][w];
+#pragma unroll
+                for (int k = 0; k < NU; ++k) {
+                    const uint32_t* h = have[r][k].w;
+                    const uint32_t z = __byte_perm(__byte_perm(h[0], h[1], q.x), __byte_perm(h[2], h[3], q.y), q.z);
+                    got[k].w[w] = (got[k].w[w] & ~q.w) | (z & q.w);
+                }
+            }
+        }
+}
+
+template <pa_dtype T, int D, bool IN_PLACE>
 __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MIX)) compact_kernel(const KParams p) {
     using G = Tile<T, D>;
     __shared__ From from[kBatchRows];
     __shared__ int64_t to[kBatchBlocks];      // byte offsets of the destination's tiles, -1: none
+    constexpr bool RUNS = IN_PLACE && T == PA_FP8_E4M3;               // (values of FP4 share bytes: slot by slot)
+    __shared__ Runs runs[RUNS ? kBatchBlocks : 1];
+    __shared__ uint8_t run_of[RUNS ? kBatchRows : 1];                 // of a row
     const int tid = threadIdx.x, s = blockIdx.z, h = blockIdx.y;
     int x = blockIdx.x;
     const int seg = x % p.segs;
@@ -179,6 +220,10 @@ __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MI
     const bool flags = h == 0 && which == 0 && slice == 0;
     for (int base = b0; base < b1; base += kBatchBlocks) {
         const int blocks = min(kBatchBlocks, b1 - base);
+        // Values of FP8 by whole tiles' permutations where there are blocks to make up for preparing them, in
+        // place (16 windows of 4100 tokens, 8 heads: 93 us, slot by slot 141; 64 paths of up to 7 rows
+        // 8.5 us, slot by slot 7.9; 24 scattered halves into other blocks 44, slot by slot 36).
+        const bool by_runs = RUNS && which == 1 && blocks > 4;
         __syncthreads();                       // (the last batch's reads of the places are done)
         if (tid < blocks) {
             const int32_t blk = __ldg(dtrow + first + base + tid);
@@ -186,14 +231,14 @@ __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MI
             if (!ok && flags) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
             to[tid] = ok ? tile(blk) : -1;
         }
-        for (int i = tid; i < blocks * kBlockTokens; i += kCompactThreads) {
+        for (int i = tid; i - tid % 32 < blocks * kBlockTokens; i += kCompactThreads) {      // (whole warps)
             const int pos = (first + base) * kBlockTokens + i, row = pos - start;
             From f = -1;
-            if (row >= 0 && row < n) {
+            if (i < blocks * kBlockTokens && row >= 0 && row < n) {
                 const int src = __ldg(p.src_pos + q0 + row);
-                if (src < 0 || src >= src_cap || (p.in_place && src < pos)) {
+                if (src < 0 || src >= src_cap || (IN_PLACE && src < pos)) {
                     if (flags) raise_flag(p.err, PA_DEV_ERR_BAD_POS);
-                } else if (!(p.in_place && src == pos)) {
+                } else if (!(IN_PLACE && src == pos)) {
                     const int32_t blk = __ldg(strow + src / kBlockTokens);
                     if (blk < 0 || blk >= p.num_blocks) {
                         if (flags) raise_flag(p.err, PA_DEV_ERR_BAD_BLOCK);
@@ -202,9 +247,45 @@ __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MI
                     }
                 }
             }
-            from[i] = f;
+            if (i < blocks * kBlockTokens) from[i] = f;
+            if constexpr (RUNS) {
+                if (by_runs) {
+                    const int lane = tid % 32, t = i % kBlockTokens, b = i / kBlockTokens;
+                    const From tile = f < 0 ? f : f & ~(From)(kBlockTokens - 1), before = __shfl_up_sync(0xffffffffu, tile, 1);
+                    const bool starts = f >= 0 && (t == 0 || before != tile);
+                    const uint32_t all = __ballot_sync(0xffffffffu, starts) >> (lane & 16) & 0xffffu;
+                    const uint32_t moves = __ballot_sync(0xffffffffu, f >= 0) >> (lane & 16) & 0xffffu;
+                    const int mine = __popc(all & ((2u << t) - 1u)) - 1;
+                    if (b < blocks) {
+                        run_of[i] = f < 0 ? 255 : mine;
+                        if (starts && mine < kRuns) runs[b].tile[mine] = tile;
+                        if (t == 0) {
+                            runs[b].count = __popc(all);
+                            runs[b].moves = moves;
+                        }
+                    }
+                }
+            }
         }
         __syncthreads();
+        if constexpr (RUNS) {
+            if (by_runs) {
+                for (int i = tid; i < blocks * kRuns * 4; i += kCompactThreads) {
+                    const int b = i / (kRuns * 4), r = i / 4 % kRuns, w = i % 4;
+                    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = b * kBlockTokens + 4 * w + j, slot = slot_of(from[row]);
+                        if (run_of[row] != r) continue;
+                        (slot < 8 ? q.x : q.y) |= (uint32_t)(slot % 8) << (4 * j);
+                        q.z |= (uint32_t)(slot < 8 ? j : 4 + j) << (4 * j);
+                        q.w |= 0xffu << (8 * j);
+                    }
+                    runs[b].word[r][w] = q;
+                }
+                __syncthreads();
+            }
+        }
         // (a row moves if it has both places)
         auto moves = [&](int row) { return from[row] >= 0 && to[row / kBlockTokens] >= 0; };
         if (!G::VALUES_MIX || which == 0) {
@@ -241,12 +322,14 @@ __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MI
                 for (int d = 0; d < kDepth; ++d) {
                     // (chunks past the last: nothing is loaded or stored, the barrier is passed by all)
                     load(at + (d + kDepth - 1) * chunk, v[(d + kDepth - 1) % kDepth]);
-                    if (p.in_place) __syncthreads();
+                    if (IN_PLACE) __syncthreads();
                     store(at + d * chunk, v[d]);
                 }
             }
         } else {
-            // units that hold all slots of a block, of a slice's where they are many two to a thread
+            // units that hold all slots of a block, of a slice's: two to a thread where they are many, four of
+            // FP8 into other blocks (the slots' places are found once for all: 24 scattered FP8 halves 36.4 us
+            // with four, 42.9 with two, 49.6 with one)
             const int per = G::MIXED >> p.slice_bits;
             auto run = [&](auto number) {
                 constexpr int NU = decltype(number)::value;
@@ -258,15 +341,26 @@ __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MI
                     for (int k = 0; k < NU; ++k) u[k] = slice * per + (NU == 1 ? j : (j / 32 * NU + k) * 32 + j % 32);
                     Mixed got[NU] = {};
                     uint32_t moved = 0u;
-                    if (i < units && to[b] >= 0) moved = gather_mixed<T, D>(pool, from + b * kBlockTokens, pool + to[b], u, got);
-                    if (p.in_place) __syncthreads();
+                    if (i < units && to[b] >= 0) {
+                        bool in_runs = false;
+                        if constexpr (RUNS) {
+                            if (by_runs && runs[b].count <= kRuns) {
+                                in_runs = true;
+                                moved = runs[b].moves;
+                                if (moved != 0u) gather_runs<D>(pool, runs[b], pool + to[b], u, got);
+                            }
+                        }
+                        if (!in_runs) moved = gather_mixed<T, D>(pool, from + b * kBlockTokens, pool + to[b], u, got);
+                    }
+                    if (IN_PLACE) __syncthreads();
                     if (moved != 0u) {
 #pragma unroll
                         for (int k = 0; k < NU; ++k) store_mixed<T, D>(pool + to[b], u[k], got[k]);
                     }
                 }
             };
-            if (per % 64 == 0) run(std::integral_constant<int, 2>{});
+            constexpr int MOST = !IN_PLACE && T == PA_FP8_E4M3 && D == 128 ? 4 : 2;
+            if (per % (32 * MOST) == 0) run(std::integral_constant<int, MOST>{});
             else run(std::integral_constant<int, 1>{});
         }
         if constexpr (G::SCALE > 0) {
@@ -293,7 +387,7 @@ __global__ void __launch_bounds__(kCompactThreads, sm_ctas(Tile<T, D>::VALUES_MI
     }
 }
 
-template <pa_dtype T, int D>
+template <pa_dtype T, int D, bool IN_PLACE>
 cudaError_t launch(KParams p, int num_seqs, cudaStream_t stream) {
     using G = Tile<T, D>;
     int dev = 0, sms = 1;
@@ -304,7 +398,7 @@ cudaError_t launch(KParams p, int num_seqs, cudaStream_t stream) {
     const long long pairs = 2ll * p.Hkv * num_seqs, room = (long long)sm_ctas(G::VALUES_MIX) * sms;
     p.slice_bits = 0;
     p.segs = 1;
-    if (p.in_place) {
+    if (IN_PLACE) {
         while ((2 << p.slice_bits) <= std::min(G::PIECES, 8) && (pairs << p.slice_bits) * 2 <= room) ++p.slice_bits;
     } else {
         const long long blocks = (p.total / num_seqs + kBlockTokens - 1) / kBlockTokens;
@@ -319,16 +413,16 @@ cudaError_t launch(KParams p, int num_seqs, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, compact_kernel<T, D>, p);
+    return cudaLaunchKernelEx(&cfg, compact_kernel<T, D, IN_PLACE>, p);
 }
 
-template <int D>
+template <int D, bool IN_PLACE>
 cudaError_t launch_type(const KParams& p, pa_dtype dtype, int num_seqs, cudaStream_t stream) {
     switch (dtype) {
-        case PA_F32: return launch<PA_F32, D>(p, num_seqs, stream);
-        case PA_BF16: return launch<PA_BF16, D>(p, num_seqs, stream);
-        case PA_FP8_E4M3: return launch<PA_FP8_E4M3, D>(p, num_seqs, stream);
-        case PA_FP4_E2M1: return launch<PA_FP4_E2M1, D>(p, num_seqs, stream);
+        case PA_F32: return launch<PA_F32, D, IN_PLACE>(p, num_seqs, stream);
+        case PA_BF16: return launch<PA_BF16, D, IN_PLACE>(p, num_seqs, stream);
+        case PA_FP8_E4M3: return launch<PA_FP8_E4M3, D, IN_PLACE>(p, num_seqs, stream);
+        case PA_FP4_E2M1: return launch<PA_FP4_E2M1, D, IN_PLACE>(p, num_seqs, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -350,8 +444,9 @@ cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream) {
     p.total = a.total_rows;
     p.num_blocks = a.num_blocks;
     p.Hkv = a.num_kv_heads;
-    p.in_place = a.in_place;
-    return a.head_dim == 64 ? launch_type<64>(p, a.dtype, a.num_seqs, stream) : launch_type<128>(p, a.dtype, a.num_seqs, stream);
+    if (a.head_dim == 64)
+        return a.in_place ? launch_type<64, true>(p, a.dtype, a.num_seqs, stream) : launch_type<64, false>(p, a.dtype, a.num_seqs, stream);
+    return a.in_place ? launch_type<128, true>(p, a.dtype, a.num_seqs, stream) : launch_type<128, false>(p, a.dtype, a.num_seqs, stream);
 }
 
 }  // namespace pa
