@@ -15,8 +15,8 @@
 // Where it is bound.  bf16 to 128 rows: by the keys' bytes (64 sequences of 4096 tokens, 32 / 8 heads of
 // 128: 1 node 166 us, 6.5 TB/s, 32 nodes 178).  bf16 with 256 rows: a key tile's MMAs take 1.5 us of the
 // 2.0 that pass (64 nodes 227 us): scores of one row tile wait for its products with the values, as the TMEM
-// holds one S tile per row tile.  FP8 (8 nodes 164, 32 nodes 171; four sequences of 80000: 182) and FP4 (191,
-// 200): 1.4 and 1.7 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
+// holds one S tile per row tile.  FP8 (8 nodes 164, 32 nodes 172; four sequences of 80000: 179) and FP4 (176,
+// 182; 190): 1.4 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
 // agreement, exponentials, publication), takes beside the conversions on the same issue slots; without
 // conversions 1.25, with the copies alone 1.05.
 //
@@ -380,20 +380,33 @@ struct Convert<D, PA_FP4_E2M1> {
     }
     // the power of two of scale code e against the reference r (code 255: infinity)
     static __device__ __forceinline__ uint32_t power(uint32_t e, int r) { return e == 255u ? 0x7c00u : f16_power((int)e - r); }
+    // Words read in an order of the lane's own, which begins at `by`, back in theirs.  (At head dim 128 a word's
+    // bank hardly depends on which row it is of: read by all lanes in one order, eight of them would want the same
+    // bank, 213 us instead of 190 for four sequences of 80000 tokens; at 64 there are four, 51.7 and 52.2 us
+    // for 64 of 4096.)
+    static __device__ __forceinline__ void turned_back(uint32_t (&x)[4], int by) {
+        const bool one = by & 1, two = by & 2;
+        const uint32_t a = one ? x[3] : x[0], b = one ? x[0] : x[1], c = one ? x[1] : x[2], d = one ? x[2] : x[3];
+        x[0] = two ? c : a;
+        x[1] = two ? d : b;
+        x[2] = two ? a : c;
+        x[3] = two ? b : d;
+    }
     static __device__ __forceinline__ void keys(uint32_t raw, uint32_t dst, int ek, int lane) {
-        const int slot = lane & 15;
+        const int slot = lane & 15, by = D == 128 ? (slot >> 1) & 3 : 0;
         uint32_t code[NB / 2][4], scale[NB / 2];
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) {
             const int w = 2 * k + (lane >> 4);
             scale[k] = code_at(raw + 8 * D + slot * NB + w);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) code[k][c] = ld_shared_u32(raw + slot * (D / 2) + c * (D / 8) + 4 * w);
+            for (int c = 0; c < 4; ++c) code[k][c] = ld_shared_u32(raw + slot * (D / 2) + ((c + by) & 3) * (D / 8) + 4 * w);
         }
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) {
             const int w = 2 * k + (lane >> 4);
             const uint32_t e = power(scale[k], ek), h = e | e << 16;
+            turned_back(code[k], by);
             uint32_t o[4][4];                                  // [c][piece]: dims 8 piece + 2 c, + 1
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -409,13 +422,13 @@ struct Convert<D, PA_FP4_E2M1> {
     // `table`: 128 bytes of the warp's, a pair of tokens' powers of two for each 32 dims: [D / 32][8 pairs]
     static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, uint32_t table, int rv, int lane, uint32_t live,
                                                   uint32_t own) {
-        const int r = lane & 7;
+        const int r = lane & 7, by = D == 128 ? r & 3 : 0;
         bool odd = false;
         uint32_t code[D / 64][4];
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) code[k][c] = ld_shared_u32(raw + ((4 * r + c) * (D / 16) + 4 * k + (lane >> 3)) * 4);
+            for (int c = 0; c < 4; ++c) code[k][c] = ld_shared_u32(raw + ((4 * r + ((c + by) & 3)) * (D / 16) + 4 * k + (lane >> 3)) * 4);
         if (lane < 8 * NB) {
             const int t = 2 * r, b = lane >> 3;
             const uint32_t at = raw + 8 * D + t * NB + b;
@@ -433,6 +446,7 @@ struct Convert<D, PA_FP4_E2M1> {
             const int mi = 4 * k + (lane >> 3);
             const uint4 lo = ld_shared_v4(table + mi / 2 * 32), hi = ld_shared_v4(table + mi / 2 * 32 + 16);
             const uint32_t h[2][4] = {{lo.x, lo.y, lo.z, lo.w}, {hi.x, hi.y, hi.z, hi.w}};
+            turned_back(code[k], by);
             uint32_t o[4][4];                                  // [c][dh, half]: tokens 2 c + 8 half, + 1 of dim 16 mi + 8 dh + r
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
