@@ -666,7 +666,8 @@ pa_status pa_bm_prepare_append(pa_block_manager* bm, int32_t seq, int32_t start_
                                int32_t num_tokens, int32_t* pairs_out, int32_t max_pairs,
                                int32_t* num_pairs_out);
 /* Cut the sequence to its first `len` tokens (at most its length): the blocks behind them lose one
- * reference each, as after a compaction or a rejected draft. */
+ * reference each, as after a compaction or a rejected draft.  PA_ERR_OUT_OF_BLOCKS when the host has
+ * no memory to note them as free (nothing changed). */
 pa_status pa_bm_truncate(pa_block_manager* bm, int32_t seq, int32_t len);
 /* Host array row_out (max_blocks entries) receives the block table, -1 padded. */
 pa_status pa_bm_block_table(const pa_block_manager* bm, int32_t seq, int32_t* row_out,

@@ -157,10 +157,19 @@ pa_status pa_bm_truncate(pa_block_manager* bm, int32_t seq, int32_t len) {
     if (it == bm->seqs.end() || len > it->second.len) return PA_ERR_INVALID_ARG;
     pa_block_manager::Seq& q = it->second;
     const size_t keep = ((size_t)len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
+    // (places in the free list first: without memory for them nothing changes)
+    std::set<int32_t> freed;
+    try {
+        for (size_t i = keep; i < q.table.size(); ++i)
+            if (bm->refcount[q.table[i]] == 1) freed.insert(q.table[i]);
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_OUT_OF_BLOCKS;
+    }
     while (q.table.size() > keep) {
-        bm->drop(q.table.back());
+        --bm->refcount[q.table.back()];
         q.table.pop_back();
     }
+    bm->free_ids.merge(freed);
     bm->logical_tokens -= q.len - len;
     q.len = len;
     return PA_OK;
