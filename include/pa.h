@@ -572,10 +572,15 @@ size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t
  * Row (i, h) attends to positions t < start_pos[s] and start_pos[s] + j for the j of its mask:
  *   out = sum_t softmax_t(scale * <q, K[t][g]>) V[t][g],  g = h / (Hq / Hkv);
  * a row that sees nothing, or only keys that score -inf, gives zeros.  K and V are read once for
- * all rows of a kv head (of up to 128 or 256 rows; more share them in groups).  Contexts are split
- * over the whole GPU at places that follow from all sequences' lengths, so that the last bits of a
- * sequence's result may depend on the batch; equal calls give equal bits.  A key or value of a node
- * that is not finite reaches only rows that see the node.
+ * all rows of a kv head, up to 128 of them (bf16: 256; f32: 32); more share them in groups of so
+ * many.  Contexts are split over the whole GPU at places that follow from all sequences' lengths, so
+ * that the last bits of a sequence's result may depend on the batch; equal calls give equal bits.
+ * What a node's key or value holds, finite or not, reaches only rows that see the node.
+ * Quantised pools: probabilities are f16, so that weights below 2^-32 of a row's largest may count
+ * as zero; FP8 values are off by 2^-11 of themselves, and by 2^-19 of the largest element of their
+ * row; FP4 values and keys, whose scales may lie 2^23 apart in a row, by 2^-24 of its largest element.
+ * Sizes of other rows do not matter; key tiles (128 tokens) whose rows' scales lie further apart than
+ * 2^14 (FP4: 2^23) take several times as long.
  * A chunk outside rows 0 .. total_q sets PA_DEV_ERR_BAD_CU and is skipped, one at positions outside
  * the table PA_DEV_ERR_BAD_POS; nodes past max_chunk set PA_DEV_ERR_HINT: they are not computed, and
  * not seen.  Rows of q and out past cu_q[num_seqs] (a padded batch) are neither read nor written.

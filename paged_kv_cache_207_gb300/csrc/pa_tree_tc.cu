@@ -15,8 +15,8 @@
 // Where it is bound.  bf16 to 128 rows: by the keys' bytes (64 sequences of 4096 tokens, 32 / 8 heads of
 // 128: 1 node 166 us, 6.5 TB/s, 32 nodes 178).  bf16 with 256 rows: a key tile's MMAs take 1.5 us of the
 // 2.0 that pass (64 nodes 227 us): scores of one row tile wait for its products with the values, as the TMEM
-// holds one S tile per row tile.  FP8 (8 nodes 164, 32 nodes 172; four sequences of 80000: 179) and FP4 (176,
-// 182; 190): 1.4 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
+// holds one S tile per row tile.  FP8 (8 nodes 169, 32 nodes 179; four sequences of 80000: 185) and FP4 (179,
+// 184; 192): 1.4 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
 // agreement, exponentials, publication), takes beside the conversions on the same issue slots; without
 // conversions 1.25, with the copies alone 1.05.
 //
@@ -36,7 +36,10 @@
 // by 2^-11 of the value, an eighth of what bf16 probabilities would lose: to keep the scales of values
 // apart would cost the softmax a product per probability.  An FP4 tile's K carries the power
 // of two that puts its largest scale at 1 .. 2; the tile's scores take it back.  V's power of two is
-// the piece's first tile's and changes, O with it, only when a tile's scales pass it by 2^6.
+// the piece's first tile's and changes, O with it, only where a tile's largest scale is 2^6 above or below.
+// That holds for scales down to 2^-14 (FP4: 2^-23) of the reference, hidden tokens' included; a tile with others
+// goes another way (wide_tile), with its columns' scales apart (against one reference alone, a hidden node of
+// 2^30 the size of the rest made zeros of it, and values of 2^-20 of an earlier tile's lost most of their bits).
 // Probabilities are taken times 2^7, at most 2^15, so that one below f16's normal range is off by at most 2^-32 of
 // a weight of 1.  FP4's query rows become f16 times a power of two of their own, their largest element
 // at 2^4 .. 2^5 (FP8: at 2^7 .. 2^8), and the row's scores give it back.
@@ -113,8 +116,13 @@ struct Layout {
     static constexpr int FIRST = RECORDS + kPieces * 32;               // the CTA's first place, for a call that gives up
     static constexpr int ROWS = FIRST + 64;                            // [row tile][part][128] maxima, sums
     static constexpr int TOPS = ROWS + SW * Roles<T, SW>::PARTS * kTileRows * 4;     // [part][128] the queries' largest
-    static constexpr int BYTES0 = TOPS + (RAW ? Roles<T, SW>::PARTS * kTileRows * 4 : 0);
-    static_assert(RECORDS % 16 == 0);
+    // wide tiles: FP8 [4] the columns' scales of values, FP4 [8] the columns' exponents, K's, then V's; [part][128] O's largest
+    static constexpr int WIDE = TOPS + (RAW ? Roles<T, SW>::PARTS * kTileRows * 4 : 0);
+    static constexpr int WIDE_TILES = NAT ? 4 : 8, WIDE_TILE = NAT ? kKeys * 4 : kKeys * 2;
+    static constexpr int LARGEST = WIDE + (RAW ? WIDE_TILES * WIDE_TILE : 0);
+    static constexpr int UNITS = LARGEST + (RAW ? Roles<T, SW>::PARTS * kTileRows * 4 : 0);      // of rows, where they differ
+    static constexpr int BYTES0 = UNITS + (RAW ? Roles<T, SW>::PARTS * kTileRows * 4 : 0);
+    static_assert(RECORDS % 16 == 0 && WIDE % 16 == 0);
     static_assert(BYTES0 <= 232448, "shared memory of one CTA");
     static_assert((Roles<T, SW>::THREADS / 32 + 6) * 8 <= KTILE, "the search's scratch, where the first tile goes");
     // one CTA (and its 512 TMEM columns) to an SM
@@ -212,6 +220,21 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x, uint32_t exponent) {
     return ((e & 0xffffu) == (exponent & 0xffffu) ? 0xffffu : 0u) | ((e >> 16) == (exponent >> 16) ? 0xffff0000u : 0u);
 }
 
+// Which of 32 keys from `node` on (below 0: of the context) a row sees of the tree's n nodes, whose mask is at `row`.
+__device__ __forceinline__ uint32_t seen_word(const int32_t* row, int words, int node, int n) {
+    const int left = n - node;
+    uint32_t v = 0u;
+    if (node < 0) {
+        v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(row) << -node;
+    } else if (left > 0) {
+        const uint32_t lo = (uint32_t)__ldg(row + node / 32);
+        const uint32_t hi = (node & 31) != 0 && node / 32 + 1 < words ? (uint32_t)__ldg(row + node / 32 + 1) : 0u;
+        v = __funnelshift_r(lo, hi, node & 31);
+    }
+    if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
+    return v;
+}
+
 // A run of key tiles of one item.
 struct Piece {
     int j0, n;               // its first key tile, and how many; none: the CTA's work has ended
@@ -289,6 +312,10 @@ struct Table {
     }
 };
 
+// What the conversions' lead and the MMA warp say of a tile beside its values' exponent of 8 bits: it is a wide one
+// (wide_tile), with its values' own scales, its keys'; then V's reference is in bits 8 .. 15 of its keys' exponent.
+constexpr uint32_t kWideValues = 1u << 8, kWideKeys = 1u << 9;
+
 // The conversions of one block of a tile by one warp: K to [D/8][8 blocks][16 slots][8 dims], V to
 // [16 token groups of 8][D/8][8 dims][8 tokens], f16.  `live`: its tokens that are keys; `own`: those of the tree.
 template <int D, pa_dtype T>
@@ -296,15 +323,35 @@ struct Convert;
 
 template <int D>
 struct Convert<D, PA_FP8_E4M3> {
-    // Largest biased exponent of the tile's finite scales (of its keys).
-    static __device__ __forceinline__ int exponent(uint32_t raw, int rec, int keys, int lane) {
-        const uint4 x = ld_shared_v4(raw + (lane >> 2) * rec + 16 * D + (lane & 3) * 16);
+    static constexpr int DEPTH = 14;           // how far scales lie below the largest in a tile that is not wide
+    // A lane's four scales of a tile, without their signs; 0 where they are no keys' or not finite.
+    struct Scales { uint32_t x[4]; };
+    static __device__ __forceinline__ Scales scales(uint32_t raw, int rec, int keys, int lane) {
+        const uint4 y = ld_shared_v4(raw + (lane >> 2) * rec + 16 * D + (lane & 3) * 16);
         const int n = keys - 4 * lane;                                     // keys of this lane's four
-        auto e = [&](uint32_t y, int i) {
-            const uint32_t z = (y >> 23) & 0xffu;
-            return n > i && z != 0xffu ? z : 0u;
-        };
-        return (int)__reduce_max_sync(0xffffffffu, max(max(e(x.x, 0), e(x.y, 1)), max(e(x.z, 2), e(x.w, 3))));
+        auto of = [&](uint32_t z, int i) { return n > i && (z & 0x7f800000u) != 0x7f800000u ? z & 0x7fffffffu : 0u; };
+        return Scales{{of(y.x, 0), of(y.y, 1), of(y.z, 2), of(y.w, 3)}};
+    }
+    // Their largest biased exponent.
+    static __device__ __forceinline__ int exponent(const Scales& s) {
+        return (int)(__reduce_max_sync(0xffffffffu, max(max(s.x[0], s.x[1]), max(s.x[2], s.x[3]))) >> 23);
+    }
+    // Whether one of the lane's that is not 0 has an exponent below e.
+    static __device__ __forceinline__ bool below(const Scales& s, int e) {
+        const uint32_t least = e > 0 ? ((uint32_t)e << 23) - 1u : 0u;      // (less 1: a scale of 0 passes to the top)
+        return min(min(s.x[0] - 1u, s.x[1] - 1u), min(s.x[2] - 1u, s.x[3] - 1u)) < least;
+    }
+    // A wide tile's scales of values as its columns lie (the keys' lie so too), 0 where the tree's own (from the ctx-th
+    // on) are not finite; in the record 1 takes their place, so that the operands are the codes.
+    static __device__ __forceinline__ void widen(uint32_t raw, int rec, uint32_t to, int keys, int ctx, int lane) {
+        const uint32_t at = raw + (lane >> 2) * rec + 16 * D + (lane & 3) * 16;
+        const uint4 y = ld_shared_v4(at);
+        auto finite = [](uint32_t z) { return (z & 0x7f800000u) != 0x7f800000u; };
+        auto keep = [&](uint32_t z, int i) { return 4 * lane + i < keys && (4 * lane + i < ctx || finite(z)) ? z : 0u; };
+        auto one = [&](uint32_t z) { return finite(z) && (z << 1) != 0u ? 0x3f800000u : z; };
+        st_shared_v4(to + ((lane >> 1) & 1) * 256 + (lane >> 2) * 32 + (lane & 1) * 16,
+                     make_uint4(keep(y.x, 0), keep(y.y, 1), keep(y.z, 2), keep(y.w, 3)));
+        st_shared_v4(at, make_uint4(one(y.x), one(y.y), one(y.z), one(y.w)));
     }
     static __device__ __forceinline__ bool values(uint32_t raw, uint32_t dst, uint32_t, int rv, int lane, uint32_t live, uint32_t own) {
         const float f = exp2i(127 - rv);
@@ -353,25 +400,62 @@ __device__ __forceinline__ uint32_t f16_power(int x) {
 template <int D>
 struct Convert<D, PA_FP4_E2M1> {
     static constexpr int NB = D / 32;
-    static __device__ __forceinline__ int exponent(uint32_t raw, int rec, int keys, int lane) {
-        // a lane has the scale codes of four tokens, NB bytes each; code 255 is no number
+    static constexpr int DEPTH = 23;           // (f16 holds every code times 2^-23 exactly)
+    // The scale codes of a lane's four tokens, NB bytes each, plus 1, two to a word; 0 where they are no keys' or 255, which
+    // is no number.  (Pairs of 16 bits have a maximum in one instruction, bytes have not.)
+    struct Scales { uint32_t x[2 * NB]; };
+    static __device__ __forceinline__ Scales scales(uint32_t raw, int rec, int keys, int lane) {
         const uint32_t at = raw + (lane >> 2) * rec + 8 * D + (lane & 3) * (4 * NB);
         const int n = keys - 4 * lane;
-        auto bytes = [&](uint32_t x, bool key) {
-            x &= ~__vcmpeq4(x, 0xffffffffu);
-            return key ? x : 0u;
+        Scales s;
+        auto put = [&](int i, uint32_t x, uint32_t key) {
+            s.x[2 * i] = ((x & 0x00ff00ffu) + 0x00010001u) & key & 0x00ff00ffu;
+            s.x[2 * i + 1] = ((x >> 8 & 0x00ff00ffu) + 0x00010001u) & key & 0x00ff00ffu;
         };
-        uint32_t m;
         if constexpr (NB == 4) {
-            const uint4 x = ld_shared_v4(at);
-            m = __vmaxu4(__vmaxu4(bytes(x.x, n > 0), bytes(x.y, n > 1)), __vmaxu4(bytes(x.z, n > 2), bytes(x.w, n > 3)));
+            const uint4 y = ld_shared_v4(at);
+            put(0, y.x, n > 0 ? ~0u : 0u);
+            put(1, y.y, n > 1 ? ~0u : 0u);
+            put(2, y.z, n > 2 ? ~0u : 0u);
+            put(3, y.w, n > 3 ? ~0u : 0u);
         } else {
-            const uint2 x = ld_shared_v2(at);
-            const uint32_t lo = n > 1 ? 0xffffffffu : n > 0 ? 0xffffu : 0u, hi = n > 3 ? 0xffffffffu : n > 2 ? 0xffffu : 0u;
-            m = __vmaxu4(bytes(x.x, true) & lo, bytes(x.y, true) & hi);
+            const uint2 y = ld_shared_v2(at);
+            put(0, y.x, n > 1 ? ~0u : n > 0 ? 0xffffu : 0u);
+            put(1, y.y, n > 3 ? ~0u : n > 2 ? 0xffffu : 0u);
         }
-        m = __vmaxu4(m, m >> 16);
-        return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffu, (m >> 8) & 0xffu));
+        return s;
+    }
+    static __device__ __forceinline__ int exponent(const Scales& s) {
+        uint32_t m = s.x[0];
+#pragma unroll
+        for (int i = 1; i < 2 * NB; ++i) m = __vmaxu2(m, s.x[i]);
+        return max((int)__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) - 1, 0);
+    }
+    // (a code of 0 counts as none: its values are 6 2^-127 at most)
+    static __device__ __forceinline__ bool below(const Scales& s, int e) {
+        uint32_t m = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) m = __vminu2(m, __vsub2(s.x[i], 0x00020002u));       // (none: passes to the top)
+        return (int)min(m & 0xffffu, m >> 16) < e - 1;
+    }
+    // The largest code of each token of a wide tile, a byte a column; in the record its codes are against that, 127.
+    static __device__ __forceinline__ void widen(uint32_t raw, int rec, uint32_t to, int, int, int lane) {
+        const uint32_t at = raw + (lane >> 2) * rec + 8 * D + (lane & 3) * (4 * NB);
+        uint32_t w = 0u;
+#pragma unroll 1
+        for (int t = 0; t < 4; ++t) {
+            int top = 0;
+            for (int b = 0; b < NB; ++b) {
+                const int e = (int)code_at(at + t * NB + b);
+                if (e != 255) top = max(top, e);
+            }
+            w |= (uint32_t)top << (8 * t);
+            for (int b = 0; b < NB; ++b) {
+                const int e = (int)code_at(at + t * NB + b);
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + t * NB + b), "r"(e == 255 ? e : max(e - top + 127, 0)) : "memory");
+            }
+        }
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * lane), "r"(w) : "memory");
     }
     static __device__ __forceinline__ uint32_t code_at(uint32_t addr) {
         uint32_t v;
@@ -548,6 +632,186 @@ __device__ __noinline__ float value_at(const char* rec, int slot, int d) {
         const uint32_t code = (uint8_t)rec[at] >> (4 * (slot & 1));
         return (code & 7u) == 0u ? __int_as_float(0x7fc00000) : __int_as_float(code & 8u ? 0xff800000 : 0x7f800000);
     }
+}
+
+// Wide tiles, whose scales lie further apart than operands of 16 bits against one reference hold: a column's own scales go
+// on its score and on its probability, and a row has its O in a unit of its own, if need be, so that no row depends on
+// the scales of keys that it does not see or that weigh nothing for it.  (64 sequences of 4096 tokens, 32 / 8 heads of 128,
+// 8 nodes, all tiles wide: FP8 1350 us,
+// not 169, FP4 950, not 179.)
+
+// A scale as 2^(e - 127) m, |m| from 1 to below 2; 0: m = 0; not finite: m is what it is.
+struct Split {
+    float m;
+    int e;
+};
+__device__ __forceinline__ Split split_scale(uint32_t bits) {
+    const float s = __uint_as_float(bits);
+    if (!(fabsf(s) <= FLT_MAX)) return Split{s, 127};
+    if (s == 0.f) return Split{0.f, 0};
+    const bool small = fabsf(s) < FLT_MIN;
+    const uint32_t b = __float_as_uint(small ? s * 0x1p64f : s);
+    return Split{__uint_as_float((b & 0x807fffffu) | 0x3f800000u), (int)((b >> 23) & 0xffu) - (small ? 64 : 0)};
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+constexpr int kOwnUnits = -2;            // for `ev`, the exponent of the rows' unit of O: each has its own
+// What a tile takes and leaves of a row: maximum, sum, ev; whether the waits went well.
+struct WideRow {
+    float m, l;
+    int ev;
+    bool ok;
+};
+// The softmax of a wide tile, the CTA's t-th, by the threads that share a row, with the same barriers as that of others;
+// a function beside the loop over the tiles, which has to be short.  first: the piece's first tile; mrow: the row's mask words
+// (null: no row), key0: its first key as a node; shift: what the row of q carries.
+template <int D, pa_dtype T>
+__device__ __noinline__ WideRow wide_tile(WideRow row, uint32_t sbase, uint32_t tmem, int t, bool first, const int32_t* mrow, int words,
+                                          int key0, int nodes, int shift, float scale, float lift) {
+    using L = Layout<D, T, 1>;
+    constexpr int PARTS = Roles<T, 1>::PARTS, COLS = kKeys / PARTS, DP = D / PARTS;
+    constexpr bool FP8 = T == PA_FP8_E4M3;
+    const int warp = threadIdx.x >> 5, quarter = warp & 3, part = warp >> 2, lr = quarter * 32 + (threadIdx.x & 31);
+    const int row_bar = 3 + quarter;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t scores = lanes + kColS + (t & 1) * kKeys + COLS * part, o = lanes + kColO + DP * part;
+    const uint32_t table = sbase + L::WIDE + t % L::WIDE_TILES * L::WIDE_TILE;
+    const uint2 e = ld_shared_v2(sbase + L::PASSED + (FP8 ? (t & 1) * L::PASS + kKeys * 4 : 8 * (t & 7)));
+    const bool own = (e.y & kWideValues) != 0u;
+    // column c's scale of values: its own, or the tile's power of two
+    auto value_scale = [&](int c) {
+        if (!own) return Split{1.f, (int)(e.y & 0xffu)};
+        if constexpr (FP8) return split_scale(ld_shared_u32(table + 4 * (COLS * part + c)));
+        else return Split{1.f, (int)ld_shared_u8(table + kKeys + COLS * part + c)};
+    };
+    auto exchange = [&](int at, float x) {
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + at + 4 * (kTileRows * part + lr)), "f"(x) : "memory");
+    };
+    auto most = [&](int at, float x) {
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) x = fmaxf(x, __uint_as_float(ld_shared_u32(sbase + at + 4 * (kTileRows * k + lr))));
+        return x;
+    };
+    // scores in log2 units, back to the TMEM; their maximum, and that of score + exponent of the value's scale
+    const Split by = split_scale(__float_as_uint(fmaxf(scale, FLT_MIN)));
+    const int ke = (int)(e.x & 0xffu) - 254 - shift + by.e;
+    float mx = -INFINITY, ux = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 16) {
+        uint32_t r[16];
+        tmem_ld(scores + c, r);
+        tmem_wait_ld();
+        // 16 columns: the keys in their order; FP8: eight of one half of each block's slots, then of the next block's
+        uint32_t see = 0u;
+        if (mrow) {
+            const int col = COLS * part + c;
+            if constexpr (FP8) {
+                const uint32_t w = seen_word(mrow, words, key0 + (col & 63) * 2, nodes) >> (col >> 6) * 8;
+                see = (w & 0xffu) | (w >> 8 & 0xff00u);
+            } else {
+                see = seen_word(mrow, words, key0 + col, nodes);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            // (FP8's keys: the scale over the power of two in e)
+            const Split s = FP8 ? split_scale(ld_shared_u32(sbase + L::PASSED + (t & 1) * L::PASS + 4 * (COLS * part + c + k)))
+                                : Split{1.f, own ? (int)ld_shared_u8(table + COLS * part + c + k) : 127};
+            // (two powers of two: past fp32's range only where the score is)
+            const int n = max(-252, min(ke + s.e - 127, 252));
+            float x = __uint_as_float(r[k]) * (s.m * by.m) * exp2i(n / 2) * exp2i(n - n / 2);
+            x = (see >> k) & 1u ? x : -INFINITY;
+            r[k] = __float_as_uint(x);
+            const Split v = value_scale(c + k);
+            mx = fmaxf(mx, x);
+            if (v.m != 0.f && fabsf(v.m) <= FLT_MAX) ux = fmaxf(ux, x + (float)v.e);
+        }
+        tmem_st16(scores + c, r);
+    }
+    tmem_wait_st();
+    // and the largest element of O
+    float ox = 0.f;
+    if (!first) {
+        row.ok = warp_wait(sbase + L::BAR + 8 * kPVDone, (t - 1) & 1);
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < DP && row.ok; c += 16) {
+            uint32_t x[16];
+            tmem_ld(o + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) ox = fmaxf(ox, fabsf(__uint_as_float(x[k])));
+        }
+    }
+    named_bar_or(row_bar, 32 * PARTS, true);
+    exchange(L::ROWS, mx);
+    exchange(L::TOPS, ux);
+    exchange(L::LARGEST, ox);
+    named_bar_sync(row_bar, 32 * PARTS);
+    mx = most(L::ROWS, mx);
+    ux = most(L::TOPS, ux);
+    ox = most(L::LARGEST, ox);
+    const float was = row.m;
+    if (mx > was) {
+        row.m = mx;
+        row.l *= fast_exp2(was - mx);
+    }
+    // O's unit over the maximum.  V's reference, while that holds what is in O and what the tile adds (2^-12 of it at least,
+    // so that f16's smallest step is 2^-20 of the largest product), for all rows, as the next tile takes it then; else for
+    // each row what this tile adds at most, unless what is in O would pass 2^100.
+    const uint32_t units = sbase + L::UNITS + 4 * (kTileRows * part + lr);
+    const float base = row.m == -INFINITY ? 0.f : row.m;
+    const int reference = own ? (int)(e.x >> 8) : (int)(e.y & 0xffu);
+    const float was_unit = (float)(row.ev == kOwnUnits ? (int)ld_shared_u32(units) : row.ev);
+    const float had = ox > 0.f ? was - base + was_unit : -INFINITY, adds = ux - base, over = adds - (float)reference;
+    const float in_o = had + (float)((int)(__float_as_uint(ox) >> 23) - 127), there = in_o - (float)reference;
+    const bool fits = !mrow || (there <= 40.f && (there >= -40.f || adds >= in_o + 40.f || in_o == -INFINITY) &&
+                                over <= 7.f && (over >= -12.f || adds <= in_o - 40.f || adds == -INFINITY));
+    int unit = reference;
+    row.ev = unit;
+    if (!__all_sync(0xffffffffu, fits)) {
+        row.ev = kOwnUnits;
+        unit = (int)fminf(fmaxf(ceilf(fmaxf(adds, in_o - 100.f)), 1.f), 254.f);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(units), "r"(unit) : "memory");
+    }
+    if (!first) {
+        // (in two steps, as a power of two alone may be out of range)
+        const float by2 = had - (float)unit, near = fmaxf(-120.f, fminf(by2, 120.f)), part1 = fast_exp2(near), part2 = fast_exp2(by2 - near);
+#pragma unroll 1
+        for (int c = 0; c < DP && row.ok; c += 16) {
+            uint32_t x[16];
+            tmem_ld(o + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * part1 * part2);
+            tmem_st(o + c, x);
+        }
+    }
+    named_bar_sync(row_bar, 32 * PARTS);                              // (the maxima are read)
+    if (!row.ok) return row;
+    // the probabilities times their values' scales, as f16 against O's unit
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 16) {
+        uint32_t r[16], w[8];
+        tmem_ld(scores + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float x = __uint_as_float(r[k]) - base + lift;
+            const Split v = value_scale(c + k);
+            sum += fast_exp2(x);
+            r[k] = __float_as_uint(fast_exp2(x + (float)(v.e - unit)) * v.m);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = pack_f16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+        tmem_st(scores + c / 2, w);
+    }
+    row.l += sum;
+    return row;
 }
 
 template <int D, pa_dtype T, int SW>
@@ -751,14 +1015,21 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     // the columns' scales in their order, against the largest's power of two (so that no score
                     // overflows that does not with the row's factor): a lane has four slots of a block
                     const uint32_t to = sbase + L::PASSED + buf * L::PASS, at = sbase + L::K + (t % KST) * KSTAGE;
-                    const int ek = Convert<D, T>::exponent(at, REC, x.end() - (x.j0 + i) * kKeys, lane);
+                    const auto scales = Convert<D, T>::scales(at, REC, x.end() - (x.j0 + i) * kKeys, lane);
+                    int ek = Convert<D, T>::exponent(scales);
+                    // (too far apart for products in fp32: as they are)
+                    const bool wide = __any_sync(0xffffffffu, Convert<D, T>::below(scales, ek - 60));
+                    if (wide) ek = 127;
                     const uint4 sk = ld_shared_v4(at + (lane >> 2) * REC + 16 * D + (lane & 3) * 16);
                     const float f = exp2i(127 - ek);
                     st_shared_v4(to + ((lane >> 1) & 1) * 256 + (lane >> 2) * 32 + (lane & 1) * 16,
                                  make_uint4(__float_as_uint(__uint_as_float(sk.x) * f), __float_as_uint(__uint_as_float(sk.y) * f),
                                             __float_as_uint(__uint_as_float(sk.z) * f), __float_as_uint(__uint_as_float(sk.w) * f)));
                     ok = warp_wait(bar(kEFull + (t & 3)), (t >> 2) & 1);
-                    if (lane == 0) st_shared_v2(to + kKeys * 4, make_uint2((uint32_t)ek, ld_shared_u32(sbase + L::EXPS + 8 * (t & 7) + 4)));
+                    if (lane == 0) {
+                        const uint2 e = ld_shared_v2(sbase + L::EXPS + 8 * (t & 7));
+                        st_shared_v2(to + kKeys * 4, make_uint2((uint32_t)ek | (e.x & 0xff00u), e.y | (wide ? kWideKeys : 0u)));
+                    }
                     __syncwarp();
                     if (elect_one()) mbar_arrive(bar(kSFull + buf));
                     __syncwarp();
@@ -903,7 +1174,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         // One warp for the keys, one for the values waits for a tile's records and for its place and lets
         // eight warps go at a named barrier, so that they do not poll (28 polling warps took half of
         // the issue slots).  The first also finds the tile's largest K scale, and V's reference: the
-        // piece's first, raised where a tile's scales pass it by 2^6.
+        // piece's first, moved to a tile's largest that is 2^6 above or below it.  O, up to 2^42, moves with it, so
+        // not by more than 2^60.  A tile with scales too far from it is a wide one.
         if constexpr (RAW) {
             using C = Convert<D, T>;
             const bool for_v = NAT || warp > W::LEAD;
@@ -913,21 +1185,44 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 Piece x;
                 ok = piece(ic, x);
                 if (!ok || x.n == 0) break;
-                int rv = 0;
+                int rv = 127, top = 0, low = 255;         // (of references: V's, the highest, the lowest; top 0: none yet)
                 for (int i = 0; i < x.n; ++i, ++t) {
                     const int uk = 2 * t, uv = NAT ? t : 2 * t + 1, rk = uk % L::RST, rs = uv % L::RST;
                     const int keys = x.end() - (x.j0 + i) * kKeys;
                     if (NAT || !for_v) {
+                        const uint32_t kraw = sbase + L::R + rk * L::HALF, vraw = sbase + L::R + rs * L::HALF;
                         int ek = 0;
+                        bool far = false;
                         if (!NAT) {
                             ok = warp_wait(bar(kRFull + rk), (uk / L::RST) & 1);
-                            ek = C::exponent(sbase + L::R + rk * L::HALF, REC, keys, lane);
+                            const auto scales = C::scales(kraw, REC, keys, lane);
+                            ek = C::exponent(scales);
+                            far = C::below(scales, ek - C::DEPTH);
                         }
                         ok = ok && warp_wait(bar(kRFull + rs), (uv / L::RST) & 1);
-                        const int ev = C::exponent(sbase + L::R + rs * L::HALF, REC, keys, lane);
-                        if (i == 0 || ev > rv + 6) rv = ev;
+                        const auto scales = C::scales(vraw, REC, keys, lane);
+                        const int ev = C::exponent(scales);
+                        if (ev > 0 && (top == 0 || ev > rv + 6 || ev < rv - 6)) {
+                            if (max(top, ev) - min(low, ev) > 60 && top > 0) {
+                                far = true;
+                            } else {
+                                rv = ev;
+                                top = max(top, ev);
+                                low = min(low, ev);
+                            }
+                        }
+                        const bool wide = __any_sync(0xffffffffu, far || C::below(scales, rv - C::DEPTH));
+                        if (wide) {
+                            const uint32_t to = sbase + L::WIDE + t % L::WIDE_TILES * L::WIDE_TILE;
+                            const int ctx = x.start - (x.j0 + i) * kKeys;
+                            if (!NAT) C::widen(kraw, REC, to, keys, ctx, lane);
+                            C::widen(vraw, REC, NAT ? to : to + kKeys, keys, ctx, lane);
+                            fence_proxy_async_smem();                // (before the next copies to the records' places)
+                            __syncwarp();
+                        }
                         if (lane == 0) {
-                            st_shared_v2(sbase + L::EXPS + 8 * (t & 7), make_uint2((uint32_t)ek, (uint32_t)rv));
+                            st_shared_v2(sbase + L::EXPS + 8 * (t & 7),
+                                         wide ? make_uint2(127u | (uint32_t)rv << 8, 127u | kWideValues) : make_uint2((uint32_t)ek, (uint32_t)rv));
                             mbar_arrive(bar(kEFull + (t & 3)));
                             if (!NAT) mbar_arrive(bar(kREmpty + rk));
                             mbar_arrive(bar(kREmpty + rs));
@@ -977,7 +1272,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     if (!ok) break;
                     mbar_test(bar(kRFull + (for_v ? rs : rk)), ((for_v ? uv : uk) / L::RST) & 1);     // (the copies are seen)
                     const uint2 e = ld_shared_v2(sbase + L::EXPS + 8 * (t & 7));
-                    const int rv = (int)e.y;
+                    const int rv = (int)(e.y & 0xffu);
                     if (for_v) {
                         bool odd = false;
                         // (FP8: an odd last block has the next one's zeros beside it)
@@ -990,7 +1285,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                         odd = __any_sync(0xffffffffu, odd);
                         if (lane == 0) *reinterpret_cast<volatile uint8_t*>(smem + L::SEEN + 8 * (t & 7) + b) = odd;
                     } else if constexpr (!NAT) {
-                        if (first < end) C::keys(smem_r + rk * L::HALF + b * REC, sbase + L::K + st * KTILE + b * 256, (int)e.x, lane);
+                        if (first < end) C::keys(smem_r + rk * L::HALF + b * REC, sbase + L::K + st * KTILE + b * 256, (int)(e.x & 0xffu), lane);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -1214,7 +1509,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (SW == 1 && y.n > 0) stage_q(y);
         float m_used = -INFINITY, l = 0.f;
         int shift_next = 0;
-        int ev = 0;
+        int ev = -1;
         // the row tile's warps without rows do not go through the keys: its first one arrives for them
         const int with_rows = PARTS * max(0, min(4, (rows - h * kTileRows + 31) / 32));
         const bool leads = warp % (4 * PARTS) == 0, runs = live || leads;
@@ -1223,9 +1518,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         // (with them in it, the instructions come too slowly: 64 ragged FP8 sequences of 4096 tokens, 32 nodes,
         // 189 us instead of 180; for the same reason a wait that does not end at once is a function, FP4 215 to 199).
         for (int lo = 0; ok && lo < n;) {
-            const int hi = SW == 1 && lo == 0 ? 1 : n;
+            int hi = SW == 1 && lo == 0 ? 1 : n, i = lo;
+            bool wide = false;
 #pragma unroll 1
-            for (int i = lo; runs && i < hi; ++i) {
+            for (; runs && i < hi; ++i) {
                 const int t = t0 + i, sb = SW == 2 ? h : t & 1;
                 const uint32_t scol = kColS + (uint32_t)(sb * kKeys);
                 // The first key as a node, of this thread's; FP8, whose columns are every other eight, of the tile's 128.
@@ -1234,19 +1530,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 uint32_t see[NC];
                 const bool full = first + (NAT ? kKeys : COLS) <= 0;
                 if (live && !full) {
-                    auto word = [&](int node) -> uint32_t {
-                        const int left = x.nodes - node;
-                        uint32_t v = 0u;
-                        if (node < 0) {
-                            v = node <= -32 ? 0xffffffffu : ~(0xffffffffu << -node) | (uint32_t)__ldg(mrow) << -node;
-                        } else if (left > 0) {
-                            const uint32_t lo = (uint32_t)__ldg(mrow + node / 32);
-                            const uint32_t hi = (node & 31) != 0 && node / 32 + 1 < p.words ? (uint32_t)__ldg(mrow + node / 32 + 1) : 0u;
-                            v = __funnelshift_r(lo, hi, node & 31);
-                        }
-                        if (left < 32) v &= left > 0 ? ~(0xffffffffu << left) : 0u;
-                        return valid ? v : 0u;
-                    };
+                    auto word = [&](int node) { return valid ? seen_word(mrow, p.words, node, x.nodes) : 0u; };
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         const int at = part * NC + c;                     // of the tile's four: FP8: [slots' half][blocks' half]
@@ -1259,12 +1543,19 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 if (live) {
                     tc_fence_after();
                     float c1 = scale;
-                    float drop = 1.f;                                     // what a raise of V's power of two puts on O
+                    float drop = 1.f;                                     // what a change of V's power of two puts on O
                     if constexpr (RAW) {
                         const uint2 e = ld_shared_v2(sbase + L::PASSED + (NAT ? sb * L::PASS + kKeys * 4 : 8 * (t & 7)));
+                        if ((int)e.y != ev) {
+                            // V's power of two changes (or the piece begins), or the tile is a wide one, each time
+                            if (e.y > 0xffu || ev == kOwnUnits) {
+                                wide = true;
+                                break;
+                            }
+                            drop = exp2i(ev - (int)e.y);
+                            ev = (int)e.y;
+                        }
                         c1 *= exp2i(max(min((int)e.x - 127 - shift, 127), -126));
-                        if (i > 0 && (int)e.y != ev) drop = exp2i(ev - (int)e.y);
-                        ev = (int)e.y;
                     }
                     c1 = fmaxf(c1, FLT_MIN);                              // (a hidden key's -inf stays -inf under a scale of 0)
                     const uint32_t mine = lanes + scol + COLS * part;
@@ -1364,6 +1655,21 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                 __syncwarp();
                 if (lane == 0) mbar_arrive_n(bar(kPFull + sb), arrivals);
             }
+            if constexpr (RAW) {
+                if (wide) {
+                    const WideRow r = wide_tile<D, T>(WideRow{m_used, l, ev, true}, sbase, tmem, t0 + i, i == 0, valid ? mrow : nullptr,
+                                                      p.words, (x.j0 + i) * kKeys - x.start, x.nodes, shift, scale, kLift);
+                    m_used = r.m;
+                    l = r.l;
+                    ev = r.ev;
+                    ok = r.ok;
+                    hi = i + 1;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive_n(bar(kPFull + ((t0 + i) & 1)), arrivals);
+                }
+            }
             // (one row tile: the last piece's scores are taken, their Q is free)
             if (SW == 1 && ok && lo == 0 && y.n > 0) shift_next = put_q(y, ic + 1);
             lo = hi;
@@ -1385,6 +1691,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             const size_t piece = (size_t)(2 * blockIdx.x + (ic == 0 ? 0 : 1));
             const size_t orow = ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.h * p.G + g) * D;
             // what is left on O: V's power of two, the probabilities' lift where the sums do not share it
+            if (RAW && ev == kOwnUnits) ev = (int)ld_shared_u32(sbase + L::UNITS + 4 * (kTileRows * part + lr));
             const float back = RAW ? exp2i(ev - 127) : 1.f;
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : exp2i(-(int)kLift);
             constexpr int EC = DP < 32 ? DP : 32;
