@@ -754,6 +754,8 @@ def _compact(kind, pool, k_pool, v_pool, block_tables, src_pos, dst_start, cu_ro
         if not isinstance(t, torch.Tensor) or t.dim() != dims:
             raise ValueError(f"{name} must be a tensor of {dims} dimensions")
     (s, width), n = block_tables.shape, src_pos.shape[0]
+    if dst_tables is not None and dst_tables.shape[1] == 0 and n > 0:
+        raise ValueError("dst_tables has no columns")        # (its address, null, would mean in place)
     for t, name, dtype, of_t in ((k_pool, "k_pool", k_pool.dtype, k_pool.shape),
                                  (v_pool, "v_pool", k_pool.dtype, k_pool.shape),
                                  (block_tables, "block_tables", _I32, (s, width)), (src_pos, "src_pos", _I32, (n,)),

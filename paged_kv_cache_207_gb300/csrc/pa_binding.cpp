@@ -329,7 +329,8 @@ PyObject* compact(PyObject* const* a, Py_ssize_t n) {
     dst.ptr.at = nullptr;
     dst.shape[1] = 0;
     if (a[7] != Py_None && (look(a[7], &dst, false) < 0 || dst.dtype != at::kInt || dst.dims != 2 ||
-                            dst.shape[0] != tables.shape[0] || !small(dst.shape[1]) || dst.device != dev))
+                            dst.shape[0] != tables.shape[0] || !small(dst.shape[1]) || dst.device != dev ||
+                            (dst.shape[1] == 0 && src.shape[0] > 0)))     /* (its address, null, would mean in place) */
         return closer();
     if (look_rest(a[8], a[9], dev, &err, &raw) < 0) return closer();
     pa_status s;

@@ -1,0 +1,23 @@
+"""Calls around drafted trees that the bindings refuse, without a GPU."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def native():
+    from paged_kv_cache_207_gb300 import build, _native
+    build.build()
+    return _native
+
+
+def test_compaction_into_a_table_without_columns(native):
+    # its address is that of no table, which would mean in place
+    i32 = torch.int32
+    pool = torch.zeros(native.pool_shape(4, 2, 64, torch.bfloat16), dtype=torch.bfloat16)
+    tables, start, cu, src = torch.zeros(3, 4, dtype=i32), torch.zeros(3, dtype=i32), torch.arange(4, dtype=i32), torch.ones(3, dtype=i32)
+    for call, pools in ((native.compact_kv, pool), (native.compact_kv_fp8, torch.zeros(native.fp8_pool_shape(4, 2, 64), dtype=torch.uint8)),
+                        (native.compact_kv_fp4, torch.zeros(native.fp4_pool_shape(4, 2, 64), dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="dst_tables"):
+            call(pools, pools, tables, src, start, cu, dst_tables=torch.zeros(3, 0, dtype=i32))
+
+
