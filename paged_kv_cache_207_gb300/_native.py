@@ -967,7 +967,7 @@ class BlockManager:
 
     def truncate(self, seq: int, length: int) -> None:
         """Cuts the sequence to its first `length` tokens; the blocks behind them are let go."""
-        check("pa_bm_truncate", lib().pa_bm_truncate(self._h, seq, length))
+        check("pa_bm_truncate", lib().pa_bm_truncate(self._h, _bound(seq), _bound(length)))
 
     def block_table(self, seq: int, max_blocks: int) -> list:
         buf = (ctypes.c_int32 * max(max_blocks, 1))()

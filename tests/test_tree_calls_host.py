@@ -21,3 +21,14 @@ def test_compaction_into_a_table_without_columns(native):
             call(pools, pools, tables, src, start, cu, dst_tables=torch.zeros(3, 0, dtype=i32))
 
 
+def test_truncate_takes_no_number_modulo_2_32(native):
+    bm = native.BlockManager(8)
+    a = bm.add_seq()
+    bm.prepare_append(a, 0, 50)
+    for seq, length in ((a, 2**32), (a, 2**32 + 5), (a, 5 - 2**32), (a, -2**32), (2**32 + a, 3), (a - 2**32, 3), (a, 2**70)):
+        with pytest.raises(native.PagedKVError):
+            bm.truncate(seq, length)
+        assert bm.seq_len(a) == 50 and bm.stats()["free_blocks"] == 4
+    bm.truncate(a, 50)
+    bm.truncate(a, 17)
+    assert bm.seq_len(a) == 17 and bm.stats()["free_blocks"] == 6
