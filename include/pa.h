@@ -582,8 +582,8 @@ size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t
  * Sizes of other rows do not matter; key tiles (128 tokens) whose rows' scales lie further apart than
  * 2^14 (FP4: 2^23) take several times as long.
  * A chunk outside rows 0 .. total_q sets PA_DEV_ERR_BAD_CU and is skipped, one at positions outside
- * the table PA_DEV_ERR_BAD_POS; nodes past max_chunk set PA_DEV_ERR_HINT: they are not computed, and
- * not seen.  Rows of q and out past cu_q[num_seqs] (a padded batch) are neither read nor written.
+ * the table PA_DEV_ERR_BAD_POS; nodes past max_chunk (which may be 0) set PA_DEV_ERR_HINT: they are
+ * not computed, and not seen.  Rows of q and out past cu_q[num_seqs] (a padded batch) are neither read nor written.
  * A table entry that is no block of the pool sets PA_DEV_ERR_BAD_BLOCK and leaves the sequence's
  * outputs undefined.  head_dim 64 or 128; at most 8 query heads per kv head.
  */

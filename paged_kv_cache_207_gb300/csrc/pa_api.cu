@@ -742,7 +742,13 @@ pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const 
     if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
     if (num_q_heads / num_kv_heads > 8) return PA_ERR_UNSUPPORTED;
     if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX) return PA_ERR_INVALID_ARG;
-    if (num_seqs == 0 || total_q == 0 || max_chunk == 0) return PA_OK;
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (max_chunk == 0) {
+        // nothing is computed; nodes that there are all the same are past the bound
+        if (!cu_q) return PA_ERR_INVALID_ARG;
+        if (!dev_err_flag) return PA_OK;
+        return cuda_status(pa::launch_tree_bound(cu_q, num_seqs, total_q, dev_err_flag, static_cast<cudaStream_t>(stream)));
+    }
     // (no tree has more nodes than there are rows)
     if (max_chunk > total_q) max_chunk = total_q;
     if ((long long)mask_words * 32 < max_chunk) return PA_ERR_INVALID_ARG;

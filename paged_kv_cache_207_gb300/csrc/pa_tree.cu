@@ -304,6 +304,16 @@ __global__ void __launch_bounds__(kThreads, f32_ctas(D)) tree_f32_kernel(const T
     }
 }
 
+__global__ void tree_bound_kernel(const int32_t* cu, int num_seqs, int total_q, int32_t* err) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int s = threadIdx.x; s < num_seqs; s += blockDim.x) {
+        const int q0 = __ldg(cu + s), q1 = __ldg(cu + s + 1);
+        if (q0 < 0 || q0 > q1 || q1 > total_q) raise_flag(err, PA_DEV_ERR_BAD_CU);
+        else if (q1 > q0) raise_flag(err, PA_DEV_ERR_HINT);
+    }
+}
+
 template <int D>
 cudaError_t launch_f32(const TreeArgs& a, cudaStream_t stream) {
     constexpr int smem = F32Layout<D>::BYTES;
@@ -322,6 +332,10 @@ size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int
     const long long tile = tree_tile_rows(rows) / G * G, tile32 = kTreeF32Rows / G * G;
     const long long tc = 2ll * kTreeCtas * std::min(rows, tile), f32 = 2ll * kTreeF32Ctas * std::min(rows, tile32);
     return (size_t)std::max(tc, f32) * (head_dim + 2) * sizeof(float) + kTreeF32Ctas * kTreeJointBytes;
+}
+
+cudaError_t launch_tree_bound(const int32_t* cu_q, int num_seqs, int total_q, int32_t* err, cudaStream_t stream) {
+    return tree_launch(tree_bound_kernel, dim3(1), 256, 0, stream, cu_q, num_seqs, total_q, err);
 }
 
 cudaError_t launch_tree_f32(const TreeArgs& a, cudaStream_t stream) {

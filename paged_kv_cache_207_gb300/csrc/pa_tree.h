@@ -33,6 +33,8 @@ inline int tree_tile_rows(long long rows) { return rows > 128 ? 256 : 128; }
 size_t tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_chunk);
 
 cudaError_t launch_tree_f32(const TreeArgs& a, cudaStream_t stream);
+// What a call with a bound of no nodes says of its sequences: PA_DEV_ERR_HINT where there are some, PA_DEV_ERR_BAD_CU.
+cudaError_t launch_tree_bound(const int32_t* cu_q, int num_seqs, int total_q, int32_t* err, cudaStream_t stream);
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream);      // every other type
 
 }  // namespace pa

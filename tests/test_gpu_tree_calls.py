@@ -38,3 +38,25 @@ def test_compaction_into_a_table_without_columns(cache, quick, monkeypatch):
     of_cache("compact_kv", cache)(c.kp, c.vp, c.tables.cuda(), i32([]), i32([0, 2]), i32([0, 0, 0]), dst_tables=none)
 
 
+@pytest.mark.parametrize("cache", CACHES)
+def test_a_bound_of_no_nodes(cache):
+    # like any other that is too small: the nodes are flagged, and not computed
+    c = Cache(cache, [20, 12], (4, 2, 64), seed=71)
+    q = c.queries(5).cuda()
+    mask, ws = torch.ones(5, 1, dtype=torch.int32, device="cuda"), pk.tree_workspace(4, 2, 64, 0)
+
+    def call(cu):
+        out, err = nan_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+        of_cache("tree_attention", cache)(out, q, c.kp, c.vp, c.tables.cuda(), i32([10, 10]), i32(cu), mask, 0.1, 0, ws, err_flag=err)
+        assert bool(out.isnan().all())
+        return int(err)
+
+    assert call([0, 3, 5]) == pk.DEV_ERR_HINT
+    assert call([0, 0, 2]) == pk.DEV_ERR_HINT
+    assert call([0, 0, 0]) == 0
+    assert call([0, 7, 7]) == pk.DEV_ERR_BAD_CU
+    out = nan_like(q)                                                # without a flag
+    of_cache("tree_attention", cache)(out, q, c.kp, c.vp, c.tables.cuda(), i32([10, 10]), i32([0, 3, 5]), mask, 0.1, 0, ws)
+    assert bool(out.isnan().all())
+
+
