@@ -173,7 +173,8 @@ __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) ? true : warp_wait_long(bar, parity);
+    // (a look gives each lane a result of its own: all have to go the same way)
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait_long(bar, parity);
 }
 // One 32-byte store (the address a multiple of 32).
 __device__ __forceinline__ void st_global_v8(void* addr, const uint32_t (&w)[8]) {
