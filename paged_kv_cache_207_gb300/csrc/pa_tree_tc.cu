@@ -58,7 +58,13 @@ namespace pa {
 
 namespace {
 
+// The longest wait of a warp for others, and of what is in flight before a CTA ends.
+#ifdef PA_TREE_TEST_WAITS
+__device__ uint64_t kWaitNs = 200000000ull;      // (a build of the tests' own, which set it)
+#else
 constexpr uint64_t kWaitNs = 200000000ull;
+#endif
+constexpr uint64_t kLandNs = 200000000ull;
 constexpr int kTileRows = 128;
 constexpr int kKeyBlocks = 8, kKeys = kKeyBlocks * kBlockTokens;
 constexpr int kPieces = 4;                // records of pieces
@@ -111,7 +117,7 @@ struct Layout {
     static constexpr int PASSED = EXPS + 64;
     static constexpr int SEEN = PASSED + (NAT ? 2 * PASS : 64);      // [8][8] a tile's block has such values
     static constexpr int TABLE = SEEN + 80;           // [8] FP4: a block's scales of values
-    static constexpr int GONE = TABLE - 8;            // [2] the conversions' lead gave up, K's and V's
+    static constexpr int GONE = TABLE - 8;            // [2] the tile at which the conversions leave, K's and V's
     static constexpr int RECORDS = TABLE + (T == PA_FP4_E2M1 ? kKeyBlocks * 128 : 0);      // [kPieces] pieces
     static constexpr int FIRST = RECORDS + kPieces * 32;               // the CTA's first place, for a call that gives up
     static constexpr int ROWS = FIRST + 64;                            // [row tile][part][128] maxima, sums
@@ -162,6 +168,10 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 }
 // All lanes wait, a fifth of a second at most; the result is the same in all.  (A look costs four
 // instructions: the waiting warps share their issue slots with those that work.)
+//
+// A warp that gives up raises the flag and waits for nothing any more, and what it does not do makes the others give up in
+// their turn.  But a named barrier has no limit: who shares one with others comes to it as often as they do,
+// whatever has become of its own waits (rows_leave, conversions_leave).
 __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = global_timer_ns();
     bool ok;
@@ -175,6 +185,16 @@ __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     // (a look gives each lane a result of its own: all have to go the same way)
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait_long(bar, parity);
+}
+// A named barrier of n threads that also says whether any of them brought `x`.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id), "r"(n)
+        : "memory");
+    return r != 0u;
 }
 // One 32-byte store (the address a multiple of 32).
 __device__ __forceinline__ void st_global_v8(void* addr, const uint32_t (&w)[8]) {
@@ -236,6 +256,27 @@ __device__ __forceinline__ uint32_t seen_word(const int32_t* row, int words, int
     return v;
 }
 
+// The conversions leave at tile t, for which a warp of theirs, or (done != 0) their lead, has given up.  gone: where
+// the tile is said; go: their barriers, of tiles in turn; done: the barriers of their results, likewise.  A lead may be ahead:
+// only when the conversions two tiles before are done is their barrier free, unless all leave there or before, and nobody
+// waits at this one.
+__device__ __noinline__ void conversions_leave(int t, uint32_t gone, uint32_t done, int go) {
+    const uint64_t t0 = global_timer_ns();
+    bool left = false;
+    while (done != 0u && t >= 2) {
+        int at;
+        asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(at) : "r"(gone) : "memory");
+        left = __any_sync(0xffffffffu, at <= t - 2);
+        if (left || __all_sync(0xffffffffu, mbar_test(done + 8 * (t & 1), ((t - 2) >> 1) & 1)) ||
+            __any_sync(0xffffffffu, global_timer_ns() - t0 > kLandNs))
+            break;
+    }
+    if (left) return;
+    if ((threadIdx.x & 31) == 0) asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(gone), "r"(t) : "memory");
+    __syncwarp();
+    named_bar_arrive(go + (t & 1), 32 * (kKeyBlocks + 1));
+}
+
 // A run of key tiles of one item.
 struct Piece {
     int j0, n;               // its first key tile, and how many; none: the CTA's work has ended
@@ -274,6 +315,53 @@ struct Walk {
 };
 
 static_assert(sizeof(Walk) <= 64, "its place in shared memory");
+
+// The rest of a CTA's work for a softmax warp that has given up at tile `tile` of its piece ic (below 0: before the first
+// queries): the barriers that it shares with the warps of its rows, in their order, then NaN for its rows.  first: where
+// the CTA's work begins; row: the thread's, of the row tile; sum: its place for the row's sum; HALVES: row tiles.
+template <int D, int HALVES, int PARTS, bool RAW>
+__device__ __noinline__ void rows_leave(const TParams& p, const Walk* first, int ic, int tile, int row, int row_bar, float* sum) {
+    const float nan = __int_as_float(0x7fc00000);
+    const int lane = threadIdx.x & 31, tl = row / p.G, g = row - tl * p.G;
+    auto busy = [&](const Piece& x) { return row - lane < x.tokens * p.G; };
+    auto meet = [&](int times) {
+        for (int k = 0; k < times; ++k) named_bar_sync(row_bar, 32 * PARTS);
+    };
+    // one row tile: queries through shared memory
+    auto queries = [&](const Piece& x) {
+        if (HALVES == 1 && x.n > 0 && busy(x)) meet(RAW ? 3 : 2);
+    };
+    Walk w = *first;
+    for (int k = 0; k < ic; ++k) w.next(p);
+    Piece x = w.piece(p);
+    if (ic < 0) queries(x);
+    for (; x.n > 0; tile = 0) {
+        w.next(p);
+        const Piece y = w.piece(p);
+        const bool live = busy(x);
+        for (int i = tile; i < x.n; ++i) {
+            // two more where a row of theirs rises
+            if (live && named_bar_or(row_bar, 32 * PARTS, false)) meet(2);
+            if (i == 0) queries(y);
+        }
+        if (live) {
+            *sum = nan;
+            meet(1);
+        }
+        x = y;
+    }
+    // the rows of this piece and of the later ones are incomplete
+    w = *first;
+    for (int k = 0; w.left > 0; ++k, w.next(p)) {
+        x = w.piece(p);
+        if (k < ic || tl >= x.tokens) continue;
+        if (!x.whole) {
+            for (int i = 0; i < 2; ++i) p.part_ml[(size_t)(2 * blockIdx.x + i) * p.slot_rows + row] = make_float2(nan, nan);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.h * p.G + g) * D);
+        for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    }
+}
 
 // The table of a piece in windows of 32 entries, one per lane, a window ahead of its use (read tile
 // by tile, every tile would wait for a load).
@@ -553,16 +641,6 @@ struct Convert<D, PA_FP4_E2M1> {
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
-// A named barrier of n threads that also says whether any of them brought `x`.
-__device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(id), "r"(n)
-        : "memory");
-    return r != 0u;
-}
 // The same of E4M3 operands, 32 of K at a time.
 __device__ __forceinline__ void umma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t acc) {
     asm volatile(
@@ -816,7 +894,7 @@ __device__ __noinline__ WideRow wide_tile(WideRow row, uint32_t sbase, uint32_t 
 }
 
 template <int D, pa_dtype T, int SW>
-__global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const TParams p) {
+__global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const __grid_constant__ TParams p) {
     using L = Layout<D, T, SW>;
     using W = Roles<T, SW>;
     constexpr bool RAW = L::RAW, NAT = L::NAT;
@@ -857,7 +935,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         mbar_init(bar(kDone), 1);
         if (RAW) {
             for (int i = 0; i < 4; ++i) mbar_init(bar(kEFull + i), 1);
-            for (int i = 0; i < 2; ++i) *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * i) = 0u;
+            for (int i = 0; i < 2; ++i) *reinterpret_cast<volatile int*>(smem + L::GONE + 4 * i) = INT32_MAX;
         }
         fence_proxy_async_smem();
     }
@@ -960,8 +1038,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         if (!ok && lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
         // before the CTA ends, every copy has landed
         if (lane == 0) {
-            for (int f = max(0, u - ST); f < u; ++f) mbar_wait_bounded(bar(full0 + f % ST), (f / ST) & 1, kWaitNs);
-            for (int f = max(0, uk - KST); f < uk; ++f) mbar_wait_bounded(bar(kKFull + f % KST), (f / KST) & 1, kWaitNs);
+            for (int f = max(0, u - ST); f < u; ++f) mbar_wait_bounded(bar(full0 + f % ST), (f / ST) & 1, kLandNs);
+            for (int f = max(0, uk - KST); f < uk; ++f) mbar_wait_bounded(bar(kKFull + f % KST), (f / KST) & 1, kLandNs);
         }
     } else if (warp == W::MMA) {
         // ------------------------------------------------------------ MMA issue
@@ -1169,7 +1247,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         // nothing may still be running on the tensor cores when the TMEM is freed
         if (elect_one()) umma_commit(bar(kDone));
         __syncwarp();
-        mbar_wait_bounded(bar(kDone), 0, kWaitNs);
+        mbar_wait_bounded(bar(kDone), 0, kLandNs);
     } else if (RAW && warp >= W::LEAD && warp < W::LEAD + W::LEADS) {
         // ------------------------------------------------------------ the conversions' lead
         // One warp for the keys, one for the values waits for a tile's records and for its place and lets
@@ -1182,9 +1260,15 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             const bool for_v = NAT || warp > W::LEAD;
             bool ok = true;
             int t = 0;
+            // (two barriers in turn: a tile's place is free when the conversions two tiles before are done, so that
+            // their barrier is too)
+            static_assert(VST == 2 && (NAT || KST == 2), "a tile's place is that of two tiles before");
+            const int go = 7 + 2 * for_v;
+            const uint32_t gone = sbase + L::GONE + 4 * for_v, done = bar(for_v ? kVFull : kKFull);
             for (int ic = 0; ok; ++ic) {
                 Piece x;
                 ok = piece(ic, x);
+                if (!ok) conversions_leave(t, gone, done, go);
                 if (!ok || x.n == 0) break;
                 int rv = 127, top = 0, low = 255;         // (of references: V's, the highest, the lowest; top 0: none yet)
                 for (int i = 0; i < x.n; ++i, ++t) {
@@ -1213,7 +1297,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                             }
                         }
                         const bool wide = __any_sync(0xffffffffu, far || C::below(scales, rv - C::DEPTH));
-                        if (wide) {
+                        if (ok && wide) {
                             const uint32_t to = sbase + L::WIDE + t % L::WIDE_TILES * L::WIDE_TILE;
                             const int ctx = x.start - (x.j0 + i) * kKeys;
                             if (!NAT) C::widen(kraw, REC, to, keys, ctx, lane);
@@ -1221,7 +1305,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                             fence_proxy_async_smem();                // (before the next copies to the records' places)
                             __syncwarp();
                         }
-                        if (lane == 0) {
+                        if (ok && lane == 0) {
                             st_shared_v2(sbase + L::EXPS + 8 * (t & 7),
                                          wide ? make_uint2(127u | (uint32_t)rv << 8, 127u | kWideValues) : make_uint2((uint32_t)ek, (uint32_t)rv));
                             mbar_arrive(bar(kEFull + (t & 3)));
@@ -1236,11 +1320,12 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     } else {
                         if (t >= KST) ok = ok && warp_wait(bar(kKEmpty + t % KST), (t / KST - 1) & 1);
                     }
-                    if (!ok && lane == 0) *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * for_v) = 1u;
+                    if (!ok) {
+                        conversions_leave(t, gone, done, go);
+                        break;
+                    }
                     __syncwarp();
-                    // (two barriers in turn: a tile's place is free when the conversions two tiles before are done)
-                    named_bar_arrive(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
-                    if (!ok) break;
+                    named_bar_arrive(go + (t & 1), 32 * (kKeyBlocks + 1));
                 }
                 piece_done(ic);
             }
@@ -1261,6 +1346,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
             for (int ic = 0; ok; ++ic) {
                 Piece x;
                 ok = piece(ic, x);
+                if (!ok) {
+                    conversions_leave(t, sbase + L::GONE + 4 * for_v, 0u, 7 + 2 * for_v);
+                    if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
+                }
                 if (!ok || x.n == 0) break;
                 const int end = x.end();
                 for (int i = 0; i < x.n; ++i, ++t) {
@@ -1269,7 +1358,7 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     const uint32_t vraw = smem_r + rs * L::HALF;
                     const int tok0 = (x.j0 + i) * kKeys, first = tok0 + b * kBlockTokens;
                     named_bar_sync(7 + 2 * for_v + (t & 1), 32 * (kKeyBlocks + 1));
-                    ok = *reinterpret_cast<volatile uint32_t*>(smem + L::GONE + 4 * for_v) == 0u;
+                    ok = *reinterpret_cast<volatile int*>(smem + L::GONE + 4 * for_v) > t;
                     if (!ok) break;
                     mbar_test(bar(kRFull + (for_v ? rs : rk)), ((for_v ? uv : uk) / L::RST) & 1);     // (the copies are seen)
                     const uint2 e = ld_shared_v2(sbase + L::EXPS + 8 * (t & 7));
@@ -1488,8 +1577,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     };
     Piece x{};
     bool ok = piece(0, x);
-    if constexpr (SW == 2) load_q(x);
-    else stage_q(x);
+    if (ok) {
+        if constexpr (SW == 2) load_q(x);
+        else stage_q(x);
+    }
     tc_fence_before();
     named_bar_sync(2, 32 * (W::SOFT + 1));
     tc_fence_after();
@@ -1497,10 +1588,14 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
     const uint32_t lanes = tmem + lanes_at;
     const uint32_t ocol = kColO + (uint32_t)(h * kKeys);
     constexpr float kLift = RAW ? 7.f : 0.f;                          // (log2) on the probabilities
-    if constexpr (SW == 2) publish_q(x);
-    else shift = put_q(x, 0);
-    int t0 = 0, ic = 0;
+    int t0 = 0, ic = -1, next = 0;                                    // (the next tile of piece ic)
+    if (ok) {
+        if constexpr (SW == 2) publish_q(x);
+        else shift = put_q(x, 0);
+        ic = 0;
+    }
     for (; ok; ++ic) {
+        next = 0;
         const int n = x.n, rows = x.tokens * p.G;
         const bool live = busy(x), valid = tl < x.tokens;
         const int32_t* mrow = p.mask + (size_t)(x.qrow + (valid ? tl : 0)) * p.words;
@@ -1628,7 +1723,10 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                             }
                         }
                         named_bar_sync(row_bar, 32 * PARTS);                     // (the maxima are read)
-                        if (!ok) break;
+                        if (!ok) {
+                            ++i;
+                            break;
+                        }
                     }
                     // probabilities, rounded to the tensor cores' type (the sums take them unrounded: the
                     // roundings are of either sign and average out), over the first columns of this thread's part of S
@@ -1664,13 +1762,14 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
                     l = r.l;
                     ev = r.ev;
                     ok = r.ok;
-                    hi = i + 1;
+                    hi = ++i;
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive_n(bar(kPFull + ((t0 + i) & 1)), arrivals);
+                    if (ok && lane == 0) mbar_arrive_n(bar(kPFull + ((t0 + i - 1) & 1)), arrivals);
                 }
             }
+            next = ok ? hi : i;
             // (one row tile: the last piece's scores are taken, their Q is free)
             if (SW == 1 && ok && lo == 0 && y.n > 0) shift_next = put_q(y, ic + 1);
             lo = hi;
@@ -1770,19 +1869,8 @@ __global__ void __launch_bounds__(Roles<T, SW>::THREADS, 1) tree_tc_kernel(const
         else shift = shift_next;
     }
     if (!ok) {
-        // a wait gave up: the rows of this piece and of the later ones are incomplete and become NaN
         if (lane == 0) raise_flag(p.err, PA_DEV_ERR_TIMEOUT);
-        walk = *reinterpret_cast<const Walk*>(smem + L::FIRST);
-        for (int k = 0; walk.left > 0; ++k, walk.next(p)) {
-            x = walk.piece(p);
-            if (k < ic || tl >= x.tokens) continue;
-            const float nan = __int_as_float(0x7fc00000);
-            if (!x.whole) {
-                for (int i = 0; i < 2; ++i) p.part_ml[(size_t)(2 * blockIdx.x + i) * p.slot_rows + row] = make_float2(nan, nan);
-            }
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((size_t)(x.qrow + tl) * p.Hq + (size_t)x.h * p.G + g) * D);
-            for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-        }
+        rows_leave<D, SW, PARTS, RAW>(p, reinterpret_cast<const Walk*>(smem + L::FIRST), ic, next, row, row_bar, shared_row + part * kTileRows);
     }
     // (no query copy may still be landing when the CTA ends)
     cp_async_wait<0>();
