@@ -80,8 +80,8 @@ typedef enum {
 #define PA_DEV_ERR_BAD_CU 8      /* cu_new_tokens is not a prefix sum ending at total_new_tokens */
 #define PA_DEV_ERR_TIMEOUT 16    /* a bulk-copy or tensor-core wait gave up after 200 ms.  The
                                     outputs of the work that gave up are written as NaN.
-                                    While this bit is set in the flag, every decode, prefill
-                                    and partition-merge kernel given the flag returns without
+                                    While this bit is set in the flag, every decode, prefill,
+                                    tree and partition-merge kernel given the flag returns without
                                     writing anything (so a broken pipeline cannot hold the GPU
                                     or overwrite results); clear the bit to resume.  Without a
                                     flag (NULL) the NaN outputs are the only sign. */
@@ -585,7 +585,8 @@ size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t
  * the table PA_DEV_ERR_BAD_POS; nodes past max_chunk (which may be 0) set PA_DEV_ERR_HINT: they are
  * not computed, and not seen.  Rows of q and out past cu_q[num_seqs] (a padded batch) are neither read nor written.
  * A table entry that is no block of the pool sets PA_DEV_ERR_BAD_BLOCK and leaves the sequence's
- * outputs undefined.  head_dim 64 or 128; at most 8 query heads per kv head.
+ * outputs undefined.  head_dim 64 or 128; at most 8 query heads per kv head; tables of at most
+ * 2^31 - 256 tokens.
  */
 pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
                             const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -619,7 +620,7 @@ pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const 
  * A position outside its table sets PA_DEV_ERR_BAD_POS, a table entry that is no block of the pool
  * PA_DEV_ERR_BAD_BLOCK: that row is not moved (a sequence whose rows would pass its destination's
  * table: none of it).  A sequence whose rows leave 0 .. total_rows sets PA_DEV_ERR_BAD_CU and is
- * skipped.  head_dim 64 or 128.
+ * skipped.  head_dim 64 or 128; at most 65535 sequences and kv heads.
  */
 pa_status pa_compact_kv(void* k_pool, void* v_pool, const int32_t* block_tables,
                         int32_t max_blocks_per_seq, const int32_t* src_pos,

@@ -741,7 +741,8 @@ pa_status pa_tree_attention(void* out, const void* q, const void* k_pool, const 
     if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
     if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
     if (num_q_heads / num_kv_heads > 8) return PA_ERR_UNSUPPORTED;
-    if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX) return PA_ERR_INVALID_ARG;
+    // (the kernels round positions up to whole tiles of keys)
+    if ((long long)max_blocks_per_seq * pa::kBlockTokens > INT32_MAX - 255) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     if (max_chunk == 0) {
         // nothing is computed; nodes that there are all the same are past the bound

@@ -32,3 +32,13 @@ def test_truncate_takes_no_number_modulo_2_32(native):
     bm.truncate(a, 50)
     bm.truncate(a, 17)
     assert bm.seq_len(a) == 17 and bm.stats()["free_blocks"] == 6
+
+
+def test_tree_attention_refuses_tables_of_2_31_tokens(native):
+    # the last tile of keys has to end within int32
+    L = native.lib()
+
+    def call(width):
+        return L.pa_tree_attention(16, 16, 16, 16, 16, width, 16, 16, 16, 1, 1, 4, 0, 4, 2, 64, 8, 0.125, 1, 16, 1 << 30, None, None)
+
+    assert [call(w) for w in (2**27 - 16, 2**27 - 15, 2**27 - 1, 2**27)] == [0, 1, 1, 1]
