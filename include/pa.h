@@ -578,9 +578,11 @@ size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t
  * What a node's key or value holds, finite or not, reaches only rows that see the node.
  * Quantised pools: probabilities are f16, so that weights below 2^-32 of a row's largest may count
  * as zero; FP8 values are off by 2^-11 of themselves, and by 2^-19 of the largest element of their
- * row; FP4 values and keys, whose scales may lie 2^23 apart in a row, by 2^-24 of its largest element.
- * Sizes of other rows do not matter; key tiles (128 tokens) whose rows' scales lie further apart than
- * 2^14 (FP4: 2^23) take several times as long.
+ * row, FP8's query elements by 2^-17 of the largest of theirs; FP4 values and keys, whose scales may
+ * lie 2^23 apart in a row, by 2^-24 of its largest element.  Sizes of rows that are not seen, or weigh
+ * nothing, do not matter; key tiles (128 tokens) whose scales lie further apart than 2^14 (FP4: 2^23)
+ * take several times as long, and there products of weight and value below 2^-20 of the row's
+ * largest may count as zero.
  * A chunk outside rows 0 .. total_q sets PA_DEV_ERR_BAD_CU and is skipped, one at positions outside
  * the table PA_DEV_ERR_BAD_POS; nodes past max_chunk (which may be 0) set PA_DEV_ERR_HINT: they are
  * not computed, and not seen.  Rows of q and out past cu_q[num_seqs] (a padded batch) are neither read nor written.

@@ -15,8 +15,8 @@
 // Where it is bound.  bf16 to 128 rows: by the keys' bytes (64 sequences of 4096 tokens, 32 / 8 heads of
 // 128: 1 node 166 us, 6.5 TB/s, 32 nodes 178).  bf16 with 256 rows: a key tile's MMAs take 1.5 us of the
 // 2.0 that pass (64 nodes 227 us): scores of one row tile wait for its products with the values, as the TMEM
-// holds one S tile per row tile.  FP8 (8 nodes 169, 32 nodes 179; four sequences of 80000: 185) and FP4 (179,
-// 184; 192): 1.4 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
+// holds one S tile per row tile.  FP8 (8 nodes 171, 32 nodes 181; four sequences of 80000: 188) and FP4 (184,
+// 186; 196): 1.4 us a tile, which is how long the softmax, of which a tile is a chain (scores, maximum,
 // agreement, exponentials, publication), takes beside the conversions on the same issue slots; without
 // conversions 1.25, with the copies alone 1.05.
 //
@@ -716,8 +716,8 @@ __device__ __noinline__ float value_at(const char* rec, int slot, int d) {
 // Wide tiles, whose scales lie further apart than operands of 16 bits against one reference hold: a column's own scales go
 // on its score and on its probability, and a row has its O in a unit of its own, if need be, so that no row depends on
 // the scales of keys that it does not see or that weigh nothing for it.  (64 sequences of 4096 tokens, 32 / 8 heads of 128,
-// 8 nodes, all tiles wide: FP8 1350 us,
-// not 169, FP4 950, not 179.)
+// 8 nodes, all tiles wide: FP8 1360 us,
+// not 171, FP4 957, not 184.)
 
 // A scale as 2^(e - 127) m, |m| from 1 to below 2; 0: m = 0; not finite: m is what it is.
 struct Split {
