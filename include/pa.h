@@ -577,7 +577,7 @@ size_t pa_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t
  * that the last bits of a sequence's result may depend on the batch; equal calls give equal bits.
  * What a node's key or value holds, finite or not, reaches only rows that see the node.
  * Quantised pools: probabilities are f16, so that weights below 2^-32 of a row's largest may count
- * as zero; FP8 values are off by 2^-11 of themselves, and by 2^-19 of the largest element of their
+ * as zero; FP8 values are off by 2^-10 of themselves, and by 2^-19 of the largest element of their
  * row, FP8's query elements by 2^-17 of the largest of theirs; FP4 values and keys, whose scales may
  * lie 2^23 apart in a row, by 2^-24 of its largest element.  Sizes of rows that are not seen, or weigh
  * nothing, do not matter; key tiles (128 tokens) whose scales lie further apart than 2^14 (FP4: 2^23)

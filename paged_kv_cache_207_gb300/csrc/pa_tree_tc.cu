@@ -716,8 +716,7 @@ __device__ __noinline__ float value_at(const char* rec, int slot, int d) {
 // Wide tiles, whose scales lie further apart than operands of 16 bits against one reference hold: a column's own scales go
 // on its score and on its probability, and a row has its O in a unit of its own, if need be, so that no row depends on
 // the scales of keys that it does not see or that weigh nothing for it.  (64 sequences of 4096 tokens, 32 / 8 heads of 128,
-// 8 nodes, all tiles wide: FP8 1360 us,
-// not 171, FP4 957, not 184.)
+// 8 nodes, all tiles wide: FP8 1360 us instead of 171, FP4 957 instead of 184.)
 
 // A scale as 2^(e - 127) m, |m| from 1 to below 2; 0: m = 0; not finite: m is what it is.
 struct Split {
